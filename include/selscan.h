@@ -383,6 +383,162 @@ int selective_scan_ssd_fwd(const void* x, const void* delta, const float* A, con
  * MI355X times picks (one segment, the whole sequence, where splitting does not pay). */
 size_t selective_scan_ssd_workspace_size(const selscan_ssd_dims* dims);
 
+/*
+ * The gated linear recurrence: one fp32 state per channel, a decay and an input gate per
+ * token and channel,
+ *     s = sigmoid(r),  la = -c softplus(lam[d]) s,  a = exp(la),  m = sqrt(1 - a^2),
+ *     h_t = a_t h_{t-1} + m_t sigmoid(g_t) x_t,     y_t = h_t.
+ * m keeps the state's variance at the input's whatever the decay.  It is the recurrence of
+ * the scan above with one state, unit readout and a transition that depends on the token
+ * through r alone; unlike there the input coefficient is not a function of a step size.
+ * Sequences packed into one row are told apart by `reset`: at a token whose reset byte is
+ * not 0 the state starts anew (a = 0, m = 1; nothing before the token reaches it or is reached
+ * by its gradient).
+ */
+typedef struct selscan_gated_dims {
+  int32_t abi_version;     /* SELSCAN_ABI_VERSION */
+  int32_t io_dtype;        /* enum selscan_dtype: x, r, g, y (and dy, dx, dr, dg) */
+  int64_t batch;           /* >= 0 */
+  int64_t seqlen;          /* >= 0 */
+  int64_t dim;             /* D >= 1 */
+  int64_t x_sb, x_sl;      /* strides in elements as in selscan_dims (unit stride over channels); */
+  int64_t r_sb, r_sl;      /* token strides at most 2^20 */
+  int64_t g_sb, g_sl;
+  int64_t y_sb, y_sl;      /* y of the forward, dy of the backward */
+  int64_t reset_sb;        /* bytes between batch rows of reset (its token stride is 1) */
+  float decay_c;           /* c, finite and > 0 */
+  int32_t reserved;        /* 0 */
+} selscan_gated_dims;
+
+/* Tokens between two checkpoints of the state (gated_scan_fwd, gated_scan_bwd). */
+#define SELSCAN_GATED_TILE 128
+
+/* Fill *dims for contiguous x, r, g, y [batch][seqlen][dim] and reset [batch][seqlen];
+ * decay_c = 8.  Never fails for a non-NULL dims. */
+void gated_scan_dims_init(selscan_gated_dims* dims, int io_dtype, int64_t batch, int64_t seqlen, int64_t dim);
+
+/*
+ * gated_scan_fwd -- enqueue the gated linear recurrence.
+ *   x, r, g        : inputs in dims->io_dtype: the input, the decay gate and the input gate
+ *                    before their sigmoids
+ *   lam            : [dim] fp32
+ *   reset          : bytes, one per token (see above), or NULL
+ *   y              : output in dims->io_dtype
+ *   initial_state, last_state : [batch][dim] fp32, or NULL (zero / not written).  They may be
+ *                    one buffer.  A last_state is the state after the row's last token.
+ *   checkpoints    : [batch][ceil(seqlen / SELSCAN_GATED_TILE)][dim] fp32 output, or NULL: the
+ *                    state entering each tile of tokens, which spares the backward pass a pass
+ *                    over the inputs
+ *   workspace      : gated_scan_workspace_size(dims) bytes, 256-byte aligned, or NULL to take it
+ *                    stream-ordered on `stream`.  Not to be used by other work until the
+ *                    enqueued call has finished (two captured graphs that may run at once need
+ *                    one each).
+ * Pointers and status codes otherwise as selective_scan_fwd; seqlen == 0 hands the initial
+ * state (zeros if NULL) to last_state.
+ */
+int gated_scan_fwd(const void* x, const void* r, const void* g, const float* lam, const uint8_t* reset, void* y,
+                   const float* initial_state, float* last_state, float* checkpoints,
+                   const selscan_gated_dims* dims, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gated_scan_fwd (0 for an empty call, invalid dims or a sequence that one
+ * workgroup takes whole). */
+size_t gated_scan_workspace_size(const selscan_gated_dims* dims);
+
+/*
+ * gated_scan_bwd -- gradients of gated_scan_fwd (same inputs and options), given dy (strides
+ * y_sb, y_sl) and optionally dlast_state [batch][dim] fp32.
+ *   checkpoints    : the forward call's, or NULL (then they are formed again from the inputs)
+ *   dx, dr, dg     : [batch][seqlen][dim] contiguous in dims->io_dtype
+ *   dlam           : [dim] fp32
+ *   dinitial_state : [batch][dim] fp32, or NULL
+ *   workspace      : gated_scan_bwd_workspace_size(dims, checkpoints != NULL) bytes, as above
+ * All outputs are written, never accumulated into; sums run in a fixed order.  The gradient
+ * through m stays finite as a tends to 1 (la/m tends to 0).
+ */
+int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam, const uint8_t* reset,
+                   const float* initial_state, const float* checkpoints, const void* dy, const float* dlast_state,
+                   void* dx, void* dr, void* dg, float* dlam, float* dinitial_state,
+                   const selscan_gated_dims* dims, void* workspace, size_t workspace_bytes, void* stream);
+size_t gated_scan_bwd_workspace_size(const selscan_gated_dims* dims, int have_checkpoints);
+
+/*
+ * gated_scan_step -- one token per batch row, the state updated in place: x, r, g, y rows at
+ * b * x_sb etc. (dims->seqlen must be 1; token strides and reset_sb are not used), state
+ * [batch][dim] fp32.  Never allocates.
+ */
+int gated_scan_step(const void* x, const void* r, const void* g, const float* lam, void* y, float* state,
+                    const selscan_gated_dims* dims, void* stream);
+
+/*
+ * The 8-bit state cache.  Decoding moves each sequence's whole state twice per token; held as
+ * 8-bit codes with one fp32 scale per row it moves a quarter of the bytes.  A cache holds
+ * `slots` states of `elems` values each, in rows of `row_len` consecutive values (the last
+ * row may be shorter):
+ *     q     [slots][elems]                   int8 codes -127 .. 127
+ *     scale [slots][ceil(elems / row_len)]   fp32
+ * and stands for the values q * scale.  Storing a row: with amax its largest magnitude,
+ *     scale = amax / 127,   q = floor(h * (127 / amax) + u),
+ * where u = 1/2 (nearest) without a seed.  With one, u = (k + 1/2) / 65536 for 16 bits k that
+ * are a function of the seed, the row's place (batch row * rows + row) and the value's place in
+ * the row: stochastic rounding, whose expectation is h.  A state that decays slowly needs it:
+ * rounded to nearest, a change of less than half a code per token never takes place.
+ * A row whose amax is below 2^-100 is stored as zeros; one that holds an infinity or a NaN is
+ * stored with a NaN scale and stands for NaN throughout.
+ * Rows of the layers: selective scan elems = dim * dstate, row_len = dstate; scalar-decay
+ * layer elems = nheads * 64 * dstate, row_len = dstate; gated recurrence elems = dim,
+ * row_len = 64.
+ * Slot ids are int32 device arrays, one id per batch row; NULL stands for 0, 1, 2, ...  An id
+ * that is negative, or not below `slots`, names no slot.  Ids of rows that are written must
+ * differ from one another, and a slot that one row writes must not be read by another row of
+ * the same call: reordering (beams that continue other beams) reads one set of slots and
+ * writes another.
+ */
+typedef struct selscan_cache_dims {
+  int32_t abi_version;     /* SELSCAN_ABI_VERSION */
+  int32_t reserved;        /* 0 */
+  int64_t slots;           /* >= 0 */
+  int64_t elems;           /* >= 1, at most 2^31 - 1 */
+  int64_t row_len;         /* 1 .. 128 */
+} selscan_cache_dims;
+
+/*
+ * state_cache_write -- store `count` states (state: [count][elems] fp32, e.g. a last_state) in
+ * the slots that slot_ids names (rows that name no slot are skipped).  seed: one int64 in device
+ * memory, or NULL.  state_cache_read -- the values of `count` slots into out ([count][elems],
+ * out_dtype an enum selscan_dtype; zeros for an id that names no slot).  In a read, ids may
+ * repeat.  count * rows must be below 2^32.  Neither allocates.
+ */
+int state_cache_write(const float* state, const int32_t* slot_ids, int64_t count, int8_t* q, float* scale,
+                      const int64_t* seed, const selscan_cache_dims* cache, void* stream);
+int state_cache_read(const int8_t* q, const float* scale, const int32_t* slot_ids, int64_t count, void* out,
+                     int out_dtype, const selscan_cache_dims* cache, void* stream);
+
+/*
+ * selective_scan_step_cached -- selective_scan_step with the state in a cache
+ * (selective coefficients only, else SELSCAN_ERR_UNSUPPORTED; cache->elems = dim * dstate,
+ * cache->row_len = dstate, else SELSCAN_ERR_DIMS).  Batch row b starts from the state in slot
+ * read_slots[b] (zero where that names no slot: a sequence's first token) and stores the new
+ * one in slot write_slots[b]; y is formed from the new state before it is rounded.  A row
+ * whose write id names no slot is padding: it is skipped, its y is left as it was.
+ * Never allocates.
+ */
+int selective_scan_step_cached(const void* u, const void* delta, const float* delta_bias, const float* A,
+                               const void* B, const void* C, const float* Dskip, const void* z, void* y,
+                               int8_t* q, float* scale, const int32_t* read_slots, const int32_t* write_slots,
+                               const int64_t* seed, const selscan_dims* dims, const selscan_cache_dims* cache,
+                               void* stream);
+
+/*
+ * selective_scan_ssd_step_cached -- one token of the scalar-decay layer with the state in a
+ * cache (elems = nheads * 64 * dstate, row_len = dstate); slots, seed and padding as above.
+ * Tensors as selective_scan_ssd_fwd with seqlen 1 (bf16 and contiguous; x, z, y, B and C 16-byte
+ * aligned; dims->path and dims->segments are not used).  Never allocates.
+ */
+int selective_scan_ssd_step_cached(const void* x, const void* delta, const float* A, const void* B, const void* C,
+                                   const float* Dskip, const void* z, void* y, int8_t* q, float* scale,
+                                   const int32_t* read_slots, const int32_t* write_slots, const int64_t* seed,
+                                   const selscan_ssd_dims* dims, const selscan_cache_dims* cache, void* stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* selective_scan_strerror(int status);
 

@@ -83,6 +83,16 @@ _SIGNATURES = [
     ("selective_scan_bwd_workspace_size", ctypes.c_size_t, [ctypes.POINTER(SelscanDims)]),
     ("selective_scan_ssd_fwd", ctypes.c_int, [_VP] * 10 + [ctypes.c_void_p, _VP, ctypes.c_size_t, _VP]),
     ("selective_scan_ssd_workspace_size", ctypes.c_size_t, [ctypes.c_void_p]),
+    ("gated_scan_dims_init", None, [_VP, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    ("gated_scan_fwd", ctypes.c_int, [_VP] * 9 + [_VP, _VP, ctypes.c_size_t, _VP]),
+    ("gated_scan_workspace_size", ctypes.c_size_t, [_VP]),
+    ("gated_scan_bwd", ctypes.c_int, [_VP] * 14 + [_VP, _VP, ctypes.c_size_t, _VP]),
+    ("gated_scan_bwd_workspace_size", ctypes.c_size_t, [_VP, ctypes.c_int]),
+    ("gated_scan_step", ctypes.c_int, [_VP] * 6 + [_VP, _VP]),
+    ("state_cache_write", ctypes.c_int, [_VP, _VP, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP]),
+    ("state_cache_read", ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int64, _VP, ctypes.c_int, _VP, _VP]),
+    ("selective_scan_step_cached", ctypes.c_int, [_VP] * 17),
+    ("selective_scan_ssd_step_cached", ctypes.c_int, [_VP] * 16),
     ("selective_scan_strerror", ctypes.c_char_p, [ctypes.c_int]),
     ("selective_scan_last_hip_error", ctypes.c_int, []),
     ("selective_scan_abi_version", ctypes.c_int, []),
@@ -561,6 +571,337 @@ def selective_scan_ssd_fwd(x, delta, A, B, C, Dskip=None, z=None, y=None, *, ini
     return y, last
 
 
+class GatedDims(ctypes.Structure):
+    """Mirror of ``selscan_gated_dims`` in include/selscan.h."""
+    _fields_ = [("abi_version", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_sb", ctypes.c_int64), ("x_sl", ctypes.c_int64), ("r_sb", ctypes.c_int64), ("r_sl", ctypes.c_int64),
+                ("g_sb", ctypes.c_int64), ("g_sl", ctypes.c_int64), ("y_sb", ctypes.c_int64), ("y_sl", ctypes.c_int64),
+                ("reset_sb", ctypes.c_int64), ("decay_c", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class CacheDims(ctypes.Structure):
+    """Mirror of ``selscan_cache_dims`` in include/selscan.h."""
+    _fields_ = [("abi_version", ctypes.c_int32), ("reserved", ctypes.c_int32), ("slots", ctypes.c_int64),
+                ("elems", ctypes.c_int64), ("row_len", ctypes.c_int64)]
+
+
+GATED_TILE = 128          # SELSCAN_GATED_TILE: tokens between two checkpoints
+CACHE_ROW = 64            # row length of a [D] state (the gated recurrence's) in the state cache
+
+
+class _On:
+    """The GPU and the stream of one call: what is allocated inside belongs to that stream."""
+
+    def __init__(self, t, stream):
+        import torch
+        if not t.is_cuda:
+            raise ValueError("the tensors must be GPU tensors")
+        self.device = t.device
+        self._guards = []
+        if torch.cuda.current_device() != t.device.index:
+            self._guards.append(torch.cuda.device(t.device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(t.device).cuda_stream
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+            self.handle = stream.cuda_stream
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+        return False
+
+    def check(self, name, t, dtype, shape, contiguous=True):
+        """t (None passes) must be of this dtype and shape, on this GPU, and contiguous unless said."""
+        if t is None:
+            return
+        if t.dtype != dtype:
+            raise TypeError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if t.device != self.device:
+            raise ValueError("%s must be on %s, got %s" % (name, self.device, t.device))
+        if contiguous and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+    def workspace(self, given, need):
+        """(pointer, bytes) of the workspace: the given one, or one of torch's caching allocator."""
+        import torch
+        if given is None:
+            if need == 0:
+                return None, None, 0
+            given = torch.empty(need, dtype=torch.uint8, device=self.device)
+        elif given.device != self.device or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % self.device)
+        return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _gated_dims(on, x, r, g, lam, y, reset, c):
+    """selscan_gated_dims of [batch, L, D] tensors; their channel axes are unit-stride."""
+    import torch
+    batch, L, D = x.shape
+    for name, t in (("x", x), ("r", r), ("g", g), ("y", y)):
+        if t is not None:
+            on.check(name, t, x.dtype, x.shape, contiguous=False)
+            if D > 1 and t.stride(2) != 1:
+                raise ValueError("%s: the channel axis must be unit-stride" % name)
+    on.check("lam", lam, torch.float32, (D,))
+    d = GatedDims(abi_version=SELSCAN_ABI_VERSION, io_dtype=_io_code(x.dtype), batch=batch, seqlen=L, dim=D,
+                  x_sb=x.stride(0), x_sl=x.stride(1), r_sb=r.stride(0), r_sl=r.stride(1), g_sb=g.stride(0),
+                  g_sl=g.stride(1), decay_c=float(c))
+    if y is not None:
+        d.y_sb, d.y_sl = y.stride(0), y.stride(1)
+    else:
+        d.y_sb, d.y_sl = L * D, D
+    if reset is not None:
+        if reset.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("reset must be a bool or uint8 [batch, L] tensor")
+        on.check("reset", reset, reset.dtype, (batch, L), contiguous=False)
+        if L > 1 and reset.stride(1) != 1:
+            raise ValueError("reset: the token axis must be unit-stride")
+        d.reset_sb = reset.stride(0)
+    return d
+
+
+def gated_checkpoints(x):
+    """A tensor for the states that gated_scan_fwd leaves for gated_scan_bwd:
+    [batch, ceil(L / GATED_TILE), D] float32 for x [batch, L, D]."""
+    import torch
+    return torch.empty((x.shape[0], -(-x.shape[1] // GATED_TILE), x.shape[2]), dtype=torch.float32, device=x.device)
+
+
+def gated_scan_fwd(x, r, g, lam, *, y=None, initial_state=None, last_state=None, return_last_state: bool = False,
+                   checkpoints=None, reset=None, c: float = 8.0, workspace=None, stream=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(g_t) x_t with
+    a_t = exp(-c softplus(lam) sigmoid(r_t)); y = h.  Returns (y, last_state or None).
+
+    x, r, g, y: [batch, L, D] float32 or bfloat16 (unit-stride channels); lam: [D] float32;
+    reset: [batch, L] bool or uint8, true where a packed sequence starts; initial_state,
+    last_state: [batch, D] float32; checkpoints (see gated_checkpoints) is filled for the
+    backward pass.  ``workspace`` is taken from torch's caching allocator when omitted."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, L, D]")
+    with _On(x, stream) as on:
+        batch, L, D = x.shape
+        if y is None:
+            y = torch.empty((batch, L, D), dtype=x.dtype, device=x.device)
+        if last_state is None and return_last_state:
+            last_state = torch.empty((batch, D), dtype=torch.float32, device=x.device)
+        dims = _gated_dims(on, x, r, g, lam, y, reset, c)
+        on.check("initial_state", initial_state, torch.float32, (batch, D))
+        on.check("last_state", last_state, torch.float32, (batch, D))
+        on.check("checkpoints", checkpoints, torch.float32, (batch, -(-L // GATED_TILE), D))
+        ref = ctypes.byref(dims)
+        keep, ws, nbytes = on.workspace(workspace, lib().gated_scan_workspace_size(ref))
+        st = lib().gated_scan_fwd(_p(x), _p(r), _p(g), _p(lam), _p(reset), _p(y), _p(initial_state), _p(last_state),
+                                  _p(checkpoints), ref, ws, nbytes, on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "gated_scan_fwd")
+    return y, last_state
+
+
+def gated_scan_bwd(x, r, g, lam, *, dy, dlast_state=None, initial_state=None, checkpoints=None, reset=None,
+                   c: float = 8.0, workspace=None, stream=None) -> dict:
+    """Gradients of gated_scan_fwd (same inputs and options) given dy and optionally
+    dlast_state.  Returns a dict: dx, dr, dg as [batch, L, D] in x's dtype; dlam [D] and (with an
+    initial_state) dinitial_state [batch, D] in float32.  ``checkpoints``: what the forward call
+    filled, or None to form them again."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, L, D]")
+    with _On(x, stream) as on:
+        batch, L, D = x.shape
+        dims = _gated_dims(on, x, r, g, lam, dy, reset, c)
+        on.check("dlast_state", dlast_state, torch.float32, (batch, D))
+        on.check("initial_state", initial_state, torch.float32, (batch, D))
+        on.check("checkpoints", checkpoints, torch.float32, (batch, -(-L // GATED_TILE), D))
+        out = {k: torch.empty((batch, L, D), dtype=x.dtype, device=x.device) for k in ("dx", "dr", "dg")}
+        out["dlam"] = torch.empty((D,), dtype=torch.float32, device=x.device)
+        if initial_state is not None:
+            out["dinitial_state"] = torch.empty((batch, D), dtype=torch.float32, device=x.device)
+        ref = ctypes.byref(dims)
+        keep, ws, nbytes = on.workspace(workspace, lib().gated_scan_bwd_workspace_size(ref, checkpoints is not None))
+        st = lib().gated_scan_bwd(_p(x), _p(r), _p(g), _p(lam), _p(reset), _p(initial_state), _p(checkpoints), _p(dy),
+                                  _p(dlast_state), _p(out["dx"]), _p(out["dr"]), _p(out["dg"]), _p(out["dlam"]),
+                                  _p(out.get("dinitial_state")), ref, ws, nbytes, on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "gated_scan_bwd")
+    return out
+
+
+def gated_scan_step(x, r, g, lam, *, state, y=None, c: float = 8.0, stream=None):
+    """One token of the gated recurrence per batch row (x, r, g, y: [batch, D]); ``state``
+    ([batch, D] float32, contiguous) is overwritten with the new one.  Returns y."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [batch, D] (one token per batch row)")
+    with _On(x, stream) as on:
+        batch, D = x.shape
+        if y is None:
+            y = torch.empty((batch, D), dtype=x.dtype, device=x.device)
+        dims = _gated_dims(on, *(t.unsqueeze(1) for t in (x, r, g)), lam, y.unsqueeze(1), None, c)
+        on.check("state", state, torch.float32, (batch, D))
+        st = lib().gated_scan_step(_p(x), _p(r), _p(g), _p(lam), _p(y), _p(state), ctypes.byref(dims), on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "gated_scan_step")
+    return y
+
+
+def state_cache(slots: int, *state_shape: int, device="cuda"):
+    """An empty 8-bit state cache (q, scale) of `slots` states of this shape: (D, N) for the
+    selective scan, (H, 64, N) for the scalar-decay layer (a scale per N values), (D,) for the
+    gated recurrence (a scale per 64 channels).  q: [slots, *state_shape] int8; scale:
+    [slots, rows] float32.  Every slot holds the zero state."""
+    import torch
+    rows = -(-state_shape[0] // CACHE_ROW) if len(state_shape) == 1 else 1
+    for n in state_shape[:-1]:
+        rows *= n
+    return (torch.zeros((slots,) + state_shape, dtype=torch.int8, device=device),
+            torch.zeros((slots, rows), dtype=torch.float32, device=device))
+
+
+def _cache_dims(on, q, scale, seed):
+    import torch
+    if q.dim() < 2:
+        raise ValueError("q must be [slots, *state_shape]")
+    row_len = CACHE_ROW if q.dim() == 2 else int(q.shape[-1])
+    slots, elems = int(q.shape[0]), 1
+    for n in q.shape[1:]:
+        elems *= int(n)
+    on.check("q", q, torch.int8, q.shape)
+    on.check("scale", scale, torch.float32, (slots, -(-elems // row_len) if row_len else 0))
+    on.check("seed", seed, torch.int64, (1,))
+    return CacheDims(abi_version=SELSCAN_ABI_VERSION, slots=slots, elems=elems, row_len=row_len)
+
+
+def state_cache_write(state, q, scale, *, slots=None, seed=None, stream=None) -> None:
+    """Store states ([count, *state_shape] float32) in the slots that ``slots`` ([count] int32;
+    0, 1, 2, ... when omitted) names, as 8-bit codes; ids outside the cache skip their row and
+    the others must differ.  ``seed``: a one-element int64 GPU tensor for stochastic rounding
+    (nearest when omitted)."""
+    import torch
+    with _On(q, stream) as on:
+        dims = _cache_dims(on, q, scale, seed)
+        on.check("state", state, torch.float32, (state.shape[0],) + tuple(q.shape[1:]))
+        on.check("slots", slots, torch.int32, (state.shape[0],))
+        st = lib().state_cache_write(_p(state), _p(slots), state.shape[0], _p(q), _p(scale), _p(seed),
+                                     ctypes.byref(dims), on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "state_cache_write")
+
+
+def state_cache_read(q, scale, *, slots=None, out=None, dtype=None, stream=None):
+    """The states that the slots stand for: [count, *state_shape], zeros for ids outside the cache.
+    dtype: float32 (the default) or bfloat16; ``out`` may be given instead."""
+    import torch
+    with _On(q, stream) as on:
+        dims = _cache_dims(on, q, scale, None)
+        shape = (int(q.shape[0]) if slots is None else int(slots.shape[0]),) + tuple(q.shape[1:])
+        on.check("slots", slots, torch.int32, shape[:1])
+        if out is None:
+            out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
+        on.check("out", out, dtype or out.dtype, shape)
+        st = lib().state_cache_read(_p(q), _p(scale), _p(slots), shape[0], _p(out), _io_code(out.dtype),
+                                    ctypes.byref(dims), on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "state_cache_read")
+    return out
+
+
+def selective_scan_step_cached(u, delta, A, B, C, Dskip=None, z=None, y=None, *, q, scale, read_slots=None,
+                               write_slots=None, seed=None, delta_bias=None, delta_softplus: bool = False,
+                               discretization: str = "zoh", stream=None):
+    """selective_scan_step with the states in an 8-bit cache (see state_cache): row b starts from
+    the state in slot read_slots[b] (the zero state where the id is outside the cache) and stores
+    the new one in slot write_slots[b]; rows whose write id is outside the cache are padding and
+    keep their y.  Ids: [batch] int32, 0, 1, 2, ... when omitted.  A slot that a row writes may be
+    read by that row alone.  delta: [batch, D] (or [D]); B, C: [batch, N].  Returns y."""
+    import torch
+    if u.dim() != 2:
+        raise ValueError("u must be [batch, D] (one token per batch row)")
+    with _On(u, stream) as on:
+        batch, D = (int(v) for v in u.shape)
+        on.check("A", A, torch.float32, (D, A.shape[-1]))
+        N = int(A.shape[1])
+        if y is None:
+            y = torch.empty((batch, D), dtype=u.dtype, device=u.device)
+        d = SelscanDims(abi_version=SELSCAN_ABI_VERSION, io_dtype=_io_code(u.dtype), batch=batch, seqlen=1, dim=D,
+                        dstate=N, discretization=DISCRETIZATIONS[discretization],
+                        delta_softplus=1 if delta_softplus else 0)
+        for name, t, width in (("u", u, D), ("delta", delta, D), ("B", B, N), ("C", C, N), ("z", z, D), ("y", y, D)):
+            if t is None:
+                continue
+            per_channel = name == "delta" and t.dim() == 1
+            on.check(name, t, u.dtype, (D,) if per_channel else (batch, width), contiguous=False)
+            if width > 1 and t.stride(-1) != 1:
+                raise ValueError("%s must have a unit-stride last axis" % name)
+            if not per_channel:
+                setattr(d, name + "_sb", t.stride(0))
+                setattr(d, name + "_sl", width)
+        on.check("Dskip", Dskip, torch.float32, (D,))
+        on.check("delta_bias", delta_bias, torch.float32, (D,))
+        cache = _cache_dims(on, q, scale, seed)
+        if tuple(q.shape[1:]) != (D, N):
+            raise ValueError("q must be [slots, %d, %d]" % (D, N))
+        on.check("read_slots", read_slots, torch.int32, (batch,))
+        on.check("write_slots", write_slots, torch.int32, (batch,))
+        st = lib().selective_scan_step_cached(_p(u), _p(delta), _p(delta_bias), _p(A), _p(B), _p(C), _p(Dskip), _p(z),
+                                              _p(y), _p(q), _p(scale), _p(read_slots), _p(write_slots), _p(seed),
+                                              ctypes.byref(d), ctypes.byref(cache), on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "selective_scan_step_cached")
+    return y
+
+
+def selective_scan_ssd_step_cached(x, delta, A, B, C, Dskip=None, z=None, y=None, *, q, scale, read_slots=None,
+                                   write_slots=None, seed=None, discretization: str = "zoh", stream=None):
+    """One token of the scalar-decay layer with the states in an 8-bit cache (slots, seed and
+    padding as selective_scan_step_cached; state shape (H, 64, N)).  x, z, y: [batch, H, 64];
+    delta: [batch, H]; B, C: [batch, N], bfloat16 and contiguous; A: [H], Dskip: [H * 64]
+    float32.  Returns y."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, H, 64] (one token per batch row)")
+    with _On(x, stream) as on:
+        batch, H, P = (int(v) for v in x.shape)
+        N = int(B.shape[-1])
+        if y is None:
+            y = torch.empty((batch, H, P), dtype=torch.bfloat16, device=x.device)
+        for name, t, shape in (("x", x, (batch, H, P)), ("delta", delta, (batch, H)), ("B", B, (batch, N)),
+                               ("C", C, (batch, N)), ("z", z, (batch, H, P)), ("y", y, (batch, H, P))):
+            on.check(name, t, torch.bfloat16, shape)
+        on.check("A", A, torch.float32, (H,))
+        on.check("Dskip", Dskip, torch.float32, (H * P,))
+        cache = _cache_dims(on, q, scale, seed)
+        if tuple(q.shape[1:]) != (H, P, N):
+            raise ValueError("q must be [slots, %d, %d, %d]" % (H, P, N))
+        on.check("read_slots", read_slots, torch.int32, (batch,))
+        on.check("write_slots", write_slots, torch.int32, (batch,))
+        dims = ssd_dims(batch, 1, H, P, N, discretization)
+        st = lib().selective_scan_ssd_step_cached(_p(x), _p(delta), _p(A), _p(B), _p(C), _p(Dskip), _p(z), _p(y),
+                                                  _p(q), _p(scale), _p(read_slots), _p(write_slots), _p(seed),
+                                                  ctypes.byref(dims), ctypes.byref(cache), on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "selective_scan_ssd_step_cached")
+    return y
+
+
 __all__ = ["selective_scan_fwd", "selective_scan_step", "selective_scan_bwd", "bwd_workspace_size",
-           "selective_scan_ssd_fwd", "ssd_dims", "ssd_workspace_size", "SsdDims", "make_dims", "dims_init", "workspace_size", "strerror", "last_hip_error",
+           "selective_scan_ssd_fwd", "ssd_dims", "ssd_workspace_size", "SsdDims",
+           "gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "gated_checkpoints", "GatedDims", "GATED_TILE",
+           "state_cache", "state_cache_write", "state_cache_read", "CacheDims", "CACHE_ROW",
+           "selective_scan_step_cached", "selective_scan_ssd_step_cached", "make_dims", "dims_init", "workspace_size", "strerror", "last_hip_error",
            "abi_version", "lib", "SelscanDims", "SelscanError", "LIB_PATH"]

@@ -23,6 +23,7 @@ SCAN_UNITS = [os.path.join(CSRC, "scan_inst_%s_%s.hip" % (io, ps))
               for io in ("f32", "bf16") for ps in ("single", "state", "apply")]
 SOURCES = SCAN_UNITS + [os.path.join(CSRC, "bwd_kernels.hip"), os.path.join(CSRC, "bwd_ti_kernels.hip"), os.path.join(CSRC, "scan_kernels.hip"),
                         os.path.join(CSRC, "conv_kernels.hip"), os.path.join(CSRC, "ssd_kernels.hip"),
+                        os.path.join(CSRC, "gated_kernels.hip"), os.path.join(CSRC, "cache_kernels.hip"),
                         os.path.join(CSRC, "selscan_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -220,3 +220,53 @@ struct SsdParams {
 hipError_t launch_ssd(const SsdParams& p, hipStream_t stream);
 
 }  // namespace selscan
+
+namespace selscan {
+
+// The gated linear recurrence (gated_kernels.hip).  Strides in elements; dx, dr, dg contiguous
+// [batch][L][D] in the I/O type.
+struct GatedParams {
+  const void* x;
+  const void* r;
+  const void* g;
+  const float* lam;
+  const uint8_t* reset;  // may be null
+  void* y;               // may be null (only the checkpoints are wanted)
+  const float* h0;       // [batch][D], may be null (zero)
+  float* last;           // [batch][D], may be null
+  float* ckpt;           // [batch][ntiles][D] state entering each tile, may be null
+  const void* dy;        // backward only, with y's strides
+  const float* dlast;    // may be null
+  void* dx;
+  void* dr;
+  void* dg;
+  float* dlam;           // [D]
+  float* dh0;            // may be null
+  int64_t batch, L, D;
+  int64_t x_sb, x_sl, r_sb, r_sl, g_sb, g_sl, y_sb, y_sl, reset_sb;
+  int64_t ntiles;        // ceil(L / SELSCAN_GATED_TILE)
+  float c;
+  float* hbuf;           // workspace
+  float* plam;           // workspace: partial sums of dlam
+};
+hipError_t launch_gated_fwd(bool bf16, const GatedParams& p, hipStream_t stream);
+hipError_t launch_gated_bwd(bool bf16, const GatedParams& p, hipStream_t stream);
+hipError_t launch_gated_step(bool bf16, const GatedParams& p, float* state, hipStream_t stream);
+
+// The 8-bit state cache (cache_kernels.hip): q [slots][elems], scale [slots][rows].
+struct CacheParams {
+  int8_t* q;
+  float* scale;
+  const int32_t* read_slots;   // may be null (0, 1, 2, ...)
+  const int32_t* write_slots;  // may be null
+  const int64_t* seed;         // may be null (round to nearest)
+  int64_t slots, elems, row_len, rows;
+  int64_t count;               // batch rows
+};
+hipError_t launch_cache_write(const float* state, const CacheParams& p, hipStream_t stream);
+hipError_t launch_cache_read(bool bf16, void* out, const CacheParams& p, hipStream_t stream);
+// one decode step of the selective scan / of the scalar-decay layer on cached states
+hipError_t launch_step_cached(bool bf16, const StepParams& s, const CacheParams& p, hipStream_t stream);
+hipError_t launch_ssd_step_cached(const SsdParams& s, const CacheParams& p, hipStream_t stream);
+
+}  // namespace selscan

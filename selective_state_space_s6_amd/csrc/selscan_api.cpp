@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "scan_launch.h"
@@ -937,6 +938,305 @@ int selective_scan_ssd_fwd(const void* x, const void* delta, const float* A, con
     if (st == SELSCAN_OK && f != hipSuccess) st = hip_fail(f);
   }
   return st;
+}
+
+// ---- the gated linear recurrence
+struct GatedPlan {
+  int64_t ntiles = 0;
+  size_t fwd_bytes = 0;                         // workspace of the forward pass
+  size_t off_ckpt = 0, off_hbuf = 0, off_plam = 0, bwd_bytes = 0;
+};
+
+// Validate dims and lay out the workspaces.  Does not look at pointers.
+static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan* out) {
+  if (!dims) return SELSCAN_ERR_NULL;
+  if (dims->abi_version != SELSCAN_ABI_VERSION) return SELSCAN_ERR_ABI;
+  const selscan_gated_dims& d = *dims;
+  if (d.batch < 0 || d.seqlen < 0 || d.dim < 1) return SELSCAN_ERR_DIMS;
+  for (int64_t s : {d.x_sb, d.x_sl, d.r_sb, d.r_sl, d.g_sb, d.g_sl, d.y_sb, d.y_sl, d.reset_sb})
+    if (s < 0) return SELSCAN_ERR_DIMS;
+  if (!(d.decay_c > 0.f) || d.decay_c > 3.0e38f) return SELSCAN_ERR_DIMS;
+  if (d.io_dtype != SELSCAN_F32 && d.io_dtype != SELSCAN_BF16) return SELSCAN_ERR_UNSUPPORTED;
+  // a tile of tokens is addressed with 32-bit offsets
+  const int64_t kMaxRow = int64_t(1) << 20;
+  if (d.x_sl > kMaxRow || d.r_sl > kMaxRow || d.g_sl > kMaxRow || d.y_sl > kMaxRow || d.dim > kMaxRow)
+    return SELSCAN_ERR_UNSUPPORTED;
+  const int64_t kMaxItems = (int64_t(1) << 31) - 1;
+  if (d.batch > kMaxItems || d.seqlen > (int64_t(1) << 40)) return SELSCAN_ERR_UNSUPPORTED;
+  GatedPlan p;
+  p.ntiles = (d.seqlen + SELSCAN_GATED_TILE - 1) / SELSCAN_GATED_TILE;
+  if (d.batch > 0 && p.ntiles > 0 && p.ntiles > kMaxItems / d.batch / ((d.dim + 63) / 64)) return SELSCAN_ERR_UNSUPPORTED;
+  if (d.batch * d.seqlen > 0) {
+    auto al = [](int64_t x) { return size_t(round_up(x, 256)); };
+    const int64_t f = int64_t(sizeof(float));
+    size_t off = 0;
+    if (!have_ckpt) off += al(f * d.batch * p.ntiles * d.dim);
+    p.off_hbuf = off;
+    off += al(f * d.batch * SELSCAN_GATED_TILE * d.dim);
+    p.off_plam = off;
+    off += al(f * d.batch * d.dim);
+    p.bwd_bytes = off;
+  }
+  *out = p;
+  return SELSCAN_OK;
+}
+
+// y rows must not overlap (every (b, l, d) is written exactly once); dy, which is read, may
+static bool gated_rows_apart(const selscan_gated_dims& d) {
+  return (d.seqlen <= 1 || d.y_sl >= d.dim) && (d.batch <= 1 || d.seqlen <= 0 || d.y_sb >= (d.seqlen - 1) * d.y_sl + d.dim);
+}
+
+static selscan::GatedParams gated_params(const void* x, const void* r, const void* g, const float* lam,
+                                         const uint8_t* reset, const selscan_gated_dims& d, const GatedPlan& pl) {
+  selscan::GatedParams p{};
+  p.x = x; p.r = r; p.g = g; p.lam = lam; p.reset = reset;
+  p.batch = d.batch; p.L = d.seqlen; p.D = d.dim;
+  p.x_sb = d.x_sb; p.x_sl = d.x_sl; p.r_sb = d.r_sb; p.r_sl = d.r_sl; p.g_sb = d.g_sb; p.g_sl = d.g_sl;
+  p.y_sb = d.y_sb; p.y_sl = d.y_sl; p.reset_sb = d.reset_sb;
+  p.ntiles = pl.ntiles;
+  p.c = d.decay_c;
+  return p;
+}
+
+static bool all_aligned(std::initializer_list<const void*> ptrs, size_t a) {
+  for (const void* q : ptrs)
+    if (q && !aligned(q, a)) return false;
+  return true;
+}
+
+void gated_scan_dims_init(selscan_gated_dims* dims, int io_dtype, int64_t batch, int64_t seqlen, int64_t dim) {
+  if (!dims) return;
+  selscan_gated_dims d{};
+  d.abi_version = SELSCAN_ABI_VERSION;
+  d.io_dtype = io_dtype;
+  d.batch = batch; d.seqlen = seqlen; d.dim = dim;
+  d.x_sb = d.r_sb = d.g_sb = d.y_sb = seqlen * dim;
+  d.x_sl = d.r_sl = d.g_sl = d.y_sl = dim;
+  d.reset_sb = seqlen;
+  d.decay_c = 8.f;
+  *dims = d;
+}
+
+size_t gated_scan_workspace_size(const selscan_gated_dims* dims) {
+  GatedPlan pl;
+  return gated_plan(dims, true, &pl) == SELSCAN_OK ? pl.fwd_bytes : 0;
+}
+
+size_t gated_scan_bwd_workspace_size(const selscan_gated_dims* dims, int have_checkpoints) {
+  GatedPlan pl;
+  return gated_plan(dims, have_checkpoints != 0, &pl) == SELSCAN_OK ? pl.bwd_bytes : 0;
+}
+
+int gated_scan_fwd(const void* x, const void* r, const void* g, const float* lam, const uint8_t* reset, void* y,
+                   const float* initial_state, float* last_state, float* checkpoints,
+                   const selscan_gated_dims* dims, void* workspace, size_t workspace_bytes, void* stream) {
+  GatedPlan pl;
+  int st = gated_plan(dims, true, &pl);
+  if (st != SELSCAN_OK) return st;
+  const selscan_gated_dims& d = *dims;
+  if (!gated_rows_apart(d)) return SELSCAN_ERR_UNSUPPORTED;
+  const bool no_tokens = d.batch * d.seqlen == 0;
+  if (!lam || (!no_tokens && (!x || !r || !g || !y))) return SELSCAN_ERR_NULL;
+  if (!all_aligned({x, r, g, y}, d.io_dtype == SELSCAN_BF16 ? 2 : 4) ||
+      !all_aligned({lam, initial_state, last_state, checkpoints}, 4))
+    return SELSCAN_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (d.batch == 0) return SELSCAN_OK;
+  hipError_t e = hipSuccess;
+  if (no_tokens) {                              // the initial state is handed back
+    if (last_state && last_state != initial_state)
+      e = initial_state ? selscan::launch_copy(last_state, initial_state, d.batch * d.dim, s)
+                        : selscan::launch_fill_zero(last_state, d.batch * d.dim, s);
+    return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  }
+  selscan::GatedParams p = gated_params(x, r, g, lam, reset, d, pl);
+  p.y = y; p.h0 = initial_state; p.last = last_state; p.ckpt = checkpoints;
+  e = selscan::launch_gated_fwd(d.io_dtype == SELSCAN_BF16, p, s);
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam, const uint8_t* reset,
+                   const float* initial_state, const float* checkpoints, const void* dy, const float* dlast_state,
+                   void* dx, void* dr, void* dg, float* dlam, float* dinitial_state,
+                   const selscan_gated_dims* dims, void* workspace, size_t workspace_bytes, void* stream) {
+  GatedPlan pl;
+  int st = gated_plan(dims, checkpoints != nullptr, &pl);
+  if (st != SELSCAN_OK) return st;
+  const selscan_gated_dims& d = *dims;
+  const bool no_tokens = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16;
+  if (!lam || !dlam || (!no_tokens && (!x || !r || !g || !dy || !dx || !dr || !dg))) return SELSCAN_ERR_NULL;
+  if (!all_aligned({x, r, g, dy, dx, dr, dg}, bf16 ? 2 : 4) ||
+      !all_aligned({lam, initial_state, checkpoints, dlast_state, dlam, dinitial_state}, 4))
+    return SELSCAN_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (no_tokens) {                              // empty sums; the last state is the initial one
+    e = selscan::launch_fill_zero(dlam, d.dim, s);
+    if (e == hipSuccess && dinitial_state && d.batch > 0 && dinitial_state != dlast_state)
+      e = dlast_state ? selscan::launch_copy(dinitial_state, dlast_state, d.batch * d.dim, s)
+                      : selscan::launch_fill_zero(dinitial_state, d.batch * d.dim, s);
+    return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  }
+  char* ws = static_cast<char*>(workspace);
+  if (pl.bwd_bytes > 0 && ws != nullptr) {
+    if (workspace_bytes < pl.bwd_bytes || !aligned(ws, 256)) return SELSCAN_ERR_WORKSPACE;
+  } else if (pl.bwd_bytes > 0) {
+    void* mem = nullptr;
+    e = hipMallocAsync(&mem, pl.bwd_bytes, s);
+    if (e != hipSuccess) return hip_fail(e);
+    ws = static_cast<char*>(mem);
+  }
+  selscan::GatedParams p = gated_params(x, r, g, lam, reset, d, pl);
+  p.h0 = initial_state;
+  p.ckpt = const_cast<float*>(checkpoints);
+  if (checkpoints == nullptr) {
+    p.ckpt = reinterpret_cast<float*>(ws + pl.off_ckpt);
+    e = selscan::launch_gated_fwd(bf16, p, s);
+  }
+  p.dy = dy; p.dlast = dlast_state; p.dx = dx; p.dr = dr; p.dg = dg; p.dlam = dlam; p.dh0 = dinitial_state;
+  p.hbuf = reinterpret_cast<float*>(ws + pl.off_hbuf);
+  p.plam = reinterpret_cast<float*>(ws + pl.off_plam);
+  if (e == hipSuccess) e = selscan::launch_gated_bwd(bf16, p, s);
+  st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  if (workspace == nullptr && pl.bwd_bytes > 0) {
+    const hipError_t f = hipFreeAsync(ws, s);
+    if (st == SELSCAN_OK && f != hipSuccess) st = hip_fail(f);
+  }
+  return st;
+}
+
+int gated_scan_step(const void* x, const void* r, const void* g, const float* lam, void* y, float* state,
+                    const selscan_gated_dims* dims, void* stream) {
+  GatedPlan pl;
+  const int st = gated_plan(dims, true, &pl);
+  if (st != SELSCAN_OK) return st;
+  const selscan_gated_dims& d = *dims;
+  if (d.seqlen != 1) return SELSCAN_ERR_DIMS;
+  if (!gated_rows_apart(d)) return SELSCAN_ERR_UNSUPPORTED;
+  if (!lam || (d.batch > 0 && (!x || !r || !g || !y || !state))) return SELSCAN_ERR_NULL;
+  if (!all_aligned({x, r, g, y}, d.io_dtype == SELSCAN_BF16 ? 2 : 4) || !all_aligned({lam, state}, 4))
+    return SELSCAN_ERR_ALIGN;
+  if (d.batch == 0) return SELSCAN_OK;
+  selscan::GatedParams p = gated_params(x, r, g, lam, nullptr, d, pl);
+  p.y = y;
+  const hipError_t e = selscan::launch_gated_step(d.io_dtype == SELSCAN_BF16, p, state, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+// ---- the 8-bit state cache
+static int cache_check(const selscan_cache_dims* c, int64_t count, const int32_t* ids, const void* q,
+                       const float* scale, const int64_t* seed, selscan::CacheParams* out) {
+  if (!c) return SELSCAN_ERR_NULL;
+  if (c->abi_version != SELSCAN_ABI_VERSION) return SELSCAN_ERR_ABI;
+  if (c->slots < 0 || c->elems < 1 || c->row_len < 1 || count < 0) return SELSCAN_ERR_DIMS;
+  if (c->row_len > 128 || c->elems > (int64_t(1) << 31) - 1 || c->slots > (int64_t(1) << 31) - 1)
+    return SELSCAN_ERR_UNSUPPORTED;
+  const int64_t rows = (c->elems + c->row_len - 1) / c->row_len;
+  if (count > ((int64_t(1) << 32) - 1) / rows) return SELSCAN_ERR_UNSUPPORTED;   // 32-bit row numbers
+  if (!ids && count > c->slots) return SELSCAN_ERR_DIMS;                          // 0, 1, 2, ... must exist
+  if (count > 0 && c->slots > 0 && (!q || !scale)) return SELSCAN_ERR_NULL;
+  if (!all_aligned({scale, ids}, 4) || !all_aligned({seed}, 8)) return SELSCAN_ERR_ALIGN;
+  selscan::CacheParams p{};
+  p.q = static_cast<int8_t*>(const_cast<void*>(q));
+  p.scale = const_cast<float*>(scale);
+  p.seed = seed;
+  p.slots = c->slots; p.elems = c->elems; p.row_len = c->row_len; p.rows = rows; p.count = count;
+  *out = p;
+  return SELSCAN_OK;
+}
+
+int state_cache_write(const float* state, const int32_t* slot_ids, int64_t count, int8_t* q, float* scale,
+                      const int64_t* seed, const selscan_cache_dims* cache, void* stream) {
+  selscan::CacheParams p;
+  const int st = cache_check(cache, count, slot_ids, q, scale, seed, &p);
+  if (st != SELSCAN_OK) return st;
+  if (count == 0 || cache->slots == 0) return SELSCAN_OK;
+  if (!state) return SELSCAN_ERR_NULL;
+  if (!aligned(state, 4)) return SELSCAN_ERR_ALIGN;
+  p.write_slots = slot_ids;
+  const hipError_t e = selscan::launch_cache_write(state, p, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+int state_cache_read(const int8_t* q, const float* scale, const int32_t* slot_ids, int64_t count, void* out,
+                     int out_dtype, const selscan_cache_dims* cache, void* stream) {
+  selscan::CacheParams p;
+  const int st = cache_check(cache, count, slot_ids, q, scale, nullptr, &p);
+  if (st != SELSCAN_OK) return st;
+  if (out_dtype != SELSCAN_F32 && out_dtype != SELSCAN_BF16) return SELSCAN_ERR_UNSUPPORTED;
+  if (count == 0) return SELSCAN_OK;
+  if (!out) return SELSCAN_ERR_NULL;
+  if (!aligned(out, out_dtype == SELSCAN_BF16 ? 2 : 4)) return SELSCAN_ERR_ALIGN;
+  p.read_slots = slot_ids;
+  const hipError_t e = selscan::launch_cache_read(out_dtype == SELSCAN_BF16, out, p, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+// The cache of a decode step: both id arrays, and the layer's state layout.
+static int step_cache_check(const selscan_cache_dims* c, int64_t batch, int64_t elems, int64_t row_len,
+                            const int32_t* read_slots, const int32_t* write_slots, const void* q, const float* scale,
+                            const int64_t* seed, selscan::CacheParams* out) {
+  int st = cache_check(c, batch, write_slots, q, scale, seed, out);
+  if (st == SELSCAN_OK) st = cache_check(c, batch, read_slots, q, scale, seed, out);
+  if (st != SELSCAN_OK) return st;
+  if (c->elems != elems || c->row_len != row_len) return SELSCAN_ERR_DIMS;
+  out->read_slots = read_slots;
+  out->write_slots = write_slots;
+  return SELSCAN_OK;
+}
+
+int selective_scan_step_cached(const void* u, const void* delta, const float* delta_bias, const float* A,
+                               const void* B, const void* C, const float* Dskip, const void* z, void* y,
+                               int8_t* q, float* scale, const int32_t* read_slots, const int32_t* write_slots,
+                               const int64_t* seed, const selscan_dims* dims, const selscan_cache_dims* cache,
+                               void* stream) {
+  Plan plan;
+  int st = make_plan(dims, &plan);
+  if (st != SELSCAN_OK) return st;
+  if (dims->seqlen != 1) return SELSCAN_ERR_DIMS;
+  if (plan.ti) return SELSCAN_ERR_UNSUPPORTED;
+  selscan::CacheParams p;
+  st = step_cache_check(cache, dims->batch, dims->dim * dims->dstate, dims->dstate, read_slots, write_slots, q, scale,
+                        seed, &p);
+  if (st != SELSCAN_OK) return st;
+  st = check_pointers(u, delta, A, B, C, Dskip, z, y, nullptr, dims->io_dtype, dims->batch == 0);
+  if (st != SELSCAN_OK) return st;
+  if (delta_bias != nullptr && !aligned(delta_bias, 4)) return SELSCAN_ERR_ALIGN;
+  if (dims->batch == 0 || cache->slots == 0) return SELSCAN_OK;
+  selscan::StepParams s{};
+  s.u = u; s.delta = delta; s.A = A; s.B = B; s.C = C; s.Dskip = Dskip; s.z = z; s.y = y;
+  s.delta_bias = delta_bias;
+  s.euler = dims->discretization == SELSCAN_DISC_EULER ? 1 : 0;
+  s.softplus = dims->delta_softplus != 0 ? 1 : 0;
+  s.batch = dims->batch; s.D = dims->dim; s.N = dims->dstate;
+  s.u_sb = dims->u_sb; s.delta_sb = dims->delta_sb; s.z_sb = dims->z_sb; s.y_sb = dims->y_sb;
+  s.B_sb = dims->B_sb; s.C_sb = dims->C_sb;
+  const hipError_t e = selscan::launch_step_cached(plan.bf16, s, p, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+int selective_scan_ssd_step_cached(const void* x, const void* delta, const float* A, const void* B, const void* C,
+                                   const float* Dskip, const void* z, void* y, int8_t* q, float* scale,
+                                   const int32_t* read_slots, const int32_t* write_slots, const int64_t* seed,
+                                   const selscan_ssd_dims* dims, const selscan_cache_dims* cache, void* stream) {
+  SsdPlan pl;
+  int st = ssd_check(dims, &pl);
+  if (st != SELSCAN_OK) return st;
+  const selscan_ssd_dims& d = *dims;
+  if (d.seqlen != 1) return SELSCAN_ERR_DIMS;
+  selscan::CacheParams p;
+  st = step_cache_check(cache, d.batch, d.nheads * 64 * d.dstate, d.dstate, read_slots, write_slots, q, scale, seed, &p);
+  if (st != SELSCAN_OK) return st;
+  if (!A || (d.batch > 0 && (!x || !delta || !B || !C || !y))) return SELSCAN_ERR_NULL;
+  if (!all_aligned({delta}, 2) || !all_aligned({x, B, C, z, y}, 16) || !all_aligned({A, Dskip}, 4))
+    return SELSCAN_ERR_ALIGN;
+  if (d.batch == 0 || cache->slots == 0) return SELSCAN_OK;
+  selscan::SsdParams s{};
+  s.x = x; s.delta = delta; s.A = A; s.B = B; s.C = C; s.Dskip = Dskip; s.z = z; s.y = y;
+  s.batch = d.batch; s.L = 1; s.H = d.nheads; s.N = d.dstate;
+  s.euler = d.discretization == SELSCAN_DISC_EULER ? 1 : 0;
+  const hipError_t e = selscan::launch_ssd_step_cached(s, p, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
 }
 
 const char* selective_scan_strerror(int status) {

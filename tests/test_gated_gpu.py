@@ -1,0 +1,390 @@
+"""The gated linear recurrence on the GPU against its 64-bit statement.
+
+Tolerances, relative to the largest reference value.  fp32: each token's decay is one rounding
+(2^-25 at most, below one) and its logarithm carries about four ulp, so a state that remembers
+M = 1 / (1 - a) tokens is off by at most M 2^-25 + 2^-21; the decays drawn here keep M below
+3000, 1e-4, and gradients have the same walk twice, 2e-4.  bf16 adds half a step of the
+output, 2^-8.  dlam is compared with the sum of the magnitudes that it adds up."""
+import numpy as np
+import pytest
+
+from oracle import recurrent as orc
+
+pytestmark = pytest.mark.gpu
+
+TOL = {"f32": 1e-4, "bf16": 1e-4 + 2.0 ** -8}
+GTOL = {"f32": 2e-4, "bf16": 2e-4 + 2.0 ** -8}
+SIZES = [(1, 1, 1), (2, 2, 3), (1, 127, 3), (2, 128, 64), (2, 129, 65), (1, 256, 2), (3, 257, 130), (2, 1000, 70),
+         (1, 5000, 64), (5, 33, 258), (1, 8321, 5), (70, 3, 128)]
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def dev(a, io="f32"):
+    t = _torch()
+    if a is None:
+        return None
+    v = t.from_numpy(np.ascontiguousarray(a)).cuda()
+    return v.to(t.bfloat16) if io == "bf16" else v
+
+
+def host(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def bf(a, io):
+    """Values as the I/O type holds them."""
+    t = _torch()
+    a = np.asarray(a, np.float32)
+    return t.from_numpy(a).to(t.bfloat16).float().numpy() if io == "bf16" else a
+
+
+def inputs(B, L, D, io="f32", seed=0, reset=None):
+    rng = np.random.default_rng(seed)
+    x, r, g, dy = (bf(rng.standard_normal((B, L, D)), io) for _ in range(4))
+    lam = np.log(np.expm1(-np.log(rng.uniform(0.9, 0.9993, D)) / 8)).astype(np.float32)
+    h0, dlast = (rng.standard_normal((B, D)).astype(np.float32) for _ in range(2))
+    marks = {None: None, "some": rng.random((B, L)) < 0.02, "all": np.ones((B, L), bool),
+             "first": np.arange(L)[None].repeat(B, 0) == 0, "last": np.arange(L)[None].repeat(B, 0) == L - 1}[reset]
+    return dict(x=x, r=r, g=g, lam=lam, dy=dy, h0=h0, dlast=dlast, reset=marks)
+
+
+def close(got, ref, tol, what):
+    got = host(got) if hasattr(got, "detach") else got
+    assert got.shape == ref.shape, what
+    if ref.size == 0:
+        return
+    assert np.all(np.isfinite(got)), what
+    err, scale = np.abs(got - ref).max(), np.abs(ref).max()
+    print("%s: error %.2e of %.2e" % (what, err, tol * scale))
+    assert err <= tol * scale, "%s: %.3e > %.3e" % (what, err, tol * scale)
+
+
+def on_gpu(i, io):
+    """The inputs as GPU tensors; a call on a stream of its own finds them written and keeps them."""
+    v = {k: dev(a, io if k in ("x", "r", "g", "dy") else "f32") for k, a in i.items() if k != "held"}
+    _torch().cuda.synchronize()
+    i["held"] = (i.get("held"), v)
+    return v
+
+
+def forward(i, io, h0=True, ckpt=True, **kw):
+    import selective_state_space_s6_amd as ss
+    v = on_gpu(i, io)
+    marks = ss.gated_checkpoints(v["x"]) if ckpt else None
+    y, last = ss.gated_scan_fwd(v["x"], v["r"], v["g"], v["lam"], reset=v["reset"], initial_state=v["h0"] if h0 else None,
+                                return_last_state=True, checkpoints=marks, **kw)
+    return y, last, marks
+
+
+def backward(i, io, h0=True, dlast=True, marks=None, **kw):
+    import selective_state_space_s6_amd as ss
+    v = on_gpu(i, io)
+    return ss.gated_scan_bwd(v["x"], v["r"], v["g"], v["lam"], dy=v["dy"], reset=v["reset"],
+                             initial_state=v["h0"] if h0 else None, dlast_state=v["dlast"] if dlast else None,
+                             checkpoints=marks, **kw)
+
+
+def check_forward(i, io, got, h0=True, what=""):
+    y, last, marks = got
+    y_ref, l_ref = orc.gated_fwd(i["x"], i["r"], i["g"], i["lam"], h0=i["h0"] if h0 else None, reset=i["reset"])
+    close(y, y_ref, TOL[io], what + " y")
+    close(last, l_ref, TOL["f32"], what + " last_state")
+    if marks is not None:
+        first = (i["h0"] if h0 else np.zeros_like(i["h0"]))[:, None]
+        close(marks, np.concatenate([first, y_ref], 1)[:, :-1:128], TOL["f32"], what + " checkpoints")
+
+
+def check_backward(i, io, g, h0=True, dlast=True, what=""):
+    ref = orc.gated_bwd(i["x"], i["r"], i["g"], i["lam"], i["dy"], h0=i["h0"] if h0 else None, reset=i["reset"],
+                        dlast=i["dlast"] if dlast else None)
+    for k in ("dx", "dr", "dg"):
+        close(g[k], ref[k], GTOL[io], what + " " + k)
+    err = np.abs(host(g["dlam"]) - ref["dlam"])
+    assert np.all(err <= 2e-4 * ref["dlam_abs"]), "%s dlam: %.3e" % (what, (err / ref["dlam_abs"]).max())
+    assert ("dinitial_state" in g) == h0
+    if h0:
+        close(g["dinitial_state"], ref["dinitial_state"], GTOL["f32"], what + " dinitial_state")
+
+
+@pytest.mark.parametrize("reset", [None, "some", "all", "first", "last"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", SIZES)
+def test_forward(size, io, reset):
+    i = inputs(*size, io=io, seed=sum(size), reset=reset)
+    check_forward(i, io, forward(i, io), what=str(size))
+
+
+@pytest.mark.parametrize("reset", [None, "some", "all", "first", "last"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", SIZES)
+def test_backward(size, io, reset):
+    i = inputs(*size, io=io, seed=sum(size) + 1, reset=reset)
+    _, _, marks = forward(i, io)
+    check_backward(i, io, backward(i, io, marks=marks), what=str(size))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 129, 65), (1, 1000, 8)])
+def test_without_the_optional_arguments(size, io):
+    i = inputs(*size, io=io, seed=9)
+    check_forward(i, io, forward(i, io, h0=False, ckpt=False), h0=False)
+    g = backward(i, io, h0=False, dlast=False)                 # checkpoints formed again
+    check_backward(i, io, g, h0=False, dlast=False)
+    _, _, marks = forward(i, io, h0=False)
+    same = backward(i, io, h0=False, dlast=False, marks=marks)
+    assert all(_torch().equal(g[k], same[k]) for k in g)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_strided_inputs(io):
+    """x, r and g as column blocks of one projection at odd offsets, y a block of a wider buffer
+    whose other columns keep what they held, dy expanded over the batch."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, L, D = 2, 300, 75
+    i = inputs(B, L, D, io=io, seed=4, reset="some")
+    proj = t.zeros((B, L, 3 * D + 7), dtype=t.bfloat16 if io == "bf16" else t.float32, device="cuda")
+    views = {}
+    for n, k in enumerate(("x", "r", "g")):
+        views[k] = proj[..., 1 + n * (D + 1):1 + n * (D + 1) + D]
+        views[k].copy_(dev(i[k], io))
+    wide = t.full((B, L, D + 5), 7.0, dtype=proj.dtype, device="cuda")
+    y, last = ss.gated_scan_fwd(views["x"], views["r"], views["g"], dev(i["lam"]), y=wide[..., 2:2 + D],
+                                reset=dev(i["reset"]), initial_state=dev(i["h0"]), return_last_state=True)
+    check_forward(i, io, (y, last, None))
+    assert t.all(wide[..., :2] == 7) and t.all(wide[..., 2 + D:] == 7)
+    i["dy"] = i["dy"][:1].repeat(B, 0)
+    g = ss.gated_scan_bwd(views["x"], views["r"], views["g"], dev(i["lam"]), dy=dev(i["dy"][:1], io).expand(B, L, D),
+                          reset=dev(i["reset"]), initial_state=dev(i["h0"]), dlast_state=dev(i["dlast"]))
+    check_backward(i, io, g)
+
+
+@pytest.mark.parametrize("lam", [-100.0, -30.0, -16.0, -14.0, -3.0, 0.0, 5.0, 30.0])
+@pytest.mark.parametrize("r", [-120.0, -20.0, 0.0, 20.0, 120.0])
+def test_extreme_gates(lam, r):
+    """Decays from exactly one to exactly zero; gates saturated both ways."""
+    i = inputs(2, 200, 6, seed=6)
+    i["lam"][:] = lam
+    i["r"][:] = r
+    i["g"][..., ::2] *= 60
+    check_forward(i, "f32", forward(i, "f32"))
+    _, _, marks = forward(i, "f32")
+    ref = orc.gated_bwd(i["x"], i["r"], i["g"], i["lam"], i["dy"], h0=i["h0"], dlast=i["dlast"])
+    g = backward(i, "f32", marks=marks)
+    # A gate below 2^-126 is zero in fp32.  Exactly, m = sqrt(2 k s) and la/m = sqrt(k s / 2) are
+    # then below sqrt(480) 2^-63 = 2.4e-18 (k = 240 at lam = 30); times adjoints below 100 and v
+    # below 5 each gradient is off by less than 1.2e-15, a sum of 400 of them by 5e-13.
+    for k in ("dx", "dr", "dg", "dinitial_state"):
+        err = np.abs(host(g[k]) - ref[k]).max()
+        assert np.all(np.isfinite(host(g[k]))) and err <= 2e-4 * np.abs(ref[k]).max() + 1.2e-15, (k, err)
+    assert np.all(np.abs(host(g["dlam"]) - ref["dlam"]) <= 2e-4 * ref["dlam_abs"] + 5e-13)
+
+
+def test_not_finite_stays_in_its_channel_and_sequence():
+    i = inputs(2, 400, 70, seed=7)
+    i["reset"] = np.zeros((2, 400), bool)
+    i["reset"][:, 250] = True
+    i["x"][0, 100, 3] = np.inf
+    i["x"][1, 100, 66] = np.nan
+    i["h0"][1, 10] = np.inf
+    y, last, _ = forward(i, "f32")
+    y = host(y)
+    hit = np.zeros_like(y, bool)
+    hit[0, 100:250, 3] = hit[1, 100:250, 66] = hit[1, :250, 10] = True
+    # h0 = inf through decays below one stays inf until the sequence ends
+    assert np.array_equal(~np.isfinite(y), hit)
+    assert np.all(np.isfinite(host(last)))
+    # gradients: a token's adjoint comes from later tokens of its sequence, its h from earlier ones
+    i = inputs(2, 400, 70, seed=7)
+    i["reset"] = np.zeros((2, 400), bool)
+    i["reset"][:, 250] = True
+    i["dy"][0, 300, 3] = np.inf
+    i["h0"][1, 10] = np.nan
+    _, _, marks = forward(i, "f32")
+    g = backward(i, "f32", marks=marks)
+    bad = np.zeros((2, 400, 70), bool)
+    bad[0, 250:301, 3] = True
+    assert np.array_equal(~np.isfinite(host(g["dx"])), bad) and np.array_equal(~np.isfinite(host(g["dg"])), bad)
+    bad[0, 250, 3] = False                              # a first token's decay gate has no gradient
+    bad[1, :250, 10] = True
+    assert np.array_equal(~np.isfinite(host(g["dr"])), bad)
+    assert np.all(np.isfinite(host(g["dinitial_state"])))
+    assert np.array_equal(np.flatnonzero(~np.isfinite(host(g["dlam"]))), [3, 10])
+
+
+@pytest.mark.parametrize("cut", [1, 63, 128, 300])
+def test_continuing_from_a_state(cut):
+    import selective_state_space_s6_amd as ss
+    i = inputs(2, 500, 40, seed=8)
+    whole, last, _ = forward(i, "f32")
+    part = {k: dev(i[k]) for k in ("x", "r", "g")}
+    state = dev(i["h0"])
+    ys = []
+    for lo, hi in ((0, cut), (cut, 500)):                       # in place: the state is both ends
+        y, _ = ss.gated_scan_fwd(*(part[k][:, lo:hi] for k in ("x", "r", "g")), dev(i["lam"]), initial_state=state,
+                                 last_state=state)
+        ys.append(y)
+    close(_torch().cat(ys, 1), host(whole), 2e-6, "y")
+    close(state, host(last), 2e-6, "state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 1), (3, 7), (2, 64), (5, 1001), (130, 256)])
+def test_steps_are_the_scan(size, io):
+    import selective_state_space_s6_amd as ss
+    B, D = size
+    i = inputs(B, 6, D, io=io, seed=10)
+    y_ref, l_ref = orc.gated_fwd(i["x"], i["r"], i["g"], i["lam"], h0=i["h0"])
+    state = dev(i["h0"])
+    t = {k: dev(i[k], io) for k in ("x", "r", "g")}
+    ys = [ss.gated_scan_step(*(t[k][:, n] for k in ("x", "r", "g")), dev(i["lam"]), state=state) for n in range(6)]
+    close(_torch().stack(ys, 1), y_ref, TOL[io], "y")
+    close(state, l_ref, TOL["f32"], "state")
+
+
+def test_empty():
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    lam, h0 = t.zeros(5, device="cuda"), t.randn(3, 5, device="cuda")
+    e = t.empty(3, 0, 5, device="cuda")
+    y, last = ss.gated_scan_fwd(e, e, e, lam, initial_state=h0, return_last_state=True)
+    assert y.shape == (3, 0, 5) and t.equal(last, h0)
+    _, last = ss.gated_scan_fwd(e, e, e, lam, return_last_state=True)
+    assert not last.any()
+    g = ss.gated_scan_bwd(e, e, e, lam, dy=e, dlast_state=h0, initial_state=h0)
+    assert not g["dlam"].any() and t.equal(g["dinitial_state"], h0) and g["dx"].shape == (3, 0, 5)
+    n = t.empty(0, 7, 5, device="cuda")
+    y, last = ss.gated_scan_fwd(n, n, n, lam, return_last_state=True)
+    assert y.shape == (0, 7, 5) and last.shape == (0, 5)
+    g = ss.gated_scan_bwd(n, n, n, lam, dy=n)
+    assert not g["dlam"].any()
+    s = t.empty(0, 5, device="cuda")
+    assert ss.gated_scan_step(s, s, s, lam, state=s).shape == (0, 5)
+
+
+@pytest.mark.parametrize("size", [(2, 3000, 130), (1, 20000, 64), (3, 100, 7)])
+def test_two_runs_give_the_same_bits(size):
+    i = inputs(*size, io="bf16", seed=11, reset="some")
+    t = _torch()
+    a, b = forward(i, "bf16"), forward(i, "bf16")
+    assert all(t.equal(p, q) for p, q in zip(a, b))
+    a, b = backward(i, "bf16", marks=a[2]), backward(i, "bf16", marks=b[2])
+    assert all(t.equal(a[k], b[k]) for k in a)
+
+
+def test_on_another_stream_and_with_a_workspace():
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    i = inputs(2, 2000, 130, seed=12)
+    base, glast, marks = forward(i, "f32")
+    grads = backward(i, "f32", marks=marks)
+    d = ss.GatedDims()
+    ss.lib().gated_scan_dims_init(ss.ctypes.byref(d), ss.SELSCAN_F32, 2, 2000, 130)
+    need = max(ss.lib().gated_scan_workspace_size(ss.ctypes.byref(d)),
+               ss.lib().gated_scan_bwd_workspace_size(ss.ctypes.byref(d), 0), 1)
+    ws = t.full((need,), 255, dtype=t.uint8, device="cuda")     # what a workspace holds does not matter
+    side = t.cuda.Stream()
+    t.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        y, last, marks = forward(i, "f32", workspace=ws, stream=stream)
+        g = backward(i, "f32", workspace=ws, stream=stream)
+        t.cuda.synchronize()
+        assert t.equal(y, base) and t.equal(last, glast) and all(t.equal(g[k], grads[k]) for k in g)
+        ws.fill_(170)
+        t.cuda.synchronize()
+
+
+def test_the_library_takes_its_own_workspace():
+    """The C entry points with no workspace."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    i = inputs(2, 2000, 130, seed=12)
+    base, _, marks = forward(i, "f32")
+    grads = backward(i, "f32", marks=marks)
+    d = ss.GatedDims()
+    ref = ss.ctypes.byref(d)
+    ss.lib().gated_scan_dims_init(ref, ss.SELSCAN_F32, 2, 2000, 130)
+    v = {k: dev(i[k]) for k in ("x", "r", "g", "lam", "h0", "dy", "dlast")}
+    P = lambda a: a.data_ptr()                                                          # noqa: E731
+    y = t.empty_like(base)
+    s = t.cuda.current_stream().cuda_stream
+    st = ss.lib().gated_scan_fwd(P(v["x"]), P(v["r"]), P(v["g"]), P(v["lam"]), None, P(y), P(v["h0"]), None, None, ref,
+                                 None, 0, s)
+    out = {k: t.empty_like(a) for k, a in grads.items()}
+    st2 = ss.lib().gated_scan_bwd(P(v["x"]), P(v["r"]), P(v["g"]), P(v["lam"]), None, P(v["h0"]), None, P(v["dy"]),
+                                  P(v["dlast"]), P(out["dx"]), P(out["dr"]), P(out["dg"]), P(out["dlam"]),
+                                  P(out["dinitial_state"]), ref, None, 0, s)
+    t.cuda.synchronize()
+    assert (st, st2) == (0, 0) and t.equal(y, base) and all(t.equal(out[k], grads[k]) for k in out)
+
+
+def test_captured_and_replayed():
+    """A training pass in a graph, replayed on new inputs between eager calls."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    i = inputs(2, 1500, 66, io="bf16", seed=13, reset="some")
+    v = {k: dev(i[k], "bf16" if k in ("x", "r", "g", "dy") else "f32") for k in ("x", "r", "g", "dy", "lam", "h0", "dlast", "reset")}
+
+    def both():
+        marks = ss.gated_checkpoints(v["x"])
+        y, last = ss.gated_scan_fwd(v["x"], v["r"], v["g"], v["lam"], reset=v["reset"], initial_state=v["h0"],
+                                    return_last_state=True, checkpoints=marks)
+        g = ss.gated_scan_bwd(v["x"], v["r"], v["g"], v["lam"], dy=v["dy"], dlast_state=v["dlast"], reset=v["reset"],
+                              initial_state=v["h0"], checkpoints=marks)
+        return [y, last] + [g[k] for k in sorted(g)]
+
+    both()
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        out = both()
+    for seed in range(20, 25):
+        new = inputs(2, 1500, 66, io="bf16", seed=seed)
+        for k in ("x", "r", "g", "dy"):
+            v[k].copy_(dev(new[k], "bf16"))
+        graph.replay()
+        t.cuda.synchronize()
+        ref = both()
+        t.cuda.synchronize()
+        assert all(t.equal(a, b) for a, b in zip(out, ref)), seed
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, workspaces of their own."""
+    t = _torch()
+    i, j = inputs(2, 6000, 130, seed=14), inputs(3, 5000, 70, seed=15)
+    ref_i, ref_j = forward(i, "f32")[0], forward(j, "f32")[0]
+    a, b = t.cuda.Stream(), t.cuda.Stream()
+    t.cuda.synchronize()
+    import selective_state_space_s6_amd as ss
+    vi, vj = on_gpu(i, "f32"), on_gpu(j, "f32")
+    call = lambda v, s: ss.gated_scan_fwd(v["x"], v["r"], v["g"], v["lam"], initial_state=v["h0"], stream=s)[0]   # noqa: E731
+    for _ in range(5):
+        got = [call(vi, a), call(vj, b), call(vi, a), call(vj, b)]
+        t.cuda.synchronize()
+        assert t.equal(got[0], ref_i) and t.equal(got[1], ref_j) and t.equal(got[2], ref_i) and t.equal(got[3], ref_j)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements a tensor: the last row's channels against the reference."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, L, D = 3, 140000, 5200
+    gen = t.Generator(device="cuda").manual_seed(3)
+    x, r, g = (t.empty((B, L, D), dtype=t.bfloat16, device="cuda").normal_(generator=gen) for _ in range(3))
+    lam = t.linspace(-7, -4, D, device="cuda")
+    y, last = ss.gated_scan_fwd(x, r, g, lam, return_last_state=True)
+    ch = [0, 1, 2599, D - 2, D - 1]
+    tail = slice(L - 9000, L)      # the first of these states is off by what 9000 decays leave of it: nothing
+    pick = lambda a: host(a[2:, tail][..., ch])                                          # noqa: E731
+    lam_h = host(lam)[ch] + 0.0
+    state = host(y[2:, L - 9001][..., ch])
+    y_ref, l_ref = orc.gated_fwd(pick(x), pick(r), pick(g), lam_h, h0=state)
+    # the state taken over is a bf16 value: half a step more, until it has decayed
+    close(y[2:, tail][..., ch], y_ref, TOL["bf16"] + 2.0 ** -8, "y")
+    got, slow = host(last[2:, ch]), np.array([0, 1])
+    assert np.abs(got - l_ref).max() <= (1e-4 + 2.0 ** -8 * np.exp(-8 * 9000 * 0.4 * np.log1p(np.exp(-7)))) * np.abs(l_ref).max() + 1e-4
