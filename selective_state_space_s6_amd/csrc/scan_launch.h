@@ -246,9 +246,18 @@ struct GatedParams {
   int64_t x_sb, x_sl, r_sb, r_sl, g_sb, g_sl, y_sb, y_sl, reset_sb;
   int64_t ntiles;        // ceil(L / SELSCAN_GATED_TILE)
   float c;
+  uint64_t* links;       // workspace: gated_link_words() words, or null (one chunk)
+  int32_t n_chunks;      // ceil(L / kGatedChunk)
+  int32_t vec;           // 1: D and every stride even, pointers aligned to channel pairs
   float* hbuf;           // workspace
   float* plam;           // workspace: partial sums of dlam
 };
+constexpr int kGatedChunk = 256;       // tokens of a workgroup
+// words of the links between chunks: the ticket (in a line of its own), a map per chunk and an
+// end state per 16 chunks, for every 64 channels
+constexpr int64_t gated_link_words(int64_t batch, int64_t D, int64_t n_chunks) {
+  return 64 + batch * ((D + 63) / 64) * 64 * (n_chunks + n_chunks / 16);
+}
 hipError_t launch_gated_fwd(bool bf16, const GatedParams& p, hipStream_t stream);
 hipError_t launch_gated_bwd(bool bf16, const GatedParams& p, hipStream_t stream);
 hipError_t launch_gated_step(bool bf16, const GatedParams& p, float* state, hipStream_t stream);

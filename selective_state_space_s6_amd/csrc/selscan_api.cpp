@@ -942,8 +942,8 @@ int selective_scan_ssd_fwd(const void* x, const void* delta, const float* A, con
 
 // ---- the gated linear recurrence
 struct GatedPlan {
-  int64_t ntiles = 0;
-  size_t fwd_bytes = 0;                         // workspace of the forward pass
+  int64_t ntiles = 0, n_chunks = 0;
+  size_t fwd_bytes = 0;                         // workspace of the forward pass: the links between chunks
   size_t off_ckpt = 0, off_hbuf = 0, off_plam = 0, bwd_bytes = 0;
 };
 
@@ -965,11 +965,14 @@ static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan*
   if (d.batch > kMaxItems || d.seqlen > (int64_t(1) << 40)) return SELSCAN_ERR_UNSUPPORTED;
   GatedPlan p;
   p.ntiles = (d.seqlen + SELSCAN_GATED_TILE - 1) / SELSCAN_GATED_TILE;
+  p.n_chunks = (d.seqlen + selscan::kGatedChunk - 1) / selscan::kGatedChunk;
   if (d.batch > 0 && p.ntiles > 0 && p.ntiles > kMaxItems / d.batch / ((d.dim + 63) / 64)) return SELSCAN_ERR_UNSUPPORTED;
   if (d.batch * d.seqlen > 0) {
     auto al = [](int64_t x) { return size_t(round_up(x, 256)); };
     const int64_t f = int64_t(sizeof(float));
-    size_t off = 0;
+    if (p.n_chunks > 1) p.fwd_bytes = al(8 * selscan::gated_link_words(d.batch, d.dim, p.n_chunks));
+    size_t off = p.fwd_bytes;
+    p.off_ckpt = off;
     if (!have_ckpt) off += al(f * d.batch * p.ntiles * d.dim);
     p.off_hbuf = off;
     off += al(f * d.batch * SELSCAN_GATED_TILE * d.dim);
@@ -994,8 +997,19 @@ static selscan::GatedParams gated_params(const void* x, const void* r, const voi
   p.x_sb = d.x_sb; p.x_sl = d.x_sl; p.r_sb = d.r_sb; p.r_sl = d.r_sl; p.g_sb = d.g_sb; p.g_sl = d.g_sl;
   p.y_sb = d.y_sb; p.y_sl = d.y_sl; p.reset_sb = d.reset_sb;
   p.ntiles = pl.ntiles;
+  p.n_chunks = int32_t(pl.n_chunks);
   p.c = d.decay_c;
   return p;
+}
+
+// Channel pairs can be moved whole: even sizes and strides, pointers on pairs.
+static bool gated_pairs(const selscan_gated_dims& d, std::initializer_list<const void*> ptrs) {
+  const size_t pair = d.io_dtype == SELSCAN_BF16 ? 4 : 8;
+  for (const void* q : ptrs)
+    if (q && !aligned(q, pair)) return false;
+  for (int64_t v : {d.dim, d.x_sb, d.x_sl, d.r_sb, d.r_sl, d.g_sb, d.g_sl, d.y_sb, d.y_sl})
+    if (v % 2 != 0) return false;
+  return true;
 }
 
 static bool all_aligned(std::initializer_list<const void*> ptrs, size_t a) {
@@ -1049,10 +1063,24 @@ int gated_scan_fwd(const void* x, const void* r, const void* g, const float* lam
                         : selscan::launch_fill_zero(last_state, d.batch * d.dim, s);
     return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   }
+  void* ws = workspace;
+  if (pl.fwd_bytes > 0 && ws != nullptr) {
+    if (workspace_bytes < pl.fwd_bytes || !aligned(ws, 256)) return SELSCAN_ERR_WORKSPACE;
+  } else if (pl.fwd_bytes > 0) {
+    e = hipMallocAsync(&ws, pl.fwd_bytes, s);
+    if (e != hipSuccess) return hip_fail(e);
+  }
   selscan::GatedParams p = gated_params(x, r, g, lam, reset, d, pl);
   p.y = y; p.h0 = initial_state; p.last = last_state; p.ckpt = checkpoints;
+  p.links = pl.fwd_bytes > 0 ? static_cast<uint64_t*>(ws) : nullptr;
+  p.vec = gated_pairs(d, {x, r, g, y});
   e = selscan::launch_gated_fwd(d.io_dtype == SELSCAN_BF16, p, s);
-  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  if (workspace == nullptr && pl.fwd_bytes > 0) {
+    const hipError_t f = hipFreeAsync(ws, s);
+    if (st == SELSCAN_OK && f != hipSuccess) st = hip_fail(f);
+  }
+  return st;
 }
 
 int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam, const uint8_t* reset,
@@ -1091,6 +1119,8 @@ int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam
   p.ckpt = const_cast<float*>(checkpoints);
   if (checkpoints == nullptr) {
     p.ckpt = reinterpret_cast<float*>(ws + pl.off_ckpt);
+    p.links = pl.fwd_bytes > 0 ? reinterpret_cast<uint64_t*>(ws) : nullptr;
+    p.vec = gated_pairs(d, {x, r, g});
     e = selscan::launch_gated_fwd(bf16, p, s);
   }
   p.dy = dy; p.dlast = dlast_state; p.dx = dx; p.dr = dr; p.dg = dg; p.dlam = dlam; p.dh0 = dinitial_state;
