@@ -943,7 +943,7 @@ int selective_scan_ssd_fwd(const void* x, const void* delta, const float* A, con
 // ---- the gated linear recurrence
 struct GatedPlan {
   int64_t ntiles = 0, n_chunks = 0;
-  size_t fwd_bytes = 0;                         // workspace of the forward pass: the links between chunks
+  size_t link_bytes = 0, fwd_bytes = 0;         // workspace of the forward pass: links between chunks, [D] floats
   size_t off_ckpt = 0, off_hbuf = 0, off_plam = 0, bwd_bytes = 0;
 };
 
@@ -965,12 +965,14 @@ static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan*
   if (d.batch > kMaxItems || d.seqlen > (int64_t(1) << 40)) return SELSCAN_ERR_UNSUPPORTED;
   GatedPlan p;
   p.ntiles = (d.seqlen + SELSCAN_GATED_TILE - 1) / SELSCAN_GATED_TILE;
-  p.n_chunks = (d.seqlen + selscan::kGatedChunk - 1) / selscan::kGatedChunk;
-  if (d.batch > 0 && p.ntiles > 0 && p.ntiles > kMaxItems / d.batch / ((d.dim + 63) / 64)) return SELSCAN_ERR_UNSUPPORTED;
+  const int64_t chunk = selscan::gated_chunk(d.io_dtype == SELSCAN_BF16);
+  p.n_chunks = (d.seqlen + chunk - 1) / chunk;
+  if (d.batch > 0 && p.n_chunks > kMaxItems / (d.batch * ((d.dim + 127) / 128) + 32)) return SELSCAN_ERR_UNSUPPORTED;
   if (d.batch * d.seqlen > 0) {
     auto al = [](int64_t x) { return size_t(round_up(x, 256)); };
     const int64_t f = int64_t(sizeof(float));
-    if (p.n_chunks > 1) p.fwd_bytes = al(8 * selscan::gated_link_words(d.batch, d.dim, p.n_chunks));
+    p.link_bytes = p.n_chunks > 1 ? al(8 * selscan::gated_link_words(d.batch, d.dim, p.n_chunks)) : 0;
+    p.fwd_bytes = p.link_bytes + al(f * d.dim);
     size_t off = p.fwd_bytes;
     p.off_ckpt = off;
     if (!have_ckpt) off += al(f * d.batch * p.ntiles * d.dim);
@@ -1000,6 +1002,11 @@ static selscan::GatedParams gated_params(const void* x, const void* r, const voi
   p.n_chunks = int32_t(pl.n_chunks);
   p.c = d.decay_c;
   return p;
+}
+
+static int compute_units_or_default(hipStream_t stream) {
+  const int n = compute_units(stream);
+  return n > 0 ? n : 256;
 }
 
 // Channel pairs can be moved whole: even sizes and strides, pointers on pairs.
@@ -1072,9 +1079,10 @@ int gated_scan_fwd(const void* x, const void* r, const void* g, const float* lam
   }
   selscan::GatedParams p = gated_params(x, r, g, lam, reset, d, pl);
   p.y = y; p.h0 = initial_state; p.last = last_state; p.ckpt = checkpoints;
-  p.links = pl.fwd_bytes > 0 ? static_cast<uint64_t*>(ws) : nullptr;
+  p.links = pl.link_bytes > 0 ? static_cast<uint64_t*>(ws) : nullptr;
+  p.kd = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.link_bytes);
   p.vec = gated_pairs(d, {x, r, g, y});
-  e = selscan::launch_gated_fwd(d.io_dtype == SELSCAN_BF16, p, s);
+  e = selscan::launch_gated_fwd(d.io_dtype == SELSCAN_BF16, p, compute_units_or_default(s), s);
   st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   if (workspace == nullptr && pl.fwd_bytes > 0) {
     const hipError_t f = hipFreeAsync(ws, s);
@@ -1119,9 +1127,10 @@ int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam
   p.ckpt = const_cast<float*>(checkpoints);
   if (checkpoints == nullptr) {
     p.ckpt = reinterpret_cast<float*>(ws + pl.off_ckpt);
-    p.links = pl.fwd_bytes > 0 ? reinterpret_cast<uint64_t*>(ws) : nullptr;
+    p.links = pl.link_bytes > 0 ? reinterpret_cast<uint64_t*>(ws) : nullptr;
+    p.kd = reinterpret_cast<float*>(ws + pl.link_bytes);
     p.vec = gated_pairs(d, {x, r, g});
-    e = selscan::launch_gated_fwd(bf16, p, s);
+    e = selscan::launch_gated_fwd(bf16, p, compute_units_or_default(s), s);
   }
   p.dy = dy; p.dlast = dlast_state; p.dx = dx; p.dr = dr; p.dg = dg; p.dlam = dlam; p.dh0 = dinitial_state;
   p.hbuf = reinterpret_cast<float*>(ws + pl.off_hbuf);
