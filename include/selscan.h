@@ -411,7 +411,7 @@ typedef struct selscan_gated_dims {
 } selscan_gated_dims;
 
 /* Tokens between two checkpoints of the state (gated_scan_fwd, gated_scan_bwd). */
-#define SELSCAN_GATED_TILE 128
+#define SELSCAN_GATED_TILE 64
 
 /* Fill *dims for contiguous x, r, g, y [batch][seqlen][dim] and reset [batch][seqlen];
  * decay_c = 8.  Never fails for a non-NULL dims. */

@@ -586,7 +586,7 @@ class CacheDims(ctypes.Structure):
                 ("elems", ctypes.c_int64), ("row_len", ctypes.c_int64)]
 
 
-GATED_TILE = 128          # SELSCAN_GATED_TILE: tokens between two checkpoints
+GATED_TILE = 64          # SELSCAN_GATED_TILE: tokens between two checkpoints
 CACHE_ROW = 64            # row length of a [D] state (the gated recurrence's) in the state cache
 
 

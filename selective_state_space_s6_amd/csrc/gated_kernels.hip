@@ -1,4 +1,6 @@
 // gated_kernels.hip -- the gated linear recurrence: forward, backward and decode step.
+#include <type_traits>
+
 #include "gated_device.h"
 
 #include "scan_launch.h"
@@ -33,6 +35,8 @@ template <> struct pair_io<float> {
     if constexpr (VEC) return __builtin_bit_cast(raw_t, __builtin_amdgcn_raw_buffer_load_b64(r, o0, row, 0));
     else return raw_t{__builtin_amdgcn_raw_buffer_load_b32(r, o0, row, 0), __builtin_amdgcn_raw_buffer_load_b32(r, o1, row, 0)};
   }
+  // the compiler no longer knows what v holds, so nothing formed from it before is kept for after
+  static __device__ __forceinline__ void forget(raw_t& v) { asm("" : "+v"(v)); }
   static __device__ __forceinline__ float lo(raw_t v) { return __uint_as_float(v.x); }
   static __device__ __forceinline__ float hi(raw_t v) { return __uint_as_float(v.y); }
   template <bool VEC>
@@ -55,6 +59,7 @@ template <> struct pair_io<uint16_t> {
     else return uint32_t(__builtin_amdgcn_raw_buffer_load_b16(r, o0, row, 0)) |
                 (uint32_t(__builtin_amdgcn_raw_buffer_load_b16(r, o1, row, 0)) << 16);
   }
+  static __device__ __forceinline__ void forget(raw_t& v) { asm("" : "+v"(v)); }
   static __device__ __forceinline__ float lo(raw_t v) { return __uint_as_float(v << 16); }
   static __device__ __forceinline__ float hi(raw_t v) { return __uint_as_float(v & 0xffff0000u); }
   template <bool VEC>
@@ -70,7 +75,7 @@ template <> struct pair_io<uint16_t> {
   }
 };
 
-// The links between the chunks of one chain (a batch row's 64 channels), in the workspace: zero
+// The links between the chunks of one chain (a batch row's 128 channels), in the workspace: zero
 // until written, each word whole or absent, so a reader needs no other order between writes.
 //   map [items][2][64]: the chunk's map h -> A h + H as {A with its sign bit set, H} (A >= 0),
 //     the even channels before the odd ones;
@@ -99,6 +104,48 @@ template <bool CUT> __device__ __forceinline__ float through(float A, float H, f
   return CUT && A == 0.f ? H : v;
 }
 
+// The links of one chunk, the pos-th of its chain (counted from the end in the backward pass).
+struct Link {
+  uint64_t* map;                           // of this chunk and lane
+  uint64_t* end;                           // of this chunk's group
+  int64_t next;                            // words between a chain's chunks
+  int pos, in_group;
+  bool last;
+  __device__ __forceinline__ Link(const GatedParams& p, uint32_t order, uint32_t chain, uint32_t chains, int lane) {
+    next = int64_t(chains) * kCh;
+    uint64_t* const base = p.links + kTicketWords + int64_t(chain) * kCh + lane;
+    map = base + order * next;
+    end = base + (int64_t(p.n_chunks) + order / kLinkGroup) * next;
+    pos = int(order);
+    in_group = pos % kLinkGroup;
+    last = pos == p.n_chunks - 1;
+  }
+  __device__ __forceinline__ void publish(float A0, float A1, float H0, float H1) const {
+    if (last) return;
+    put_word(map, __float_as_uint(A0) | 0x80000000u, H0);
+    put_word(map + 64, __float_as_uint(A1) | 0x80000000u, H1);
+  }
+  __device__ __forceinline__ void publish_end(float h0, float h1) const {
+    if (last || in_group != kLinkGroup - 1) return;
+    put_word(end, 1u, h0);
+    put_word(end + 64, 1u, h1);
+  }
+  // Wavefront 0 reads the state behind the group before (none: zero, the first chunk's map
+  // takes nothing from it), wavefront j the map of the group's chunk j - 1.
+  __device__ __forceinline__ void read(int wave, float4* to) const {
+    if (pos == 0 || wave > in_group) return;
+    if (wave == 0 && pos < kLinkGroup) {
+      *to = make_float4(0.f, 0.f, 0.f, 0.f);
+      return;
+    }
+    const uint64_t* const q = wave == 0 ? end - next : map - (in_group - wave + 1) * next;
+    const uint64_t f0 = get_word(q), f1 = get_word(q + 64);
+    const uint64_t w0 = wait_word(q, f0), w1 = wait_word(q + 64, f1);
+    *to = make_float4(fabsf(__uint_as_float(uint32_t(w0 >> 32))), fabsf(__uint_as_float(uint32_t(w1 >> 32))),
+                      __uint_as_float(uint32_t(w0)), __uint_as_float(uint32_t(w1)));
+  }
+};
+
 // What a ticket stands for: one chunk of one chain.  Tickets run over all chains' first chunks,
 // then their second ones, and so on.
 struct Chunk {
@@ -106,6 +153,12 @@ struct Chunk {
   int64_t t0;
   int rest;                                // tokens
 };
+// c softplus(lam) of a channel, zero behind the last
+__device__ __forceinline__ float gated_rate(const GatedParams& p, int c) {
+  if (c >= int(p.D)) return 0.f;
+  return p.kd != nullptr ? p.kd[c] : p.c * softplus_f32(p.lam[c]);
+}
+
 template <int LEN>
 __device__ __forceinline__ Chunk chunk_of(const GatedParams& p, uint32_t ticket, uint32_t chains, uint32_t ctiles) {
   // (the quotients come from the vector unit: back into scalar registers, or every address
@@ -130,10 +183,10 @@ __device__ __forceinline__ Chunk chunk_of(const GatedParams& p, uint32_t ticket,
 template <typename IO, int NW, int S, bool VEC, bool RESET>
 __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
-  constexpr int kLen = NW * S, kGroup = kLinkGroup;
-  static_assert(kGroup <= NW, "a wavefront reads one link");
+  constexpr int kLen = NW * S;
+  static_assert(kLinkGroup <= NW, "a wavefront reads one link");
   __shared__ float4 maps[2][NW][kCh / 2];          // of the wavefronts' tokens
-  __shared__ float4 links[2][kGroup][kCh / 2];        // of the chunks before; [0] the state behind their group
+  __shared__ float4 links[2][kLinkGroup][kCh / 2];    // of the chunks before; [0] the state behind their group
   __shared__ uint32_t tickets[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t ctiles = uint32_t((p.D + kCh - 1) / kCh), chains = uint32_t(p.batch) * ctiles;
@@ -160,8 +213,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
     const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
     const int c = int(k.ct) * kCh + 2 * lane;
-    w.k0 = c < D ? p.kd[c] : 0.f;
-    w.k1 = c + 1 < D ? p.kd[c + 1] : 0.f;
+    w.k0 = gated_rate(p, c);
+    w.k1 = gated_rate(p, c + 1);
     const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -245,11 +298,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     maps[par][wave][lane] = make_float4(A0, A1, H0, H1);
     if (tid == 0) tickets[par] = after;
     __syncthreads();
-    const int pos = int(k.chunk) % kGroup;         // maps between the last published state and this chunk
-    uint64_t* const map = p.links + kTicketWords + (int64_t(k.chunk) * chains + k.chain) * kCh + lane;
-    uint64_t* const end = p.links + kTicketWords +
-                          (int64_t(p.n_chunks) * chains + int64_t(k.chunk / kGroup) * chains + k.chain) * kCh + lane;
-    if (wave == NW - 1 && !last) {                 // the chunk's map, before any wait
+    const Link link(p, k.chunk, k.chain, chains, lane);
+    if (wave == NW - 1 && p.links != nullptr) {    // the chunk's map, before any wait
       float A0 = 1.f, A1 = 1.f, H0 = 0.f, H1 = 0.f;
 #pragma unroll
       for (int j = 0; j < NW; ++j) {
@@ -259,26 +309,13 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
         A0 = RESET && m.x == 0.f ? 0.f : A0 * m.x;
         A1 = RESET && m.y == 0.f ? 0.f : A1 * m.y;
       }
-      put_word(map, __float_as_uint(A0) | 0x80000000u, H0);
-      put_word(map + 64, __float_as_uint(A1) | 0x80000000u, H1);
+      link.publish(A0, A1, H0, H1);
     }
-    if (k.chunk > 0 && wave <= pos && wave < kGroup) {
-      // wavefront 0 reads the state behind the group before, wavefront j the map of the group's
-      // chunk j - 1
-      const uint64_t* const q = wave == 0 ? end - int64_t(chains) * kCh : map - int64_t(pos - wave + 1) * chains * kCh;
-      if (wave > 0 || int(k.chunk) >= kGroup) {
-        const uint64_t f0 = get_word(q), f1 = get_word(q + 64);
-        const uint64_t w0 = wait_word(q, f0), w1 = wait_word(q + 64, f1);
-        links[par][wave][lane] = make_float4(fabsf(__uint_as_float(uint32_t(w0 >> 32))), fabsf(__uint_as_float(uint32_t(w1 >> 32))),
-                                        __uint_as_float(uint32_t(w0)), __uint_as_float(uint32_t(w1)));
-      } else {
-        links[par][0][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
+    link.read(wave, &links[par][wave][lane]);
     __syncthreads();
     after = __builtin_amdgcn_readfirstlane(tickets[par]);
     float h0 = links[par][0][lane].z, h1 = links[par][0][lane].w;
-    for (int j = 1; j <= pos; ++j) {
+    for (int j = 1; j <= link.in_group; ++j) {
       const float4 m = links[par][j][lane];
       h0 = through<RESET>(m.x, m.z, h0);
       h1 = through<RESET>(m.y, m.w, h1);
@@ -303,10 +340,7 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
       if (p.y != nullptr) T::template store<VEC>(yp, o0, o1, (s0 + i) * ys, h0, h1);
     }
     if (wave == NW - 1) {                          // the state behind the chunk
-      if (!last && pos == kGroup - 1) {
-        put_word(end, 1u, h0);
-        put_word(end + 64, 1u, h1);
-      }
+      if (p.links != nullptr) link.publish_end(h0, h1);
       if (last && p.last != nullptr) {
         float* const o = p.last + int64_t(k.b) * D + c;
         if (ok0) o[0] = h0;
@@ -338,64 +372,268 @@ __global__ __launch_bounds__(256) void gated_begin_kernel(uint64_t* links, int64
   for (int64_t i = i0; i < D; i += n) kd[i] = c * softplus_f32(lam[i]);
 }
 
-// One thread walks one channel of one batch row backwards, tile by tile; a tile's states are
-// formed again from its checkpoint.
-template <typename IO>
-__global__ __launch_bounds__(64) void gated_bwd_kernel(GatedParams p) {
-  using T = io_traits<IO>;
-  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (i >= p.batch * p.D) return;
-  const int64_t b = i / p.D, d = i % p.D;
-  const IO* x = static_cast<const IO*>(p.x) + b * p.x_sb + d;
-  const IO* r = static_cast<const IO*>(p.r) + b * p.r_sb + d;
-  const IO* g = static_cast<const IO*>(p.g) + b * p.g_sb + d;
-  const IO* dy = static_cast<const IO*>(p.dy) + b * p.y_sb + d;
-  const int64_t o = b * p.L * p.D + d;
-  IO* dx = static_cast<IO*>(p.dx) + o;
-  IO* dr = static_cast<IO*>(p.dr) + o;
-  IO* dg = static_cast<IO*>(p.dg) + o;
-  float* hb = p.hbuf + b * kTile * p.D + d;               // state before each token of the tile
-  const float k = p.c * softplus_f32(p.lam[d]);
-  float adj = p.dlast ? p.dlast[i] : 0.f, sum = 0.f;
-  for (int64_t tile = p.ntiles - 1; tile >= 0; --tile) {
-    const int64_t t0 = tile * kTile, t1 = t0 + kTile < p.L ? t0 + kTile : p.L;
-    float h = p.ckpt[(b * p.ntiles + tile) * p.D + d];
-    for (int64_t t = t0; t < t1; ++t) {
-      hb[(t - t0) * p.D] = h;
-      float a, m;
-      gated_decay(-k * sigmoid_f32(T::widen(r[t * p.r_sl])), a, m);
-      if (p.reset && p.reset[b * p.reset_sb + t]) { a = h = 0.f; m = 1.f; }
-      h = fmaf(a, h, m * (sigmoid_f32(T::widen(g[t * p.g_sl])) * T::widen(x[t * p.x_sl])));
-    }
-    for (int64_t t = t1 - 1; t >= t0; --t) {
-      float s, s1, sg, sg1;
-      sigmoid_pair(T::widen(r[t * p.r_sl]), s, s1);
-      sigmoid_pair(T::widen(g[t * p.g_sl]), sg, sg1);
-      const float v = sg * T::widen(x[t * p.x_sl]), la = -k * s;
-      float a, m;
-      gated_decay(la, a, m);
-      const bool first = p.reset && p.reset[b * p.reset_sb + t];
-      if (first) { a = 0.f; m = 1.f; }
-      adj += T::widen(dy[t * p.y_sl]);
-      const float w = m > 0.f ? la / m : 0.f, dv = adj * m;
-      const float e = first ? 0.f : adj * a * (la * hb[(t - t0) * p.D] - a * w * v);
-      dx[t * p.D] = narrow<IO>(dv * sg);
-      dr[t * p.D] = narrow<IO>(e * s1);
-      dg[t * p.D] = narrow<IO>(dv * v * sg1);
-      sum += e;
-      adj = first ? 0.f : adj * a;
-    }
+// The backward pass over chunks of NW S tokens and 128 channels, from the last one on.  With
+// G_t = a_t l_t, what token t hands to the adjoint l_{t-1} = dy_{t-1} + G_t, the map of a token
+// is G -> a (G + dy): the same kind as the forward pass's, joined in the same way along the
+// reversed sequence.  The states are formed again from the chunk's checkpoint.  The gates'
+// sigmoids are computed twice, before the exchange of maps (the decays stay in registers)
+// and after it: keeping them would halve the wavefronts that a compute unit holds.
+template <typename IO, int NW, int S, bool VEC, bool RESET>
+#ifndef BLB
+#define BLB 4
+#endif
+__global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) {
+  using T = pair_io<IO>;
+  constexpr int kLen = NW * S, es = int(sizeof(IO));
+  static_assert(kLinkGroup <= NW && kLen % kTile == 0, "a wavefront reads one link; a chunk starts at a checkpoint");
+  __shared__ float4 maps[NW][kCh / 2];             // of the wavefronts' tokens, forward
+  __shared__ float2 backs[NW][kCh / 2];            // and backward (with the same A)
+  __shared__ float4 links[kLinkGroup][kCh / 2];    // of the chunks behind; [0] what their group receives
+  __shared__ float2 sums[NW][kCh / 2];
+  __shared__ uint32_t ticket;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t ctiles = uint32_t((p.D + kCh - 1) / kCh), chains = uint32_t(p.batch) * ctiles;
+  const uint32_t total = chains * uint32_t(p.n_chunks);
+  const int D = int(p.D);
+  uint32_t* const counter = reinterpret_cast<uint32_t*>(p.links);
+  uint32_t now = blockIdx.x, next = total;
+  if (p.links != nullptr) {
+    if (tid == 0) ticket = atomicAdd(counter, 1u);
+    __syncthreads();
+    now = __builtin_amdgcn_readfirstlane(ticket);
   }
-  if (p.dh0) p.dh0[i] = adj;
-  p.plam[i] = sum;
+  while (now < total) {
+    // (formed anew in every turn: kept over all turns, the rows' offsets fill the scalar
+    // registers and spill into vector ones)
+    int s0 = wave * S;
+    asm("" : "+s"(s0));
+    const int xs = int(p.x_sl) * es, rs = int(p.r_sl) * es, gs = int(p.g_sl) * es, ys = int(p.y_sl) * es;
+    Chunk k = chunk_of<kLen>(p, now, chains, ctiles);
+    const Link link(p, k.chunk, k.chain, chains, lane);
+    k.chunk = uint32_t(p.n_chunks) - 1 - k.chunk;
+    k.t0 = int64_t(k.chunk) * kLen;
+    k.rest = int(p.L - k.t0 < kLen ? p.L - k.t0 : kLen);
+    const int c = int(k.ct) * kCh + 2 * lane;
+    const bool ok0 = c < D, ok1 = c + 1 < D;
+    const uint32_t o0 = ok0 ? c * es : kNoChannel, o1 = ok1 ? (c + 1) * es : kNoChannel;
+    typename T::raw_t xr[S], rr[S], gr[S], yr[S];
+    {
+      const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
+      const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
+      const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
+      const auto yp = chunk_rsrc(static_cast<const IO*>(p.dy) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        rr[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
+        gr[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
+        xr[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
+        yr[i] = T::template load<VEC>(yp, o0, o1, (s0 + i) * ys);
+      }
+    }
+    uint32_t cuts = 0;                             // bit i: token i starts a sequence
+    if constexpr (RESET) {
+      const int t = s0 + (lane & (S - 1));
+      cuts = uint32_t(__ballot(t < k.rest && p.reset[k.b * p.reset_sb + k.t0 + t] != 0)) & ((1u << S) - 1u);
+    }
+    const float k0 = gated_rate(p, c), k1 = gated_rate(p, c + 1);
+    float h0 = 0.f, h1 = 0.f;                      // the state entering the chunk
+    {
+      const float* const q = p.ckpt + (k.b * p.ntiles + k.t0 / kTile) * p.D + c;
+      if (ok0) h0 = q[0];
+      if (ok1) h1 = q[1];
+    }
+    if (p.persistent && tid == 0) next = atomicAdd(counter, 1u);
+
+    float a0[S], a1[S], m0[S], m1[S], b0[S], b1[S];
+    float A0 = 1.f, A1 = 1.f, H0 = 0.f, H1 = 0.f;
+    const bool small = __all(k0 < kGatedSmall && k1 < kGatedSmall);
+#pragma unroll
+    for (int i0 = 0; i0 < S; i0 += 4) {
+      if (small) {
+#pragma unroll
+        for (int i = i0; i < i0 + 4; ++i) {
+          gated_decay_small(-k0 * sigmoid_f32(T::lo(rr[i])), a0[i], m0[i]);
+          gated_decay_small(-k1 * sigmoid_f32(T::hi(rr[i])), a1[i], m1[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = i0; i < i0 + 4; ++i) {
+          gated_decay(-k0 * sigmoid_f32(T::lo(rr[i])), a0[i], m0[i]);
+          gated_decay(-k1 * sigmoid_f32(T::hi(rr[i])), a1[i], m1[i]);
+        }
+      }
+#pragma unroll
+      for (int i = i0; i < i0 + 4; ++i) {
+        if (RESET && (cuts >> i & 1)) {
+          a0[i] = a1[i] = 0.f;
+          m0[i] = m1[i] = 1.f;
+          A0 = A1 = H0 = H1 = 0.f;
+        }
+        if (s0 + i >= k.rest) {                    // behind the last token (its inputs read as zero): changes nothing
+          a0[i] = a1[i] = 1.f;
+          m0[i] = m1[i] = 0.f;
+        }
+        b0[i] = m0[i] * (sigmoid_f32(T::lo(gr[i])) * T::lo(xr[i]));
+        b1[i] = m1[i] * (sigmoid_f32(T::hi(gr[i])) * T::hi(xr[i]));
+        H0 = fmaf(a0[i], H0, b0[i]);
+        H1 = fmaf(a1[i], H1, b1[i]);
+        A0 *= a0[i];
+        A1 *= a1[i];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    float G0 = 0.f, G1 = 0.f;
+#pragma unroll
+    for (int i = S - 1; i >= 0; --i) {
+      G0 = a0[i] * (G0 + T::lo(yr[i]));
+      G1 = a1[i] * (G1 + T::hi(yr[i]));
+      if (RESET && (cuts >> i & 1)) G0 = G1 = 0.f;
+    }
+    maps[wave][lane] = make_float4(A0, A1, H0, H1);
+    backs[wave][lane] = make_float2(G0, G1);
+    if (tid == 0) ticket = next;
+    __syncthreads();
+    next = __builtin_amdgcn_readfirstlane(ticket);
+    if (wave == 0 && p.links != nullptr) {         // the chunk's map, before any wait
+      float P0 = 1.f, P1 = 1.f, R0 = 0.f, R1 = 0.f;
+      if (link.pos == 0 && p.dlast != nullptr) {   // the last chunk knows what it receives
+        if (ok0) R0 = p.dlast[int64_t(k.b) * D + c];
+        if (ok1) R1 = p.dlast[int64_t(k.b) * D + c + 1];
+      }
+#pragma unroll 2
+      for (int j = NW - 1; j >= 0; --j) {
+        const float4 m = maps[j][lane];
+        const float2 g = backs[j][lane];
+        R0 = through<RESET>(m.x, g.x, R0);
+        R1 = through<RESET>(m.y, g.y, R1);
+        P0 = RESET && m.x == 0.f ? 0.f : P0 * m.x;
+        P1 = RESET && m.y == 0.f ? 0.f : P1 * m.y;
+      }
+      if (link.pos == 0) P0 = P1 = 0.f;
+      link.publish(P0, P1, R0, R1);
+    }
+    if (link.pos == 0) {
+      if (wave == 0) {
+        float g0 = 0.f, g1 = 0.f;
+        if (p.dlast != nullptr) {
+          if (ok0) g0 = p.dlast[int64_t(k.b) * D + c];
+          if (ok1) g1 = p.dlast[int64_t(k.b) * D + c + 1];
+        }
+        links[0][lane] = make_float4(0.f, 0.f, g0, g1);
+      }
+    } else {
+      link.read(wave, &links[wave][lane]);
+    }
+    // the states before this wavefront's tokens, while the links arrive
+#pragma unroll 2
+    for (int j = 0; j < wave; ++j) {
+      const float4 m = maps[j][lane];
+      h0 = through<RESET>(m.x, m.z, h0);
+      h1 = through<RESET>(m.y, m.w, h1);
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i) {                  // b becomes the state before its token
+      const float q0 = h0, q1 = h1;
+      if (RESET && (cuts >> i & 1)) h0 = h1 = 0.f;
+      h0 = fmaf(a0[i], h0, b0[i]);
+      h1 = fmaf(a1[i], h1, b1[i]);
+      b0[i] = q0;
+      b1[i] = q1;
+      // the gates anew, not their sigmoids from before the exchange
+      T::forget(rr[i]);
+      T::forget(gr[i]);
+    }
+    __syncthreads();
+    G0 = links[0][lane].z;
+    G1 = links[0][lane].w;
+#pragma unroll 2
+    for (int j = 1; j <= link.in_group; ++j) {
+      const float4 m = links[j][lane];
+      G0 = through<RESET>(m.x, m.z, G0);
+      G1 = through<RESET>(m.y, m.w, G1);
+    }
+#pragma unroll 2
+    for (int j = NW - 1; j > wave; --j) {
+      const float4 m = maps[j][lane];
+      const float2 g = backs[j][lane];
+      G0 = through<RESET>(m.x, g.x, G0);
+      G1 = through<RESET>(m.y, g.y, G1);
+    }
+    float e0 = 0.f, e1 = 0.f;
+    {
+      const int64_t o = (int64_t(k.b) * p.L + k.t0) * p.D;
+      const int os = D * es;
+      const auto dxp = chunk_rsrc(static_cast<IO*>(p.dx) + o, k.rest, os, os);
+      const auto drp = chunk_rsrc(static_cast<IO*>(p.dr) + o, k.rest, os, os);
+      const auto dgp = chunk_rsrc(static_cast<IO*>(p.dg) + o, k.rest, os, os);
+      // one token and channel: its adjoint l, the gradients of x, r and g, and G to hand on
+      auto token = [&](float r, float g, float x, float dy, float k, float a, float m, float h, bool cut, float& G, float& sum,
+                       float& dx, float& dr, float& dg) __attribute__((always_inline)) {
+        float s, s1, sg, sg1;
+        sigmoid_pair(r, s, s1);
+        sigmoid_pair(g, sg, sg1);
+        const float l = G + dy, v = sg * x, la = -k * s, dv = l * m;
+        const float w = m > 0.f ? la * __builtin_amdgcn_rcpf(m) : 0.f;
+        G = cut ? 0.f : a * l;
+        const float e = cut ? 0.f : (a * l) * fmaf(-a * w, v, la * h);
+        dx = dv * sg;
+        dg = dv * v * sg1;
+        dr = e * s1;
+        sum += e;
+      };
+#pragma unroll
+      for (int i = S - 1; i >= 0; --i) {
+        const bool cut = RESET && (cuts >> i & 1);
+        float dx0, dx1, dr0, dr1, dg0, dg1;
+        token(T::lo(rr[i]), T::lo(gr[i]), T::lo(xr[i]), T::lo(yr[i]), k0, a0[i], m0[i], b0[i], cut, G0, e0, dx0, dr0, dg0);
+        token(T::hi(rr[i]), T::hi(gr[i]), T::hi(xr[i]), T::hi(yr[i]), k1, a1[i], m1[i], b1[i], cut, G1, e1, dx1, dr1, dg1);
+        if (s0 + i >= k.rest) e0 = e1 = 0.f;       // (nothing before it in this walk)
+        T::template store<VEC>(dxp, o0, o1, (s0 + i) * os, dx0, dx1);
+        T::template store<VEC>(drp, o0, o1, (s0 + i) * os, dr0, dr1);
+        T::template store<VEC>(dgp, o0, o1, (s0 + i) * os, dg0, dg1);
+        __builtin_amdgcn_sched_barrier(0);         // a token at a time: all at once take twice the registers
+      }
+    }
+    if (wave == 0) {                               // what the chunk before receives
+      if (p.links != nullptr) link.publish_end(G0, G1);
+      if (k.chunk == 0 && p.dh0 != nullptr) {
+        float* const q = p.dh0 + int64_t(k.b) * D + c;
+        if (ok0) q[0] = G0;
+        if (ok1) q[1] = G1;
+      }
+    }
+    sums[wave][lane] = make_float2(e0, e1);
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int j = 1; j < NW; ++j) {
+        e0 += sums[j][lane].x;
+        e1 += sums[j][lane].y;
+      }
+      float* const q = p.plam + (int64_t(k.chunk) * p.batch + k.b) * p.D + c;
+      if (ok0) q[0] = e0;
+      if (ok1) q[1] = e1;
+    }
+    now = next;
+  }
 }
 
-__global__ __launch_bounds__(64) void gated_dlam_kernel(GatedParams p) {
-  const int64_t d = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (d >= p.D) return;
+// dlam: the sum of the parts [nparts][D] in a fixed order, times sigmoid(lam) / softplus(lam)
+__global__ __launch_bounds__(1024) void gated_dlam_kernel(GatedParams p, int64_t nparts) {
+  __shared__ float part[32][33];
+  const int col = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int64_t d = int64_t(blockIdx.x) * 32 + col;
   float sum = 0.f;
-  for (int64_t b = 0; b < p.batch; ++b) sum += p.plam[b * p.D + d];
-  p.dlam[d] = sum * gated_lam_ratio(p.lam[d]);
+  if (d < p.D) {
+#pragma unroll 8
+    for (int64_t j = row; j < nparts; j += 32) sum += p.plam[j * p.D + d];
+  }
+  part[row][col] = sum;
+  __syncthreads();
+  if (row == 0 && d < p.D) {
+    for (int j = 1; j < 32; ++j) sum += part[j][col];
+    p.dlam[d] = sum * gated_lam_ratio(p.lam[d]);
+  }
 }
 
 template <typename IO>
@@ -421,6 +659,20 @@ unsigned blocks_for(int64_t n, int per) { return unsigned((n + per - 1) / per); 
 
 }  // namespace
 
+// Clears the links and, with them, forms the channels' rates; with one chunk each workgroup
+// forms its own.
+static hipError_t launch_gated_begin(GatedParams& p, hipStream_t stream) {
+  if (p.links == nullptr) {
+    p.kd = nullptr;
+    return hipSuccess;
+  }
+  const int64_t words = gated_link_words(p.batch, p.D, p.n_chunks);
+  const int64_t blocks = ((words > p.D ? words : p.D) + 1023) / 1024;
+  hipLaunchKernelGGL(gated_begin_kernel, dim3(unsigned(blocks < 1024 ? blocks : 1024)), dim3(256), 0, stream, p.links, words,
+                     p.lam, p.c, p.kd, p.D);
+  return hipGetLastError();
+}
+
 template <typename IO, bool VEC, bool RESET>
 static hipError_t launch_gated_fwd_t(GatedParams p, int cus, hipStream_t stream) {
   const int64_t items = p.batch * ((p.D + kCh - 1) / kCh) * p.n_chunks;
@@ -431,27 +683,44 @@ static hipError_t launch_gated_fwd_t(GatedParams p, int cus, hipStream_t stream)
   return hipGetLastError();
 }
 
-hipError_t launch_gated_fwd(bool bf16, const GatedParams& p, int cus, hipStream_t stream) {
-  const int64_t words = p.links ? gated_link_words(p.batch, p.D, p.n_chunks) : 0;
-  const int64_t blocks = ((words > p.D ? words : p.D) + 1023) / 1024;
-  hipLaunchKernelGGL(gated_begin_kernel, dim3(unsigned(blocks < 1024 ? blocks : 1024)), dim3(256), 0, stream, p.links, words,
-                     p.lam, p.c, p.kd, p.D);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const bool reset = p.reset != nullptr;
-  if (bf16)
-    return p.vec ? (reset ? launch_gated_fwd_t<uint16_t, true, true>(p, cus, stream) : launch_gated_fwd_t<uint16_t, true, false>(p, cus, stream))
-                 : (reset ? launch_gated_fwd_t<uint16_t, false, true>(p, cus, stream) : launch_gated_fwd_t<uint16_t, false, false>(p, cus, stream));
-  return p.vec ? (reset ? launch_gated_fwd_t<float, true, true>(p, cus, stream) : launch_gated_fwd_t<float, true, false>(p, cus, stream))
-               : (reset ? launch_gated_fwd_t<float, false, true>(p, cus, stream) : launch_gated_fwd_t<float, false, false>(p, cus, stream));
+#ifndef BNPER
+#define BNPER 2
+#endif
+template <typename IO, bool VEC, bool RESET>
+static hipError_t launch_gated_bwd_t(GatedParams p, int cus, hipStream_t stream) {
+  const int64_t items = p.batch * ((p.D + kCh - 1) / kCh) * p.n_chunks;
+  const int64_t resident = BNPER * int64_t(cus);
+  p.persistent = p.links != nullptr && items > resident;
+  const dim3 grid(unsigned(p.persistent ? resident : items));
+  hipLaunchKernelGGL((gated_bwd_kernel<IO, kGatedWaves, kGatedBwdChunk / kGatedWaves, VEC, RESET>), grid, dim3(kGatedWaves * 64),
+                     0, stream, p);
+  hipLaunchKernelGGL(gated_dlam_kernel, dim3(unsigned((p.D + 31) / 32)), dim3(1024), 0, stream, p, p.batch * p.n_chunks);
+  return hipGetLastError();
 }
 
-hipError_t launch_gated_bwd(bool bf16, const GatedParams& p, hipStream_t stream) {
-  const dim3 grid(blocks_for(p.batch * p.D, 64));
-  if (bf16) hipLaunchKernelGGL(gated_bwd_kernel<uint16_t>, grid, dim3(64), 0, stream, p);
-  else hipLaunchKernelGGL(gated_bwd_kernel<float>, grid, dim3(64), 0, stream, p);
-  hipLaunchKernelGGL(gated_dlam_kernel, dim3(blocks_for(p.D, 64)), dim3(64), 0, stream, p);
-  return hipGetLastError();
+template <typename F> static hipError_t by_type(bool bf16, const GatedParams& p, F f) {
+  const bool reset = p.reset != nullptr;
+  auto with = [&](auto io, auto vec) {
+    return reset ? f(io, vec, std::true_type{}) : f(io, vec, std::false_type{});
+  };
+  auto typed = [&](auto io) { return p.vec ? with(io, std::true_type{}) : with(io, std::false_type{}); };
+  return bf16 ? typed(uint16_t{}) : typed(float{});
+}
+
+hipError_t launch_gated_fwd(bool bf16, GatedParams p, int cus, hipStream_t stream) {
+  const hipError_t e = launch_gated_begin(p, stream);
+  if (e != hipSuccess) return e;
+  return by_type(bf16, p, [&](auto io, auto vec, auto reset) {
+    return launch_gated_fwd_t<decltype(io), decltype(vec)::value, decltype(reset)::value>(p, cus, stream);
+  });
+}
+
+hipError_t launch_gated_bwd(bool bf16, GatedParams p, int cus, hipStream_t stream) {
+  const hipError_t e = launch_gated_begin(p, stream);
+  if (e != hipSuccess) return e;
+  return by_type(bf16, p, [&](auto io, auto vec, auto reset) {
+    return launch_gated_bwd_t<decltype(io), decltype(vec)::value, decltype(reset)::value>(p, cus, stream);
+  });
 }
 
 hipError_t launch_gated_step(bool bf16, const GatedParams& p, float* state, hipStream_t stream) {

@@ -248,22 +248,22 @@ struct GatedParams {
   float c;
   uint64_t* links;       // workspace: gated_link_words() words, or null (one chunk)
   float* kd;             // workspace [D]: c softplus(lam)
-  int32_t n_chunks;      // ceil(L / gated_chunk())
+  int32_t n_chunks;      // chunks of the pass: ceil(L / gated_chunk()), ceil(L / kGatedBwdChunk)
   int32_t persistent;    // workgroups take chunks by ticket (links)
   int32_t vec;           // 1: D and every stride even, pointers aligned to channel pairs
-  float* hbuf;           // workspace
-  float* plam;           // workspace: partial sums of dlam
+  float* plam;           // workspace [n_chunks][batch][D]: partial sums of dlam
 };
 // tokens of a workgroup: eight runs of as many as its registers hold twice over
 constexpr int gated_chunk(bool bf16) { return bf16 ? 128 : 64; }
+constexpr int kGatedBwdChunk = 64;     // of the backward pass
 constexpr int kTicketWords = 16;       // a cache line for the ticket counter
-// words of the links between chunks: the ticket, a map per chunk and an end state per 16
+// words of the links between chunks: the ticket, a map per chunk and an end state per 8
 // chunks, for every 128 channels
 constexpr int64_t gated_link_words(int64_t batch, int64_t D, int64_t n_chunks) {
   return kTicketWords + batch * ((D + 127) / 128) * 128 * (n_chunks + n_chunks / 8);
 }
-hipError_t launch_gated_fwd(bool bf16, const GatedParams& p, int cus, hipStream_t stream);
-hipError_t launch_gated_bwd(bool bf16, const GatedParams& p, hipStream_t stream);
+hipError_t launch_gated_fwd(bool bf16, GatedParams p, int cus, hipStream_t stream);
+hipError_t launch_gated_bwd(bool bf16, GatedParams p, int cus, hipStream_t stream);
 hipError_t launch_gated_step(bool bf16, const GatedParams& p, float* state, hipStream_t stream);
 
 // The 8-bit state cache (cache_kernels.hip): q [slots][elems], scale [slots][rows].

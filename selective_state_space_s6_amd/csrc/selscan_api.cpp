@@ -942,9 +942,9 @@ int selective_scan_ssd_fwd(const void* x, const void* delta, const float* A, con
 
 // ---- the gated linear recurrence
 struct GatedPlan {
-  int64_t ntiles = 0, n_chunks = 0;
+  int64_t ntiles = 0, n_chunks = 0, bwd_chunks = 0;
   size_t link_bytes = 0, fwd_bytes = 0;         // workspace of the forward pass: links between chunks, [D] floats
-  size_t off_ckpt = 0, off_hbuf = 0, off_plam = 0, bwd_bytes = 0;
+  size_t bwd_link_bytes = 0, off_kd = 0, off_ckpt = 0, off_plam = 0, bwd_bytes = 0;
 };
 
 // Validate dims and lay out the workspaces.  Does not look at pointers.
@@ -967,19 +967,22 @@ static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan*
   p.ntiles = (d.seqlen + SELSCAN_GATED_TILE - 1) / SELSCAN_GATED_TILE;
   const int64_t chunk = selscan::gated_chunk(d.io_dtype == SELSCAN_BF16);
   p.n_chunks = (d.seqlen + chunk - 1) / chunk;
-  if (d.batch > 0 && p.n_chunks > kMaxItems / (d.batch * ((d.dim + 127) / 128) + 32)) return SELSCAN_ERR_UNSUPPORTED;
+  p.bwd_chunks = (d.seqlen + selscan::kGatedBwdChunk - 1) / selscan::kGatedBwdChunk;
+  if (d.batch > 0 && p.bwd_chunks > kMaxItems / (d.batch * ((d.dim + 127) / 128) + 32)) return SELSCAN_ERR_UNSUPPORTED;
   if (d.batch * d.seqlen > 0) {
     auto al = [](int64_t x) { return size_t(round_up(x, 256)); };
     const int64_t f = int64_t(sizeof(float));
     p.link_bytes = p.n_chunks > 1 ? al(8 * selscan::gated_link_words(d.batch, d.dim, p.n_chunks)) : 0;
     p.fwd_bytes = p.link_bytes + al(f * d.dim);
-    size_t off = p.fwd_bytes;
+    // backward: links (of a forward pass that forms the checkpoints, then of the backward one)
+    p.bwd_link_bytes = p.bwd_chunks > 1 ? al(8 * selscan::gated_link_words(d.batch, d.dim, p.bwd_chunks)) : 0;
+    size_t off = have_ckpt || p.bwd_link_bytes > p.link_bytes ? p.bwd_link_bytes : p.link_bytes;
+    p.off_kd = off;
+    off += al(f * d.dim);
     p.off_ckpt = off;
     if (!have_ckpt) off += al(f * d.batch * p.ntiles * d.dim);
-    p.off_hbuf = off;
-    off += al(f * d.batch * SELSCAN_GATED_TILE * d.dim);
     p.off_plam = off;
-    off += al(f * d.batch * d.dim);
+    off += al(f * d.batch * p.bwd_chunks * d.dim);
     p.bwd_bytes = off;
   }
   *out = p;
@@ -1125,17 +1128,19 @@ int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam
   selscan::GatedParams p = gated_params(x, r, g, lam, reset, d, pl);
   p.h0 = initial_state;
   p.ckpt = const_cast<float*>(checkpoints);
+  p.kd = reinterpret_cast<float*>(ws + pl.off_kd);
   if (checkpoints == nullptr) {
     p.ckpt = reinterpret_cast<float*>(ws + pl.off_ckpt);
     p.links = pl.link_bytes > 0 ? reinterpret_cast<uint64_t*>(ws) : nullptr;
-    p.kd = reinterpret_cast<float*>(ws + pl.link_bytes);
     p.vec = gated_pairs(d, {x, r, g});
     e = selscan::launch_gated_fwd(bf16, p, compute_units_or_default(s), s);
   }
   p.dy = dy; p.dlast = dlast_state; p.dx = dx; p.dr = dr; p.dg = dg; p.dlam = dlam; p.dh0 = dinitial_state;
-  p.hbuf = reinterpret_cast<float*>(ws + pl.off_hbuf);
   p.plam = reinterpret_cast<float*>(ws + pl.off_plam);
-  if (e == hipSuccess) e = selscan::launch_gated_bwd(bf16, p, s);
+  p.links = pl.bwd_link_bytes > 0 ? reinterpret_cast<uint64_t*>(ws) : nullptr;
+  p.n_chunks = int32_t(pl.bwd_chunks);
+  p.vec = gated_pairs(d, {x, r, g, dy, dx, dr, dg});
+  if (e == hipSuccess) e = selscan::launch_gated_bwd(bf16, p, compute_units_or_default(s), s);
   st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   if (workspace == nullptr && pl.bwd_bytes > 0) {
     const hipError_t f = hipFreeAsync(ws, s);

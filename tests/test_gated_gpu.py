@@ -95,7 +95,7 @@ def check_forward(i, io, got, h0=True, what=""):
     close(last, l_ref, TOL["f32"], what + " last_state")
     if marks is not None:
         first = (i["h0"] if h0 else np.zeros_like(i["h0"]))[:, None]
-        close(marks, np.concatenate([first, y_ref], 1)[:, :-1:128], TOL["f32"], what + " checkpoints")
+        close(marks, np.concatenate([first, y_ref], 1)[:, :-1:64], TOL["f32"], what + " checkpoints")
 
 
 def check_backward(i, io, g, h0=True, dlast=True, what=""):
