@@ -173,6 +173,27 @@ __device__ __forceinline__ Chunk chunk_of(const GatedParams& p, uint32_t ticket,
   return k;
 }
 
+// The map of a run of S tokens, and the states before each of them.
+template <int S, bool CUT>
+__device__ __forceinline__ void run_map(const float (&a)[S], const float (&b)[S], uint32_t cuts, float& A, float& H) {
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    if (CUT && (cuts >> i & 1)) A = H = 0.f;
+    H = fmaf(a[i], H, b[i]);
+    A *= a[i];
+  }
+}
+template <int S, bool CUT>
+__device__ __forceinline__ void run_states(const float (&a)[S], float (&b)[S], uint32_t cuts, float& h) {
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const float before = h;
+    if (CUT && (cuts >> i & 1)) h = 0.f;
+    h = fmaf(a[i], h, b[i]);
+    b[i] = before;
+  }
+}
+
 // Chunks of NW S tokens and 128 channels.  Each wavefront forms the map of its S tokens in
 // registers; the maps meet in LDS, the workgroup's in the links, where the maps of the chunks
 // since the last published state and that state are read, one by each wavefront; every
@@ -205,7 +226,7 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
 
   struct Raw {
     typename T::raw_t x[S], r[S], g[S];
-    uint32_t firsts;                               // bit i: token i starts a sequence
+    uint32_t first;                                // lane i: token i starts a sequence
     float k0, k1;
   };
   auto load = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
@@ -213,6 +234,11 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
     const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
     const int c = int(k.ct) * kCh + 2 * lane;
+    w.first = 0;
+    if constexpr (RESET) {
+      const int t = s0 + lane;
+      if (lane < S && t < k.rest) w.first = p.reset[k.b * p.reset_sb + k.t0 + t];
+    }
     w.k0 = gated_rate(p, c);
     w.k1 = gated_rate(p, c + 1);
     const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
@@ -221,11 +247,6 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
       w.r[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
       w.g[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
       w.x[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
-    }
-    if constexpr (RESET) {
-      const int t = s0 + (lane & (S - 1));
-      const bool f = t < k.rest && p.reset[k.b * p.reset_sb + k.t0 + t] != 0;
-      w.firsts = uint32_t(__ballot(f)) & ((1u << S) - 1u);
     }
   };
 
@@ -238,6 +259,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     uint32_t after = total;
     if (more && tid == 0) after = atomicAdd(counter, 1u);
     float a0[S], a1[S], b0[S], b1[S];
+    uint32_t cuts = 0;                             // bit i: token i starts a sequence
+    if constexpr (RESET) cuts = uint32_t(__ballot(w.first != 0));
     // |log a| is at most k: where that is small for the whole wavefront, no exp2 is needed.  (The
     // branch is taken four tokens at a time: around all of them, the compiler keeps every
     // gate's sigmoid in registers across it.)
@@ -260,7 +283,10 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (RESET && (w.firsts >> (i0 + i) & 1)) { a0[i0 + i] = a1[i0 + i] = 0.f; m0[i] = m1[i] = 1.f; }
+        if (RESET && (cuts >> i0 & 15) != 0 && (cuts >> (i0 + i) & 1)) {
+          a0[i0 + i] = a1[i0 + i] = 0.f;
+          m0[i] = m1[i] = 1.f;
+        }
         b0[i0 + i] = m0[i] * (sigmoid_f32(T::lo(w.g[i0 + i])) * T::lo(w.x[i0 + i]));
         b1[i0 + i] = m1[i] * (sigmoid_f32(T::hi(w.g[i0 + i])) * T::hi(w.x[i0 + i]));
       }
@@ -270,15 +296,13 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
       for (int i = 0; i < S; ++i)
         if (s0 + i >= k.rest) { a0[i] = a1[i] = 1.f; b0[i] = b1[i] = 0.f; }
     }
-    const uint32_t cuts = w.firsts;
     float A0 = 1.f, A1 = 1.f, H0 = 0.f, H1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      if (RESET && (cuts >> i & 1)) { A0 = A1 = H0 = H1 = 0.f; }
-      H0 = fmaf(a0[i], H0, b0[i]);
-      H1 = fmaf(a1[i], H1, b1[i]);
-      A0 *= a0[i];
-      A1 *= a1[i];
+    if (RESET && cuts != 0) {                      // (rare)
+      run_map<S, true>(a0, b0, cuts, A0, H0);
+      run_map<S, true>(a1, b1, cuts, A1, H1);
+    } else {
+      run_map<S, false>(a0, b0, 0, A0, H0);
+      run_map<S, false>(a1, b1, 0, A1, H1);
     }
     const int c = int(k.ct) * kCh + 2 * lane;
     const bool ok0 = c < D, ok1 = c + 1 < D, last = int(k.chunk) == p.n_chunks - 1;
@@ -332,12 +356,19 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     }
     const auto yp = chunk_rsrc(static_cast<IO*>(p.y) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
     const uint32_t o0 = ok0 ? c * es : kNoChannel, o1 = ok1 ? (c + 1) * es : kNoChannel;
+    if (RESET && cuts != 0) {
+      run_states<S, true>(a0, b0, cuts, h0);
+      run_states<S, true>(a1, b1, cuts, h1);
+    } else {
+      run_states<S, false>(a0, b0, 0, h0);
+      run_states<S, false>(a1, b1, 0, h1);
+    }
+    if (p.y != nullptr) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      if (RESET && (cuts >> i & 1)) h0 = h1 = 0.f;
-      h0 = fmaf(a0[i], h0, b0[i]);
-      h1 = fmaf(a1[i], h1, b1[i]);
-      if (p.y != nullptr) T::template store<VEC>(yp, o0, o1, (s0 + i) * ys, h0, h1);
+      for (int i = 0; i < S; ++i) {
+        const bool end = i == S - 1;               // b holds the state before each token
+        T::template store<VEC>(yp, o0, o1, (s0 + i) * ys, end ? h0 : b0[i + 1 < S ? i + 1 : i], end ? h1 : b1[i + 1 < S ? i + 1 : i]);
+      }
     }
     if (wave == NW - 1) {                          // the state behind the chunk
       if (p.links != nullptr) link.publish_end(h0, h1);
@@ -379,10 +410,7 @@ __global__ __launch_bounds__(256) void gated_begin_kernel(uint64_t* links, int64
 // sigmoids are computed twice, before the exchange of maps (the decays stay in registers)
 // and after it: keeping them would halve the wavefronts that a compute unit holds.
 template <typename IO, int NW, int S, bool VEC, bool RESET>
-#ifndef BLB
-#define BLB 4
-#endif
-__global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) {
+__global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
   constexpr int kLen = NW * S, es = int(sizeof(IO));
   static_assert(kLinkGroup <= NW && kLen % kTile == 0, "a wavefront reads one link; a chunk starts at a checkpoint");
@@ -417,6 +445,11 @@ __global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) 
     const bool ok0 = c < D, ok1 = c + 1 < D;
     const uint32_t o0 = ok0 ? c * es : kNoChannel, o1 = ok1 ? (c + 1) * es : kNoChannel;
     typename T::raw_t xr[S], rr[S], gr[S], yr[S];
+    uint32_t first = 0;                            // lane i: token i starts a sequence
+    if constexpr (RESET) {
+      const int t = s0 + lane;
+      if (lane < S && t < k.rest) first = p.reset[k.b * p.reset_sb + k.t0 + t];
+    }
     {
       const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
       const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
@@ -430,11 +463,6 @@ __global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) 
         yr[i] = T::template load<VEC>(yp, o0, o1, (s0 + i) * ys);
       }
     }
-    uint32_t cuts = 0;                             // bit i: token i starts a sequence
-    if constexpr (RESET) {
-      const int t = s0 + (lane & (S - 1));
-      cuts = uint32_t(__ballot(t < k.rest && p.reset[k.b * p.reset_sb + k.t0 + t] != 0)) & ((1u << S) - 1u);
-    }
     const float k0 = gated_rate(p, c), k1 = gated_rate(p, c + 1);
     float h0 = 0.f, h1 = 0.f;                      // the state entering the chunk
     {
@@ -444,6 +472,8 @@ __global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) 
     }
     if (p.persistent && tid == 0) next = atomicAdd(counter, 1u);
 
+    uint32_t cuts = 0;                             // bit i: token i starts a sequence
+    if constexpr (RESET) cuts = uint32_t(__ballot(first != 0));
     float a0[S], a1[S], m0[S], m1[S], b0[S], b1[S];
     float A0 = 1.f, A1 = 1.f, H0 = 0.f, H1 = 0.f;
     const bool small = __all(k0 < kGatedSmall && k1 < kGatedSmall);
@@ -462,32 +492,45 @@ __global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) 
           gated_decay(-k1 * sigmoid_f32(T::hi(rr[i])), a1[i], m1[i]);
         }
       }
+      // (rare: a token that starts a sequence or lies behind the last)
+      if ((RESET && (cuts >> i0 & 15) != 0) || s0 + i0 + 4 > k.rest) {
+#pragma unroll
+        for (int i = i0; i < i0 + 4; ++i) {
+          if (RESET && (cuts >> i & 1)) {
+            a0[i] = a1[i] = 0.f;
+            m0[i] = m1[i] = 1.f;
+          }
+          if (s0 + i >= k.rest) {                  // its inputs read as zero: the map that changes nothing
+            a0[i] = a1[i] = 1.f;
+            m0[i] = m1[i] = 0.f;
+          }
+        }
+      }
 #pragma unroll
       for (int i = i0; i < i0 + 4; ++i) {
-        if (RESET && (cuts >> i & 1)) {
-          a0[i] = a1[i] = 0.f;
-          m0[i] = m1[i] = 1.f;
-          A0 = A1 = H0 = H1 = 0.f;
-        }
-        if (s0 + i >= k.rest) {                    // behind the last token (its inputs read as zero): changes nothing
-          a0[i] = a1[i] = 1.f;
-          m0[i] = m1[i] = 0.f;
-        }
         b0[i] = m0[i] * (sigmoid_f32(T::lo(gr[i])) * T::lo(xr[i]));
         b1[i] = m1[i] * (sigmoid_f32(T::hi(gr[i])) * T::hi(xr[i]));
-        H0 = fmaf(a0[i], H0, b0[i]);
-        H1 = fmaf(a1[i], H1, b1[i]);
-        A0 *= a0[i];
-        A1 *= a1[i];
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     float G0 = 0.f, G1 = 0.f;
+    if (RESET && cuts != 0) {                      // (rare)
+      run_map<S, true>(a0, b0, cuts, A0, H0);
+      run_map<S, true>(a1, b1, cuts, A1, H1);
 #pragma unroll
-    for (int i = S - 1; i >= 0; --i) {
-      G0 = a0[i] * (G0 + T::lo(yr[i]));
-      G1 = a1[i] * (G1 + T::hi(yr[i]));
-      if (RESET && (cuts >> i & 1)) G0 = G1 = 0.f;
+      for (int i = S - 1; i >= 0; --i) {
+        const bool cut = cuts >> i & 1;
+        G0 = cut ? 0.f : a0[i] * (G0 + T::lo(yr[i]));
+        G1 = cut ? 0.f : a1[i] * (G1 + T::hi(yr[i]));
+      }
+    } else {
+      run_map<S, false>(a0, b0, 0, A0, H0);
+      run_map<S, false>(a1, b1, 0, A1, H1);
+#pragma unroll
+      for (int i = S - 1; i >= 0; --i) {
+        G0 = a0[i] * (G0 + T::lo(yr[i]));
+        G1 = a1[i] * (G1 + T::hi(yr[i]));
+      }
     }
     maps[wave][lane] = make_float4(A0, A1, H0, H1);
     backs[wave][lane] = make_float2(G0, G1);
@@ -531,15 +574,16 @@ __global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) 
       h0 = through<RESET>(m.x, m.z, h0);
       h1 = through<RESET>(m.y, m.w, h1);
     }
+    // b becomes the state before its token
+    if (RESET && cuts != 0) {
+      run_states<S, true>(a0, b0, cuts, h0);
+      run_states<S, true>(a1, b1, cuts, h1);
+    } else {
+      run_states<S, false>(a0, b0, 0, h0);
+      run_states<S, false>(a1, b1, 0, h1);
+    }
 #pragma unroll
-    for (int i = 0; i < S; ++i) {                  // b becomes the state before its token
-      const float q0 = h0, q1 = h1;
-      if (RESET && (cuts >> i & 1)) h0 = h1 = 0.f;
-      h0 = fmaf(a0[i], h0, b0[i]);
-      h1 = fmaf(a1[i], h1, b1[i]);
-      b0[i] = q0;
-      b1[i] = q1;
-      // the gates anew, not their sigmoids from before the exchange
+    for (int i = 0; i < S; ++i) {                  // the gates anew, not their sigmoids from before the exchange
       T::forget(rr[i]);
       T::forget(gr[i]);
     }
@@ -574,8 +618,9 @@ __global__ __launch_bounds__(NW * 64, BLB) void gated_bwd_kernel(GatedParams p) 
         sigmoid_pair(g, sg, sg1);
         const float l = G + dy, v = sg * x, la = -k * s, dv = l * m;
         const float w = m > 0.f ? la * __builtin_amdgcn_rcpf(m) : 0.f;
-        G = cut ? 0.f : a * l;
-        const float e = cut ? 0.f : (a * l) * fmaf(-a * w, v, la * h);
+        G = a * l;
+        float e = G * fmaf(-a * w, v, la * h);
+        if (RESET && cut) G = e = 0.f;             // (a scalar branch)
         dx = dv * sg;
         dg = dv * v * sg1;
         dr = e * s1;
@@ -683,13 +728,10 @@ static hipError_t launch_gated_fwd_t(GatedParams p, int cus, hipStream_t stream)
   return hipGetLastError();
 }
 
-#ifndef BNPER
-#define BNPER 2
-#endif
 template <typename IO, bool VEC, bool RESET>
 static hipError_t launch_gated_bwd_t(GatedParams p, int cus, hipStream_t stream) {
   const int64_t items = p.batch * ((p.D + kCh - 1) / kCh) * p.n_chunks;
-  const int64_t resident = BNPER * int64_t(cus);
+  const int64_t resident = cus;
   p.persistent = p.links != nullptr && items > resident;
   const dim3 grid(unsigned(p.persistent ? resident : items));
   hipLaunchKernelGGL((gated_bwd_kernel<IO, kGatedWaves, kGatedBwdChunk / kGatedWaves, VEC, RESET>), grid, dim3(kGatedWaves * 64),
