@@ -1,5 +1,10 @@
 // cache_kernels.hip -- the 8-bit state cache: writing, reading, and the decode steps of the
-// selective scan and of the scalar-decay layer on cached states.
+// selective scan and of the scalar-decay layer on cached states.  Every kernel is bound by the
+// bytes of the states, or close to it by the arithmetic on each of them, which therefore is
+// kept short: codes are widened from biased bytes (v_cvt_f32_ubyte), rounded and packed in one
+// instruction (v_cvt_pk_u8_f32), and a pair of values shares one 32-bit mix for its rounding.
+#include <type_traits>
+
 #include "device_common.h"
 #include "scan_launch.h"
 
@@ -8,6 +13,7 @@ namespace {
 
 constexpr float kTinyRow = 0x1p-100f;     // rows whose largest magnitude is below are zero
 constexpr float kCodes = 127.f;
+constexpr uint32_t kBias = 0x80808080u;   // code + 128 in each byte
 
 // ---- the 16 random bits of a value: whole-number mixing of the seed, the row's index and the
 // value's place in the row.  Rounding needs no more than that neighbouring values, rows and
@@ -24,24 +30,40 @@ __device__ __forceinline__ uint32_t row_key(int64_t seed, uint32_t row) {
 }
 // of the values 2 pair (low half) and 2 pair + 1 (high half)
 __device__ __forceinline__ uint32_t pair_bits(uint32_t key, uint32_t pair) { return mix_bits(key + pair * 0x9E3779B9u); }
-__device__ __forceinline__ float rounding_offset(bool seeded, uint32_t key, uint32_t j) {
-  if (!seeded) return 0.5f;
-  const uint32_t w = pair_bits(key, j >> 1);
-  return (float((j & 1) ? w >> 16 : w & 0xffffu) + 0.5f) * 0x1p-16f;
-}
 
 struct RowScale {
   float scale, inv;
+  bool bad;                               // an infinity or a NaN in the row: a NaN scale, zero codes
 };
-// NaN or infinity anywhere in the row (bad): a NaN scale and zero codes
+// The codes' factor is a hair under 127 / amax, so that -127 stays clear of the code below it
+// whatever is added for rounding; that is 1.2e-7 of a code's value.
 __device__ __forceinline__ RowScale row_scale(float amax, bool bad) {
-  if (bad) return {__builtin_nanf(""), 0.f};
-  if (!(amax >= kTinyRow)) return {0.f, 0.f};
-  return {amax / kCodes, kCodes / amax};
+  if (bad) return {__builtin_nanf(""), 0.f, true};
+  if (!(amax >= kTinyRow)) return {0.f, 0.f, false};
+  return {amax / kCodes, 126.99998f / amax, false};
 }
-__device__ __forceinline__ int8_t code(float h, float inv, float off, bool bad) {
-  if (bad) return 0;
-  return int8_t(fminf(fmaxf(floorf(fmaf(h, inv, off)), -kCodes), kCodes));
+// Four codes of values 4 quad .. 4 quad + 3 of a row.  v_cvt_pk_u8_f32 rounds to nearest, ties
+// to even: floor(t + u) is the rounding of t + u - 1/2, u = (k + 1/2) / 65536, formed as 128 +
+// k / 65536 by putting k behind the bits of 128.f (the sum's own rounding to 2^-16 stands for
+// the half); without a seed, u = 1/2 and 2^-16 more sends ties up.
+template <bool SEEDED>
+__device__ __forceinline__ uint32_t pack_codes(const float (&h)[4], const RowScale& r, uint32_t key, uint32_t quad) {
+  float off[4];
+  if constexpr (SEEDED) {
+    const uint32_t w0 = pair_bits(key, 2 * quad), w1 = pair_bits(key, 2 * quad + 1);
+    off[0] = __uint_as_float((w0 & 0xffffu) | 0x43000000u) - 0.5f;
+    off[1] = __uint_as_float((w0 >> 16) | 0x43000000u) - 0.5f;
+    off[2] = __uint_as_float((w1 & 0xffffu) | 0x43000000u) - 0.5f;
+    off[3] = __uint_as_float((w1 >> 16) | 0x43000000u) - 0.5f;
+  } else {
+    off[0] = off[1] = off[2] = off[3] = 128.f + 0x1p-16f;
+  }
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[0], r.inv, off[0]), 0, q);
+  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[1], r.inv, off[1]), 1, q);
+  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[2], r.inv, off[2]), 2, q);
+  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[3], r.inv, off[3]), 3, q);
+  return r.bad ? 0u : q ^ kBias;
 }
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
 
@@ -51,151 +73,458 @@ __device__ __forceinline__ int64_t slot_of(const int32_t* ids, int64_t b, int64_
   return s >= 0 && s < slots ? s : -1;
 }
 
-// One thread per row.
-__global__ __launch_bounds__(64) void cache_write_kernel(const float* state, CacheParams p) {
-  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (i >= p.count * p.rows) return;
-  const int64_t b = i / p.rows, row = i % p.rows, slot = slot_of(p.write_slots, b, p.slots);
-  if (slot < 0) return;
-  const int64_t e0 = row * p.row_len, n = e0 + p.row_len < p.elems ? p.row_len : p.elems - e0;
-  const float* h = state + b * p.elems + e0;
-  float amax = 0.f;
-  bool bad = false;
-  for (int64_t j = 0; j < n; ++j) {
-    amax = fmaxf(amax, fabsf(h[j]));
-    bad |= !finite(h[j]);
+// Over the L lanes (a power of two) that share a row.  After the exchanges within a quad all its
+// lanes agree, so mirrors of 8 and of 16 lanes join quads and halves of a row of 16.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, false));
+}
+template <int L, typename F> __device__ __forceinline__ float group_all(float v, F f) {
+  if constexpr (L >= 2) v = f(v, dpp<0xB1>(v));
+  if constexpr (L >= 4) v = f(v, dpp<0x4E>(v));
+  if constexpr (L >= 8) v = f(v, dpp<0x141>(v));
+  if constexpr (L >= 16) v = f(v, dpp<0x140>(v));
+  if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16));
+  return v;
+}
+__device__ __forceinline__ float fmax2(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float fadd2(float a, float b) { return a + b; }
+
+// Four codes of a row, n of them present, and back; WORDS: whole and on a 4-byte boundary.
+template <bool WORDS> __device__ __forceinline__ uint32_t load_codes(const int8_t* q, int n) {
+  if constexpr (WORDS) return n > 0 ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < n) w |= uint32_t(uint8_t(q[j])) << (8 * j);
+  return w;
+}
+template <bool WORDS> __device__ __forceinline__ void store_codes(int8_t* q, int n, uint32_t w) {
+  if constexpr (WORDS) {
+    if (n > 0) *reinterpret_cast<uint32_t*>(q) = w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) q[j] = int8_t(w >> (8 * j));
   }
-  const RowScale s = row_scale(amax, bad);
-  const uint32_t key = p.seed ? row_key(*p.seed, uint32_t(i)) : 0;
-  int8_t* q = p.q + slot * p.elems + e0;
-  for (int64_t j = 0; j < n; ++j) q[j] = code(h[j], s.inv, rounding_offset(p.seed != nullptr, key, uint32_t(j)), bad);
-  p.scale[slot * p.rows + row] = s.scale;
+}
+// two floats as bf16, to nearest even
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+}
+// byte j of biased codes as a float 1 .. 255
+template <int J> __device__ __forceinline__ float code_byte(uint32_t w) { return float((w >> (8 * J)) & 0xffu); }
+
+// Writing: four values a lane, L lanes a row, whole lines in and out.
+template <int L, bool WORDS, bool SEEDED>
+__global__ __launch_bounds__(256) void cache_write_kernel(const float* __restrict__ state, CacheParams p) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / L;
+  const uint32_t quad = threadIdx.x % L;
+  const int64_t total = p.count * p.rows;
+  const int64_t row_id = i < total ? i : total - 1;
+  const int64_t b = row_id / p.rows, row = row_id - b * p.rows;
+  const int64_t slot = i < total ? slot_of(p.write_slots, b, p.slots) : -1;
+  const int64_t e0 = row * p.row_len;
+  const int64_t left = (e0 + p.row_len < p.elems ? p.row_len : p.elems - e0) - 4 * int64_t(quad);
+  const int n = slot < 0 || left < 0 ? 0 : left < 4 ? int(left) : 4;
+  const float* const src = state + b * p.elems + e0 + 4 * quad;
+  float h[4] = {0.f, 0.f, 0.f, 0.f};
+  if (WORDS && n == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(src);
+    h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) h[j] = src[j];
+  }
+  const float amax = group_all<L>(fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3]))), fmax2);
+  const bool ok = finite(h[0]) && finite(h[1]) && finite(h[2]) && finite(h[3]);
+  const float bad = group_all<L>(ok ? 0.f : 1.f, fmax2);
+  const RowScale r = row_scale(amax, bad != 0.f);
+  const uint32_t key = SEEDED ? row_key(*p.seed, uint32_t(i)) : 0;
+  const uint32_t w = pack_codes<SEEDED>(h, r, key, quad);
+  store_codes<WORDS>(p.q + (slot < 0 ? 0 : slot) * p.elems + e0 + 4 * quad, n, w);
+  if (quad == 0 && slot >= 0) p.scale[slot * p.rows + row] = r.scale;
 }
 
-template <typename OUT>
-__global__ __launch_bounds__(64) void cache_read_kernel(OUT* out, CacheParams p) {
-  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (i >= p.count * p.rows) return;
-  const int64_t b = i / p.rows, row = i % p.rows, slot = slot_of(p.read_slots, b, p.slots);
-  const int64_t e0 = row * p.row_len, n = e0 + p.row_len < p.elems ? p.row_len : p.elems - e0;
-  const float scale = slot < 0 ? 0.f : p.scale[slot * p.rows + row];
-  for (int64_t j = 0; j < n; ++j) {
-    const float v = slot < 0 ? 0.f : float(p.q[slot * p.elems + e0 + j]) * scale;
-    if constexpr (sizeof(OUT) == 2) out[b * p.elems + e0 + j] = bf16_rne(v);
-    else out[b * p.elems + e0 + j] = v;
+// Reading: eight values a thread (VEC: row_len % 8 == 0 and everything aligned), else one.
+template <typename OUT, bool VEC>
+__global__ __launch_bounds__(256) void cache_read_kernel(OUT* __restrict__ out, CacheParams p) {
+  constexpr int W = VEC ? 8 : 1;
+  const uint32_t elems = uint32_t(p.elems), per = (elems + 256 * W - 1) / (256 * W);   // workgroups a state
+  const int64_t b = blockIdx.x / per, slot = slot_of(p.read_slots, b, p.slots);
+  const uint32_t e = ((blockIdx.x % per) * 256u + threadIdx.x) * W;
+  if (e >= elems) return;
+  float v[W];
+  if (slot < 0) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = 0.f;
+  } else {
+    const float scale = p.scale[slot * p.rows + e / uint32_t(p.row_len)];
+    const int8_t* const q = p.q + slot * p.elems + e;
+    if constexpr (VEC) {
+      const uint2 w = *reinterpret_cast<const uint2*>(q);
+      const uint32_t lo = w.x ^ kBias, hi = w.y ^ kBias;
+      v[0] = code_byte<0>(lo); v[1] = code_byte<1>(lo); v[2] = code_byte<2>(lo); v[3] = code_byte<3>(lo);
+      v[4] = code_byte<0>(hi); v[5] = code_byte<1>(hi); v[6] = code_byte<2>(hi); v[7] = code_byte<3>(hi);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (v[j] - 128.f) * scale;
+    } else {
+      v[0] = float(*q) * scale;
+    }
+  }
+  OUT* const o = out + b * p.elems + e;
+  if constexpr (!VEC) {
+    if constexpr (sizeof(OUT) == 2) *o = bf16_rne(v[0]);
+    else *o = v[0];
+  } else if constexpr (sizeof(OUT) == 2) {
+    uint4 w;
+    w.x = pack_bf16(v[0], v[1]); w.y = pack_bf16(v[2], v[3]); w.z = pack_bf16(v[4], v[5]); w.w = pack_bf16(v[6], v[7]);
+    *reinterpret_cast<uint4*>(o) = w;
+  } else {
+    *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
 
-// One thread per channel: a first walk over its states for the readout and the largest
-// magnitude, a second one for the codes.
-template <typename IO>
-__global__ __launch_bounds__(64) void step_cached_kernel(StepParams s, CacheParams p) {
+// The 16 states of a lane behind one token, their part of the readout and their largest
+// magnitude: h = keep_j h + in_j with the kept factor and the input given by `coeff(j, keep, in)`.
+// A NaN or an infinity among them shows in the readout (0 * inf is NaN), where it is looked for
+// only then.
+struct LaneStates {
+  float h[16], y, amax;
+  bool bad;
+};
+template <typename F>
+__device__ __forceinline__ void advance(const uint32_t (&w)[4], const float (&C)[16], LaneStates& s, F coeff) {
+  float y = 0.f, amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t c = w[j >> 2] ^ kBias;
+    const float f = float((c >> (8 * (j & 3))) & 0xffu) - 128.f;
+    float keep, in;
+    coeff(j, keep, in);
+    s.h[j] = fmaf(keep, f, in);
+    y = fmaf(C[j], s.h[j], y);
+    amax = fmaxf(amax, fabsf(s.h[j]));
+  }
+  s.y = y;
+  s.amax = amax;
+  s.bad = false;
+  if (__any(!finite(y))) {
+    bool ok = true;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) ok = ok && finite(s.h[j]);
+    s.bad = !ok;
+  }
+}
+
+__device__ __forceinline__ float silu(float z) {
+  return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
+}
+
+// One token of the selective scan.  L lanes a channel, 16 states a lane; a workgroup's channels
+// walk R batch rows, so that the channels' rates stay in registers; B and C of those rows are
+// staged in LDS.  WORDS: dstate % 4 == 0 and the codes on 4-byte boundaries; LINES: dstate % 16
+// == 0 and 16-byte boundaries.
+template <typename IO, int L, bool WORDS, bool LINES, bool SEEDED, int R>
+__global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CacheParams p) {
   using T = io_traits<IO>;
-  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (i >= p.count * p.rows) return;
-  const int64_t b = i / p.rows, d = i % p.rows;
-  const int64_t from = slot_of(p.read_slots, b, p.slots), to = slot_of(p.write_slots, b, p.slots);
-  if (to < 0) return;
-  const float u = T::widen(static_cast<const IO*>(s.u)[b * s.u_sb + d]);
-  const float dt = step_size(T::widen(static_cast<const IO*>(s.delta)[b * s.delta_sb + d]),
-                             s.delta_bias ? s.delta_bias[d] : 0.f, s.softplus != 0);
-  const float scale = from < 0 ? 0.f : p.scale[from * p.rows + d];
-  const IO* const B = static_cast<const IO*>(s.B) + b * s.B_sb;
-  const IO* const C = static_cast<const IO*>(s.C) + b * s.C_sb;
-  auto state = [&](int64_t j) {
-    const float a = s.A[d * s.N + j], ab = __builtin_amdgcn_exp2f(dt * a * kLog2e);
-    const float coeff = (s.euler || a == 0.f) ? dt : zoh_coeff_exact(dt, a, 1.f / a, ab);
-    const float h = from < 0 ? 0.f : float(p.q[(from * p.rows + d) * s.N + j]) * scale;
-    return fmaf(ab, h, coeff * (T::widen(B[j]) * u));
+  constexpr int kN = 16 * L;
+  __shared__ float bc[R][2][kN];
+  const int N = int(s.N), l = threadIdx.x % L;
+  const uint32_t groups = uint32_t((p.rows * L + 255) / 256);       // workgroups a batch row
+  const int64_t d = int64_t(blockIdx.x % groups) * (256 / L) + threadIdx.x / L, b0 = int64_t(blockIdx.x / groups) * R;
+  for (int i = threadIdx.x; i < R * 2 * kN; i += 256) {
+    const int r = i / (2 * kN), c = i / kN % 2, n = i % kN;
+    const int64_t b = b0 + r;
+    float v = 0.f;
+    if (n < N && b < s.batch)
+      v = T::widen(c == 0 ? static_cast<const IO*>(s.B)[b * s.B_sb + n] : static_cast<const IO*>(s.C)[b * s.C_sb + n]);
+    bc[r][c][n] = v;
+  }
+  __syncthreads();
+  const bool live = d < p.rows;
+  const int n0 = 16 * l;                           // this lane's first state
+  float A[16], iA[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float a = live && n0 + j < N ? s.A[d * N + n0 + j] : 0.f;
+    A[j] = s.euler ? 0.f : a;                      // (first order: the coefficient of a zero rate)
+    iA[j] = A[j] == 0.f ? 0.f : 1.f / A[j];
+    if (s.euler) iA[j] = a;                        // (and the rate of the decay alone)
+  }
+  const float skip = live && s.Dskip ? s.Dskip[d] : 0.f, bias = live && s.delta_bias ? s.delta_bias[d] : 0.f;
+  const int64_t seed = SEEDED ? *p.seed : 0;
+
+  struct Row {
+    uint32_t w[4];
+    float scale, u, dt, z;
+    int64_t to;
   };
-  float y = s.Dskip ? s.Dskip[d] * u : 0.f, amax = 0.f;
-  bool bad = false;
-  for (int64_t j = 0; j < s.N; ++j) {
-    const float h = state(j);
-    y = fmaf(T::widen(C[j]), h, y);
-    amax = fmaxf(amax, fabsf(h));
-    bad |= !finite(h);
+  auto load = [&](int r, Row& v) __attribute__((always_inline)) {
+    const int64_t b = b0 + r;
+    v.to = b < s.batch ? slot_of(p.write_slots, b, p.slots) : -1;
+    v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
+    v.scale = v.u = v.dt = v.z = 0.f;
+    if (v.to < 0 || !live) return;
+    const int64_t from = slot_of(p.read_slots, b, p.slots);
+    v.u = T::widen(static_cast<const IO*>(s.u)[b * s.u_sb + d]);
+    v.dt = T::widen(static_cast<const IO*>(s.delta)[b * s.delta_sb + d]);
+    if (s.z) v.z = T::widen(static_cast<const IO*>(s.z)[b * s.z_sb + d]);
+    if (from < 0) return;
+    const int8_t* const q = p.q + (from * p.rows + d) * N + n0;
+    v.scale = p.scale[from * p.rows + d];
+    if constexpr (LINES) {
+      if (n0 < N) {
+        const uint4 t = *reinterpret_cast<const uint4*>(q);
+        v.w[0] = t.x; v.w[1] = t.y; v.w[2] = t.z; v.w[3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v.w[k] = load_codes<WORDS>(q + 4 * k, N - n0 - 4 * k);
+    }
+  };
+  Row cur;
+  load(0, cur);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    Row next;
+    if (r + 1 < R) load(r + 1, next);
+    if (cur.to >= 0) {                             // (the whole workgroup alike)
+      const float x = cur.dt + bias, dt = s.softplus ? softplus_f32(x) : x;
+      float C[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) C[j] = bc[r][1][n0 + j];
+      LaneStates st;
+      if (s.euler) {
+        advance(cur.w, C, st, [&](int j, float& keep, float& in) {
+          keep = __builtin_amdgcn_exp2f(dt * iA[j] * kLog2e) * cur.scale;
+          in = dt * (bc[r][0][n0 + j] * cur.u);
+        });
+      } else {
+        advance(cur.w, C, st, [&](int j, float& keep, float& in) {
+          const float ab = __builtin_amdgcn_exp2f(dt * A[j] * kLog2e);
+          keep = ab * cur.scale;
+          in = zoh_coeff_exact(dt, A[j], iA[j], ab) * (bc[r][0][n0 + j] * cur.u);
+        });
+      }
+      const float amax = group_all<L>(st.amax, fmax2), bad = group_all<L>(st.bad ? 1.f : 0.f, fmax2);
+      float y = group_all<L>(st.y, fadd2);
+      const RowScale rs = row_scale(amax, bad != 0.f);
+      const int64_t b = b0 + r;
+      const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows + d)) : 0;
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float h4[4] = {st.h[4 * k], st.h[4 * k + 1], st.h[4 * k + 2], st.h[4 * k + 3]};
+        w[k] = pack_codes<SEEDED>(h4, rs, key, uint32_t(4 * l + k));
+      }
+      if (live) {
+        int8_t* const q = p.q + (cur.to * p.rows + d) * N + n0;
+        if constexpr (LINES) {
+          if (n0 < N) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) store_codes<WORDS>(q + 4 * k, N - n0 - 4 * k, w[k]);
+        }
+        if (l == 0) {
+          p.scale[cur.to * p.rows + d] = rs.scale;
+          y = fmaf(skip, cur.u, y);
+          if (s.z) y *= silu(cur.z);
+          IO* const o = static_cast<IO*>(s.y) + b * s.y_sb + d;
+          if constexpr (sizeof(IO) == 2) *o = bf16_rne(y);
+          else *o = y;
+        }
+      }
+    }
+    if (r + 1 < R) cur = next;
   }
-  const RowScale rs = row_scale(amax, bad);
-  const uint32_t key = p.seed ? row_key(*p.seed, uint32_t(i)) : 0;
-  for (int64_t j = 0; j < s.N; ++j)
-    p.q[(to * p.rows + d) * s.N + j] = code(state(j), rs.inv, rounding_offset(p.seed != nullptr, key, uint32_t(j)), bad);
-  p.scale[to * p.rows + d] = rs.scale;
-  if (s.z) {
-    const float z = T::widen(static_cast<const IO*>(s.z)[b * s.z_sb + d]);
-    y *= z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
-  }
-  IO* const yo = static_cast<IO*>(s.y) + b * s.y_sb + d;
-  if constexpr (sizeof(IO) == 2) *yo = bf16_rne(y);
-  else *yo = y;
 }
 
-// One thread per (head, channel) row of N states.
-__global__ __launch_bounds__(64) void ssd_step_cached_kernel(SsdParams s, CacheParams p) {
+// One token of the scalar-decay layer.  N / 16 lanes a row (head and channel), 16 states a
+// lane; a workgroup walks `passes` groups of rows of one batch row, whose B and C stay in
+// registers.
+template <int N, bool LINES, bool SEEDED>
+__global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, CacheParams p, int passes) {
   using T = io_traits<uint16_t>;
-  const int64_t i = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (i >= p.count * p.rows) return;
-  const int64_t b = i / p.rows, row = i % p.rows, head = row / 64;
-  const int64_t from = slot_of(p.read_slots, b, p.slots), to = slot_of(p.write_slots, b, p.slots);
-  if (to < 0) return;
-  const float x = T::widen(static_cast<const uint16_t*>(s.x)[i]);
-  const float dt = T::widen(static_cast<const uint16_t*>(s.delta)[b * s.H + head]), a = s.A[head];
-  const float ab = __builtin_amdgcn_exp2f(dt * a * kLog2e);
-  const float drive = ((s.euler || a == 0.f) ? dt : zoh_coeff_exact(dt, a, 1.f / a, ab)) * x;
-  const float scale = from < 0 ? 0.f : p.scale[from * p.rows + row];
-  const uint16_t* const B = static_cast<const uint16_t*>(s.B) + b * s.N;
-  const uint16_t* const C = static_cast<const uint16_t*>(s.C) + b * s.N;
-  auto state = [&](int64_t j) {
-    const float h = from < 0 ? 0.f : float(p.q[(from * p.rows + row) * s.N + j]) * scale;
-    return fmaf(ab, h, drive * T::widen(B[j]));
+  constexpr int L = N / 16, RP = 256 / L;
+  const int l = threadIdx.x % L;
+  const uint32_t groups = uint32_t((p.rows + RP * passes - 1) / (RP * passes));     // workgroups a batch row
+  const int64_t b = blockIdx.x / groups, to = slot_of(p.write_slots, b, p.slots), from = slot_of(p.read_slots, b, p.slots);
+  if (to < 0) return;                              // padding
+  const int64_t row0 = int64_t(blockIdx.x % groups) * passes * RP + threadIdx.x / L;
+  float B[16], C[16];
+  {
+    const uint4* const bp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.B) + b * N + 16 * l);
+    const uint4* const cp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.C) + b * N + 16 * l);
+    const uint4 b0 = bp[0], b1 = bp[1], c0 = cp[0], c1 = cp[1];
+    const uint32_t bw[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+    const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      B[2 * j] = __uint_as_float(bw[j] << 16);
+      B[2 * j + 1] = __uint_as_float(bw[j] & 0xffff0000u);
+      C[2 * j] = __uint_as_float(cw[j] << 16);
+      C[2 * j + 1] = __uint_as_float(cw[j] & 0xffff0000u);
+    }
+  }
+  const int64_t seed = SEEDED ? *p.seed : 0;
+  struct Row {
+    uint32_t w[4];
+    float scale, x, z, dt, a;
   };
-  float y = s.Dskip ? s.Dskip[row] * x : 0.f, amax = 0.f;
-  bool bad = false;
-  for (int64_t j = 0; j < s.N; ++j) {
-    const float h = state(j);
-    y = fmaf(T::widen(C[j]), h, y);
-    amax = fmaxf(amax, fabsf(h));
-    bad |= !finite(h);
+  auto load = [&](int64_t row, Row& v) __attribute__((always_inline)) {
+    v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
+    v.scale = v.x = v.z = v.dt = v.a = 0.f;
+    if (row >= p.rows) return;
+    const int64_t head = row >> 6;
+    v.x = T::widen(static_cast<const uint16_t*>(s.x)[b * p.rows + row]);
+    v.dt = T::widen(static_cast<const uint16_t*>(s.delta)[b * s.H + head]);
+    v.a = s.A[head];
+    if (s.z) v.z = T::widen(static_cast<const uint16_t*>(s.z)[b * p.rows + row]);
+    if (from < 0) return;
+    const int8_t* const q = p.q + (from * p.rows + row) * N + 16 * l;
+    v.scale = p.scale[from * p.rows + row];
+    if constexpr (LINES) {
+      const uint4 t = *reinterpret_cast<const uint4*>(q);
+      v.w[0] = t.x; v.w[1] = t.y; v.w[2] = t.z; v.w[3] = t.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v.w[k] = load_codes<false>(q + 4 * k, 4);
+    }
+  };
+  Row cur;
+  load(row0, cur);
+  for (int t = 0; t < passes; ++t) {
+    const int64_t row = row0 + int64_t(t) * RP;
+    Row next;
+    if (t + 1 < passes) load(row + RP, next);
+    const float ab = __builtin_amdgcn_exp2f(cur.dt * cur.a * kLog2e);
+    const float drive = ((s.euler || cur.a == 0.f) ? cur.dt : zoh_coeff_exact(cur.dt, cur.a, 1.f / cur.a, ab)) * cur.x;
+    const float keep = ab * cur.scale;
+    LaneStates st;
+    advance(cur.w, C, st, [&](int j, float& k, float& in) {
+      k = keep;
+      in = drive * B[j];
+    });
+    const float amax = group_all<L>(st.amax, fmax2), bad = group_all<L>(st.bad ? 1.f : 0.f, fmax2);
+    float y = group_all<L>(st.y, fadd2);
+    const RowScale rs = row_scale(amax, bad != 0.f);
+    const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows + row)) : 0;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float h4[4] = {st.h[4 * k], st.h[4 * k + 1], st.h[4 * k + 2], st.h[4 * k + 3]};
+      w[k] = pack_codes<SEEDED>(h4, rs, key, uint32_t(4 * l + k));
+    }
+    if (row < p.rows) {
+      int8_t* const q = p.q + (to * p.rows + row) * N + 16 * l;
+      if constexpr (LINES) {
+        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) store_codes<false>(q + 4 * k, 4, w[k]);
+      }
+      if (l == 0) {
+        p.scale[to * p.rows + row] = rs.scale;
+        if (s.Dskip) y = fmaf(s.Dskip[row], cur.x, y);
+        if (s.z) y *= silu(cur.z);
+        static_cast<uint16_t*>(s.y)[b * p.rows + row] = bf16_rne(y);
+      }
+    }
+    cur = next;
   }
-  const RowScale rs = row_scale(amax, bad);
-  const uint32_t key = p.seed ? row_key(*p.seed, uint32_t(i)) : 0;
-  for (int64_t j = 0; j < s.N; ++j)
-    p.q[(to * p.rows + row) * s.N + j] =
-        code(state(j), rs.inv, rounding_offset(p.seed != nullptr, key, uint32_t(j)), bad);
-  p.scale[to * p.rows + row] = rs.scale;
-  if (s.z) {
-    const float z = T::widen(static_cast<const uint16_t*>(s.z)[i]);
-    y *= z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
-  }
-  static_cast<uint16_t*>(s.y)[i] = bf16_rne(y);
 }
 
-unsigned row_blocks(const CacheParams& p, int per) { return unsigned((p.count * p.rows + per - 1) / per); }
+bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <int L, bool WORDS>
+hipError_t launch_write_t(const float* state, const CacheParams& p, hipStream_t stream) {
+  const dim3 grid(unsigned((p.count * p.rows * L + 255) / 256));
+  if (p.seed) hipLaunchKernelGGL((cache_write_kernel<L, WORDS, true>), grid, dim3(256), 0, stream, state, p);
+  else hipLaunchKernelGGL((cache_write_kernel<L, WORDS, false>), grid, dim3(256), 0, stream, state, p);
+  return hipGetLastError();
+}
+
+template <typename IO, int L, bool WORDS, bool LINES, int R>
+hipError_t launch_step_t(const StepParams& s, const CacheParams& p, hipStream_t stream) {
+  const dim3 grid(unsigned((p.rows * L + 255) / 256 * ((s.batch + R - 1) / R)));
+  if (p.seed) hipLaunchKernelGGL((step_cached_kernel<IO, L, WORDS, LINES, true, R>), grid, dim3(256), 0, stream, s, p);
+  else hipLaunchKernelGGL((step_cached_kernel<IO, L, WORDS, LINES, false, R>), grid, dim3(256), 0, stream, s, p);
+  return hipGetLastError();
+}
+
+template <typename IO, int L>
+hipError_t launch_step_l(const StepParams& s, const CacheParams& p, hipStream_t stream) {
+  const bool words = s.N % 4 == 0 && on(p.q, 4), lines = s.N % 16 == 0 && on(p.q, 16);
+  // several batch rows a workgroup once they still leave several workgroups a compute unit
+  const bool many = (p.rows * L + 255) / 256 * s.batch >= 4096;
+  if (lines) return many ? launch_step_t<IO, L, true, true, 4>(s, p, stream) : launch_step_t<IO, L, true, true, 1>(s, p, stream);
+  if (words) return launch_step_t<IO, L, true, false, 1>(s, p, stream);
+  return launch_step_t<IO, L, false, false, 1>(s, p, stream);
+}
+
+template <int N>
+hipError_t launch_ssd_n(const SsdParams& s, const CacheParams& p, hipStream_t stream) {
+  constexpr int RP = 256 / (N / 16);
+  const int64_t groups = (p.rows + RP - 1) / RP;
+  int passes = 1;                                  // a power of two that leaves at least 1024 workgroups, at most 8
+  while (passes < 8 && groups * p.count >= 2048 * int64_t(passes)) passes *= 2;
+  const dim3 grid(unsigned((p.rows + RP * passes - 1) / (RP * passes) * p.count));
+  const bool lines = on(p.q, 16);
+  if (lines) {
+    if (p.seed) hipLaunchKernelGGL((ssd_step_cached_kernel<N, true, true>), grid, dim3(256), 0, stream, s, p, passes);
+    else hipLaunchKernelGGL((ssd_step_cached_kernel<N, true, false>), grid, dim3(256), 0, stream, s, p, passes);
+  } else {
+    if (p.seed) hipLaunchKernelGGL((ssd_step_cached_kernel<N, false, true>), grid, dim3(256), 0, stream, s, p, passes);
+    else hipLaunchKernelGGL((ssd_step_cached_kernel<N, false, false>), grid, dim3(256), 0, stream, s, p, passes);
+  }
+  return hipGetLastError();
+}
 
 }  // namespace
 
 hipError_t launch_cache_write(const float* state, const CacheParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(cache_write_kernel, dim3(row_blocks(p, 64)), dim3(64), 0, stream, state, p);
-  return hipGetLastError();
+  const bool words = p.row_len % 4 == 0 && p.elems % 4 == 0 && on(p.q, 4) && on(state, 16);
+  auto with = [&](auto w) {
+    constexpr bool W = decltype(w)::value;
+    if (p.row_len <= 4) return launch_write_t<1, W>(state, p, stream);
+    if (p.row_len <= 8) return launch_write_t<2, W>(state, p, stream);
+    if (p.row_len <= 16) return launch_write_t<4, W>(state, p, stream);
+    if (p.row_len <= 32) return launch_write_t<8, W>(state, p, stream);
+    if (p.row_len <= 64) return launch_write_t<16, W>(state, p, stream);
+    return launch_write_t<32, W>(state, p, stream);
+  };
+  return words ? with(std::true_type{}) : with(std::false_type{});
 }
 
 hipError_t launch_cache_read(bool bf16, void* out, const CacheParams& p, hipStream_t stream) {
-  const dim3 grid(row_blocks(p, 64));
-  if (bf16) hipLaunchKernelGGL(cache_read_kernel<uint16_t>, grid, dim3(64), 0, stream, static_cast<uint16_t*>(out), p);
-  else hipLaunchKernelGGL(cache_read_kernel<float>, grid, dim3(64), 0, stream, static_cast<float*>(out), p);
-  return hipGetLastError();
+  const bool vec = p.row_len % 8 == 0 && p.elems % 8 == 0 && on(p.q, 8) && on(out, 16);
+  const int64_t per = vec ? 2048 : 256;
+  const dim3 grid(unsigned((p.elems + per - 1) / per * p.count));
+  auto with = [&](auto io, auto v) {
+    using OUT = decltype(io);
+    hipLaunchKernelGGL((cache_read_kernel<OUT, decltype(v)::value>), grid, dim3(256), 0, stream, static_cast<OUT*>(out), p);
+    return hipGetLastError();
+  };
+  if (bf16) return vec ? with(uint16_t{}, std::true_type{}) : with(uint16_t{}, std::false_type{});
+  return vec ? with(float{}, std::true_type{}) : with(float{}, std::false_type{});
 }
 
 hipError_t launch_step_cached(bool bf16, const StepParams& s, const CacheParams& p, hipStream_t stream) {
-  const dim3 grid(row_blocks(p, 64));
-  if (bf16) hipLaunchKernelGGL(step_cached_kernel<uint16_t>, grid, dim3(64), 0, stream, s, p);
-  else hipLaunchKernelGGL(step_cached_kernel<float>, grid, dim3(64), 0, stream, s, p);
-  return hipGetLastError();
+  auto with = [&](auto io) {
+    using IO = decltype(io);
+    if (s.N <= 16) return launch_step_l<IO, 1>(s, p, stream);
+    if (s.N <= 32) return launch_step_l<IO, 2>(s, p, stream);
+    return launch_step_l<IO, 4>(s, p, stream);
+  };
+  return bf16 ? with(uint16_t{}) : with(float{});
 }
 
 hipError_t launch_ssd_step_cached(const SsdParams& s, const CacheParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(ssd_step_cached_kernel, dim3(row_blocks(p, 64)), dim3(64), 0, stream, s, p);
-  return hipGetLastError();
+  return s.N == 64 ? launch_ssd_n<64>(s, p, stream) : launch_ssd_n<128>(s, p, stream);
 }
 
 }  // namespace selscan

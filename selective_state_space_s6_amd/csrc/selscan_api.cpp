@@ -1176,7 +1176,9 @@ static int cache_check(const selscan_cache_dims* c, int64_t count, const int32_t
   if (c->row_len > 128 || c->elems > (int64_t(1) << 31) - 1 || c->slots > (int64_t(1) << 31) - 1)
     return SELSCAN_ERR_UNSUPPORTED;
   const int64_t rows = (c->elems + c->row_len - 1) / c->row_len;
-  if (count > ((int64_t(1) << 32) - 1) / rows) return SELSCAN_ERR_UNSUPPORTED;   // 32-bit row numbers
+  // 32-bit row numbers, and workgroups of at least 256 values in one grid
+  if (count > ((int64_t(1) << 32) - 1) / rows || count > ((int64_t(1) << 31) - 1) / ((c->elems + 255) / 256))
+    return SELSCAN_ERR_UNSUPPORTED;
   if (!ids && count > c->slots) return SELSCAN_ERR_DIMS;                          // 0, 1, 2, ... must exist
   if (count > 0 && c->slots > 0 && (!q || !scale)) return SELSCAN_ERR_NULL;
   if (!all_aligned({scale, ids}, 4) || !all_aligned({seed}, 8)) return SELSCAN_ERR_ALIGN;
