@@ -592,22 +592,23 @@ CACHE_ROW = 64            # row length of a [D] state (the gated recurrence's) i
 
 class _On:
     """The GPU and the stream of one call: what is allocated inside belongs to that stream."""
+    __slots__ = ("device", "index", "handle", "_guards")
 
     def __init__(self, t, stream):
         import torch
-        if not t.is_cuda:
+        index = t.get_device()
+        if index < 0:
             raise ValueError("the tensors must be GPU tensors")
-        self.device = t.device
-        self._guards = []
-        if torch.cuda.current_device() != t.device.index:
-            self._guards.append(torch.cuda.device(t.device))
+        self.device, self.index, self._guards = t.device, index, ()
         if stream is None:
-            self.handle = torch.cuda.current_stream(t.device).cuda_stream
+            self.handle = torch.cuda.current_stream(index).cuda_stream
         else:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
             self.handle = stream.cuda_stream
-            self._guards.append(torch.cuda.stream(stream))
+            self._guards = (torch.cuda.stream(stream),)
+        if torch.cuda.current_device() != index:
+            self._guards = (torch.cuda.device(index),) + self._guards
 
     def __enter__(self):
         for g in self._guards:
@@ -621,25 +622,26 @@ class _On:
 
     def check(self, name, t, dtype, shape, contiguous=True):
         """t (None passes) must be of this dtype and shape, on this GPU, and contiguous unless said."""
-        if t is None:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == self.index
+                         and (not contiguous or t.is_contiguous())):
             return
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-        if t.device != self.device:
+        if t.get_device() != self.index:
             raise ValueError("%s must be on %s, got %s" % (name, self.device, t.device))
-        if contiguous and not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
+        raise ValueError("%s must be contiguous" % name)
 
     def workspace(self, given, need):
-        """(pointer, bytes) of the workspace: the given one, or one of torch's caching allocator."""
+        """(tensor, pointer, bytes) of the workspace: the given one, or one of torch's caching allocator."""
         import torch
         if given is None:
             if need == 0:
                 return None, None, 0
             given = torch.empty(need, dtype=torch.uint8, device=self.device)
-        elif given.device != self.device or not given.is_contiguous():
+            return given, given.data_ptr(), need
+        if given.get_device() != self.index or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on %s" % self.device)
         return given, given.data_ptr(), given.numel() * given.element_size()
 
@@ -658,13 +660,9 @@ def _gated_dims(on, x, r, g, lam, y, reset, c):
             if D > 1 and t.stride(2) != 1:
                 raise ValueError("%s: the channel axis must be unit-stride" % name)
     on.check("lam", lam, torch.float32, (D,))
-    d = GatedDims(abi_version=SELSCAN_ABI_VERSION, io_dtype=_io_code(x.dtype), batch=batch, seqlen=L, dim=D,
-                  x_sb=x.stride(0), x_sl=x.stride(1), r_sb=r.stride(0), r_sl=r.stride(1), g_sb=g.stride(0),
-                  g_sl=g.stride(1), decay_c=float(c))
-    if y is not None:
-        d.y_sb, d.y_sl = y.stride(0), y.stride(1)
-    else:
-        d.y_sb, d.y_sl = L * D, D
+    ys = (L * D, D) if y is None else (y.stride(0), y.stride(1))
+    d = GatedDims(SELSCAN_ABI_VERSION, _io_code(x.dtype), batch, L, D, x.stride(0), x.stride(1), r.stride(0), r.stride(1),
+                  g.stride(0), g.stride(1), ys[0], ys[1], 0, c, 0)
     if reset is not None:
         if reset.dtype not in (torch.bool, torch.uint8):
             raise TypeError("reset must be a bool or uint8 [batch, L] tensor")
@@ -752,7 +750,14 @@ def gated_scan_step(x, r, g, lam, *, state, y=None, c: float = 8.0, stream=None)
         batch, D = x.shape
         if y is None:
             y = torch.empty((batch, D), dtype=x.dtype, device=x.device)
-        dims = _gated_dims(on, *(t.unsqueeze(1) for t in (x, r, g)), lam, y.unsqueeze(1), None, c)
+        shape = x.shape
+        for name, t in (("x", x), ("r", r), ("g", g), ("y", y)):
+            on.check(name, t, x.dtype, shape, contiguous=False)
+            if D > 1 and t.stride(1) != 1:
+                raise ValueError("%s: the channel axis must be unit-stride" % name)
+        on.check("lam", lam, torch.float32, (D,))
+        dims = GatedDims(SELSCAN_ABI_VERSION, _io_code(x.dtype), batch, 1, D, x.stride(0), D, r.stride(0), D, g.stride(0), D,
+                         y.stride(0), D, 0, c, 0)
         on.check("state", state, torch.float32, (batch, D))
         st = lib().gated_scan_step(_p(x), _p(r), _p(g), _p(lam), _p(y), _p(state), ctypes.byref(dims), on.handle)
         if st != SELSCAN_OK:
@@ -775,16 +780,17 @@ def state_cache(slots: int, *state_shape: int, device="cuda"):
 
 def _cache_dims(on, q, scale, seed):
     import torch
-    if q.dim() < 2:
+    shape = q.shape
+    if len(shape) < 2:
         raise ValueError("q must be [slots, *state_shape]")
-    row_len = CACHE_ROW if q.dim() == 2 else int(q.shape[-1])
-    slots, elems = int(q.shape[0]), 1
-    for n in q.shape[1:]:
-        elems *= int(n)
-    on.check("q", q, torch.int8, q.shape)
-    on.check("scale", scale, torch.float32, (slots, -(-elems // row_len) if row_len else 0))
+    row_len = CACHE_ROW if len(shape) == 2 else shape[-1]
+    elems = 1
+    for n in shape[1:]:
+        elems *= n
+    on.check("q", q, torch.int8, shape)
+    on.check("scale", scale, torch.float32, (shape[0], -(-elems // row_len) if row_len else 0))
     on.check("seed", seed, torch.int64, (1,))
-    return CacheDims(abi_version=SELSCAN_ABI_VERSION, slots=slots, elems=elems, row_len=row_len)
+    return CacheDims(SELSCAN_ABI_VERSION, 0, shape[0], elems, row_len)
 
 
 def state_cache_write(state, q, scale, *, slots=None, seed=None, stream=None) -> None:
@@ -795,7 +801,7 @@ def state_cache_write(state, q, scale, *, slots=None, seed=None, stream=None) ->
     import torch
     with _On(q, stream) as on:
         dims = _cache_dims(on, q, scale, seed)
-        on.check("state", state, torch.float32, (state.shape[0],) + tuple(q.shape[1:]))
+        on.check("state", state, torch.float32, state.shape[:1] + q.shape[1:])
         on.check("slots", slots, torch.int32, (state.shape[0],))
         st = lib().state_cache_write(_p(state), _p(slots), state.shape[0], _p(q), _p(scale), _p(seed),
                                      ctypes.byref(dims), on.handle)
@@ -809,7 +815,7 @@ def state_cache_read(q, scale, *, slots=None, out=None, dtype=None, stream=None)
     import torch
     with _On(q, stream) as on:
         dims = _cache_dims(on, q, scale, None)
-        shape = (int(q.shape[0]) if slots is None else int(slots.shape[0]),) + tuple(q.shape[1:])
+        shape = (q if slots is None else slots).shape[:1] + q.shape[1:]
         on.check("slots", slots, torch.int32, shape[:1])
         if out is None:
             out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
@@ -833,28 +839,27 @@ def selective_scan_step_cached(u, delta, A, B, C, Dskip=None, z=None, y=None, *,
     if u.dim() != 2:
         raise ValueError("u must be [batch, D] (one token per batch row)")
     with _On(u, stream) as on:
-        batch, D = (int(v) for v in u.shape)
-        on.check("A", A, torch.float32, (D, A.shape[-1]))
-        N = int(A.shape[1])
+        batch, D = u.shape
+        N = A.shape[-1]
+        on.check("A", A, torch.float32, (D, N))
         if y is None:
             y = torch.empty((batch, D), dtype=u.dtype, device=u.device)
-        d = SelscanDims(abi_version=SELSCAN_ABI_VERSION, io_dtype=_io_code(u.dtype), batch=batch, seqlen=1, dim=D,
-                        dstate=N, discretization=DISCRETIZATIONS[discretization],
-                        delta_softplus=1 if delta_softplus else 0)
-        for name, t, width in (("u", u, D), ("delta", delta, D), ("B", B, N), ("C", C, N), ("z", z, D), ("y", y, D)):
+        io, per_channel = u.dtype, delta.dim() == 1
+        for name, t, shape in (("u", u, (batch, D)), ("delta", delta, (D,) if per_channel else (batch, D)), ("B", B, (batch, N)),
+                               ("C", C, (batch, N)), ("z", z, (batch, D)), ("y", y, (batch, D))):
             if t is None:
                 continue
-            per_channel = name == "delta" and t.dim() == 1
-            on.check(name, t, u.dtype, (D,) if per_channel else (batch, width), contiguous=False)
-            if width > 1 and t.stride(-1) != 1:
+            on.check(name, t, io, shape, contiguous=False)
+            if shape[-1] > 1 and t.stride(-1) != 1:
                 raise ValueError("%s must have a unit-stride last axis" % name)
-            if not per_channel:
-                setattr(d, name + "_sb", t.stride(0))
-                setattr(d, name + "_sl", width)
+        d = SelscanDims(SELSCAN_ABI_VERSION, _io_code(io), batch, 1, D, N, u.stride(0), D,
+                        0 if per_channel else delta.stride(0), 0 if per_channel else D, 0 if z is None else z.stride(0), D,
+                        y.stride(0), D, B.stride(0), N, 0, C.stride(0), N, 0, 0, 0, DISCRETIZATIONS[discretization],
+                        1 if delta_softplus else 0)
         on.check("Dskip", Dskip, torch.float32, (D,))
         on.check("delta_bias", delta_bias, torch.float32, (D,))
         cache = _cache_dims(on, q, scale, seed)
-        if tuple(q.shape[1:]) != (D, N):
+        if q.shape[1:] != (D, N):
             raise ValueError("q must be [slots, %d, %d]" % (D, N))
         on.check("read_slots", read_slots, torch.int32, (batch,))
         on.check("write_slots", write_slots, torch.int32, (batch,))
@@ -876,8 +881,8 @@ def selective_scan_ssd_step_cached(x, delta, A, B, C, Dskip=None, z=None, y=None
     if x.dim() != 3:
         raise ValueError("x must be [batch, H, 64] (one token per batch row)")
     with _On(x, stream) as on:
-        batch, H, P = (int(v) for v in x.shape)
-        N = int(B.shape[-1])
+        batch, H, P = x.shape
+        N = B.shape[-1]
         if y is None:
             y = torch.empty((batch, H, P), dtype=torch.bfloat16, device=x.device)
         for name, t, shape in (("x", x, (batch, H, P)), ("delta", delta, (batch, H)), ("B", B, (batch, N)),
@@ -886,7 +891,7 @@ def selective_scan_ssd_step_cached(x, delta, A, B, C, Dskip=None, z=None, y=None
         on.check("A", A, torch.float32, (H,))
         on.check("Dskip", Dskip, torch.float32, (H * P,))
         cache = _cache_dims(on, q, scale, seed)
-        if tuple(q.shape[1:]) != (H, P, N):
+        if q.shape[1:] != (H, P, N):
             raise ValueError("q must be [slots, %d, %d, %d]" % (H, P, N))
         on.check("read_slots", read_slots, torch.int32, (batch,))
         on.check("write_slots", write_slots, torch.int32, (batch,))
