@@ -1,8 +1,7 @@
 // cache_kernels.hip -- the 8-bit state cache: writing, reading, and the decode steps of the
 // selective scan and of the scalar-decay layer on cached states.  Every kernel is bound by the
 // bytes of the states, or close to it by the arithmetic on each of them, which therefore is
-// kept short: codes are widened from biased bytes (v_cvt_f32_ubyte), rounded and packed in one
-// instruction (v_cvt_pk_u8_f32), and a pair of values shares one 32-bit mix for its rounding.
+// kept short: codes are rounded and packed in one instruction (v_cvt_pk_u8_f32, biased by 128), and a pair of values shares one 32-bit mix for its rounding.
 #include <type_traits>
 
 #include "device_common.h"
@@ -41,6 +40,13 @@ __device__ __forceinline__ RowScale row_scale(float amax, bool bad) {
   if (bad) return {__builtin_nanf(""), 0.f, true};
   if (!(amax >= kTinyRow)) return {0.f, 0.f, false};
   return {amax / kCodes, 126.99998f / amax, false};
+}
+// The same within 2^-20, without a division: for states that a step has just formed.
+__device__ __forceinline__ RowScale row_scale_fast(float amax, bool bad) {
+  RowScale r{amax * (1.f / kCodes), 126.9999f * __builtin_amdgcn_rcpf(amax), bad};
+  if (!(amax >= kTinyRow)) r.scale = r.inv = 0.f;
+  if (bad) r.scale = __builtin_nanf("");
+  return r;
 }
 // Four codes of values 4 quad .. 4 quad + 3 of a row.  v_cvt_pk_u8_f32 rounds to nearest, ties
 // to even: floor(t + u) is the rounding of t + u - 1/2, u = (k + 1/2) / 65536, formed as 128 +
@@ -113,8 +119,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
-// byte j of biased codes as a float 1 .. 255
-template <int J> __device__ __forceinline__ float code_byte(uint32_t w) { return float((w >> (8 * J)) & 0xffu); }
+// code j of four (one v_cvt_f32_i32 of a sign-extended byte)
+__device__ __forceinline__ float code_value(uint32_t w, int j) { return float(int8_t(w >> (8 * j))); }
 
 // Writing: four values a lane, L lanes a row, whole lines in and out.
 template <int L, bool WORDS, bool SEEDED>
@@ -165,11 +171,8 @@ __global__ __launch_bounds__(256) void cache_read_kernel(OUT* __restrict__ out, 
     const int8_t* const q = p.q + slot * p.elems + e;
     if constexpr (VEC) {
       const uint2 w = *reinterpret_cast<const uint2*>(q);
-      const uint32_t lo = w.x ^ kBias, hi = w.y ^ kBias;
-      v[0] = code_byte<0>(lo); v[1] = code_byte<1>(lo); v[2] = code_byte<2>(lo); v[3] = code_byte<3>(lo);
-      v[4] = code_byte<0>(hi); v[5] = code_byte<1>(hi); v[6] = code_byte<2>(hi); v[7] = code_byte<3>(hi);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (v[j] - 128.f) * scale;
+      for (int j = 0; j < 8; ++j) v[j] = code_value(j < 4 ? w.x : w.y, j & 3) * scale;
     } else {
       v[0] = float(*q) * scale;
     }
@@ -189,9 +192,8 @@ __global__ __launch_bounds__(256) void cache_read_kernel(OUT* __restrict__ out, 
 }
 
 // The 16 states of a lane behind one token, their part of the readout and their largest
-// magnitude: h = keep_j h + in_j with the kept factor and the input given by `coeff(j, keep, in)`.
-// A NaN or an infinity among them shows in the readout (0 * inf is NaN), where it is looked for
-// only then.
+// magnitude: h = keep q + a b, where `coeff(j, keep, a, b)` gives the factors.  A NaN or an
+// infinity among the states shows in the readout (0 * inf is NaN); only then is it looked for.
 struct LaneStates {
   float h[16], y, amax;
   bool bad;
@@ -201,11 +203,9 @@ __device__ __forceinline__ void advance(const uint32_t (&w)[4], const float (&C)
   float y = 0.f, amax = 0.f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const uint32_t c = w[j >> 2] ^ kBias;
-    const float f = float((c >> (8 * (j & 3))) & 0xffu) - 128.f;
-    float keep, in;
-    coeff(j, keep, in);
-    s.h[j] = fmaf(keep, f, in);
+    float keep, a, b;
+    coeff(j, keep, a, b);
+    s.h[j] = fmaf(a, b, keep * code_value(w[j >> 2], j & 3));
     y = fmaf(C[j], s.h[j], y);
     amax = fmaxf(amax, fabsf(s.h[j]));
   }
@@ -219,6 +219,16 @@ __device__ __forceinline__ void advance(const uint32_t (&w)[4], const float (&C)
     s.bad = !ok;
   }
 }
+// whether a lane of the row found one
+template <int L> __device__ __forceinline__ bool row_bad(bool bad) {
+  return __any(bad) ? group_all<L>(bad ? 1.f : 0.f, fmax2) != 0.f : false;
+}
+
+// 1 / a to half an ulp (v_rcp_f32 and a Newton step); 0 for 0
+__device__ __forceinline__ float reciprocal(float a) {
+  const float r = __builtin_amdgcn_rcpf(a);
+  return a == 0.f ? 0.f : fmaf(fmaf(-a, r, 1.f), r, r);
+}
 
 __device__ __forceinline__ float silu(float z) {
   return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
@@ -227,7 +237,8 @@ __device__ __forceinline__ float silu(float z) {
 // One token of the selective scan.  L lanes a channel, 16 states a lane; a workgroup's channels
 // walk R batch rows, so that the channels' rates stay in registers; B and C of those rows are
 // staged in LDS.  WORDS: dstate % 4 == 0 and the codes on 4-byte boundaries; LINES: dstate % 16
-// == 0 and 16-byte boundaries.
+// == 0 and codes and rates on 16-byte boundaries (a lane whose states all lie behind the last
+// works on its channel's first rates and zero codes, and stores nothing).
 template <typename IO, int L, bool WORDS, bool LINES, bool SEEDED, int R>
 __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CacheParams p) {
   using T = io_traits<IO>;
@@ -236,6 +247,60 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
   const int N = int(s.N), l = threadIdx.x % L;
   const uint32_t groups = uint32_t((p.rows * L + 255) / 256);       // workgroups a batch row
   const int64_t d = int64_t(blockIdx.x % groups) * (256 / L) + threadIdx.x / L, b0 = int64_t(blockIdx.x / groups) * R;
+  const bool live = d < p.rows;
+  const int n0 = 16 * l;                           // this lane's first state
+  // everything is asked for before anything is waited for
+  int64_t from[R], to[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    to[r] = b0 + r < s.batch ? slot_of(p.write_slots, b0 + r, p.slots) : -1;
+    from[r] = to[r] >= 0 ? slot_of(p.read_slots, b0 + r, p.slots) : -1;
+  }
+  struct Row {                                     // (as loaded: a conversion here would wait for it)
+    uint32_t w[4];
+    float scale;
+    IO u, dt, z;
+  } rows[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    Row& v = rows[r];
+    const int64_t b = b0 + r;
+    v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
+    v.scale = 0.f;
+    v.u = v.dt = v.z = 0;
+    if (to[r] >= 0 && live) {
+      v.u = static_cast<const IO*>(s.u)[b * s.u_sb + d];
+      v.dt = static_cast<const IO*>(s.delta)[b * s.delta_sb + d];
+      if (s.z) v.z = static_cast<const IO*>(s.z)[b * s.z_sb + d];
+    }
+    if (from[r] >= 0 && live) {
+      const int8_t* const q = p.q + (from[r] * p.rows + d) * N + n0;
+      v.scale = p.scale[from[r] * p.rows + d];
+      if constexpr (LINES) {
+        if (n0 < N) {
+          const uint4 t = *reinterpret_cast<const uint4*>(q);
+          v.w[0] = t.x; v.w[1] = t.y; v.w[2] = t.z; v.w[3] = t.w;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v.w[k] = load_codes<WORDS>(q + 4 * k, N - n0 - 4 * k);
+      }
+    }
+  }
+  float A[16], iA[16];
+  if constexpr (LINES) {
+    const float4* const q = reinterpret_cast<const float4*>(s.A + (live ? d * N + (n0 < N ? n0 : 0) : 0));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = q[k];
+      A[4 * k] = v.x; A[4 * k + 1] = v.y; A[4 * k + 2] = v.z; A[4 * k + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) A[j] = live && n0 + j < N ? s.A[d * N + n0 + j] : -1.f;   // (any decay: no state)
+  }
+  const float skip = live && s.Dskip ? s.Dskip[d] : 0.f, bias = live && s.delta_bias ? s.delta_bias[d] : 0.f;
+  const int64_t seed = SEEDED ? *p.seed : 0;
   for (int i = threadIdx.x; i < R * 2 * kN; i += 256) {
     const int r = i / (2 * kN), c = i / kN % 2, n = i % kN;
     const int64_t b = b0 + r;
@@ -245,74 +310,39 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
     bc[r][c][n] = v;
   }
   __syncthreads();
-  const bool live = d < p.rows;
-  const int n0 = 16 * l;                           // this lane's first state
-  float A[16], iA[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float a = live && n0 + j < N ? s.A[d * N + n0 + j] : 0.f;
-    A[j] = s.euler ? 0.f : a;                      // (first order: the coefficient of a zero rate)
-    iA[j] = A[j] == 0.f ? 0.f : 1.f / A[j];
-    if (s.euler) iA[j] = a;                        // (and the rate of the decay alone)
-  }
-  const float skip = live && s.Dskip ? s.Dskip[d] : 0.f, bias = live && s.delta_bias ? s.delta_bias[d] : 0.f;
-  const int64_t seed = SEEDED ? *p.seed : 0;
-
-  struct Row {
-    uint32_t w[4];
-    float scale, u, dt, z;
-    int64_t to;
-  };
-  auto load = [&](int r, Row& v) __attribute__((always_inline)) {
-    const int64_t b = b0 + r;
-    v.to = b < s.batch ? slot_of(p.write_slots, b, p.slots) : -1;
-    v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
-    v.scale = v.u = v.dt = v.z = 0.f;
-    if (v.to < 0 || !live) return;
-    const int64_t from = slot_of(p.read_slots, b, p.slots);
-    v.u = T::widen(static_cast<const IO*>(s.u)[b * s.u_sb + d]);
-    v.dt = T::widen(static_cast<const IO*>(s.delta)[b * s.delta_sb + d]);
-    if (s.z) v.z = T::widen(static_cast<const IO*>(s.z)[b * s.z_sb + d]);
-    if (from < 0) return;
-    const int8_t* const q = p.q + (from * p.rows + d) * N + n0;
-    v.scale = p.scale[from * p.rows + d];
-    if constexpr (LINES) {
-      if (n0 < N) {
-        const uint4 t = *reinterpret_cast<const uint4*>(q);
-        v.w[0] = t.x; v.w[1] = t.y; v.w[2] = t.z; v.w[3] = t.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v.w[k] = load_codes<WORDS>(q + 4 * k, N - n0 - 4 * k);
-    }
-  };
-  Row cur;
-  load(0, cur);
+  for (int j = 0; j < 16; ++j) iA[j] = reciprocal(A[j]);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    Row next;
-    if (r + 1 < R) load(r + 1, next);
-    if (cur.to >= 0) {                             // (the whole workgroup alike)
-      const float x = cur.dt + bias, dt = s.softplus ? softplus_f32(x) : x;
+    const Row& cur = rows[r];
+    if (to[r] >= 0) {                              // (the whole workgroup alike)
+      const float u = T::widen(cur.u), x = T::widen(cur.dt) + bias, dt = s.softplus ? softplus_f32(x) : x;
       float C[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) C[j] = bc[r][1][n0 + j];
       LaneStates st;
       if (s.euler) {
-        advance(cur.w, C, st, [&](int j, float& keep, float& in) {
-          keep = __builtin_amdgcn_exp2f(dt * iA[j] * kLog2e) * cur.scale;
-          in = dt * (bc[r][0][n0 + j] * cur.u);
+        const float du = dt * u;
+        advance(cur.w, C, st, [&](int j, float& keep, float& a, float& b) {
+          keep = __builtin_amdgcn_exp2f(dt * A[j] * kLog2e) * cur.scale;
+          a = du;
+          b = bc[r][0][n0 + j];
         });
       } else {
-        advance(cur.w, C, st, [&](int j, float& keep, float& in) {
-          const float ab = __builtin_amdgcn_exp2f(dt * A[j] * kLog2e);
+        const float du = dt * u;
+        advance(cur.w, C, st, [&](int j, float& keep, float& a, float& b) {
+          // (e^x - 1) / A times u: from |x| = 1/16 down dt u (1 + x/2 + x^2/6 + x^3/24), whose
+          // next term is 1.3e-7 of it; above, e^x - 1 keeps 1e-6
+          const float x = dt * A[j], ab = __builtin_amdgcn_exp2f(x * kLog2e);
+          const float ser = du * fmaf(x, fmaf(x, fmaf(x, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
+          const float gen = fmaf(ab, iA[j], -iA[j]) * u;
           keep = ab * cur.scale;
-          in = zoh_coeff_exact(dt, A[j], iA[j], ab) * (bc[r][0][n0 + j] * cur.u);
+          a = fabsf(x) < 0.0625f ? ser : gen;
+          b = bc[r][0][n0 + j];
         });
       }
-      const float amax = group_all<L>(st.amax, fmax2), bad = group_all<L>(st.bad ? 1.f : 0.f, fmax2);
       float y = group_all<L>(st.y, fadd2);
-      const RowScale rs = row_scale(amax, bad != 0.f);
+      const RowScale rs = row_scale_fast(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
       const int64_t b = b0 + r;
       const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows + d)) : 0;
       uint32_t w[4];
@@ -322,7 +352,7 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
         w[k] = pack_codes<SEEDED>(h4, rs, key, uint32_t(4 * l + k));
       }
       if (live) {
-        int8_t* const q = p.q + (cur.to * p.rows + d) * N + n0;
+        int8_t* const q = p.q + (to[r] * p.rows + d) * N + n0;
         if constexpr (LINES) {
           if (n0 < N) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
@@ -330,16 +360,15 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
           for (int k = 0; k < 4; ++k) store_codes<WORDS>(q + 4 * k, N - n0 - 4 * k, w[k]);
         }
         if (l == 0) {
-          p.scale[cur.to * p.rows + d] = rs.scale;
-          y = fmaf(skip, cur.u, y);
-          if (s.z) y *= silu(cur.z);
+          p.scale[to[r] * p.rows + d] = rs.scale;
+          y = fmaf(skip, u, y);
+          if (s.z) y *= silu(T::widen(cur.z));
           IO* const o = static_cast<IO*>(s.y) + b * s.y_sb + d;
           if constexpr (sizeof(IO) == 2) *o = bf16_rne(y);
           else *o = y;
         }
       }
     }
-    if (r + 1 < R) cur = next;
   }
 }
 
@@ -371,19 +400,22 @@ __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, Cache
     }
   }
   const int64_t seed = SEEDED ? *p.seed : 0;
-  struct Row {
+  struct Row {                                     // (as loaded: a conversion here would wait for it)
     uint32_t w[4];
-    float scale, x, z, dt, a;
+    float scale, a, skip;
+    uint16_t x, z, dt;
   };
   auto load = [&](int64_t row, Row& v) __attribute__((always_inline)) {
     v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
-    v.scale = v.x = v.z = v.dt = v.a = 0.f;
+    v.scale = v.a = v.skip = 0.f;
+    v.x = v.z = v.dt = 0;
     if (row >= p.rows) return;
     const int64_t head = row >> 6;
-    v.x = T::widen(static_cast<const uint16_t*>(s.x)[b * p.rows + row]);
-    v.dt = T::widen(static_cast<const uint16_t*>(s.delta)[b * s.H + head]);
+    v.x = static_cast<const uint16_t*>(s.x)[b * p.rows + row];
+    v.dt = static_cast<const uint16_t*>(s.delta)[b * s.H + head];
     v.a = s.A[head];
-    if (s.z) v.z = T::widen(static_cast<const uint16_t*>(s.z)[b * p.rows + row]);
+    if (s.z) v.z = static_cast<const uint16_t*>(s.z)[b * p.rows + row];
+    if (s.Dskip) v.skip = s.Dskip[row];
     if (from < 0) return;
     const int8_t* const q = p.q + (from * p.rows + row) * N + 16 * l;
     v.scale = p.scale[from * p.rows + row];
@@ -401,17 +433,17 @@ __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, Cache
     const int64_t row = row0 + int64_t(t) * RP;
     Row next;
     if (t + 1 < passes) load(row + RP, next);
-    const float ab = __builtin_amdgcn_exp2f(cur.dt * cur.a * kLog2e);
-    const float drive = ((s.euler || cur.a == 0.f) ? cur.dt : zoh_coeff_exact(cur.dt, cur.a, 1.f / cur.a, ab)) * cur.x;
+    const float x = T::widen(cur.x), dt = T::widen(cur.dt), ab = __builtin_amdgcn_exp2f(dt * cur.a * kLog2e);
+    const float drive = (s.euler ? dt : zoh_coeff_exact(dt, cur.a, reciprocal(cur.a), ab)) * x;
     const float keep = ab * cur.scale;
     LaneStates st;
-    advance(cur.w, C, st, [&](int j, float& k, float& in) {
+    advance(cur.w, C, st, [&](int j, float& k, float& a, float& c) {
       k = keep;
-      in = drive * B[j];
+      a = drive;
+      c = B[j];
     });
-    const float amax = group_all<L>(st.amax, fmax2), bad = group_all<L>(st.bad ? 1.f : 0.f, fmax2);
     float y = group_all<L>(st.y, fadd2);
-    const RowScale rs = row_scale(amax, bad != 0.f);
+    const RowScale rs = row_scale_fast(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
     const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows + row)) : 0;
     uint32_t w[4];
 #pragma unroll
@@ -429,8 +461,8 @@ __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, Cache
       }
       if (l == 0) {
         p.scale[to * p.rows + row] = rs.scale;
-        if (s.Dskip) y = fmaf(s.Dskip[row], cur.x, y);
-        if (s.z) y *= silu(cur.z);
+        y = fmaf(cur.skip, x, y);
+        if (s.z) y *= silu(T::widen(cur.z));
         static_cast<uint16_t*>(s.y)[b * p.rows + row] = bf16_rne(y);
       }
     }
@@ -458,10 +490,12 @@ hipError_t launch_step_t(const StepParams& s, const CacheParams& p, hipStream_t 
 
 template <typename IO, int L>
 hipError_t launch_step_l(const StepParams& s, const CacheParams& p, hipStream_t stream) {
-  const bool words = s.N % 4 == 0 && on(p.q, 4), lines = s.N % 16 == 0 && on(p.q, 16);
-  // several batch rows a workgroup once they still leave several workgroups a compute unit
+  const bool words = s.N % 4 == 0 && on(p.q, 4), lines = s.N % 16 == 0 && on(p.q, 16) && on(s.A, 16);
+  // two batch rows a workgroup (the channels' rates and their reciprocals then serve twice) once
+  // that leaves eight workgroups a compute unit; 512 rows x 2560 x 16: 25 us, one row at a time
+  // ONEROW, four (whose registers leave three wavefronts a SIMD) 32
   const bool many = (p.rows * L + 255) / 256 * s.batch >= 4096;
-  if (lines) return many ? launch_step_t<IO, L, true, true, 4>(s, p, stream) : launch_step_t<IO, L, true, true, 1>(s, p, stream);
+  if (lines) return many ? launch_step_t<IO, L, true, true, 2>(s, p, stream) : launch_step_t<IO, L, true, true, 1>(s, p, stream);
   if (words) return launch_step_t<IO, L, true, false, 1>(s, p, stream);
   return launch_step_t<IO, L, false, false, 1>(s, p, stream);
 }
@@ -470,8 +504,8 @@ template <int N>
 hipError_t launch_ssd_n(const SsdParams& s, const CacheParams& p, hipStream_t stream) {
   constexpr int RP = 256 / (N / 16);
   const int64_t groups = (p.rows + RP - 1) / RP;
-  int passes = 1;                                  // a power of two that leaves at least 1024 workgroups, at most 8
-  while (passes < 8 && groups * p.count >= 2048 * int64_t(passes)) passes *= 2;
+  int passes = 1;                                  // a power of two that leaves at least 1024 workgroups, at most 4
+  while (passes < 4 && groups * p.count >= 2048 * int64_t(passes)) passes *= 2;
   const dim3 grid(unsigned((p.rows + RP * passes - 1) / (RP * passes) * p.count));
   const bool lines = on(p.q, 16);
   if (lines) {

@@ -681,19 +681,31 @@ __global__ __launch_bounds__(1024) void gated_dlam_kernel(GatedParams p, int64_t
   }
 }
 
-template <typename IO>
-__global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p, float* state) {
+// One token: V channels a thread (4: whole vectors of every operand).
+template <typename IO, int V>
+__global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p, float* __restrict__ state) {
   using T = io_traits<IO>;
+  struct alignas(V * sizeof(IO)) Vec { IO v[V]; };
+  struct alignas(V * 4) Vec32 { float v[V]; };
+  const uint32_t per = uint32_t(p.D / V);                            // threads a batch row
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.batch * p.D) return;
-  const int64_t b = i / p.D, d = i % p.D;
-  float a, m;
-  gated_decay(-p.c * softplus_f32(p.lam[d]) * sigmoid_f32(T::widen(static_cast<const IO*>(p.r)[b * p.r_sb + d])), a, m);
-  const float v = sigmoid_f32(T::widen(static_cast<const IO*>(p.g)[b * p.g_sb + d])) *
-                  T::widen(static_cast<const IO*>(p.x)[b * p.x_sb + d]);
-  const float h = fmaf(a, state[i], m * v);
-  state[i] = h;
-  static_cast<IO*>(p.y)[b * p.y_sb + d] = narrow<IO>(h);
+  if (i >= p.batch * per) return;
+  const int64_t b = i / per, d = (i - b * per) * V;
+  const Vec x = *reinterpret_cast<const Vec*>(static_cast<const IO*>(p.x) + b * p.x_sb + d);
+  const Vec r = *reinterpret_cast<const Vec*>(static_cast<const IO*>(p.r) + b * p.r_sb + d);
+  const Vec g = *reinterpret_cast<const Vec*>(static_cast<const IO*>(p.g) + b * p.g_sb + d);
+  Vec32 h = *reinterpret_cast<const Vec32*>(state + b * p.D + d);
+  const Vec32 lam = *reinterpret_cast<const Vec32*>(p.lam + d);
+  Vec y;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float a, m;
+    gated_decay(-p.c * softplus_f32(lam.v[j]) * sigmoid_f32(T::widen(r.v[j])), a, m);
+    h.v[j] = fmaf(a, h.v[j], m * (sigmoid_f32(T::widen(g.v[j])) * T::widen(x.v[j])));
+    y.v[j] = narrow<IO>(h.v[j]);
+  }
+  *reinterpret_cast<Vec32*>(state + b * p.D + d) = h;
+  *reinterpret_cast<Vec*>(static_cast<IO*>(p.y) + b * p.y_sb + d) = y;
 }
 
 constexpr int kGatedWaves = 8;
@@ -766,10 +778,20 @@ hipError_t launch_gated_bwd(bool bf16, GatedParams p, int cus, hipStream_t strea
 }
 
 hipError_t launch_gated_step(bool bf16, const GatedParams& p, float* state, hipStream_t stream) {
-  const dim3 grid(blocks_for(p.batch * p.D, 256));
-  if (bf16) hipLaunchKernelGGL(gated_step_kernel<uint16_t>, grid, dim3(256), 0, stream, p, state);
-  else hipLaunchKernelGGL(gated_step_kernel<float>, grid, dim3(256), 0, stream, p, state);
-  return hipGetLastError();
+  const uintptr_t ptrs = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.r) | reinterpret_cast<uintptr_t>(p.g) |
+                         reinterpret_cast<uintptr_t>(p.y);
+  const uintptr_t floats = reinterpret_cast<uintptr_t>(state) | reinterpret_cast<uintptr_t>(p.lam);
+  const bool vec = (p.D | p.x_sb | p.r_sb | p.g_sb | p.y_sb) % 4 == 0 && ptrs % (bf16 ? 8 : 16) == 0 && floats % 16 == 0;
+  auto with = [&](auto io, auto v) {
+    constexpr int V = decltype(v)::value;
+    hipLaunchKernelGGL((gated_step_kernel<decltype(io), V>), dim3(blocks_for(p.batch * (p.D / V), 256)), dim3(256), 0, stream, p,
+                       state);
+    return hipGetLastError();
+  };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  if (bf16) return vec ? with(uint16_t{}, Four{}) : with(uint16_t{}, One{});
+  return vec ? with(float{}, Four{}) : with(float{}, One{});
 }
 
 }  // namespace selscan
