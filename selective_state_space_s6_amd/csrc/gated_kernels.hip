@@ -208,7 +208,7 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   static_assert(kLinkGroup <= NW, "a wavefront reads one link");
   __shared__ float4 maps[2][NW][kCh / 2];          // of the wavefronts' tokens
   __shared__ float4 links[2][kLinkGroup][kCh / 2];    // of the chunks before; [0] the state behind their group
-  __shared__ uint32_t tickets[2];
+  __shared__ uint32_t tickets[3];                  // by turns; [2] the first
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t ctiles = uint32_t((p.D + kCh - 1) / kCh), chains = uint32_t(p.batch) * ctiles;
   const uint32_t total = chains * uint32_t(p.n_chunks);
@@ -218,9 +218,9 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   uint32_t* const counter = reinterpret_cast<uint32_t*>(p.links);
   uint32_t now = blockIdx.x, next = total;         // the first chunk's ticket and the following one's
   if (p.links != nullptr) {
-    if (tid == 0) tickets[0] = atomicAdd(counter, 1u);
+    if (tid == 0) tickets[2] = atomicAdd(counter, 1u);
     __syncthreads();
-    now = __builtin_amdgcn_readfirstlane(tickets[0]);
+    now = __builtin_amdgcn_readfirstlane(tickets[2]);
     if (now >= total) return;
   }
 
@@ -414,66 +414,91 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
   constexpr int kLen = NW * S, es = int(sizeof(IO));
   static_assert(kLinkGroup <= NW && kLen % kTile == 0, "a wavefront reads one link; a chunk starts at a checkpoint");
-  __shared__ float4 maps[NW][kCh / 2];             // of the wavefronts' tokens, forward
-  __shared__ float2 backs[NW][kCh / 2];            // and backward (with the same A)
-  __shared__ float4 links[kLinkGroup][kCh / 2];    // of the chunks behind; [0] what their group receives
-  __shared__ float2 sums[NW][kCh / 2];
-  __shared__ uint32_t ticket;
+  __shared__ float4 maps[2][NW][kCh / 2];          // of the wavefronts' tokens, forward
+  __shared__ float2 backs[2][NW][kCh / 2];         // and backward (with the same A)
+  __shared__ float4 links[2][kLinkGroup][kCh / 2]; // of the chunks behind; [0] what their group receives
+  __shared__ float2 sums[2][NW][kCh / 2];
+  __shared__ uint32_t tickets[3];                  // by turns; [2] the first
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t ctiles = uint32_t((p.D + kCh - 1) / kCh), chains = uint32_t(p.batch) * ctiles;
   const uint32_t total = chains * uint32_t(p.n_chunks);
   const int D = int(p.D);
   uint32_t* const counter = reinterpret_cast<uint32_t*>(p.links);
-  uint32_t now = blockIdx.x, next = total;
+  uint32_t now = blockIdx.x, next = total;         // the first chunk's ticket and the following one's
   if (p.links != nullptr) {
-    if (tid == 0) ticket = atomicAdd(counter, 1u);
+    if (tid == 0) tickets[2] = atomicAdd(counter, 1u);
     __syncthreads();
-    now = __builtin_amdgcn_readfirstlane(ticket);
+    now = __builtin_amdgcn_readfirstlane(tickets[2]);
+    if (now >= total) return;
   }
-  while (now < total) {
-    // (formed anew in every turn: kept over all turns, the rows' offsets fill the scalar
+  struct Raw {
+    typename T::raw_t x[S], r[S], g[S], y[S];
+    uint32_t first;                                // lane i: token i starts a sequence
+    float k0, k1, h0, h1;                          // the channels' rates, the state entering the chunk
+  };
+  // the chunk of a ticket: the order-th from the end
+  auto chunk_back = [&](uint32_t ticket, uint32_t& order) __attribute__((always_inline)) {
+    Chunk k = chunk_of<kLen>(p, ticket, chains, ctiles);
+    order = k.chunk;
+    k.chunk = uint32_t(p.n_chunks) - 1 - order;
+    k.t0 = int64_t(k.chunk) * kLen;
+    k.rest = int(p.L - k.t0 < kLen ? p.L - k.t0 : kLen);
+    return k;
+  };
+  auto load = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
+    // (formed anew for every chunk: kept over all of them, the rows' offsets fill the scalar
     // registers and spill into vector ones)
     int s0 = wave * S;
     asm("" : "+s"(s0));
     const int xs = int(p.x_sl) * es, rs = int(p.r_sl) * es, gs = int(p.g_sl) * es, ys = int(p.y_sl) * es;
-    Chunk k = chunk_of<kLen>(p, now, chains, ctiles);
-    const Link link(p, k.chunk, k.chain, chains, lane);
-    k.chunk = uint32_t(p.n_chunks) - 1 - k.chunk;
-    k.t0 = int64_t(k.chunk) * kLen;
-    k.rest = int(p.L - k.t0 < kLen ? p.L - k.t0 : kLen);
     const int c = int(k.ct) * kCh + 2 * lane;
-    const bool ok0 = c < D, ok1 = c + 1 < D;
-    const uint32_t o0 = ok0 ? c * es : kNoChannel, o1 = ok1 ? (c + 1) * es : kNoChannel;
-    typename T::raw_t xr[S], rr[S], gr[S], yr[S];
-    uint32_t first = 0;                            // lane i: token i starts a sequence
+    const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+    w.first = 0;
     if constexpr (RESET) {
       const int t = s0 + lane;
-      if (lane < S && t < k.rest) first = p.reset[k.b * p.reset_sb + k.t0 + t];
+      if (lane < S && t < k.rest) w.first = p.reset[k.b * p.reset_sb + k.t0 + t];
     }
-    {
-      const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
-      const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
-      const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
-      const auto yp = chunk_rsrc(static_cast<const IO*>(p.dy) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
+    w.k0 = gated_rate(p, c);
+    w.k1 = gated_rate(p, c + 1);
+    w.h0 = w.h1 = 0.f;
+    const float* const q = p.ckpt + (k.b * p.ntiles + k.t0 / kTile) * p.D + c;
+    if (c < D) w.h0 = q[0];
+    if (c + 1 < D) w.h1 = q[1];
+    const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
+    const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
+    const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
+    const auto yp = chunk_rsrc(static_cast<const IO*>(p.dy) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
 #pragma unroll
-      for (int i = 0; i < S; ++i) {
-        rr[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
-        gr[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
-        xr[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
-        yr[i] = T::template load<VEC>(yp, o0, o1, (s0 + i) * ys);
-      }
+    for (int i = 0; i < S; ++i) {
+      w.r[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
+      w.g[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
+      w.x[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
+      w.y[i] = T::template load<VEC>(yp, o0, o1, (s0 + i) * ys);
     }
-    const float k0 = gated_rate(p, c), k1 = gated_rate(p, c + 1);
-    float h0 = 0.f, h1 = 0.f;                      // the state entering the chunk
-    {
-      const float* const q = p.ckpt + (k.b * p.ntiles + k.t0 / kTile) * p.D + c;
-      if (ok0) h0 = q[0];
-      if (ok1) h1 = q[1];
-    }
-    if (p.persistent && tid == 0) next = atomicAdd(counter, 1u);
+  };
 
+  uint32_t order;
+  Chunk k = chunk_back(now, order);
+  // Chunk k from `w`, the following one's inputs on their way into `wn`; false after the last.
+  auto step = [&](Raw& w, Raw& wn, const int par) __attribute__((always_inline)) -> bool {
+    const bool more = next < total;
+    uint32_t order_n;
+    const Chunk kn = chunk_back(more ? next : 0, order_n);
+    if (more) load(kn, wn);
+    uint32_t after = total;
+    if (more && tid == 0) after = atomicAdd(counter, 1u);
+    const Link link(p, order, k.chain, chains, lane);
+    const int c = int(k.ct) * kCh + 2 * lane, s0 = wave * S;
+    const bool ok0 = c < D, ok1 = c + 1 < D;
+    const uint32_t o0 = ok0 ? c * es : kNoChannel, o1 = ok1 ? (c + 1) * es : kNoChannel;
+    auto& xr = w.x;
+    auto& rr = w.r;
+    auto& gr = w.g;
+    auto& yr = w.y;
+    const float k0 = w.k0, k1 = w.k1;
+    float h0 = w.h0, h1 = w.h1;
     uint32_t cuts = 0;                             // bit i: token i starts a sequence
-    if constexpr (RESET) cuts = uint32_t(__ballot(first != 0));
+    if constexpr (RESET) cuts = uint32_t(__ballot(w.first != 0));
     float a0[S], a1[S], m0[S], m1[S], b0[S], b1[S];
     float A0 = 1.f, A1 = 1.f, H0 = 0.f, H1 = 0.f;
     const bool small = __all(k0 < kGatedSmall && k1 < kGatedSmall);
@@ -532,11 +557,11 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
         G1 = a1[i] * (G1 + T::hi(yr[i]));
       }
     }
-    maps[wave][lane] = make_float4(A0, A1, H0, H1);
-    backs[wave][lane] = make_float2(G0, G1);
-    if (tid == 0) ticket = next;
+    maps[par][wave][lane] = make_float4(A0, A1, H0, H1);
+    backs[par][wave][lane] = make_float2(G0, G1);
+    if (tid == 0) tickets[par] = after;
     __syncthreads();
-    next = __builtin_amdgcn_readfirstlane(ticket);
+    after = __builtin_amdgcn_readfirstlane(tickets[par]);
     if (wave == 0 && p.links != nullptr) {         // the chunk's map, before any wait
       float P0 = 1.f, P1 = 1.f, R0 = 0.f, R1 = 0.f;
       if (link.pos == 0 && p.dlast != nullptr) {   // the last chunk knows what it receives
@@ -545,8 +570,8 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
       }
 #pragma unroll 2
       for (int j = NW - 1; j >= 0; --j) {
-        const float4 m = maps[j][lane];
-        const float2 g = backs[j][lane];
+        const float4 m = maps[par][j][lane];
+        const float2 g = backs[par][j][lane];
         R0 = through<RESET>(m.x, g.x, R0);
         R1 = through<RESET>(m.y, g.y, R1);
         P0 = RESET && m.x == 0.f ? 0.f : P0 * m.x;
@@ -562,15 +587,15 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
           if (ok0) g0 = p.dlast[int64_t(k.b) * D + c];
           if (ok1) g1 = p.dlast[int64_t(k.b) * D + c + 1];
         }
-        links[0][lane] = make_float4(0.f, 0.f, g0, g1);
+        links[par][0][lane] = make_float4(0.f, 0.f, g0, g1);
       }
     } else {
-      link.read(wave, &links[wave][lane]);
+      link.read(wave, &links[par][wave][lane]);
     }
     // the states before this wavefront's tokens, while the links arrive
 #pragma unroll 2
     for (int j = 0; j < wave; ++j) {
-      const float4 m = maps[j][lane];
+      const float4 m = maps[par][j][lane];
       h0 = through<RESET>(m.x, m.z, h0);
       h1 = through<RESET>(m.y, m.w, h1);
     }
@@ -588,18 +613,18 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
       T::forget(gr[i]);
     }
     __syncthreads();
-    G0 = links[0][lane].z;
-    G1 = links[0][lane].w;
+    G0 = links[par][0][lane].z;
+    G1 = links[par][0][lane].w;
 #pragma unroll 2
     for (int j = 1; j <= link.in_group; ++j) {
-      const float4 m = links[j][lane];
+      const float4 m = links[par][j][lane];
       G0 = through<RESET>(m.x, m.z, G0);
       G1 = through<RESET>(m.y, m.w, G1);
     }
 #pragma unroll 2
     for (int j = NW - 1; j > wave; --j) {
-      const float4 m = maps[j][lane];
-      const float2 g = backs[j][lane];
+      const float4 m = maps[par][j][lane];
+      const float2 g = backs[par][j][lane];
       G0 = through<RESET>(m.x, g.x, G0);
       G1 = through<RESET>(m.y, g.y, G1);
     }
@@ -647,19 +672,33 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
         if (ok1) q[1] = G1;
       }
     }
-    sums[wave][lane] = make_float2(e0, e1);
+    sums[par][wave][lane] = make_float2(e0, e1);
     __syncthreads();
     if (wave == 0) {
 #pragma unroll
       for (int j = 1; j < NW; ++j) {
-        e0 += sums[j][lane].x;
-        e1 += sums[j][lane].y;
+        e0 += sums[par][j][lane].x;
+        e1 += sums[par][j][lane].y;
       }
       float* const q = p.plam + (int64_t(k.chunk) * p.batch + k.b) * p.D + c;
       if (ok0) q[0] = e0;
       if (ok1) q[1] = e1;
     }
-    now = next;
+    if (!more) return false;
+    k = kn;
+    order = order_n;
+    next = after;
+    return true;
+  };
+
+  Raw w0, w1;
+  load(k, w0);
+  if (p.persistent) {
+    if (tid == 0) tickets[1] = atomicAdd(counter, 1u);
+    __syncthreads();
+    next = __builtin_amdgcn_readfirstlane(tickets[1]);
+  }
+  while (step(w0, w1, 0) && step(w1, w0, 1)) {
   }
 }
 
