@@ -229,8 +229,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     uint32_t first;                                // lane i: token i starts a sequence
     float k0, k1;
   };
-  auto load = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
-    const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
+  // the gates of a chunk, and its x
+  auto load_gates = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
     const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
     const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
     const int c = int(k.ct) * kCh + 2 * lane;
@@ -246,8 +246,14 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     for (int i = 0; i < S; ++i) {
       w.r[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
       w.g[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
-      w.x[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
     }
+  };
+  auto load_x = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
+    const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
+    const int c = int(k.ct) * kCh + 2 * lane;
+    const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+#pragma unroll
+    for (int i = 0; i < S; ++i) w.x[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
   };
 
   Chunk k = chunk_of<kLen>(p, now, chains, ctiles);
@@ -255,7 +261,7 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   auto step = [&](Raw& w, Raw& wn, const int par) __attribute__((always_inline)) -> bool {
     const bool more = next < total;
     const Chunk kn = chunk_of<kLen>(p, more ? next : 0, chains, ctiles);
-    if (more) load(kn, wn);
+    if (more) load_gates(kn, wn);
     uint32_t after = total;
     if (more && tid == 0) after = atomicAdd(counter, 1u);
     float a0[S], a1[S], b0[S], b1[S];
@@ -336,6 +342,7 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
       link.publish(A0, A1, H0, H1);
     }
     link.read(wave, &links[par][wave][lane]);
+    if (more) load_x(kn, wn);
     __syncthreads();
     after = __builtin_amdgcn_readfirstlane(tickets[par]);
     float h0 = links[par][0][lane].z, h1 = links[par][0][lane].w;
@@ -385,7 +392,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   };
 
   Raw w0, w1;
-  load(k, w0);
+  load_gates(k, w0);
+  load_x(k, w0);
   if (p.persistent) {
     if (tid == 0) tickets[1] = atomicAdd(counter, 1u);
     __syncthreads();
@@ -445,12 +453,12 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     k.rest = int(p.L - k.t0 < kLen ? p.L - k.t0 : kLen);
     return k;
   };
-  auto load = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
-    // (formed anew for every chunk: kept over all of them, the rows' offsets fill the scalar
-    // registers and spill into vector ones)
+  // The gates of a chunk, and the rest of its inputs.  (The rows' offsets are formed anew for every
+  // chunk: kept over all of them, they fill the scalar registers and spill into vector ones.)
+  auto load_gates = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
     int s0 = wave * S;
     asm("" : "+s"(s0));
-    const int xs = int(p.x_sl) * es, rs = int(p.r_sl) * es, gs = int(p.g_sl) * es, ys = int(p.y_sl) * es;
+    const int rs = int(p.r_sl) * es, gs = int(p.g_sl) * es;
     const int c = int(k.ct) * kCh + 2 * lane;
     const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
     w.first = 0;
@@ -464,14 +472,24 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     const float* const q = p.ckpt + (k.b * p.ntiles + k.t0 / kTile) * p.D + c;
     if (c < D) w.h0 = q[0];
     if (c + 1 < D) w.h1 = q[1];
-    const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
     const auto rp = chunk_rsrc(static_cast<const IO*>(p.r) + k.b * p.r_sb + k.t0 * p.r_sl, k.rest, rs, D * es);
     const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
-    const auto yp = chunk_rsrc(static_cast<const IO*>(p.dy) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       w.r[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
       w.g[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
+    }
+  };
+  auto load_rest = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
+    int s0 = wave * S;
+    asm("" : "+s"(s0));
+    const int xs = int(p.x_sl) * es, ys = int(p.y_sl) * es;
+    const int c = int(k.ct) * kCh + 2 * lane;
+    const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+    const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
+    const auto yp = chunk_rsrc(static_cast<const IO*>(p.dy) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
       w.x[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
       w.y[i] = T::template load<VEC>(yp, o0, o1, (s0 + i) * ys);
     }
@@ -484,7 +502,7 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     const bool more = next < total;
     uint32_t order_n;
     const Chunk kn = chunk_back(more ? next : 0, order_n);
-    if (more) load(kn, wn);
+    if (more) load_gates(kn, wn);
     uint32_t after = total;
     if (more && tid == 0) after = atomicAdd(counter, 1u);
     const Link link(p, order, k.chain, chains, lane);
@@ -592,6 +610,7 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     } else {
       link.read(wave, &links[par][wave][lane]);
     }
+    if (more) load_rest(kn, wn);
     // the states before this wavefront's tokens, while the links arrive
 #pragma unroll 2
     for (int j = 0; j < wave; ++j) {
@@ -692,7 +711,8 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
   };
 
   Raw w0, w1;
-  load(k, w0);
+  load_gates(k, w0);
+  load_rest(k, w0);
   if (p.persistent) {
     if (tid == 0) tickets[1] = atomicAdd(counter, 1u);
     __syncthreads();
