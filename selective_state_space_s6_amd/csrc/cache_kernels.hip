@@ -1,7 +1,8 @@
 // cache_kernels.hip -- the 8-bit state cache: writing, reading, and the decode steps of the
 // selective scan and of the scalar-decay layer on cached states.  Every kernel is bound by the
 // bytes of the states, or close to it by the arithmetic on each of them, which therefore is
-// kept short: codes are rounded and packed in one instruction (v_cvt_pk_u8_f32, biased by 128), and a pair of values shares one 32-bit mix for its rounding.
+// kept short: codes are rounded and packed in one instruction (v_cvt_pk_u8_f32, biased by 128),
+// and a pair of values shares one 32-bit mix for its rounding.
 #include <type_traits>
 
 #include "device_common.h"
@@ -234,60 +235,49 @@ __device__ __forceinline__ float silu(float z) {
   return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
 }
 
-// One token of the selective scan.  L lanes a channel, 16 states a lane; a workgroup's channels
-// walk R batch rows, so that the channels' rates stay in registers; B and C of those rows are
-// staged in LDS.  WORDS: dstate % 4 == 0 and the codes on 4-byte boundaries; LINES: dstate % 16
-// == 0 and codes and rates on 16-byte boundaries (a lane whose states all lie behind the last
-// works on its channel's first rates and zero codes, and stores nothing).
-template <typename IO, int L, bool WORDS, bool LINES, bool SEEDED, int R>
+// One token of the selective scan.  L lanes a channel, 16 states a lane; B and C of the batch row
+// are staged in LDS.  WORDS: dstate % 4 == 0 and the codes on 4-byte boundaries; LINES: dstate %
+// 16 == 0 and codes and rates on 16-byte boundaries (a lane whose states all lie behind the last
+// works on its channel's first rates and zero codes, and stores nothing).  Per state some 30
+// vector instructions (decay, input coefficient, readout, rounding) stand against 2 bytes of
+// codes, so neither alone bounds it: 512 rows x 2560 x 16 in bf16 take 27 us (2.1 TB/s), some 18 of which
+// the instructions would fill and 10 the bytes.  Walking two batch rows with a channel's rates
+// kept in registers measured the same, four slower (three wavefronts a SIMD).
+template <typename IO, int L, bool WORDS, bool LINES, bool SEEDED>
 __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CacheParams p) {
   using T = io_traits<IO>;
   constexpr int kN = 16 * L;
-  __shared__ float bc[R][2][kN];
+  __shared__ float bc[2][kN];
   const int N = int(s.N), l = threadIdx.x % L;
   const uint32_t groups = uint32_t((p.rows * L + 255) / 256);       // workgroups a batch row
-  const int64_t d = int64_t(blockIdx.x % groups) * (256 / L) + threadIdx.x / L, b0 = int64_t(blockIdx.x / groups) * R;
+  const int64_t b = blockIdx.x / groups, d = int64_t(blockIdx.x % groups) * (256 / L) + threadIdx.x / L;
+  const int64_t to = slot_of(p.write_slots, b, p.slots), from = slot_of(p.read_slots, b, p.slots);
+  if (to < 0) return;                              // padding
   const bool live = d < p.rows;
   const int n0 = 16 * l;                           // this lane's first state
-  // everything is asked for before anything is waited for
-  int64_t from[R], to[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    to[r] = b0 + r < s.batch ? slot_of(p.write_slots, b0 + r, p.slots) : -1;
-    from[r] = to[r] >= 0 ? slot_of(p.read_slots, b0 + r, p.slots) : -1;
+  // everything is asked for before anything is waited for (and converted when it is used)
+  uint32_t w[4] = {0, 0, 0, 0};
+  float scale = 0.f;
+  IO u_raw = 0, dt_raw = 0, z_raw = 0;
+  if (live) {
+    u_raw = static_cast<const IO*>(s.u)[b * s.u_sb + d];
+    dt_raw = static_cast<const IO*>(s.delta)[b * s.delta_sb + d];
+    if (s.z) z_raw = static_cast<const IO*>(s.z)[b * s.z_sb + d];
   }
-  struct Row {                                     // (as loaded: a conversion here would wait for it)
-    uint32_t w[4];
-    float scale;
-    IO u, dt, z;
-  } rows[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    Row& v = rows[r];
-    const int64_t b = b0 + r;
-    v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
-    v.scale = 0.f;
-    v.u = v.dt = v.z = 0;
-    if (to[r] >= 0 && live) {
-      v.u = static_cast<const IO*>(s.u)[b * s.u_sb + d];
-      v.dt = static_cast<const IO*>(s.delta)[b * s.delta_sb + d];
-      if (s.z) v.z = static_cast<const IO*>(s.z)[b * s.z_sb + d];
-    }
-    if (from[r] >= 0 && live) {
-      const int8_t* const q = p.q + (from[r] * p.rows + d) * N + n0;
-      v.scale = p.scale[from[r] * p.rows + d];
-      if constexpr (LINES) {
-        if (n0 < N) {
-          const uint4 t = *reinterpret_cast<const uint4*>(q);
-          v.w[0] = t.x; v.w[1] = t.y; v.w[2] = t.z; v.w[3] = t.w;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v.w[k] = load_codes<WORDS>(q + 4 * k, N - n0 - 4 * k);
+  if (live && from >= 0) {
+    const int8_t* const q = p.q + (from * p.rows + d) * N + n0;
+    scale = p.scale[from * p.rows + d];
+    if constexpr (LINES) {
+      if (n0 < N) {
+        const uint4 t = *reinterpret_cast<const uint4*>(q);
+        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = load_codes<WORDS>(q + 4 * k, N - n0 - 4 * k);
     }
   }
-  float A[16], iA[16];
+  float A[16];
   if constexpr (LINES) {
     const float4* const q = reinterpret_cast<const float4*>(s.A + (live ? d * N + (n0 < N ? n0 : 0) : 0));
 #pragma unroll
@@ -300,75 +290,59 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
     for (int j = 0; j < 16; ++j) A[j] = live && n0 + j < N ? s.A[d * N + n0 + j] : -1.f;   // (any decay: no state)
   }
   const float skip = live && s.Dskip ? s.Dskip[d] : 0.f, bias = live && s.delta_bias ? s.delta_bias[d] : 0.f;
-  const int64_t seed = SEEDED ? *p.seed : 0;
-  for (int i = threadIdx.x; i < R * 2 * kN; i += 256) {
-    const int r = i / (2 * kN), c = i / kN % 2, n = i % kN;
-    const int64_t b = b0 + r;
+  const uint32_t key = SEEDED ? row_key(*p.seed, uint32_t(b * p.rows + d)) : 0;
+  if (threadIdx.x < 2 * kN) {
+    const int i = threadIdx.x / kN, n = threadIdx.x % kN;
     float v = 0.f;
-    if (n < N && b < s.batch)
-      v = T::widen(c == 0 ? static_cast<const IO*>(s.B)[b * s.B_sb + n] : static_cast<const IO*>(s.C)[b * s.C_sb + n]);
-    bc[r][c][n] = v;
+    if (n < N) v = T::widen(i == 0 ? static_cast<const IO*>(s.B)[b * s.B_sb + n] : static_cast<const IO*>(s.C)[b * s.C_sb + n]);
+    bc[i][n] = v;
   }
   __syncthreads();
+  const float u = T::widen(u_raw), x = T::widen(dt_raw) + bias, dt = s.softplus ? softplus_f32(x) : x, du = dt * u;
+  float C[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) iA[j] = reciprocal(A[j]);
+  for (int j = 0; j < 16; ++j) C[j] = bc[1][n0 + j];
+  LaneStates st;
+  if (s.euler) {
+    advance(w, C, st, [&](int j, float& keep, float& a, float& b) {
+      keep = __builtin_amdgcn_exp2f(dt * A[j] * kLog2e) * scale;
+      a = du;
+      b = bc[0][n0 + j];
+    });
+  } else {
+    advance(w, C, st, [&](int j, float& keep, float& a, float& b) {
+      // (e^x - 1) / A times u: from |x| = 1/16 down dt u (1 + x/2 + x^2/6 + x^3/24), whose next
+      // term is 1.3e-7 of it (and where A is zero dt u); above, e^x - 1 keeps 1e-6
+      const float x = dt * A[j], ab = __builtin_amdgcn_exp2f(x * kLog2e), iA = reciprocal(A[j]);
+      const float ser = du * fmaf(x, fmaf(x, fmaf(x, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
+      const float gen = fmaf(ab, iA, -iA) * u;
+      keep = ab * scale;
+      a = fabsf(x) < 0.0625f ? ser : gen;
+      b = bc[0][n0 + j];
+    });
+  }
+  float y = group_all<L>(st.y, fadd2);
+  const RowScale rs = row_scale_fast(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const Row& cur = rows[r];
-    if (to[r] >= 0) {                              // (the whole workgroup alike)
-      const float u = T::widen(cur.u), x = T::widen(cur.dt) + bias, dt = s.softplus ? softplus_f32(x) : x;
-      float C[16];
+  for (int k = 0; k < 4; ++k) {
+    const float h4[4] = {st.h[4 * k], st.h[4 * k + 1], st.h[4 * k + 2], st.h[4 * k + 3]};
+    w[k] = pack_codes<SEEDED>(h4, rs, key, uint32_t(4 * l + k));
+  }
+  if (!live) return;
+  int8_t* const q = p.q + (to * p.rows + d) * N + n0;
+  if constexpr (LINES) {
+    if (n0 < N) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) C[j] = bc[r][1][n0 + j];
-      LaneStates st;
-      if (s.euler) {
-        const float du = dt * u;
-        advance(cur.w, C, st, [&](int j, float& keep, float& a, float& b) {
-          keep = __builtin_amdgcn_exp2f(dt * A[j] * kLog2e) * cur.scale;
-          a = du;
-          b = bc[r][0][n0 + j];
-        });
-      } else {
-        const float du = dt * u;
-        advance(cur.w, C, st, [&](int j, float& keep, float& a, float& b) {
-          // (e^x - 1) / A times u: from |x| = 1/16 down dt u (1 + x/2 + x^2/6 + x^3/24), whose
-          // next term is 1.3e-7 of it; above, e^x - 1 keeps 1e-6
-          const float x = dt * A[j], ab = __builtin_amdgcn_exp2f(x * kLog2e);
-          const float ser = du * fmaf(x, fmaf(x, fmaf(x, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
-          const float gen = fmaf(ab, iA[j], -iA[j]) * u;
-          keep = ab * cur.scale;
-          a = fabsf(x) < 0.0625f ? ser : gen;
-          b = bc[r][0][n0 + j];
-        });
-      }
-      float y = group_all<L>(st.y, fadd2);
-      const RowScale rs = row_scale_fast(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
-      const int64_t b = b0 + r;
-      const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows + d)) : 0;
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float h4[4] = {st.h[4 * k], st.h[4 * k + 1], st.h[4 * k + 2], st.h[4 * k + 3]};
-        w[k] = pack_codes<SEEDED>(h4, rs, key, uint32_t(4 * l + k));
-      }
-      if (live) {
-        int8_t* const q = p.q + (to[r] * p.rows + d) * N + n0;
-        if constexpr (LINES) {
-          if (n0 < N) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) store_codes<WORDS>(q + 4 * k, N - n0 - 4 * k, w[k]);
-        }
-        if (l == 0) {
-          p.scale[to[r] * p.rows + d] = rs.scale;
-          y = fmaf(skip, u, y);
-          if (s.z) y *= silu(T::widen(cur.z));
-          IO* const o = static_cast<IO*>(s.y) + b * s.y_sb + d;
-          if constexpr (sizeof(IO) == 2) *o = bf16_rne(y);
-          else *o = y;
-        }
-      }
-    }
+    for (int k = 0; k < 4; ++k) store_codes<WORDS>(q + 4 * k, N - n0 - 4 * k, w[k]);
+  }
+  if (l == 0) {
+    p.scale[to * p.rows + d] = rs.scale;
+    y = fmaf(skip, u, y);
+    if (s.z) y *= silu(T::widen(z_raw));
+    IO* const o = static_cast<IO*>(s.y) + b * s.y_sb + d;
+    if constexpr (sizeof(IO) == 2) *o = bf16_rne(y);
+    else *o = y;
   }
 }
 
@@ -480,24 +454,20 @@ hipError_t launch_write_t(const float* state, const CacheParams& p, hipStream_t 
   return hipGetLastError();
 }
 
-template <typename IO, int L, bool WORDS, bool LINES, int R>
+template <typename IO, int L, bool WORDS, bool LINES>
 hipError_t launch_step_t(const StepParams& s, const CacheParams& p, hipStream_t stream) {
-  const dim3 grid(unsigned((p.rows * L + 255) / 256 * ((s.batch + R - 1) / R)));
-  if (p.seed) hipLaunchKernelGGL((step_cached_kernel<IO, L, WORDS, LINES, true, R>), grid, dim3(256), 0, stream, s, p);
-  else hipLaunchKernelGGL((step_cached_kernel<IO, L, WORDS, LINES, false, R>), grid, dim3(256), 0, stream, s, p);
+  const dim3 grid(unsigned((p.rows * L + 255) / 256 * s.batch));
+  if (p.seed) hipLaunchKernelGGL((step_cached_kernel<IO, L, WORDS, LINES, true>), grid, dim3(256), 0, stream, s, p);
+  else hipLaunchKernelGGL((step_cached_kernel<IO, L, WORDS, LINES, false>), grid, dim3(256), 0, stream, s, p);
   return hipGetLastError();
 }
 
 template <typename IO, int L>
 hipError_t launch_step_l(const StepParams& s, const CacheParams& p, hipStream_t stream) {
   const bool words = s.N % 4 == 0 && on(p.q, 4), lines = s.N % 16 == 0 && on(p.q, 16) && on(s.A, 16);
-  // two batch rows a workgroup (the channels' rates and their reciprocals then serve twice) once
-  // that leaves eight workgroups a compute unit; 512 rows x 2560 x 16: 25 us, one row at a time
-  // ONEROW, four (whose registers leave three wavefronts a SIMD) 32
-  const bool many = (p.rows * L + 255) / 256 * s.batch >= 4096;
-  if (lines) return many ? launch_step_t<IO, L, true, true, 2>(s, p, stream) : launch_step_t<IO, L, true, true, 1>(s, p, stream);
-  if (words) return launch_step_t<IO, L, true, false, 1>(s, p, stream);
-  return launch_step_t<IO, L, false, false, 1>(s, p, stream);
+  if (lines) return launch_step_t<IO, L, true, true>(s, p, stream);
+  if (words) return launch_step_t<IO, L, true, false>(s, p, stream);
+  return launch_step_t<IO, L, false, false>(s, p, stream);
 }
 
 template <int N>

@@ -404,10 +404,10 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
 }
 
 // What the chunks of one call share: the links, empty, and the channels' c softplus(lam).
-__global__ __launch_bounds__(256) void gated_begin_kernel(uint64_t* links, int64_t words, const float* lam, float c, float* kd,
+__global__ __launch_bounds__(256) void gated_begin_kernel(ulonglong2* links, int64_t pairs, const float* lam, float c, float* kd,
                                                           int64_t D) {
   const int64_t i0 = blockIdx.x * int64_t(256) + threadIdx.x, n = int64_t(gridDim.x) * 256;
-  for (int64_t i = i0; i < words; i += n) links[i] = 0;
+  for (int64_t i = i0; i < pairs; i += n) links[i] = make_ulonglong2(0, 0);
   for (int64_t i = i0; i < D; i += n) kd[i] = c * softplus_f32(lam[i]);
 }
 
@@ -782,10 +782,10 @@ static hipError_t launch_gated_begin(GatedParams& p, hipStream_t stream) {
     p.kd = nullptr;
     return hipSuccess;
   }
-  const int64_t words = gated_link_words(p.batch, p.D, p.n_chunks);
-  const int64_t blocks = ((words > p.D ? words : p.D) + 1023) / 1024;
-  hipLaunchKernelGGL(gated_begin_kernel, dim3(unsigned(blocks < 1024 ? blocks : 1024)), dim3(256), 0, stream, p.links, words,
-                     p.lam, p.c, p.kd, p.D);
+  const int64_t pairs = gated_link_words(p.batch, p.D, p.n_chunks) / 2;       // (an even number of words)
+  const int64_t blocks = ((pairs > p.D ? pairs : p.D) + 255) / 256;
+  hipLaunchKernelGGL(gated_begin_kernel, dim3(unsigned(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream,
+                     reinterpret_cast<ulonglong2*>(p.links), pairs, p.lam, p.c, p.kd, p.D);
   return hipGetLastError();
 }
 
