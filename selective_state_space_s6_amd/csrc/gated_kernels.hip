@@ -543,9 +543,10 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
             a0[i] = a1[i] = 0.f;
             m0[i] = m1[i] = 1.f;
           }
-          if (s0 + i >= k.rest) {                  // its inputs read as zero: the map that changes nothing
+          if (s0 + i >= k.rest) {                  // the map that changes nothing
             a0[i] = a1[i] = 1.f;
             m0[i] = m1[i] = 0.f;
+            xr[i] = yr[i] = typename T::raw_t{};   // (where rows overlap, theirs lie in range)
           }
         }
       }

@@ -163,6 +163,24 @@ def test_strided_inputs(io):
     check_backward(i, io, g)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [1, 63, 64, 65, 300, 130])
+def test_rows_shared_by_all_tokens(L, io):
+    """Inputs and dy expanded over the tokens (as the gradient of a sum is), the last tokens not
+    filling a tile: what the tokens behind it would read is not zero."""
+    import selective_state_space_s6_amd as ss
+    B, D = 2, 70
+    i = inputs(B, L, D, io=io, seed=L)
+    for k in ("x", "r", "g", "dy"):
+        i[k] = i[k][:, :1].repeat(L, 1)
+    v = {k: dev(i[k][:, :1], io).expand(B, L, D) for k in ("x", "r", "g", "dy")}
+    y, last = ss.gated_scan_fwd(v["x"], v["r"], v["g"], dev(i["lam"]), initial_state=dev(i["h0"]), return_last_state=True)
+    check_forward(i, io, (y, last, None))
+    g = ss.gated_scan_bwd(v["x"], v["r"], v["g"], dev(i["lam"]), dy=v["dy"], initial_state=dev(i["h0"]),
+                          dlast_state=dev(i["dlast"]))
+    check_backward(i, io, g)
+
+
 @pytest.mark.parametrize("lam", [-100.0, -30.0, -16.0, -14.0, -3.0, 0.0, 5.0, 30.0])
 @pytest.mark.parametrize("r", [-120.0, -20.0, 0.0, 20.0, 120.0])
 def test_extreme_gates(lam, r):
