@@ -287,7 +287,7 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) A[j] = live && n0 + j < N ? s.A[d * N + n0 + j] : -1.f;   // (any decay: no state)
+    for (int j = 0; j < 16; ++j) A[j] = live && n0 + j < N ? s.A[d * N + n0 + j] : 0.f;
   }
   const float skip = live && s.Dskip ? s.Dskip[d] : 0.f, bias = live && s.delta_bias ? s.delta_bias[d] : 0.f;
   const uint32_t key = SEEDED ? row_key(*p.seed, uint32_t(b * p.rows + d)) : 0;
@@ -299,6 +299,11 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
   }
   __syncthreads();
   const float u = T::widen(u_raw), x = T::widen(dt_raw) + bias, dt = s.softplus ? softplus_f32(x) : x, du = dt * u;
+  if constexpr (!LINES) {                          // no state: any rate that decays (a zero must stay one)
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (n0 + j >= N) A[j] = -copysignf(1.f, dt);
+  }
   float C[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) C[j] = bc[1][n0 + j];

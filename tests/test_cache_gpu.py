@@ -282,6 +282,28 @@ def test_not_finite_states_in_a_step():
     assert t.equal(~t.isfinite(y), bad) and t.equal(t.isnan(back).all(-1), bad) and t.equal(t.isnan(back).any(-1), bad)
 
 
+@pytest.mark.parametrize("N", [1, 3, 4, 12, 16, 20, 48])
+@pytest.mark.parametrize("euler", [False, True])
+def test_growing_states(N, euler):
+    """Positive exponents from steps and rates of either sign; steps of size 200, at which a rate of
+    one would overflow.  All states stay in range, whatever stands behind the last of them."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, D = 2, 9
+    rng = np.random.default_rng(N)
+    b = Beams(B, (D, N), N)
+    u, Bm, Cm = (rng.standard_normal(s).astype(np.float32) for s in ((B, D), (B, N), (B, N)))
+    delta = np.array([-200.0, 200.0], np.float32)[:, None].repeat(D, 1)
+    A = (rng.uniform(-0.01, 0.01, (D, N))).astype(np.float32)
+    y_ref, h_ref = orc.step(b.h.reshape(B, D, N), u, delta, A, Bm, Cm, euler=euler)
+    h_abs = orc.step(np.abs(b.h).reshape(B, D, N), np.abs(u), np.abs(delta), np.abs(A), np.abs(Bm), Cm, euler=euler)[1]
+    q, scale, y = dev(b.q), dev(b.scale), t.zeros(B, D, device="cuda")
+    ss.selective_scan_step_cached(dev(u), dev(delta), dev(A), dev(Bm), dev(Cm), None, None, y, q=q, scale=scale,
+                                  read_slots=dev(b.read), write_slots=dev(b.write),
+                                  discretization="euler" if euler else "zoh")
+    check_step(b, q, scale, y, np.zeros((B, D)), y_ref, h_ref, h_abs, "f32", None, "N %d" % N)
+
+
 def test_stochastic_rounding_lets_slow_decays_through():
     """200 tokens without input, decay 0.99 each, in 4096 rows.  Rounded to nearest, values under
     half the largest never move (each token's change is below half a code); with a seed the
