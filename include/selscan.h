@@ -423,7 +423,9 @@ void gated_scan_dims_init(selscan_gated_dims* dims, int io_dtype, int64_t batch,
  *                    before their sigmoids
  *   lam            : [dim] fp32
  *   reset          : bytes, one per token (see above), or NULL
- *   y              : output in dims->io_dtype
+ *   y              : output in dims->io_dtype; its rows must not overlap, those of one sequence or
+ *                    those of one token follow one another (else SELSCAN_ERR_UNSUPPORTED).  Rows
+ *                    of what is read may overlap (a stride of 0)
  *   initial_state, last_state : [batch][dim] fp32, or NULL (zero / not written).  They may be
  *                    one buffer.  A last_state is the state after the row's last token.
  *   checkpoints    : [batch][ceil(seqlen / SELSCAN_GATED_TILE)][dim] fp32 output, or NULL: the

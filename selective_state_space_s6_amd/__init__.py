@@ -655,14 +655,12 @@ def _gated_dims(on, x, r, g, lam, y, reset, c):
     import torch
     batch, L, D = x.shape
     for name, t in (("x", x), ("r", r), ("g", g), ("y", y)):
-        if t is not None:
-            on.check(name, t, x.dtype, x.shape, contiguous=False)
-            if D > 1 and t.stride(2) != 1:
-                raise ValueError("%s: the channel axis must be unit-stride" % name)
+        on.check(name, t, x.dtype, x.shape, contiguous=False)
+        if D > 1 and t.stride(2) != 1:
+            raise ValueError("%s: the channel axis must be unit-stride" % name)
     on.check("lam", lam, torch.float32, (D,))
-    ys = (L * D, D) if y is None else (y.stride(0), y.stride(1))
-    d = GatedDims(SELSCAN_ABI_VERSION, _io_code(x.dtype), batch, L, D, x.stride(0), x.stride(1), r.stride(0), r.stride(1),
-                  g.stride(0), g.stride(1), ys[0], ys[1], 0, c, 0)
+    strides = [n for t in (x, r, g, y) for n in (t.stride(0), t.stride(1) if L > 1 else D)]    # (one token: any stride)
+    d = GatedDims(SELSCAN_ABI_VERSION, _io_code(x.dtype), batch, L, D, *strides, 0, c, 0)
     if reset is not None:
         if reset.dtype not in (torch.bool, torch.uint8):
             raise TypeError("reset must be a bool or uint8 [batch, L] tensor")

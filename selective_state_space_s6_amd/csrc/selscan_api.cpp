@@ -989,9 +989,12 @@ static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan*
   return SELSCAN_OK;
 }
 
-// y rows must not overlap (every (b, l, d) is written exactly once); dy, which is read, may
+// y rows must not overlap (every (b, l, d) is written exactly once); dy, which is read, may.
+// Rows of one sequence follow one another, or (time-major) those of one token do.
 static bool gated_rows_apart(const selscan_gated_dims& d) {
-  return (d.seqlen <= 1 || d.y_sl >= d.dim) && (d.batch <= 1 || d.seqlen <= 0 || d.y_sb >= (d.seqlen - 1) * d.y_sl + d.dim);
+  if (d.seqlen <= 0 || d.batch <= 0) return true;
+  const bool rows = (d.seqlen == 1 || d.y_sl >= d.dim) && (d.batch == 1 || d.y_sb >= (d.seqlen - 1) * d.y_sl + d.dim);
+  return rows || (d.y_sb >= d.dim && d.y_sb <= d.y_sl && d.y_sl >= (d.batch - 1) * d.y_sb + d.dim);
 }
 
 static selscan::GatedParams gated_params(const void* x, const void* r, const void* g, const float* lam,

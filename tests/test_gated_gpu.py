@@ -181,6 +181,25 @@ def test_rows_shared_by_all_tokens(L, io):
     check_backward(i, io, g)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(3, 70, 10), (1, 65, 3), (4, 1, 6), (2, 300, 64)])
+def test_time_major(size, io):
+    """[L, batch, D] buffers seen as [batch, L, D]: inputs, y and dy; a single token whose axis has
+    any stride."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    i = inputs(*size, io=io, seed=11)
+    v = {k: dev(i[k].transpose(1, 0, 2).copy(), io).transpose(0, 1) for k in ("x", "r", "g", "dy")}
+    if size[1] == 1:
+        v = {k: a.as_strided(a.shape, (a.stride(0), (1 << 20) + 1, 1)) for k, a in v.items()}
+    y = t.zeros_like(v["x"].transpose(0, 1).contiguous()).transpose(0, 1)
+    got, last = ss.gated_scan_fwd(v["x"], v["r"], v["g"], dev(i["lam"]), y=y, initial_state=dev(i["h0"]), return_last_state=True)
+    check_forward(i, io, (got, last, None))
+    g = ss.gated_scan_bwd(v["x"], v["r"], v["g"], dev(i["lam"]), dy=v["dy"], initial_state=dev(i["h0"]),
+                          dlast_state=dev(i["dlast"]))
+    check_backward(i, io, g)
+
+
 @pytest.mark.parametrize("lam", [-100.0, -30.0, -16.0, -14.0, -3.0, 0.0, 5.0, 30.0])
 @pytest.mark.parametrize("r", [-120.0, -20.0, 0.0, 20.0, 120.0])
 def test_extreme_gates(lam, r):
