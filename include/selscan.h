@@ -452,7 +452,7 @@ size_t gated_scan_workspace_size(const selscan_gated_dims* dims);
  *   checkpoints    : the forward call's, or NULL (then they are formed again from the inputs)
  *   dx, dr, dg     : [batch][seqlen][dim] contiguous in dims->io_dtype
  *   dlam           : [dim] fp32
- *   dinitial_state : [batch][dim] fp32, or NULL
+ *   dinitial_state : [batch][dim] fp32, or NULL; it and dlast_state may be one buffer
  *   workspace      : gated_scan_bwd_workspace_size(dims, checkpoints != NULL) bytes, as above
  * All outputs are written, never accumulated into; sums run in a fixed order.  The gradient
  * through m stays finite as a tends to 1 (la/m tends to 0).

@@ -581,36 +581,32 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     if (tid == 0) tickets[par] = after;
     __syncthreads();
     after = __builtin_amdgcn_readfirstlane(tickets[par]);
-    if (wave == 0 && p.links != nullptr) {         // the chunk's map, before any wait
+    if (wave == 0) {
       float P0 = 1.f, P1 = 1.f, R0 = 0.f, R1 = 0.f;
-      if (link.pos == 0 && p.dlast != nullptr) {   // the last chunk knows what it receives
-        if (ok0) R0 = p.dlast[int64_t(k.b) * D + c];
-        if (ok1) R1 = p.dlast[int64_t(k.b) * D + c + 1];
-      }
-#pragma unroll 2
-      for (int j = NW - 1; j >= 0; --j) {
-        const float4 m = maps[par][j][lane];
-        const float2 g = backs[par][j][lane];
-        R0 = through<RESET>(m.x, g.x, R0);
-        R1 = through<RESET>(m.y, g.y, R1);
-        P0 = RESET && m.x == 0.f ? 0.f : P0 * m.x;
-        P1 = RESET && m.y == 0.f ? 0.f : P1 * m.y;
-      }
-      if (link.pos == 0) P0 = P1 = 0.f;
-      link.publish(P0, P1, R0, R1);
-    }
-    if (link.pos == 0) {
-      if (wave == 0) {
-        float g0 = 0.f, g1 = 0.f;
+      if (link.pos == 0) {
+        // The last chunk knows what it receives; nobody else reads dlast, and it is read before
+        // anything is published: it may lie where the first chunk writes dh0.
         if (p.dlast != nullptr) {
-          if (ok0) g0 = p.dlast[int64_t(k.b) * D + c];
-          if (ok1) g1 = p.dlast[int64_t(k.b) * D + c + 1];
+          if (ok0) R0 = p.dlast[int64_t(k.b) * D + c];
+          if (ok1) R1 = p.dlast[int64_t(k.b) * D + c + 1];
         }
-        links[par][0][lane] = make_float4(0.f, 0.f, g0, g1);
+        links[par][0][lane] = make_float4(0.f, 0.f, R0, R1);
       }
-    } else {
-      link.read(wave, &links[par][wave][lane]);
+      if (p.links != nullptr) {                    // the chunk's map, before any wait
+#pragma unroll 2
+        for (int j = NW - 1; j >= 0; --j) {
+          const float4 m = maps[par][j][lane];
+          const float2 g = backs[par][j][lane];
+          R0 = through<RESET>(m.x, g.x, R0);
+          R1 = through<RESET>(m.y, g.y, R1);
+          P0 = RESET && m.x == 0.f ? 0.f : P0 * m.x;
+          P1 = RESET && m.y == 0.f ? 0.f : P1 * m.y;
+        }
+        if (link.pos == 0) P0 = P1 = 0.f;
+        link.publish(P0, P1, R0, R1);
+      }
     }
+    if (link.pos != 0) link.read(wave, &links[par][wave][lane]);
     if (more) load_rest(kn, wn);
     // the states before this wavefront's tokens, while the links arrive
 #pragma unroll 2

@@ -247,7 +247,7 @@ struct GatedParams {
   int64_t ntiles;        // ceil(L / SELSCAN_GATED_TILE)
   float c;
   uint64_t* links;       // workspace: gated_link_words() words, or null (one chunk)
-  float* kd;             // workspace [D]: c softplus(lam)
+  float* kd;             // workspace [D]: c softplus(lam) (links)
   int32_t n_chunks;      // chunks of the pass: ceil(L / gated_chunk()), ceil(L / kGatedBwdChunk)
   int32_t persistent;    // workgroups take chunks by ticket (links)
   int32_t vec;           // 1: D and every stride even, pointers aligned to channel pairs

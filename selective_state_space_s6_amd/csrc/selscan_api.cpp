@@ -943,7 +943,7 @@ int selective_scan_ssd_fwd(const void* x, const void* delta, const float* A, con
 // ---- the gated linear recurrence
 struct GatedPlan {
   int64_t ntiles = 0, n_chunks = 0, bwd_chunks = 0;
-  size_t link_bytes = 0, fwd_bytes = 0;         // workspace of the forward pass: links between chunks, [D] floats
+  size_t link_bytes = 0, fwd_bytes = 0;         // workspace of the forward pass: links between chunks and [D] floats, none for one chunk
   size_t bwd_link_bytes = 0, off_kd = 0, off_ckpt = 0, off_plam = 0, bwd_bytes = 0;
 };
 
@@ -973,12 +973,12 @@ static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan*
     auto al = [](int64_t x) { return size_t(round_up(x, 256)); };
     const int64_t f = int64_t(sizeof(float));
     p.link_bytes = p.n_chunks > 1 ? al(8 * selscan::gated_link_words(d.batch, d.dim, p.n_chunks)) : 0;
-    p.fwd_bytes = p.link_bytes + al(f * d.dim);
+    p.fwd_bytes = p.link_bytes + (p.link_bytes > 0 ? al(f * d.dim) : 0);
     // backward: links (of a forward pass that forms the checkpoints, then of the backward one)
     p.bwd_link_bytes = p.bwd_chunks > 1 ? al(8 * selscan::gated_link_words(d.batch, d.dim, p.bwd_chunks)) : 0;
     size_t off = have_ckpt || p.bwd_link_bytes > p.link_bytes ? p.bwd_link_bytes : p.link_bytes;
     p.off_kd = off;
-    off += al(f * d.dim);
+    if (p.bwd_link_bytes > 0) off += al(f * d.dim);
     p.off_ckpt = off;
     if (!have_ckpt) off += al(f * d.batch * p.ntiles * d.dim);
     p.off_plam = off;

@@ -221,3 +221,9 @@ def test_the_binding_wants_gpu_tensors():
         ss.selective_scan_step_cached(x[0], x[0], torch.zeros(8, 16), x[0], x[0], q=q, scale=scale)
     with pytest.raises(ValueError):
         ss.selective_scan_ssd_step_cached(torch.zeros(1, 2, 64), x[0], x[0], x[0], x[0], q=q, scale=scale)
+
+
+def test_gated_workspace_of_one_chunk_is_empty():
+    for io, chunk in ((ss.SELSCAN_F32, 64), (ss.SELSCAN_BF16, 128)):
+        size = lambda n: ss.lib().gated_scan_workspace_size(ctypes.byref(gated(io, L=n, D=200)))       # noqa: E731
+        assert size(chunk) == 0 and size(chunk + 1) > 0

@@ -425,3 +425,32 @@ def test_offsets_past_32_bits():
     close(y[2:, tail][..., ch], y_ref, TOL["bf16"] + 2.0 ** -8, "y")
     got, slow = host(last[2:, ch]), np.array([0, 1])
     assert np.abs(got - l_ref).max() <= (1e-4 + 2.0 ** -8 * np.exp(-8 * 9000 * 0.4 * np.log1p(np.exp(-7)))) * np.abs(l_ref).max() + 1e-4
+
+
+@pytest.mark.parametrize("L", [1, 64, 200, 1500])
+def test_states_in_one_buffer(L):
+    """initial_state and last_state, dlast_state and dinitial_state share their memory (through the C
+    entry points: the Python ones allocate the gradients)."""
+    import ctypes
+
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, D = 3, 130
+    i = inputs(B, L, D, seed=L)
+    v = on_gpu(i, "f32")
+    lib, p = ss.lib(), lambda a: None if a is None else a.data_ptr()                    # noqa: E731
+    d = ss.GatedDims()
+    lib.gated_scan_dims_init(ctypes.byref(d), 0, B, L, D)
+    state, y, marks = v["h0"].clone(), t.empty_like(v["x"]), ss.gated_checkpoints(v["x"])
+    stream = t.cuda.current_stream().cuda_stream
+    assert lib.gated_scan_fwd(p(v["x"]), p(v["r"]), p(v["g"]), p(v["lam"]), None, p(y), p(state), p(state), p(marks),
+                              ctypes.byref(d), None, 0, stream) == 0
+    check_forward(i, "f32", (y, state, marks))
+    grad = v["dlast"].clone()
+    out = {k: t.empty_like(v["x"]) for k in ("dx", "dr", "dg")}
+    out["dlam"] = t.empty_like(v["lam"])
+    assert lib.gated_scan_bwd(p(v["x"]), p(v["r"]), p(v["g"]), p(v["lam"]), None, p(v["h0"]), p(marks), p(v["dy"]), p(grad),
+                              p(out["dx"]), p(out["dr"]), p(out["dg"]), p(out["dlam"]), p(grad), ctypes.byref(d), None, 0,
+                              stream) == 0
+    check_backward(i, "f32", dict(out, dinitial_state=grad))
+    t.cuda.synchronize()
