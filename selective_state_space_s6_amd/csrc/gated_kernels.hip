@@ -104,6 +104,14 @@ template <bool CUT> __device__ __forceinline__ float through(float A, float H, f
   return CUT && A == 0.f ? H : v;
 }
 
+// The product of decays.  With CUT it is zero behind a reset alone: one that merely leaves fp32 is
+// held at its least normal number, so an infinity does not end there.
+constexpr float kLeastDecay = 0x1p-126f;
+template <bool CUT> __device__ __forceinline__ float decays(float A, float a) {
+  if (CUT) return A == 0.f || a == 0.f ? 0.f : fmaxf(A * a, kLeastDecay);
+  return A * a;
+}
+
 // The links of one chunk, the pos-th of its chain (counted from the end in the backward pass).
 struct Link {
   uint64_t* map;                           // of this chunk and lane
@@ -309,6 +317,7 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     } else {
       run_map<S, false>(a0, b0, 0, A0, H0);
       run_map<S, false>(a1, b1, 0, A1, H1);
+      if (RESET) { A0 = fmaxf(A0, kLeastDecay); A1 = fmaxf(A1, kLeastDecay); }
     }
     const int c = int(k.ct) * kCh + 2 * lane;
     const bool ok0 = c < D, ok1 = c + 1 < D, last = int(k.chunk) == p.n_chunks - 1;
@@ -336,8 +345,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
         const float4 m = maps[par][j][lane];
         H0 = through<RESET>(m.x, m.z, H0);
         H1 = through<RESET>(m.y, m.w, H1);
-        A0 = RESET && m.x == 0.f ? 0.f : A0 * m.x;
-        A1 = RESET && m.y == 0.f ? 0.f : A1 * m.y;
+        A0 = decays<RESET>(A0, m.x);
+        A1 = decays<RESET>(A1, m.y);
       }
       link.publish(A0, A1, H0, H1);
     }
@@ -570,6 +579,7 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     } else {
       run_map<S, false>(a0, b0, 0, A0, H0);
       run_map<S, false>(a1, b1, 0, A1, H1);
+      if (RESET) { A0 = fmaxf(A0, kLeastDecay); A1 = fmaxf(A1, kLeastDecay); }
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
         G0 = a0[i] * (G0 + T::lo(yr[i]));
@@ -599,8 +609,8 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
           const float2 g = backs[par][j][lane];
           R0 = through<RESET>(m.x, g.x, R0);
           R1 = through<RESET>(m.y, g.y, R1);
-          P0 = RESET && m.x == 0.f ? 0.f : P0 * m.x;
-          P1 = RESET && m.y == 0.f ? 0.f : P1 * m.y;
+          P0 = decays<RESET>(P0, m.x);
+          P1 = decays<RESET>(P1, m.y);
         }
         if (link.pos == 0) P0 = P1 = 0.f;
         link.publish(P0, P1, R0, R1);

@@ -253,6 +253,31 @@ def test_not_finite_stays_in_its_channel_and_sequence():
     assert np.array_equal(np.flatnonzero(~np.isfinite(host(g["dlam"]))), [3, 10])
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("marks", [None, [0, 700]])
+def test_an_infinity_stays_through_strong_decays(marks, io):
+    """Every decay rounds to zero, none of them is zero: an infinite input leaves no finite state
+    behind it but by a reset, and no finite adjoint before an infinite gradient."""
+    B, L, D, at = 1, 900, 4, 200
+    i = inputs(B, L, D, io=io, seed=3)
+    i["lam"][:], i["r"][:] = 30.0, 20.0
+    i["x"][0, at, 1] = np.inf
+    i["dy"][0, at, 2] = -np.inf
+    if marks is not None:
+        i["reset"] = np.isin(np.arange(L), marks)[None]
+    y, last, ck = forward(i, io)
+    end = L if marks is None else marks[1]
+    bad = np.zeros((L, D), bool)
+    bad[at:end, 1] = True
+    assert np.array_equal(~np.isfinite(host(y)[0]), bad)
+    assert np.array_equal(~np.isfinite(host(last)[0]), bad[-1])
+    g = backward(i, io, marks=ck)
+    for k in ("dx", "dr", "dg"):                           # (a first token's decay gate has no gradient)
+        got = ~np.isfinite(host(g[k])[0])
+        assert got[int(k == "dr" and marks is not None):at + 1, 2].all() and not got[at + 1:, 2].any() and not got[:, [0, 3]].any(), k
+    assert np.array_equal(~np.isfinite(host(g["dinitial_state"])[0]), [False, False, marks is None, False])
+
+
 @pytest.mark.parametrize("cut", [1, 63, 128, 300])
 def test_continuing_from_a_state(cut):
     import selective_state_space_s6_amd as ss
