@@ -398,9 +398,9 @@ size_t selective_scan_ssd_workspace_size(const selscan_ssd_dims* dims);
 typedef struct selscan_gated_dims {
   int32_t abi_version;     /* SELSCAN_ABI_VERSION */
   int32_t io_dtype;        /* enum selscan_dtype: x, r, g, y (and dy, dx, dr, dg) */
-  int64_t batch;           /* >= 0 */
+  int64_t batch;           /* >= 0; batch * ceil(dim / 128) below 2^23 */
   int64_t seqlen;          /* >= 0 */
-  int64_t dim;             /* D >= 1 */
+  int64_t dim;             /* D >= 1, at most 2^20 */
   int64_t x_sb, x_sl;      /* strides in elements as in selscan_dims (unit stride over channels); */
   int64_t r_sb, r_sl;      /* token strides at most 2^20 */
   int64_t g_sb, g_sl;
@@ -508,7 +508,7 @@ typedef struct selscan_cache_dims {
  * the slots that slot_ids names (rows that name no slot are skipped).  seed: one int64 in device
  * memory, or NULL.  state_cache_read -- the values of `count` slots into out ([count][elems],
  * out_dtype an enum selscan_dtype; zeros for an id that names no slot).  In a read, ids may
- * repeat.  count * rows must be below 2^32 and count * ceil(elems / 256) below 2^31.  Neither
+ * repeat.  count * rows must be below 2^32 and count * ceil(elems / 256) below 2^24.  Neither
  * allocates.
  */
 int state_cache_write(const float* state, const int32_t* slot_ids, int64_t count, int8_t* q, float* scale,

@@ -963,6 +963,8 @@ static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan*
     return SELSCAN_ERR_UNSUPPORTED;
   const int64_t kMaxItems = (int64_t(1) << 31) - 1;
   if (d.batch > kMaxItems || d.seqlen > (int64_t(1) << 40)) return SELSCAN_ERR_UNSUPPORTED;
+  // workgroups of 512 threads (short sequences: one each), fewer than 2^32 threads a launch
+  if (d.batch * ((d.dim + 127) / 128) >= int64_t(1) << 23) return SELSCAN_ERR_UNSUPPORTED;
   GatedPlan p;
   p.ntiles = (d.seqlen + SELSCAN_GATED_TILE - 1) / SELSCAN_GATED_TILE;
   const int64_t chunk = selscan::gated_chunk(d.io_dtype == SELSCAN_BF16);
@@ -1179,8 +1181,8 @@ static int cache_check(const selscan_cache_dims* c, int64_t count, const int32_t
   if (c->row_len > 128 || c->elems > (int64_t(1) << 31) - 1 || c->slots > (int64_t(1) << 31) - 1)
     return SELSCAN_ERR_UNSUPPORTED;
   const int64_t rows = (c->elems + c->row_len - 1) / c->row_len;
-  // 32-bit row numbers, and workgroups of at least 256 values in one grid
-  if (count > ((int64_t(1) << 32) - 1) / rows || count > ((int64_t(1) << 31) - 1) / ((c->elems + 255) / 256))
+  // 32-bit row numbers, and one launch's fewer than 2^32 threads, each of at least one value
+  if (count > ((int64_t(1) << 32) - 1) / rows || count > ((int64_t(1) << 24) - 1) / ((c->elems + 255) / 256))
     return SELSCAN_ERR_UNSUPPORTED;
   if (!ids && count > c->slots) return SELSCAN_ERR_DIMS;                          // 0, 1, 2, ... must exist
   if (count > 0 && c->slots > 0 && (!q || !scale)) return SELSCAN_ERR_NULL;

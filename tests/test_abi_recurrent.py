@@ -227,3 +227,9 @@ def test_gated_workspace_of_one_chunk_is_empty():
     for io, chunk in ((ss.SELSCAN_F32, 64), (ss.SELSCAN_BF16, 128)):
         size = lambda n: ss.lib().gated_scan_workspace_size(ctypes.byref(gated(io, L=n, D=200)))       # noqa: E731
         assert size(chunk) == 0 and size(chunk + 1) > 0
+
+
+def test_one_launch_has_fewer_than_2_32_threads():
+    assert fwd(gated(batch=1 << 23)) == step(gated(batch=1 << 22, L=1, D=129)) == -3
+    c = cache(elems=1 << 20, row_len=64, slots=1 << 20)
+    assert cwrite(c, count=1 << 12) == cread(c, count=1 << 12) == -3
