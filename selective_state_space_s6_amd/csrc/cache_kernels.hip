@@ -120,8 +120,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
-// code j of four (one v_cvt_f32_i32 of a sign-extended byte)
-__device__ __forceinline__ float code_value(uint32_t w, int j) { return float(int8_t(w >> (8 * j))); }
+// Code j of four.  (Written out: the compiler takes the byte apart first, two instructions a code.)
+__device__ __forceinline__ float code_value(uint32_t w, int j) {
+  float v;
+  if (j == 0) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(v) : "v"(w));
+  else if (j == 1) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(v) : "v"(w));
+  else if (j == 2) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(v) : "v"(w));
+  else asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(v) : "v"(w));
+  return v;
+}
 
 // Writing: four values a lane, L lanes a row, whole lines in and out.
 template <int L, bool WORDS, bool SEEDED>
@@ -315,14 +322,16 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
       b = bc[0][n0 + j];
     });
   } else {
+    // (e^x - 1) / A u = dt u phi, phi = (e^x - 1) / x, x = dt A.  In y = x log2 e: from |y| = 1/12
+    // down ln2 phi is the series of phi to x^3 / 24, whose next term is 9e-8 of it; above it is
+    // (2^y - 1) / y, where the difference and v_rcp_f32 leave 1.3e-6.
+    constexpr float kLn2 = 0.693147181f;
+    const float lt = dt * kLog2e, dul = du * kLog2e;
     advance(w, C, st, [&](int j, float& keep, float& a, float& b) {
-      // (e^x - 1) / A times u: from |x| = 1/16 down dt u (1 + x/2 + x^2/6 + x^3/24), whose next
-      // term is 1.3e-7 of it (and where A is zero dt u); above, e^x - 1 keeps 1e-6
-      const float x = dt * A[j], ab = __builtin_amdgcn_exp2f(x * kLog2e), iA = reciprocal(A[j]);
-      const float ser = du * fmaf(x, fmaf(x, fmaf(x, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
-      const float gen = fmaf(ab, iA, -iA) * u;
+      const float y = lt * A[j], ab = __builtin_amdgcn_exp2f(y), iy = __builtin_amdgcn_rcpf(y);
+      const float ser = fmaf(y, fmaf(y, fmaf(y, kLn2 * kLn2 * kLn2 * kLn2 / 24.f, kLn2 * kLn2 * kLn2 / 6.f), kLn2 * kLn2 / 2.f), kLn2);
       keep = ab * scale;
-      a = fabsf(x) < 0.0625f ? ser : gen;
+      a = (fabsf(y) < 1.f / 12.f ? ser : fmaf(ab, iy, -iy)) * dul;
       b = bc[0][n0 + j];
     });
   }
