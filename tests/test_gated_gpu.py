@@ -479,3 +479,44 @@ def test_states_in_one_buffer(L):
                               stream) == 0
     check_backward(i, "f32", dict(out, dinitial_state=grad))
     t.cuda.synchronize()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 1, 2), (1, 65, 70), (2, 130, 3), (1, 300, 130)])
+def test_nothing_is_written_behind_the_last_row(size, io):
+    """200 rows behind y's sequences and behind each gradient keep what they held, and what lies
+    behind the inputs' last rows does not matter."""
+    import ctypes
+
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, L, D = size
+    i = inputs(B, L, D, io=io, seed=17)
+    dt = t.bfloat16 if io == "bf16" else t.float32
+    v = {k: t.full((B, L + 200, D), float("nan"), dtype=dt, device="cuda") for k in ("x", "r", "g", "dy")}
+    for k in v:
+        v[k][:, :L].copy_(dev(i[k], io))
+    buf = t.full((B, L + 200, D), 7.0, dtype=dt, device="cuda")
+    args = [v[k][:, :L] for k in ("x", "r", "g")]
+    marks = ss.gated_checkpoints(args[0])
+    y, last = ss.gated_scan_fwd(*args, dev(i["lam"]), y=buf[:, :L], initial_state=dev(i["h0"]), return_last_state=True,
+                                checkpoints=marks)
+    check_forward(i, io, (y, last, marks))
+    assert t.all(buf[:, L:] == 7)
+    p = lambda a: a.data_ptr()                                                          # noqa: E731
+    d = ss.GatedDims()
+    ss.lib().gated_scan_dims_init(ctypes.byref(d), ss.SELSCAN_BF16 if io == "bf16" else ss.SELSCAN_F32, B, L, D)
+    for k in ("x_sb", "r_sb", "g_sb", "y_sb"):
+        setattr(d, k, (L + 200) * D)
+    f = {k: dev(i[k]) for k in ("lam", "h0", "dlast")}
+    n = B * L * D
+    out = {k: t.full((n + 200 * D,), 7.0, dtype=dt, device="cuda") for k in ("dx", "dr", "dg")}
+    out.update(dlam=t.full((D + 200,), 7.0, device="cuda"), dinitial_state=t.full((B * D + 200,), 7.0, device="cuda"))
+    assert ss.lib().gated_scan_bwd(p(v["x"]), p(v["r"]), p(v["g"]), p(f["lam"]), None, p(f["h0"]), p(marks), p(v["dy"]),
+                                   p(f["dlast"]), *(p(a) for a in out.values()), ctypes.byref(d), None, 0,
+                                   t.cuda.current_stream().cuda_stream) == 0
+    t.cuda.synchronize()
+    shape = {"dlam": (D,), "dinitial_state": (B, D)}
+    g = {k: a[:int(np.prod(shape.get(k, size)))].view(shape.get(k, size)) for k, a in out.items()}
+    check_backward(i, io, g)
+    assert all(t.all(a[g[k].numel():] == 7) for k, a in out.items())
