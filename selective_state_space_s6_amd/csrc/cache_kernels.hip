@@ -360,22 +360,31 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
   }
 }
 
+// A view of n bytes from p on; loads behind its end give zero and stores there are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, int64_t n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, int(p != nullptr ? n : 0), 0x00020000);
+}
+
 // One token of the scalar-decay layer.  N / 16 lanes a row (head and channel), 16 states a
 // lane; a workgroup walks `passes` groups of rows of one batch row, whose B and C stay in
-// registers.
+// registers.  A group lies within one head.  All of a batch row is reached through views whose
+// ends stand for its bounds, at offsets of which only a scalar part changes from group to group.
 template <int N, bool LINES, bool SEEDED>
 __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, CacheParams p, int passes) {
   using T = io_traits<uint16_t>;
+  typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
   constexpr int L = N / 16, RP = 256 / L;
+  static_assert(64 % RP == 0, "a group of rows lies within one head");
   const int l = threadIdx.x % L;
   const uint32_t groups = uint32_t((p.rows + RP * passes - 1) / (RP * passes));     // workgroups a batch row
-  const int64_t b = blockIdx.x / groups, to = slot_of(p.write_slots, b, p.slots), from = slot_of(p.read_slots, b, p.slots);
+  const uint32_t b = __builtin_amdgcn_readfirstlane(blockIdx.x / groups);
+  const int64_t to = slot_of(p.write_slots, b, p.slots), from = slot_of(p.read_slots, b, p.slots);
   if (to < 0) return;                              // padding
-  const int64_t row0 = int64_t(blockIdx.x % groups) * passes * RP + threadIdx.x / L;
+  const uint32_t row0 = (blockIdx.x - b * groups) * uint32_t(passes) * RP;          // of the workgroup
   float B[16], C[16];
   {
-    const uint4* const bp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.B) + b * N + 16 * l);
-    const uint4* const cp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.C) + b * N + 16 * l);
+    const uint4* const bp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.B) + int64_t(b) * N + 16 * l);
+    const uint4* const cp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.C) + int64_t(b) * N + 16 * l);
     const uint4 b0 = bp[0], b1 = bp[1], c0 = cp[0], c1 = cp[1];
     const uint32_t bw[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
     const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
@@ -388,73 +397,80 @@ __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, Cache
     }
   }
   const int64_t seed = SEEDED ? *p.seed : 0;
+  const auto xv = view(static_cast<const uint16_t*>(s.x) + b * p.rows, p.rows * 2);
+  const auto zv = view(s.z ? static_cast<const uint16_t*>(s.z) + b * p.rows : nullptr, p.rows * 2);
+  const auto dv = view(static_cast<const uint16_t*>(s.delta) + b * s.H, s.H * 2);
+  const auto av = view(s.A, s.H * 4), kv = view(s.Dskip, p.rows * 4);
+  const auto qv = view(from >= 0 ? p.q + from * p.elems : nullptr, p.elems);
+  const auto sv = view(from >= 0 ? p.scale + from * p.rows : nullptr, p.rows * 4);
+  const auto yv = view(static_cast<uint16_t*>(s.y) + b * p.rows, p.rows * 2);
+  const auto qo = view(p.q + to * p.elems, p.elems), so = view(p.scale + to * p.rows, p.rows * 4);
+  const uint32_t own = threadIdx.x / L, codes = own * N + 16 * l;                   // in a group
+  const uint32_t first2 = l == 0 ? own * 2 : 0x80000000u, first4 = l == 0 ? own * 4 : 0x80000000u;
   struct Row {                                     // (as loaded: a conversion here would wait for it)
-    uint32_t w[4];
-    float scale, a, skip;
+    u32x4_t w;
+    uint32_t scale, a, skip;
     uint16_t x, z, dt;
   };
-  auto load = [&](int64_t row, Row& v) __attribute__((always_inline)) {
-    v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
-    v.scale = v.a = v.skip = 0.f;
-    v.x = v.z = v.dt = 0;
-    if (row >= p.rows) return;
-    const int64_t head = row >> 6;
-    v.x = static_cast<const uint16_t*>(s.x)[b * p.rows + row];
-    v.dt = static_cast<const uint16_t*>(s.delta)[b * s.H + head];
-    v.a = s.A[head];
-    if (s.z) v.z = static_cast<const uint16_t*>(s.z)[b * p.rows + row];
-    if (s.Dskip) v.skip = s.Dskip[row];
-    if (from < 0) return;
-    const int8_t* const q = p.q + (from * p.rows + row) * N + 16 * l;
-    v.scale = p.scale[from * p.rows + row];
+  auto load = [&](uint32_t row, Row& v) __attribute__((always_inline)) {
+    v.x = __builtin_amdgcn_raw_buffer_load_b16(xv, own * 2, row * 2, 0);
+    v.dt = __builtin_amdgcn_raw_buffer_load_b16(dv, 0, (row >> 6) * 2, 0);
+    v.a = __builtin_amdgcn_raw_buffer_load_b32(av, 0, (row >> 6) * 4, 0);
+    v.z = __builtin_amdgcn_raw_buffer_load_b16(zv, own * 2, row * 2, 0);
+    v.skip = __builtin_amdgcn_raw_buffer_load_b32(kv, own * 4, row * 4, 0);
+    v.scale = __builtin_amdgcn_raw_buffer_load_b32(sv, own * 4, row * 4, 0);
     if constexpr (LINES) {
-      const uint4 t = *reinterpret_cast<const uint4*>(q);
-      v.w[0] = t.x; v.w[1] = t.y; v.w[2] = t.z; v.w[3] = t.w;
+      v.w = __builtin_amdgcn_raw_buffer_load_b128(qv, codes, row * N, 0);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v.w[k] = load_codes<false>(q + 4 * k, 4);
+      for (int k = 0; k < 4; ++k) {
+        v.w[k] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v.w[k] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(qv, codes + 4 * k + j, row * N, 0)) << (8 * j);
+      }
     }
   };
-  Row cur;
-  load(row0, cur);
-  for (int t = 0; t < passes; ++t) {
-    const int64_t row = row0 + int64_t(t) * RP;
-    Row next;
-    if (t + 1 < passes) load(row + RP, next);
-    const float x = T::widen(cur.x), dt = T::widen(cur.dt), ab = __builtin_amdgcn_exp2f(dt * cur.a * kLog2e);
-    const float drive = (s.euler ? dt : zoh_coeff_exact(dt, cur.a, reciprocal(cur.a), ab)) * x;
-    const float keep = ab * cur.scale;
+  auto work = [&](uint32_t row, const Row& v) __attribute__((always_inline)) {
+    const float x = T::widen(v.x), dt = T::widen(v.dt), A = __uint_as_float(v.a);
+    const float ab = __builtin_amdgcn_exp2f(dt * A * kLog2e);
+    const float drive = (s.euler ? dt : zoh_coeff_exact(dt, A, reciprocal(A), ab)) * x;
+    const float keep = ab * __uint_as_float(v.scale);
+    uint32_t w[4] = {v.w[0], v.w[1], v.w[2], v.w[3]};
     LaneStates st;
-    advance(cur.w, C, st, [&](int j, float& k, float& a, float& c) {
+    advance(w, C, st, [&](int j, float& k, float& a, float& c) {
       k = keep;
       a = drive;
       c = B[j];
     });
     float y = group_all<L>(st.y, fadd2);
     const RowScale rs = row_scale_fast(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
-    const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows + row)) : 0;
-    uint32_t w[4];
+    const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows) + row + own) : 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float h4[4] = {st.h[4 * k], st.h[4 * k + 1], st.h[4 * k + 2], st.h[4 * k + 3]};
       w[k] = pack_codes<SEEDED>(h4, rs, key, uint32_t(4 * l + k));
     }
-    if (row < p.rows) {
-      int8_t* const q = p.q + (to * p.rows + row) * N + 16 * l;
-      if constexpr (LINES) {
-        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
+    if constexpr (LINES) {
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{w[0], w[1], w[2], w[3]}, qo, codes, row * N, 0);
+    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) store_codes<false>(q + 4 * k, 4, w[k]);
-      }
-      if (l == 0) {
-        p.scale[to * p.rows + row] = rs.scale;
-        y = fmaf(cur.skip, x, y);
-        if (s.z) y *= silu(T::widen(cur.z));
-        static_cast<uint16_t*>(s.y)[b * p.rows + row] = bf16_rne(y);
-      }
+      for (int k = 0; k < 16; ++k) __builtin_amdgcn_raw_buffer_store_b8(uint8_t(w[k / 4] >> (8 * (k % 4))), qo, codes + k, row * N, 0);
     }
-    cur = next;
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rs.scale), so, first4, row * 4, 0);
+    y = fmaf(__uint_as_float(v.skip), x, y);
+    if (s.z) y *= silu(T::widen(v.z));
+    __builtin_amdgcn_raw_buffer_store_b16(bf16_rne(y), yv, first2, row * 2, 0);
+  };
+  Row r0, r1;
+  load(row0, r0);
+  for (int t = 0;;) {                              // the next group's loads ahead of this one's work
+    if (t + 1 < passes) load(row0 + (t + 1) * RP, r1);
+    work(row0 + t * RP, r0);
+    if (++t == passes) break;
+    if (t + 1 < passes) load(row0 + (t + 1) * RP, r0);
+    work(row0 + t * RP, r1);
+    if (++t == passes) break;
   }
 }
 
