@@ -133,16 +133,15 @@ __device__ __forceinline__ float code_value(uint32_t w, int j) {
 // Writing: four values a lane, L lanes a row, whole lines in and out.
 template <int L, bool WORDS, bool SEEDED>
 __global__ __launch_bounds__(256) void cache_write_kernel(const float* __restrict__ state, CacheParams p) {
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / L;
-  const uint32_t quad = threadIdx.x % L;
-  const int64_t total = p.count * p.rows;
-  const int64_t row_id = i < total ? i : total - 1;
-  const int64_t b = row_id / p.rows, row = row_id - b * p.rows;
-  const int64_t slot = i < total ? slot_of(p.write_slots, b, p.slots) : -1;
-  const int64_t e0 = row * p.row_len;
-  const int64_t left = (e0 + p.row_len < p.elems ? p.row_len : p.elems - e0) - 4 * int64_t(quad);
-  const int n = slot < 0 || left < 0 ? 0 : left < 4 ? int(left) : 4;
-  const float* const src = state + b * p.elems + e0 + 4 * quad;
+  // (the calls of one launch have fewer than 2^32 rows, a state fewer than 2^31 values)
+  const uint32_t i = (blockIdx.x * 256u + threadIdx.x) / L, quad = threadIdx.x % L;
+  const uint32_t total = uint32_t(p.count * p.rows), rows = uint32_t(p.rows), len = uint32_t(p.row_len), elems = uint32_t(p.elems);
+  const uint32_t row_id = i < total ? i : total - 1;
+  const uint32_t b = row_id / rows, row = row_id - b * rows;
+  const uint32_t e0 = row * len;
+  const int left = int(e0 + len < elems ? len : elems - e0) - 4 * int(quad);
+  const int n = left < 0 ? 0 : left < 4 ? left : 4;
+  const float* const src = state + int64_t(b) * elems + e0 + 4 * quad;
   float h[4] = {0.f, 0.f, 0.f, 0.f};
   if (WORDS && n == 4) {
     const float4 v = *reinterpret_cast<const float4*>(src);
@@ -152,14 +151,16 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const float* __restric
     for (int j = 0; j < 4; ++j)
       if (j < n) h[j] = src[j];
   }
+  const int64_t slot = i < total ? slot_of(p.write_slots, b, p.slots) : -1;
   const float amax = group_all<L>(fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3]))), fmax2);
   const bool ok = finite(h[0]) && finite(h[1]) && finite(h[2]) && finite(h[3]);
   const float bad = group_all<L>(ok ? 0.f : 1.f, fmax2);
   const RowScale r = row_scale(amax, bad != 0.f);
-  const uint32_t key = SEEDED ? row_key(*p.seed, uint32_t(i)) : 0;
+  const uint32_t key = SEEDED ? row_key(*p.seed, i) : 0;
   const uint32_t w = pack_codes<SEEDED>(h, r, key, quad);
-  store_codes<WORDS>(p.q + (slot < 0 ? 0 : slot) * p.elems + e0 + 4 * quad, n, w);
-  if (quad == 0 && slot >= 0) p.scale[slot * p.rows + row] = r.scale;
+  if (slot < 0) return;
+  store_codes<WORDS>(p.q + slot * p.elems + e0 + 4 * quad, n, w);
+  if (quad == 0) p.scale[slot * p.rows + row] = r.scale;
 }
 
 // Reading: eight values a thread (VEC: row_len % 8 == 0 and everything aligned), else one.
