@@ -590,6 +590,20 @@ GATED_TILE = 64          # SELSCAN_GATED_TILE: tokens between two checkpoints
 CACHE_ROW = 64            # row length of a [D] state (the gated recurrence's) in the state cache
 
 
+_raw_stream = None
+
+
+def _current_stream(index):
+    """The handle of torch's current stream on GPU `index`, without a Stream object where torch has
+    that (1 us less a call)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
+
+
 class _On:
     """The GPU and the stream of one call: what is allocated inside belongs to that stream."""
     __slots__ = ("device", "index", "handle", "_guards")
@@ -601,7 +615,7 @@ class _On:
             raise ValueError("the tensors must be GPU tensors")
         self.device, self.index, self._guards = t.device, index, ()
         if stream is None:
-            self.handle = torch.cuda.current_stream(index).cuda_stream
+            self.handle = _current_stream(index)
         else:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=self.device)
@@ -654,13 +668,15 @@ def _gated_dims(on, x, r, g, lam, y, reset, c):
     """selscan_gated_dims of [batch, L, D] tensors; their channel axes are unit-stride."""
     import torch
     batch, L, D = x.shape
+    io, shape, strides = x.dtype, x.shape, []
     for name, t in (("x", x), ("r", r), ("g", g), ("y", y)):
-        on.check(name, t, x.dtype, x.shape, contiguous=False)
-        if D > 1 and t.stride(2) != 1:
+        on.check(name, t, io, shape, contiguous=False)
+        sb, sl, sd = t.stride()
+        if sd != 1 and D > 1:
             raise ValueError("%s: the channel axis must be unit-stride" % name)
+        strides += (sb, sl if L > 1 else D)                    # (one token: any stride)
     on.check("lam", lam, torch.float32, (D,))
-    strides = [n for t in (x, r, g, y) for n in (t.stride(0), t.stride(1) if L > 1 else D)]    # (one token: any stride)
-    d = GatedDims(SELSCAN_ABI_VERSION, _io_code(x.dtype), batch, L, D, *strides, 0, c, 0)
+    d = GatedDims(SELSCAN_ABI_VERSION, _io_code(io), batch, L, D, *strides, 0, c, 0)
     if reset is not None:
         if reset.dtype not in (torch.bool, torch.uint8):
             raise TypeError("reset must be a bool or uint8 [batch, L] tensor")
@@ -693,7 +709,7 @@ def gated_scan_fwd(x, r, g, lam, *, y=None, initial_state=None, last_state=None,
     with _On(x, stream) as on:
         batch, L, D = x.shape
         if y is None:
-            y = torch.empty((batch, L, D), dtype=x.dtype, device=x.device)
+            y = x.new_empty((batch, L, D))
         if last_state is None and return_last_state:
             last_state = torch.empty((batch, D), dtype=torch.float32, device=x.device)
         dims = _gated_dims(on, x, r, g, lam, y, reset, c)
@@ -747,17 +763,20 @@ def gated_scan_step(x, r, g, lam, *, state, y=None, c: float = 8.0, stream=None)
     with _On(x, stream) as on:
         batch, D = x.shape
         if y is None:
-            y = torch.empty((batch, D), dtype=x.dtype, device=x.device)
+            y = x.new_empty((batch, D))
         shape = x.shape
+        io, strides = x.dtype, []
         for name, t in (("x", x), ("r", r), ("g", g), ("y", y)):
-            on.check(name, t, x.dtype, shape, contiguous=False)
-            if D > 1 and t.stride(1) != 1:
+            on.check(name, t, io, shape, contiguous=False)
+            sb, sd = t.stride()
+            if sd != 1 and D > 1:
                 raise ValueError("%s: the channel axis must be unit-stride" % name)
+            strides += (sb, D)
         on.check("lam", lam, torch.float32, (D,))
-        dims = GatedDims(SELSCAN_ABI_VERSION, _io_code(x.dtype), batch, 1, D, x.stride(0), D, r.stride(0), D, g.stride(0), D,
-                         y.stride(0), D, 0, c, 0)
-        on.check("state", state, torch.float32, (batch, D))
-        st = lib().gated_scan_step(_p(x), _p(r), _p(g), _p(lam), _p(y), _p(state), ctypes.byref(dims), on.handle)
+        dims = GatedDims(SELSCAN_ABI_VERSION, _io_code(io), batch, 1, D, *strides, 0, c, 0)
+        on.check("state", state, torch.float32, shape)
+        st = lib().gated_scan_step(x.data_ptr(), r.data_ptr(), g.data_ptr(), lam.data_ptr(), y.data_ptr(), state.data_ptr(),
+                                   ctypes.byref(dims), on.handle)
         if st != SELSCAN_OK:
             raise SelscanError(st, "gated_scan_step")
     return y
@@ -813,12 +832,15 @@ def state_cache_read(q, scale, *, slots=None, out=None, dtype=None, stream=None)
     import torch
     with _On(q, stream) as on:
         dims = _cache_dims(on, q, scale, None)
-        shape = (q if slots is None else slots).shape[:1] + q.shape[1:]
-        on.check("slots", slots, torch.int32, shape[:1])
+        count, *rest = q.shape
+        if slots is not None:
+            count = slots.shape[0] if slots.dim() == 1 else -1
+            on.check("slots", slots, torch.int32, (count,))
         if out is None:
-            out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
-        on.check("out", out, dtype or out.dtype, shape)
-        st = lib().state_cache_read(_p(q), _p(scale), _p(slots), shape[0], _p(out), _io_code(out.dtype),
+            out = q.new_empty((count, *rest), dtype=dtype or torch.float32)
+        else:
+            on.check("out", out, dtype or out.dtype, (count, *rest))
+        st = lib().state_cache_read(q.data_ptr(), scale.data_ptr(), _p(slots), count, out.data_ptr(), _io_code(out.dtype),
                                     ctypes.byref(dims), on.handle)
         if st != SELSCAN_OK:
             raise SelscanError(st, "state_cache_read")
@@ -841,18 +863,23 @@ def selective_scan_step_cached(u, delta, A, B, C, Dskip=None, z=None, y=None, *,
         N = A.shape[-1]
         on.check("A", A, torch.float32, (D, N))
         if y is None:
-            y = torch.empty((batch, D), dtype=u.dtype, device=u.device)
-        io, per_channel = u.dtype, delta.dim() == 1
-        for name, t, shape in (("u", u, (batch, D)), ("delta", delta, (D,) if per_channel else (batch, D)), ("B", B, (batch, N)),
-                               ("C", C, (batch, N)), ("z", z, (batch, D)), ("y", y, (batch, D))):
+            y = u.new_empty((batch, D))
+        io, per_channel, sb = u.dtype, delta.dim() == 1, []
+        row, states = (batch, D), (batch, N)
+        for name, t, shape in (("u", u, row), ("delta", delta, (D,) if per_channel else row), ("z", z, row), ("y", y, row),
+                               ("B", B, states), ("C", C, states)):
             if t is None:
+                sb.append(0)
                 continue
             on.check(name, t, io, shape, contiguous=False)
-            if shape[-1] > 1 and t.stride(-1) != 1:
+            strides = t.stride()
+            if strides[-1] != 1 and shape[-1] > 1:
                 raise ValueError("%s must have a unit-stride last axis" % name)
-        d = SelscanDims(SELSCAN_ABI_VERSION, _io_code(io), batch, 1, D, N, u.stride(0), D,
-                        0 if per_channel else delta.stride(0), 0 if per_channel else D, 0 if z is None else z.stride(0), D,
-                        y.stride(0), D, B.stride(0), N, 0, C.stride(0), N, 0, 0, 0, DISCRETIZATIONS[discretization],
+            sb.append(strides[0])
+        if per_channel:
+            sb[1] = 0
+        d = SelscanDims(SELSCAN_ABI_VERSION, _io_code(io), batch, 1, D, N, sb[0], D, sb[1], 0 if per_channel else D, sb[2], D,
+                        sb[3], D, sb[4], N, 0, sb[5], N, 0, 0, 0, DISCRETIZATIONS[discretization],
                         1 if delta_softplus else 0)
         on.check("Dskip", Dskip, torch.float32, (D,))
         on.check("delta_bias", delta_bias, torch.float32, (D,))
@@ -882,7 +909,7 @@ def selective_scan_ssd_step_cached(x, delta, A, B, C, Dskip=None, z=None, y=None
         batch, H, P = x.shape
         N = B.shape[-1]
         if y is None:
-            y = torch.empty((batch, H, P), dtype=torch.bfloat16, device=x.device)
+            y = x.new_empty((batch, H, P))
         for name, t, shape in (("x", x, (batch, H, P)), ("delta", delta, (batch, H)), ("B", B, (batch, N)),
                                ("C", C, (batch, N)), ("z", z, (batch, H, P)), ("y", y, (batch, H, P))):
             on.check(name, t, torch.bfloat16, shape)
