@@ -40,11 +40,12 @@ struct RowScale {
 __device__ __forceinline__ RowScale row_scale(float amax, bool bad) {
   if (bad) return {__builtin_nanf(""), 0.f, true};
   if (!(amax >= kTinyRow)) return {0.f, 0.f, false};
-  return {amax / kCodes, 126.99998f / amax, false};
+  return {amax * (1.f / kCodes), 126.99998f / amax, false};     // (the scale to an ulp)
 }
 // The same within 2^-20, without a division: for states that a step has just formed.
 __device__ __forceinline__ RowScale row_scale_fast(float amax, bool bad) {
-  RowScale r{amax * (1.f / kCodes), 126.9999f * __builtin_amdgcn_rcpf(amax), bad};
+  // (v_rcp_f32 gives no subnormal number: amax / 128 keeps its result above)
+  RowScale r{amax * (1.f / kCodes), (126.9999f / 128.f) * __builtin_amdgcn_rcpf(amax * (1.f / 128.f)), bad};
   if (!(amax >= kTinyRow)) r.scale = r.inv = 0.f;
   if (bad) r.scale = __builtin_nanf("");
   return r;
@@ -96,6 +97,11 @@ template <int L, typename F> __device__ __forceinline__ float group_all(float v,
 __device__ __forceinline__ float fmax2(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ float fadd2(float a, float b) { return a + b; }
 
+// whether a lane of the row found one
+template <int L> __device__ __forceinline__ bool row_bad(bool bad) {
+  return __any(bad) ? group_all<L>(bad ? 1.f : 0.f, fmax2) != 0.f : false;
+}
+
 // Four codes of a row, n of them present, and back; WORDS: whole and on a 4-byte boundary.
 template <bool WORDS> __device__ __forceinline__ uint32_t load_codes(const int8_t* q, int n) {
   if constexpr (WORDS) return n > 0 ? *reinterpret_cast<const uint32_t*>(q) : 0u;
@@ -130,37 +136,36 @@ __device__ __forceinline__ float code_value(uint32_t w, int j) {
   return v;
 }
 
-// Writing: four values a lane, L lanes a row, whole lines in and out.
+// Writing: four values a lane, L lanes a row, whole lines in and out; a workgroup stays within one
+// state, so its slot and the division for it are scalar.
 template <int L, bool WORDS, bool SEEDED>
 __global__ __launch_bounds__(256) void cache_write_kernel(const float* __restrict__ state, CacheParams p) {
-  // (the calls of one launch have fewer than 2^32 rows, a state fewer than 2^31 values)
-  const uint32_t i = (blockIdx.x * 256u + threadIdx.x) / L, quad = threadIdx.x % L;
-  const uint32_t total = uint32_t(p.count * p.rows), rows = uint32_t(p.rows), len = uint32_t(p.row_len), elems = uint32_t(p.elems);
-  const uint32_t row_id = i < total ? i : total - 1;
-  const uint32_t b = row_id / rows, row = row_id - b * rows;
-  const uint32_t e0 = row * len;
-  const int left = int(e0 + len < elems ? len : elems - e0) - 4 * int(quad);
+  const uint32_t rows = uint32_t(p.rows), len = uint32_t(p.row_len), elems = uint32_t(p.elems);
+  const uint32_t per = (rows + 256 / L - 1) / (256 / L);            // workgroups a state
+  const uint32_t b = __builtin_amdgcn_readfirstlane(blockIdx.x / per);
+  const int64_t slot = slot_of(p.write_slots, b, p.slots);
+  if (slot < 0) return;                            // padding
+  const uint32_t row = (blockIdx.x - b * per) * (256 / L) + threadIdx.x / L, quad = threadIdx.x % L;
+  const uint32_t e0 = row * len + 4 * quad;        // (below 2^31 + 2^15)
+  const int left = row < rows ? int(row * len + len < elems ? row * len + len : elems) - int(e0) : 0;
   const int n = left < 0 ? 0 : left < 4 ? left : 4;
-  const float* const src = state + int64_t(b) * elems + e0 + 4 * quad;
+  const float* const src = state + int64_t(b) * elems;
   float h[4] = {0.f, 0.f, 0.f, 0.f};
   if (WORDS && n == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(src);
+    const float4 v = *reinterpret_cast<const float4*>(src + e0);
     h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (j < n) h[j] = src[j];
+      if (j < n) h[j] = src[e0 + j];
   }
-  const int64_t slot = i < total ? slot_of(p.write_slots, b, p.slots) : -1;
   const float amax = group_all<L>(fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3]))), fmax2);
   const bool ok = finite(h[0]) && finite(h[1]) && finite(h[2]) && finite(h[3]);
-  const float bad = group_all<L>(ok ? 0.f : 1.f, fmax2);
-  const RowScale r = row_scale(amax, bad != 0.f);
-  const uint32_t key = SEEDED ? row_key(*p.seed, i) : 0;
+  const RowScale r = row_scale(amax, row_bad<L>(!ok));
+  const uint32_t key = SEEDED ? row_key(*p.seed, b * rows + row) : 0;
   const uint32_t w = pack_codes<SEEDED>(h, r, key, quad);
-  if (slot < 0) return;
-  store_codes<WORDS>(p.q + slot * p.elems + e0 + 4 * quad, n, w);
-  if (quad == 0) p.scale[slot * p.rows + row] = r.scale;
+  store_codes<WORDS>(p.q + slot * elems + e0, n, w);
+  if (quad == 0 && row < rows) p.scale[slot * rows + row] = r.scale;
 }
 
 // Reading: eight values a thread (VEC: row_len % 8 == 0 and everything aligned), else one.
@@ -228,11 +233,6 @@ __device__ __forceinline__ void advance(const uint32_t (&w)[4], const float (&C)
     s.bad = !ok;
   }
 }
-// whether a lane of the row found one
-template <int L> __device__ __forceinline__ bool row_bad(bool bad) {
-  return __any(bad) ? group_all<L>(bad ? 1.f : 0.f, fmax2) != 0.f : false;
-}
-
 // 1 / a to half an ulp (v_rcp_f32 and a Newton step); 0 for 0
 __device__ __forceinline__ float reciprocal(float a) {
   const float r = __builtin_amdgcn_rcpf(a);
@@ -479,7 +479,7 @@ bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 
 template <int L, bool WORDS>
 hipError_t launch_write_t(const float* state, const CacheParams& p, hipStream_t stream) {
-  const dim3 grid(unsigned((p.count * p.rows * L + 255) / 256));
+  const dim3 grid(unsigned((p.rows + 256 / L - 1) / (256 / L) * p.count));
   if (p.seed) hipLaunchKernelGGL((cache_write_kernel<L, WORDS, true>), grid, dim3(256), 0, stream, state, p);
   else hipLaunchKernelGGL((cache_write_kernel<L, WORDS, false>), grid, dim3(256), 0, stream, state, p);
   return hipGetLastError();

@@ -304,6 +304,28 @@ def test_growing_states(N, euler):
     check_step(b, q, scale, y, np.zeros((B, D)), y_ref, h_ref, h_abs, "f32", None, "N %d" % N)
 
 
+def test_states_near_the_largest_number_are_kept():
+    """2^127 down to 2^-98 through a step that changes nothing (no input, rate zero)."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    D, N = 226, 4
+    h = (t.tensor([1.0, -0.5, 0.25, 0.75], device="cuda") * 2.0 ** t.arange(127.0, 127.0 - D, -1.0, device="cuda",
+                                                                            dtype=t.float64)[:, None]).float()[None]
+    q, scale = ss.state_cache(1, D, N)
+    ss.state_cache_write(h, q, scale)
+    zero, one = t.zeros(1, D, device="cuda"), t.ones(1, N, device="cuda")
+    for _ in range(2):
+        back = ss.state_cache_read(q, scale)
+        assert t.all((back.double() - h.double()).abs() <= scale.double()[..., None] * 0.51) and t.all(scale > 0)
+        ss.selective_scan_step_cached(zero, zero, t.zeros(D, N, device="cuda"), one, one, q=q, scale=scale)
+    q, scale = ss.state_cache(1, 64, 64, 64)
+    ss.state_cache_write((h[:, :64, :1, None] * t.ones(64, 64, device="cuda")).contiguous(), q, scale)
+    kept = ss.state_cache_read(q, scale)
+    bf = lambda *s: t.zeros(*s, dtype=t.bfloat16, device="cuda")                          # noqa: E731
+    ss.selective_scan_ssd_step_cached(bf(1, 64, 64), bf(1, 64), t.zeros(64, device="cuda"), bf(1, 64), bf(1, 64), q=q, scale=scale)
+    assert t.all((ss.state_cache_read(q, scale).double() - kept.double()).abs() <= kept.double().abs() * 2.0 ** -18)
+
+
 def test_stochastic_rounding_lets_slow_decays_through():
     """200 tokens without input, decay 0.99 each, in 4096 rows.  Rounded to nearest, values under
     half the largest never move (each token's change is below half a code); with a seed the
