@@ -1,6 +1,6 @@
 // cache_kernels.hip -- the 8-bit state cache: writing, reading, and the decode steps of the
-// selective scan and of the scalar-decay layer on cached states.  Every kernel is bound by the
-// bytes of the states, or close to it by the arithmetic on each of them, which therefore is
+// selective scan and of the scalar-decay layer on cached states.  Reading is bound by its bytes;
+// the others stand between their bytes and the arithmetic on each value, which therefore is
 // kept short: codes are rounded and packed in one instruction (v_cvt_pk_u8_f32, biased by 128),
 // and a pair of values shares one 32-bit mix for its rounding.
 #include <type_traits>
@@ -137,7 +137,10 @@ __device__ __forceinline__ float code_value(uint32_t w, int j) {
 }
 
 // Writing: four values a lane, L lanes a row, whole lines in and out; a workgroup stays within one
-// state, so its slot and the division for it are scalar.
+// state, so its slot and the division for it are scalar.  256 states of 2560 x 16 (55 MB): 11.4 us,
+// 4.8 TB/s (with a vector division for every lane's state 12.4, in 64 bits 14.1).  WORDS: rows of
+// whole fours, codes on 4-byte and states on 16-byte boundaries; 1024 states take 36.3 us, value
+// by value 48.6.
 template <int L, bool WORDS, bool SEEDED>
 __global__ __launch_bounds__(256) void cache_write_kernel(const float* __restrict__ state, CacheParams p) {
   const uint32_t rows = uint32_t(p.rows), len = uint32_t(p.row_len), elems = uint32_t(p.elems);
@@ -168,7 +171,9 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const float* __restric
   if (quad == 0 && row < rows) p.scale[slot * rows + row] = r.scale;
 }
 
-// Reading: eight values a thread (VEC: row_len % 8 == 0 and everything aligned), else one.
+// Reading: eight values a thread (VEC: row_len % 8 == 0 and everything aligned), else one.  64 states
+// of 80 heads x 64 x 128 into bf16 (127 MB): 18.5 us, 6.9 TB/s (partly from the last-level cache).
+// 1024 states of 2560 x 16: 22.2 us by eights, 80.8 one by one.
 template <typename OUT, bool VEC>
 __global__ __launch_bounds__(256) void cache_read_kernel(OUT* __restrict__ out, CacheParams p) {
   constexpr int W = VEC ? 8 : 1;
@@ -244,12 +249,13 @@ __device__ __forceinline__ float silu(float z) {
 }
 
 // One token of the selective scan.  L lanes a channel, 16 states a lane; B and C of the batch row
-// are staged in LDS.  WORDS: dstate % 4 == 0 and the codes on 4-byte boundaries; LINES: dstate %
-// 16 == 0 and codes and rates on 16-byte boundaries (a lane whose states all lie behind the last
-// works on its channel's first rates and zero codes, and stores nothing).  Per state some 30
-// vector instructions (decay, input coefficient, readout, rounding) stand against 2 bytes of
-// codes, so neither alone bounds it: 512 rows x 2560 x 16 in bf16 take 27 us (2.1 TB/s), some 18 of which
-// the instructions would fill and 10 the bytes.  Walking two batch rows with a channel's rates
+// are staged in LDS.  WORDS: dstate % 4 == 0, codes on 4-byte and rates on 16-byte boundaries; LINES:
+// dstate % 16 == 0, both on 16-byte boundaries (a lane whose states all lie behind the last works
+// on its channel's first rates and zero codes, and stores nothing).  1024 rows x 2560 x 16 in
+// bf16: 43.1 us with LINES, 49.8 with WORDS, 144 value by value.
+// Some 27 vector instructions a state (decay, input coefficient, readout, rounding; two of them at
+// a quarter of the rate) stand against 2 bytes of codes: 512 rows (63 MB) take 23.3 us, 16 of
+// which the instructions fill and 11 the bytes.  Walking two batch rows with a channel's rates
 // kept in registers measured the same, four slower (three wavefronts a SIMD).
 template <typename IO, int L, bool WORDS, bool LINES, bool SEEDED>
 __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CacheParams p) {
@@ -291,6 +297,13 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float4 v = q[k];
+      A[4 * k] = v.x; A[4 * k + 1] = v.y; A[4 * k + 2] = v.z; A[4 * k + 3] = v.w;
+    }
+  } else if constexpr (WORDS) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (live && n0 + 4 * k < N) v = *reinterpret_cast<const float4*>(s.A + d * N + n0 + 4 * k);
       A[4 * k] = v.x; A[4 * k + 1] = v.y; A[4 * k + 2] = v.z; A[4 * k + 3] = v.w;
     }
   } else {
@@ -370,6 +383,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, int64_t n)
 // lane; a workgroup walks `passes` groups of rows of one batch row, whose B and C stay in
 // registers.  A group lies within one head.  All of a batch row is reached through views whose
 // ends stand for its bounds, at offsets of which only a scalar part changes from group to group.
+// LINES: the codes on 16-byte boundaries (128 rows: 42.2 us), else byte by byte (150).
+// 64 rows x 80 heads x 64 x 128 (88 MB): 24.1 us, 17 of which the instructions fill (16 a state)
+// and 15 the bytes; with 64-bit addresses and branches at the bounds 26.2.
 template <int N, bool LINES, bool SEEDED>
 __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, CacheParams p, int passes) {
   using T = io_traits<uint16_t>;
@@ -495,7 +511,7 @@ hipError_t launch_step_t(const StepParams& s, const CacheParams& p, hipStream_t 
 
 template <typename IO, int L>
 hipError_t launch_step_l(const StepParams& s, const CacheParams& p, hipStream_t stream) {
-  const bool words = s.N % 4 == 0 && on(p.q, 4), lines = s.N % 16 == 0 && on(p.q, 16) && on(s.A, 16);
+  const bool words = s.N % 4 == 0 && on(p.q, 4) && on(s.A, 16), lines = s.N % 16 == 0 && on(p.q, 16) && on(s.A, 16);
   if (lines) return launch_step_t<IO, L, true, true>(s, p, stream);
   if (words) return launch_step_t<IO, L, true, false>(s, p, stream);
   return launch_step_t<IO, L, false, false>(s, p, stream);
@@ -505,7 +521,9 @@ template <int N>
 hipError_t launch_ssd_n(const SsdParams& s, const CacheParams& p, hipStream_t stream) {
   constexpr int RP = 256 / (N / 16);
   const int64_t groups = (p.rows + RP - 1) / RP;
-  int passes = 1;                                  // a power of two that leaves at least 1024 workgroups, at most 4
+  // A power of two that leaves at least 1024 workgroups, at most 4 (64 rows x 80 heads, with the
+  // read-back: 48.6 us with 1, 45.6 with 2, 45.0 with 4, 47.3 with 8).
+  int passes = 1;
   while (passes < 4 && groups * p.count >= 2048 * int64_t(passes)) passes *= 2;
   const dim3 grid(unsigned((p.rows + RP * passes - 1) / (RP * passes) * p.count));
   const bool lines = on(p.q, 16);

@@ -1,4 +1,9 @@
 // gated_kernels.hip -- the gated linear recurrence: forward, backward and decode step.
+//
+// A token is the map h -> a h + b with a = e^la, b = m sigmoid(g) x, and maps compose:
+// (A', H') after (A, H) is (A' A, A' H + H').  So a run of tokens is worked on by one wavefront in
+// registers, runs meet in LDS, and chunks of them in the workspace, without a second pass over
+// the inputs.  Composition always takes the same order, so results do not depend on timing.
 #include <type_traits>
 
 #include "gated_device.h"
@@ -79,15 +84,15 @@ template <> struct pair_io<uint16_t> {
 // until written, each word whole or absent, so a reader needs no other order between writes.
 //   map [items][2][64]: the chunk's map h -> A h + H as {A with its sign bit set, H} (A >= 0),
 //     the even channels before the odd ones;
-//   end [groups][2][64]: the state behind the chunk as {1, h}, by every kLinkGroup-th chunk.
+//   end [groups][2][64]: the state behind the chunk as {1, h}, by the last chunk of a group.
 __device__ __forceinline__ void put_word(uint64_t* p, uint32_t tag, float v) {
   __hip_atomic_store(p, (uint64_t(tag) << 32) | __float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ uint64_t get_word(const uint64_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// The wait ends (see the kernels' tickets).  It is bounded all the same; a word that never comes
-// reads as NaN.
+// The wait ends (see the kernels' tickets).  It is bounded all the same (some seconds); a word
+// that never comes reads as NaN.
 constexpr int kMaxPolls = 1 << 21;
 __device__ __forceinline__ uint64_t wait_word(const uint64_t* p, uint64_t first) {
   uint64_t w = first;
@@ -209,6 +214,17 @@ __device__ __forceinline__ void run_states(const float (&a)[S], float (&b)[S], u
 // The inputs are read once.  A workgroup takes chunk after chunk by ticket, the next one's
 // inputs in flight while it waits for the links of this one.  A chunk's predecessors have
 // lower tickets, so whoever holds them works on them or on still lower ones: every wait ends.
+//
+// Four tensors pass through HBM once: 4 x 16384 tokens x 2560 channels in bf16 are 1342 MB and take
+// 270 us, 5.0 TB/s where a large copy reaches 5.9.  Without the links (and so with wrong
+// states) it is 250, without the arithmetic 246: bytes, arithmetic (55 % of the vector
+// instructions' slots) and the exchange hide one another but for some 10 % each.  128 tokens
+// of bf16 a chunk, 64 of fp32, are what two chunks' raw inputs leave room for (64 of bf16:
+// twice the links, slower; two chunks ahead: spills, 314).  Workgroups of 64 channels and four
+// wavefronts, three a compute unit, took 294 against 281 here, and 32 against 25 in fp32.
+// One wavefront that reads all links for the others: 347.  VEC: channel pairs in one access
+// (even sizes and strides, aligned), else one by one: 2 x 16384 x 2560 in bf16 take 173 us and
+// 552, in fp32 299 and 416.
 template <typename IO, int NW, int S, bool VEC, bool RESET>
 __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
@@ -275,7 +291,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     float a0[S], a1[S], b0[S], b1[S];
     uint32_t cuts = 0;                             // bit i: token i starts a sequence
     if constexpr (RESET) cuts = uint32_t(__ballot(w.first != 0));
-    // |log a| is at most k: where that is small for the whole wavefront, no exp2 is needed.  (The
+    // |log a| is at most k: where that is small for the whole wavefront, no exp2 is needed (2 x
+    // 16384 x 2560 in bf16: 173 us so, 186 with both forms formed and one chosen).  (The
     // branch is taken four tokens at a time: around all of them, the compiler keeps every
     // gate's sigmoid in registers across it.)
     const bool small = __all(w.k0 < kGatedSmall && w.k1 < kGatedSmall);
@@ -412,7 +429,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   }
 }
 
-// What the chunks of one call share: the links, empty, and the channels' c softplus(lam).
+// What the chunks of one call share: the links, empty, and the channels' c softplus(lam).  A
+// kernel, not a memset: calls may be captured.  (11 MB of links take 6 us.)
 __global__ __launch_bounds__(256) void gated_begin_kernel(ulonglong2* links, int64_t pairs, const float* lam, float c, float* kd,
                                                           int64_t D) {
   const int64_t i0 = blockIdx.x * int64_t(256) + threadIdx.x, n = int64_t(gridDim.x) * 256;
@@ -426,6 +444,13 @@ __global__ __launch_bounds__(256) void gated_begin_kernel(ulonglong2* links, int
 // reversed sequence.  The states are formed again from the chunk's checkpoint.  The gates'
 // sigmoids are computed twice, before the exchange of maps (the decays stay in registers)
 // and after it: keeping them would halve the wavefronts that a compute unit holds.
+//
+// Seven tensors pass through HBM once: 4 x 4096 x 2560 in bf16 are 587 MB and take 184 us,
+// 3.2 TB/s.  The loads alone take 113 and the arithmetic fills 55 % of its slots: the
+// three phases of a chunk (map, wait, gradients) follow one another with one workgroup on a
+// compute unit, since the raw inputs of two chunks fill its registers.  Workgroups of half as
+// many channels, three a compute unit, took 183; in fp32 42 against 38.  VEC as above: 2 x 16384 x
+// 2560 in bf16 take 385 us and 961, in fp32 468 and 612.
 template <typename IO, int NW, int S, bool VEC, bool RESET>
 __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
@@ -729,7 +754,8 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
   }
 }
 
-// dlam: the sum of the parts [nparts][D] in a fixed order, times sigmoid(lam) / softplus(lam)
+// dlam: the sum of the parts [nparts][D] in a fixed order, times sigmoid(lam) / softplus(lam).
+// (256 parts of 2560 channels: 4.7 us, a launch and its latencies.)
 __global__ __launch_bounds__(1024) void gated_dlam_kernel(GatedParams p, int64_t nparts) {
   __shared__ float part[32][33];
   const int col = threadIdx.x & 31, row = threadIdx.x >> 5;
@@ -747,7 +773,9 @@ __global__ __launch_bounds__(1024) void gated_dlam_kernel(GatedParams p, int64_t
   }
 }
 
-// One token: V channels a thread (4: whole vectors of every operand).
+// One token: V channels a thread.  V = 4 where every operand can be moved in whole vectors (aligned,
+// sizes and strides a multiple of 4), else 1.  512 rows of 2560 channels in bf16 (21 MB): 6.1 us
+// (a call takes 8.5 on the host); 8192 rows: 52.0 us with 4, 69.4 with 1, in fp32 81.8 and 92.2.
 template <typename IO, int V>
 __global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p, float* __restrict__ state) {
   using T = io_traits<IO>;
