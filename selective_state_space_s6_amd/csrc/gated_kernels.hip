@@ -33,22 +33,32 @@ constexpr uint32_t kNoChannel = 0x80000000u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const void* p, int rows, int row_bytes, int cols_bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (rows - 1) * row_bytes + cols_bytes, 0x00020000);
 }
+// How a lane's two channels are moved.  kPairs: in one access, on any element's boundary (the
+// memory system takes those).  kOddPairs, where D is odd: the same, but the last channel is
+// loaded as the second one of the pair that ends there (`last` moves it into place) and stored
+// by itself, both behind a branch that only the last tile of channels takes; for every D that
+// branch costs 6 % (4 x 16384 x 2560 in bf16).  kSingle: one by one, for D = 1, which has no pair.
+// Forward and backward of 2 x 16384 x 2560 in bf16 take 172 and 385 us in pairs, 229 and 431
+// where these straddle words, 552 and 961 one by one; D = 2559: 197 and 450.
+enum { kSingle, kPairs, kOddPairs };
 template <typename IO> struct pair_io;
 template <> struct pair_io<float> {
   typedef uint32_t raw_t __attribute__((ext_vector_type(2)));
-  template <bool VEC> static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row) {
-    if constexpr (VEC) return __builtin_bit_cast(raw_t, __builtin_amdgcn_raw_buffer_load_b64(r, o0, row, 0));
+  template <int VEC> static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row) {
+    if constexpr (VEC != kSingle) return __builtin_bit_cast(raw_t, __builtin_amdgcn_raw_buffer_load_b64(r, o0, row, 0));
     else return raw_t{__builtin_amdgcn_raw_buffer_load_b32(r, o0, row, 0), __builtin_amdgcn_raw_buffer_load_b32(r, o1, row, 0)};
   }
   // the compiler no longer knows what v holds, so nothing formed from it before is kept for after
   static __device__ __forceinline__ void forget(raw_t& v) { asm("" : "+v"(v)); }
+  static __device__ __forceinline__ void last(raw_t& v, bool lane) { v.x = lane ? v.y : v.x; }
   static __device__ __forceinline__ float lo(raw_t v) { return __uint_as_float(v.x); }
   static __device__ __forceinline__ float hi(raw_t v) { return __uint_as_float(v.y); }
-  template <bool VEC>
-  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row, float a, float b) {
+  template <int VEC>
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row, float a, float b, bool odd) {
     const raw_t v = {__float_as_uint(a), __float_as_uint(b)};
-    if constexpr (VEC) {
+    if constexpr (VEC != kSingle) {
       __builtin_amdgcn_raw_buffer_store_b64(v, r, o0, row, 0);
+      if (VEC == kOddPairs && odd) __builtin_amdgcn_raw_buffer_store_b32(v.x, r, o1, row, 0);
     } else {
       __builtin_amdgcn_raw_buffer_store_b32(v.x, r, o0, row, 0);
       __builtin_amdgcn_raw_buffer_store_b32(v.y, r, o1, row, 0);
@@ -59,23 +69,42 @@ template <> struct pair_io<uint16_t> {
   using raw_t = uint32_t;
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  template <bool VEC> static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row) {
-    if constexpr (VEC) return __builtin_amdgcn_raw_buffer_load_b32(r, o0, row, 0);
+  template <int VEC> static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row) {
+    if constexpr (VEC != kSingle) return __builtin_amdgcn_raw_buffer_load_b32(r, o0, row, 0);
     else return uint32_t(__builtin_amdgcn_raw_buffer_load_b16(r, o0, row, 0)) |
                 (uint32_t(__builtin_amdgcn_raw_buffer_load_b16(r, o1, row, 0)) << 16);
   }
   static __device__ __forceinline__ void forget(raw_t& v) { asm("" : "+v"(v)); }
+  static __device__ __forceinline__ void last(raw_t& v, bool lane) { v = lane ? v >> 16 : v; }
   static __device__ __forceinline__ float lo(raw_t v) { return __uint_as_float(v << 16); }
   static __device__ __forceinline__ float hi(raw_t v) { return __uint_as_float(v & 0xffff0000u); }
-  template <bool VEC>
-  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row, float a, float b) {
+  template <int VEC>
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t o0, uint32_t o1, int row, float a, float b, bool odd) {
     const f32x2_t f = {a, b};                              // to nearest even
     const uint32_t v = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
-    if constexpr (VEC) {
+    if constexpr (VEC != kSingle) {
       __builtin_amdgcn_raw_buffer_store_b32(v, r, o0, row, 0);
+      if (VEC == kOddPairs && odd) __builtin_amdgcn_raw_buffer_store_b16(uint16_t(v), r, o1, row, 0);
     } else {
       __builtin_amdgcn_raw_buffer_store_b16(uint16_t(v), r, o0, row, 0);
       __builtin_amdgcn_raw_buffer_store_b16(uint16_t(v >> 16), r, o1, row, 0);
+    }
+  }
+};
+
+// The offsets of a lane's channels c, c + 1 in a row of D, for loads and for stores.
+template <int VEC> struct Columns {
+  uint32_t l0, l1, s0, s1;
+  bool odd, lane;                          // (kOddPairs) the last tile of channels, the last channel's lane
+  __device__ __forceinline__ Columns(int c, int D, int es, bool last_tile) {
+    odd = VEC == kOddPairs && last_tile;
+    lane = c + 1 == D;
+    l0 = s0 = c < D ? c * es : kNoChannel;
+    l1 = s1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+    if constexpr (VEC == kOddPairs) {
+      l0 = c + 1 < D ? c * es : c < D ? (c - 1) * es : kNoChannel;
+      s0 = c + 1 < D ? c * es : kNoChannel;
+      s1 = lane ? c * es : kNoChannel;
     }
   }
 };
@@ -222,10 +251,8 @@ __device__ __forceinline__ void run_states(const float (&a)[S], float (&b)[S], u
 // of bf16 a chunk, 64 of fp32, are what two chunks' raw inputs leave room for (64 of bf16:
 // twice the links, slower; two chunks ahead: spills, 314).  Workgroups of 64 channels and four
 // wavefronts, three a compute unit, took 294 against 281 here, and 32 against 25 in fp32.
-// One wavefront that reads all links for the others: 347.  VEC: channel pairs in one access
-// (even sizes and strides, aligned), else one by one: 2 x 16384 x 2560 in bf16 take 173 us and
-// 552, in fp32 299 and 416.
-template <typename IO, int NW, int S, bool VEC, bool RESET>
+// One wavefront that reads all links for the others: 347.
+template <typename IO, int NW, int S, int VEC, bool RESET>
 __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
   constexpr int kLen = NW * S;
@@ -265,19 +292,19 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     }
     w.k0 = gated_rate(p, c);
     w.k1 = gated_rate(p, c + 1);
-    const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+    const Columns<VEC> col(c, D, es, k.ct == ctiles - 1);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      w.r[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
-      w.g[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
+      w.r[i] = T::template load<VEC>(rp, col.l0, col.l1, (s0 + i) * rs);
+      w.g[i] = T::template load<VEC>(gp, col.l0, col.l1, (s0 + i) * gs);
     }
   };
   auto load_x = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
     const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
     const int c = int(k.ct) * kCh + 2 * lane;
-    const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+    const Columns<VEC> col(c, D, es, k.ct == ctiles - 1);
 #pragma unroll
-    for (int i = 0; i < S; ++i) w.x[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
+    for (int i = 0; i < S; ++i) w.x[i] = T::template load<VEC>(xp, col.l0, col.l1, (s0 + i) * xs);
   };
 
   Chunk k = chunk_of<kLen>(p, now, chains, ctiles);
@@ -288,6 +315,15 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     if (more) load_gates(kn, wn);
     uint32_t after = total;
     if (more && tid == 0) after = atomicAdd(counter, 1u);
+    const Columns<VEC> col(int(k.ct) * kCh + 2 * lane, D, es, k.ct == ctiles - 1);
+    if (VEC == kOddPairs && col.odd) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        T::last(w.x[i], col.lane);
+        T::last(w.r[i], col.lane);
+        T::last(w.g[i], col.lane);
+      }
+    }
     float a0[S], a1[S], b0[S], b1[S];
     uint32_t cuts = 0;                             // bit i: token i starts a sequence
     if constexpr (RESET) cuts = uint32_t(__ballot(w.first != 0));
@@ -388,7 +424,6 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
       if (ok1) o[1] = h1;
     }
     const auto yp = chunk_rsrc(static_cast<IO*>(p.y) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
-    const uint32_t o0 = ok0 ? c * es : kNoChannel, o1 = ok1 ? (c + 1) * es : kNoChannel;
     if (RESET && cuts != 0) {
       run_states<S, true>(a0, b0, cuts, h0);
       run_states<S, true>(a1, b1, cuts, h1);
@@ -400,7 +435,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const bool end = i == S - 1;               // b holds the state before each token
-        T::template store<VEC>(yp, o0, o1, (s0 + i) * ys, end ? h0 : b0[i + 1 < S ? i + 1 : i], end ? h1 : b1[i + 1 < S ? i + 1 : i]);
+        T::template store<VEC>(yp, col.s0, col.s1, (s0 + i) * ys, end ? h0 : b0[i + 1 < S ? i + 1 : i],
+                               end ? h1 : b1[i + 1 < S ? i + 1 : i], col.odd);
       }
     }
     if (wave == NW - 1) {                          // the state behind the chunk
@@ -449,9 +485,8 @@ __global__ __launch_bounds__(256) void gated_begin_kernel(ulonglong2* links, int
 // 3.2 TB/s.  The loads alone take 113 and the arithmetic fills 55 % of its slots: the
 // three phases of a chunk (map, wait, gradients) follow one another with one workgroup on a
 // compute unit, since the raw inputs of two chunks fill its registers.  Workgroups of half as
-// many channels, three a compute unit, took 183; in fp32 42 against 38.  VEC as above: 2 x 16384 x
-// 2560 in bf16 take 385 us and 961, in fp32 468 and 612.
-template <typename IO, int NW, int S, bool VEC, bool RESET>
+// many channels, three a compute unit, took 183; in fp32 42 against 38.
+template <typename IO, int NW, int S, int VEC, bool RESET>
 __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
   constexpr int kLen = NW * S, es = int(sizeof(IO));
@@ -494,7 +529,7 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     asm("" : "+s"(s0));
     const int rs = int(p.r_sl) * es, gs = int(p.g_sl) * es;
     const int c = int(k.ct) * kCh + 2 * lane;
-    const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+    const Columns<VEC> col(c, D, es, k.ct == ctiles - 1);
     w.first = 0;
     if constexpr (RESET) {
       const int t = s0 + lane;
@@ -510,22 +545,21 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     const auto gp = chunk_rsrc(static_cast<const IO*>(p.g) + k.b * p.g_sb + k.t0 * p.g_sl, k.rest, gs, D * es);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      w.r[i] = T::template load<VEC>(rp, o0, o1, (s0 + i) * rs);
-      w.g[i] = T::template load<VEC>(gp, o0, o1, (s0 + i) * gs);
+      w.r[i] = T::template load<VEC>(rp, col.l0, col.l1, (s0 + i) * rs);
+      w.g[i] = T::template load<VEC>(gp, col.l0, col.l1, (s0 + i) * gs);
     }
   };
   auto load_rest = [&](const Chunk& k, Raw& w) __attribute__((always_inline)) {
     int s0 = wave * S;
     asm("" : "+s"(s0));
     const int xs = int(p.x_sl) * es, ys = int(p.y_sl) * es;
-    const int c = int(k.ct) * kCh + 2 * lane;
-    const uint32_t o0 = c < D ? c * es : kNoChannel, o1 = c + 1 < D ? (c + 1) * es : kNoChannel;
+    const Columns<VEC> col(int(k.ct) * kCh + 2 * lane, D, es, k.ct == ctiles - 1);
     const auto xp = chunk_rsrc(static_cast<const IO*>(p.x) + k.b * p.x_sb + k.t0 * p.x_sl, k.rest, xs, D * es);
     const auto yp = chunk_rsrc(static_cast<const IO*>(p.dy) + k.b * p.y_sb + k.t0 * p.y_sl, k.rest, ys, D * es);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      w.x[i] = T::template load<VEC>(xp, o0, o1, (s0 + i) * xs);
-      w.y[i] = T::template load<VEC>(yp, o0, o1, (s0 + i) * ys);
+      w.x[i] = T::template load<VEC>(xp, col.l0, col.l1, (s0 + i) * xs);
+      w.y[i] = T::template load<VEC>(yp, col.l0, col.l1, (s0 + i) * ys);
     }
   };
 
@@ -542,11 +576,20 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     const Link link(p, order, k.chain, chains, lane);
     const int c = int(k.ct) * kCh + 2 * lane, s0 = wave * S;
     const bool ok0 = c < D, ok1 = c + 1 < D;
-    const uint32_t o0 = ok0 ? c * es : kNoChannel, o1 = ok1 ? (c + 1) * es : kNoChannel;
+    const Columns<VEC> col(c, D, es, k.ct == ctiles - 1);
     auto& xr = w.x;
     auto& rr = w.r;
     auto& gr = w.g;
     auto& yr = w.y;
+    if (VEC == kOddPairs && col.odd) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        T::last(xr[i], col.lane);
+        T::last(rr[i], col.lane);
+        T::last(gr[i], col.lane);
+        T::last(yr[i], col.lane);
+      }
+    }
     const float k0 = w.k0, k1 = w.k1;
     float h0 = w.h0, h1 = w.h1;
     uint32_t cuts = 0;                             // bit i: token i starts a sequence
@@ -709,9 +752,9 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
         token(T::lo(rr[i]), T::lo(gr[i]), T::lo(xr[i]), T::lo(yr[i]), k0, a0[i], m0[i], b0[i], cut, G0, e0, dx0, dr0, dg0);
         token(T::hi(rr[i]), T::hi(gr[i]), T::hi(xr[i]), T::hi(yr[i]), k1, a1[i], m1[i], b1[i], cut, G1, e1, dx1, dr1, dg1);
         if (s0 + i >= k.rest) e0 = e1 = 0.f;       // (nothing before it in this walk)
-        T::template store<VEC>(dxp, o0, o1, (s0 + i) * os, dx0, dx1);
-        T::template store<VEC>(drp, o0, o1, (s0 + i) * os, dr0, dr1);
-        T::template store<VEC>(dgp, o0, o1, (s0 + i) * os, dg0, dg1);
+        T::template store<VEC>(dxp, col.s0, col.s1, (s0 + i) * os, dx0, dx1, col.odd);
+        T::template store<VEC>(drp, col.s0, col.s1, (s0 + i) * os, dr0, dr1, col.odd);
+        T::template store<VEC>(dgp, col.s0, col.s1, (s0 + i) * os, dg0, dg1, col.odd);
         __builtin_amdgcn_sched_barrier(0);         // a token at a time: all at once take twice the registers
       }
     }
@@ -824,7 +867,7 @@ static hipError_t launch_gated_begin(GatedParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename IO, bool VEC, bool RESET>
+template <typename IO, int VEC, bool RESET>
 static hipError_t launch_gated_fwd_t(GatedParams p, int cus, hipStream_t stream) {
   const int64_t items = p.batch * ((p.D + kCh - 1) / kCh) * p.n_chunks;
   const int64_t resident = cus;                    // a workgroup of eight wavefronts fills a compute unit's registers
@@ -834,7 +877,7 @@ static hipError_t launch_gated_fwd_t(GatedParams p, int cus, hipStream_t stream)
   return hipGetLastError();
 }
 
-template <typename IO, bool VEC, bool RESET>
+template <typename IO, int VEC, bool RESET>
 static hipError_t launch_gated_bwd_t(GatedParams p, int cus, hipStream_t stream) {
   const int64_t items = p.batch * ((p.D + kCh - 1) / kCh) * p.n_chunks;
   const int64_t resident = cus;
@@ -851,7 +894,11 @@ template <typename F> static hipError_t by_type(bool bf16, const GatedParams& p,
   auto with = [&](auto io, auto vec) {
     return reset ? f(io, vec, std::true_type{}) : f(io, vec, std::false_type{});
   };
-  auto typed = [&](auto io) { return p.vec ? with(io, std::true_type{}) : with(io, std::false_type{}); };
+  auto typed = [&](auto io) {
+    if (p.D == 1) return with(io, std::integral_constant<int, kSingle>{});
+    if (p.D % 2 != 0) return with(io, std::integral_constant<int, kOddPairs>{});
+    return with(io, std::integral_constant<int, kPairs>{});
+  };
   return bf16 ? typed(uint16_t{}) : typed(float{});
 }
 

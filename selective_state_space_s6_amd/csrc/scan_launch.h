@@ -250,7 +250,6 @@ struct GatedParams {
   float* kd;             // workspace [D]: c softplus(lam) (links)
   int32_t n_chunks;      // chunks of the pass: ceil(L / gated_chunk()), ceil(L / kGatedBwdChunk)
   int32_t persistent;    // workgroups take chunks by ticket (links)
-  int32_t vec;           // 1: D and every stride even, pointers aligned to channel pairs
   float* plam;           // workspace [n_chunks][batch][D]: partial sums of dlam
 };
 // tokens of a workgroup: eight runs of as many as its registers hold twice over

@@ -1017,16 +1017,6 @@ static int compute_units_or_default(hipStream_t stream) {
   return n > 0 ? n : 256;
 }
 
-// Channel pairs can be moved whole: even sizes and strides, pointers on pairs.
-static bool gated_pairs(const selscan_gated_dims& d, std::initializer_list<const void*> ptrs) {
-  const size_t pair = d.io_dtype == SELSCAN_BF16 ? 4 : 8;
-  for (const void* q : ptrs)
-    if (q && !aligned(q, pair)) return false;
-  for (int64_t v : {d.dim, d.x_sb, d.x_sl, d.r_sb, d.r_sl, d.g_sb, d.g_sl, d.y_sb, d.y_sl})
-    if (v % 2 != 0) return false;
-  return true;
-}
-
 static bool all_aligned(std::initializer_list<const void*> ptrs, size_t a) {
   for (const void* q : ptrs)
     if (q && !aligned(q, a)) return false;
@@ -1089,7 +1079,6 @@ int gated_scan_fwd(const void* x, const void* r, const void* g, const float* lam
   p.y = y; p.h0 = initial_state; p.last = last_state; p.ckpt = checkpoints;
   p.links = pl.link_bytes > 0 ? static_cast<uint64_t*>(ws) : nullptr;
   p.kd = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.link_bytes);
-  p.vec = gated_pairs(d, {x, r, g, y});
   e = selscan::launch_gated_fwd(d.io_dtype == SELSCAN_BF16, p, compute_units_or_default(s), s);
   st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   if (workspace == nullptr && pl.fwd_bytes > 0) {
@@ -1137,14 +1126,12 @@ int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam
   if (checkpoints == nullptr) {
     p.ckpt = reinterpret_cast<float*>(ws + pl.off_ckpt);
     p.links = pl.link_bytes > 0 ? reinterpret_cast<uint64_t*>(ws) : nullptr;
-    p.vec = gated_pairs(d, {x, r, g});
     e = selscan::launch_gated_fwd(bf16, p, compute_units_or_default(s), s);
   }
   p.dy = dy; p.dlast = dlast_state; p.dx = dx; p.dr = dr; p.dg = dg; p.dlam = dlam; p.dh0 = dinitial_state;
   p.plam = reinterpret_cast<float*>(ws + pl.off_plam);
   p.links = pl.bwd_link_bytes > 0 ? reinterpret_cast<uint64_t*>(ws) : nullptr;
   p.n_chunks = int32_t(pl.bwd_chunks);
-  p.vec = gated_pairs(d, {x, r, g, dy, dx, dr, dg});
   if (e == hipSuccess) e = selscan::launch_gated_bwd(bf16, p, compute_units_or_default(s), s);
   st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   if (workspace == nullptr && pl.bwd_bytes > 0) {

@@ -164,6 +164,39 @@ def test_strided_inputs(io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [1, 2, 3, 127, 128, 129, 130, 257])
+@pytest.mark.parametrize("first,pad", [(1, 0), (0, 1), (1, 2), (3, 4)])
+def test_channel_pairs_on_any_boundary(D, first, pad, io):
+    """Rows that start at odd elements, with odd strides: every operand a block of a buffer whose
+    other elements are NaN (read) or kept (written)."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, L = 2, 70
+    i = inputs(B, L, D, io=io, seed=D + pad, reset="some")
+    n, W = B * L * (D + pad), D + pad
+
+    def block(fill):
+        flat = t.full((first + n + 5,), fill, dtype=t.bfloat16 if io == "bf16" else t.float32, device="cuda")
+        return flat, flat[first:first + n].view(B, L, W)[..., :D]
+
+    v = {}
+    for k in ("x", "r", "g", "dy"):
+        _, v[k] = block(float("nan"))
+        v[k].copy_(dev(i[k], io))
+    flat, y = block(7.0)
+    f = {k: dev(i[k]) for k in ("lam", "h0", "dlast", "reset")}
+    marks = ss.gated_checkpoints(v["x"])
+    _, last = ss.gated_scan_fwd(v["x"], v["r"], v["g"], f["lam"], y=y, reset=f["reset"], initial_state=f["h0"],
+                                return_last_state=True, checkpoints=marks)
+    check_forward(i, io, (y, last, marks))
+    y.fill_(7.0)
+    assert t.all(flat == 7)
+    g = ss.gated_scan_bwd(v["x"], v["r"], v["g"], f["lam"], dy=v["dy"], reset=f["reset"], initial_state=f["h0"],
+                          dlast_state=f["dlast"], checkpoints=marks)
+    check_backward(i, io, g)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("L", [1, 63, 64, 65, 300, 130])
 def test_rows_shared_by_all_tokens(L, io):
     """Inputs and dy expanded over the tokens (as the gradient of a sum is), the last tokens not
