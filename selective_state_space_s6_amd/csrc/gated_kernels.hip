@@ -26,7 +26,7 @@ constexpr int kCh = 128;                   // channels of a workgroup
 constexpr int kLinkGroup = 8;              // chunks between two chunks that publish their end state
 
 // Two channels of one token, through a buffer descriptor on the chunk: the row's offset in a
-// scalar register, the channels' in one (VEC) or two vector registers.  The descriptor ends
+// scalar register, the channels' in one (pairs) or two vector registers.  The descriptor ends
 // with the chunk's last row and kNoChannel lies behind any: loads out of range give zero and
 // stores are dropped, so neither the last tokens nor the last channels need a branch.
 constexpr uint32_t kNoChannel = 0x80000000u;
