@@ -484,6 +484,8 @@ int gated_scan_step(const void* x, const void* r, const void* g, const float* la
  * are a function of the seed, the row's place (batch row * rows + row) and the value's place in
  * the row: stochastic rounding, whose expectation is h.  A state that decays slowly needs it:
  * rounded to nearest, a change of less than half a code per token never takes place.
+ * The sum is formed to 2^-16: a value within 2^-16 of a code (of its scale) is stored as that
+ * code whatever u is, so a state that a token leaves as it was keeps its codes.
  * A row whose amax is below 2^-100 is stored as zeros; one that holds an infinity or a NaN is
  * stored with a NaN scale and stands for NaN throughout.
  * Rows of the layers: selective scan elems = dim * dstate, row_len = dstate; scalar-decay

@@ -1,8 +1,8 @@
 // cache_kernels.hip -- the 8-bit state cache: writing, reading, and the decode steps of the
 // selective scan and of the scalar-decay layer on cached states.  Reading is bound by its bytes;
 // the others stand between their bytes and the arithmetic on each value, which therefore is
-// kept short: codes are rounded and packed in one instruction (v_cvt_pk_u8_f32, biased by 128),
-// and a pair of values shares one 32-bit mix for its rounding.
+// kept short: a code is the integer part of a sum (seeded) or rounded and packed in one instruction
+// (v_cvt_pk_u8_f32), both biased by 128, and a pair of values shares one 32-bit mix for its rounding.
 #include <type_traits>
 
 #include "device_common.h"
@@ -35,42 +35,43 @@ struct RowScale {
   float scale, inv;
   bool bad;                               // an infinity or a NaN in the row: a NaN scale, zero codes
 };
-// The codes' factor is a hair under 127 / amax, so that -127 stays clear of the code below it
-// whatever is added for rounding; that is 1.2e-7 of a code's value.
+// The scale amax / 127 and the codes' factor 1 / scale, each within half an ulp (a Newton step after
+// the product with 1 / 127 and after v_rcp_f32): |h| inv stays below 127 (1 + 2^-23), 127 + 2^-16.
 __device__ __forceinline__ RowScale row_scale(float amax, bool bad) {
-  if (bad) return {__builtin_nanf(""), 0.f, true};
-  if (!(amax >= kTinyRow)) return {0.f, 0.f, false};
-  return {amax * (1.f / kCodes), 126.99998f / amax, false};     // (the scale to an ulp)
-}
-// The same within 2^-20, without a division: for states that a step has just formed.
-__device__ __forceinline__ RowScale row_scale_fast(float amax, bool bad) {
-  // (v_rcp_f32 gives no subnormal number: amax / 128 keeps its result above)
-  RowScale r{amax * (1.f / kCodes), (126.9999f / 128.f) * __builtin_amdgcn_rcpf(amax * (1.f / 128.f)), bad};
+  constexpr float kOne127 = 1.f / kCodes;
+  const float s0 = amax * kOne127, s = fmaf(fmaf(-kCodes, s0, amax), kOne127, s0);
+  const float r0 = __builtin_amdgcn_rcpf(s);
+  RowScale r{s, fmaf(fmaf(-s, r0, 1.f), r0, r0), bad};
   if (!(amax >= kTinyRow)) r.scale = r.inv = 0.f;
   if (bad) r.scale = __builtin_nanf("");
   return r;
 }
-// Four codes of values 4 quad .. 4 quad + 3 of a row.  v_cvt_pk_u8_f32 rounds to nearest, ties
-// to even: floor(t + u) is the rounding of t + u - 1/2, u = (k + 1/2) / 65536, formed as 128 +
-// k / 65536 by putting k behind the bits of 128.f (the sum's own rounding to 2^-16 stands for
-// the half); without a seed, u = 1/2 and 2^-16 more sends ties up.
+// Four codes of values 4 quad .. 4 quad + 3 of a row.
+// Seeded: floor(t + u), t = h inv, u = (k + 1/2) / 65536, from the sum t + 384 + j / 32768, j = k / 2
+// rounded down.  It lies in (256, 512), where numbers are 2^-15 apart, so its bits 15 to 22 are the
+// floor + 128, and t's rounding to 2^-15 stands for the rest of u.  A t within 2^-16 of a code is
+// that code's whatever k is: a state that a token leaves as it was, c scale, is off by half an ulp
+// like inv, 127 2^-23 < 2^-16 together, and keeps c.  (With 128 in place of 384 and a rounding
+// conversion, one in 2^16 of the odd codes fell by one a token, and 127 cannot rise again.)
+// To nearest: v_cvt_pk_u8_f32 rounds ties to even, 2^-16 more sends them up.
 template <bool SEEDED>
 __device__ __forceinline__ uint32_t pack_codes(const float (&h)[4], const RowScale& r, uint32_t key, uint32_t quad) {
-  float off[4];
+  uint32_t q = 0;
   if constexpr (SEEDED) {
     const uint32_t w0 = pair_bits(key, 2 * quad), w1 = pair_bits(key, 2 * quad + 1);
-    off[0] = __uint_as_float((w0 & 0xffffu) | 0x43000000u) - 0.5f;
-    off[1] = __uint_as_float((w0 >> 16) | 0x43000000u) - 0.5f;
-    off[2] = __uint_as_float((w1 & 0xffffu) | 0x43000000u) - 0.5f;
-    off[3] = __uint_as_float((w1 >> 16) | 0x43000000u) - 0.5f;
+    auto sum = [&](float v, uint32_t j) { return __float_as_uint(fmaf(v, r.inv, __uint_as_float(j | 0x43c00000u))); };
+    const uint32_t s0 = sum(h[0], (w0 >> 1) & 0x7fffu), s1 = sum(h[1], w0 >> 17);
+    const uint32_t s2 = sum(h[2], (w1 >> 1) & 0x7fffu), s3 = sum(h[3], w1 >> 17);
+    // bytes 1 and 2 of two sums side by side, shifted to whole bytes
+    const uint32_t p0 = __builtin_amdgcn_perm(s1, s0, 0x06050201u) >> 7, p1 = __builtin_amdgcn_perm(s3, s2, 0x06050201u) >> 7;
+    q = __builtin_amdgcn_perm(p1, p0, 0x06040200u);
   } else {
-    off[0] = off[1] = off[2] = off[3] = 128.f + 0x1p-16f;
+    constexpr float kOff = 128.f + 0x1p-16f;
+    q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[0], r.inv, kOff), 0, q);
+    q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[1], r.inv, kOff), 1, q);
+    q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[2], r.inv, kOff), 2, q);
+    q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[3], r.inv, kOff), 3, q);
   }
-  uint32_t q = 0;
-  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[0], r.inv, off[0]), 0, q);
-  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[1], r.inv, off[1]), 1, q);
-  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[2], r.inv, off[2]), 2, q);
-  q = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(h[3], r.inv, off[3]), 3, q);
   return r.bad ? 0u : q ^ kBias;
 }
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
@@ -350,7 +351,7 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
     });
   }
   float y = group_all<L>(st.y, fadd2);
-  const RowScale rs = row_scale_fast(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
+  const RowScale rs = row_scale(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float h4[4] = {st.h[4 * k], st.h[4 * k + 1], st.h[4 * k + 2], st.h[4 * k + 3]};
@@ -461,7 +462,7 @@ __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, Cache
       c = B[j];
     });
     float y = group_all<L>(st.y, fadd2);
-    const RowScale rs = row_scale_fast(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
+    const RowScale rs = row_scale(group_all<L>(st.amax, fmax2), row_bad<L>(st.bad));
     const uint32_t key = SEEDED ? row_key(seed, uint32_t(b * p.rows) + row + own) : 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

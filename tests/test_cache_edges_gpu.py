@@ -1,0 +1,82 @@
+"""The state cache and the steps on it where large batches, held states and infinite numbers take
+them.  Tolerances as in test_cache_gpu."""
+import numpy as np
+import pytest
+
+from oracle import recurrent as orc
+from tests.test_cache_gpu import Beams, _torch, check_step
+from tests.test_gated_gpu import bf, dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("layer", ["s6", "s6 softplus", "ssd"])
+def test_held_states_keep_their_codes(layer):
+    """1500 tokens whose step size leaves the states as they are, a new seed each.  A state is then
+    c s for its code c and scale s, off by half an ulp (2^-24) like the factor that takes it back to
+    c: 127 (2^-24 + 2^-24) < 2^-16, within which a code is kept whatever is drawn.  The scale is
+    127 s / 127 again, both rounded, and that is s but where 127 s lies halfway between two
+    numbers (one scale in 128): it moves by an ulp in the first token and stays from there on."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    gen = t.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s: t.randn(*s, generator=gen, device="cuda")                           # noqa: E731
+    B, D, N = (2, 192, 128) if layer == "ssd" else (3, 512, 16)
+    q, scale = ss.state_cache(B, D // 64, 64, N) if layer == "ssd" else ss.state_cache(B, D, N)
+    h = rnd(*q.shape) * t.exp(rnd(*q.shape[:-1], 1))
+    seed = t.tensor([1 << 40], dtype=t.int64, device="cuda")
+    ss.state_cache_write(h, q, scale, seed=seed)
+    written, first = (q.clone(), scale.clone()), None
+    A = -1.0 - t.arange(N, device="cuda", dtype=t.float32).expand(D, N).contiguous()
+    Bm, Cm, u = rnd(B, N), rnd(B, N), rnd(B, D)
+    low = lambda a: a.to(t.bfloat16)                                                     # noqa: E731
+    for n in range(1500):
+        seed.add_(1)
+        if layer == "ssd":
+            ss.selective_scan_ssd_step_cached(low(u).view(B, D // 64, 64), low(t.zeros(B, D // 64, device="cuda")), A[0, :D // 64].contiguous(),
+                                              low(Bm), low(Cm), q=q, scale=scale, seed=seed)
+        elif layer == "s6":
+            ss.selective_scan_step_cached(u, t.zeros_like(u), A, Bm, Cm, q=q, scale=scale, seed=seed)
+        else:                                                    # softplus(-60) = 9e-27
+            ss.selective_scan_step_cached(u, t.full_like(u, -60.0), A, Bm, Cm, q=q, scale=scale, seed=seed, delta_softplus=True)
+        if n == 0:
+            first = (q.clone(), scale.clone())
+    assert t.equal(q, first[0]) and t.equal(scale, first[1])
+    assert t.equal(first[0], written[0])
+    moved = (first[1] != written[1])
+    assert moved.float().mean() < 0.05 and t.all((first[1] - written[1]).abs() <= written[1] * 2.0 ** -23)
+
+
+def test_stochastic_rounding_follows_where_rounding_to_nearest_stalls():
+    """A row's largest value does not decay, so the codes keep their size; the others decay by 0.99 a
+    token, less than half a code at first and so for ever when rounded to nearest.  Rounding
+    changes a value by less than a scale s a token, with a variance of s^2 / 4 at most, which
+    later tokens shrink: after many of them s^2 / 4 / (1 - 0.99^2) = (3.55 s)^2 for a value, and
+    the mean of 65536 rows is within six of its deviations, 0.083 s, of the decay."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, D, N, steps = 16, 4096, 4, 200
+    h0 = t.tensor([1.0, 0.3, -0.2, 0.1], device="cuda").expand(B, D, N).contiguous()
+    zero, one = t.zeros(B, D, device="cuda"), t.ones(B, N, device="cuda")
+    rate = -float(np.log(0.99))
+    dt, A = t.ones(B, D, device="cuda"), t.tensor([0.0, -rate, -rate, -rate], device="cuda").expand(D, N).contiguous()
+    got = {}
+    for name in ("nearest", "seeded"):
+        q, scale = ss.state_cache(B, D, N)
+        seed = t.tensor([1], dtype=t.int64, device="cuda") if name == "seeded" else None
+        ss.state_cache_write(h0, q, scale, seed=seed)
+        stored = ss.state_cache_read(q, scale)
+        for _ in range(steps):
+            if seed is not None:
+                seed.add_(1)
+            ss.selective_scan_step_cached(zero, dt, A, one, one, q=q, scale=scale, seed=seed)
+        back = ss.state_cache_read(q, scale)
+        if name == "nearest":
+            assert t.equal(back, stored)
+        assert t.all((back[..., 0] - 1).abs() <= 2.0 ** -20)
+        got[name] = host(back).reshape(-1, N).mean(0)
+    true = 0.99 ** (steps * (np.arange(N) > 0)) * host(h0)[0, 0]
+    err = {k: np.abs(v - true)[1:] for k, v in got.items()}
+    bound = 6 * 0.5 / 127 / np.sqrt(1 - 0.99 ** 2) / np.sqrt(B * D)
+    print(err, bound)
+    assert np.all(err["seeded"] <= bound) and np.all(err["nearest"] > 20 * bound)
