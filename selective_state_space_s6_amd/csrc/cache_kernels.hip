@@ -337,16 +337,17 @@ __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CachePar
       b = bc[0][n0 + j];
     });
   } else {
-    // (e^x - 1) / A u = dt u phi, phi = (e^x - 1) / x, x = dt A.  In y = x log2 e: from |y| = 1/12
-    // down ln2 phi is the series of phi to x^3 / 24, whose next term is 9e-8 of it; above it is
-    // (2^y - 1) / y, where the difference and v_rcp_f32 leave 1.3e-6.
+    // (e^x - 1) / A u, x = dt A, y = x log2 e.  From |y| = 1/12 down the series of dt u (e^x - 1) / x to
+    // x^3 / 24, whose next term is 9e-8 of it; above it (2^y - 1) / A, where the difference and
+    // v_rcp_f32 leave 1.3e-6.  (dt enters that through the exponential alone: an infinite step
+    // gives -u / A, a product with dt would be 0 * inf.)
     constexpr float kLn2 = 0.693147181f;
-    const float lt = dt * kLog2e, dul = du * kLog2e;
+    const float lt = dt * kLog2e, k1 = du * (kLn2 / 2.f), k2 = du * (kLn2 * kLn2 / 6.f), k3 = du * (kLn2 * kLn2 * kLn2 / 24.f);
     advance(w, C, st, [&](int j, float& keep, float& a, float& b) {
-      const float y = lt * A[j], ab = __builtin_amdgcn_exp2f(y), iy = __builtin_amdgcn_rcpf(y);
-      const float ser = fmaf(y, fmaf(y, fmaf(y, kLn2 * kLn2 * kLn2 * kLn2 / 24.f, kLn2 * kLn2 * kLn2 / 6.f), kLn2 * kLn2 / 2.f), kLn2);
+      const float y = lt * A[j], ab = __builtin_amdgcn_exp2f(y), ia = __builtin_amdgcn_rcpf(A[j]);
+      const float ser = fmaf(y, fmaf(y, fmaf(y, k3, k2), k1), du);
       keep = ab * scale;
-      a = (fabsf(y) < 1.f / 12.f ? ser : fmaf(ab, iy, -iy)) * dul;
+      a = fabsf(y) < 1.f / 12.f ? ser : fmaf(ab, ia, -ia) * u;
       b = bc[0][n0 + j];
     });
   }

@@ -80,3 +80,28 @@ def test_stochastic_rounding_follows_where_rounding_to_nearest_stalls():
     bound = 6 * 0.5 / 127 / np.sqrt(1 - 0.99 ** 2) / np.sqrt(B * D)
     print(err, bound)
     assert np.all(err["seeded"] <= bound) and np.all(err["nearest"] > 20 * bound)
+
+
+@pytest.mark.parametrize("N", [5, 16, 20, 48])
+def test_steps_too_large_for_a_product(N):
+    """Zero-order hold of step sizes up to infinity: the coefficient is (e^(dt A) - 1) / A, -1 / A from
+    where the exponential is nothing."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    sizes = np.array([np.inf, 3e38, 1e38, 1e30, 2.0 ** 21, 2.0 ** 20, 1e4, 0.01], np.float32)
+    B, D = len(sizes), 40
+    rng = np.random.default_rng(N)
+    b = Beams(B, (D, N), N)
+    u, Bm, Cm = (rng.standard_normal(s).astype(np.float32) for s in ((B, D), (B, N), (B, N)))
+    A = (-np.exp(rng.uniform(-4, 4, (D, N)))).astype(np.float32)
+    delta = sizes[:, None].repeat(D, 1)
+    y_ref, h_ref = orc.step(b.h.reshape(B, D, N), u, delta, A, Bm, Cm)
+    h_abs = orc.step(np.abs(b.h).reshape(B, D, N), np.abs(u), delta, A, np.abs(Bm), Cm)[1]
+    for softplus in (False, True):
+        q, scale, y = dev(b.q), dev(b.scale), t.zeros(B, D, device="cuda")
+        raw = np.where(delta < 1, np.log(np.expm1(np.minimum(delta.astype(np.float64), 1))), delta).astype(np.float32)
+        if softplus:
+            y_ref, h_ref = orc.step(b.h.reshape(B, D, N), u, raw, A, Bm, Cm, softplus=True)
+        ss.selective_scan_step_cached(dev(u), dev(raw if softplus else delta), dev(A), dev(Bm), dev(Cm), None, None, y, q=q,
+                                      scale=scale, read_slots=dev(b.read), write_slots=dev(b.write), delta_softplus=softplus)
+        check_step(b, q, scale, y, np.zeros((B, D)), y_ref, h_ref, h_abs, "f32", None, "softplus %d" % softplus)
