@@ -139,8 +139,9 @@ template <bool CUT> __device__ __forceinline__ float through(float A, float H, f
 }
 
 // The product of decays.  With CUT it is zero behind a reset alone: one that merely leaves fp32 is
-// held at its least normal number, so an infinity does not end there.
-constexpr float kLeastDecay = 0x1p-126f;
+// held at its least number, so an infinity does not end there.  (Of the largest state that leaves
+// 2^-21, what a product rounded to fp32 may be off by; the least normal number would leave 4.)
+constexpr float kLeastDecay = 0x1p-149f;
 template <bool CUT> __device__ __forceinline__ float decays(float A, float a) {
   if (CUT) return A == 0.f || a == 0.f ? 0.f : fmaxf(A * a, kLeastDecay);
   return A * a;
