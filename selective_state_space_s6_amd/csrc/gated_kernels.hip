@@ -138,13 +138,14 @@ template <bool CUT> __device__ __forceinline__ float through(float A, float H, f
   return CUT && A == 0.f ? H : v;
 }
 
-// The product of decays.  With CUT it is zero behind a reset alone: one that merely leaves fp32 is
-// held at its least number, so an infinity does not end there.  (Of the largest state that leaves
-// 2^-21, what a product rounded to fp32 may be off by; the least normal number would leave 4.)
+// The product of decays.  One that leaves fp32 is held at its least number, so an infinity does not
+// end there (in 0 * inf); with CUT it is zero behind a reset alone.  (Of the largest state that
+// leaves 2^-21, what a product rounded to fp32 may be off by; the least normal number would
+// leave 4.)
 constexpr float kLeastDecay = 0x1p-149f;
 template <bool CUT> __device__ __forceinline__ float decays(float A, float a) {
-  if (CUT) return A == 0.f || a == 0.f ? 0.f : fmaxf(A * a, kLeastDecay);
-  return A * a;
+  if (CUT && (A == 0.f || a == 0.f)) return 0.f;
+  return fmaxf(A * a, kLeastDecay);
 }
 
 // The links of one chunk, the pos-th of its chain (counted from the end in the backward pass).
@@ -371,7 +372,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     } else {
       run_map<S, false>(a0, b0, 0, A0, H0);
       run_map<S, false>(a1, b1, 0, A1, H1);
-      if (RESET) { A0 = fmaxf(A0, kLeastDecay); A1 = fmaxf(A1, kLeastDecay); }
+      A0 = fmaxf(A0, kLeastDecay);
+      A1 = fmaxf(A1, kLeastDecay);
     }
     const int c = int(k.ct) * kCh + 2 * lane;
     const bool ok0 = c < D, ok1 = c + 1 < D, last = int(k.chunk) == p.n_chunks - 1;
@@ -409,6 +411,8 @@ __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
     __syncthreads();
     after = __builtin_amdgcn_readfirstlane(tickets[par]);
     float h0 = links[par][0][lane].z, h1 = links[par][0][lane].w;
+    // (the first map holds the initial state: an infinite one, taken again times its A = 0, would be NaN)
+    if (k.chunk == 0 && wave != 0) h0 = h1 = 0.f;
     for (int j = 1; j <= link.in_group; ++j) {
       const float4 m = links[par][j][lane];
       h0 = through<RESET>(m.x, m.z, h0);
@@ -648,7 +652,8 @@ __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
     } else {
       run_map<S, false>(a0, b0, 0, A0, H0);
       run_map<S, false>(a1, b1, 0, A1, H1);
-      if (RESET) { A0 = fmaxf(A0, kLeastDecay); A1 = fmaxf(A1, kLeastDecay); }
+      A0 = fmaxf(A0, kLeastDecay);
+      A1 = fmaxf(A1, kLeastDecay);
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
         G0 = a0[i] * (G0 + T::lo(yr[i]));

@@ -4,9 +4,63 @@ import numpy as np
 import pytest
 
 from oracle import recurrent as orc
-from tests.test_gated_gpu import GTOL, TOL, backward, close, forward, inputs
+from tests.test_gated_gpu import GTOL, TOL, backward, close, forward, host, inputs
 
 pytestmark = pytest.mark.gpu
+
+
+def same_infinities(got, ref, tol, what, signs=True):
+    """NaN nowhere, infinities (of the same sign) where the reference has them, the rest close to it."""
+    got = host(got)
+    assert not np.isnan(ref).any() and not np.isnan(got).any(), what
+    assert np.array_equal(np.isinf(got), np.isinf(ref)), what
+    if signs:
+        assert np.array_equal(got == np.inf, ref == np.inf), what
+    fine = np.isfinite(ref)
+    close(np.where(fine, got, 0), np.where(fine, ref, 0), tol, what)
+
+
+def bwd_by_sequences(i, cut):
+    """The statement's gradients of rows that a reset at token `cut` (None: nowhere) parts, sequence by
+    sequence: no infinity is multiplied by the reset's zero."""
+    part = lambda lo, hi: [i[k][:, lo:hi] for k in ("x", "r", "g")] + [i["lam"], i["dy"][:, lo:hi]]       # noqa: E731
+    if cut is None:
+        return orc.gated_bwd(*part(0, None), h0=i["h0"], dlast=i["dlast"])
+    one = orc.gated_bwd(*part(0, cut), h0=i["h0"])
+    two = orc.gated_bwd(*part(cut, None), reset=i["reset"][:, cut:], dlast=i["dlast"])
+    two["dr"][:, 0] = 0
+    return dict({k: np.concatenate([one[k], two[k]], 1) for k in ("dx", "dr", "dg")}, dinitial_state=one["dinitial_state"])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 40, 70), (2, 700, 70), (2, 3001, 71)])
+@pytest.mark.parametrize("cut", [False, True])
+def test_an_infinity_stays_one(cut, size, io):
+    """From the initial state, from an input and from gradients, through decays of which a run's product
+    stays in fp32 (channels 3 and 7) and through ones of which it does not (2, 5)."""
+    B, L, D = size
+    i = inputs(B, L, D, io=io, seed=L)
+    i["lam"][[2, 5]] = 2.0
+    if cut:
+        i["reset"] = np.arange(L)[None].repeat(B, 0) == L - 10
+    i["h0"][0, 3], i["h0"][1, 2] = np.inf, -np.inf
+    i["x"][1, L // 3, 5], i["x"][0, L // 3, 7] = np.inf, -np.inf
+    got, last, marks = forward(i, io)
+    y, l = orc.gated_fwd(i["x"], i["r"], i["g"], i["lam"], h0=i["h0"], reset=i["reset"])
+    same_infinities(got, y, TOL[io], "y")
+    same_infinities(last, l, TOL["f32"], "last_state")
+    same_infinities(marks, np.concatenate([i["h0"].astype(np.float64)[:, None], y], 1)[:, :-1:64], TOL["f32"], "checkpoints")
+    i["h0"], i["x"] = (np.where(np.isinf(i[k]), 1, i[k]).astype(np.float32) for k in ("h0", "x"))
+    _, _, marks = forward(i, io)
+    i["dlast"][0, 3], i["dlast"][1, 2] = np.inf, -np.inf
+    i["dy"][1, L // 3, 5], i["dy"][0, L // 3, 7] = np.inf, -np.inf
+    g = backward(i, io, marks=marks)
+    ref = bwd_by_sequences(i, L - 10 if cut else None)
+    same_infinities(g["dx"], ref["dx"], GTOL[io], "dx")
+    same_infinities(g["dg"], ref["dg"], GTOL[io], "dg")
+    same_infinities(g["dr"], ref["dr"], GTOL[io], "dr", signs=False)     # (a difference of like numbers)
+    same_infinities(g["dinitial_state"], ref["dinitial_state"], GTOL["f32"], "dinitial_state")
+    assert np.array_equal(np.flatnonzero(~np.isfinite(host(g["dlam"]))), [2, 3, 5, 7])
 
 
 @pytest.mark.parametrize("cut", [False, True])
