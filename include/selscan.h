@@ -402,7 +402,7 @@ typedef struct selscan_gated_dims {
   int64_t seqlen;          /* >= 0 */
   int64_t dim;             /* D >= 1, at most 2^20 */
   int64_t x_sb, x_sl;      /* strides in elements as in selscan_dims (unit stride over channels); */
-  int64_t r_sb, r_sl;      /* token strides at most 2^20 */
+  int64_t r_sb, r_sl;      /* token strides at most 2^20, not used where seqlen is 1 */
   int64_t g_sb, g_sl;
   int64_t y_sb, y_sl;      /* y of the forward, dy of the backward */
   int64_t reset_sb;        /* bytes between batch rows of reset (its token stride is 1) */

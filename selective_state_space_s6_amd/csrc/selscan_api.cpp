@@ -947,11 +947,17 @@ struct GatedPlan {
   size_t bwd_link_bytes = 0, off_kd = 0, off_ckpt = 0, off_plam = 0, bwd_bytes = 0;
 };
 
+// One token has no stride to a next one: whatever stands there is not looked at.
+static selscan_gated_dims gated_used(selscan_gated_dims d) {
+  if (d.seqlen == 1) d.x_sl = d.r_sl = d.g_sl = d.y_sl = d.dim;
+  return d;
+}
+
 // Validate dims and lay out the workspaces.  Does not look at pointers.
 static int gated_plan(const selscan_gated_dims* dims, bool have_ckpt, GatedPlan* out) {
   if (!dims) return SELSCAN_ERR_NULL;
   if (dims->abi_version != SELSCAN_ABI_VERSION) return SELSCAN_ERR_ABI;
-  const selscan_gated_dims& d = *dims;
+  const selscan_gated_dims d = gated_used(*dims);
   if (d.batch < 0 || d.seqlen < 0 || d.dim < 1) return SELSCAN_ERR_DIMS;
   for (int64_t s : {d.x_sb, d.x_sl, d.r_sb, d.r_sl, d.g_sb, d.g_sl, d.y_sb, d.y_sl, d.reset_sb})
     if (s < 0) return SELSCAN_ERR_DIMS;
@@ -1052,7 +1058,7 @@ int gated_scan_fwd(const void* x, const void* r, const void* g, const float* lam
   GatedPlan pl;
   int st = gated_plan(dims, true, &pl);
   if (st != SELSCAN_OK) return st;
-  const selscan_gated_dims& d = *dims;
+  const selscan_gated_dims d = gated_used(*dims);
   if (!gated_rows_apart(d)) return SELSCAN_ERR_UNSUPPORTED;
   const bool no_tokens = d.batch * d.seqlen == 0;
   if (!lam || (!no_tokens && (!x || !r || !g || !y))) return SELSCAN_ERR_NULL;
@@ -1095,7 +1101,7 @@ int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam
   GatedPlan pl;
   int st = gated_plan(dims, checkpoints != nullptr, &pl);
   if (st != SELSCAN_OK) return st;
-  const selscan_gated_dims& d = *dims;
+  const selscan_gated_dims d = gated_used(*dims);
   const bool no_tokens = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16;
   if (!lam || !dlam || (!no_tokens && (!x || !r || !g || !dy || !dx || !dr || !dg))) return SELSCAN_ERR_NULL;
   if (!all_aligned({x, r, g, dy, dx, dr, dg}, bf16 ? 2 : 4) ||
@@ -1143,10 +1149,12 @@ int gated_scan_bwd(const void* x, const void* r, const void* g, const float* lam
 
 int gated_scan_step(const void* x, const void* r, const void* g, const float* lam, void* y, float* state,
                     const selscan_gated_dims* dims, void* stream) {
+  if (!dims) return SELSCAN_ERR_NULL;
+  selscan_gated_dims d = gated_used(*dims);
+  d.reset_sb = 0;                               // no reset marks
   GatedPlan pl;
-  const int st = gated_plan(dims, true, &pl);
+  const int st = gated_plan(&d, true, &pl);
   if (st != SELSCAN_OK) return st;
-  const selscan_gated_dims& d = *dims;
   if (d.seqlen != 1) return SELSCAN_ERR_DIMS;
   if (!gated_rows_apart(d)) return SELSCAN_ERR_UNSUPPORTED;
   if (!lam || (d.batch > 0 && (!x || !r || !g || !y || !state))) return SELSCAN_ERR_NULL;

@@ -233,3 +233,14 @@ def test_one_launch_has_fewer_than_2_32_threads():
     assert fwd(gated(batch=1 << 23)) == step(gated(batch=1 << 22, L=1, D=129)) == -3
     c = cache(elems=1 << 20, row_len=64, slots=1 << 20)
     assert cwrite(c, count=1 << 12) == cread(c, count=1 << 12) == -3
+
+
+def test_one_token_has_no_token_stride():
+    far = dict(x_sl=(1 << 20) + 1, r_sl=1 << 40, g_sl=-1, y_sl=1 << 22)
+    d = gated(batch=0, L=1, **far)
+    assert fwd(d, x=None, r=None, g=None, y=None) == step(d, x=None, r=None, g=None, y=None, state=None) == 0
+    assert step(gated(batch=0, L=1, reset_sb=-1), x=None, r=None, g=None, y=None, state=None) == 0
+    d = gated(L=1, **far)
+    assert fwd(d, x=None) == bwd(d, dx=None) == step(d, state=None) == -1       # on to the pointers
+    assert fwd(gated(L=1, y_sb=7, **far)) == step(gated(L=1, y_sb=7, **far)) == -3
+    assert fwd(gated(L=2, **far)) == bwd(gated(L=2, **far)) == -2

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import recurrent as orc
-from tests.test_gated_gpu import GTOL, TOL, backward, close, forward, host, inputs
+from tests.test_gated_gpu import (GTOL, TOL, _torch, backward, check_backward, check_forward, close, dev, forward, host, inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,33 @@ def test_nothing_is_left_of_a_large_state(size, lam, cut):
     ref = orc.gated_bwd(i["x"], i["r"], i["g"], i["lam"], i["dy"], h0=i["h0"], reset=i["reset"], dlast=i["dlast"])
     for k in ("dx", "dg"):
         close(g[k][:, :-8], ref[k][:, :-8], GTOL["f32"], k)
+
+
+def test_one_token_of_a_time_major_buffer():
+    """A token's rows with a token stride past 2^20, which one token does not use (the C entry points)."""
+    import ctypes
+
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, D = 512, 2560
+    i = inputs(B, 1, D, seed=5)
+    v = {k: dev(i[k]) for k in ("x", "r", "g", "lam", "h0", "dy", "dlast")}
+    p, lib, s = (lambda a: a.data_ptr()), ss.lib(), t.cuda.current_stream().cuda_stream       # noqa: E731
+    d = ss.GatedDims()
+    lib.gated_scan_dims_init(ctypes.byref(d), 0, B, 1, D)
+    d.x_sl = d.r_sl = d.g_sl = d.y_sl = B * D
+    assert B * D > 1 << 20
+    y, last, marks = t.empty_like(v["x"]), t.empty_like(v["h0"]), ss.gated_checkpoints(v["x"])
+    assert lib.gated_scan_fwd(p(v["x"]), p(v["r"]), p(v["g"]), p(v["lam"]), None, p(y), p(v["h0"]), p(last), p(marks),
+                              ctypes.byref(d), None, 0, s) == 0
+    check_forward(i, "f32", (y, last, marks))
+    g = {k: t.empty_like(v["x"]) for k in ("dx", "dr", "dg")}
+    g.update(dlam=t.empty_like(v["lam"]), dinitial_state=t.empty_like(v["h0"]))
+    assert lib.gated_scan_bwd(p(v["x"]), p(v["r"]), p(v["g"]), p(v["lam"]), None, p(v["h0"]), p(marks), p(v["dy"]), p(v["dlast"]),
+                              *(p(g[k]) for k in ("dx", "dr", "dg", "dlam", "dinitial_state")), ctypes.byref(d), None, 0, s) == 0
+    check_backward(i, "f32", g)
+    d.reset_sb = -1
+    state = v["h0"].clone()
+    y.zero_()
+    assert lib.gated_scan_step(p(v["x"]), p(v["r"]), p(v["g"]), p(v["lam"]), p(y), p(state), ctypes.byref(d), s) == 0
+    check_forward(i, "f32", (y, state, None))
