@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 
 from oracle import recurrent as orc
-from tests.test_gated_gpu import (GTOL, TOL, _torch, backward, check_backward, check_forward, close, dev, forward, host, inputs)
+from tests.test_gated_gpu import (GTOL, TOL, _torch, backward, check_backward, check_forward, close, dev, forward, host,
+                                   inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +114,38 @@ def test_one_token_of_a_time_major_buffer():
     y.zero_()
     assert lib.gated_scan_step(p(v["x"]), p(v["r"]), p(v["g"]), p(v["lam"]), p(y), p(state), ctypes.byref(d), s) == 0
     check_forward(i, "f32", (y, state, None))
+
+
+# Chunks of the forward (fp32, bf16) and of the backward pass: 525, 273 and 525; 1560, 780 and 1560; 516, 260
+# and 516, where the 256 workgroups that are resident take a second, a third and more of them.
+LARGE = [(3, 1537, 771), (6, 8300, 130), (4, 8193, 1)]
+
+
+@pytest.mark.parametrize("reset", [None, "some"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", LARGE)
+def test_workgroups_that_take_several_chunks(size, io, reset):
+    i = inputs(*size, io=io, seed=sum(size), reset=reset)
+    got = forward(i, io)
+    check_forward(i, io, got, what=str(size))
+    check_backward(i, io, backward(i, io, marks=got[2]), what=str(size))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_several_chunks_without_checkpoints(io):
+    i = inputs(3, 1537, 770, io=io, seed=1, reset="some")
+    check_backward(i, io, backward(i, io))
+
+
+@pytest.mark.parametrize("reset", [None, "some"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 129, 65), (2, 1000, 70), (3, 257, 130), (3, 1537, 771)])
+def test_decays_on_both_sides_of_the_series(size, io, reset):
+    """log a between -17 and 0: tokens and channels of one wavefront on both sides of 1/8, from which on
+    the decay comes from exp2.  Its argument, off by four ulp, leaves |y| 2^-21 of a, at most 2^-22.5
+    of one; m and log a keep their relative errors, so the tolerances of the series hold."""
+    i = inputs(*size, io=io, seed=sum(size) + 2, reset=reset)
+    i["lam"] = np.random.default_rng(size[2]).uniform(-7, 2, size[2]).astype(np.float32)
+    got = forward(i, io)
+    check_forward(i, io, got, what=str(size))
+    check_backward(i, io, backward(i, io, marks=got[2]), what=str(size))
