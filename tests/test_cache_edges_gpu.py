@@ -105,3 +105,52 @@ def test_steps_too_large_for_a_product(N):
         ss.selective_scan_step_cached(dev(u), dev(raw if softplus else delta), dev(A), dev(Bm), dev(Cm), None, None, y, q=q,
                                       scale=scale, read_slots=dev(b.read), write_slots=dev(b.write), delta_softplus=softplus)
         check_step(b, q, scale, y, np.zeros((B, D)), y_ref, h_ref, h_abs, "f32", None, "softplus %d" % softplus)
+
+
+def ssd_case(B, H, N, seeded, first=0, steps=None):
+    """One scalar-decay step of B rows, codes from the `first`-th byte of a buffer on, against the statement."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    rng = np.random.default_rng(N + H + B)
+    b = Beams(B, (H, 64, N), H)
+    x, z, y0 = (bf(rng.standard_normal((B, H, 64)), "bf16") for _ in range(3))
+    Bm, Cm = (bf(rng.standard_normal((B, N)), "bf16") for _ in range(2))
+    delta = bf(np.exp(rng.standard_normal((B, H)) - 4), "bf16")
+    if steps is not None:
+        delta = bf(np.resize(steps, (B, H)), "bf16")
+    A = -rng.uniform(0.5, 16, H).astype(np.float32)
+    Ds = rng.standard_normal(H * 64).astype(np.float32)
+    args = (np.repeat(delta, 64, 1), np.repeat(A, 64)[:, None].repeat(N, 1))
+    y_ref, h_ref = orc.step(b.h, x.reshape(B, -1), *args, Bm, Cm, Ds, z.reshape(B, -1))
+    h_abs = orc.step(np.abs(b.h), np.abs(x).reshape(B, -1), *args, np.abs(Bm), Cm)[1]
+    buf = t.full((b.q.size + first + 64,), 77, dtype=t.int8, device="cuda")
+    q = buf[first:first + b.q.size].view(b.q.shape)
+    q.copy_(dev(b.q))
+    scale, y = dev(b.scale), dev(y0, "bf16")
+    seed = 1000 if seeded else None
+    ss.selective_scan_ssd_step_cached(dev(x, "bf16"), dev(delta, "bf16"), dev(A), dev(Bm, "bf16"), dev(Cm, "bf16"), dev(Ds),
+                                      dev(z, "bf16"), y, q=q, scale=scale, read_slots=dev(b.read), write_slots=dev(b.write),
+                                      seed=None if seed is None else t.tensor([seed], dtype=t.int64, device="cuda"))
+    check_step(b, q, scale, y, y0.astype(np.float64), y_ref, h_ref, h_abs, "bf16", seed, "%d rows, %d heads" % (B, H))
+    assert t.all(buf[:first] == 77) and t.all(buf[first + b.q.size:] == 77)
+
+
+@pytest.mark.parametrize("seeded", [False, True])
+@pytest.mark.parametrize("B,H,N", [(64, 33, 64), (64, 65, 64), (64, 17, 128), (64, 33, 128)])
+def test_ssd_step_of_large_batches(B, H, N, seeded):
+    """Workgroups that walk 2, 4, 2 and 4 groups of rows; with 33 heads (64 states: 33 groups, 128: 66) and
+    with 65 the last workgroup's walk ends behind the last row.  All slots but the written ones are
+    compared, so nothing may be stored there."""
+    ssd_case(B, H, N, seeded)
+
+
+@pytest.mark.parametrize("seeded", [False, True])
+@pytest.mark.parametrize("first", [1, 4, 8])
+@pytest.mark.parametrize("B,H,N", [(3, 2, 64), (64, 33, 128)])
+def test_ssd_step_on_a_misaligned_cache(B, H, N, first, seeded):
+    ssd_case(B, H, N, seeded, first)
+
+
+@pytest.mark.parametrize("N", [64, 128])
+def test_ssd_steps_too_large_for_a_product(N):
+    ssd_case(5, 7, N, True, steps=np.array([np.inf, 3e38, 1e30, 1e4, 0.01, 0.0], np.float32))
