@@ -1265,10 +1265,12 @@ int selective_scan_ssd_step_cached(const void* x, const void* delta, const float
                                    const float* Dskip, const void* z, void* y, int8_t* q, float* scale,
                                    const int32_t* read_slots, const int32_t* write_slots, const int64_t* seed,
                                    const selscan_ssd_dims* dims, const selscan_cache_dims* cache, void* stream) {
+  if (!dims) return SELSCAN_ERR_NULL;
+  selscan_ssd_dims d = *dims;
+  d.path = d.segments = 0;                      // one token has no path
   SsdPlan pl;
-  int st = ssd_check(dims, &pl);
+  int st = ssd_check(&d, &pl);
   if (st != SELSCAN_OK) return st;
-  const selscan_ssd_dims& d = *dims;
   if (d.seqlen != 1) return SELSCAN_ERR_DIMS;
   selscan::CacheParams p;
   st = step_cache_check(cache, d.batch, d.nheads * 64 * d.dstate, d.dstate, read_slots, write_slots, q, scale, seed, &p);

@@ -244,3 +244,9 @@ def test_one_token_has_no_token_stride():
     assert fwd(d, x=None) == bwd(d, dx=None) == step(d, state=None) == -1       # on to the pointers
     assert fwd(gated(L=1, y_sb=7, **far)) == step(gated(L=1, y_sb=7, **far)) == -3
     assert fwd(gated(L=2, **far)) == bwd(gated(L=2, **far)) == -2
+
+
+def test_the_ssd_step_does_not_look_at_path_and_segments():
+    d, c = ss.ssd_dims(4, 1, 3, 64, 128), cache(elems=3 * 64 * 128, row_len=128)
+    for d.path, d.segments in ((0, 2), (3, 2), (7, 0), (-1, -1)):
+        assert ssd(d, c, x=None) == -1 and ssd(d, c, x=F + 8) == -4       # on to the pointers
