@@ -154,3 +154,76 @@ def test_ssd_step_on_a_misaligned_cache(B, H, N, first, seeded):
 @pytest.mark.parametrize("N", [64, 128])
 def test_ssd_steps_too_large_for_a_product(N):
     ssd_case(5, 7, N, True, steps=np.array([np.inf, 3e38, 1e30, 1e4, 0.01, 0.0], np.float32))
+
+
+def test_a_step_size_for_all_rows_and_shared_inputs():
+    """delta [D], and u, B and C of one row expanded over the batch: as written out."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, D, N = 7, 70, 16
+    gen = t.Generator(device="cuda").manual_seed(8)
+    rnd = lambda *s: t.randn(*s, generator=gen, device="cuda")                           # noqa: E731
+    u, Bm, Cm, delta, A = rnd(1, D), rnd(1, N), rnd(1, N), t.rand(D, generator=gen, device="cuda"), -t.ones(D, N, device="cuda")
+    got = []
+    for wide in (lambda a, n: a.expand(B, n), lambda a, n: a.expand(B, n).contiguous()):
+        q, scale = ss.state_cache(B, D, N)
+        ss.state_cache_write(t.arange(B * D * N, device="cuda", dtype=t.float32).view(B, D, N), q, scale)
+        d = delta if not got else delta.expand(B, D).contiguous()
+        y = ss.selective_scan_step_cached(wide(u, D), d, A, wide(Bm, N), wide(Cm, N), q=q, scale=scale)
+        got.append((y, q, scale))
+    assert all(t.equal(a, b) for a, b in zip(*got)) and got[0][0].unique(dim=0).shape[0] == B
+
+
+def test_cached_layers_on_two_streams_and_in_a_graph():
+    """Writing, both steps and reading in one graph, replayed on new inputs between eager calls, and as
+    eager calls on two other streams at once (a cache of its own each)."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, H, N, D, M = 5, 6, 64, 384, 16
+    gen = t.Generator(device="cuda").manual_seed(9)
+    rnd = lambda *s: t.randn(*s, generator=gen, device="cuda")                           # noqa: E731
+    low = lambda *s: rnd(*s).to(t.bfloat16)                                              # noqa: E731
+    A, AH = -t.rand(D, M, generator=gen, device="cuda"), -t.rand(H, generator=gen, device="cuda")
+    read = t.tensor([4, 3, -1, 4, 0], dtype=t.int32, device="cuda")
+    write = t.tensor([5, 6, 7, -1, 8], dtype=t.int32, device="cuda")
+
+    def inputs():
+        return [rnd(B, D), 0.1 * t.rand(B, D, generator=gen, device="cuda"), rnd(B, M), rnd(B, M), low(B, H, 64),
+                (0.1 * t.rand(B, H, generator=gen, device="cuda")).to(t.bfloat16), low(B, N), low(B, N), rnd(B, D, M), rnd(B, H, 64, N)]
+
+    def caches():
+        return ss.state_cache(9, D, M) + ss.state_cache(9, H, 64, N) + (t.ones(1, dtype=t.int64, device="cuda"), t.zeros(B, D, device="cuda"),
+                                                                         t.zeros(B, H, 64, device="cuda", dtype=t.bfloat16))
+
+    def once(v, c, stream=None):
+        u, d, b1, c1, x, dh, b2, c2, s1, s2 = v
+        q1, e1, q2, e2, seed, y1, y2 = c
+        kw = dict(read_slots=read, write_slots=write, seed=seed, stream=stream)
+        ss.state_cache_write(s1, q1, e1, seed=seed, stream=stream)
+        ss.state_cache_write(s2, q2, e2, seed=seed, stream=stream)
+        ss.selective_scan_step_cached(u, d, A, b1, c1, None, None, y1, q=q1, scale=e1, **kw)
+        ss.selective_scan_ssd_step_cached(x, dh, AH, b2, c2, None, None, y2, q=q2, scale=e2, **kw)
+        return [ss.state_cache_read(q1, e1, slots=write, stream=stream), ss.state_cache_read(q2, e2, slots=write, stream=stream), y1, y2]
+
+    v, c = inputs(), caches()
+    once(v, c)
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        out = once(v, c)
+    for n in range(4):
+        for a, b in zip(v, inputs()):
+            a.copy_(b)
+        c[4].fill_(n)
+        graph.replay()
+        t.cuda.synchronize()
+        got = [a.clone() for a in out]
+        assert all(t.equal(a, b) for a, b in zip(got, once(v, c))), n
+    w, e, f = inputs(), caches(), caches()
+    alone = [[a.clone() for a in once(i, k)] for i, k in ((v, e), (w, f))]
+    one, two = t.cuda.Stream(), t.cuda.Stream()
+    t.cuda.synchronize()
+    for _ in range(3):
+        both = [once(v, e, one), once(w, f, two.cuda_stream)]
+        t.cuda.synchronize()
+        assert all(t.equal(a, b) for p, r in zip(both, alone) for a, b in zip(p, r))

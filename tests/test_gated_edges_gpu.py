@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import recurrent as orc
-from tests.test_gated_gpu import (GTOL, TOL, _torch, backward, check_backward, check_forward, close, dev, forward, host,
+from tests.test_gated_gpu import (GTOL, TOL, _torch, backward, bf, check_backward, check_forward, close, dev, forward, host,
                                    inputs)
 
 pytestmark = pytest.mark.gpu
@@ -149,3 +149,46 @@ def test_decays_on_both_sides_of_the_series(size, io, reset):
     got = forward(i, io)
     check_forward(i, io, got, what=str(size))
     check_backward(i, io, backward(i, io, marks=got[2]), what=str(size))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_windows_of_one_buffer_and_shared_marks(io):
+    """Rows that overlap (a window of D elements at every second one), a batch that shares r, and reset
+    marks of one sequence expanded over the batch."""
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    B, L, D = 3, 200, 37
+    i = inputs(B, L, D, io=io, seed=6, reset="some")
+    flat = dev(bf(np.random.default_rng(1).standard_normal(B * 3 * L + D), io), io)
+    x = flat.as_strided((B, L, D), (3 * L, 2, 1))
+    i["x"] = host(x)
+    i["r"] = i["r"][:1].repeat(B, 0)
+    i["reset"] = i["reset"][:1].repeat(B, 0)
+    r, marks = dev(i["r"][:1], io).expand(B, L, D), dev(i["reset"][:1]).expand(B, L)
+    g, dy = dev(i["g"], io), dev(i["dy"], io)
+    y, last = ss.gated_scan_fwd(x, r, g, dev(i["lam"]), reset=marks, initial_state=dev(i["h0"]), return_last_state=True)
+    check_forward(i, io, (y, last, None))
+    check_backward(i, io, ss.gated_scan_bwd(x, r, g, dev(i["lam"]), dy=dy, reset=marks.to(t.uint8) * 3, initial_state=dev(i["h0"]),
+                                            dlast_state=dev(i["dlast"])))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_captured_step(io):
+    import selective_state_space_s6_amd as ss
+    t = _torch()
+    i = inputs(6, 1, 250, io=io, seed=3)
+    v = {k: dev(i[k][:, 0], io) for k in ("x", "r", "g")}
+    lam, state, y = dev(i["lam"]), dev(i["h0"]), t.zeros_like(v["x"])
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        ss.gated_scan_step(v["x"], v["r"], v["g"], lam, state=state, y=y)
+    for seed in range(3, 7):
+        i = inputs(6, 1, 250, io=io, seed=seed)
+        for k in v:
+            v[k].copy_(dev(i[k][:, 0], io))
+        lam.copy_(dev(i["lam"]))
+        state.copy_(dev(i["h0"]))
+        graph.replay()
+        t.cuda.synchronize()
+        check_forward(i, io, (y[:, None], state, None))
