@@ -486,6 +486,9 @@ int gated_scan_step(const void* x, const void* r, const void* g, const float* la
  * rounded to nearest, a change of less than half a code per token never takes place.
  * The sum is formed to 2^-16: a value within 2^-16 of a code (of its scale) is stored as that
  * code whatever u is, so a state that a token leaves as it was keeps its codes.
+ * The seed is to be another one at every call (the kernels read it and leave it): with the
+ * same seed every value is rounded the same way token after token, and what is lost that way
+ * adds up as it does to nearest.
  * A row whose amax is below 2^-100 is stored as zeros; one that holds an infinity or a NaN is
  * stored with a NaN scale and stands for NaN throughout.
  * Rows of the layers: selective scan elems = dim * dstate, row_len = dstate; scalar-decay
@@ -508,7 +511,7 @@ typedef struct selscan_cache_dims {
 /*
  * state_cache_write -- store `count` states (state: [count][elems] fp32, e.g. a last_state) in
  * the slots that slot_ids names (rows that name no slot are skipped).  seed: one int64 in device
- * memory, or NULL.  state_cache_read -- the values of `count` slots into out ([count][elems],
+ * memory, another value at every call, or NULL.  state_cache_read -- the values of `count` slots into out ([count][elems],
  * out_dtype an enum selscan_dtype; zeros for an id that names no slot).  In a read, ids may
  * repeat.  count * rows must be below 2^32 and count * ceil(elems / 256) below 2^24.  Neither
  * allocates.

@@ -814,7 +814,8 @@ def state_cache_write(state, q, scale, *, slots=None, seed=None, stream=None) ->
     """Store states ([count, *state_shape] float32) in the slots that ``slots`` ([count] int32;
     0, 1, 2, ... when omitted) names, as 8-bit codes; ids outside the cache skip their row and
     the others must differ.  ``seed``: a one-element int64 GPU tensor for stochastic rounding
-    (nearest when omitted)."""
+    (nearest when omitted); it is only read, so change it before every call (``seed.add_(1)``,
+    which a graph can hold): the same seed rounds the same value the same way each time."""
     import torch
     with _On(q, stream) as on:
         dims = _cache_dims(on, q, scale, seed)
@@ -854,7 +855,9 @@ def selective_scan_step_cached(u, delta, A, B, C, Dskip=None, z=None, y=None, *,
     the state in slot read_slots[b] (the zero state where the id is outside the cache) and stores
     the new one in slot write_slots[b]; rows whose write id is outside the cache are padding and
     keep their y.  Ids: [batch] int32, 0, 1, 2, ... when omitted.  A slot that a row writes may be
-    read by that row alone.  delta: [batch, D] (or [D]); B, C: [batch, N].  Returns y."""
+    read by that row alone.  ``seed``: as state_cache_write, to be changed before every token (a
+    seed that stays rounds every value the same way, and the errors add up).  delta: [batch, D]
+    (or [D]); B, C: [batch, N].  Returns y."""
     import torch
     if u.dim() != 2:
         raise ValueError("u must be [batch, D] (one token per batch row)")
@@ -898,8 +901,8 @@ def selective_scan_step_cached(u, delta, A, B, C, Dskip=None, z=None, y=None, *,
 
 def selective_scan_ssd_step_cached(x, delta, A, B, C, Dskip=None, z=None, y=None, *, q, scale, read_slots=None,
                                    write_slots=None, seed=None, discretization: str = "zoh", stream=None):
-    """One token of the scalar-decay layer with the states in an 8-bit cache (slots, seed and
-    padding as selective_scan_step_cached; state shape (H, 64, N)).  x, z, y: [batch, H, 64];
+    """One token of the scalar-decay layer with the states in an 8-bit cache (slots, padding and a
+    seed to be changed before every token as selective_scan_step_cached; state shape (H, 64, N)).  x, z, y: [batch, H, 64];
     delta: [batch, H]; B, C: [batch, N], bfloat16 and contiguous; A: [H], Dskip: [H * 64]
     float32.  Returns y."""
     import torch
