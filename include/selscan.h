@@ -511,10 +511,10 @@ typedef struct selscan_cache_dims {
 /*
  * state_cache_write -- store `count` states (state: [count][elems] fp32, e.g. a last_state) in
  * the slots that slot_ids names (rows that name no slot are skipped).  seed: one int64 in device
- * memory, another value at every call, or NULL.  state_cache_read -- the values of `count` slots into out ([count][elems],
- * out_dtype an enum selscan_dtype; zeros for an id that names no slot).  In a read, ids may
- * repeat.  count * rows must be below 2^32 and count * ceil(elems / 256) below 2^24.  Neither
- * allocates.
+ * memory, another value at every call, or NULL.  state_cache_read -- the values of `count` slots
+ * into out ([count][elems], out_dtype an enum selscan_dtype; zeros for an id that names no slot).
+ * In a read, ids may repeat.  count * rows must be below 2^32 and count * ceil(elems / 256) below
+ * 2^24.  Neither allocates.
  */
 int state_cache_write(const float* state, const int32_t* slot_ids, int64_t count, int8_t* q, float* scale,
                       const int64_t* seed, const selscan_cache_dims* cache, void* stream);

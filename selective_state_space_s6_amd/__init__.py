@@ -902,9 +902,9 @@ def selective_scan_step_cached(u, delta, A, B, C, Dskip=None, z=None, y=None, *,
 def selective_scan_ssd_step_cached(x, delta, A, B, C, Dskip=None, z=None, y=None, *, q, scale, read_slots=None,
                                    write_slots=None, seed=None, discretization: str = "zoh", stream=None):
     """One token of the scalar-decay layer with the states in an 8-bit cache (slots, padding and a
-    seed to be changed before every token as selective_scan_step_cached; state shape (H, 64, N)).  x, z, y: [batch, H, 64];
-    delta: [batch, H]; B, C: [batch, N], bfloat16 and contiguous; A: [H], Dskip: [H * 64]
-    float32.  Returns y."""
+    seed to be changed before every token as selective_scan_step_cached; state shape
+    (H, 64, N)).  x, z, y: [batch, H, 64]; delta: [batch, H]; B, C: [batch, N], bfloat16 and
+    contiguous; A: [H], Dskip: [H * 64] float32.  Returns y."""
     import torch
     if x.dim() != 3:
         raise ValueError("x must be [batch, H, 64] (one token per batch row)")

@@ -138,10 +138,10 @@ __device__ __forceinline__ float code_value(uint32_t w, int j) {
 }
 
 // Writing: four values a lane, L lanes a row, whole lines in and out; a workgroup stays within one
-// state, so its slot and the division for it are scalar.  256 states of 2560 x 16 (55 MB): 11.4 us,
-// 4.8 TB/s (with a vector division for every lane's state 12.4, in 64 bits 14.1).  WORDS: rows of
-// whole fours, codes on 4-byte and states on 16-byte boundaries; 1024 states take 36.3 us, value
-// by value 48.6.
+// state, so its slot and the division for it are scalar.  256 states of 2560 x 16 (55 MB): 11.2 us,
+// 4.9 TB/s, seeded 11.8 (with a vector division for every lane's state 12.4, in 64 bits 14.1).
+// WORDS: rows of whole fours, codes on 4-byte and states on 16-byte boundaries; 1024 states take
+// 36.0 us (seeded 37.1), value by value 48.0.
 template <int L, bool WORDS, bool SEEDED>
 __global__ __launch_bounds__(256) void cache_write_kernel(const float* __restrict__ state, CacheParams p) {
   const uint32_t rows = uint32_t(p.rows), len = uint32_t(p.row_len), elems = uint32_t(p.elems);
@@ -252,11 +252,14 @@ __device__ __forceinline__ float silu(float z) {
 // One token of the selective scan.  L lanes a channel, 16 states a lane; B and C of the batch row
 // are staged in LDS.  WORDS: dstate % 4 == 0, codes on 4-byte and rates on 16-byte boundaries; LINES:
 // dstate % 16 == 0, both on 16-byte boundaries (a lane whose states all lie behind the last works
-// on its channel's first rates and zero codes, and stores nothing).  1024 rows x 2560 x 16 in
-// bf16: 43.1 us with LINES, 49.8 with WORDS, 144 value by value.
+// on its channel's first rates and zero codes, and stores nothing).  512 rows x 2560 x 16
+// and x 64 in bf16, seeded: 22.8 and 69.6 us with LINES, 24.4 and 77.8 with WORDS; 1024 rows x
+// 16 on other values: 44 with either, 143 value by value.
 // Some 27 vector instructions a state (decay, input coefficient, readout, rounding; two of them at
-// a quarter of the rate) stand against 2 bytes of codes: 512 rows (63 MB) take 23.3 us, 16 of
-// which the instructions fill and 11 the bytes.  Walking two batch rows with a channel's rates
+// a quarter of the rate) stand against 2 bytes of codes: 512 rows (63 MB) take 23.6 us in bf16 and
+// 22.8 in fp32, 16 of which the instructions fill and 11 the bytes; rounded to nearest 21.0 and
+// 20.1.  A workgroup loads, waits and works once, so only others on the unit fill its wait:
+// that is taken to be the rest.  Walking two batch rows with a channel's rates
 // kept in registers measured the same, four slower (three wavefronts a SIMD).
 template <typename IO, int L, bool WORDS, bool LINES, bool SEEDED>
 __global__ __launch_bounds__(256) void step_cached_kernel(StepParams s, CacheParams p) {
@@ -385,9 +388,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* p, int64_t n)
 // lane; a workgroup walks `passes` groups of rows of one batch row, whose B and C stay in
 // registers.  A group lies within one head.  All of a batch row is reached through views whose
 // ends stand for its bounds, at offsets of which only a scalar part changes from group to group.
-// LINES: the codes on 16-byte boundaries (128 rows: 42.2 us), else byte by byte (150).
-// 64 rows x 80 heads x 64 x 128 (88 MB): 24.1 us, 17 of which the instructions fill (16 a state)
-// and 15 the bytes; with 64-bit addresses and branches at the bounds 26.2.
+// LINES: the codes on 16-byte boundaries (128 rows: 42.0 us), else byte by byte (150).
+// 64 rows x 80 heads x 64 x 128 (88 MB): 23.6 us, 17 of which the instructions fill (16 a state,
+// the coefficient formed once a row) and 15 the bytes; to nearest 18.0, 64 states 14.3.  With
+// 64-bit addresses and branches at the bounds it took 26.2.
 template <int N, bool LINES, bool SEEDED>
 __global__ __launch_bounds__(256) void ssd_step_cached_kernel(SsdParams s, CacheParams p, int passes) {
   using T = io_traits<uint16_t>;

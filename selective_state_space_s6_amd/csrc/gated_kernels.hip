@@ -249,11 +249,14 @@ __device__ __forceinline__ void run_states(const float (&a)[S], float (&b)[S], u
 // Four tensors pass through HBM once: 4 x 16384 tokens x 2560 channels in bf16 are 1342 MB and take
 // 270 us, 5.0 TB/s where a large copy reaches 5.9.  Without the links (and so with wrong
 // states) it is 250, without the arithmetic 246: bytes, arithmetic (55 % of the vector
-// instructions' slots) and the exchange hide one another but for some 10 % each.  128 tokens
-// of bf16 a chunk, 64 of fp32, are what two chunks' raw inputs leave room for (64 of bf16:
-// twice the links, slower; two chunks ahead: spills, 314).  Workgroups of 64 channels and four
-// wavefronts, three a compute unit, took 294 against 281 here, and 32 against 25 in fp32.
-// One wavefront that reads all links for the others: 347.
+// instructions' slots) and the exchange hide one another but for some 10 % each.  One, two and
+// four sequences take 102, 171 and 277 a call: up to 65 us of it do not shrink with the bytes
+// (start, drain, the clearing launch, links between chunks in work at once; not told apart).
+// 128 tokens of bf16 a chunk, 64 of fp32, are what two chunks' raw inputs leave room for.
+// Measured against a state of this kernel that took 281 (25 at 3 x 1537 x 771 in fp32): chunks
+// of 64 tokens in bf16, twice the links, slower; two chunks ahead, which spills, 314;
+// workgroups of 64 channels and four wavefronts, three a compute unit, 294 (32); one wavefront
+// that reads all links for the others, 347.
 template <typename IO, int NW, int S, int VEC, bool RESET>
 __global__ __launch_bounds__(NW * 64) void gated_fwd_kernel(GatedParams p) {
   using T = pair_io<IO>;
@@ -484,13 +487,16 @@ __global__ __launch_bounds__(256) void gated_begin_kernel(ulonglong2* links, int
 // is G -> a (G + dy): the same kind as the forward pass's, joined in the same way along the
 // reversed sequence.  The states are formed again from the chunk's checkpoint.  The gates'
 // sigmoids are computed twice, before the exchange of maps (the decays stay in registers)
-// and after it: keeping them would halve the wavefronts that a compute unit holds.
+// and after it: keeping them takes 32 registers, which fp32 (236 of 256 at its two wavefronts a
+// SIMD) has not and bf16 (204) has; that is not built.
 //
 // Seven tensors pass through HBM once: 4 x 4096 x 2560 in bf16 are 587 MB and take 184 us,
-// 3.2 TB/s.  The loads alone take 113 and the arithmetic fills 55 % of its slots: the
-// three phases of a chunk (map, wait, gradients) follow one another with one workgroup on a
-// compute unit, since the raw inputs of two chunks fill its registers.  Workgroups of half as
-// many channels, three a compute unit, took 183; in fp32 42 against 38.
+// 3.2 TB/s.  The loads alone take 113 and the arithmetic fills 55 % of its slots, 84 vector
+// instructions an element of which ten are transcendental, four of those the sigmoids formed
+// again.  The three phases of a chunk (map, wait, gradients) follow one another with one
+// workgroup on a compute unit, since the raw inputs of two chunks fill its registers; but
+// workgroups of half as many channels, three a compute unit, took 183 (in fp32 42 against 38),
+// so the phases alone are not what it waits for.
 template <typename IO, int NW, int S, int VEC, bool RESET>
 __global__ __launch_bounds__(NW * 64) void gated_bwd_kernel(GatedParams p) {
   using T = pair_io<IO>;

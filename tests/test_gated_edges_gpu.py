@@ -33,6 +33,7 @@ def bwd_by_sequences(i, cut):
     return dict({k: np.concatenate([one[k], two[k]], 1) for k in ("dx", "dr", "dg")}, dinitial_state=one["dinitial_state"])
 
 
+@pytest.mark.filterwarnings("ignore::RuntimeWarning")
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("size", [(2, 40, 70), (2, 700, 70), (2, 3001, 71)])
 @pytest.mark.parametrize("cut", [False, True])
