@@ -547,6 +547,152 @@ int selective_scan_ssd_step_cached(const void* x, const void* delta, const float
                                    const int32_t* read_slots, const int32_t* write_slots, const int64_t* seed,
                                    const selscan_ssd_dims* dims, const selscan_cache_dims* cache, void* stream);
 
+/*
+ * Linear attention with a decay for each head.  Per (batch row, head), with a K x V state,
+ *     a_t = exp(log_decay_t),   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t.
+ * It is the scalar-decay layer's recurrence with queries and keys of their own for each head
+ * (or for groups of heads: head h reads query and key head h / (nheads / qk_heads)), any widths,
+ * either I/O type, and the decay given by its logarithm: one per head, or one per token and head.
+ * A log decay is normally <= 0.  Where it is -infinity (or its decay below 2^-150) the state
+ * starts anew: nothing before that token reaches it or is reached by its gradient, not even
+ * an infinity or a NaN, so packed documents and padding on the left are told apart by it.  (Padding
+ * on the right that is to leave the last state as it is: k = 0 and log decay 0.)  A token that is
+ * not finite makes what depends on it so, and nothing else; such chunks are walked token by
+ * token, far more slowly.
+ */
+typedef struct selscan_linattn_dims {
+  int32_t abi_version;     /* SELSCAN_ABI_VERSION */
+  int32_t io_dtype;        /* enum selscan_dtype: q, k, v, o (and do, dq, dk, dv) */
+  int64_t batch;           /* >= 0 */
+  int64_t seqlen;          /* >= 0 */
+  int64_t nheads;          /* H >= 1: heads of v and o */
+  int64_t qk_heads;        /* heads of q and k, a divisor of nheads */
+  int64_t dk;              /* K: 1 .. 256 */
+  int64_t dv;              /* V: 1 .. 256 */
+  int64_t q_sb, q_sl, q_sh;   /* strides in elements between batch rows, tokens and heads; the last */
+  int64_t k_sb, k_sl, k_sh;   /* axis is unit-stride.  Token strides at most 2^22, not used where */
+  int64_t v_sb, v_sl, v_sh;   /* seqlen is 1 */
+  int64_t o_sb, o_sl, o_sh;   /* o of the forward, do of the backward */
+  int64_t g_sb, g_sl, g_sh;   /* log_decay (decay_tokens 0: g_sh only) */
+  int32_t decay_tokens;    /* 1: log_decay per token and head; 0: [nheads], the same for every token */
+  float scale;             /* of o; finite */
+} selscan_linattn_dims;
+
+/* Fill *dims for contiguous q, k [batch][seqlen][qk_heads][dk], v, o [batch][seqlen][nheads][dv] and
+ * log_decay [batch][seqlen][nheads]; decay_tokens = 1, scale = 1.  Never fails for a non-NULL dims. */
+void linear_attention_dims_init(selscan_linattn_dims* dims, int io_dtype, int64_t batch, int64_t seqlen,
+                                int64_t nheads, int64_t qk_heads, int64_t dk, int64_t dv);
+
+/*
+ * linear_attention_fwd -- enqueue the layer: matrix products inside chunks of tokens on the matrix
+ * cores, a state carried between them, long sequences of few heads split into segments.
+ *   q, k, v        : inputs in dims->io_dtype; their rows may overlap (strides of 0)
+ *   log_decay      : fp32
+ *   o              : output in dims->io_dtype; its rows must not overlap (else SELSCAN_ERR_UNSUPPORTED),
+ *                    in whichever order its axes lie
+ *   initial_state, last_state : [batch][nheads][dk][dv] fp32, or NULL (zero / not written).  They
+ *                    may be one buffer.
+ *   workspace      : linear_attention_workspace_size(dims) bytes, 256-byte aligned, or NULL to take it
+ *                    stream-ordered on `stream`.  Not to be used by other work until the enqueued
+ *                    call has finished (two captured graphs that may run at once need one each).
+ * Products are formed of the inputs as they are and summed in fp32.  With bf16 I/O the pairs of a
+ * chunk are rounded to bf16 before they meet v, the state keeps 16 bits of mantissa where it
+ * meets q and 24 where it is carried.
+ * batch * nheads * ceil(dv / 64) must be below 2^22.  Pointers and status codes otherwise as
+ * selective_scan_fwd; seqlen == 0 hands the initial state (zeros if NULL) to last_state.
+ */
+int linear_attention_fwd(const void* q, const void* k, const void* v, const float* log_decay, void* o,
+                         const float* initial_state, float* last_state, const selscan_linattn_dims* dims,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of linear_attention_fwd (0 for an empty call, invalid dims or a sequence that is not
+ * split into segments). */
+size_t linear_attention_workspace_size(const selscan_linattn_dims* dims);
+
+/*
+ * linear_attention_bwd -- gradients of linear_attention_fwd (same inputs and options), given do
+ * (`d_o`, strides o_sb, o_sl, o_sh) and optionally dlast_state.
+ *   dq, dk         : [batch][seqlen][qk_heads][dk] contiguous in dims->io_dtype (summed over the heads
+ *                    that share them)
+ *   dv             : [batch][seqlen][nheads][dv] contiguous in dims->io_dtype
+ *   dlog_decay     : fp32, [batch][seqlen][nheads] contiguous, or [nheads] where decay_tokens is 0;
+ *                    or NULL.  Zero where the state starts anew.
+ *   dinitial_state : [batch][nheads][dk][dv] fp32, or NULL; it and dlast_state may be one buffer
+ *   workspace      : linear_attention_bwd_workspace_size(dims, dlog_decay != NULL) bytes, as above
+ * All outputs are written, never accumulated into; sums run in a fixed order.
+ */
+int linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                         const float* initial_state, const void* d_o, const float* dlast_state, void* dq, void* dk,
+                         void* dv, float* dlog_decay, float* dinitial_state, const selscan_linattn_dims* dims,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t linear_attention_bwd_workspace_size(const selscan_linattn_dims* dims, int want_dlog_decay);
+
+/*
+ * linear_attention_step -- one token per batch row (dims->seqlen must be 1; token strides are not
+ * used), states [slots][nheads][dk][dv] fp32.  Batch row b starts from the state in slot read_slots[b]
+ * (zero where that names no slot: a sequence's first token) and stores the new one in slot
+ * write_slots[b].  Ids are int32 device arrays; NULL stands for 0, 1, 2, ..., so with neither
+ * the states are updated in place.  An id that is negative, or not below `slots`, names no slot; a
+ * row whose write id names none is padding: it is skipped, its o is left as it was.  Ids of rows
+ * that are written must differ from one another, and a slot that one row writes must not be read by
+ * another row of the same call.  o is formed from the new state.  Never allocates.
+ */
+int linear_attention_step(const void* q, const void* k, const void* v, const float* log_decay, void* o, float* state,
+                          int64_t slots, const int32_t* read_slots, const int32_t* write_slots,
+                          const selscan_linattn_dims* dims, void* stream);
+
+/*
+ * Group norm with an activation: the output stage of a layer whose heads are normalised each for
+ * itself.  Channels last; the statistics are those of one token's group of dim / groups consecutive
+ * channels (so a token's result depends on that token alone, and decoding gives what the whole
+ * sequence gave):
+ *     n = (x - mean) / sqrt(var + eps) * weight + bias
+ *     y = act(n) without a gate,   y = n * act(z) with one;     act(t) = t sigmoid(t) (silu), or t
+ * var is the mean of the squared deviations, formed in fp32 (from |x| of about 1e19 on it overflows).
+ */
+enum selscan_activation { SELSCAN_ACT_NONE = 0, SELSCAN_ACT_SILU = 1 };
+
+typedef struct selscan_norm_dims {
+  int32_t abi_version;     /* SELSCAN_ABI_VERSION */
+  int32_t io_dtype;        /* enum selscan_dtype: x, z, y (and dy, dx, dz) */
+  int64_t batch;           /* >= 0 */
+  int64_t seqlen;          /* >= 0 */
+  int64_t dim;             /* C >= 1, a multiple of groups, at most 2^20 */
+  int64_t groups;          /* >= 1; dim / groups at most 8192 */
+  int64_t x_sb, x_sl;      /* strides in elements (unit stride over channels); token strides are */
+  int64_t z_sb, z_sl;      /* not used where seqlen is 1 */
+  int64_t y_sb, y_sl;      /* y of the forward, dy of the backward */
+  float eps;               /* finite and > 0 */
+  int32_t activation;      /* enum selscan_activation */
+} selscan_norm_dims;
+
+/* Fill *dims for contiguous x, z, y [batch][seqlen][dim]; eps = 1e-5, activation = SELSCAN_ACT_SILU.
+ * Never fails for a non-NULL dims. */
+void group_norm_dims_init(selscan_norm_dims* dims, int io_dtype, int64_t batch, int64_t seqlen, int64_t dim,
+                          int64_t groups);
+
+/*
+ * group_norm_fwd -- x, z (or NULL: no gate), y in dims->io_dtype; weight, bias: [dim] fp32, or NULL
+ * (ones, zeros).  y may be x or z themselves (same strides); its rows must not overlap otherwise
+ * (else SELSCAN_ERR_UNSUPPORTED).  batch * seqlen * groups must be below 2^31 and the call's
+ * threads below 2^32.  Never allocates.  Status codes as selective_scan_fwd.
+ */
+int group_norm_fwd(const void* x, const float* weight, const float* bias, const void* z, void* y,
+                   const selscan_norm_dims* dims, void* stream);
+
+/*
+ * group_norm_bwd -- gradients of group_norm_fwd (same inputs and options), given dy (strides y_sb,
+ * y_sl).  The statistics are formed again from x.
+ *   dx, dz         : [batch][seqlen][dim] contiguous in dims->io_dtype (dz with a gate only, else NULL)
+ *   dweight, dbias : [dim] fp32, or NULL; written, summed in a fixed order
+ *   workspace      : group_norm_bwd_workspace_size(dims) bytes, 256-byte aligned (not needed where neither
+ *                    dweight nor dbias is wanted), or NULL to take it stream-ordered on `stream`
+ */
+int group_norm_bwd(const void* x, const float* weight, const float* bias, const void* z, const void* dy, void* dx,
+                   float* dweight, float* dbias, void* dz, const selscan_norm_dims* dims, void* workspace,
+                   size_t workspace_bytes, void* stream);
+size_t group_norm_bwd_workspace_size(const selscan_norm_dims* dims);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* selective_scan_strerror(int status);
 

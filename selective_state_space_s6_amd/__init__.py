@@ -93,6 +93,16 @@ _SIGNATURES = [
     ("state_cache_read", ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int64, _VP, ctypes.c_int, _VP, _VP]),
     ("selective_scan_step_cached", ctypes.c_int, [_VP] * 17),
     ("selective_scan_ssd_step_cached", ctypes.c_int, [_VP] * 16),
+    ("linear_attention_dims_init", None, [_VP, ctypes.c_int] + [ctypes.c_int64] * 6),
+    ("linear_attention_fwd", ctypes.c_int, [_VP] * 7 + [_VP, _VP, ctypes.c_size_t, _VP]),
+    ("linear_attention_workspace_size", ctypes.c_size_t, [_VP]),
+    ("linear_attention_bwd", ctypes.c_int, [_VP] * 12 + [_VP, _VP, ctypes.c_size_t, _VP]),
+    ("linear_attention_bwd_workspace_size", ctypes.c_size_t, [_VP, ctypes.c_int]),
+    ("linear_attention_step", ctypes.c_int, [_VP] * 6 + [ctypes.c_int64, _VP, _VP, _VP, _VP]),
+    ("group_norm_dims_init", None, [_VP, ctypes.c_int] + [ctypes.c_int64] * 4),
+    ("group_norm_fwd", ctypes.c_int, [_VP] * 7),
+    ("group_norm_bwd", ctypes.c_int, [_VP] * 9 + [_VP, _VP, ctypes.c_size_t, _VP]),
+    ("group_norm_bwd_workspace_size", ctypes.c_size_t, [_VP]),
     ("selective_scan_strerror", ctypes.c_char_p, [ctypes.c_int]),
     ("selective_scan_last_hip_error", ctypes.c_int, []),
     ("selective_scan_abi_version", ctypes.c_int, []),
@@ -932,9 +942,206 @@ def selective_scan_ssd_step_cached(x, delta, A, B, C, Dskip=None, z=None, y=None
     return y
 
 
+class LinattnDims(ctypes.Structure):
+    """Mirror of ``selscan_linattn_dims`` in include/selscan.h."""
+    _fields_ = ([("abi_version", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+                + [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "qk_heads", "dk", "dv",
+                                                 "q_sb", "q_sl", "q_sh", "k_sb", "k_sl", "k_sh", "v_sb", "v_sl", "v_sh",
+                                                 "o_sb", "o_sl", "o_sh", "g_sb", "g_sl", "g_sh")]
+                + [("decay_tokens", ctypes.c_int32), ("scale", ctypes.c_float)])
+
+
+class NormDims(ctypes.Structure):
+    """Mirror of ``selscan_norm_dims`` in include/selscan.h."""
+    _fields_ = ([("abi_version", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+                + [(n, ctypes.c_int64) for n in ("batch", "seqlen", "dim", "groups", "x_sb", "x_sl", "z_sb", "z_sl",
+                                                 "y_sb", "y_sl")]
+                + [("eps", ctypes.c_float), ("activation", ctypes.c_int32)])
+
+
+ACTIVATIONS = {"none": 0, "silu": 1}
+
+
+def _linattn_dims(on, q, k, v, log_decay, o, scale, step=False):
+    """selscan_linattn_dims of [batch, L, heads, width] tensors (a step: [batch, heads, width])."""
+    import torch
+    io, lead = q.dtype, q.shape[:-2]
+    Hk, K = q.shape[-2:]
+    H, V = v.shape[-2:]
+    if Hk == 0 or H % Hk:
+        raise ValueError("the heads of v (%d) must be a multiple of those of q and k (%d)" % (H, Hk))
+    batch, L = (lead[0], 1) if step else lead
+    strides = []
+    for name, t, shape in (("q", q, lead + (Hk, K)), ("k", k, lead + (Hk, K)), ("v", v, lead + (H, V)), ("o", o, lead + (H, V))):
+        on.check(name, t, io, shape, contiguous=False)
+        s = t.stride()
+        if s[-1] != 1 and shape[-1] > 1:
+            raise ValueError("%s: the last axis must be unit-stride" % name)
+        strides += (s[0], 0, s[1]) if step else (s[0], s[1] if L > 1 else 0, s[2])      # (one token: any stride)
+    tokens = log_decay.dim() > 1
+    on.check("log_decay", log_decay, torch.float32, lead + (H,) if tokens else (H,), contiguous=False)
+    g = log_decay.stride()
+    g = (0, 0, g[0]) if not tokens else (g[0], 0, g[1]) if step else g
+    return LinattnDims(SELSCAN_ABI_VERSION, _io_code(io), batch, L, H, Hk, K, V, *strides, *g, 1 if tokens else 0, scale)
+
+
+def linear_attention_fwd(q, k, v, log_decay, *, scale: float = 1.0, o=None, initial_state=None, last_state=None,
+                         return_last_state: bool = False, workspace=None, stream=None):
+    """Linear attention with a decay for each head: S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T,
+    o_t = scale q_t^T S_t.  Returns (o, last_state or None).
+
+    q, k: [batch, L, Hk, K]; v, o: [batch, L, H, V], float32 or bfloat16 with unit-stride last
+    axes, K and V up to 256; head h reads query and key head h // (H / Hk).  log_decay: [H] or
+    [batch, L, H] float32 (any strides), -inf where the state starts anew (packed documents).
+    initial_state, last_state: [batch, H, K, V] float32.  ``workspace`` is taken from torch's
+    caching allocator when omitted."""
+    import torch
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must be [batch, L, heads, width]")
+    with _On(q, stream) as on:
+        if o is None:
+            o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        dims = _linattn_dims(on, q, k, v, log_decay, o, scale)
+        states = (dims.batch, dims.nheads, dims.dk, dims.dv)
+        if last_state is None and return_last_state:
+            last_state = torch.empty(states, dtype=torch.float32, device=q.device)
+        on.check("initial_state", initial_state, torch.float32, states)
+        on.check("last_state", last_state, torch.float32, states)
+        ref = ctypes.byref(dims)
+        keep, ws, nbytes = on.workspace(workspace, lib().linear_attention_workspace_size(ref))
+        st = lib().linear_attention_fwd(_p(q), _p(k), _p(v), _p(log_decay), _p(o), _p(initial_state), _p(last_state), ref,
+                                        ws, nbytes, on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "linear_attention_fwd")
+    return o, last_state
+
+
+def linear_attention_bwd(q, k, v, log_decay, *, do, scale: float = 1.0, initial_state=None, dlast_state=None,
+                         decay_grad: bool = True, workspace=None, stream=None) -> dict:
+    """Gradients of linear_attention_fwd (same inputs and options) given do ([batch, L, H, V]) and
+    optionally dlast_state.  Returns a dict of contiguous tensors: dq, dk, dv in q's dtype; dlog_decay
+    (unless decay_grad is False) in log_decay's shape and, with an initial_state, dinitial_state in
+    float32."""
+    import torch
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must be [batch, L, heads, width]")
+    with _On(q, stream) as on:
+        dims = _linattn_dims(on, q, k, v, log_decay, do, scale)
+        states = (dims.batch, dims.nheads, dims.dk, dims.dv)
+        on.check("initial_state", initial_state, torch.float32, states)
+        on.check("dlast_state", dlast_state, torch.float32, states)
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=q.device)      # noqa: E731
+        out = {"dq": new(q.shape, q.dtype), "dk": new(q.shape, q.dtype), "dv": new(v.shape, q.dtype)}
+        if decay_grad:
+            out["dlog_decay"] = new(log_decay.shape, torch.float32)
+        if initial_state is not None:
+            out["dinitial_state"] = new(states, torch.float32)
+        ref = ctypes.byref(dims)
+        keep, ws, nbytes = on.workspace(workspace, lib().linear_attention_bwd_workspace_size(ref, 1 if decay_grad else 0))
+        st = lib().linear_attention_bwd(_p(q), _p(k), _p(v), _p(log_decay), _p(initial_state), _p(do), _p(dlast_state),
+                                        _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _p(out.get("dlog_decay")),
+                                        _p(out.get("dinitial_state")), ref, ws, nbytes, on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "linear_attention_bwd")
+    return out
+
+
+def linear_attention_step(q, k, v, log_decay, *, state, scale: float = 1.0, o=None, read_slots=None, write_slots=None,
+                          stream=None):
+    """One token of linear attention per batch row.  q, k: [batch, Hk, K]; v, o: [batch, H, V];
+    log_decay: [H] or [batch, H]; state: [slots, H, K, V] float32, contiguous.  Without ids row b's
+    state is slot b, updated in place; with them ([batch] int32) row b starts from slot read_slots[b]
+    (the zero state where the id is outside) and stores the new state in slot write_slots[b]; rows
+    whose write id is outside are padding and keep their o.  A slot that a row writes may be read
+    by that row alone.  Returns o."""
+    import torch
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must be [batch, heads, width] (one token per batch row)")
+    with _On(q, stream) as on:
+        if o is None:
+            o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        dims = _linattn_dims(on, q, k, v, log_decay, o, scale, step=True)
+        slots = state.shape[0]
+        on.check("state", state, torch.float32, (slots, dims.nheads, dims.dk, dims.dv))
+        on.check("read_slots", read_slots, torch.int32, (dims.batch,))
+        on.check("write_slots", write_slots, torch.int32, (dims.batch,))
+        st = lib().linear_attention_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), o.data_ptr(),
+                                         state.data_ptr(), slots, _p(read_slots), _p(write_slots), ctypes.byref(dims),
+                                         on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "linear_attention_step")
+    return o
+
+
+def _norm_dims(on, x, weight, bias, z, y, groups, eps, activation):
+    """selscan_norm_dims of [batch, L, C] or [rows, C] tensors with unit-stride channels."""
+    import torch
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [batch, L, C] or [rows, C]")
+    io, shape, strides = x.dtype, x.shape, []
+    for name, t in (("x", x), ("z", z), ("y", y)):
+        if t is None:
+            strides += (0, 0)
+            continue
+        on.check(name, t, io, shape, contiguous=False)
+        s = t.stride()
+        if s[-1] != 1 and shape[-1] > 1:
+            raise ValueError("%s: the channel axis must be unit-stride" % name)
+        strides += (0, s[0]) if len(s) == 2 else s[:2]
+    C = shape[-1]
+    on.check("weight", weight, torch.float32, (C,))
+    on.check("bias", bias, torch.float32, (C,))
+    batch, L = (1, shape[0]) if len(shape) == 2 else shape[:2]
+    return NormDims(SELSCAN_ABI_VERSION, _io_code(io), batch, L, C, groups, *strides, eps, ACTIVATIONS[activation])
+
+
+def group_norm_fwd(x, weight=None, bias=None, z=None, *, groups: int, eps: float = 1e-5, activation: str = "silu", y=None,
+                   stream=None):
+    """Group norm with an activation, channels last: each token's groups of C / groups channels are
+    normalised for themselves, n = (x - mean) / sqrt(var + eps) * weight + bias; y = act(n), or with a
+    gate z  y = n * act(z).  Returns y.
+
+    x, z, y: [batch, L, C] or [rows, C] float32 or bfloat16 (unit-stride channels; y may be x or z);
+    weight, bias: [C] float32 or None; activation: "silu" or "none"."""
+    with _On(x, stream) as on:
+        if y is None:
+            y = x.new_empty(x.shape)
+        dims = _norm_dims(on, x, weight, bias, z, y, groups, eps, activation)
+        st = lib().group_norm_fwd(_p(x), _p(weight), _p(bias), _p(z), _p(y), ctypes.byref(dims), on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "group_norm_fwd")
+    return y
+
+
+def group_norm_bwd(x, weight=None, bias=None, z=None, *, dy, groups: int, eps: float = 1e-5, activation: str = "silu",
+                   workspace=None, stream=None) -> dict:
+    """Gradients of group_norm_fwd (same inputs and options) given dy.  Returns a dict: dx and (with a
+    gate) dz, contiguous in x's dtype; dweight, dbias [C] float32 where weight and bias were given."""
+    import torch
+    with _On(x, stream) as on:
+        dims = _norm_dims(on, x, weight, bias, z, dy, groups, eps, activation)
+        C = (x.shape[-1],)
+        out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device)}
+        if z is not None:
+            out["dz"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        for name, t in (("dweight", weight), ("dbias", bias)):
+            if t is not None:
+                out[name] = torch.empty(C, dtype=torch.float32, device=x.device)
+        ref = ctypes.byref(dims)
+        need = lib().group_norm_bwd_workspace_size(ref) if weight is not None or bias is not None else 0
+        keep, ws, nbytes = on.workspace(workspace, need)
+        st = lib().group_norm_bwd(_p(x), _p(weight), _p(bias), _p(z), _p(dy), _p(out["dx"]), _p(out.get("dweight")),
+                                  _p(out.get("dbias")), _p(out.get("dz")), ref, ws, nbytes, on.handle)
+        if st != SELSCAN_OK:
+            raise SelscanError(st, "group_norm_bwd")
+    return out
+
+
 __all__ = ["selective_scan_fwd", "selective_scan_step", "selective_scan_bwd", "bwd_workspace_size",
            "selective_scan_ssd_fwd", "ssd_dims", "ssd_workspace_size", "SsdDims",
            "gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "gated_checkpoints", "GatedDims", "GATED_TILE",
            "state_cache", "state_cache_write", "state_cache_read", "CacheDims", "CACHE_ROW",
+           "linear_attention_fwd", "linear_attention_bwd", "linear_attention_step", "LinattnDims",
+           "group_norm_fwd", "group_norm_bwd", "NormDims", "ACTIVATIONS",
            "selective_scan_step_cached", "selective_scan_ssd_step_cached", "make_dims", "dims_init", "workspace_size", "strerror", "last_hip_error",
            "abi_version", "lib", "SelscanDims", "SelscanError", "LIB_PATH"]

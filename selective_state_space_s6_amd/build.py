@@ -21,9 +21,12 @@ MICROBENCH_LIB = os.path.join(PKG, "libselscan_microbench.so")
 # own (scan_inst_*.hip), which compile in parallel
 SCAN_UNITS = [os.path.join(CSRC, "scan_inst_%s_%s.hip" % (io, ps))
               for io in ("f32", "bf16") for ps in ("single", "state", "apply")]
-SOURCES = SCAN_UNITS + [os.path.join(CSRC, "bwd_kernels.hip"), os.path.join(CSRC, "bwd_ti_kernels.hip"), os.path.join(CSRC, "scan_kernels.hip"),
+# the linear-attention walk likewise, per element type and width of q and k
+LIN_UNITS = [os.path.join(CSRC, "linattn_inst_%s_%d.hip" % (io, kd)) for io in ("f32", "bf16") for kd in (64, 128, 256)]
+SOURCES = SCAN_UNITS + LIN_UNITS + [os.path.join(CSRC, "bwd_kernels.hip"), os.path.join(CSRC, "bwd_ti_kernels.hip"), os.path.join(CSRC, "scan_kernels.hip"),
                         os.path.join(CSRC, "conv_kernels.hip"), os.path.join(CSRC, "ssd_kernels.hip"),
                         os.path.join(CSRC, "gated_kernels.hip"), os.path.join(CSRC, "cache_kernels.hip"),
+                        os.path.join(CSRC, "linattn_kernels.hip"), os.path.join(CSRC, "norm_kernels.hip"),
                         os.path.join(CSRC, "selscan_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

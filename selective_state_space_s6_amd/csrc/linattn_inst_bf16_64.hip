@@ -1,0 +1,13 @@
+// One instantiation unit of the linear-attention walk (linattn_kernels.h): bf16 I/O, q and k
+// of at most 64 channels.  Units compile in parallel.
+#include "linattn_kernels.h"
+
+namespace selscan {
+
+hipError_t launch_lin_bf16_64(bool rev, bool state, const LinParams& p, hipStream_t stream) {
+  if (p.vd <= 64)
+    return p.parts == 3 ? lin_dispatch<uint16_t, 64, 1, 3>(rev, state, p, stream) : lin_dispatch<uint16_t, 64, 1, 2>(rev, state, p, stream);
+  return p.parts == 3 ? lin_dispatch<uint16_t, 64, 2, 3>(rev, state, p, stream) : lin_dispatch<uint16_t, 64, 2, 2>(rev, state, p, stream);
+}
+
+}  // namespace selscan

@@ -1,0 +1,11 @@
+// One instantiation unit of the linear-attention walk (linattn_kernels.h): fp32 I/O, q and k
+// of at most 128 channels.  Units compile in parallel.
+#include "linattn_kernels.h"
+
+namespace selscan {
+
+hipError_t launch_lin_f32_128(bool rev, bool state, const LinParams& p, hipStream_t stream) {
+  return p.vd <= 64 ? lin_dispatch<float, 128, 1, 1>(rev, state, p, stream) : lin_dispatch<float, 128, 2, 1>(rev, state, p, stream);
+}
+
+}  // namespace selscan

@@ -1,0 +1,244 @@
+// linattn_kernels.hip -- linear attention: what surrounds the chunk walk of linattn_kernels.h (the
+// states that enter the segments, sums over shared heads, the decays' gradient) and the decode step.
+#include <hip/hip_runtime.h>
+
+#include "device_common.h"
+#include "scan_launch.h"
+
+namespace selscan {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+
+// Segment states, from zero, into the states that enter the segments, in place: s := e^c s + own.
+template <bool REV>
+__global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams p, int KD, int NT) {
+  const int block = KD * 64 * NT, at = (blockIdx.x % (block / 1024)) * 1024 + threadIdx.x * 4;
+  const int64_t item = blockIdx.x / (block / 1024), bh = item / p.nblk;
+  const int nb = int(item % p.nblk);
+  // the place in the walk's layout: [a][u][t] by [256 threads][4 rows]
+  const int tid = (at / 4) % 256, t = (at / 1024) % NT, u = (at / 1024 / NT) % 2, a = at / 1024 / NT / 2;
+  const int l16 = tid & 15, g = (tid & 63) >> 4;
+  const int n = nb * 64 * NT + (tid >> 6) * 16 * NT + 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3);
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (p.s0)
+    for (int r = 0; r < 4; ++r) {
+      const int kd = 32 * a + 8 * g + 4 * u + r;
+      if (kd < p.kd && n < p.vd) s[r] = p.s0[bh * p.kd * p.vd + p.s_row * kd + p.s_col * n];
+    }
+  float* ws = p.seg + item * p.nseg * block + at;
+  for (int i = 0; i < p.nseg; ++i) {
+    const int seg = REV ? p.nseg - 1 - i : i;
+    f32x4* slot = reinterpret_cast<f32x4*>(ws + int64_t(seg) * block);
+    const bool more = i + 1 < p.nseg;             // (nothing was left behind the last segment)
+    const f32x4 own = more ? *slot : s;
+    *slot = s;
+    if (more) {
+      const float d = p.seg_decay[bh * p.nseg + seg];
+      for (int r = 0; r < 4; ++r) s[r] = d < 0.f ? own[r] : fmaf(d, s[r], own[r]);
+    }
+  }
+}
+
+hipError_t lin_walk(bool bf16, bool rev, bool state, const LinParams& p, hipStream_t stream) {
+  switch (lin_kd(p.kd)) {
+    case 64: return bf16 ? launch_lin_bf16_64(rev, state, p, stream) : launch_lin_f32_64(rev, state, p, stream);
+    case 128: return bf16 ? launch_lin_bf16_128(rev, state, p, stream) : launch_lin_f32_128(rev, state, p, stream);
+    default: return bf16 ? launch_lin_bf16_256(rev, state, p, stream) : launch_lin_f32_256(rev, state, p, stream);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* out, int64_t n, int share, int width) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {   // [tokens * shared heads][width]
+    const float* src = part + i / width * share * width + i % width;
+    float s = 0.f;
+    for (int k = 0; k < share; ++k) s += src[int64_t(k) * width];
+    if constexpr (sizeof(T) == 2)
+      out[i] = bf16_rne(s);
+    else
+      out[i] = s;
+  }
+}
+
+__device__ __forceinline__ double block_sum(double v, double* tmp) {
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return tmp[0] + tmp[1] + tmp[2] + tmp[3];
+}
+
+// One workgroup per (batch row, head), 256 tokens at a time from the last.  The sums run in 64 bits: what
+// a token's decay passes is the small difference of what follows it and what precedes it.
+__global__ __launch_bounds__(256) void lin_decay_kernel(LinDecayParams p) {
+  __shared__ double tmp[4];
+  const int64_t bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  double carry = 0.0;
+  if (p.last && p.dlast) {
+    double s = 0.0;
+    for (int64_t i = tid; i < p.state; i += 256) s += double(p.last[bh * p.state + i]) * double(p.dlast[bh * p.state + i]);
+    carry = block_sum(s, tmp);
+  }
+  double sum = 0.0;
+  const int64_t part = p.batch * p.L * p.H;
+  for (int64_t t1 = (p.L + 255) / 256 * 256; t1 > 0; t1 -= 256) {
+    const int64_t t = t1 - 1 - tid;               // thread 0 has the last token
+    double v = 0.0;
+    bool start = false;
+    if (t < p.L) {
+      const int64_t at = (b * p.L + t) * p.H + h;
+      for (int i = 0; i < p.nq; ++i) v += double(p.qdq[i * part + at]);
+      for (int i = 0; i < p.nk; ++i) v -= double(p.kdk[i * part + at]);
+      start = double(p.g[b * p.g_sb + t * p.g_sl + h * p.g_sh]) * 1.4426950408889634 < -150.0;
+    }
+    for (int d = 1; d < 64; d *= 2) {
+      const double o = __shfl_up(v, d);
+      if (lane >= d) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) tmp[wave] = v;
+    __syncthreads();
+    double before = carry;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) before += tmp[w];
+      carry += tmp[w];
+    }
+    v = start ? 0.0 : v + before;
+    if (t < p.L) {
+      if (p.dg) p.dg[(b * p.L + t) * p.H + h] = float(v);
+      sum += v;
+    }
+  }
+  if (p.dg_heads) {
+    sum = block_sum(sum, tmp);
+    if (tid == 0) p.sums[bh] = sum;
+  }
+}
+
+__global__ __launch_bounds__(256) void lin_decay_heads_kernel(const double* sums, float* out, int64_t batch, int64_t H) {
+  const int64_t h = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (h >= H) return;
+  double s = 0.0;
+  for (int64_t b = 0; b < batch; ++b) s += sums[b * H + h];
+  out[h] = float(s);
+}
+
+// One workgroup per (batch row, head): S := a S + k v^T, o = scale q^T S, on a state of [K][V].  A row
+// of the state is taken by `lanes` lanes of 4 columns; the 256 / lanes rows of a pass are summed through LDS.
+template <typename T>
+__global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lanes) {
+  __shared__ float sq[256], sk[256];
+  __shared__ f32x4 part[256];
+  const int64_t b = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  const int64_t src = p.read_slots ? int64_t(p.read_slots[b]) : b, dst = p.write_slots ? int64_t(p.write_slots[b]) : b;
+  if (dst < 0 || dst >= p.slots) return;          // padding
+  const bool from = src >= 0 && src < p.slots;
+  const int tid = threadIdx.x, col = (tid % lanes) * 4, row0 = tid / lanes, rows = 256 / lanes;
+  const int64_t hk = h / p.share;
+  auto at = [](const void* t, int64_t i) { return io_traits<T>::widen(static_cast<const T*>(t)[i]); };
+  if (tid < p.kd) {
+    sq[tid] = at(p.q, b * p.q_sb + hk * p.q_sh + tid) * p.scale;
+    sk[tid] = at(p.k, b * p.k_sb + hk * p.k_sh + tid);
+  }
+  f32x4 v = {0.f, 0.f, 0.f, 0.f}, o = v;
+  for (int e = 0; e < 4; ++e)
+    if (col + e < p.vd) v[e] = at(p.v, b * p.v_sb + h * p.v_sh + col + e);
+  const float lg = p.g[b * p.g_sb + h * p.g_sh];
+  const bool keep = from && !(double(lg) * 1.4426950408889634 < -150.0);
+  const float a = expf(lg);
+  const int64_t block = int64_t(p.kd) * p.vd;
+  const float* s_in = p.state + (src * p.H + h) * block + col;
+  float* s_out = p.state + (dst * p.H + h) * block + col;
+  __syncthreads();
+  for (int r = row0; r < p.kd; r += rows) {
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (keep && col < p.vd) {
+      if (p.vec)
+        s = *reinterpret_cast<const f32x4*>(s_in + int64_t(r) * p.vd);
+      else
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.vd) s[e] = s_in[int64_t(r) * p.vd + e];
+    }
+    const float k = sk[r], q = sq[r];
+    for (int e = 0; e < 4; ++e) {
+      s[e] = keep ? fmaf(a, s[e], k * v[e]) : k * v[e];
+      o[e] = fmaf(q, s[e], o[e]);
+    }
+    if (col < p.vd) {
+      if (p.vec)
+        *reinterpret_cast<f32x4*>(s_out + int64_t(r) * p.vd) = s;
+      else
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.vd) s_out[int64_t(r) * p.vd + e] = s[e];
+    }
+  }
+  part[tid] = o;
+  __syncthreads();
+  if (tid < lanes) {
+    for (int r = 1; r < rows; ++r) o += part[r * lanes + tid];
+    T* dsto = static_cast<T*>(p.o) + b * p.o_sb + h * p.o_sh + col;
+    for (int e = 0; e < 4; ++e)
+      if (col + e < p.vd) {
+        if constexpr (sizeof(T) == 2)
+          dsto[e] = bf16_rne(o[e]);
+        else
+          dsto[e] = o[e];
+      }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_lin(bool bf16, bool rev, const LinParams& p, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (p.nseg > 1) {
+    e = lin_walk(bf16, rev, true, p, stream);
+    if (e != hipSuccess) return e;
+    const int KD = lin_kd(p.kd), NT = lin_cols(p.vd) / 64;
+    const dim3 grid(uint32_t(p.batch * p.H * p.nblk * (KD * 64 * NT / 1024)));
+    if (rev)
+      lin_prefix_kernel<true><<<grid, dim3(256), 0, stream>>>(p, KD, NT);
+    else
+      lin_prefix_kernel<false><<<grid, dim3(256), 0, stream>>>(p, KD, NT);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return lin_walk(bf16, rev, false, p, stream);
+}
+
+hipError_t launch_lin_heads(bool bf16, const float* part, void* out, int64_t tokens, int64_t H, int share, int width,
+                            hipStream_t stream) {
+  const int64_t n = tokens * (H / share) * width;
+  const int64_t blocks = (n + 255) / 256;
+  const dim3 grid(uint32_t(blocks < (1 << 20) ? blocks : 1 << 20));
+  if (bf16)
+    lin_heads_kernel<uint16_t><<<grid, dim3(256), 0, stream>>>(part, static_cast<uint16_t*>(out), n, share, width);
+  else
+    lin_heads_kernel<float><<<grid, dim3(256), 0, stream>>>(part, static_cast<float*>(out), n, share, width);
+  return hipGetLastError();
+}
+
+hipError_t launch_lin_decay(const LinDecayParams& p, hipStream_t stream) {
+  lin_decay_kernel<<<dim3(uint32_t(p.batch * p.H)), dim3(256), 0, stream>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && p.dg_heads) {
+    lin_decay_heads_kernel<<<dim3(uint32_t((p.H + 255) / 256)), dim3(256), 0, stream>>>(p.sums, p.dg_heads, p.batch, p.H);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+hipError_t launch_lin_step(bool bf16, const LinStepParams& p, hipStream_t stream) {
+  int lanes = 1;
+  while (lanes * 4 < p.vd) lanes *= 2;
+  const dim3 grid(uint32_t(p.batch * p.H));
+  if (bf16)
+    lin_step_kernel<uint16_t><<<grid, dim3(256), 0, stream>>>(p, lanes);
+  else
+    lin_step_kernel<float><<<grid, dim3(256), 0, stream>>>(p, lanes);
+  return hipGetLastError();
+}
+
+}  // namespace selscan

@@ -1,0 +1,300 @@
+// norm_kernels.hip -- group norm with an activation, token by token, channels last.
+//
+//     xh = (x - mean) / sqrt(var + eps) over the channels of a token's group,  n = xh w + b,
+//     y = act(n), or with a gate y = n act(z);   act(t) = t sigmoid(t), or t
+// Backward, dn = dy act'(n) (gate: dy act(z), dz = dy n act'(z)), u = dn w, r = 1 / sqrt(var + eps):
+//     dx = r (u - mean(u) - xh mean(u xh)),  dw = sum dn xh,  db = sum dn
+#include <hip/hip_runtime.h>
+
+#include "device_common.h"
+#include "scan_launch.h"
+
+namespace selscan {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+// VEC consecutive elements: 16 bytes, or one element.
+template <typename T, int VEC> __device__ __forceinline__ void norm_load(const T* p, float* v) {
+  if constexpr (VEC == 1) {
+    v[0] = io_traits<T>::widen(*p);
+  } else {
+    union { u32x4 q; T e[VEC]; } u;
+    u.q = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = io_traits<T>::widen(u.e[i]);
+  }
+}
+template <int VEC> __device__ __forceinline__ void norm_load_f32(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < VEC; i += VEC < 4 ? 1 : 4) norm_load<float, VEC < 4 ? 1 : 4>(p + i, v + i);
+}
+template <typename T, int VEC> __device__ __forceinline__ void norm_store(T* p, const float* v) {
+  if constexpr (VEC == 1) {
+    if constexpr (sizeof(T) == 2) *p = bf16_rne(v[0]); else *p = v[0];
+  } else if constexpr (sizeof(T) == 2) {
+    typedef __attribute__((ext_vector_type(VEC))) __bf16 b;
+    typedef __attribute__((ext_vector_type(VEC))) float f;
+    f x;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = v[i];
+    *reinterpret_cast<b*>(p) = __builtin_convertvector(x, b);
+  } else {
+    typedef __attribute__((ext_vector_type(4))) float f;
+    *reinterpret_cast<f*>(p) = f{v[0], v[1], v[2], v[3]};
+  }
+}
+
+// The sum over the `lanes` threads of a group, in every one of them.
+__device__ __forceinline__ float norm_sum(float v, int lanes, float* tmp) {
+  for (int d = (lanes < 64 ? lanes : 64) / 2; d > 0; d /= 2) v += __shfl_xor(v, d);
+  if (lanes > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+  }
+  return v;
+}
+
+// act(t) and act'(t)
+__device__ __forceinline__ float norm_act(float t, bool silu, float& slope) {
+  if (!silu) { slope = 1.f; return t; }
+  const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-t * kLog2e));
+  slope = fmaf(t * s, 1.f - s, s);
+  return t * s;
+}
+
+template <typename T, int VEC, int EPT>
+struct NormRow {
+  float x[EPT * VEC];      // then (x - mean) / sqrt(var + eps)
+  float r;
+  __device__ __forceinline__ void load(const T* src, int lanes, int lane, int width, float eps, float* tmp) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = (i * lanes + lane) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[i * VEC + e] = 0.f;
+      if (c < width) norm_load<T, VEC>(src + c, x + i * VEC);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += x[i * VEC + e];
+    }
+    const float inv = 1.f / float(width);
+    const float mean = norm_sum(s, lanes, tmp) * inv;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = (i * lanes + lane) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        x[i * VEC + e] = c < width ? x[i * VEC + e] - mean : 0.f;
+        q = fmaf(x[i * VEC + e], x[i * VEC + e], q);
+      }
+    }
+    r = 1.f / sqrtf(fmaf(norm_sum(q, lanes, tmp), inv, eps));
+#pragma unroll
+    for (int i = 0; i < EPT * VEC; ++i) x[i] *= r;
+  }
+};
+
+template <typename T, int VEC, int EPT>
+__global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
+  __shared__ float tmp[4];
+  const int lanes = p.lanes, lane = threadIdx.x % lanes;
+  const int64_t gi = int64_t(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
+  if (gi >= p.rows * p.groups) return;
+  const int64_t row = gi / p.groups, b = row / p.L, l = row % p.L;
+  const int64_t c0 = gi % p.groups * p.width;
+  const T* x = static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0;
+  const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0 : nullptr;
+  T* y = static_cast<T*>(p.y) + b * p.y_sb + l * p.y_sl + c0;
+  NormRow<T, VEC, EPT> n;
+  n.load(x, lanes, lane, p.width, p.eps, tmp);
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const int c = (i * lanes + lane) * VEC;
+    if (c >= p.width) break;
+    float w[VEC], o[VEC], t[VEC];
+    if (p.weight) norm_load_f32<VEC>(p.weight + c0 + c, w);
+    if (p.bias) norm_load_f32<VEC>(p.bias + c0 + c, o);
+    if (z) norm_load<T, VEC>(z + c, t);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float v = fmaf(n.x[i * VEC + e], p.weight ? w[e] : 1.f, p.bias ? o[e] : 0.f);
+      float slope;
+      o[e] = z ? v * norm_act(t[e], p.silu, slope) : norm_act(v, p.silu, slope);
+    }
+    norm_store<T, VEC>(y + c, o);
+  }
+}
+
+// A workgroup keeps to `256 / lanes` groups of channels (of several rows at once where there are fewer groups)
+// and walks every `splits`-th row, so that the sums for weight and bias stay in registers.
+template <typename T, int VEC, int EPT>
+__global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
+  __shared__ float tmp[4];
+  const int lanes = p.lanes, lane = threadIdx.x % lanes, slot = threadIdx.x / lanes;
+  const int gslot = slot % p.gper, rslot = slot / p.gper, rows_at_once = 256 / lanes / p.gper;
+  const int64_t cb = blockIdx.x % p.cblocks, split = blockIdx.x / p.cblocks;
+  const int64_t group = cb * p.gper + gslot;
+  const bool live = group < p.groups;
+  const int64_t c0 = group * p.width;
+  const int64_t part = split * rows_at_once + rslot;
+  float w[EPT * VEC], o[EPT * VEC], dw[EPT * VEC], db[EPT * VEC];
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const int c = (i * lanes + lane) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) { w[i * VEC + e] = 1.f; o[i * VEC + e] = dw[i * VEC + e] = db[i * VEC + e] = 0.f; }
+    if (live && c < p.width) {
+      if (p.weight) norm_load_f32<VEC>(p.weight + c0 + c, w + i * VEC);
+      if (p.bias) norm_load_f32<VEC>(p.bias + c0 + c, o + i * VEC);
+    }
+  }
+  const float inv = 1.f / float(p.width);
+  for (int64_t row = part; row < p.rows && live; row += p.splits * rows_at_once) {
+    const int64_t b = row / p.L, l = row % p.L;
+    const T* dy = static_cast<const T*>(p.dy) + b * p.y_sb + l * p.y_sl + c0;
+    const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0 : nullptr;
+    const int64_t out = row * p.groups * p.width + c0;
+    NormRow<T, VEC, EPT> n;
+    n.load(static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0, lanes, lane, p.width, p.eps, tmp);
+    float u[EPT * VEC], m1 = 0.f, m2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = (i * lanes + lane) * VEC;
+      float d[VEC], t[VEC], dz[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) u[i * VEC + e] = 0.f;
+      if (c < p.width) {
+        norm_load<T, VEC>(dy + c, d);
+        if (z) norm_load<T, VEC>(z + c, t);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int k = i * VEC + e;
+          const float v = fmaf(n.x[k], w[k], o[k]);
+          float slope, dn;
+          if (z) {
+            dn = d[e] * norm_act(t[e], p.silu, slope);
+            dz[e] = d[e] * v * slope;
+          } else {
+            norm_act(v, p.silu, slope);
+            dn = d[e] * slope;
+          }
+          dw[k] = fmaf(dn, n.x[k], dw[k]);
+          db[k] += dn;
+          u[k] = dn * w[k];
+          m1 += u[k];
+          m2 = fmaf(u[k], n.x[k], m2);
+        }
+        if (z) norm_store<T, VEC>(static_cast<T*>(p.dz) + out + c, dz);
+      }
+    }
+    m1 = norm_sum(m1, lanes, tmp) * inv;
+    m2 = norm_sum(m2, lanes, tmp) * inv;
+    // two channels: what is left of u - mean(u) beside xh is eps / (var + eps) of it
+    const float two = p.width == 2 ? n.r * n.r * p.eps : 0.f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = (i * lanes + lane) * VEC;
+      float d[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float a = u[i * VEC + e] - m1;
+        d[e] = n.r * (p.width == 2 ? a * two : fmaf(-n.x[i * VEC + e], m2, a));
+      }
+      if (c < p.width) norm_store<T, VEC>(static_cast<T*>(p.dx) + out + c, d);
+    }
+  }
+  if (!live || !p.part) return;
+  const int64_t C = p.groups * p.width;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const int c = (i * lanes + lane) * VEC;
+    if (c >= p.width) break;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      p.part[2 * part * C + c0 + c + e] = dw[i * VEC + e];
+      p.part[(2 * part + 1) * C + c0 + c + e] = db[i * VEC + e];
+    }
+  }
+}
+
+// dweight and dbias: 64 columns a workgroup, every fourth part a wavefront
+__global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64_t parts, int64_t C, float* dw, float* db) {
+  __shared__ float s[2][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+  float a = 0.f, b = 0.f;
+  if (c < C)
+    for (int64_t i = wave; i < parts; i += 4) {
+      a += part[2 * i * C + c];
+      b += part[(2 * i + 1) * C + c];
+    }
+  s[0][wave][lane] = a;
+  s[1][wave][lane] = b;
+  __syncthreads();
+  if (wave == 0 && c < C) {
+    if (dw) dw[c] = (s[0][0][lane] + s[0][1][lane]) + (s[0][2][lane] + s[0][3][lane]);
+    if (db) db[c] = (s[1][0][lane] + s[1][1][lane]) + (s[1][2][lane] + s[1][3][lane]);
+  }
+}
+
+template <typename T, int VEC, int EPT>
+hipError_t norm_launch(bool bwd, const NormParams& p, hipStream_t stream) {
+  if (bwd) {
+    norm_bwd_kernel<T, VEC, EPT><<<dim3(uint32_t(p.cblocks * p.splits)), dim3(256), 0, stream>>>(p);
+  } else {
+    const int64_t per = 256 / p.lanes;
+    norm_fwd_kernel<T, VEC, EPT><<<dim3(uint32_t((p.rows * p.groups + per - 1) / per)), dim3(256), 0, stream>>>(p);
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t norm_dispatch(bool bwd, const NormParams& p, hipStream_t stream) {
+  constexpr int VEC = 16 / sizeof(T);
+  if (!p.vec)
+    return p.ept <= 1 ? norm_launch<T, 1, 1>(bwd, p, stream) : p.ept <= 4 ? norm_launch<T, 1, 4>(bwd, p, stream)
+         : p.ept <= 8 ? norm_launch<T, 1, 8>(bwd, p, stream) : norm_launch<T, 1, 32>(bwd, p, stream);
+  switch (p.ept) {
+    case 1: return norm_launch<T, VEC, 1>(bwd, p, stream);
+    case 2: return norm_launch<T, VEC, 2>(bwd, p, stream);
+  }
+  if (VEC == 8 || p.ept <= 4) return norm_launch<T, VEC, 4>(bwd, p, stream);
+  return norm_launch<T, VEC, VEC == 8 ? 4 : 8>(bwd, p, stream);
+}
+
+}  // namespace
+
+NormPlan norm_plan(bool bf16, bool vec, int64_t rows, int64_t groups, int64_t width) {
+  NormPlan pl{};
+  const int64_t per = vec ? (bf16 ? 8 : 4) : 1, pieces = (width + per - 1) / per;
+  pl.lanes = 1;
+  while (pl.lanes < 64 && pl.lanes < pieces) pl.lanes *= 2;
+  if (width > 64 * kNormElems) pl.lanes = 256;
+  pl.ept = int32_t((pieces + pl.lanes - 1) / pl.lanes);
+  const int64_t slots = 256 / pl.lanes;
+  pl.gper = 1;
+  while (pl.gper < slots && pl.gper < groups) pl.gper *= 2;
+  pl.cblocks = (groups + pl.gper - 1) / pl.gper;
+  const int64_t at_once = slots / pl.gper, most = (rows + at_once - 1) / at_once;
+  pl.splits = (1024 + pl.cblocks - 1) / pl.cblocks;
+  if (pl.splits > most) pl.splits = most;
+  if (pl.splits < 1) pl.splits = 1;
+  pl.parts = pl.splits * at_once;
+  return pl;
+}
+
+hipError_t launch_norm(bool bf16, bool bwd, const NormParams& p, hipStream_t stream) {
+  hipError_t e = bf16 ? norm_dispatch<uint16_t>(bwd, p, stream) : norm_dispatch<float>(bwd, p, stream);
+  if (e == hipSuccess && bwd && p.part) {
+    const int64_t C = p.groups * p.width;
+    norm_sums_kernel<<<dim3(uint32_t((C + 63) / 64)), dim3(256), 0, stream>>>(p.part, p.parts, C, p.dweight, p.dbias);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace selscan

@@ -282,3 +282,118 @@ hipError_t launch_step_cached(bool bf16, const StepParams& s, const CacheParams&
 hipError_t launch_ssd_step_cached(const SsdParams& s, const CacheParams& p, hipStream_t stream);
 
 }  // namespace selscan
+
+namespace selscan {
+
+// Linear attention with a decay for each head (linattn_kernels.h, linattn_kernels.hip).
+// A [batch][tokens][heads / share][width] operand; strides in elements.
+struct LinTensor {
+  const void* p;
+  int64_t sb, sl, sh;
+  int32_t share;        // heads that share one row
+  int32_t vec;          // 1: 16-byte accesses (base and strides on 16 bytes)
+};
+// One walk over the chunks (the header of linattn_kernels.h): the operands in the roles that they have in it.
+struct LinParams {
+  LinTensor q, k, v;
+  void* out;            // [batch][tokens][H][vd] in the I/O type, or fp32 (out_f32)
+  int64_t o_sb, o_sl, o_sh;
+  int32_t out_f32, out_vec;
+  const float* g;       // logarithms of the decays
+  int64_t g_sb, g_sl, g_sh;
+  const float* s0;      // state that the walk begins with, (batch, head) blocks of kd * vd; may be null (zero)
+  float* s1;            // state that it ends with, or null
+  int64_t s_row, s_col; // strides of s0 and s1 within a block
+  float* seg;           // workspace: a state for each (batch, head, block of columns, segment)
+  float* seg_decay;     // workspace: [batch][H][nseg], negative where the state starts anew
+  LinTensor x;          // dot: out . x per token, [nblk][batch][L][H]; null: not wanted
+  float* dot;
+  int64_t batch, L, H;
+  int32_t kd, vd;       // width of q and k, of v and out (1 .. 256)
+  float pscale, fscale, wscale;   // of the pairs, of a row's product with the state, of its share in the state
+  int64_t nchunks;      // ceil(L / lin_chunk())
+  int64_t seg_chunks;   // chunks of a segment
+  int32_t nseg, nblk;   // segments; blocks of lin_cols() columns
+  int32_t parts;        // parts that fp32 values are split into for the bf16 matrix cores: 1, 2 or 3
+};
+constexpr int lin_kd(int64_t kd) { return kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
+constexpr int lin_cols(int64_t vd) { return vd <= 64 ? 64 : 128; }
+constexpr int lin_chunk(bool bf16, int64_t kd) { return !bf16 && kd > 128 ? 32 : 64; }
+// one walk; with nseg > 1 the states that enter the segments are formed first
+hipError_t launch_lin(bool bf16, bool rev, const LinParams& p, hipStream_t stream);
+// units of one element type and width of q and k
+hipError_t launch_lin_bf16_64(bool rev, bool state, const LinParams& p, hipStream_t stream);
+hipError_t launch_lin_bf16_128(bool rev, bool state, const LinParams& p, hipStream_t stream);
+hipError_t launch_lin_bf16_256(bool rev, bool state, const LinParams& p, hipStream_t stream);
+hipError_t launch_lin_f32_64(bool rev, bool state, const LinParams& p, hipStream_t stream);
+hipError_t launch_lin_f32_128(bool rev, bool state, const LinParams& p, hipStream_t stream);
+hipError_t launch_lin_f32_256(bool rev, bool state, const LinParams& p, hipStream_t stream);
+
+// Sums over the heads that share one: part [tokens][H][width] fp32 -> out [tokens][H / share][width]
+hipError_t launch_lin_heads(bool bf16, const float* part, void* out, int64_t tokens, int64_t H, int share, int width,
+                            hipStream_t stream);
+
+// The decays' gradient from the rows' products: dg_t = <last, dlast> + sum_{i >= t} (qdq_i - kdk_i)
+struct LinDecayParams {
+  const float* qdq;     // [nq][batch][L][H]
+  const float* kdk;     // [nk][batch][L][H]
+  const float* last;    // [batch][H][state], with dlast; both may be null (zero)
+  const float* dlast;
+  const float* g;
+  int64_t g_sb, g_sl, g_sh;
+  float* dg;            // [batch][L][H], or null: the heads' sums only
+  double* sums;         // workspace [batch][H]
+  float* dg_heads;      // [H], or null
+  int64_t batch, L, H, state;
+  int32_t nq, nk;
+};
+hipError_t launch_lin_decay(const LinDecayParams& p, hipStream_t stream);
+
+// One token per batch row, states in slots.
+struct LinStepParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  void* o;
+  float* state;               // [slots][H][K][V]
+  const int32_t* read_slots;  // may be null (0, 1, 2, ...)
+  const int32_t* write_slots;
+  int64_t slots, batch, H;
+  int32_t share, kd, vd, vec; // vec: the state's rows are on 16 bytes
+  int64_t q_sb, q_sh, k_sb, k_sh, v_sb, v_sh, o_sb, o_sh, g_sb, g_sh;
+  float scale;
+};
+hipError_t launch_lin_step(bool bf16, const LinStepParams& p, hipStream_t stream);
+
+// Group norm with an activation (norm_kernels.hip).
+constexpr int kNormElems = 32;          // of a group in one thread, at most
+struct NormPlan {
+  int32_t lanes;        // threads of a group: a power of two up to 64, or 256
+  int32_t ept;          // accesses of a thread
+  int64_t gper, cblocks, splits, parts;  // backward: groups side by side in a workgroup, blocks of them, workgroups
+                        // that share the rows, partial sums of dweight and dbias
+};
+NormPlan norm_plan(bool bf16, bool vec, int64_t rows, int64_t groups, int64_t width);
+struct NormParams {
+  const void* x;
+  const float* weight;  // [C], may be null
+  const float* bias;    // [C], may be null
+  const void* z;        // may be null (no gate)
+  void* y;
+  const void* dy;       // backward, with y's strides
+  void* dx;
+  void* dz;
+  float* dweight;
+  float* dbias;
+  float* part;          // workspace [parts][2][C], or null (neither is wanted)
+  int64_t rows, L, groups;
+  int32_t width, silu, vec;
+  int64_t x_sb, x_sl, z_sb, z_sl, y_sb, y_sl;
+  float eps;
+  int32_t lanes, ept;
+  int64_t gper, cblocks, splits, parts;
+};
+hipError_t launch_norm(bool bf16, bool bwd, const NormParams& p, hipStream_t stream);
+
+}  // namespace selscan

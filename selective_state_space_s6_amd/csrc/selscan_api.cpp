@@ -7,6 +7,7 @@
 #include <atomic>
 #include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "scan_launch.h"
 
@@ -1285,6 +1286,484 @@ int selective_scan_ssd_step_cached(const void* x, const void* delta, const float
   s.euler = d.discretization == SELSCAN_DISC_EULER ? 1 : 0;
   const hipError_t e = selscan::launch_ssd_step_cached(s, p, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+// ---- linear attention with a decay for each head
+static size_t ws_round(int64_t bytes) { return size_t(round_up(bytes, 256)); }
+
+// One walk (the queries' and keys' width kd, the values' vd): its blocks of columns and segments.
+struct LinWalk {
+  int64_t nchunks = 0, seg_chunks = 0;
+  int32_t nseg = 1, nblk = 1;
+  size_t seg_bytes = 0, decay_bytes = 0;
+};
+
+static LinWalk lin_walk_plan(bool bf16, const selscan_linattn_dims& d, int64_t kd, int64_t vd) {
+  LinWalk w;
+  const int64_t chunk = selscan::lin_chunk(bf16, kd), cols = selscan::lin_cols(vd);
+  w.nchunks = (d.seqlen + chunk - 1) / chunk;
+  w.nblk = int32_t((vd + cols - 1) / cols);
+  w.seg_chunks = w.nchunks;
+  const int64_t items = d.batch * d.nheads * w.nblk;
+  // fewer workgroups than fill the GPU's 256 compute units: the sequence is split into segments of at
+  // least 4 chunks
+  if (items > 0 && items < 384) {
+    int64_t n = (512 + items - 1) / items;
+    if (n > w.nchunks / 4) n = w.nchunks / 4;
+    if (n > 1) {
+      w.seg_chunks = (w.nchunks + n - 1) / n;
+      w.nseg = int32_t((w.nchunks + w.seg_chunks - 1) / w.seg_chunks);
+    }
+  }
+  if (w.nseg > 1) {
+    w.seg_bytes = ws_round(int64_t(sizeof(float)) * items * w.nseg * selscan::lin_kd(kd) * cols);
+    w.decay_bytes = ws_round(int64_t(sizeof(float)) * d.batch * d.nheads * w.nseg);
+  }
+  return w;
+}
+
+struct LinPlan {
+  LinWalk fwd, dq, dv;          // dk's walk is planned as dq's
+  size_t fwd_bytes = 0, bwd_bytes = 0;
+  size_t off_decay = 0, off_qdq = 0, off_kdk = 0, off_last = 0, off_sums = 0, off_part = 0;
+};
+
+// Rows of `width` elements on axes of these sizes and strides: whether none overlaps another.
+static bool rows_apart(std::initializer_list<std::pair<int64_t, int64_t>> axes, int64_t width) {
+  std::pair<int64_t, int64_t> a[4];
+  int n = 0;
+  for (auto x : axes)
+    if (x.first > 1) a[n++] = x;
+  for (int i = 1; i < n; ++i)
+    for (int j = i; j > 0 && a[j].second < a[j - 1].second; --j) std::swap(a[j], a[j - 1]);
+  int64_t extent = width;
+  for (int i = 0; i < n; ++i) {
+    if (a[i].second < extent) return false;
+    // (beyond any memory: nothing larger can overlap)
+    if (a[i].second > (int64_t(1) << 62) / a[i].first) return i + 1 == n;
+    extent += a[i].second * (a[i].first - 1);
+  }
+  return true;
+}
+
+static int lin_plan(const selscan_linattn_dims* dims, bool want_dg, LinPlan* out) {
+  if (!dims) return SELSCAN_ERR_NULL;
+  if (dims->abi_version != SELSCAN_ABI_VERSION) return SELSCAN_ERR_ABI;
+  const selscan_linattn_dims& d = *dims;
+  if (d.batch < 0 || d.seqlen < 0 || d.nheads < 1 || d.qk_heads < 1 || d.dk < 1 || d.dv < 1) return SELSCAN_ERR_DIMS;
+  if (d.nheads % d.qk_heads != 0) return SELSCAN_ERR_DIMS;
+  for (int64_t s : {d.q_sb, d.q_sl, d.q_sh, d.k_sb, d.k_sl, d.k_sh, d.v_sb, d.v_sl, d.v_sh, d.o_sb, d.o_sl, d.o_sh,
+                    d.g_sb, d.g_sl, d.g_sh})
+    if (s < 0) return SELSCAN_ERR_DIMS;
+  if (!(d.scale > -3.0e38f && d.scale < 3.0e38f)) return SELSCAN_ERR_DIMS;
+  if (d.io_dtype != SELSCAN_F32 && d.io_dtype != SELSCAN_BF16) return SELSCAN_ERR_UNSUPPORTED;
+  if (d.decay_tokens != 0 && d.decay_tokens != 1) return SELSCAN_ERR_UNSUPPORTED;
+  if (d.dk > 256 || d.dv > 256) return SELSCAN_ERR_UNSUPPORTED;
+  const int64_t kMaxRow = int64_t(1) << 22;
+  if (d.seqlen > 1)
+    for (int64_t s : {d.q_sl, d.k_sl, d.v_sl, d.o_sl})
+      if (s > kMaxRow) return SELSCAN_ERR_UNSUPPORTED;
+  // workgroups of 256 threads, fewer than 2^32 threads a launch
+  const int64_t kMaxItems = int64_t(1) << 22, wide = d.dk > d.dv ? d.dk : d.dv;
+  if (d.batch >= kMaxItems || d.nheads >= kMaxItems || d.batch * d.nheads >= kMaxItems ||
+      d.batch * d.nheads * ((wide + 63) / 64) >= kMaxItems)
+    return SELSCAN_ERR_UNSUPPORTED;
+  if (d.seqlen > (int64_t(1) << 31) - 1) return SELSCAN_ERR_UNSUPPORTED;
+  LinPlan p;
+  if (d.batch * d.seqlen > 0) {
+    const bool bf16 = d.io_dtype == SELSCAN_BF16;
+    const int64_t f = int64_t(sizeof(float)), bh = d.batch * d.nheads, rows = bh * d.seqlen;
+    p.fwd = lin_walk_plan(bf16, d, d.dk, d.dv);
+    p.fwd_bytes = p.fwd.seg_bytes + p.fwd.decay_bytes;
+    p.dq = lin_walk_plan(bf16, d, d.dv, d.dk);
+    p.dv = p.fwd;
+    // the walks of the backward pass follow one another in one workspace
+    size_t off = p.dq.seg_bytes > p.dv.seg_bytes ? p.dq.seg_bytes : p.dv.seg_bytes;
+    p.off_decay = off;
+    off += p.dq.decay_bytes > p.dv.decay_bytes ? p.dq.decay_bytes : p.dv.decay_bytes;
+    if (want_dg) {
+      p.off_qdq = off;
+      off += ws_round(f * rows * p.dq.nblk);
+      p.off_kdk = off;
+      off += ws_round(f * rows * p.dq.nblk);
+      p.off_last = off;
+      off += ws_round(f * bh * d.dk * d.dv);
+      p.off_sums = off;
+      off += ws_round(int64_t(sizeof(double)) * bh);
+    }
+    p.off_part = off;
+    if (d.nheads != d.qk_heads) off += ws_round(f * rows * d.dk);
+    p.bwd_bytes = off;
+  }
+  *out = p;
+  return SELSCAN_OK;
+}
+
+static selscan::LinTensor lin_tensor(const void* ptr, const selscan_linattn_dims& d, int64_t heads, int64_t sb, int64_t sl,
+                                     int64_t sh) {
+  const int64_t v = d.io_dtype == SELSCAN_BF16 ? 8 : 4;
+  selscan::LinTensor t{};
+  t.p = ptr;
+  t.sb = d.batch > 1 ? sb : 0;
+  t.sl = d.seqlen > 1 ? sl : 0;
+  t.sh = heads > 1 ? sh : 0;
+  t.share = int32_t(d.nheads / heads);
+  t.vec = aligned(ptr, 16) && t.sb % v == 0 && t.sl % v == 0 && t.sh % v == 0;
+  return t;
+}
+
+static selscan::LinParams lin_params(const LinWalk& w, const selscan::LinTensor& q, const selscan::LinTensor& k,
+                                     const selscan::LinTensor& v, int64_t kd, int64_t vd, const float* g,
+                                     const selscan_linattn_dims& d, void* ws, size_t off_decay) {
+  selscan::LinParams p{};
+  p.q = q; p.k = k; p.v = v;
+  p.g = g;
+  p.g_sb = d.decay_tokens ? d.g_sb : 0; p.g_sl = d.decay_tokens ? d.g_sl : 0; p.g_sh = d.g_sh;
+  p.batch = d.batch; p.L = d.seqlen; p.H = d.nheads;
+  p.kd = int32_t(kd); p.vd = int32_t(vd);
+  p.nchunks = w.nchunks; p.seg_chunks = w.seg_chunks; p.nseg = w.nseg; p.nblk = w.nblk;
+  p.seg = static_cast<float*>(ws);
+  p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(ws) + off_decay);
+  p.parts = 2;
+  return p;
+}
+
+static void lin_out(selscan::LinParams* p, void* out, bool f32, const selscan_linattn_dims& d, int64_t sb, int64_t sl,
+                    int64_t sh) {
+  const int64_t v = f32 || d.io_dtype == SELSCAN_F32 ? 4 : 8;
+  p->out = out;
+  p->out_f32 = f32;
+  p->o_sb = d.batch > 1 ? sb : 0; p->o_sl = d.seqlen > 1 ? sl : 0; p->o_sh = d.nheads > 1 ? sh : 0;
+  p->out_vec = aligned(out, 16) && p->o_sb % v == 0 && p->o_sl % v == 0 && p->o_sh % v == 0;
+}
+
+void linear_attention_dims_init(selscan_linattn_dims* dims, int io_dtype, int64_t batch, int64_t seqlen, int64_t nheads,
+                                int64_t qk_heads, int64_t dk, int64_t dv) {
+  if (!dims) return;
+  selscan_linattn_dims d{};
+  d.abi_version = SELSCAN_ABI_VERSION;
+  d.io_dtype = io_dtype;
+  d.batch = batch; d.seqlen = seqlen; d.nheads = nheads; d.qk_heads = qk_heads; d.dk = dk; d.dv = dv;
+  d.q_sh = d.k_sh = dk;
+  d.q_sl = d.k_sl = qk_heads * dk;
+  d.q_sb = d.k_sb = seqlen * qk_heads * dk;
+  d.v_sh = d.o_sh = dv;
+  d.v_sl = d.o_sl = nheads * dv;
+  d.v_sb = d.o_sb = seqlen * nheads * dv;
+  d.g_sh = 1; d.g_sl = nheads; d.g_sb = seqlen * nheads;
+  d.decay_tokens = 1;
+  d.scale = 1.f;
+  *dims = d;
+}
+
+size_t linear_attention_workspace_size(const selscan_linattn_dims* dims) {
+  LinPlan pl;
+  return lin_plan(dims, false, &pl) == SELSCAN_OK ? pl.fwd_bytes : 0;
+}
+
+size_t linear_attention_bwd_workspace_size(const selscan_linattn_dims* dims, int want_dlog_decay) {
+  LinPlan pl;
+  return lin_plan(dims, want_dlog_decay != 0, &pl) == SELSCAN_OK ? pl.bwd_bytes : 0;
+}
+
+int linear_attention_fwd(const void* q, const void* k, const void* v, const float* log_decay, void* o,
+                         const float* initial_state, float* last_state, const selscan_linattn_dims* dims,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  LinPlan pl;
+  int st = lin_plan(dims, false, &pl);
+  if (st != SELSCAN_OK) return st;
+  const selscan_linattn_dims& d = *dims;
+  const bool no_tokens = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16;
+  if (!no_tokens && !rows_apart({{d.batch, d.o_sb}, {d.seqlen, d.o_sl}, {d.nheads, d.o_sh}}, d.dv)) return SELSCAN_ERR_UNSUPPORTED;
+  if (!no_tokens && (!q || !k || !v || !log_decay || !o)) return SELSCAN_ERR_NULL;
+  if (!all_aligned({q, k, v, o}, bf16 ? 2 : 4) || !all_aligned({log_decay, initial_state, last_state}, 4))
+    return SELSCAN_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (d.batch == 0) return SELSCAN_OK;
+  hipError_t e = hipSuccess;
+  if (no_tokens) {                              // the initial state is handed back
+    const int64_t n = d.batch * d.nheads * d.dk * d.dv;
+    if (last_state && last_state != initial_state)
+      e = initial_state ? selscan::launch_copy(last_state, initial_state, n, s) : selscan::launch_fill_zero(last_state, n, s);
+    return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  }
+  void* ws = workspace;
+  if (pl.fwd_bytes > 0 && ws != nullptr) {
+    if (workspace_bytes < pl.fwd_bytes || !aligned(ws, 256)) return SELSCAN_ERR_WORKSPACE;
+  } else if (pl.fwd_bytes > 0) {
+    e = hipMallocAsync(&ws, pl.fwd_bytes, s);
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  selscan::LinParams p = lin_params(pl.fwd, lin_tensor(q, d, d.qk_heads, d.q_sb, d.q_sl, d.q_sh),
+                                    lin_tensor(k, d, d.qk_heads, d.k_sb, d.k_sl, d.k_sh),
+                                    lin_tensor(v, d, d.nheads, d.v_sb, d.v_sl, d.v_sh), d.dk, d.dv, log_decay, d, ws,
+                                    pl.fwd.seg_bytes);
+  lin_out(&p, o, false, d, d.o_sb, d.o_sl, d.o_sh);
+  p.s0 = initial_state; p.s1 = last_state;
+  p.s_row = d.dv; p.s_col = 1;
+  p.pscale = p.fscale = d.scale; p.wscale = 1.f;
+  e = selscan::launch_lin(bf16, false, p, s);
+  st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  if (workspace == nullptr && pl.fwd_bytes > 0) {
+    const hipError_t f = hipFreeAsync(ws, s);
+    if (st == SELSCAN_OK && f != hipSuccess) st = hip_fail(f);
+  }
+  return st;
+}
+
+int linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                         const float* initial_state, const void* d_o, const float* dlast_state, void* dq, void* dk,
+                         void* dv, float* dlog_decay, float* dinitial_state, const selscan_linattn_dims* dims,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  LinPlan pl;
+  const bool want_dg = dlog_decay != nullptr;
+  int st = lin_plan(dims, want_dg, &pl);
+  if (st != SELSCAN_OK) return st;
+  const selscan_linattn_dims& d = *dims;
+  const bool no_tokens = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16, shared = d.nheads != d.qk_heads;
+  if (!no_tokens && (!q || !k || !v || !log_decay || !d_o || !dq || !dk || !dv)) return SELSCAN_ERR_NULL;
+  if (!all_aligned({q, k, v, d_o, dq, dk, dv}, bf16 ? 2 : 4) ||
+      !all_aligned({log_decay, initial_state, dlast_state, dlog_decay, dinitial_state}, 4))
+    return SELSCAN_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t states = d.batch * d.nheads * d.dk * d.dv;
+  hipError_t e = hipSuccess;
+  if (no_tokens) {                              // empty sums; the last state is the initial one
+    if (want_dg && !d.decay_tokens) e = selscan::launch_fill_zero(dlog_decay, d.nheads, s);
+    if (e == hipSuccess && dinitial_state && states > 0 && dinitial_state != dlast_state)
+      e = dlast_state ? selscan::launch_copy(dinitial_state, dlast_state, states, s)
+                      : selscan::launch_fill_zero(dinitial_state, states, s);
+    return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  }
+  char* ws = static_cast<char*>(workspace);
+  if (pl.bwd_bytes > 0 && ws != nullptr) {
+    if (workspace_bytes < pl.bwd_bytes || !aligned(ws, 256)) return SELSCAN_ERR_WORKSPACE;
+  } else if (pl.bwd_bytes > 0) {
+    void* mem = nullptr;
+    e = hipMallocAsync(&mem, pl.bwd_bytes, s);
+    if (e != hipSuccess) return hip_fail(e);
+    ws = static_cast<char*>(mem);
+  }
+  const selscan::LinTensor tq = lin_tensor(q, d, d.qk_heads, d.q_sb, d.q_sl, d.q_sh),
+                           tk = lin_tensor(k, d, d.qk_heads, d.k_sb, d.k_sl, d.k_sh),
+                           tv = lin_tensor(v, d, d.nheads, d.v_sb, d.v_sl, d.v_sh),
+                           to = lin_tensor(d_o, d, d.nheads, d.o_sb, d.o_sl, d.o_sh);
+  const int64_t tokens = d.batch * d.seqlen;
+  float* part = reinterpret_cast<float*>(ws + pl.off_part);
+  float* last = reinterpret_cast<float*>(ws + pl.off_last);
+  const bool want_last = want_dg && dlast_state != nullptr;
+  // dq: do meets v, and the state S of the forward pass meets do (S read with its axes exchanged)
+  selscan::LinParams p = lin_params(pl.dq, to, tv, tk, d.dv, d.dk, log_decay, d, ws, pl.off_decay);
+  lin_out(&p, shared ? part : dq, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
+  p.s0 = initial_state; p.s1 = want_last ? last : nullptr;
+  p.s_row = 1; p.s_col = d.dv;
+  p.pscale = p.fscale = d.scale; p.wscale = 1.f;
+  if (want_dg) {
+    p.x = tq;
+    p.dot = reinterpret_cast<float*>(ws + pl.off_qdq);
+    p.parts = 3;
+  }
+  e = selscan::launch_lin(bf16, false, p, s);
+  if (e == hipSuccess && shared)
+    e = selscan::launch_lin_heads(bf16, part, dq, tokens, d.nheads, int(d.nheads / d.qk_heads), int(d.dk), s);
+  // dk: v meets do, and the gradient R of the state meets v
+  if (e == hipSuccess) {
+    p = lin_params(pl.dq, tv, to, tq, d.dv, d.dk, log_decay, d, ws, pl.off_decay);
+    lin_out(&p, shared ? part : dk, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
+    p.s0 = dlast_state;
+    p.s_row = 1; p.s_col = d.dv;
+    p.pscale = p.wscale = d.scale; p.fscale = 1.f;
+    if (want_dg) {
+      p.x = tk;
+      p.dot = reinterpret_cast<float*>(ws + pl.off_kdk);
+      p.parts = 3;
+    }
+    e = selscan::launch_lin(bf16, true, p, s);
+  }
+  if (e == hipSuccess && shared)
+    e = selscan::launch_lin_heads(bf16, part, dk, tokens, d.nheads, int(d.nheads / d.qk_heads), int(d.dk), s);
+  if (e == hipSuccess && want_dg) {
+    selscan::LinDecayParams c{};
+    c.qdq = reinterpret_cast<float*>(ws + pl.off_qdq);
+    c.kdk = reinterpret_cast<float*>(ws + pl.off_kdk);
+    c.last = want_last ? last : nullptr;
+    c.dlast = dlast_state;
+    c.g = log_decay; c.g_sb = p.g_sb; c.g_sl = p.g_sl; c.g_sh = p.g_sh;
+    c.dg = d.decay_tokens ? dlog_decay : nullptr;
+    c.dg_heads = d.decay_tokens ? nullptr : dlog_decay;
+    c.sums = reinterpret_cast<double*>(ws + pl.off_sums);
+    c.batch = d.batch; c.L = d.seqlen; c.H = d.nheads; c.state = d.dk * d.dv;
+    c.nq = c.nk = pl.dq.nblk;
+    e = selscan::launch_lin_decay(c, s);
+  }
+  // dv: k meets q, and R meets k; R before the first token is the initial state's gradient (last: it
+  // may take dlast_state's place)
+  if (e == hipSuccess) {
+    p = lin_params(pl.dv, tk, tq, to, d.dk, d.dv, log_decay, d, ws, pl.off_decay);
+    lin_out(&p, dv, false, d, d.seqlen * d.nheads * d.dv, d.nheads * d.dv, d.dv);
+    p.s0 = dlast_state; p.s1 = dinitial_state;
+    p.s_row = d.dv; p.s_col = 1;
+    p.pscale = p.wscale = d.scale; p.fscale = 1.f;
+    e = selscan::launch_lin(bf16, true, p, s);
+  }
+  st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  if (workspace == nullptr && pl.bwd_bytes > 0) {
+    const hipError_t f = hipFreeAsync(ws, s);
+    if (st == SELSCAN_OK && f != hipSuccess) st = hip_fail(f);
+  }
+  return st;
+}
+
+int linear_attention_step(const void* q, const void* k, const void* v, const float* log_decay, void* o, float* state,
+                          int64_t slots, const int32_t* read_slots, const int32_t* write_slots,
+                          const selscan_linattn_dims* dims, void* stream) {
+  LinPlan pl;
+  const int st = lin_plan(dims, false, &pl);
+  if (st != SELSCAN_OK) return st;
+  const selscan_linattn_dims& d = *dims;
+  if (d.seqlen != 1 || slots < 0) return SELSCAN_ERR_DIMS;
+  if (slots > (int64_t(1) << 31) - 1) return SELSCAN_ERR_UNSUPPORTED;
+  if ((!read_slots || !write_slots) && d.batch > slots) return SELSCAN_ERR_DIMS;      // 0, 1, 2, ... must exist
+  if (!rows_apart({{d.batch, d.o_sb}, {d.nheads, d.o_sh}}, d.dv)) return SELSCAN_ERR_UNSUPPORTED;
+  if (d.batch > 0 && (!q || !k || !v || !log_decay || !o || (slots > 0 && !state))) return SELSCAN_ERR_NULL;
+  const bool bf16 = d.io_dtype == SELSCAN_BF16;
+  if (!all_aligned({q, k, v, o}, bf16 ? 2 : 4) || !all_aligned({log_decay, state, read_slots, write_slots}, 4))
+    return SELSCAN_ERR_ALIGN;
+  if (d.batch == 0 || slots == 0) return SELSCAN_OK;
+  selscan::LinStepParams p{};
+  p.q = q; p.k = k; p.v = v; p.g = log_decay; p.o = o;
+  p.state = state; p.read_slots = read_slots; p.write_slots = write_slots; p.slots = slots;
+  p.batch = d.batch; p.H = d.nheads; p.share = int32_t(d.nheads / d.qk_heads);
+  p.kd = int32_t(d.dk); p.vd = int32_t(d.dv);
+  p.vec = aligned(state, 16) && d.dv % 4 == 0;
+  p.q_sb = d.q_sb; p.q_sh = d.q_sh; p.k_sb = d.k_sb; p.k_sh = d.k_sh; p.v_sb = d.v_sb; p.v_sh = d.v_sh;
+  p.o_sb = d.o_sb; p.o_sh = d.o_sh;
+  p.g_sb = d.decay_tokens ? d.g_sb : 0; p.g_sh = d.g_sh;
+  p.scale = d.scale;
+  const hipError_t e = selscan::launch_lin_step(bf16, p, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+// ---- group norm with an activation
+static int norm_check(const selscan_norm_dims* dims) {
+  if (!dims) return SELSCAN_ERR_NULL;
+  if (dims->abi_version != SELSCAN_ABI_VERSION) return SELSCAN_ERR_ABI;
+  const selscan_norm_dims& d = *dims;
+  if (d.batch < 0 || d.seqlen < 0 || d.dim < 1 || d.groups < 1 || d.dim % d.groups != 0) return SELSCAN_ERR_DIMS;
+  for (int64_t s : {d.x_sb, d.x_sl, d.z_sb, d.z_sl, d.y_sb, d.y_sl})
+    if (s < 0) return SELSCAN_ERR_DIMS;
+  if (!(d.eps > 0.f && d.eps < 3.0e38f)) return SELSCAN_ERR_DIMS;
+  if (d.io_dtype != SELSCAN_F32 && d.io_dtype != SELSCAN_BF16) return SELSCAN_ERR_UNSUPPORTED;
+  if (d.activation != SELSCAN_ACT_NONE && d.activation != SELSCAN_ACT_SILU) return SELSCAN_ERR_UNSUPPORTED;
+  const int64_t width = d.dim / d.groups;
+  if (d.dim > (int64_t(1) << 20) || width > 8192) return SELSCAN_ERR_UNSUPPORTED;
+  const int64_t kMost = (int64_t(1) << 31) - 1;
+  if (d.batch > kMost || d.seqlen > kMost || (d.batch > 0 && d.seqlen > kMost / d.batch)) return SELSCAN_ERR_UNSUPPORTED;
+  // a launch has fewer than 2^32 threads
+  const int64_t rows = d.batch * d.seqlen;
+  if (rows > 0) {
+    if (d.groups > kMost / rows) return SELSCAN_ERR_UNSUPPORTED;
+    const selscan::NormPlan pl = selscan::norm_plan(false, false, rows, d.groups, width);
+    if (rows * d.groups > ((int64_t(1) << 32) - 256) / pl.lanes) return SELSCAN_ERR_UNSUPPORTED;
+  }
+  return SELSCAN_OK;
+}
+
+static size_t norm_bwd_bytes(const selscan_norm_dims& d, bool vec) {
+  const selscan::NormPlan pl = selscan::norm_plan(d.io_dtype == SELSCAN_BF16, vec, d.batch * d.seqlen, d.groups, d.dim / d.groups);
+  return ws_round(int64_t(sizeof(float)) * pl.parts * 2 * d.dim);
+}
+
+static selscan::NormParams norm_params(const void* x, const float* weight, const float* bias, const void* z,
+                                       std::initializer_list<const void*> others, const selscan_norm_dims& d) {
+  selscan::NormParams p{};
+  const bool bf16 = d.io_dtype == SELSCAN_BF16;
+  const int64_t v = bf16 ? 8 : 4;
+  p.x = x; p.weight = weight; p.bias = bias; p.z = z;
+  p.rows = d.batch * d.seqlen; p.L = d.seqlen; p.groups = d.groups; p.width = int32_t(d.dim / d.groups);
+  p.silu = d.activation == SELSCAN_ACT_SILU;
+  auto sb = [&](int64_t s) { return d.batch > 1 ? s : 0; };
+  auto sl = [&](int64_t s) { return d.seqlen > 1 ? s : 0; };
+  p.x_sb = sb(d.x_sb); p.x_sl = sl(d.x_sl); p.z_sb = sb(d.z_sb); p.z_sl = sl(d.z_sl); p.y_sb = sb(d.y_sb); p.y_sl = sl(d.y_sl);
+  p.eps = d.eps;
+  p.vec = p.width % v == 0 && all_aligned({x, weight, bias, z}, 16) && all_aligned(others, 16) && p.x_sb % v == 0 &&
+          p.x_sl % v == 0 && p.y_sb % v == 0 && p.y_sl % v == 0 && (!z || (p.z_sb % v == 0 && p.z_sl % v == 0));
+  const selscan::NormPlan pl = selscan::norm_plan(bf16, p.vec, p.rows, p.groups, p.width);
+  p.lanes = pl.lanes; p.ept = pl.ept;
+  p.gper = pl.gper; p.cblocks = pl.cblocks; p.splits = pl.splits; p.parts = pl.parts;
+  return p;
+}
+
+void group_norm_dims_init(selscan_norm_dims* dims, int io_dtype, int64_t batch, int64_t seqlen, int64_t dim, int64_t groups) {
+  if (!dims) return;
+  selscan_norm_dims d{};
+  d.abi_version = SELSCAN_ABI_VERSION;
+  d.io_dtype = io_dtype;
+  d.batch = batch; d.seqlen = seqlen; d.dim = dim; d.groups = groups;
+  d.x_sl = d.z_sl = d.y_sl = dim;
+  d.x_sb = d.z_sb = d.y_sb = seqlen * dim;
+  d.eps = 1e-5f;
+  d.activation = SELSCAN_ACT_SILU;
+  *dims = d;
+}
+
+int group_norm_fwd(const void* x, const float* weight, const float* bias, const void* z, void* y,
+                   const selscan_norm_dims* dims, void* stream) {
+  const int st = norm_check(dims);
+  if (st != SELSCAN_OK) return st;
+  const selscan_norm_dims& d = *dims;
+  const bool empty = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16;
+  if (!empty && !rows_apart({{d.batch, d.y_sb}, {d.seqlen, d.y_sl}}, d.dim)) return SELSCAN_ERR_UNSUPPORTED;
+  if (!empty && (!x || !y)) return SELSCAN_ERR_NULL;
+  if (!all_aligned({x, z, y}, bf16 ? 2 : 4) || !all_aligned({weight, bias}, 4)) return SELSCAN_ERR_ALIGN;
+  if (empty) return SELSCAN_OK;
+  selscan::NormParams p = norm_params(x, weight, bias, z, {y}, d);
+  p.y = y;
+  const hipError_t e = selscan::launch_norm(bf16, false, p, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+}
+
+size_t group_norm_bwd_workspace_size(const selscan_norm_dims* dims) {
+  if (norm_check(dims) != SELSCAN_OK || dims->batch * dims->seqlen == 0) return 0;
+  const size_t a = norm_bwd_bytes(*dims, false), b = norm_bwd_bytes(*dims, true);   // the pointers decide which
+  return a > b ? a : b;
+}
+
+int group_norm_bwd(const void* x, const float* weight, const float* bias, const void* z, const void* dy, void* dx,
+                   float* dweight, float* dbias, void* dz, const selscan_norm_dims* dims, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  int st = norm_check(dims);
+  if (st != SELSCAN_OK) return st;
+  const selscan_norm_dims& d = *dims;
+  const bool empty = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16;
+  if (!empty && (!x || !dy || !dx || (z && !dz))) return SELSCAN_ERR_NULL;
+  if (!all_aligned({x, z, dy, dx, dz}, bf16 ? 2 : 4) || !all_aligned({weight, bias, dweight, dbias}, 4))
+    return SELSCAN_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (empty) {                                  // empty sums
+    if (dweight) e = selscan::launch_fill_zero(dweight, d.dim, s);
+    if (e == hipSuccess && dbias) e = selscan::launch_fill_zero(dbias, d.dim, s);
+    return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  }
+  selscan::NormParams p = norm_params(x, weight, bias, z, {dy, dx, dz}, d);
+  p.dy = dy; p.dx = dx; p.dz = dz; p.dweight = dweight; p.dbias = dbias;
+  const size_t need = dweight || dbias ? group_norm_bwd_workspace_size(dims) : 0;
+  void* ws = workspace;
+  if (need > 0 && ws != nullptr) {
+    if (workspace_bytes < need || !aligned(ws, 256)) return SELSCAN_ERR_WORKSPACE;
+  } else if (need > 0) {
+    e = hipMallocAsync(&ws, need, s);
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  p.part = need > 0 ? static_cast<float*>(ws) : nullptr;
+  e = selscan::launch_norm(bf16, true, p, s);
+  st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
+  if (workspace == nullptr && need > 0) {
+    const hipError_t f = hipFreeAsync(ws, s);
+    if (st == SELSCAN_OK && f != hipSuccess) st = hip_fail(f);
+  }
+  return st;
 }
 
 const char* selective_scan_strerror(int status) {
