@@ -51,8 +51,8 @@ template <> struct lin_io<uint16_t> {
   static __device__ __forceinline__ f32x8 wide(frag a) { return __builtin_convertvector(a, f32x8); }
   static __device__ __forceinline__ frag round(f32x8 a) { return __builtin_convertvector(a, frag); }
   static __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
-  static __device__ __forceinline__ uint16_t narrow(float v) { return bf16_rne(v); }
-  // N consecutive values (N = 4, 8) to p
+  // N consecutive values (N = 4, 8) to p: in LDS (aligned), or to global memory (on any element's boundary),
+  // the first `room` of them
   template <int N> static __device__ __forceinline__ void store(uint16_t* p, const float* v) {
     typedef __attribute__((ext_vector_type(N))) __bf16 b;
     typedef __attribute__((ext_vector_type(N))) float f;
@@ -60,6 +60,19 @@ template <> struct lin_io<uint16_t> {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = v[i];
     *reinterpret_cast<b*>(p) = __builtin_convertvector(x, b);
+  }
+  template <int N> static __device__ __forceinline__ void put(uint16_t* p, const float* v, int room) {
+    typedef __attribute__((ext_vector_type(N))) __bf16 b;
+    typedef __attribute__((ext_vector_type(N))) float f;
+    typedef b loose __attribute__((aligned(2)));
+    f x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = v[i];
+    if (room >= N)
+      *reinterpret_cast<loose*>(p) = __builtin_convertvector(x, b);
+    else
+      for (int i = 0; i < N; ++i)
+        if (i < room) p[i] = bf16_rne(v[i]);
   }
 };
 template <> struct lin_io<float> {
@@ -84,10 +97,19 @@ template <> struct lin_io<float> {
   static __device__ __forceinline__ f32x8 wide(frag a) { return a; }
   static __device__ __forceinline__ frag round(f32x8 a) { return a; }
   static __device__ __forceinline__ float widen(float b) { return b; }
-  static __device__ __forceinline__ float narrow(float v) { return v; }
   template <int N> static __device__ __forceinline__ void store(float* p, const float* v) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  }
+  template <int N> static __device__ __forceinline__ void put(float* p, const float* v, int room) {
+    typedef f32x4 loose __attribute__((aligned(4)));
+    if (room >= N) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<loose*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+      for (int i = 0; i < N; ++i)
+        if (i < room) p[i] = v[i];
+    }
   }
 };
 
@@ -132,6 +154,19 @@ __device__ __forceinline__ float lin_decay(float log2d) {
 // fp32 channels.
 template <typename T, int KD> constexpr int lin_chunk_of() { return sizeof(T) == 4 && KD == 256 ? 32 : 64; }
 
+// Wavefronts a SIMD is to hold: two workgroups of a compute unit hide each other's waits; states of 256 x 32
+// and more in a wavefront's registers leave room for one.
+template <typename T, int KD, int NT> constexpr int lin_waves() { return KD * NT * (sizeof(T) == 4 ? 2 : 1) <= 256 ? 2 : 1; }
+
+// What the tokens of a chunk are to one another.
+template <int C> struct LinDecays {
+  float hi[C], lo[C];       // log2 of the decays since the chunk's start, in two parts
+  float f[C], w[C];         // factor of a row's product with the state; of a row's share in the new state
+  int lim[C];               // the row's first visible key (forward), its last (backward)
+  float carry;
+  int fresh;                // a token of the chunk starts anew
+};
+
 template <typename T, int KD, int NT, bool STATE, int NPP>
 struct alignas(16) LinShared {
   static constexpr int C = lin_chunk_of<T, KD>();
@@ -140,50 +175,79 @@ struct alignas(16) LinShared {
   T k[C * kLdK];
   T v[C * kLdV];
   T p[STATE ? 8 : NPP * C * kLdP];
-  float hi[C], lo[C];       // log2 of the decays since the chunk's start, in two parts
-  float f[C], w[C];         // factor of a row's product with the state; of a row's share in the new state
-  int lim[C];               // the row's first visible key (forward), its last (backward)
+  LinDecays<C> dec[2];      // this job's, and the next one's
   float dot[4][C];
-  float carry;
-  int fresh;                // a token of the chunk starts anew
   int bad;
 };
 
-// Rows lo .. hi - 1 of a [tokens][heads][width] tensor (of `rows`, from token t0) into an LDS tile of
-// W columns; zeros elsewhere.
+// An operand's tile of C rows and W columns on its way: rows lo .. hi - 1 of `rows` tokens, zeros
+// elsewhere.  A thread has 16-byte pieces of a row (on any element's boundary); where the width is
+// not a multiple of a piece, the end of row `lane` is a piece of wavefront `tail`'s own.
 template <typename T, int W, int LD, int C>
-__device__ __forceinline__ void lin_tile(T* tile, const LinTensor& x, int64_t b, int64_t h, int64_t t0, int lo, int hi, int col0,
-                                         int width, int tid) {
-  constexpr int V = lin_io<T>::kVec, kPieces = W / V;
-  const T* base = static_cast<const T*>(x.p) + b * x.sb + t0 * x.sl + (h / x.share) * x.sh + col0;
-  const int n = width - col0;
+struct LinTile {
+  static constexpr int V = lin_io<T>::kVec, kPieces = W / V, kRows = 256 / kPieces, N = C / kRows;
+  u32x4 piece[N];
+  T end[V - 1];
+
+  __device__ __forceinline__ void load(const LinTensor& x, int64_t b, int64_t h, int64_t t0, int n, int lo, int hi, int col0,
+                                       int width, int tail) {
+    const int tid = threadIdx.x;
+    const T* base = static_cast<const T*>(x.p) + b * x.sb + t0 * x.sl + (h / x.share) * x.sh + col0;
+    const int sl = int(x.sl), cols = width - col0 < W ? width - col0 : W;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), (short)0, int(((n - 1) * sl + cols) * int(sizeof(T))),
+                                                        0x00020000);
+    const int row0 = tid / kPieces, c = (tid % kPieces) * V;
 #pragma unroll
-  for (int i = 0; i < C * kPieces / 256; ++i) {
-    const int at = tid + 256 * i, row = at / kPieces, c = (at % kPieces) * V;
-    u32x4 val = {0, 0, 0, 0};
-    const T* src = base + int64_t(row) * x.sl + c;
-    if (row >= lo && row < hi) {
-      if (x.vec && c + V <= n) {
-        val = *reinterpret_cast<const u32x4*>(src);
-      } else if (c < n) {
-        union { u32x4 v; T e[V]; } u;
-        u.v = val;
-        for (int e = 0; e < V; ++e)
-          if (c + e < n) u.e[e] = src[e];
-        val = u.v;
+    for (int i = 0; i < N; ++i) {
+      const int row = row0 + i * kRows;
+      const bool in = row >= lo && row < hi && c + V <= cols;
+      piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, in ? (row * sl + c) * int(sizeof(T)) : kOutside, 0, 0);
+    }
+    if (cols % V != 0 && (tid >> 6) == tail) {
+      const int row = tid & 63, first = cols - cols % V;
+#pragma unroll
+      for (int e = 0; e < V - 1; ++e) {
+        const bool in = row >= lo && row < hi && first + e < cols;
+        const int at = in ? (row * sl + first + e) * int(sizeof(T)) : kOutside;
+        if constexpr (sizeof(T) == 2)
+          end[e] = T(__builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0));
+        else
+          end[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0));
       }
     }
-    *reinterpret_cast<u32x4*>(tile + row * LD + c) = val;
   }
-}
+  __device__ __forceinline__ void store(T* tile, int col0, int width, int tail) const {
+    const int tid = threadIdx.x, cols = width - col0 < W ? width - col0 : W;
+    const int row0 = tid / kPieces, c = (tid % kPieces) * V;
+    // (the piece of a row's end is its owner's)
+    if (cols % V == 0 || c != cols - cols % V) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (row0 + i * kRows) * LD + c) = piece[i];
+    }
+    if (cols % V != 0 && (tid >> 6) == tail && (tid & 63) < C) {
+      union { u32x4 v; T e[V]; } u;
+      u.v = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < V - 1; ++e) u.e[e] = end[e];
+      *reinterpret_cast<u32x4*>(tile + (tid & 63) * LD + cols - cols % V) = u.v;
+    }
+  }
+  static constexpr int kOutside = 0x7ffffff0;    // beyond any tile: reads as zero
+};
+
+// What a workgroup does at once: the tokens lo .. hi - 1 of a chunk (all of it, or one token).
+struct LinJob {
+  int ci, lo, hi;
+  bool single;
+};
 
 // One workgroup of four wavefronts walks the chunks of one segment of one (batch row, head) for 64 NT
 // columns of v: wavefront w owns 16 NT of them, and the state's [KD][16 NT] in its accumulators,
 // which are at once the operand of its product with the queries.
 // STATE: only the state at the segment's end, from zero.
-// NS: parts that a fp32 value is split into where it meets the matrix cores (P and the state; 1 rounds it).
+// NS: parts that a fp32 value is split into where it meets the matrix cores (the state; 3: the pairs too).
 template <typename T, int KD, int NT, bool REV, bool STATE, int NS>
-__global__ __launch_bounds__(256) void lin_kernel(LinParams p) {
+__global__ __launch_bounds__(256, (lin_waves<T, KD, NT>())) void lin_kernel(LinParams p) {
   using io = lin_io<T>;
   using frag = typename io::frag;
   constexpr int NP = sizeof(T) == 2 ? NS : 1, NPP = NP == 3 ? 3 : 1;
@@ -232,6 +296,66 @@ __global__ __launch_bounds__(256) void lin_kernel(LinParams p) {
             if (kd < p.kd && n < p.vd) f(S[a][u][t], r, p.s_row * kd + p.s_col * n);
           }
   };
+
+  auto start_of = [&](int ci) { return (chunk0 + (REV ? chunks - 1 - ci : ci)) * C; };
+  auto tokens_of = [&](int64_t t0) { return int(p.L - t0 < C ? p.L - t0 : C); };
+  auto whole = [&](int ci) { return LinJob{ci, 0, tokens_of(start_of(ci)), false}; };
+  auto first_token = [&](int ci) {
+    const int t = REV ? tokens_of(start_of(ci)) - 1 : 0;
+    return LinJob{ci, t, t + 1, true};
+  };
+
+  LinTile<T, KD, Sh::kLdK, C> tq, tk;
+  LinTile<T, 64 * NT, Sh::kLdV, C> tv;
+  float gate = 0.f;
+  auto load = [&](const LinJob& j) {
+    const int64_t t0 = start_of(j.ci);
+    const int n = tokens_of(t0);
+    if (!STATE) tq.load(p.q, b, h, t0, n, j.lo, j.hi, 0, p.kd, 0);
+    tk.load(p.k, b, h, t0, n, j.lo, j.hi, 0, p.kd, 1);
+    tv.load(p.v, b, h, t0, n, j.lo, j.hi, col0, p.vd, 2);
+    if (wave == 3) {
+      gate = 0.f;
+      if (lane >= j.lo && lane < j.hi) gate = p.g[b * p.g_sb + (t0 + lane) * p.g_sl + h * p.g_sh];
+    }
+  };
+
+  double total = 0.0;                             // STATE: log2 of the segment's decay
+  bool anew = false;
+  // the factors of a job's tokens, of the gates that wavefront 3 has loaded
+  auto decays = [&](LinDecays<C>& d) {
+    double c = double(gate) * 1.4426950408889634;
+    const bool start = c < -150.0;                // a decay below 2^-150 is none at all
+    if (start) c = 0.0;
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+      const double o = __shfl_up(c, s);
+      if (lane >= s) c += o;
+    }
+    const uint64_t starts = __ballot(start);
+    const double all = __shfl(c, 63);
+    const uint64_t upto = (uint64_t(2) << lane) - 1;
+    const uint64_t before = starts & upto, after = starts & ~upto;
+    const float in = before ? 0.f : lin_decay(float(c));
+    const float out = after ? 0.f : lin_decay(float(all - c));
+    if (lane < C) {
+      d.hi[lane] = float(c);
+      d.lo[lane] = float(c - double(float(c)));
+      d.f[lane] = (REV ? out : in) * p.fscale;
+      d.w[lane] = (REV ? in : out) * p.wscale;
+      d.lim[lane] = REV ? (after ? __builtin_ctzll(after) - 1 : C) : (before ? 63 - __builtin_clzll(before) : 0);
+    }
+    if (lane == 0) {
+      d.carry = lin_decay(float(all));
+      d.fresh = starts != 0;
+    }
+    if (STATE) {
+      total += all;
+      anew |= starts != 0;
+    }
+  };
+
+  LinJob job = whole(0);
   zero_state();
   if (!STATE) {
     if (p.nseg > 1) {
@@ -247,253 +371,213 @@ __global__ __launch_bounds__(256) void lin_kernel(LinParams p) {
     }
   }
 
-  double total = 0.0;                             // STATE: log2 of the segment's decay
-  bool anew = false, slow = false;
-  if (tid == 0) sh.bad = 0;
+  // A chunk is first walked as a whole.  Inside it a token is kept from another by a zero factor, which
+  // an infinity or a NaN would turn into a NaN: if anything that comes out is not finite, what the
+  // wavefront has formed is dropped and the chunk is walked token by token.  `done`: what this
+  // wavefront formed of the whole chunk stands.
+  bool done = false, retry = false, ahead = false;
+  for (int cur = 0;; cur ^= 1) {
+    LinDecays<C>& dec = sh.dec[cur];
+    if (!ahead) {
+      load(job);
+      if (wave == 3) decays(dec);
+    }
+    const int64_t t0 = start_of(job.ci);
+    if (!STATE) tq.store(sh.q, 0, p.kd, 0);
+    tk.store(sh.k, 0, p.kd, 1);
+    tv.store(sh.v, col0, p.vd, 2);
+    __syncthreads();
+    // ---- the next job's operands are asked for
+    LinJob next = job;
+    if (job.single && (REV ? job.lo > 0 : job.hi < tokens_of(t0))) {
+      next.lo += REV ? -1 : 1;
+      next.hi = next.lo + 1;
+    } else if (job.ci + 1 < chunks) {
+      next = STATE && retry ? first_token(job.ci + 1) : whole(job.ci + 1);
+    } else {
+      next.ci = chunks;
+    }
+    if (next.ci < chunks) load(next);
+    if (!STATE && tid == 0) sh.bad = 0;
 
-  for (int ci = 0; ci < chunks; ++ci) {
-    const int64_t t0 = (chunk0 + (REV ? chunks - 1 - ci : ci)) * C;
-    const int n = int(p.L - t0 < C ? p.L - t0 : C);
-    // First the whole chunk.  Inside a chunk a token is kept from another by a zero factor, which an
-    // infinity or a NaN would turn into a NaN: if anything that comes out is not finite, what the
-    // wavefront has formed is dropped and the chunk is walked token by token.
-    bool done = false;
-    int lo = 0, hi = n;
-    if (STATE && slow) { lo = REV ? n - 1 : 0; hi = lo + 1; }
-    bool single = STATE && slow;
-    for (;;) {
-      // ---- the chunk's tiles and decays
-      if (!STATE) lin_tile<T, KD, Sh::kLdK, C>(sh.q, p.q, b, h, t0, lo, hi, 0, p.kd, tid);
-      lin_tile<T, KD, Sh::kLdK, C>(sh.k, p.k, b, h, t0, lo, hi, 0, p.kd, tid);
-      lin_tile<T, 64 * NT, Sh::kLdV, C>(sh.v, p.v, b, h, t0, lo, hi, col0, p.vd, tid);
-      if (wave == 0) {
-        double c = 0.0;
-        bool start = false;
-        if (lane >= lo && lane < hi) {
-          c = double(p.g[b * p.g_sb + (t0 + lane) * p.g_sl + h * p.g_sh]) * 1.4426950408889634;
-          start = c < -150.0;                     // a decay below 2^-150 is none at all
-          if (start) c = 0.0;
-        }
+    // ---- the pairs: P_ij = e^{c_i - c_j} (q_i . k_j), as its transpose's tiles (lane: one i, four j)
+    if (!STATE) {
+      constexpr int kUnits = C == 64 ? 6 : 2;     // 16 rows by 32 keys, those that see each other
+#pragma unroll 1
+      for (int unit = wave; unit < kUnits; unit += 4) {
+        // C = 64 forward: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1); backward: (3,1) (2,1) (1,1) (1,0) (0,1) (0,0)
+        int it = C == 32 ? unit : unit < 2 ? unit : unit / 2 + 1, ks = C == 32 || unit < 2 ? 0 : unit & 1;
+        if (REV) { it = IT - 1 - it; ks = KS - 1 - ks; }
+        f32x4 acc[2] = {};
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-          const double o = __shfl_up(c, d);
-          if (lane >= d) c += o;
+        for (int a = 0; a < KK; ++a) {
+          const frag fq = io::row(sh.q + (16 * it + l16) * Sh::kLdK + 32 * a + 8 * g);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            acc[u] = io::mma(io::row(sh.k + (32 * ks + 16 * u + l16) * Sh::kLdK + 32 * a + 8 * g), fq, acc[u]);
         }
-        const uint64_t starts = __ballot(start);
-        const double all = __shfl(c, 63);
-        const uint64_t upto = (uint64_t(2) << lane) - 1;
-        const uint64_t before = starts & upto, after = starts & ~upto;
-        const float in = before ? 0.f : lin_decay(float(c));
-        const float out = after ? 0.f : lin_decay(float(all - c));
-        if (lane < C) {
-          sh.hi[lane] = float(c);
-          sh.lo[lane] = float(c - double(float(c)));
-          sh.f[lane] = (REV ? out : in) * p.fscale;
-          sh.w[lane] = (REV ? in : out) * p.wscale;
-          sh.lim[lane] = REV ? (after ? __builtin_ctzll(after) - 1 : C) : (before ? 63 - __builtin_clzll(before) : 0);
-        }
-        if (lane == 0) {
-          sh.carry = lin_decay(float(all));
-          sh.fresh = starts != 0;
-        }
-        if (STATE) {
-          total += all;
-          anew |= starts != 0;
+        const int i = 16 * it + l16;
+        const float chi = dec.hi[i], clo = dec.lo[i];
+        const int lim = dec.lim[i];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j0 = 32 * ks + 16 * u + 4 * g;
+          float val[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = j0 + r;
+            const float d = (chi - dec.hi[j]) + (clo - dec.lo[j]);
+            const bool seen = REV ? j >= i && j <= lim : j <= i && j >= lim;
+            val[r] = seen ? acc[u][r] * (__builtin_amdgcn_exp2f(REV ? -d : d) * p.pscale) : 0.f;
+          }
+#pragma unroll
+          for (int x = 0; x < NPP; ++x) {
+            io::template store<4>(sh.p + (x * C + i) * Sh::kLdP + j0, val);
+            if (x + 1 < NPP)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) val[r] = lin_rest(val[r]);
+          }
         }
       }
       __syncthreads();
-      if (!STATE && tid == 0) sh.bad = 0;
+    }
 
-      // ---- the pairs: P_ij = e^{c_i - c_j} (q_i . k_j), as its transpose's tiles (lane: one i, four j)
+    if (!done) {
+      frag fv[KS][NT];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          fv[ks][t] = lin_column<T>(sh.v, Sh::kLdV, 32 * ks + 8 * g, wcol + 4 * t, kSpread, l16);
+
+      bool fine = true;
       if (!STATE) {
+        // ---- out^T: columns of v down, tokens across
+        f32x4 acc[IT][NT] = {};
 #pragma unroll
-        for (int unit = wave; unit < IT * KS; unit += 4) {
-          const int it = unit / KS, ks = unit % KS;
-          if (REV ? 32 * ks + 31 < 16 * it : 32 * ks > 16 * it + 15) continue;
-          f32x4 acc[2] = {};
-#pragma unroll
-          for (int a = 0; a < KK; ++a) {
-            const frag fq = io::row(sh.q + (16 * it + l16) * Sh::kLdK + 32 * a + 8 * g);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              acc[u] = io::mma(io::row(sh.k + (32 * ks + 16 * u + l16) * Sh::kLdK + 32 * a + 8 * g), fq, acc[u]);
-          }
-          const int i = 16 * it + l16;
-          const float chi = sh.hi[i], clo = sh.lo[i];
-          const int lim = sh.lim[i];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int j0 = 32 * ks + 16 * u + 4 * g;
-            float val[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int j = j0 + r;
-              const float d = (chi - sh.hi[j]) + (clo - sh.lo[j]);
-              const bool seen = REV ? j >= i && j <= lim : j <= i && j >= lim;
-              val[r] = seen ? acc[u][r] * (__builtin_amdgcn_exp2f(REV ? -d : d) * p.pscale) : 0.f;
-            }
-#pragma unroll
-            for (int x = 0; x < NPP; ++x) {
-              io::template store<4>(sh.p + (x * C + i) * Sh::kLdP + j0, val);
-              if (x + 1 < NPP)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) val[r] = lin_rest(val[r]);
-            }
-          }
-        }
-        __syncthreads();
-      }
-
-      if (!done) {
-        frag fv[KS][NT];
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int a = 0; a < KK; ++a) {
+          frag fs[NT][NP];
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            fv[ks][t] = lin_column<T>(sh.v, Sh::kLdV, 32 * ks + 8 * g, wcol + 4 * t, kSpread, l16);
-
-        bool fine = true;
-        if (!STATE) {
-          // ---- out^T: columns of v down, tokens across
-          f32x4 acc[IT][NT] = {};
-#pragma unroll
-          for (int a = 0; a < KK; ++a) {
-            frag fs[NT][NP];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              lin_split<T, NP>(__builtin_shufflevector(S[a][0][t], S[a][1][t], 0, 1, 2, 3, 4, 5, 6, 7), fs[t]);
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-              const frag fq = io::row(sh.q + (16 * it + l16) * Sh::kLdK + 32 * a + 8 * g);
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int x = 0; x < NP; ++x) acc[it][t] = io::mma(fs[t][x], fq, acc[it][t]);
-            }
-          }
-          float chk = 0.f;
+            lin_split<T, NP>(__builtin_shufflevector(S[a][0][t], S[a][1][t], 0, 1, 2, 3, 4, 5, 6, 7), fs[t]);
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
-            const float f = sh.f[16 * it + l16];
+            const frag fq = io::row(sh.q + (16 * it + l16) * Sh::kLdK + 32 * a + 8 * g);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[it][t][r] = f == 0.f ? 0.f : acc[it][t][r] * f;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              if (REV ? 32 * ks + 31 < 16 * it : 32 * ks > 16 * it + 15) continue;
-#pragma unroll
-              for (int x = 0; x < NPP; ++x) {
-                const frag fp = io::row(sh.p + (x * C + 16 * it + l16) * Sh::kLdP + 32 * ks + 8 * g);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[it][t] = io::mma(fv[ks][t], fp, acc[it][t]);
-              }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) chk = fmaf(acc[it][t][r], 0.f, chk);
-          }
-          fine = single || __all(chk == 0.f);
-          if (fine) {
-            const int width = p.vd - col0;
-            const int cbase = wcol + 4 * NT * g;
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-              const int i = 16 * it + l16;
-              float val[4 * NT];
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) val[4 * t + r] = acc[it][t][r];
-              if (i >= lo && i < hi) {
-                const int64_t at = b * p.o_sb + (t0 + i) * p.o_sl + h * p.o_sh + col0 + cbase;
-                if (p.out_f32) {
-                  float* dst = static_cast<float*>(p.out) + at;
-                  if (p.out_vec && cbase + 4 * NT <= width)
-                    lin_io<float>::template store<4 * NT>(dst, val);
-                  else
-                    for (int e = 0; e < 4 * NT; ++e)
-                      if (cbase + e < width) dst[e] = val[e];
-                } else {
-                  T* dst = static_cast<T*>(p.out) + at;
-                  if (p.out_vec && cbase + 4 * NT <= width)
-                    io::template store<4 * NT>(dst, val);
-                  else
-                    for (int e = 0; e < 4 * NT; ++e)
-                      if (cbase + e < width) dst[e] = io::narrow(val[e]);
-                }
-              }
-              if (p.dot) {                        // out_i . x_i, for the decays' gradient
-                float sum = 0.f;
-                if (i >= lo && i < hi) {
-                  const T* x = static_cast<const T*>(p.x.p) + b * p.x.sb + (t0 + i) * p.x.sl + (h / p.x.share) * p.x.sh + col0 + cbase;
-                  for (int e = 0; e < 4 * NT; ++e)
-                    if (cbase + e < width) sum = fmaf(val[e], io::widen(x[e]), sum);
-                }
-                sum += __shfl_xor(sum, 16);
-                sum += __shfl_xor(sum, 32);
-                if (g == 0) sh.dot[wave][i] = sum;
-              }
-            }
-          } else if (lane == 0) {
-            sh.bad = 1;
+              for (int x = 0; x < NP; ++x) acc[it][t] = io::mma(fs[t][x], fq, acc[it][t]);
           }
         }
+        float chk = 0.f;
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          const float f = dec.f[16 * it + l16];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[it][t][r] = f == 0.f ? 0.f : acc[it][t][r] * f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            if (REV ? 32 * ks + 31 < 16 * it : 32 * ks > 16 * it + 15) continue;
+#pragma unroll
+            for (int x = 0; x < NPP; ++x) {
+              const frag fp = io::row(sh.p + (x * C + 16 * it + l16) * Sh::kLdP + 32 * ks + 8 * g);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) acc[it][t] = io::mma(fv[ks][t], fp, acc[it][t]);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) chk = fmaf(acc[it][t][r], 0.f, chk);
+        }
+        fine = job.single || __all(chk == 0.f);
         if (fine) {
-          // ---- the new state: w_j v_j in parts, so that nothing of what is added to fp32 is lost
-          const float keep = sh.carry;
-          const bool fresh = sh.fresh != 0;
+          const int cbase = wcol + 4 * NT * g, room = p.vd - col0 - cbase;   // columns that are there
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int i = 16 * it + l16;
+            const bool in = i >= job.lo && i < job.hi;
+            float val[4 * NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) val[4 * t + r] = acc[it][t][r];
+            if (in) {
+              const int64_t at = b * p.o_sb + (t0 + i) * p.o_sl + h * p.o_sh + col0 + cbase;
+              if (p.out_f32)
+                lin_io<float>::template put<4 * NT>(static_cast<float*>(p.out) + at, val, room);
+              else
+                io::template put<4 * NT>(static_cast<T*>(p.out) + at, val, room);
+            }
+            if (p.dot) {                          // out_i . x_i, for the decays' gradient
+              float sum = 0.f;
+              if (in) {
+                const T* x = static_cast<const T*>(p.x.p) + b * p.x.sb + (t0 + i) * p.x.sl + (h / p.x.share) * p.x.sh + col0 + cbase;
+                for (int e = 0; e < 4 * NT; ++e)
+                  if (e < room) sum = fmaf(val[e], io::widen(x[e]), sum);
+              }
+              sum += __shfl_xor(sum, 16);
+              sum += __shfl_xor(sum, 32);
+              if (g == 0) sh.dot[wave][i] = sum;
+            }
+          }
+        } else if (lane == 0) {
+          sh.bad = 1;
+        }
+      }
+      if (fine) {
+        // ---- the new state: w_j v_j in parts, so that nothing of what is added to fp32 is lost
+        const float keep = dec.carry;
+        const bool fresh = dec.fresh != 0;
+#pragma unroll
+        for (int a = 0; a < KK; ++a)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) S[a][u][t][r] = fresh ? 0.f : S[a][u][t][r] * keep;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          frag fw[NT][NW];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            f32x8 x = io::wide(fv[ks][t]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float w = dec.w[32 * ks + 8 * g + e];
+              x[e] = w == 0.f ? 0.f : w * x[e];
+            }
+            lin_split<T, NW>(x, fw[t]);
+          }
 #pragma unroll
           for (int a = 0; a < KK; ++a)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+              const frag fk = lin_column<T>(sh.k, Sh::kLdK, 32 * ks + 8 * g, 32 * a + 4 * u, 8, l16);
 #pragma unroll
               for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[a][u][t][r] = fresh ? 0.f : S[a][u][t][r] * keep;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            frag fw[NT][NW];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              f32x8 x = io::wide(fv[ks][t]);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float w = sh.w[32 * ks + 8 * g + e];
-                x[e] = w == 0.f ? 0.f : w * x[e];
-              }
-              lin_split<T, NW>(x, fw[t]);
+                for (int x = 0; x < NW; ++x) S[a][u][t] = io::mma(fk, fw[t][x], S[a][u][t]);
             }
-#pragma unroll
-            for (int a = 0; a < KK; ++a)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const frag fk = lin_column<T>(sh.k, Sh::kLdK, 32 * ks + 8 * g, 32 * a + 4 * u, 8, l16);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                  for (int x = 0; x < NW; ++x) S[a][u][t] = io::mma(fk, fw[t][x], S[a][u][t]);
-              }
-          }
-          done = !single;
         }
-      }
-      __syncthreads();
-      if (!STATE && p.dot && tid >= lo && tid < hi && sh.bad == 0)
-        p.dot[((int64_t(nb) * p.batch + b) * p.L + t0 + tid) * p.H + h] = sh.dot[0][tid] + sh.dot[1][tid] + sh.dot[2][tid] + sh.dot[3][tid];
-      if (single) {
-        if (REV ? --lo < 0 : ++lo == n) break;
-        hi = lo + 1;
-      } else {
-        if (STATE || sh.bad == 0) break;
-        single = true;
-        lo = REV ? n - 1 : 0;
-        hi = lo + 1;
+        done = !job.single;
       }
     }
-    if (STATE && !slow && ci == chunks - 1) {
-      // the same for a segment: from its start again, token by token
+    if (wave == 3 && next.ci < chunks) decays(sh.dec[cur ^ 1]);
+    __syncthreads();
+    const bool bad = !STATE && !job.single && sh.bad != 0;
+    if (!STATE && p.dot && !bad && tid >= job.lo && tid < job.hi)
+      p.dot[((int64_t(nb) * p.batch + b) * p.L + t0 + tid) * p.H + h] = sh.dot[0][tid] + sh.dot[1][tid] + sh.dot[2][tid] + sh.dot[3][tid];
+    ahead = true;
+    if (bad) {
+      next = first_token(job.ci);
+      ahead = false;
+    } else if (next.ci == chunks) {
+      if (!STATE || retry) break;
+      // the same for a segment's state: from its start again, token by token
       float chk = 0.f;
 #pragma unroll
       for (int a = 0; a < KK; ++a)
@@ -503,13 +587,15 @@ __global__ __launch_bounds__(256) void lin_kernel(LinParams p) {
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) chk = fmaf(S[a][u][t][r], 0.f, chk);
-      if (__syncthreads_or(chk != 0.f)) {
-        slow = true;
-        ci = -1;
-        total = 0.0;
-        zero_state();
-      }
+      if (!__syncthreads_or(chk != 0.f)) break;
+      retry = true;
+      total = 0.0;
+      zero_state();
+      next = first_token(0);
+      ahead = false;
     }
+    if (!next.single || STATE) done = false;
+    job = next;
   }
 
   if (STATE) {
@@ -520,7 +606,7 @@ __global__ __launch_bounds__(256) void lin_kernel(LinParams p) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           *reinterpret_cast<f32x4*>(seg_at + (((a * 2 + u) * NT + t) * 256 + tid) * 4) = S[a][u][t];
-    if (tid == 0 && nb == 0)
+    if (tid == 192 && nb == 0)
       p.seg_decay[bh * p.nseg + seg] = anew ? -1.f : lin_decay(float(total));
   } else if (p.s1 && seg == (REV ? 0 : p.nseg - 1)) {
     each_state([&](f32x4& s, int r, int64_t at) { p.s1[sbase + at] = s[r]; });
