@@ -6,8 +6,8 @@ namespace selscan {
 
 hipError_t launch_lin_bf16_64(bool rev, bool state, const LinParams& p, hipStream_t stream) {
   if (p.vd <= 64)
-    return p.parts == 3 ? lin_dispatch<uint16_t, 64, 1, 3>(rev, state, p, stream) : lin_dispatch<uint16_t, 64, 1, 2>(rev, state, p, stream);
-  return p.parts == 3 ? lin_dispatch<uint16_t, 64, 2, 3>(rev, state, p, stream) : lin_dispatch<uint16_t, 64, 2, 2>(rev, state, p, stream);
+    return p.parts == 3 ? lin_dispatch<uint16_t, 64, 4, 3>(rev, state, p, stream) : lin_dispatch<uint16_t, 64, 4, 2>(rev, state, p, stream);
+  return p.parts == 3 ? lin_dispatch<uint16_t, 64, 8, 3>(rev, state, p, stream) : lin_dispatch<uint16_t, 64, 8, 2>(rev, state, p, stream);
 }
 
 }  // namespace selscan

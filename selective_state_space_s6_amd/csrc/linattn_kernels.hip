@@ -12,14 +12,14 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 // Segment states, from zero, into the states that enter the segments, in place: s := e^c s + own.
 template <bool REV>
-__global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams p, int KD, int NT) {
-  const int block = KD * 64 * NT, at = (blockIdx.x % (block / 1024)) * 1024 + threadIdx.x * 4;
+__global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams p, int KD, int cols) {
+  const int block = KD * cols, at = (blockIdx.x % (block / 1024)) * 1024 + threadIdx.x * 4;
   const int64_t item = blockIdx.x / (block / 1024), bh = item / p.nblk;
   const int nb = int(item % p.nblk);
-  // the place in the walk's layout: [a][u][t] by [256 threads][4 rows]
-  const int tid = (at / 4) % 256, t = (at / 1024) % NT, u = (at / 1024 / NT) % 2, a = at / 1024 / NT / 2;
+  // the place in the walk's layout: [a][u] by [threads][4 rows]
+  const int threads = cols * 4, tid = (at / 4) % threads, u = at / 4 / threads % 2, a = at / 4 / threads / 2;
   const int l16 = tid & 15, g = (tid & 63) >> 4;
-  const int n = nb * 64 * NT + (tid >> 6) * 16 * NT + 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3);
+  const int n = nb * cols + (tid >> 6) * 16 + l16;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
   if (p.s0)
     for (int r = 0; r < 4; ++r) {
@@ -196,12 +196,12 @@ hipError_t launch_lin(bool bf16, bool rev, const LinParams& p, hipStream_t strea
   if (p.nseg > 1) {
     e = lin_walk(bf16, rev, true, p, stream);
     if (e != hipSuccess) return e;
-    const int KD = lin_kd(p.kd), NT = lin_cols(p.vd) / 64;
-    const dim3 grid(uint32_t(p.batch * p.H * p.nblk * (KD * 64 * NT / 1024)));
+    const int KD = lin_kd(p.kd), cols = lin_cols(p.vd);
+    const dim3 grid(uint32_t(p.batch * p.H * p.nblk * (KD * cols / 1024)));
     if (rev)
-      lin_prefix_kernel<true><<<grid, dim3(256), 0, stream>>>(p, KD, NT);
+      lin_prefix_kernel<true><<<grid, dim3(256), 0, stream>>>(p, KD, cols);
     else
-      lin_prefix_kernel<false><<<grid, dim3(256), 0, stream>>>(p, KD, NT);
+      lin_prefix_kernel<false><<<grid, dim3(256), 0, stream>>>(p, KD, cols);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
