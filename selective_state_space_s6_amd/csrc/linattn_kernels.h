@@ -19,11 +19,13 @@
 namespace selscan {
 namespace {
 
+typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(8))) float f32x8;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
@@ -100,11 +102,23 @@ template <> struct lin_io<float> {
 // not finite, neither is the sum.
 template <typename T, int N>
 __device__ __forceinline__ void lin_split(f32x8 x, typename lin_io<T>::frag* out) {
-  out[0] = lin_io<T>::round(x);
+  if constexpr (sizeof(T) == 4) {
+    out[0] = x;
+  } else {
+    u32x4 part[N];
 #pragma unroll
-  for (int n = 1; n < N; ++n) {
-    x -= lin_io<T>::wide(out[n - 1]);
-    out[n] = lin_io<T>::round(x);
+    for (int i = 0; i < 4; ++i) {
+      float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const uint32_t r = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+        part[n][i] = r;
+        a -= __uint_as_float(r << 16);
+        b -= __uint_as_float(r & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) out[n] = __builtin_bit_cast(bf16x8, part[n]);
   }
 }
 
@@ -128,14 +142,14 @@ template <typename T, int KD, int NW, bool STATE> constexpr int lin_waves() {
 }
 
 // What the tokens of a chunk are to one another.
-template <int C> struct LinDecays {
+template <int C> struct alignas(16) LinDecays {
   float hi[C], lo[C];       // log2 of the decays since the chunk's start, in two parts
   float f[C], w[C];         // factor of a row's product with the state; of a row's share in the new state
   int lim[C];               // the row's first visible key (forward), its last (backward)
   float carry;              // of the state over the chunk
 };
 
-template <typename T, int KD, int NW, bool STATE, int NPP>
+template <typename T, int KD, int NW, bool STATE, bool DOT, int NPP>
 struct alignas(16) LinShared {
   static constexpr int C = lin_chunk_of<T, KD>(), kWP = C * int(sizeof(T)) < 128 ? 128 / int(sizeof(T)) : C;
   T q[STATE ? 8 : C * KD];
@@ -143,7 +157,7 @@ struct alignas(16) LinShared {
   T v[C * 16 * NW];
   T p[STATE ? 8 : NPP * C * kWP];
   LinDecays<C> dec[2];      // this chunk's, and the next one's
-  float dot[STATE ? 1 : NW][C];
+  float dot[DOT ? NW : 1][DOT ? C : 1];
   int bad;
 };
 
@@ -158,22 +172,22 @@ struct LinTile {
   static constexpr int kOutside = 0x7ffffff0;    // beyond any tile: reads as zero
   u32x4 piece[N];
   const T* base;          // the head's first token
-  int sl, cols, at;
+  int sl, cols;
 
   __device__ __forceinline__ void init(const LinTensor& x, int64_t b, int64_t h, int col0, int width) {
     base = static_cast<const T*>(x.p) + b * x.sb + (h / x.share) * x.sh + col0;
     sl = int(x.sl);
     cols = width - col0 < W ? width - col0 : W;
-    int c = (int(threadIdx.x) % kPieces) * V;
-    const bool in = c < cols && cols >= V;
-    if (c + V > cols) c = cols - V;
-    at = in ? (int(threadIdx.x) / kPieces * sl + c) * int(sizeof(T)) : kOutside;
   }
-  __device__ __forceinline__ void load(int64_t t0, int n) {
-    const int row0 = int(threadIdx.x) / kPieces;
+  __device__ __forceinline__ void load(int tid, int64_t t0, int n) {
+    const int row0 = tid / kPieces;
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base + t0 * sl), (short)0,
                                                         int(((n - 1) * sl + cols) * int(sizeof(T))), 0x00020000);
     const int step = kRows * sl * int(sizeof(T));
+    int c = (tid % kPieces) * V;
+    const bool in = c < cols && cols >= V;
+    if (c + V > cols) c = cols - V;
+    const int at = in ? (row0 * sl + c) * int(sizeof(T)) : kOutside;
     if (n == C) {
 #pragma unroll
       for (int i = 0; i < N; ++i) piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + i * step, 0, 0);
@@ -211,14 +225,14 @@ struct LinTile {
 // columns of v: a wavefront owns 16 of them, and the state's [KD][16] in its accumulators, which are at
 // once the operand of its product with the queries.
 // STATE: only the state at the segment's end, from zero.
-// NS: parts that a fp32 value is split into where it meets the matrix cores (the state; 3: the pairs too).
-template <typename T, int KD, int NW, bool REV, bool STATE, int NS>
+// DOT: the rows' products with x too; then the parts of P and of the state have 24 bits, else the state's 16.
+template <typename T, int KD, int NW, bool REV, bool STATE, bool DOT>
 __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_kernel(LinParams p) {
   using io = lin_io<T>;
   using frag = typename io::frag;
-  constexpr int NP = sizeof(T) == 2 ? NS : 1, NPP = NP == 3 ? 3 : 1;
+  constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2, NPP = NP == 3 ? 3 : 1;   // parts of fp32 values on the matrix cores
   constexpr int NX = sizeof(T) == 2 ? 3 : 1;      // the state is held in fp32: what is added to it keeps 24 bits
-  using Sh = LinShared<T, KD, NW, STATE, NPP>;
+  using Sh = LinShared<T, KD, NW, STATE, DOT, NPP>;
   constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * NW, kWP = Sh::kWP, kThreads = 64 * NW;
   constexpr int kDecayWave = NW - 1;              // has the least to do with the pairs
   __shared__ Sh sh;
@@ -264,15 +278,24 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   if (!STATE) tq.init(p.q, b, h, 0, p.kd);
   tk.init(p.k, b, h, 0, p.kd);
   tv.init(p.v, b, h, col0, p.vd);
+  float* const dots = p.dot + (int64_t(nb) * p.batch + b) * p.L * p.H + h;
   const float* const gates = p.g + b * p.g_sb + h * p.g_sh;
   float gate = 0.f;
   auto load = [&](int ci) {
-    const int64_t t0 = start_of(ci);
+    // (places in the tiles and tensors are formed again for each chunk: kept, they would not leave the
+    // registers room)
+    int64_t t0 = start_of(ci);
+    int tid = threadIdx.x;
+    asm volatile("" : "+s"(t0), "+v"(tid));
     const int n = tokens_of(t0);
-    if (!STATE) tq.load(t0, n);
-    tk.load(t0, n);
-    tv.load(t0, n);
-    if (wave == kDecayWave) gate = lane < n ? gates[(t0 + lane) * p.g_sl] : 0.f;
+    if (!STATE) tq.load(tid, t0, n);
+    tk.load(tid, t0, n);
+    tv.load(tid, t0, n);
+    if (wave == kDecayWave) {
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(gates + t0 * p.g_sl), (short)0,
+                                                          ((n - 1) * int(p.g_sl) + 1) * 4, 0x00020000);
+      gate = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, (tid & 63) < n ? (tid & 63) * int(p.g_sl) * 4 : 0x7ffffff0, 0, 0));
+    }
   };
 
   double total = 0.0;                             // STATE: log2 of the segment's decay
@@ -316,11 +339,20 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       int it = C == 32 ? unit : unit < 2 ? unit : unit / 2 + 1, ks = C == 32 || unit < 2 ? 0 : unit & 1;
       if (REV) { it = IT - 1 - it; ks = KS - 1 - ks; }
       f32x4 acc[2] = {};
+      frag fq[2], fk[2][2];                       // (those of the next product on their way during this one)
+      auto ask = [&](int a) {
+        fq[a & 1] = io::template row<KD>(sh.q, 16 * it + l16, 32 * a + 8 * g);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) fk[a & 1][u] = io::template row<KD>(sh.k, 32 * ks + 16 * u + l16, 32 * a + 8 * g);
+      };
+      ask(0);
 #pragma unroll
       for (int a = 0; a < KK; ++a) {
-        const frag fq = io::template row<KD>(sh.q, 16 * it + l16, 32 * a + 8 * g);
+        if (a + 1 < KK) ask(a + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) acc[u] = io::mma(io::template row<KD>(sh.k, 32 * ks + 16 * u + l16, 32 * a + 8 * g), fq, acc[u]);
+        for (int u = 0; u < 2; ++u) acc[u] = io::mma(fk[a & 1][u], fq[a & 1], acc[u]);
+        __builtin_amdgcn_sched_barrier(0);
       }
       const int i = 16 * it + l16;
       const float chi = dec.hi[i], clo = dec.lo[i];
@@ -351,16 +383,23 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   auto from_state = [&](const LinDecays<C>& dec) {
 #pragma unroll
     for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int kHalf = IT / 2;
+    frag fq[2][2], fs[NP];
+    auto ask = [&](int i) {
 #pragma unroll
-    for (int a = 0; a < KK; ++a) {
-      frag fs[NP];
-      lin_split<T, NP>(__builtin_shufflevector(S[a][0], S[a][1], 0, 1, 2, 3, 4, 5, 6, 7), fs);
+      for (int x = 0; x < 2; ++x) fq[i & 1][x] = io::template row<KD>(sh.q, 16 * (2 * (i % kHalf) + x) + l16, 32 * (i / kHalf) + 8 * g);
+    };
+    ask(0);
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        const frag fq = io::template row<KD>(sh.q, 16 * it + l16, 32 * a + 8 * g);
+    for (int i = 0; i < KK * kHalf; ++i) {
+      const int a = i / kHalf, it = 2 * (i % kHalf);
+      if (i + 1 < KK * kHalf) ask(i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (it == 0) lin_split<T, NP>(__builtin_shufflevector(S[a][0], S[a][1], 0, 1, 2, 3, 4, 5, 6, 7), fs);
 #pragma unroll
-        for (int x = 0; x < NP; ++x) acc[it] = io::mma(fs[x], fq, acc[it]);
-      }
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) acc[it + x] = io::mma(fs[n], fq[i & 1][x], acc[it + x]);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -378,64 +417,69 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   // ... and that of the pairs; false if something of it is not finite
   auto from_pairs = [&] {
     float chk = 0.f;
+    auto seen = [](int it, int ks) { return REV ? 32 * ks + 31 >= 16 * it : 32 * ks <= 16 * it + 15; };
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
+    for (int x = 0; x < NPP; ++x) {
+      frag fp[IT][KS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (REV ? 32 * ks + 31 < 16 * it : 32 * ks > 16 * it + 15) continue;
+      for (int it = 0; it < IT; ++it)
 #pragma unroll
-        for (int x = 0; x < NPP; ++x)
-          acc[it] = io::mma(fv[ks], io::template row<kWP>(sh.p + x * C * kWP, 16 * it + l16, 32 * ks + 8 * g), acc[it]);
-      }
+        for (int ks = 0; ks < KS; ++ks)
+          if (seen(it, ks)) fp[it][ks] = io::template row<kWP>(sh.p + x * C * kWP, 16 * it + l16, 32 * ks + 8 * g);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+          if (seen(it, ks)) acc[it] = io::mma(fv[ks], fp[it][ks], acc[it]);
+    }
+#pragma unroll
+    for (int it = 0; it < IT; ++it)
 #pragma unroll
       for (int r = 0; r < 4; ++r) chk = fmaf(acc[it][r], 0.f, chk);
-    }
     return __all(chk == 0.f);
   };
-  // four columns of a row of the chunk's tile of `out` (rows and columns that are not there: beyond it, dropped)
-  const int room = p.vd - (col0 + wcol + 4 * g);  // columns that are there
+  // Four columns of a row of the chunk's tile of `out`; rows and columns that are not there are beyond it,
+  // and dropped.
+  const int ocols = p.vd - (col0 + wcol), room = ocols - 4 * g;     // columns that are there
   const int osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
   char* const obase = static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + col0 + wcol) * oes;
-  const T* const xbase = p.dot ? static_cast<const T*>(p.x.p) + b * p.x.sb + (h / p.x.share) * p.x.sh + col0 + wcol : nullptr;
+  const T* const xbase = DOT ? static_cast<const T*>(p.x.p) + b * p.x.sb + (h / p.x.share) * p.x.sh + col0 + wcol : nullptr;
   auto write = [&](int64_t t0) {
     constexpr int kOutside = 0x7ffffff0;
-    const int n = tokens_of(t0), cols = p.vd - (col0 + wcol);
+    const int n = tokens_of(t0);
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(obase + t0 * osl * oes, (short)0,
-                                                        cols > 0 ? ((n - 1) * osl + cols) * oes : 0, 0x00020000);
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int i = 16 * it + l16;
-      const int to = i < n && room > 0 ? (i * osl + 4 * g) * oes : kOutside;
-      if (p.out_f32) {
-        if (room >= 4) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), rsrc, to, 0, 0);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 3; ++r)
-            if (r < room) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][r]), rsrc, to + 4 * r, 0, 0);
-        }
-      } else if constexpr (sizeof(T) == 4) {
-        if (room >= 4) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it]), rsrc, to, 0, 0);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 3; ++r)
-            if (r < room) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][r]), rsrc, to + 4 * r, 0, 0);
-        }
+                                                        ocols > 0 ? ((n - 1) * osl + ocols) * oes : 0, 0x00020000);
+    const int at = (l16 * osl + 4 * g) * oes, step = 16 * osl * oes;
+    auto put = [&](f32x4 v, int to) {
+      if (sizeof(T) == 4 || p.out_f32) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, to, 0, 0);
       } else {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_convertvector(acc[it], bf16x4));
-        if (room >= 4) {
-          __builtin_amdgcn_raw_buffer_store_b64(v, rsrc, to, 0, 0);
-        } else {
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4)), rsrc, to, 0, 0);
+      }
+    };
+    if (n == C && ocols >= 16) {
 #pragma unroll
-          for (int r = 0; r < 3; ++r)
-            if (r < room) __builtin_amdgcn_raw_buffer_store_b16((short)(v[r / 2] >> (16 * (r % 2))), rsrc, to + 2 * r, 0, 0);
+      for (int it = 0; it < IT; ++it) put(acc[it], at + it * step);
+    } else {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int to = 16 * it + l16 < n ? at + it * step : kOutside;
+        put(acc[it], room >= 4 ? to : kOutside);
+        if (room > 0 && room < 4) {
+#pragma unroll
+          for (int r = 0; r < 3; ++r) {
+            const int one = r < room ? to + r * oes : kOutside;
+            if (sizeof(T) == 4 || p.out_f32)
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][r]), rsrc, one, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b16((short)bf16_rne(acc[it][r]), rsrc, one, 0, 0);
+          }
         }
       }
     }
-    if (p.dot) {                                  // out_i . x_i, for the decays' gradient
+    if constexpr (DOT) {                          // out_i . x_i, for the decays' gradient
       const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(xbase + t0 * xsl), (short)0,
-                                                          cols > 0 ? ((n - 1) * xsl + cols) * int(sizeof(T)) : 0, 0x00020000);
+                                                          ocols > 0 ? ((n - 1) * xsl + ocols) * int(sizeof(T)) : 0, 0x00020000);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
         const int i = 16 * it + l16, at = i < n ? (i * xsl + 4 * g) * int(sizeof(T)) : kOutside;
@@ -463,24 +507,28 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[a][u][r] *= keep;
+    frag fk[2][2], fw[NX];
+    auto ask = [&](int i) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      frag fw[NX];
-      f32x8 x = io::wide(fv[ks]);
+      for (int u = 0; u < 2; ++u) fk[i & 1][u] = io::template column<KD>(sh.k, 32 * (i / KK) + 8 * g, 32 * (i % KK) + 4 * u, 8, l16);
+    };
+    ask(0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= dec.w[32 * ks + 8 * g + e];
-      lin_split<T, NX>(x, fw);
-#pragma unroll
-      for (int a = 0; a < KK; ++a) {
-        frag fk[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) fk[u] = io::template column<KD>(sh.k, 32 * ks + 8 * g, 32 * a + 4 * u, 8, l16);
-#pragma unroll
-        for (int n = 0; n < NX; ++n)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) S[a][u] = io::mma(fk[u], fw[n], S[a][u]);
-        __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < KS * KK; ++i) {
+      const int ks = i / KK, a = i % KK;
+      if (i + 1 < KS * KK) ask(i + 1);
+      if (a == 0) {
+        f32x8 x = io::wide(fv[ks]);
+        const f32x4* const w = reinterpret_cast<const f32x4*>(dec.w + 32 * ks + 8 * g);
+        x *= __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        lin_split<T, NX>(x, fw);
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < NX; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) S[a][u] = io::mma(fk[i & 1][u], fw[n], S[a][u]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -506,22 +554,21 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   if (!STATE && tid == 0) sh.bad = 0;
   for (;; ++ci) {
     LinDecays<C>& dec = sh.dec[ci & 1];
-    const int64_t t0 = start_of(ci);
-    // (places in the tiles are formed again for each chunk: kept, they would not leave the registers room)
+    int64_t t0 = start_of(ci);
     int at = tid;
-    asm volatile("" : "+v"(at));
+    asm volatile("" : "+s"(t0), "+v"(at));
     l16 = at & 15;
     g = (at & 63) >> 4;
     if (!STATE) tq.store(sh.q, at, t0, tokens_of(t0));
     tk.store(sh.k, at, t0, tokens_of(t0));
     tv.store(sh.v, at, t0, tokens_of(t0));
     __syncthreads();
-    if (ci + 1 < chunks) load(ci + 1);            // the next one's operands are asked for
     if (!STATE) {
       pairs(dec);
       from_state(dec);
       __syncthreads();
     }
+    if (ci + 1 < chunks) load(ci + 1);            // the next one's operands are asked for
     values();
     if (!STATE) {
       done = from_pairs();
@@ -534,11 +581,12 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     if (wave == kDecayWave && ci + 1 < chunks) decays(sh.dec[(ci + 1) & 1]);
     __syncthreads();
     if (!STATE && sh.bad != 0) break;
-    if (!STATE && p.dot && tid < tokens_of(t0)) {
+    if (DOT && at < tokens_of(t0)) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) sum += sh.dot[w][tid];
-      p.dot[((int64_t(nb) * p.batch + b) * p.L + t0 + tid) * p.H + h] = sum;
+      for (int w = 0; w < NW; ++w) sum += sh.dot[w][at];
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(dots + t0 * H, (short)0, (C - 1) * H * 4 + 4, 0x00020000);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, at * H * 4, 0, 0);
     }
     if (ci + 1 == chunks) break;
   }
@@ -561,6 +609,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   if (slow) {
     float* const row_q = reinterpret_cast<float*>(sh.k);           // [KD], and of k
     float* const row_k = row_q + KD;
+    asm volatile("" : "+s"(ci));                  // (its addresses are not to be kept up to date by the loop above)
 #pragma unroll 1
     for (; ci < chunks; ++ci) {
       const int64_t t0 = start_of(ci);
@@ -614,9 +663,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
               else
                 io::narrow(reinterpret_cast<T*>(obase) + t * osl + l16, out);
             }
-            if (p.dot) dot = out * io::widen(xbase[t * xsl + l16]);
+            if (DOT) dot = out * io::widen(xbase[t * xsl + l16]);
           }
-          if (p.dot) {
+          if constexpr (DOT) {
             // (what a wavefront whose first chunk stands has left there is that chunk's)
             for (int x = 8; x > 0; x /= 2) dot += __shfl_xor(dot, x);
             if (lane == 0 && !stands) sh.dot[wave][t - t0] = dot;
@@ -624,7 +673,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
             if (tid == 0) {
               float sum = 0.f;
               for (int w = 0; w < NW; ++w) sum += sh.dot[w][t - t0];
-              p.dot[((int64_t(nb) * p.batch + b) * p.L + t) * p.H + h] = sum;
+              dots[t * H] = sum;
             }
           }
         }
@@ -645,18 +694,19 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   }
 }
 
-template <typename T, int KD, int NW, bool REV, bool STATE, int NS>
+template <typename T, int KD, int NW, bool REV, bool STATE, bool DOT>
 hipError_t lin_launch(const LinParams& p, hipStream_t stream) {
   const int64_t items = p.batch * p.H * p.nblk * (STATE ? p.nseg - 1 : p.nseg);
   if (items == 0) return hipSuccess;
-  lin_kernel<T, KD, NW, REV, STATE, NS><<<dim3(uint32_t(items)), dim3(64 * NW), 0, stream>>>(p);
+  lin_kernel<T, KD, NW, REV, STATE, DOT><<<dim3(uint32_t(items)), dim3(64 * NW), 0, stream>>>(p);
   return hipGetLastError();
 }
 
-template <typename T, int KD, int NW, int NS>
+template <typename T, int KD, int NW>
 hipError_t lin_dispatch(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  if (state) return rev ? lin_launch<T, KD, NW, true, true, 1>(p, stream) : lin_launch<T, KD, NW, false, true, 1>(p, stream);
-  return rev ? lin_launch<T, KD, NW, true, false, NS>(p, stream) : lin_launch<T, KD, NW, false, false, NS>(p, stream);
+  if (state) return rev ? lin_launch<T, KD, NW, true, true, false>(p, stream) : lin_launch<T, KD, NW, false, true, false>(p, stream);
+  if (p.dot) return rev ? lin_launch<T, KD, NW, true, false, true>(p, stream) : lin_launch<T, KD, NW, false, false, true>(p, stream);
+  return rev ? lin_launch<T, KD, NW, true, false, false>(p, stream) : lin_launch<T, KD, NW, false, false, false>(p, stream);
 }
 
 }  // namespace

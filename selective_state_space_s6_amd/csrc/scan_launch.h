@@ -314,7 +314,6 @@ struct LinParams {
   int64_t nchunks;      // ceil(L / lin_chunk())
   int64_t seg_chunks;   // chunks of a segment
   int32_t nseg, nblk;   // segments; blocks of lin_cols() columns
-  int32_t parts;        // parts that fp32 values are split into for the bf16 matrix cores: 1, 2 or 3
 };
 constexpr int lin_kd(int64_t kd) { return kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
 constexpr int lin_cols(int64_t vd) { return vd <= 64 ? 64 : 128; }

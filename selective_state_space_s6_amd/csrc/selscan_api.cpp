@@ -1361,7 +1361,7 @@ static int lin_plan(const selscan_linattn_dims* dims, bool want_dg, LinPlan* out
   if (d.dk > 256 || d.dv > 256) return SELSCAN_ERR_UNSUPPORTED;
   const int64_t kMaxRow = int64_t(1) << 22;
   if (d.seqlen > 1)
-    for (int64_t s : {d.q_sl, d.k_sl, d.v_sl, d.o_sl})
+    for (int64_t s : {d.q_sl, d.k_sl, d.v_sl, d.o_sl, d.decay_tokens ? d.g_sl : int64_t(0)})
       if (s > kMaxRow) return SELSCAN_ERR_UNSUPPORTED;
   // workgroups of 256 threads, fewer than 2^32 threads a launch
   const int64_t kMaxItems = int64_t(1) << 22, wide = d.dk > d.dv ? d.dk : d.dv;
@@ -1424,7 +1424,6 @@ static selscan::LinParams lin_params(const LinWalk& w, const selscan::LinTensor&
   p.nchunks = w.nchunks; p.seg_chunks = w.seg_chunks; p.nseg = w.nseg; p.nblk = w.nblk;
   p.seg = static_cast<float*>(ws);
   p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(ws) + off_decay);
-  p.parts = 2;
   return p;
 }
 
@@ -1561,7 +1560,6 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
   if (want_dg) {
     p.x = tq;
     p.dot = reinterpret_cast<float*>(ws + pl.off_qdq);
-    p.parts = 3;
   }
   e = selscan::launch_lin(bf16, false, p, s);
   if (e == hipSuccess && shared)
@@ -1576,8 +1574,7 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
     if (want_dg) {
       p.x = tk;
       p.dot = reinterpret_cast<float*>(ws + pl.off_kdk);
-      p.parts = 3;
-    }
+      }
     e = selscan::launch_lin(bf16, true, p, s);
   }
   if (e == hipSuccess && shared)
