@@ -125,6 +125,14 @@ __device__ __forceinline__ void lin_split(f32x8 x, typename lin_io<T>::frag* out
 // What rounding to bfloat16 leaves of a value.
 __device__ __forceinline__ float lin_rest(float v) { return v - float(__bf16(v)); }
 
+// The lane's number, formed anew wherever it is asked for: kept, what is formed of it (places in tiles and
+// tensors) would not leave the walk's registers room.
+__device__ __forceinline__ int lin_lane() {
+  int zero = 0;
+  asm volatile("" : "+s"(zero));
+  return int(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, uint32_t(zero))));
+}
+
 // A product of decays that fp32 cannot hold is held at its smallest value: only a token that starts
 // anew ends an infinity.
 __device__ __forceinline__ float lin_decay(float log2d) {
@@ -165,59 +173,74 @@ struct alignas(16) LinShared {
 // thread has 16-byte pieces of a row (on any element's boundary).  Where the width is not a multiple of a
 // piece, the last one is read so that it ends where the row does, and its values are moved when they are
 // stored; rows shorter than a piece are read element by element then.
+// (What a call forms of `tid`, it forms again at each chunk: kept, it would not leave the registers room.)
 template <typename T, int W, int C, int THREADS>
 struct LinTile {
   static constexpr int V = lin_io<T>::kVec, kPieces = W / V, kRows = THREADS / kPieces, N = C / kRows;
   static_assert(N >= 1 && N * kRows == C, "");
   static constexpr int kOutside = 0x7ffffff0;    // beyond any tile: reads as zero
   u32x4 piece[N];
-  const T* base;          // the head's first token
+  const T* at;            // the next chunk's first token
   int sl, cols;
+  bool even;
 
-  __device__ __forceinline__ void init(const LinTensor& x, int64_t b, int64_t h, int col0, int width) {
-    base = static_cast<const T*>(x.p) + b * x.sb + (h / x.share) * x.sh + col0;
+  static __device__ __forceinline__ const T* head(const LinTensor& x, int64_t b, int64_t h, int col0) {
+    return static_cast<const T*>(x.p) + b * x.sb + (h / x.share) * x.sh + col0;
+  }
+  __device__ __forceinline__ void init(const LinTensor& x, int64_t b, int64_t h, int64_t t0, int col0, int width) {
+    at = head(x, b, h, col0) + t0 * x.sl;
     sl = int(x.sl);
     cols = width - col0 < W ? width - col0 : W;
+    even = cols % V == 0;
   }
-  __device__ __forceinline__ void load(int tid, int64_t t0, int n) {
-    const int row0 = tid / kPieces;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base + t0 * sl), (short)0,
-                                                        int(((n - 1) * sl + cols) * int(sizeof(T))), 0x00020000);
-    const int step = kRows * sl * int(sizeof(T));
+  // asks for the pieces of a chunk and goes on to the next
+  template <bool REV> __device__ __forceinline__ void load(int tid, int n) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), (short)0,
+                                                        ((n - 1) * sl + cols) * int(sizeof(T)), 0x00020000);
+    const int row0 = tid / kPieces, step = kRows * sl * int(sizeof(T));
     int c = (tid % kPieces) * V;
-    const bool in = c < cols && cols >= V;
+    const bool in = c < cols;
     if (c + V > cols) c = cols - V;
-    const int at = in ? (row0 * sl + c) * int(sizeof(T)) : kOutside;
+    const int to = in && c >= 0 ? (row0 * sl + c) * int(sizeof(T)) : kOutside;
     if (n == C) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + i * step, 0, 0);
+      for (int i = 0; i < N; ++i) piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, to + i * step, 0, 0);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = row0 + i * kRows;
-        piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, row < n ? at + i * step : kOutside, 0, 0);
-      }
+      for (int i = 0; i < N; ++i)
+        piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, row0 + i * kRows < n ? to + i * step : kOutside, 0, 0);
     }
+    at += (REV ? -int64_t(C) : int64_t(C)) * sl;
   }
-  __device__ __forceinline__ void store(T* tile, int tid, int64_t t0, int n) const {
-    const int row0 = tid / kPieces, c = (tid % kPieces) * V, odd = cols % V;
+  // ... and their place in the tile; `now`: the chunk's first token
+  __device__ __forceinline__ void store(T* tile, int tid, const T* now, int n) {
+    const int row0 = tid / kPieces, c = (tid % kPieces) * V;
+    if (!even) {
+      int cols = this->cols;
+      asm volatile("" : "+s"(cols));
+      const int by = (V - cols % V) * int(sizeof(T));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      u32x4 x = piece[i];
-      if (odd != 0 && c + V > cols) {             // the end of a row: down by V - odd values
-        const int by = (V - odd) * int(sizeof(T));
+      for (int i = 0; i < N; ++i) {
+        u32x4 x = piece[i];
         if (by & 2) x = u32x4{(x[0] >> 16) | (x[1] << 16), (x[1] >> 16) | (x[2] << 16), (x[2] >> 16) | (x[3] << 16), x[3] >> 16};
         if (by & 4) x = u32x4{x[1], x[2], x[3], 0};
         if (by & 8) x = u32x4{x[2], x[3], 0, 0};
+        if (c + V > cols) piece[i] = x;           // the end of a row: down by V - cols % V values
       }
-      *reinterpret_cast<u32x4*>(tile + lin_at<T, W>(row0 + i * kRows, c)) = x;
-    }
-    if (cols < V && c == 0) {
+      if (cols < V) {
+        if (c == 0)
 #pragma unroll 1
-      for (int row = row0; row < n; row += kRows)
+          for (int i = 0; i < N; ++i)
 #pragma unroll 1
-        for (int e = 0; e < cols; ++e) tile[lin_at<T, W>(row, e)] = base[(t0 + row) * sl + e];
+            for (int e = 0; e < V; ++e) {
+              const int row = row0 + i * kRows;
+              tile[lin_at<T, W>(row, e)] = e < cols && row < n ? now[int64_t(row) * sl + e] : T(0);
+            }
+        if (c == 0) return;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + lin_at<T, W>(row0 + i * kRows, c)) = piece[i];
   }
 };
 
@@ -237,9 +260,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   constexpr int kDecayWave = NW - 1;              // has the least to do with the pairs
   __shared__ Sh sh;
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  int l16 = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  int lane = lin_lane(), tid = 64 * wave + lane, l16 = lane & 15, g = lane >> 4;
   // The heads of a token lie next to one another, so the rows of one head are a power of two apart as a
   // rule, in one channel of the L2: an XCD takes the heads side by side.
   const int item = xcd_contiguous_block(blockIdx.x, gridDim.x);
@@ -259,6 +281,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   };
   // f(four state values, which of them, its place in the states' tensor)
   auto each_state = [&](auto&& f) {
+    const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int a = 0; a < KK; ++a)
 #pragma unroll
@@ -275,26 +298,26 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
 
   LinTile<T, KD, C, kThreads> tq, tk;
   LinTile<T, kWV, C, kThreads> tv;
-  if (!STATE) tq.init(p.q, b, h, 0, p.kd);
-  tk.init(p.k, b, h, 0, p.kd);
-  tv.init(p.v, b, h, col0, p.vd);
-  float* const dots = p.dot + (int64_t(nb) * p.batch + b) * p.L * p.H + h;
-  const float* const gates = p.g + b * p.g_sb + h * p.g_sh;
+  if (!STATE) tq.init(p.q, b, h, start_of(0), 0, p.kd);
+  tk.init(p.k, b, h, start_of(0), 0, p.kd);
+  tv.init(p.v, b, h, start_of(0), col0, p.vd);
+  constexpr int64_t kOn = REV ? -C : C;           // tokens from a chunk to the next
+  auto load = [&](int64_t t0) {
+    const int n = tokens_of(t0), tid = 64 * wave + lin_lane();
+    if (!STATE) tq.template load<REV>(tid, n);
+    tk.template load<REV>(tid, n);
+    tv.template load<REV>(tid, n);
+  };
+  // the log decays of a chunk, a chunk ahead of its operands
+  const float* gates = p.g + b * p.g_sb + h * p.g_sh + start_of(0) * p.g_sl;
+  const int gsl = int(p.g_sl);
   float gate = 0.f;
-  auto load = [&](int ci) {
-    // (places in the tiles and tensors are formed again for each chunk: kept, they would not leave the
-    // registers room)
-    int64_t t0 = start_of(ci);
-    int tid = threadIdx.x;
-    asm volatile("" : "+s"(t0), "+v"(tid));
-    const int n = tokens_of(t0);
-    if (!STATE) tq.load(tid, t0, n);
-    tk.load(tid, t0, n);
-    tv.load(tid, t0, n);
+  auto load_gate = [&](int64_t t0) {
     if (wave == kDecayWave) {
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(gates + t0 * p.g_sl), (short)0,
-                                                          ((n - 1) * int(p.g_sl) + 1) * 4, 0x00020000);
-      gate = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, (tid & 63) < n ? (tid & 63) * int(p.g_sl) * 4 : 0x7ffffff0, 0, 0));
+      const int n = tokens_of(t0), lane = lin_lane();
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(gates), (short)0, ((n - 1) * gsl + 1) * 4, 0x00020000);
+      gate = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, lane < n ? lane * gsl * 4 : 0x7ffffff0, 0, 0));
+      gates += kOn * gsl;
     }
   };
 
@@ -302,6 +325,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   bool anew = false;
   // the factors of a chunk's tokens, of the gates that kDecayWave has loaded
   auto decays = [&](LinDecays<C>& d) {
+    const int lane = lin_lane();
     double c = double(gate) * 1.4426950408889634;
     const bool start = c < -150.0;                // a decay below 2^-150 is none at all
     if (start) c = 0.0;
@@ -366,7 +390,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
           const int j = j0 + r;
           const float d = (chi - dec.hi[j]) + (clo - dec.lo[j]);
           const bool seen = REV ? j >= i && j <= lim : j <= i && j >= lim;
-          val[r] = seen ? acc[u][r] * (__builtin_amdgcn_exp2f(REV ? -d : d) * p.pscale) : 0.f;
+          val[r] = acc[u][r] * (__builtin_amdgcn_exp2f(seen ? (REV ? -d : d) : -1e30f) * p.pscale);
         }
 #pragma unroll
         for (int x = 0; x < NPP; ++x) {
@@ -440,14 +464,15 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   };
   // Four columns of a row of the chunk's tile of `out`; rows and columns that are not there are beyond it,
   // and dropped.
-  const int ocols = p.vd - (col0 + wcol), room = ocols - 4 * g;     // columns that are there
-  const int osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
-  char* const obase = static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + col0 + wcol) * oes;
-  const T* const xbase = DOT ? static_cast<const T*>(p.x.p) + b * p.x.sb + (h / p.x.share) * p.x.sh + col0 + wcol : nullptr;
-  auto write = [&](int64_t t0) {
+  const int ocols = p.vd - (col0 + wcol), osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
+  auto out_at = [&](int64_t t) { return static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + t * p.o_sl + col0 + wcol) * oes; };
+  auto x_at = [&](int64_t t) { return DOT ? LinTile<T, kWV, C, kThreads>::head(p.x, b, h, col0 + wcol) + t * p.x.sl : nullptr; };
+  char* out = out_at(start_of(0));
+  const T* xs = x_at(start_of(0));
+  auto write = [&](int n) {
     constexpr int kOutside = 0x7ffffff0;
-    const int n = tokens_of(t0);
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(obase + t0 * osl * oes, (short)0,
+    const int room = ocols - 4 * g;               // columns that are there
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(out, (short)0,
                                                         ocols > 0 ? ((n - 1) * osl + ocols) * oes : 0, 0x00020000);
     const int at = (l16 * osl + 4 * g) * oes, step = 16 * osl * oes;
     auto put = [&](f32x4 v, int to) {
@@ -478,7 +503,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       }
     }
     if constexpr (DOT) {                          // out_i . x_i, for the decays' gradient
-      const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(xbase + t0 * xsl), (short)0,
+      const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(xs), (short)0,
                                                           ocols > 0 ? ((n - 1) * xsl + ocols) * int(sizeof(T)) : 0, 0x00020000);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
@@ -549,44 +574,57 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   // and the rest of the segment is walked token by token.
   bool done = true;
   int ci = 0;
-  load(0);
+  int64_t t0 = start_of(0);
+  const T *now_q = tq.at, *now_k = tk.at, *now_v = tv.at;
+  load_gate(t0);
+  load(t0);
   if (wave == kDecayWave) decays(sh.dec[0]);
+  if (chunks > 1) load_gate(t0 + kOn);
   if (!STATE && tid == 0) sh.bad = 0;
-  for (;; ++ci) {
+  for (;; ++ci, t0 += kOn) {
     LinDecays<C>& dec = sh.dec[ci & 1];
-    int64_t t0 = start_of(ci);
-    int at = tid;
-    asm volatile("" : "+s"(t0), "+v"(at));
-    l16 = at & 15;
-    g = (at & 63) >> 4;
-    if (!STATE) tq.store(sh.q, at, t0, tokens_of(t0));
-    tk.store(sh.k, at, t0, tokens_of(t0));
-    tv.store(sh.v, at, t0, tokens_of(t0));
+    const int n = tokens_of(t0);
+    lane = lin_lane();
+    tid = 64 * wave + lane;
+    l16 = lane & 15;
+    g = lane >> 4;
+    if (!STATE) tq.store(sh.q, tid, now_q, n);
+    tk.store(sh.k, tid, now_k, n);
+    tv.store(sh.v, tid, now_v, n);
     __syncthreads();
+    if (wave == kDecayWave && ci + 1 < chunks) decays(sh.dec[(ci + 1) & 1]);
     if (!STATE) {
       pairs(dec);
       from_state(dec);
       __syncthreads();
     }
-    if (ci + 1 < chunks) load(ci + 1);            // the next one's operands are asked for
+    if (ci + 1 < chunks) {                        // the next one's operands are asked for
+      if (!STATE) now_q = tq.at;
+      now_k = tk.at;
+      now_v = tv.at;
+      load(t0 + kOn);
+      if (ci + 2 < chunks) load_gate(t0 + 2 * kOn);
+    }
     values();
     if (!STATE) {
       done = from_pairs();
       if (done)
-        write(t0);
+        write(n);
       else if (lane == 0)
         sh.bad = 1;
+      out += kOn * osl * oes;
+      if (DOT) xs += kOn * xsl;
     }
     if (done) update(dec);
-    if (wave == kDecayWave && ci + 1 < chunks) decays(sh.dec[(ci + 1) & 1]);
     __syncthreads();
     if (!STATE && sh.bad != 0) break;
-    if (DOT && at < tokens_of(t0)) {
+    if (DOT && tid < n) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) sum += sh.dot[w][at];
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(dots + t0 * H, (short)0, (C - 1) * H * 4 + 4, 0x00020000);
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, at * H * 4, 0, 0);
+      for (int w = 0; w < NW; ++w) sum += sh.dot[w][tid];
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p.dot + ((int64_t(nb) * p.batch + b) * p.L + t0) * p.H + h, (short)0,
+                                                          ((C - 1) * H + 1) * 4, 0x00020000);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, tid * H * 4, 0, 0);
     }
     if (ci + 1 == chunks) break;
   }
@@ -610,6 +648,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     float* const row_q = reinterpret_cast<float*>(sh.k);           // [KD], and of k
     float* const row_k = row_q + KD;
     asm volatile("" : "+s"(ci));                  // (its addresses are not to be kept up to date by the loop above)
+    const T* const base_q = STATE ? nullptr : tq.head(p.q, b, h, 0);
+    const T *const base_k = tk.head(p.k, b, h, 0), *const base_v = tv.head(p.v, b, h, col0);
+    const float* const base_g = p.g + b * p.g_sb + h * p.g_sh;
 #pragma unroll 1
     for (; ci < chunks; ++ci) {
       const int64_t t0 = start_of(ci);
@@ -618,20 +659,22 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const int64_t t = t0 + (REV ? n - 1 - i : i);
+        lane = lin_lane();
+        tid = 64 * wave + lane;
+        l16 = lane & 15;
+        g = lane >> 4;
         __syncthreads();
         for (int c = tid; c < KD; c += kThreads) {
-          row_q[c] = !STATE && c < p.kd ? io::widen(tq.base[t * tq.sl + c]) : 0.f;
-          row_k[c] = c < p.kd ? io::widen(tk.base[t * tk.sl + c]) : 0.f;
+          row_q[c] = !STATE && c < p.kd ? io::widen(base_q[t * p.q.sl + c]) : 0.f;
+          row_k[c] = c < p.kd ? io::widen(base_k[t * p.k.sl + c]) : 0.f;
         }
         __syncthreads();
         const int col = col0 + wcol + l16;
-        const float v = col < p.vd ? io::widen(tv.base[t * tv.sl + wcol + l16]) : 0.f;
-        const double c = double(gates[t * p.g_sl]) * 1.4426950408889634;
+        const float v = col < p.vd ? io::widen(base_v[t * p.v.sl + wcol + l16]) * p.wscale : 0.f;
+        const double c = double(base_g[t * p.g_sl]) * 1.4426950408889634;
         const bool start = c < -150.0;
         const float d = start ? 0.f : lin_decay(float(c));
         float out = 0.f;
-        int group = g;
-        asm volatile("" : "+v"(group));           // (which rows are there is asked each time, not kept)
         if (!stands) {
 #pragma unroll
           for (int a = 0; a < KK; ++a)
@@ -639,16 +682,15 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const int kd = 32 * a + 8 * group + 4 * u + r;
-                float& s = reinterpret_cast<float*>(&S[a][u])[r];
-                if (!REV) {
-                  s = start ? 0.f : s * d;
-                  s = kd < p.kd ? fmaf(row_k[kd], v * p.wscale, s) : 0.f;
-                } else if (kd < p.kd) {
-                  s = fmaf(row_k[kd], v * p.wscale, s);
+                const int kd = 32 * a + 8 * g + 4 * u + r;
+                float s = S[a][u][r];
+                if (!REV) s = start ? 0.f : s * d;
+                if (kd < p.kd) {
+                  s = fmaf(row_k[kd], v, s);
+                  out = fmaf(row_q[kd], s, out);
                 }
-                out = kd < p.kd ? fmaf(row_q[kd], s, out) : out;
                 if (REV) s = start ? 0.f : s * d;
+                S[a][u][r] = s;
               }
         }
         if (!STATE) {
@@ -659,11 +701,11 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
           if (!stands && col < p.vd) {
             if (g == 0) {
               if (p.out_f32)
-                reinterpret_cast<float*>(obase)[t * osl + l16] = out;
+                reinterpret_cast<float*>(out_at(t))[l16] = out;
               else
-                io::narrow(reinterpret_cast<T*>(obase) + t * osl + l16, out);
+                io::narrow(reinterpret_cast<T*>(out_at(t)) + l16, out);
             }
-            if (DOT) dot = out * io::widen(xbase[t * xsl + l16]);
+            if (DOT) dot = out * io::widen(x_at(t)[l16]);
           }
           if constexpr (DOT) {
             // (what a wavefront whose first chunk stands has left there is that chunk's)
@@ -673,7 +715,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
             if (tid == 0) {
               float sum = 0.f;
               for (int w = 0; w < NW; ++w) sum += sh.dot[w][t - t0];
-              dots[t * H] = sum;
+              p.dot[((int64_t(nb) * p.batch + b) * p.L + t) * p.H + h] = sum;
             }
           }
         }
@@ -687,7 +729,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     for (int a = 0; a < KK; ++a)
 #pragma unroll
       for (int u = 0; u < 2; ++u) *reinterpret_cast<f32x4*>(seg_at + ((a * 2 + u) * kThreads + tid) * 4) = S[a][u];
-    if (tid == 64 * kDecayWave && nb == 0)
+    if (wave == kDecayWave && lane == 0 && nb == 0)
       p.seg_decay[bh * p.nseg + seg] = anew ? -1.f : lin_decay(float(total));
   } else if (p.s1 && seg == (REV ? 0 : p.nseg - 1)) {
     each_state([&](f32x4& s, int r, int64_t at) { p.s1[at] = s[r]; });
