@@ -274,12 +274,11 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   const int col0 = nb * kWV, wcol = wave * 16;
 
   f32x4 S[KK][2];
-  float* const seg_at = p.seg + ((bh * p.nblk + nb) * p.nseg + seg) * (KD * kWV);
   auto zero_state = [&] {
 #pragma unroll
     for (int a = 0; a < KK; ++a) S[a][0] = S[a][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   };
-  // f(four state values, which of them, its place in the states' tensor)
+  // f(four state values, which of them, its place in a head's state)
   auto each_state = [&](auto&& f) {
     const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -289,7 +288,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int kd = 32 * a + 8 * g + 4 * u + r, n = col0 + wcol + l16;
-          if (kd < p.kd && n < p.vd) f(S[a][u], r, bh * p.kd * p.vd + p.s_row * kd + p.s_col * n);
+          if (kd < p.kd && n < p.vd) f(S[a][u], r, p.s_row * kd + p.s_col * n);
         }
   };
 
@@ -469,6 +468,40 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   auto x_at = [&](int64_t t) { return DOT ? LinTile<T, kWV, C, kThreads>::head(p.x, b, h, col0 + wcol) + t * p.x.sl : nullptr; };
   char* out = out_at(start_of(0));
   const T* xs = x_at(start_of(0));
+  // x's rows, asked for before they meet the result (16 bits a value: two a register)
+  constexpr int kXRegs = sizeof(T) == 2 ? 2 : 4;
+  uint32_t xv[DOT ? IT : 1][kXRegs];
+  auto load_x = [&](int n) {
+    constexpr int kOutside = 0x7ffffff0;
+    const int room = ocols - 4 * g, es = int(sizeof(T));
+    const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(xs), (short)0,
+                                                        ocols > 0 ? ((n - 1) * xsl + ocols) * es : 0, 0x00020000);
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int i = 16 * it + l16, at = i < n ? (i * xsl + 4 * g) * es : kOutside;
+      if (ocols >= 16) {
+        if constexpr (sizeof(T) == 2) {
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, 0);
+          xv[it][0] = v[0]; xv[it][1] = v[1];
+        } else {
+          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) xv[it][r] = v[r];
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < kXRegs; ++r) xv[it][r] = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int to = r < room ? at + r * es : kOutside;
+          if constexpr (sizeof(T) == 2)
+            xv[it][r / 2] |= uint32_t(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(from, to, 0, 0))) << (16 * (r % 2));
+          else
+            xv[it][r] = __builtin_amdgcn_raw_buffer_load_b32(from, to, 0, 0);
+        }
+      }
+    }
+  };
   auto write = [&](int n) {
     constexpr int kOutside = 0x7ffffff0;
     const int room = ocols - 4 * g;               // columns that are there
@@ -503,23 +536,18 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       }
     }
     if constexpr (DOT) {                          // out_i . x_i, for the decays' gradient
-      const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(xs), (short)0,
-                                                          ocols > 0 ? ((n - 1) * xsl + ocols) * int(sizeof(T)) : 0, 0x00020000);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        const int i = 16 * it + l16, at = i < n ? (i * xsl + 4 * g) * int(sizeof(T)) : kOutside;
         float sum = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int to = r < room ? at + r * int(sizeof(T)) : kOutside;
-          if constexpr (sizeof(T) == 2)
-            sum = fmaf(acc[it][r], io::widen(T(__builtin_amdgcn_raw_buffer_load_b16(from, to, 0, 0))), sum);
-          else
-            sum = fmaf(acc[it][r], __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, to, 0, 0)), sum);
+          const float x = sizeof(T) == 4 ? __uint_as_float(xv[it][r % kXRegs])
+                                         : __uint_as_float(r % 2 ? xv[it][r / 2] & 0xffff0000u : xv[it][r / 2] << 16);
+          sum = fmaf(acc[it][r], x, sum);
         }
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (g == 0) sh.dot[wave][i] = sum;
+        if (g == 0) sh.dot[wave][16 * it + l16] = sum;
       }
     }
   };
@@ -558,15 +586,10 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   };
 
   zero_state();
+  const int block = p.kd * p.vd;                  // of a head's state
   if (!STATE) {
-    if (p.nseg > 1) {
-#pragma unroll
-      for (int a = 0; a < KK; ++a)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) S[a][u] = *reinterpret_cast<const f32x4*>(seg_at + ((a * 2 + u) * kThreads + tid) * 4);
-    } else if (p.s0) {
-      each_state([&](f32x4& s, int r, int64_t at) { s[r] = p.s0[at]; });
-    }
+    const float* const from = p.nseg > 1 ? p.seg + (bh * p.nseg + seg) * block : p.s0 ? p.s0 + bh * block : nullptr;
+    if (from) each_state([&](f32x4& s, int r, int at) { s[r] = from[at]; });
   }
 
   // Inside a chunk a token is kept from another by a zero factor, which an infinity or a NaN turns into a
@@ -594,6 +617,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     __syncthreads();
     if (wave == kDecayWave && ci + 1 < chunks) decays(sh.dec[(ci + 1) & 1]);
     if (!STATE) {
+      if (DOT) load_x(n);
       pairs(dec);
       from_state(dec);
       __syncthreads();
@@ -725,14 +749,13 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   }
 
   if (STATE) {
-#pragma unroll
-    for (int a = 0; a < KK; ++a)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) *reinterpret_cast<f32x4*>(seg_at + ((a * 2 + u) * kThreads + tid) * 4) = S[a][u];
+    float* const to = p.seg + (bh * p.nseg + seg) * block;
+    each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
     if (wave == kDecayWave && lane == 0 && nb == 0)
       p.seg_decay[bh * p.nseg + seg] = anew ? -1.f : lin_decay(float(total));
   } else if (p.s1 && seg == (REV ? 0 : p.nseg - 1)) {
-    each_state([&](f32x4& s, int r, int64_t at) { p.s1[at] = s[r]; });
+    float* const to = p.s1 + bh * block;
+    each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
   }
 }
 

@@ -10,33 +10,33 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
-// Segment states, from zero, into the states that enter the segments, in place: s := e^c s + own.
+// Segment states, from zero, into the states that enter the segments, in place: s := e^c s + own.  A thread has
+// one value of a head's state; eight segments' are asked for at once.
 template <bool REV>
-__global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams p, int KD, int cols) {
-  const int block = KD * cols, at = (blockIdx.x % (block / 1024)) * 1024 + threadIdx.x * 4;
-  const int64_t item = blockIdx.x / (block / 1024), bh = item / p.nblk;
-  const int nb = int(item % p.nblk);
-  // the place in the walk's layout: [a][u] by [threads][4 rows]
-  const int threads = cols * 4, tid = (at / 4) % threads, u = at / 4 / threads % 2, a = at / 4 / threads / 2;
-  const int l16 = tid & 15, g = (tid & 63) >> 4;
-  const int n = nb * cols + (tid >> 6) * 16 + l16;
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  if (p.s0)
-    for (int r = 0; r < 4; ++r) {
-      const int kd = 32 * a + 8 * g + 4 * u + r;
-      if (kd < p.kd && n < p.vd) s[r] = p.s0[bh * p.kd * p.vd + p.s_row * kd + p.s_col * n];
+__global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams p, int blocks) {
+  const int block = p.kd * p.vd, at = int(blockIdx.x % blocks) * 256 + int(threadIdx.x);
+  const int64_t bh = blockIdx.x / blocks;
+  if (at >= block) return;
+  float s = p.s0 ? p.s0[bh * block + at] : 0.f;
+  float* const ws = p.seg + bh * p.nseg * block + at;
+  const float* const decay = p.seg_decay + bh * p.nseg;
+  for (int first = 0; first < p.nseg; first += 8) {
+    const int n = p.nseg - first < 8 ? p.nseg - first : 8;
+    float own[8], d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = first + i + 1 < p.nseg ? first + i : 0;        // (nothing was left behind the last segment)
+      const int seg = REV ? p.nseg - 1 - k : k;
+      own[i] = ws[int64_t(seg) * block];
+      d[i] = decay[seg];
     }
-  float* ws = p.seg + item * p.nseg * block + at;
-  for (int i = 0; i < p.nseg; ++i) {
-    const int seg = REV ? p.nseg - 1 - i : i;
-    f32x4* slot = reinterpret_cast<f32x4*>(ws + int64_t(seg) * block);
-    const bool more = i + 1 < p.nseg;             // (nothing was left behind the last segment)
-    const f32x4 own = more ? *slot : s;
-    *slot = s;
-    if (more) {
-      const float d = p.seg_decay[bh * p.nseg + seg];
-      for (int r = 0; r < 4; ++r) s[r] = d < 0.f ? own[r] : fmaf(d, s[r], own[r]);
-    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        const int seg = REV ? p.nseg - 1 - first - i : first + i;
+        ws[int64_t(seg) * block] = s;
+        s = d[i] < 0.f ? own[i] : fmaf(d[i], s, own[i]);
+      }
   }
 }
 
@@ -61,58 +61,72 @@ __global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* ou
   }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* tmp) {
-  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return tmp[0] + tmp[1] + tmp[2] + tmp[3];
-}
-
-// One workgroup per (batch row, head), 256 tokens at a time from the last.  The sums run in 64 bits: what
-// a token's decay passes is the small difference of what follows it and what precedes it.
-__global__ __launch_bounds__(256) void lin_decay_kernel(LinDecayParams p) {
-  __shared__ double tmp[4];
+// One workgroup per (batch row, head), 4096 tokens at a time from the last, four a thread.  The sums run in
+// 64 bits: what a token's decay passes is the small difference of what follows it and what precedes it.
+constexpr int kDecayThreads = 1024;
+__global__ __launch_bounds__(kDecayThreads) void lin_decay_kernel(LinDecayParams p) {
+  __shared__ double tmp[kDecayThreads / 64];
   const int64_t bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto block_sum = [&](double v) {
+    for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+    __syncthreads();
+    if (lane == 0) tmp[wave] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int w = 0; w < kDecayThreads / 64; ++w) s += tmp[w];
+    return s;
+  };
   double carry = 0.0;
   if (p.last && p.dlast) {
     double s = 0.0;
-    for (int64_t i = tid; i < p.state; i += 256) s += double(p.last[bh * p.state + i]) * double(p.dlast[bh * p.state + i]);
-    carry = block_sum(s, tmp);
+    for (int64_t i = tid; i < p.state; i += kDecayThreads) s += double(p.last[bh * p.state + i]) * double(p.dlast[bh * p.state + i]);
+    carry = block_sum(s);
   }
   double sum = 0.0;
   const int64_t part = p.batch * p.L * p.H;
-  for (int64_t t1 = (p.L + 255) / 256 * 256; t1 > 0; t1 -= 256) {
-    const int64_t t = t1 - 1 - tid;               // thread 0 has the last token
-    double v = 0.0;
-    bool start = false;
-    if (t < p.L) {
-      const int64_t at = (b * p.L + t) * p.H + h;
-      for (int i = 0; i < p.nq; ++i) v += double(p.qdq[i * part + at]);
-      for (int i = 0; i < p.nk; ++i) v -= double(p.kdk[i * part + at]);
-      start = double(p.g[b * p.g_sb + t * p.g_sl + h * p.g_sh]) * 1.4426950408889634 < -150.0;
+  constexpr int64_t kStep = 4 * kDecayThreads;
+  for (int64_t t1 = (p.L + kStep - 1) / kStep * kStep; t1 > 0; t1 -= kStep) {
+    const int64_t t = t1 - 4 * tid - 4;           // thread 0 has the last four tokens
+    double v[4];
+    bool start[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = 0.0;
+      start[e] = false;
+      if (t + e < p.L) {
+        const int64_t at = (b * p.L + t + e) * p.H + h;
+        for (int i = 0; i < p.nq; ++i) v[e] += double(p.qdq[i * part + at]);
+        for (int i = 0; i < p.nk; ++i) v[e] -= double(p.kdk[i * part + at]);
+        start[e] = double(p.g[b * p.g_sb + (t + e) * p.g_sl + h * p.g_sh]) * 1.4426950408889634 < -150.0;
+      }
     }
+#pragma unroll
+    for (int e = 2; e >= 0; --e) v[e] += v[e + 1];
+    double all = v[0];
     for (int d = 1; d < 64; d *= 2) {
-      const double o = __shfl_up(v, d);
-      if (lane >= d) v += o;
+      const double o = __shfl_up(all, d);
+      if (lane >= d) all += o;
     }
     __syncthreads();
-    if (lane == 63) tmp[wave] = v;
+    if (lane == 63) tmp[wave] = all;
     __syncthreads();
-    double before = carry;
-    for (int w = 0; w < 4; ++w) {
-      if (w < wave) before += tmp[w];
+    double later = carry + (all - v[0]);          // of the threads with later tokens
+    for (int w = 0; w < kDecayThreads / 64; ++w) {
+      if (w < wave) later += tmp[w];
       carry += tmp[w];
     }
-    v = start ? 0.0 : v + before;
-    if (t < p.L) {
-      if (p.dg) p.dg[(b * p.L + t) * p.H + h] = float(v);
-      sum += v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double g = start[e] ? 0.0 : v[e] + later;
+      if (t + e < p.L) {
+        if (p.dg) p.dg[(b * p.L + t + e) * p.H + h] = float(g);
+        sum += g;
+      }
     }
   }
   if (p.dg_heads) {
-    sum = block_sum(sum, tmp);
+    sum = block_sum(sum);
     if (tid == 0) p.sums[bh] = sum;
   }
 }
@@ -191,20 +205,20 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
 
 }  // namespace
 
+hipError_t launch_lin_states(bool bf16, bool rev, const LinParams& p, hipStream_t stream) {
+  if (p.nseg == 1) return hipSuccess;
+  const hipError_t e = lin_walk(bf16, rev, true, p, stream);
+  if (e != hipSuccess) return e;
+  const int blocks = (p.kd * p.vd + 255) / 256;
+  const dim3 grid(uint32_t(p.batch * p.H * blocks));
+  if (rev)
+    lin_prefix_kernel<true><<<grid, dim3(256), 0, stream>>>(p, blocks);
+  else
+    lin_prefix_kernel<false><<<grid, dim3(256), 0, stream>>>(p, blocks);
+  return hipGetLastError();
+}
+
 hipError_t launch_lin(bool bf16, bool rev, const LinParams& p, hipStream_t stream) {
-  hipError_t e = hipSuccess;
-  if (p.nseg > 1) {
-    e = lin_walk(bf16, rev, true, p, stream);
-    if (e != hipSuccess) return e;
-    const int KD = lin_kd(p.kd), cols = lin_cols(p.vd);
-    const dim3 grid(uint32_t(p.batch * p.H * p.nblk * (KD * cols / 1024)));
-    if (rev)
-      lin_prefix_kernel<true><<<grid, dim3(256), 0, stream>>>(p, KD, cols);
-    else
-      lin_prefix_kernel<false><<<grid, dim3(256), 0, stream>>>(p, KD, cols);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
   return lin_walk(bf16, rev, false, p, stream);
 }
 
@@ -221,7 +235,7 @@ hipError_t launch_lin_heads(bool bf16, const float* part, void* out, int64_t tok
 }
 
 hipError_t launch_lin_decay(const LinDecayParams& p, hipStream_t stream) {
-  lin_decay_kernel<<<dim3(uint32_t(p.batch * p.H)), dim3(256), 0, stream>>>(p);
+  lin_decay_kernel<<<dim3(uint32_t(p.batch * p.H)), dim3(kDecayThreads), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.dg_heads) {
     lin_decay_heads_kernel<<<dim3(uint32_t((p.H + 255) / 256)), dim3(256), 0, stream>>>(p.sums, p.dg_heads, p.batch, p.H);

@@ -221,23 +221,27 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   }
 }
 
-// dweight and dbias: 64 columns a workgroup, every fourth part a wavefront
+// dweight and dbias: 16 columns a workgroup, every sixteenth part a row of threads
 __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64_t parts, int64_t C, float* dw, float* db) {
-  __shared__ float s[2][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+  __shared__ float s[2][16][17];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+  const int64_t c = int64_t(blockIdx.x) * 16 + x;
   float a = 0.f, b = 0.f;
-  if (c < C)
-    for (int64_t i = wave; i < parts; i += 4) {
+  if (c < C) {
+#pragma unroll 8
+    for (int64_t i = y; i < parts; i += 16) {
       a += part[2 * i * C + c];
       b += part[(2 * i + 1) * C + c];
     }
-  s[0][wave][lane] = a;
-  s[1][wave][lane] = b;
+  }
+  s[0][y][x] = a;
+  s[1][y][x] = b;
   __syncthreads();
-  if (wave == 0 && c < C) {
-    if (dw) dw[c] = (s[0][0][lane] + s[0][1][lane]) + (s[0][2][lane] + s[0][3][lane]);
-    if (db) db[c] = (s[1][0][lane] + s[1][1][lane]) + (s[1][2][lane] + s[1][3][lane]);
+  if (y < 2 && c < C) {
+    float t = 0.f;
+    for (int i = 0; i < 16; ++i) t += s[y][i][x];
+    float* const out = y == 0 ? dw : db;
+    if (out) out[c] = t;
   }
 }
 
@@ -291,7 +295,7 @@ hipError_t launch_norm(bool bf16, bool bwd, const NormParams& p, hipStream_t str
   hipError_t e = bf16 ? norm_dispatch<uint16_t>(bwd, p, stream) : norm_dispatch<float>(bwd, p, stream);
   if (e == hipSuccess && bwd && p.part) {
     const int64_t C = p.groups * p.width;
-    norm_sums_kernel<<<dim3(uint32_t((C + 63) / 64)), dim3(256), 0, stream>>>(p.part, p.parts, C, p.dweight, p.dbias);
+    norm_sums_kernel<<<dim3(uint32_t((C + 15) / 16)), dim3(256), 0, stream>>>(p.part, p.parts, C, p.dweight, p.dbias);
     e = hipGetLastError();
   }
   return e;

@@ -304,7 +304,7 @@ struct LinParams {
   const float* s0;      // state that the walk begins with, (batch, head) blocks of kd * vd; may be null (zero)
   float* s1;            // state that it ends with, or null
   int64_t s_row, s_col; // strides of s0 and s1 within a block
-  float* seg;           // workspace: a state for each (batch, head, block of columns, segment)
+  float* seg;           // workspace: [batch][H][nseg] blocks of kd * vd, laid out as s0's
   float* seg_decay;     // workspace: [batch][H][nseg], negative where the state starts anew
   LinTensor x;          // dot: out . x per token, [nblk][batch][L][H]; null: not wanted
   float* dot;
@@ -318,7 +318,10 @@ struct LinParams {
 constexpr int lin_kd(int64_t kd) { return kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
 constexpr int lin_cols(int64_t vd) { return vd <= 64 ? 64 : 128; }
 constexpr int lin_chunk(bool bf16, int64_t kd) { return !bf16 && kd > 128 ? 32 : 64; }
-// one walk; with nseg > 1 the states that enter the segments are formed first
+// nseg > 1: the states that enter the segments, from k, v and s0 (kd x vd, rows s_row apart, s_col == 1 or the
+// other way round)
+hipError_t launch_lin_states(bool bf16, bool rev, const LinParams& p, hipStream_t stream);
+// one walk, from s0 or (nseg > 1) from the states that enter the segments
 hipError_t launch_lin(bool bf16, bool rev, const LinParams& p, hipStream_t stream);
 // units of one element type and width of q and k
 hipError_t launch_lin_bf16_64(bool rev, bool state, const LinParams& p, hipStream_t stream);

@@ -1291,42 +1291,15 @@ int selective_scan_ssd_step_cached(const void* x, const void* delta, const float
 // ---- linear attention with a decay for each head
 static size_t ws_round(int64_t bytes) { return size_t(round_up(bytes, 256)); }
 
-// One walk (the queries' and keys' width kd, the values' vd): its blocks of columns and segments.
-struct LinWalk {
-  int64_t nchunks = 0, seg_chunks = 0;
-  int32_t nseg = 1, nblk = 1;
-  size_t seg_bytes = 0, decay_bytes = 0;
-};
-
-static LinWalk lin_walk_plan(bool bf16, const selscan_linattn_dims& d, int64_t kd, int64_t vd) {
-  LinWalk w;
-  const int64_t chunk = selscan::lin_chunk(bf16, kd), cols = selscan::lin_cols(vd);
-  w.nchunks = (d.seqlen + chunk - 1) / chunk;
-  w.nblk = int32_t((vd + cols - 1) / cols);
-  w.seg_chunks = w.nchunks;
-  const int64_t items = d.batch * d.nheads * w.nblk;
-  // fewer workgroups than fill the GPU's 256 compute units: the sequence is split into segments of at
-  // least 4 chunks
-  if (items > 0 && items < 384) {
-    int64_t n = (512 + items - 1) / items;
-    if (n > w.nchunks / 4) n = w.nchunks / 4;
-    if (n > 1) {
-      w.seg_chunks = (w.nchunks + n - 1) / n;
-      w.nseg = int32_t((w.nchunks + w.seg_chunks - 1) / w.seg_chunks);
-    }
-  }
-  if (w.nseg > 1) {
-    w.seg_bytes = ws_round(int64_t(sizeof(float)) * items * w.nseg * selscan::lin_kd(kd) * cols);
-    w.decay_bytes = ws_round(int64_t(sizeof(float)) * d.batch * d.nheads * w.nseg);
-  }
-  return w;
-}
-
 struct LinPlan {
-  LinWalk fwd, dq, dv;          // dk's walk is planned as dq's
+  int64_t seg_len = 0;          // tokens of a segment (the sequence's, or a multiple of 64)
+  int32_t nseg = 1;
+  size_t seg_bytes = 0;         // states of one direction
   size_t fwd_bytes = 0, bwd_bytes = 0;
   size_t off_decay = 0, off_qdq = 0, off_kdk = 0, off_last = 0, off_sums = 0, off_part = 0;
 };
+
+static int64_t lin_blocks(int64_t vd) { return (vd + selscan::lin_cols(vd) - 1) / selscan::lin_cols(vd); }
 
 // Rows of `width` elements on axes of these sizes and strides: whether none overlaps another.
 static bool rows_apart(std::initializer_list<std::pair<int64_t, int64_t>> axes, int64_t width) {
@@ -1371,21 +1344,32 @@ static int lin_plan(const selscan_linattn_dims* dims, bool want_dg, LinPlan* out
   if (d.seqlen > (int64_t(1) << 31) - 1) return SELSCAN_ERR_UNSUPPORTED;
   LinPlan p;
   if (d.batch * d.seqlen > 0) {
-    const bool bf16 = d.io_dtype == SELSCAN_BF16;
     const int64_t f = int64_t(sizeof(float)), bh = d.batch * d.nheads, rows = bh * d.seqlen;
-    p.fwd = lin_walk_plan(bf16, d, d.dk, d.dv);
-    p.fwd_bytes = p.fwd.seg_bytes + p.fwd.decay_bytes;
-    p.dq = lin_walk_plan(bf16, d, d.dv, d.dk);
-    p.dv = p.fwd;
-    // the walks of the backward pass follow one another in one workspace
-    size_t off = p.dq.seg_bytes > p.dv.seg_bytes ? p.dq.seg_bytes : p.dv.seg_bytes;
-    p.off_decay = off;
-    off += p.dq.decay_bytes > p.dv.decay_bytes ? p.dq.decay_bytes : p.dv.decay_bytes;
+    const int64_t chunks = (d.seqlen + 63) / 64, items = bh * lin_blocks(d.dv);
+    p.seg_len = d.seqlen;
+    // fewer workgroups than fill the GPU's 256 compute units: the sequence is split into segments of at
+    // least 4 chunks of 64 tokens
+    if (items < 384) {
+      int64_t n = (512 + items - 1) / items;
+      if (n > chunks / 4) n = chunks / 4;
+      if (n > 1) {
+        const int64_t len = (chunks + n - 1) / n;
+        p.seg_len = 64 * len;
+        p.nseg = int32_t((chunks + len - 1) / len);
+      }
+    }
+    if (p.nseg > 1) {
+      p.seg_bytes = ws_round(f * bh * p.nseg * d.dk * d.dv);
+      p.fwd_bytes = p.seg_bytes + ws_round(f * bh * p.nseg);
+    }
+    // the states of one direction, then of the other
+    p.off_decay = p.seg_bytes;
+    size_t off = p.fwd_bytes;
     if (want_dg) {
       p.off_qdq = off;
-      off += ws_round(f * rows * p.dq.nblk);
+      off += ws_round(f * rows * lin_blocks(d.dk));
       p.off_kdk = off;
-      off += ws_round(f * rows * p.dq.nblk);
+      off += ws_round(f * rows * lin_blocks(d.dk));
       p.off_last = off;
       off += ws_round(f * bh * d.dk * d.dv);
       p.off_sums = off;
@@ -1412,18 +1396,23 @@ static selscan::LinTensor lin_tensor(const void* ptr, const selscan_linattn_dims
   return t;
 }
 
-static selscan::LinParams lin_params(const LinWalk& w, const selscan::LinTensor& q, const selscan::LinTensor& k,
+// One walk: queries and keys of width kd, values of width vd.
+static selscan::LinParams lin_params(const LinPlan& pl, const selscan::LinTensor& q, const selscan::LinTensor& k,
                                      const selscan::LinTensor& v, int64_t kd, int64_t vd, const float* g,
-                                     const selscan_linattn_dims& d, void* ws, size_t off_decay) {
+                                     const selscan_linattn_dims& d, void* ws) {
   selscan::LinParams p{};
   p.q = q; p.k = k; p.v = v;
   p.g = g;
   p.g_sb = d.decay_tokens ? d.g_sb : 0; p.g_sl = d.decay_tokens ? d.g_sl : 0; p.g_sh = d.g_sh;
   p.batch = d.batch; p.L = d.seqlen; p.H = d.nheads;
   p.kd = int32_t(kd); p.vd = int32_t(vd);
-  p.nchunks = w.nchunks; p.seg_chunks = w.seg_chunks; p.nseg = w.nseg; p.nblk = w.nblk;
+  const int64_t chunk = selscan::lin_chunk(d.io_dtype == SELSCAN_BF16, kd);
+  p.nchunks = (d.seqlen + chunk - 1) / chunk;
+  p.seg_chunks = (pl.seg_len + chunk - 1) / chunk;
+  p.nseg = pl.nseg;
+  p.nblk = int32_t(lin_blocks(vd));
   p.seg = static_cast<float*>(ws);
-  p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(ws) + off_decay);
+  p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off_decay);
   return p;
 }
 
@@ -1493,15 +1482,15 @@ int linear_attention_fwd(const void* q, const void* k, const void* v, const floa
     e = hipMallocAsync(&ws, pl.fwd_bytes, s);
     if (e != hipSuccess) return hip_fail(e);
   }
-  selscan::LinParams p = lin_params(pl.fwd, lin_tensor(q, d, d.qk_heads, d.q_sb, d.q_sl, d.q_sh),
+  selscan::LinParams p = lin_params(pl, lin_tensor(q, d, d.qk_heads, d.q_sb, d.q_sl, d.q_sh),
                                     lin_tensor(k, d, d.qk_heads, d.k_sb, d.k_sl, d.k_sh),
-                                    lin_tensor(v, d, d.nheads, d.v_sb, d.v_sl, d.v_sh), d.dk, d.dv, log_decay, d, ws,
-                                    pl.fwd.seg_bytes);
+                                    lin_tensor(v, d, d.nheads, d.v_sb, d.v_sl, d.v_sh), d.dk, d.dv, log_decay, d, ws);
   lin_out(&p, o, false, d, d.o_sb, d.o_sl, d.o_sh);
   p.s0 = initial_state; p.s1 = last_state;
   p.s_row = d.dv; p.s_col = 1;
   p.pscale = p.fscale = d.scale; p.wscale = 1.f;
-  e = selscan::launch_lin(bf16, false, p, s);
+  e = selscan::launch_lin_states(bf16, false, p, s);
+  if (e == hipSuccess) e = selscan::launch_lin(bf16, false, p, s);
   st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   if (workspace == nullptr && pl.fwd_bytes > 0) {
     const hipError_t f = hipFreeAsync(ws, s);
@@ -1551,22 +1540,38 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
   float* part = reinterpret_cast<float*>(ws + pl.off_part);
   float* last = reinterpret_cast<float*>(ws + pl.off_last);
   const bool want_last = want_dg && dlast_state != nullptr;
+  // the states of the forward pass, as it forms them
+  selscan::LinParams p = lin_params(pl, tq, tk, tv, d.dk, d.dv, log_decay, d, ws);
+  p.s0 = initial_state;
+  p.s_row = d.dv; p.s_col = 1;
+  p.wscale = 1.f;
+  e = selscan::launch_lin_states(bf16, false, p, s);
   // dq: do meets v, and the state S of the forward pass meets do (S read with its axes exchanged)
-  selscan::LinParams p = lin_params(pl.dq, to, tv, tk, d.dv, d.dk, log_decay, d, ws, pl.off_decay);
-  lin_out(&p, shared ? part : dq, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
-  p.s0 = initial_state; p.s1 = want_last ? last : nullptr;
-  p.s_row = 1; p.s_col = d.dv;
-  p.pscale = p.fscale = d.scale; p.wscale = 1.f;
-  if (want_dg) {
-    p.x = tq;
-    p.dot = reinterpret_cast<float*>(ws + pl.off_qdq);
+  if (e == hipSuccess) {
+    p = lin_params(pl, to, tv, tk, d.dv, d.dk, log_decay, d, ws);
+    lin_out(&p, shared ? part : dq, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
+    p.s0 = initial_state; p.s1 = want_last ? last : nullptr;
+    p.s_row = 1; p.s_col = d.dv;
+    p.pscale = p.fscale = d.scale; p.wscale = 1.f;
+    if (want_dg) {
+      p.x = tq;
+      p.dot = reinterpret_cast<float*>(ws + pl.off_qdq);
+    }
+    e = selscan::launch_lin(bf16, false, p, s);
   }
-  e = selscan::launch_lin(bf16, false, p, s);
   if (e == hipSuccess && shared)
     e = selscan::launch_lin_heads(bf16, part, dq, tokens, d.nheads, int(d.nheads / d.qk_heads), int(d.dk), s);
-  // dk: v meets do, and the gradient R of the state meets v
+  // the gradient R of the states, from the last token on
   if (e == hipSuccess) {
-    p = lin_params(pl.dq, tv, to, tq, d.dv, d.dk, log_decay, d, ws, pl.off_decay);
+    p = lin_params(pl, tk, tq, to, d.dk, d.dv, log_decay, d, ws);
+    p.s0 = dlast_state;
+    p.s_row = d.dv; p.s_col = 1;
+    p.wscale = d.scale;
+    e = selscan::launch_lin_states(bf16, true, p, s);
+  }
+  // dk: v meets do, and R meets v (R read with its axes exchanged)
+  if (e == hipSuccess) {
+    p = lin_params(pl, tv, to, tq, d.dv, d.dk, log_decay, d, ws);
     lin_out(&p, shared ? part : dk, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
     p.s0 = dlast_state;
     p.s_row = 1; p.s_col = d.dv;
@@ -1574,7 +1579,7 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
     if (want_dg) {
       p.x = tk;
       p.dot = reinterpret_cast<float*>(ws + pl.off_kdk);
-      }
+    }
     e = selscan::launch_lin(bf16, true, p, s);
   }
   if (e == hipSuccess && shared)
@@ -1590,13 +1595,13 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
     c.dg_heads = d.decay_tokens ? nullptr : dlog_decay;
     c.sums = reinterpret_cast<double*>(ws + pl.off_sums);
     c.batch = d.batch; c.L = d.seqlen; c.H = d.nheads; c.state = d.dk * d.dv;
-    c.nq = c.nk = pl.dq.nblk;
+    c.nq = c.nk = int32_t(lin_blocks(d.dk));
     e = selscan::launch_lin_decay(c, s);
   }
   // dv: k meets q, and R meets k; R before the first token is the initial state's gradient (last: it
   // may take dlast_state's place)
   if (e == hipSuccess) {
-    p = lin_params(pl.dv, tk, tq, to, d.dk, d.dv, log_decay, d, ws, pl.off_decay);
+    p = lin_params(pl, tk, tq, to, d.dk, d.dv, log_decay, d, ws);
     lin_out(&p, dv, false, d, d.seqlen * d.nheads * d.dv, d.nheads * d.dv, d.dv);
     p.s0 = dlast_state; p.s1 = dinitial_state;
     p.s_row = d.dv; p.s_col = 1;
