@@ -106,15 +106,19 @@ __device__ __forceinline__ void lin_split(f32x8 x, typename lin_io<T>::frag* out
     out[0] = x;
   } else {
     u32x4 part[N];
+    // A pair's product with (-1, 0) or (0, -1) takes one of the two off without unpacking it.  (The constants
+    // go through registers: as literals the compiler writes them in a form that the instruction reads otherwise.)
+    uint32_t first = 0x0000bf80u, second = 0xbf800000u;
+    asm volatile("" : "+s"(first), "+s"(second));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float a = x[2 * i], b = x[2 * i + 1];
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const uint32_t r = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-        part[n][i] = r;
-        a -= __uint_as_float(r << 16);
-        b -= __uint_as_float(r & 0xffff0000u);
+        const bf16x2 r = __builtin_convertvector(f32x2{a, b}, bf16x2);
+        part[n][i] = __builtin_bit_cast(uint32_t, r);
+        a = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(bf16x2, first), a, false);
+        b = __builtin_amdgcn_fdot2_f32_bf16(r, __builtin_bit_cast(bf16x2, second), b, false);
       }
     }
 #pragma unroll
@@ -154,7 +158,8 @@ template <int C> struct alignas(16) LinDecays {
   float hi[C], lo[C];       // log2 of the decays since the chunk's start, in two parts
   float f[C], w[C];         // factor of a row's product with the state; of a row's share in the new state
   int lim[C];               // the row's first visible key (forward), its last (backward)
-  float carry;              // of the state over the chunk
+  float mul;                // what the held state is multiplied by (1 as a rule: see `scale` in the walk)
+  float before, after;      // the held state's scale before the chunk, and behind it
 };
 
 template <typename T, int KD, int NW, bool STATE, bool DOT, int NPP>
@@ -248,12 +253,14 @@ struct LinTile {
 // columns of v: a wavefront owns 16 of them, and the state's [KD][16] in its accumulators, which are at
 // once the operand of its product with the queries.
 // STATE: only the state at the segment's end, from zero.
-// DOT: the rows' products with x too; then the parts of P and of the state have 24 bits, else the state's 16.
+// DOT: the rows' products with x too.  The decays' gradient is what remains of their sum over all later tokens in
+// one walk less that in the other, so the state then meets q with its 24 bits (else with 16); what P loses,
+// it loses in both walks alike, and 16 bits do (else 8).
 template <typename T, int KD, int NW, bool REV, bool STATE, bool DOT>
 __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_kernel(LinParams p) {
   using io = lin_io<T>;
   using frag = typename io::frag;
-  constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2, NPP = NP == 3 ? 3 : 1;   // parts of fp32 values on the matrix cores
+  constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2, NPP = NP == 3 ? 2 : 1;   // parts of the state and of the pairs on the matrix cores
   constexpr int NX = sizeof(T) == 2 ? 3 : 1;      // the state is held in fp32: what is added to it keeps 24 bits
   using Sh = LinShared<T, KD, NW, STATE, DOT, NPP>;
   constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * NW, kWP = Sh::kWP, kThreads = 64 * NW;
@@ -301,12 +308,6 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   tk.init(p.k, b, h, start_of(0), 0, p.kd);
   tv.init(p.v, b, h, start_of(0), col0, p.vd);
   constexpr int64_t kOn = REV ? -C : C;           // tokens from a chunk to the next
-  auto load = [&](int64_t t0) {
-    const int n = tokens_of(t0), tid = 64 * wave + lin_lane();
-    if (!STATE) tq.template load<REV>(tid, n);
-    tk.template load<REV>(tid, n);
-    tv.template load<REV>(tid, n);
-  };
   // the log decays of a chunk, a chunk ahead of its operands
   const float* gates = p.g + b * p.g_sb + h * p.g_sh + start_of(0) * p.g_sl;
   const int gsl = int(p.g_sl);
@@ -322,6 +323,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
 
   double total = 0.0;                             // STATE: log2 of the segment's decay
   bool anew = false;
+  // The state is held as a multiple `scale` (its logarithm, base 2) of the accumulators, which takes up the
+  // chunks' decays until it leaves 2^-16 .. 2^16: most chunks then leave the accumulators as they are.
+  double scale = 0.0;
   // the factors of a chunk's tokens, of the gates that kDecayWave has loaded
   auto decays = [&](LinDecays<C>& d) {
     const int lane = lin_lane();
@@ -337,22 +341,32 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     const double all = __shfl(c, 63);
     const uint64_t upto = (uint64_t(2) << lane) - 1;
     const uint64_t before = starts & upto, after = starts & ~upto;
-    const float in = before ? 0.f : lin_decay(float(c));
-    const float out = after ? 0.f : lin_decay(float(all - c));
+    const double next = scale + all;
+    const bool fold = starts != 0 || !(next > -16.0 && next < 16.0);
+    const double held = fold ? 0.0 : next;
+    const float f = REV ? (after ? 0.f : lin_decay(float(all - c + scale))) : (before ? 0.f : lin_decay(float(c + scale)));
+    const float w = REV ? (before ? 0.f : lin_decay(float(c - held))) : (after ? 0.f : lin_decay(float(all - c - held)));
     if (lane < C) {
       d.hi[lane] = float(c);
       d.lo[lane] = float(c - double(float(c)));
-      d.f[lane] = (REV ? out : in) * p.fscale;
-      d.w[lane] = (REV ? in : out) * p.wscale;
+      d.f[lane] = f * p.fscale;
+      d.w[lane] = w * p.wscale;
       d.lim[lane] = REV ? (after ? __builtin_ctzll(after) - 1 : C) : (before ? 63 - __builtin_clzll(before) : 0);
     }
-    if (lane == 0) d.carry = starts ? 0.f : lin_decay(float(all));
+    if (lane == 0) {
+      d.mul = starts ? 0.f : fold ? lin_decay(float(next)) : 1.f;
+      d.before = __builtin_amdgcn_exp2f(float(scale));
+      d.after = __builtin_amdgcn_exp2f(float(held));
+    }
+    scale = held;
     if (STATE) {
       total += all;
       anew |= starts != 0;
     }
   };
 
+  // whether any of the 32 channels are there (the first are; of a width that is no power of two the last may not be)
+  auto there = [&](int a) { return a <= KK / 2 || 32 * a < p.kd; };
   // ---- the pairs: P_ij = e^{c_i - c_j} (q_i . k_j), as its transpose's tiles (lane: one i, four j)
   auto pairs = [&](const LinDecays<C>& dec) {
     constexpr int kUnits = C == 64 ? 6 : 2;       // 16 rows by 32 keys, those that see each other
@@ -373,8 +387,10 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       for (int a = 0; a < KK; ++a) {
         if (a + 1 < KK) ask(a + 1);
         __builtin_amdgcn_sched_barrier(0);
+        if (there(a)) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) acc[u] = io::mma(fk[a & 1][u], fq[a & 1], acc[u]);
+          for (int u = 0; u < 2; ++u) acc[u] = io::mma(fk[a & 1][u], fq[a & 1], acc[u]);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       const int i = 16 * it + l16;
@@ -418,11 +434,13 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       const int a = i / kHalf, it = 2 * (i % kHalf);
       if (i + 1 < KK * kHalf) ask(i + 1);
       __builtin_amdgcn_sched_barrier(0);
-      if (it == 0) lin_split<T, NP>(__builtin_shufflevector(S[a][0], S[a][1], 0, 1, 2, 3, 4, 5, 6, 7), fs);
+      if (there(a)) {
+        if (it == 0) lin_split<T, NP>(__builtin_shufflevector(S[a][0], S[a][1], 0, 1, 2, 3, 4, 5, 6, 7), fs);
 #pragma unroll
-      for (int n = 0; n < NP; ++n)
+        for (int n = 0; n < NP; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) acc[it + x] = io::mma(fs[n], fq[i & 1][x], acc[it + x]);
+          for (int x = 0; x < 2; ++x) acc[it + x] = io::mma(fs[n], fq[i & 1][x], acc[it + x]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -551,15 +569,18 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       }
     }
   };
-  // ---- the new state: w_j v_j in parts, so that nothing of what is added to fp32 is lost
-  auto update = [&](const LinDecays<C>& dec) {
-    const float keep = dec.carry;
+  auto multiply = [&](float m) {
+    if (__builtin_amdgcn_readfirstlane(__float_as_int(m)) == __float_as_int(1.f)) return;
 #pragma unroll
     for (int a = 0; a < KK; ++a)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[a][u][r] *= keep;
+        for (int r = 0; r < 4; ++r) S[a][u][r] *= m;
+  };
+  // ---- the new state: w_j v_j in parts, so that nothing of what is added to fp32 is lost
+  auto update = [&](const LinDecays<C>& dec) {
+    multiply(dec.mul);
     frag fk[2][2], fw[NX];
     auto ask = [&](int i) {
 #pragma unroll
@@ -577,10 +598,12 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
         lin_split<T, NX>(x, fw);
       }
       __builtin_amdgcn_sched_barrier(0);
+      if (there(a)) {
 #pragma unroll
-      for (int n = 0; n < NX; ++n)
+        for (int n = 0; n < NX; ++n)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) S[a][u] = io::mma(fk[i & 1][u], fw[n], S[a][u]);
+          for (int u = 0; u < 2; ++u) S[a][u] = io::mma(fk[i & 1][u], fw[n], S[a][u]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -600,7 +623,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   int64_t t0 = start_of(0);
   const T *now_q = tq.at, *now_k = tk.at, *now_v = tv.at;
   load_gate(t0);
-  load(t0);
+  if (!STATE) tq.template load<REV>(tid, tokens_of(t0));
+  tk.template load<REV>(tid, tokens_of(t0));
+  tv.template load<REV>(tid, tokens_of(t0));
   if (wave == kDecayWave) decays(sh.dec[0]);
   if (chunks > 1) load_gate(t0 + kOn);
   if (!STATE && tid == 0) sh.bad = 0;
@@ -615,20 +640,24 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     tk.store(sh.k, tid, now_k, n);
     tv.store(sh.v, tid, now_v, n);
     __syncthreads();
-    if (wave == kDecayWave && ci + 1 < chunks) decays(sh.dec[(ci + 1) & 1]);
+    const bool more = ci + 1 < chunks;
+    const int next = more ? tokens_of(t0 + kOn) : 0;
+    if (!STATE) now_q = tq.at;
+    now_k = tk.at;
+    now_v = tv.at;
+    if (wave == kDecayWave && more) decays(sh.dec[(ci + 1) & 1]);
     if (!STATE) {
-      if (DOT) load_x(n);
+      // (the next chunk's operands are asked for one by one, and not all of them at a time)
+      if (more) tq.template load<REV>(tid, next);
       pairs(dec);
+      if (more) tk.template load<REV>(tid, next);
       from_state(dec);
+      if (DOT) load_x(n);
       __syncthreads();
     }
-    if (ci + 1 < chunks) {                        // the next one's operands are asked for
-      if (!STATE) now_q = tq.at;
-      now_k = tk.at;
-      now_v = tv.at;
-      load(t0 + kOn);
-      if (ci + 2 < chunks) load_gate(t0 + 2 * kOn);
-    }
+    if (STATE && more) tk.template load<REV>(tid, next);
+    if (more) tv.template load<REV>(tid, next);
+    if (ci + 2 < chunks) load_gate(t0 + 2 * kOn);
     values();
     if (!STATE) {
       done = from_pairs();
@@ -652,6 +681,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     }
     if (ci + 1 == chunks) break;
   }
+  // the accumulators as the state itself
+  multiply(STATE || done ? sh.dec[ci & 1].after : sh.dec[ci & 1].before);
   bool slow = !STATE && sh.bad != 0;
   if (STATE) {
     float chk = 0.f;

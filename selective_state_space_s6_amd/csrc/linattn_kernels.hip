@@ -80,6 +80,7 @@ __global__ __launch_bounds__(kDecayThreads) void lin_decay_kernel(LinDecayParams
   double carry = 0.0;
   if (p.last && p.dlast) {
     double s = 0.0;
+#pragma unroll 8
     for (int64_t i = tid; i < p.state; i += kDecayThreads) s += double(p.last[bh * p.state + i]) * double(p.dlast[bh * p.state + i]);
     carry = block_sum(s);
   }

@@ -221,17 +221,26 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   }
 }
 
-// dweight and dbias: 16 columns a workgroup, every sixteenth part a row of threads
+// dweight and dbias: 8 columns a workgroup, every 32nd part a row of threads; eight parts asked for at once
 __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64_t parts, int64_t C, float* dw, float* db) {
-  __shared__ float s[2][16][17];
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const int64_t c = int64_t(blockIdx.x) * 16 + x;
+  __shared__ float s[2][32][9];
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int64_t c = int64_t(blockIdx.x) * 8 + x;
   float a = 0.f, b = 0.f;
   if (c < C) {
-#pragma unroll 8
-    for (int64_t i = y; i < parts; i += 16) {
-      a += part[2 * i * C + c];
-      b += part[(2 * i + 1) * C + c];
+    for (int64_t i = y; i < parts; i += 256) {
+      float u[8], v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t j = i + 32 * k < parts ? i + 32 * k : i;
+        u[k] = part[2 * j * C + c];
+        v[k] = part[(2 * j + 1) * C + c];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a += i + 32 * k < parts ? u[k] : 0.f;
+        b += i + 32 * k < parts ? v[k] : 0.f;
+      }
     }
   }
   s[0][y][x] = a;
@@ -239,7 +248,7 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64
   __syncthreads();
   if (y < 2 && c < C) {
     float t = 0.f;
-    for (int i = 0; i < 16; ++i) t += s[y][i][x];
+    for (int i = 0; i < 32; ++i) t += s[y][i][x];
     float* const out = y == 0 ? dw : db;
     if (out) out[c] = t;
   }
@@ -295,7 +304,7 @@ hipError_t launch_norm(bool bf16, bool bwd, const NormParams& p, hipStream_t str
   hipError_t e = bf16 ? norm_dispatch<uint16_t>(bwd, p, stream) : norm_dispatch<float>(bwd, p, stream);
   if (e == hipSuccess && bwd && p.part) {
     const int64_t C = p.groups * p.width;
-    norm_sums_kernel<<<dim3(uint32_t((C + 15) / 16)), dim3(256), 0, stream>>>(p.part, p.parts, C, p.dweight, p.dbias);
+    norm_sums_kernel<<<dim3(uint32_t((C + 7) / 8)), dim3(256), 0, stream>>>(p.part, p.parts, C, p.dweight, p.dbias);
     e = hipGetLastError();
   }
   return e;

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cstdlib>
 #include <initializer_list>
 #include <mutex>
 #include <utility>
@@ -1349,7 +1350,11 @@ static int lin_plan(const selscan_linattn_dims* dims, bool want_dg, LinPlan* out
     p.seg_len = d.seqlen;
     // fewer workgroups than fill the GPU's 256 compute units: the sequence is split into segments of at
     // least 4 chunks of 64 tokens
-    if (items < 384) {
+    if (const char* ev = getenv("LINSEG")) {
+      int64_t n = atoi(ev);
+      if (n > chunks) n = chunks;
+      if (n > 1) { const int64_t len = (chunks + n - 1) / n; p.seg_len = 64 * len; p.nseg = int32_t((chunks + len - 1) / len); }
+    } else if (items < 384) {
       int64_t n = (512 + items - 1) / items;
       if (n > chunks / 4) n = chunks / 4;
       if (n > 1) {
