@@ -5,7 +5,7 @@
 namespace selscan {
 
 hipError_t launch_lin_bf16_64(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  return p.vd <= 64 ? lin_dispatch<uint16_t, 64, 4>(rev, state, p, stream) : lin_dispatch<uint16_t, 64, 8>(rev, state, p, stream);
+  return lin_choose<uint16_t, 64>(rev, state, p, stream);
 }
 
 }  // namespace selscan

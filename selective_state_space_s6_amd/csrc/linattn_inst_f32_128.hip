@@ -5,7 +5,7 @@
 namespace selscan {
 
 hipError_t launch_lin_f32_128(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  return p.vd <= 64 ? lin_dispatch<float, 128, 4>(rev, state, p, stream) : lin_dispatch<float, 128, 8>(rev, state, p, stream);
+  return lin_choose<float, 128>(rev, state, p, stream);
 }
 
 }  // namespace selscan

@@ -162,14 +162,14 @@ template <int C> struct alignas(16) LinDecays {
   float before, after;      // the held state's scale before the chunk, and behind it
 };
 
-template <typename T, int KD, int NW, bool STATE, bool DOT, int NPP>
+template <typename T, int KD, int NW, int HP, bool STATE, bool DOT, int NPP>
 struct alignas(16) LinShared {
   static constexpr int C = lin_chunk_of<T, KD>(), kWP = C * int(sizeof(T)) < 128 ? 128 / int(sizeof(T)) : C;
   T q[STATE ? 8 : C * KD];
   T k[C * KD];
   T v[C * 16 * NW];
-  T p[STATE ? 8 : NPP * C * kWP];
-  LinDecays<C> dec[2];      // this chunk's, and the next one's
+  T p[STATE ? 8 : HP * NPP * C * kWP];
+  LinDecays<C> dec[HP][2];  // this chunk's, and the next one's
   float dot[DOT ? NW : 1][DOT ? C : 1];
   int bad;
 };
@@ -249,32 +249,33 @@ struct LinTile {
   }
 };
 
-// One workgroup of NW wavefronts walks the chunks of one segment of one (batch row, head) for 16 NW
-// columns of v: a wavefront owns 16 of them, and the state's [KD][16] in its accumulators, which are at
-// once the operand of its product with the queries.
+// One workgroup of NW wavefronts walks the chunks of one segment of HP heads of one batch row that share their
+// queries and keys, for 16 NW / HP columns of v each: a wavefront owns 16 of them, and the state's [KD][16] in
+// its accumulators, which are at once the operand of its product with the queries.
 // STATE: only the state at the segment's end, from zero.
 // DOT: the rows' products with x too.  The decays' gradient is what remains of their sum over all later tokens in
 // one walk less that in the other, so the state then meets q with its 24 bits (else with 16); what P loses,
 // it loses in both walks alike, and 16 bits do (else 8).
-template <typename T, int KD, int NW, bool REV, bool STATE, bool DOT>
+template <typename T, int KD, int NW, int HP, bool REV, bool STATE, bool DOT>
 __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_kernel(LinParams p) {
   using io = lin_io<T>;
   using frag = typename io::frag;
   constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2, NPP = NP == 3 ? 2 : 1;   // parts of the state and of the pairs on the matrix cores
   constexpr int NX = sizeof(T) == 2 ? 3 : 1;      // the state is held in fp32: what is added to it keeps 24 bits
-  using Sh = LinShared<T, KD, NW, STATE, DOT, NPP>;
-  constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * NW, kWP = Sh::kWP, kThreads = 64 * NW;
-  constexpr int kDecayWave = NW - 1;              // has the least to do with the pairs
+  using Sh = LinShared<T, KD, NW, HP, STATE, DOT, NPP>;
+  constexpr int kWaves = NW / HP;                 // of a head
+  constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kWP = Sh::kWP, kThreads = 64 * NW;
+  constexpr int kDecayWave = kWaves - 1;          // has the least to do with the pairs
   __shared__ Sh sh;
 
-  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-  int lane = lin_lane(), tid = 64 * wave + lane, l16 = lane & 15, g = lane >> 4;
+  const int all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), part = all_wave / kWaves, wave = all_wave % kWaves;
+  int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
   // The heads of a token lie next to one another, so the rows of one head are a power of two apart as a
   // rule, in one channel of the L2: an XCD takes the heads side by side.
   const int item = xcd_contiguous_block(blockIdx.x, gridDim.x);
   const int segs = STATE ? p.nseg - 1 : p.nseg;   // (nothing is behind the last segment)
-  const int H = int(p.H), nb = item / H % p.nblk, sidx = item / H / p.nblk % segs;
-  const int64_t h = item % H, b = item / H / p.nblk / segs, bh = b * H + h;
+  const int H = int(p.H), heads = H / HP, nb = item / heads % p.nblk, sidx = item / heads / p.nblk % segs;
+  const int64_t h = item % heads * HP + part, b = item / heads / p.nblk / segs, bh = b * H + h;
   const int seg = STATE && REV ? sidx + 1 : sidx;
   const int64_t chunk0 = int64_t(seg) * p.seg_chunks;
   const int chunks = int(p.nchunks - chunk0 < p.seg_chunks ? p.nchunks - chunk0 : p.seg_chunks);
@@ -303,7 +304,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   auto tokens_of = [&](int64_t t0) { return int(p.L - t0 < C ? p.L - t0 : C); };
 
   LinTile<T, KD, C, kThreads> tq, tk;
-  LinTile<T, kWV, C, kThreads> tv;
+  LinTile<T, kWV, C, 64 * kWaves> tv;
+  T* const sv = sh.v + part * C * kWV;
+  T* const sp = STATE ? sh.p : sh.p + part * NPP * C * kWP;
   if (!STATE) tq.init(p.q, b, h, start_of(0), 0, p.kd);
   tk.init(p.k, b, h, start_of(0), 0, p.kd);
   tv.init(p.v, b, h, start_of(0), col0, p.vd);
@@ -371,7 +374,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   auto pairs = [&](const LinDecays<C>& dec) {
     constexpr int kUnits = C == 64 ? 6 : 2;       // 16 rows by 32 keys, those that see each other
 #pragma unroll 1
-    for (int unit = wave; unit < kUnits; unit += NW) {
+    for (int unit = wave; unit < kUnits; unit += kWaves) {
       // C = 64 forward: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1); backward: (3,1) (2,1) (1,1) (1,0) (0,1) (0,0)
       int it = C == 32 ? unit : unit < 2 ? unit : unit / 2 + 1, ks = C == 32 || unit < 2 ? 0 : unit & 1;
       if (REV) { it = IT - 1 - it; ks = KS - 1 - ks; }
@@ -409,7 +412,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
         }
 #pragma unroll
         for (int x = 0; x < NPP; ++x) {
-          io::store(sh.p + x * C * kWP + lin_at<T, kWP>(i, j0), val);
+          io::store(sp + x * C * kWP + lin_at<T, kWP>(i, j0), val);
           if (x + 1 < NPP)
 #pragma unroll
             for (int r = 0; r < 4; ++r) val[r] = lin_rest(val[r]);
@@ -453,7 +456,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   frag fv[KS];
   auto values = [&] {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) fv[ks] = io::template column<kWV>(sh.v, 32 * ks + 8 * g, wcol, 4, l16);
+    for (int ks = 0; ks < KS; ++ks) fv[ks] = io::template column<kWV>(sv, 32 * ks + 8 * g, wcol, 4, l16);
   };
   // ... and that of the pairs; false if something of it is not finite
   auto from_pairs = [&] {
@@ -466,7 +469,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       for (int it = 0; it < IT; ++it)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-          if (seen(it, ks)) fp[it][ks] = io::template row<kWP>(sh.p + x * C * kWP, 16 * it + l16, 32 * ks + 8 * g);
+          if (seen(it, ks)) fp[it][ks] = io::template row<kWP>(sp + x * C * kWP, 16 * it + l16, 32 * ks + 8 * g);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   // and dropped.
   const int ocols = p.vd - (col0 + wcol), osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
   auto out_at = [&](int64_t t) { return static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + t * p.o_sl + col0 + wcol) * oes; };
-  auto x_at = [&](int64_t t) { return DOT ? LinTile<T, kWV, C, kThreads>::head(p.x, b, h, col0 + wcol) + t * p.x.sl : nullptr; };
+  auto x_at = [&](int64_t t) { return DOT ? LinTile<T, kWV, C, 64 * kWaves>::head(p.x, b, h, col0 + wcol) + t * p.x.sl : nullptr; };
   char* out = out_at(start_of(0));
   const T* xs = x_at(start_of(0));
   // x's rows, asked for before they meet the result (16 bits a value: two a register)
@@ -565,7 +568,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
         }
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (g == 0) sh.dot[wave][16 * it + l16] = sum;
+        if (g == 0) sh.dot[all_wave][16 * it + l16] = sum;
       }
     }
   };
@@ -625,27 +628,28 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   load_gate(t0);
   if (!STATE) tq.template load<REV>(tid, tokens_of(t0));
   tk.template load<REV>(tid, tokens_of(t0));
-  tv.template load<REV>(tid, tokens_of(t0));
-  if (wave == kDecayWave) decays(sh.dec[0]);
+  tv.template load<REV>(64 * wave + lane, tokens_of(t0));
+  if (wave == kDecayWave) decays(sh.dec[part][0]);
   if (chunks > 1) load_gate(t0 + kOn);
   if (!STATE && tid == 0) sh.bad = 0;
   for (;; ++ci, t0 += kOn) {
-    LinDecays<C>& dec = sh.dec[ci & 1];
+    LinDecays<C>& dec = sh.dec[part][ci & 1];
     const int n = tokens_of(t0);
     lane = lin_lane();
-    tid = 64 * wave + lane;
+    tid = 64 * all_wave + lane;
+    const int vid = 64 * wave + lane;             // of the head's threads
     l16 = lane & 15;
     g = lane >> 4;
     if (!STATE) tq.store(sh.q, tid, now_q, n);
     tk.store(sh.k, tid, now_k, n);
-    tv.store(sh.v, tid, now_v, n);
+    tv.store(sv, vid, now_v, n);
     __syncthreads();
     const bool more = ci + 1 < chunks;
     const int next = more ? tokens_of(t0 + kOn) : 0;
     if (!STATE) now_q = tq.at;
     now_k = tk.at;
     now_v = tv.at;
-    if (wave == kDecayWave && more) decays(sh.dec[(ci + 1) & 1]);
+    if (wave == kDecayWave && more) decays(sh.dec[part][(ci + 1) & 1]);
     if (!STATE) {
       // (the next chunk's operands are asked for one by one, and not all of them at a time)
       if (more) tq.template load<REV>(tid, next);
@@ -656,7 +660,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       __syncthreads();
     }
     if (STATE && more) tk.template load<REV>(tid, next);
-    if (more) tv.template load<REV>(tid, next);
+    if (more) tv.template load<REV>(vid, next);
     if (ci + 2 < chunks) load_gate(t0 + 2 * kOn);
     values();
     if (!STATE) {
@@ -671,18 +675,18 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
     if (done) update(dec);
     __syncthreads();
     if (!STATE && sh.bad != 0) break;
-    if (DOT && tid < n) {
+    if (DOT && vid < n) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) sum += sh.dot[w][tid];
+      for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][vid];
       const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p.dot + ((int64_t(nb) * p.batch + b) * p.L + t0) * p.H + h, (short)0,
                                                           ((C - 1) * H + 1) * 4, 0x00020000);
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, tid * H * 4, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, vid * H * 4, 0, 0);
     }
     if (ci + 1 == chunks) break;
   }
   // the accumulators as the state itself
-  multiply(STATE || done ? sh.dec[ci & 1].after : sh.dec[ci & 1].before);
+  multiply(STATE || done ? sh.dec[part][ci & 1].after : sh.dec[part][ci & 1].before);
   bool slow = !STATE && sh.bad != 0;
   if (STATE) {
     float chk = 0.f;
@@ -715,7 +719,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       for (int i = 0; i < n; ++i) {
         const int64_t t = t0 + (REV ? n - 1 - i : i);
         lane = lin_lane();
-        tid = 64 * wave + lane;
+        tid = 64 * all_wave + lane;
         l16 = lane & 15;
         g = lane >> 4;
         __syncthreads();
@@ -765,11 +769,11 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
           if constexpr (DOT) {
             // (what a wavefront whose first chunk stands has left there is that chunk's)
             for (int x = 8; x > 0; x /= 2) dot += __shfl_xor(dot, x);
-            if (lane == 0 && !stands) sh.dot[wave][t - t0] = dot;
+            if (lane == 0 && !stands) sh.dot[all_wave][t - t0] = dot;
             __syncthreads();
-            if (tid == 0) {
+            if (wave == 0 && lane == 0) {
               float sum = 0.f;
-              for (int w = 0; w < NW; ++w) sum += sh.dot[w][t - t0];
+              for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][t - t0];
               p.dot[((int64_t(nb) * p.batch + b) * p.L + t) * p.H + h] = sum;
             }
           }
@@ -790,19 +794,26 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
   }
 }
 
-template <typename T, int KD, int NW, bool REV, bool STATE, bool DOT>
+template <typename T, int KD, int NW, int HP, bool REV, bool STATE, bool DOT>
 hipError_t lin_launch(const LinParams& p, hipStream_t stream) {
-  const int64_t items = p.batch * p.H * p.nblk * (STATE ? p.nseg - 1 : p.nseg);
+  const int64_t items = p.batch * (p.H / HP) * p.nblk * (STATE ? p.nseg - 1 : p.nseg);
   if (items == 0) return hipSuccess;
-  lin_kernel<T, KD, NW, REV, STATE, DOT><<<dim3(uint32_t(items)), dim3(64 * NW), 0, stream>>>(p);
+  lin_kernel<T, KD, NW, HP, REV, STATE, DOT><<<dim3(uint32_t(items)), dim3(64 * NW), 0, stream>>>(p);
   return hipGetLastError();
 }
 
-template <typename T, int KD, int NW>
+template <typename T, int KD, int NW, int HP>
 hipError_t lin_dispatch(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  if (state) return rev ? lin_launch<T, KD, NW, true, true, false>(p, stream) : lin_launch<T, KD, NW, false, true, false>(p, stream);
-  if (p.dot) return rev ? lin_launch<T, KD, NW, true, false, true>(p, stream) : lin_launch<T, KD, NW, false, false, true>(p, stream);
-  return rev ? lin_launch<T, KD, NW, true, false, false>(p, stream) : lin_launch<T, KD, NW, false, false, false>(p, stream);
+  if (state) return rev ? lin_launch<T, KD, NW, HP, true, true, false>(p, stream) : lin_launch<T, KD, NW, HP, false, true, false>(p, stream);
+  if constexpr (HP == 1)
+    if (p.dot) return rev ? lin_launch<T, KD, NW, HP, true, false, true>(p, stream) : lin_launch<T, KD, NW, HP, false, false, true>(p, stream);
+  return rev ? lin_launch<T, KD, NW, HP, true, false, false>(p, stream) : lin_launch<T, KD, NW, HP, false, false, false>(p, stream);
+}
+
+template <typename T, int KD>
+hipError_t lin_choose(bool rev, bool state, const LinParams& p, hipStream_t stream) {
+  if (p.vd > 64) return lin_dispatch<T, KD, 8, 1>(rev, state, p, stream);
+  return p.pairs ? lin_dispatch<T, KD, 8, 2>(rev, state, p, stream) : lin_dispatch<T, KD, 4, 1>(rev, state, p, stream);
 }
 
 }  // namespace

@@ -314,6 +314,7 @@ struct LinParams {
   int64_t nchunks;      // ceil(L / lin_chunk())
   int64_t seg_chunks;   // chunks of a segment
   int32_t nseg, nblk;   // segments; blocks of lin_cols() columns
+  int32_t pairs;        // 1: heads 2 i and 2 i + 1 share their q and k and vd is at most 64: a workgroup takes both
 };
 constexpr int lin_kd(int64_t kd) { return kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
 constexpr int lin_cols(int64_t vd) { return vd <= 64 ? 64 : 128; }

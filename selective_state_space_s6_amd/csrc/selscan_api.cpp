@@ -5,7 +5,6 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
-#include <cstdlib>
 #include <initializer_list>
 #include <mutex>
 #include <utility>
@@ -1320,7 +1319,17 @@ static bool rows_apart(std::initializer_list<std::pair<int64_t, int64_t>> axes, 
   return true;
 }
 
-static int lin_plan(const selscan_linattn_dims* dims, bool want_dg, LinPlan* out) {
+// How often a walk's workgroups (one per batch row, head or pair of heads, and block of columns) fit onto 256 compute
+// units at once: the registers and the LDS of one hold two of eight wavefronts or three of four, those of
+// fp32 or of 256 channels one, and more of the narrowest.
+static int64_t lin_slots(bool bf16, int64_t kd, int64_t vd, bool shared, int64_t heads) {
+  const int KD = selscan::lin_kd(kd);
+  const bool pairs = vd <= 64 && shared, eight = vd > 64 || pairs;
+  const int64_t at_once = !bf16 ? (KD == 64 && !eight ? 2 : 1) : KD == 256 ? 1 : eight ? 2 : KD == 64 ? 4 : 3;
+  return 256 * at_once / ((pairs ? (heads + 1) / 2 : heads) * lin_blocks(vd));
+}
+
+static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, LinPlan* out) {
   if (!dims) return SELSCAN_ERR_NULL;
   if (dims->abi_version != SELSCAN_ABI_VERSION) return SELSCAN_ERR_ABI;
   const selscan_linattn_dims& d = *dims;
@@ -1346,22 +1355,24 @@ static int lin_plan(const selscan_linattn_dims* dims, bool want_dg, LinPlan* out
   LinPlan p;
   if (d.batch * d.seqlen > 0) {
     const int64_t f = int64_t(sizeof(float)), bh = d.batch * d.nheads, rows = bh * d.seqlen;
-    const int64_t chunks = (d.seqlen + 63) / 64, items = bh * lin_blocks(d.dv);
+    const int64_t chunks = (d.seqlen + 63) / 64, share = d.nheads / d.qk_heads;
+    const bool bf16 = d.io_dtype == SELSCAN_BF16;
     p.seg_len = d.seqlen;
-    // fewer workgroups than fill the GPU's 256 compute units: the sequence is split into segments of at
-    // least 4 chunks of 64 tokens
-    if (const char* ev = getenv("LINSEG")) {
-      int64_t n = atoi(ev);
-      if (n > chunks) n = chunks;
-      if (n > 1) { const int64_t len = (chunks + n - 1) / n; p.seg_len = 64 * len; p.nseg = int32_t((chunks + len - 1) / len); }
-    } else if (items < 384) {
-      int64_t n = (512 + items - 1) / items;
-      if (n > chunks / 4) n = chunks / 4;
-      if (n > 1) {
-        const int64_t len = (chunks + n - 1) / n;
-        p.seg_len = 64 * len;
-        p.nseg = int32_t((chunks + len - 1) / len);
-      }
+    // Fewer workgroups than a third of what 256 compute units hold: the sequence is split into segments, as many as
+    // fill them once, of 2 chunks of 64 tokens at least (fp32: 1).  Between a third and one, what the split's
+    // passes cost is what it gains (bf16, 4 x 80 heads x 8192, 128 x 64: 725 us whole, 739 in 2; 1 x 32 x
+    // 16384, 128 x 128: 1190 whole, 232 in 16; fp32, 1 x 12 x 333, 128 x 128: 92 whole, 42 in 6).
+    int64_t n = lin_slots(bf16, d.dk, d.dv, share % 2 == 0, bh);
+    if (bwd) {
+      const int64_t m = lin_slots(bf16, d.dv, d.dk, false, bh);
+      if (m < n) n = m;
+    }
+    const int64_t most = bf16 ? chunks / 2 : chunks;
+    if (n > most) n = most;
+    if (n >= 3) {
+      const int64_t len = (chunks + n - 1) / n;
+      p.seg_len = 64 * len;
+      p.nseg = int32_t((chunks + len - 1) / len);
     }
     if (p.nseg > 1) {
       p.seg_bytes = ws_round(f * bh * p.nseg * d.dk * d.dv);
@@ -1416,6 +1427,7 @@ static selscan::LinParams lin_params(const LinPlan& pl, const selscan::LinTensor
   p.seg_chunks = (pl.seg_len + chunk - 1) / chunk;
   p.nseg = pl.nseg;
   p.nblk = int32_t(lin_blocks(vd));
+  p.pairs = vd <= 64 && q.share % 2 == 0 && k.share % 2 == 0;
   p.seg = static_cast<float*>(ws);
   p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off_decay);
   return p;
@@ -1451,19 +1463,19 @@ void linear_attention_dims_init(selscan_linattn_dims* dims, int io_dtype, int64_
 
 size_t linear_attention_workspace_size(const selscan_linattn_dims* dims) {
   LinPlan pl;
-  return lin_plan(dims, false, &pl) == SELSCAN_OK ? pl.fwd_bytes : 0;
+  return lin_plan(dims, false, false, &pl) == SELSCAN_OK ? pl.fwd_bytes : 0;
 }
 
 size_t linear_attention_bwd_workspace_size(const selscan_linattn_dims* dims, int want_dlog_decay) {
   LinPlan pl;
-  return lin_plan(dims, want_dlog_decay != 0, &pl) == SELSCAN_OK ? pl.bwd_bytes : 0;
+  return lin_plan(dims, true, want_dlog_decay != 0, &pl) == SELSCAN_OK ? pl.bwd_bytes : 0;
 }
 
 int linear_attention_fwd(const void* q, const void* k, const void* v, const float* log_decay, void* o,
                          const float* initial_state, float* last_state, const selscan_linattn_dims* dims,
                          void* workspace, size_t workspace_bytes, void* stream) {
   LinPlan pl;
-  int st = lin_plan(dims, false, &pl);
+  int st = lin_plan(dims, false, false, &pl);
   if (st != SELSCAN_OK) return st;
   const selscan_linattn_dims& d = *dims;
   const bool no_tokens = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16;
@@ -1510,7 +1522,7 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
                          void* workspace, size_t workspace_bytes, void* stream) {
   LinPlan pl;
   const bool want_dg = dlog_decay != nullptr;
-  int st = lin_plan(dims, want_dg, &pl);
+  int st = lin_plan(dims, true, want_dg, &pl);
   if (st != SELSCAN_OK) return st;
   const selscan_linattn_dims& d = *dims;
   const bool no_tokens = d.batch * d.seqlen == 0, bf16 = d.io_dtype == SELSCAN_BF16, shared = d.nheads != d.qk_heads;
@@ -1625,7 +1637,7 @@ int linear_attention_step(const void* q, const void* k, const void* v, const flo
                           int64_t slots, const int32_t* read_slots, const int32_t* write_slots,
                           const selscan_linattn_dims* dims, void* stream) {
   LinPlan pl;
-  const int st = lin_plan(dims, false, &pl);
+  const int st = lin_plan(dims, false, false, &pl);
   if (st != SELSCAN_OK) return st;
   const selscan_linattn_dims& d = *dims;
   if (d.seqlen != 1 || slots < 0) return SELSCAN_ERR_DIMS;
