@@ -619,7 +619,8 @@ size_t linear_attention_workspace_size(const selscan_linattn_dims* dims);
  *                    or NULL.  Zero where the state starts anew.
  *   dinitial_state : [batch][nheads][dk][dv] fp32, or NULL; it and dlast_state may be one buffer
  *   workspace      : linear_attention_bwd_workspace_size(dims, dlog_decay != NULL) bytes, as above
- * All outputs are written, never accumulated into; sums run in a fixed order.
+ * All outputs are written, never accumulated into; sums run in a fixed order.  nheads * dk and
+ * nheads * dv must be at most 2^22 where seqlen is above 1.
  */
 int linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay,
                          const float* initial_state, const void* d_o, const float* dlast_state, void* dq, void* dk,

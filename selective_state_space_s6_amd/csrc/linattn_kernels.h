@@ -679,9 +679,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][vid];
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p.dot + ((int64_t(nb) * p.batch + b) * p.L + t0) * p.H + h, (short)0,
-                                                          ((C - 1) * H + 1) * 4, 0x00020000);
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, vid * H * 4, 0, 0);
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p.dot + (nb * p.batch * p.H + bh) * p.L + t0, (short)0, n * 4, 0x00020000);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, vid * 4, 0, 0);
     }
     if (ci + 1 == chunks) break;
   }
@@ -774,7 +773,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_
             if (wave == 0 && lane == 0) {
               float sum = 0.f;
               for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][t - t0];
-              p.dot[((int64_t(nb) * p.batch + b) * p.L + t) * p.H + h] = sum;
+              p.dot[(nb * p.batch * p.H + bh) * p.L + t] = sum;
             }
           }
         }

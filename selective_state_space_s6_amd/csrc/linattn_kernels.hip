@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kDecayThreads) void lin_decay_kernel(LinDecayParams
       v[e] = 0.0;
       start[e] = false;
       if (t + e < p.L) {
-        const int64_t at = (b * p.L + t + e) * p.H + h;
+        const int64_t at = bh * p.L + t + e;
         for (int i = 0; i < p.nq; ++i) v[e] += double(p.qdq[i * part + at]);
         for (int i = 0; i < p.nk; ++i) v[e] -= double(p.kdk[i * part + at]);
         start[e] = double(p.g[b * p.g_sb + (t + e) * p.g_sl + h * p.g_sh]) * 1.4426950408889634 < -150.0;

@@ -14,20 +14,31 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
-// VEC consecutive elements: 16 bytes, or one element.
-template <typename T, int VEC> __device__ __forceinline__ void norm_load(const T* p, float* v) {
-  if constexpr (VEC == 1) {
-    v[0] = io_traits<T>::widen(*p);
-  } else {
-    union { u32x4 q; T e[VEC]; } u;
-    u.q = *reinterpret_cast<const u32x4*>(p);
+// VEC consecutive elements as they lie in memory: 16 bytes, or one element.
+template <typename T, int VEC> struct NormRaw {
+  using type = u32x4;
+  static __device__ __forceinline__ type load(const T* p) { return *reinterpret_cast<const u32x4*>(p); }
+  static __device__ __forceinline__ void widen(type r, float* v) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = io_traits<T>::widen(u.e[i]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        v[2 * i] = __uint_as_float(r[i] << 16);
+        v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+      } else {
+        v[i] = __uint_as_float(r[i]);
+      }
+    }
   }
-}
+};
+template <typename T> struct NormRaw<T, 1> {
+  using type = T;
+  static __device__ __forceinline__ type load(const T* p) { return *p; }
+  static __device__ __forceinline__ void widen(type r, float* v) { v[0] = io_traits<T>::widen(r); }
+};
 template <int VEC> __device__ __forceinline__ void norm_load_f32(const float* p, float* v) {
+  constexpr int N = VEC < 4 ? 1 : 4;
 #pragma unroll
-  for (int i = 0; i < VEC; i += VEC < 4 ? 1 : 4) norm_load<float, VEC < 4 ? 1 : 4>(p + i, v + i);
+  for (int i = 0; i < VEC; i += N) NormRaw<float, N>::widen(NormRaw<float, N>::load(p + i), v + i);
 }
 template <typename T, int VEC> __device__ __forceinline__ void norm_store(T* p, const float* v) {
   if constexpr (VEC == 1) {
@@ -44,6 +55,21 @@ template <typename T, int VEC> __device__ __forceinline__ void norm_store(T* p, 
     *reinterpret_cast<f*>(p) = f{v[0], v[1], v[2], v[3]};
   }
 }
+
+// What a thread has of a group of channels of one row, on its way: all that a row needs is asked for before
+// anything of it is waited for.
+template <typename T, int VEC, int EPT> struct NormPiece {
+  typename NormRaw<T, VEC>::type raw[EPT];
+  __device__ __forceinline__ void load(const T* src, int lanes, int lane, int width) {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = (i * lanes + lane) * VEC;
+      raw[i] = typename NormRaw<T, VEC>::type{};
+      if (c < width) raw[i] = NormRaw<T, VEC>::load(src + c);
+    }
+  }
+  __device__ __forceinline__ void widen(int i, float* v) const { NormRaw<T, VEC>::widen(raw[i], v); }
+};
 
 // The sum over the `lanes` threads of a group, in every one of them.
 __device__ __forceinline__ float norm_sum(float v, int lanes, float* tmp) {
@@ -67,16 +93,13 @@ __device__ __forceinline__ float norm_act(float t, bool silu, float& slope) {
 
 template <typename T, int VEC, int EPT>
 struct NormRow {
-  float x[EPT * VEC];      // then (x - mean) / sqrt(var + eps)
+  float x[EPT * VEC];      // (x - mean) / sqrt(var + eps)
   float r;
-  __device__ __forceinline__ void load(const T* src, int lanes, int lane, int width, float eps, float* tmp) {
+  __device__ __forceinline__ void form(const NormPiece<T, VEC, EPT>& raw, int lanes, int lane, int width, float eps, float* tmp) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = (i * lanes + lane) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[i * VEC + e] = 0.f;
-      if (c < width) norm_load<T, VEC>(src + c, x + i * VEC);
+      raw.widen(i, x + i * VEC);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s += x[i * VEC + e];
     }
@@ -106,11 +129,13 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
   if (gi >= p.rows * p.groups) return;
   const int64_t row = gi / p.groups, b = row / p.L, l = row % p.L;
   const int64_t c0 = gi % p.groups * p.width;
-  const T* x = static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0;
-  const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0 : nullptr;
+  const bool gate = p.z != nullptr;
+  NormPiece<T, VEC, EPT> x, z;
+  x.load(static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0, lanes, lane, p.width);
+  if (gate) z.load(static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0, lanes, lane, p.width);
   T* y = static_cast<T*>(p.y) + b * p.y_sb + l * p.y_sl + c0;
   NormRow<T, VEC, EPT> n;
-  n.load(x, lanes, lane, p.width, p.eps, tmp);
+  n.form(x, lanes, lane, p.width, p.eps, tmp);
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int c = (i * lanes + lane) * VEC;
@@ -118,19 +143,20 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
     float w[VEC], o[VEC], t[VEC];
     if (p.weight) norm_load_f32<VEC>(p.weight + c0 + c, w);
     if (p.bias) norm_load_f32<VEC>(p.bias + c0 + c, o);
-    if (z) norm_load<T, VEC>(z + c, t);
+    if (gate) z.widen(i, t);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float v = fmaf(n.x[i * VEC + e], p.weight ? w[e] : 1.f, p.bias ? o[e] : 0.f);
       float slope;
-      o[e] = z ? v * norm_act(t[e], p.silu, slope) : norm_act(v, p.silu, slope);
+      o[e] = gate ? v * norm_act(t[e], p.silu, slope) : norm_act(v, p.silu, slope);
     }
     norm_store<T, VEC>(y + c, o);
   }
 }
 
 // A workgroup keeps to `256 / lanes` groups of channels (of several rows at once where there are fewer groups)
-// and walks every `splits`-th row, so that the sums for weight and bias stay in registers.
+// and walks every `splits`-th row, so that the sums for weight and bias stay in registers.  The next row is
+// asked for before this one is looked at.
 template <typename T, int VEC, int EPT>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   __shared__ float tmp[4];
@@ -138,58 +164,62 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   const int gslot = slot % p.gper, rslot = slot / p.gper, rows_at_once = 256 / lanes / p.gper;
   const int64_t cb = blockIdx.x % p.cblocks, split = blockIdx.x / p.cblocks;
   const int64_t group = cb * p.gper + gslot;
-  const bool live = group < p.groups;
+  if (group >= p.groups) return;                  // (a group's threads all leave, or none)
   const int64_t c0 = group * p.width;
-  const int64_t part = split * rows_at_once + rslot;
+  const int64_t part = split * rows_at_once + rslot, step = p.splits * rows_at_once;
+  const bool gate = p.z != nullptr;
   float w[EPT * VEC], o[EPT * VEC], dw[EPT * VEC], db[EPT * VEC];
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int c = (i * lanes + lane) * VEC;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) { w[i * VEC + e] = 1.f; o[i * VEC + e] = dw[i * VEC + e] = db[i * VEC + e] = 0.f; }
-    if (live && c < p.width) {
+    if (c < p.width) {
       if (p.weight) norm_load_f32<VEC>(p.weight + c0 + c, w + i * VEC);
       if (p.bias) norm_load_f32<VEC>(p.bias + c0 + c, o + i * VEC);
     }
   }
   const float inv = 1.f / float(p.width);
-  for (int64_t row = part; row < p.rows && live; row += p.splits * rows_at_once) {
+  NormPiece<T, VEC, EPT> x, z, dy;
+  auto ask = [&](int64_t row) {
     const int64_t b = row / p.L, l = row % p.L;
-    const T* dy = static_cast<const T*>(p.dy) + b * p.y_sb + l * p.y_sl + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0 : nullptr;
+    x.load(static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0, lanes, lane, p.width);
+    if (gate) z.load(static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0, lanes, lane, p.width);
+    dy.load(static_cast<const T*>(p.dy) + b * p.y_sb + l * p.y_sl + c0, lanes, lane, p.width);
+  };
+  if (part < p.rows) ask(part);
+  for (int64_t row = part; row < p.rows; row += step) {
+    const NormPiece<T, VEC, EPT> now_x = x, now_z = z, now_dy = dy;
+    if (EPT * VEC <= 16 && row + step < p.rows) ask(row + step);   // (wider groups leave no registers for it)
     const int64_t out = row * p.groups * p.width + c0;
     NormRow<T, VEC, EPT> n;
-    n.load(static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0, lanes, lane, p.width, p.eps, tmp);
+    n.form(now_x, lanes, lane, p.width, p.eps, tmp);
     float u[EPT * VEC], m1 = 0.f, m2 = 0.f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
       const int c = (i * lanes + lane) * VEC;
       float d[VEC], t[VEC], dz[VEC];
+      now_dy.widen(i, d);                         // (zero behind the group's end: nothing comes of it there)
+      if (gate) now_z.widen(i, t);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) u[i * VEC + e] = 0.f;
-      if (c < p.width) {
-        norm_load<T, VEC>(dy + c, d);
-        if (z) norm_load<T, VEC>(z + c, t);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int k = i * VEC + e;
-          const float v = fmaf(n.x[k], w[k], o[k]);
-          float slope, dn;
-          if (z) {
-            dn = d[e] * norm_act(t[e], p.silu, slope);
-            dz[e] = d[e] * v * slope;
-          } else {
-            norm_act(v, p.silu, slope);
-            dn = d[e] * slope;
-          }
-          dw[k] = fmaf(dn, n.x[k], dw[k]);
-          db[k] += dn;
-          u[k] = dn * w[k];
-          m1 += u[k];
-          m2 = fmaf(u[k], n.x[k], m2);
+      for (int e = 0; e < VEC; ++e) {
+        const int k = i * VEC + e;
+        const float v = fmaf(n.x[k], w[k], o[k]);
+        float slope, dn;
+        if (gate) {
+          dn = d[e] * norm_act(t[e], p.silu, slope);
+          dz[e] = d[e] * v * slope;
+        } else {
+          norm_act(v, p.silu, slope);
+          dn = d[e] * slope;
         }
-        if (z) norm_store<T, VEC>(static_cast<T*>(p.dz) + out + c, dz);
+        dw[k] = fmaf(dn, n.x[k], dw[k]);
+        db[k] += dn;
+        u[k] = dn * w[k];
+        m1 += u[k];
+        m2 = fmaf(u[k], n.x[k], m2);
       }
+      if (gate && c < p.width) norm_store<T, VEC>(static_cast<T*>(p.dz) + out + c, dz);
     }
     m1 = norm_sum(m1, lanes, tmp) * inv;
     m2 = norm_sum(m2, lanes, tmp) * inv;
@@ -206,17 +236,28 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
       }
       if (c < p.width) norm_store<T, VEC>(static_cast<T*>(p.dx) + out + c, d);
     }
+    if (EPT * VEC > 16 && row + step < p.rows) ask(row + step);
   }
-  if (!live || !p.part) return;
-  const int64_t C = p.groups * p.width;
+  if (!p.part) return;
+  // the rows that a wavefront takes at once, into its first threads
+  for (int d = lanes * p.gper; d < 64; d *= 2) {
+#pragma unroll
+    for (int k = 0; k < EPT * VEC; ++k) {
+      dw[k] += __shfl_xor(dw[k], d);
+      db[k] += __shfl_xor(db[k], d);
+    }
+  }
+  const int span = lanes * p.gper < 64 ? 64 : lanes * p.gper;      // threads of one part
+  if (int(threadIdx.x) % span >= lanes * p.gper) return;
+  const int64_t C = p.groups * p.width, at = split * (256 / span) + threadIdx.x / span;
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int c = (i * lanes + lane) * VEC;
     if (c >= p.width) break;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      p.part[2 * part * C + c0 + c + e] = dw[i * VEC + e];
-      p.part[(2 * part + 1) * C + c0 + c + e] = db[i * VEC + e];
+      p.part[2 * at * C + c0 + c + e] = dw[i * VEC + e];
+      p.part[(2 * at + 1) * C + c0 + c + e] = db[i * VEC + e];
     }
   }
 }
@@ -296,7 +337,8 @@ NormPlan norm_plan(bool bf16, bool vec, int64_t rows, int64_t groups, int64_t wi
   pl.splits = (1024 + pl.cblocks - 1) / pl.cblocks;
   if (pl.splits > most) pl.splits = most;
   if (pl.splits < 1) pl.splits = 1;
-  pl.parts = pl.splits * at_once;
+  const int64_t span = pl.lanes * pl.gper < 64 ? 64 : pl.lanes * pl.gper;
+  pl.parts = pl.splits * (256 / span);
   return pl;
 }
 

@@ -306,7 +306,7 @@ struct LinParams {
   int64_t s_row, s_col; // strides of s0 and s1 within a block
   float* seg;           // workspace: [batch][H][nseg] blocks of kd * vd, laid out as s0's
   float* seg_decay;     // workspace: [batch][H][nseg], negative where the state starts anew
-  LinTensor x;          // dot: out . x per token, [nblk][batch][L][H]; null: not wanted
+  LinTensor x;          // dot: out . x per token, [nblk][batch][H][L]; null: not wanted
   float* dot;
   int64_t batch, L, H;
   int32_t kd, vd;       // width of q and k, of v and out (1 .. 256)
@@ -338,8 +338,8 @@ hipError_t launch_lin_heads(bool bf16, const float* part, void* out, int64_t tok
 
 // The decays' gradient from the rows' products: dg_t = <last, dlast> + sum_{i >= t} (qdq_i - kdk_i)
 struct LinDecayParams {
-  const float* qdq;     // [nq][batch][L][H]
-  const float* kdk;     // [nk][batch][L][H]
+  const float* qdq;     // [nq][batch][H][L]
+  const float* kdk;     // [nk][batch][H][L]
   const float* last;    // [batch][H][state], with dlast; both may be null (zero)
   const float* dlast;
   const float* g;

@@ -1352,6 +1352,8 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       d.batch * d.nheads * ((wide + 63) / 64) >= kMaxItems)
     return SELSCAN_ERR_UNSUPPORTED;
   if (d.seqlen > (int64_t(1) << 31) - 1) return SELSCAN_ERR_UNSUPPORTED;
+  // the gradients are contiguous: their tokens are this far apart
+  if (bwd && d.seqlen > 1 && d.nheads * wide > kMaxRow) return SELSCAN_ERR_UNSUPPORTED;
   LinPlan p;
   if (d.batch * d.seqlen > 0) {
     const int64_t f = int64_t(sizeof(float)), bh = d.batch * d.nheads, rows = bh * d.seqlen;
@@ -1367,7 +1369,7 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       const int64_t m = lin_slots(bf16, d.dv, d.dk, false, bh);
       if (m < n) n = m;
     }
-    const int64_t most = bf16 ? chunks / 2 : chunks;
+    const int64_t most = bf16 ? (chunks + 1) / 2 : chunks;
     if (n > most) n = most;
     if (n >= 3) {
       const int64_t len = (chunks + n - 1) / n;

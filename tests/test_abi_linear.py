@@ -102,6 +102,9 @@ def test_long_token_strides(name):
     assert fwd(lin(batch=1, **{name: (1 << 22) + 1})) == -3 and bwd(lin(batch=1, **{name: (1 << 22) + 1})) == -3
     assert bwd(lin(batch=1, L=1, **{name: 1 << 30}), ws=F + 16, n=1 << 40) == -6      # one token's is not looked at
     assert fwd(lin(L=1 << 31, batch=1)) == -3
+    assert fwd(lin(batch=1, g_sl=(1 << 22) + 1)) == -3
+    wide = lin(batch=1, L=3, H=1 << 16, Hk=1, K=8, V=128)                       # its gradients' rows are 2^23 apart
+    assert bwd(wide, ws=F + 16, n=1 << 60) == -3
 
 
 def test_linear_null_and_alignment():
