@@ -149,8 +149,8 @@ __device__ __forceinline__ float lin_decay(float log2d) {
 template <typename T, int KD> constexpr int lin_chunk_of() { return sizeof(T) == 4 && KD == 256 ? 32 : 64; }
 
 // Wavefronts that a SIMD is to hold, NW of them a workgroup: as many as the LDS of a compute unit holds tiles for.
-template <typename T, int KD, int NW, bool STATE> constexpr int lin_waves() {
-  return sizeof(T) == 4 || KD == 256 ? (NW == 8 ? 2 : 1) : NW == 8 ? 4 : 3;
+template <typename T, int KD, int NW, bool DOT> constexpr int lin_waves() {
+  return sizeof(T) == 4 || KD == 256 ? (NW == 8 ? 2 : 1) : NW == 8 ? 4 : KD == 128 && DOT ? 2 : 3;
 }
 
 // What the tokens of a chunk are to one another.
@@ -254,13 +254,13 @@ struct LinTile {
 // its accumulators, which are at once the operand of its product with the queries.
 // STATE: only the state at the segment's end, from zero.
 // DOT: the rows' products with x too.  The decays' gradient is what remains of their sum over all later tokens in
-// one walk less that in the other, so the state then meets q with its 24 bits (else with 16); what P loses,
-// it loses in both walks alike, and 16 bits do (else 8).
+// one walk less that in the other, so pairs and state then go to the matrix cores with 24 bits.  Else the pairs
+// are rounded to 8, as the result is, and the state to 16.
 template <typename T, int KD, int NW, int HP, bool REV, bool STATE, bool DOT>
-__global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, STATE>())) void lin_kernel(LinParams p) {
+__global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, DOT>())) void lin_kernel(LinParams p) {
   using io = lin_io<T>;
   using frag = typename io::frag;
-  constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2, NPP = NP == 3 ? 2 : 1;   // parts of the state and of the pairs on the matrix cores
+  constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2, NPP = NP == 3 ? 3 : 1;   // parts of the state and of the pairs on the matrix cores
   constexpr int NX = sizeof(T) == 2 ? 3 : 1;      // the state is held in fp32: what is added to it keeps 24 bits
   using Sh = LinShared<T, KD, NW, HP, STATE, DOT, NPP>;
   constexpr int kWaves = NW / HP;                 // of a head
