@@ -4,8 +4,8 @@
 
 namespace selscan {
 
-hipError_t launch_lin_bf16_64(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  return lin_choose<uint16_t, 64>(rev, state, p, stream);
+hipError_t launch_lin_bf16_64(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  return lin_choose<uint16_t, 64>(walk, p, stream);
 }
 
 }  // namespace selscan

@@ -4,8 +4,8 @@
 
 namespace selscan {
 
-hipError_t launch_lin_f32_128(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  return lin_choose<float, 128>(rev, state, p, stream);
+hipError_t launch_lin_f32_128(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  return lin_choose<float, 128>(walk, p, stream);
 }
 
 }  // namespace selscan

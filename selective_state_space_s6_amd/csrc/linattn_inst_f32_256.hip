@@ -4,8 +4,8 @@
 
 namespace selscan {
 
-hipError_t launch_lin_f32_256(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  return lin_choose<float, 256>(rev, state, p, stream);
+hipError_t launch_lin_f32_256(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  return lin_choose<float, 256>(walk, p, stream);
 }
 
 }  // namespace selscan

@@ -162,8 +162,9 @@ template <int C> struct alignas(16) LinDecays {
   float before, after;      // the held state's scale before the chunk, and behind it
 };
 
-template <typename T, int KD, int NW, int HP, bool STATE, bool DOT, int NPP>
+template <typename T, int KD, int NW, int HP, bool STATE, bool DOT>
 struct alignas(16) LinShared {
+  static constexpr int NPP = sizeof(T) == 2 && DOT ? 3 : 1;       // parts of the pairs on the matrix cores
   static constexpr int C = lin_chunk_of<T, KD>(), kWP = C * int(sizeof(T)) < 128 ? 128 / int(sizeof(T)) : C;
   T q[STATE ? 8 : C * KD];
   T k[C * KD];
@@ -249,6 +250,8 @@ struct LinTile {
   }
 };
 
+template <LinWalk WALK> struct LinWalks { LinParams p[WALK == LinWalk::states || WALK == LinWalk::grads ? 2 : 1]; };
+
 // One workgroup of NW wavefronts walks the chunks of one segment of HP heads of one batch row that share their
 // queries and keys, for 16 NW / HP columns of v each: a wavefront owns 16 of them, and the state's [KD][16] in
 // its accumulators, which are at once the operand of its product with the queries.
@@ -256,563 +259,584 @@ struct LinTile {
 // DOT: the rows' products with x too.  The decays' gradient is what remains of their sum over all later tokens in
 // one walk less that in the other, so pairs and state then go to the matrix cores with 24 bits.  Else the pairs
 // are rounded to 8, as the result is, and the state to 16.
-template <typename T, int KD, int NW, int HP, bool REV, bool STATE, bool DOT>
-__global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, DOT>())) void lin_kernel(LinParams p) {
+template <typename T, int KD, int NW, int HP, LinWalk WALK>
+__global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::grads>())) void lin_kernel(LinWalks<WALK> walks) {
+  constexpr bool STATE = WALK == LinWalk::state || WALK == LinWalk::states, DOT = WALK == LinWalk::grads;
   using io = lin_io<T>;
   using frag = typename io::frag;
-  constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2, NPP = NP == 3 ? 3 : 1;   // parts of the state and of the pairs on the matrix cores
+  constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2;   // parts of the state on the matrix cores
   constexpr int NX = sizeof(T) == 2 ? 3 : 1;      // the state is held in fp32: what is added to it keeps 24 bits
-  using Sh = LinShared<T, KD, NW, HP, STATE, DOT, NPP>;
-  constexpr int kWaves = NW / HP;                 // of a head
-  constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kWP = Sh::kWP, kThreads = 64 * NW;
-  constexpr int kDecayWave = kWaves - 1;          // has the least to do with the pairs
+  using Sh = LinShared<T, KD, NW, HP, STATE, DOT>;
+  constexpr int NPP = Sh::NPP;
   __shared__ Sh sh;
 
-  const int all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), part = all_wave / kWaves, wave = all_wave % kWaves;
-  int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
-  // The heads of a token lie next to one another, so the rows of one head are a power of two apart as a
-  // rule, in one channel of the L2: an XCD takes the heads side by side.
-  const int item = xcd_contiguous_block(blockIdx.x, gridDim.x);
-  const int segs = STATE ? p.nseg - 1 : p.nseg;   // (nothing is behind the last segment)
-  const int H = int(p.H), heads = H / HP, nb = item / heads % p.nblk, sidx = item / heads / p.nblk % segs;
-  const int64_t h = item % heads * HP + part, b = item / heads / p.nblk / segs, bh = b * H + h;
-  const int seg = STATE && REV ? sidx + 1 : sidx;
-  const int64_t chunk0 = int64_t(seg) * p.seg_chunks;
-  const int chunks = int(p.nchunks - chunk0 < p.seg_chunks ? p.nchunks - chunk0 : p.seg_chunks);
-  const int col0 = nb * kWV, wcol = wave * 16;
+  auto segment = [&](auto reversed, const LinParams& p, const int item) __attribute__((always_inline)) {
+    constexpr bool REV = decltype(reversed)::value;
+    constexpr int kWaves = NW / HP;                 // of a head
+    constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kWP = Sh::kWP, kThreads = 64 * NW;
+    constexpr int kDecayWave = kWaves - 1;          // has the least to do with the pairs
 
-  f32x4 S[KK][2];
-  auto zero_state = [&] {
-#pragma unroll
-    for (int a = 0; a < KK; ++a) S[a][0] = S[a][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  };
-  // f(four state values, which of them, its place in a head's state)
-  auto each_state = [&](auto&& f) {
-    const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int a = 0; a < KK; ++a)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int kd = 32 * a + 8 * g + 4 * u + r, n = col0 + wcol + l16;
-          if (kd < p.kd && n < p.vd) f(S[a][u], r, p.s_row * kd + p.s_col * n);
-        }
-  };
+    const int all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), part = all_wave / kWaves, wave = all_wave % kWaves;
+    int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
+    const int segs = STATE ? p.nseg - 1 : p.nseg;   // (nothing is behind the last segment)
+    const int H = int(p.H), heads = H / HP, nb = item / heads % p.nblk, sidx = item / heads / p.nblk % segs;
+    const int64_t h = item % heads * HP + part, b = item / heads / p.nblk / segs, bh = b * H + h;
+    const int seg = STATE && REV ? sidx + 1 : sidx;
+    const int64_t chunk0 = int64_t(seg) * p.seg_chunks;
+    const int chunks = int(p.nchunks - chunk0 < p.seg_chunks ? p.nchunks - chunk0 : p.seg_chunks);
+    const int col0 = nb * kWV, wcol = wave * 16;
 
-  auto start_of = [&](int ci) { return (chunk0 + (REV ? chunks - 1 - ci : ci)) * C; };
-  auto tokens_of = [&](int64_t t0) { return int(p.L - t0 < C ? p.L - t0 : C); };
-
-  LinTile<T, KD, C, kThreads> tq, tk;
-  LinTile<T, kWV, C, 64 * kWaves> tv;
-  T* const sv = sh.v + part * C * kWV;
-  T* const sp = STATE ? sh.p : sh.p + part * NPP * C * kWP;
-  if (!STATE) tq.init(p.q, b, h, start_of(0), 0, p.kd);
-  tk.init(p.k, b, h, start_of(0), 0, p.kd);
-  tv.init(p.v, b, h, start_of(0), col0, p.vd);
-  constexpr int64_t kOn = REV ? -C : C;           // tokens from a chunk to the next
-  // the log decays of a chunk, a chunk ahead of its operands
-  const float* gates = p.g + b * p.g_sb + h * p.g_sh + start_of(0) * p.g_sl;
-  const int gsl = int(p.g_sl);
-  float gate = 0.f;
-  auto load_gate = [&](int64_t t0) {
-    if (wave == kDecayWave) {
-      const int n = tokens_of(t0), lane = lin_lane();
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(gates), (short)0, ((n - 1) * gsl + 1) * 4, 0x00020000);
-      gate = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, lane < n ? lane * gsl * 4 : 0x7ffffff0, 0, 0));
-      gates += kOn * gsl;
-    }
-  };
-
-  double total = 0.0;                             // STATE: log2 of the segment's decay
-  bool anew = false;
-  // The state is held as a multiple `scale` (its logarithm, base 2) of the accumulators, which takes up the
-  // chunks' decays until it leaves 2^-16 .. 2^16: most chunks then leave the accumulators as they are.
-  double scale = 0.0;
-  // the factors of a chunk's tokens, of the gates that kDecayWave has loaded
-  auto decays = [&](LinDecays<C>& d) {
-    const int lane = lin_lane();
-    double c = double(gate) * 1.4426950408889634;
-    const bool start = c < -150.0;                // a decay below 2^-150 is none at all
-    if (start) c = 0.0;
+    f32x4 S[KK][2];
+    auto zero_state = [&] {
 #pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const double o = __shfl_up(c, s);
-      if (lane >= s) c += o;
-    }
-    const uint64_t starts = __ballot(start);
-    const double all = __shfl(c, 63);
-    const uint64_t upto = (uint64_t(2) << lane) - 1;
-    const uint64_t before = starts & upto, after = starts & ~upto;
-    const double next = scale + all;
-    const bool fold = starts != 0 || !(next > -16.0 && next < 16.0);
-    const double held = fold ? 0.0 : next;
-    const float f = REV ? (after ? 0.f : lin_decay(float(all - c + scale))) : (before ? 0.f : lin_decay(float(c + scale)));
-    const float w = REV ? (before ? 0.f : lin_decay(float(c - held))) : (after ? 0.f : lin_decay(float(all - c - held)));
-    if (lane < C) {
-      d.hi[lane] = float(c);
-      d.lo[lane] = float(c - double(float(c)));
-      d.f[lane] = f * p.fscale;
-      d.w[lane] = w * p.wscale;
-      d.lim[lane] = REV ? (after ? __builtin_ctzll(after) - 1 : C) : (before ? 63 - __builtin_clzll(before) : 0);
-    }
-    if (lane == 0) {
-      d.mul = starts ? 0.f : fold ? lin_decay(float(next)) : 1.f;
-      d.before = __builtin_amdgcn_exp2f(float(scale));
-      d.after = __builtin_amdgcn_exp2f(float(held));
-    }
-    scale = held;
-    if (STATE) {
-      total += all;
-      anew |= starts != 0;
-    }
-  };
+      for (int a = 0; a < KK; ++a) S[a][0] = S[a][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    // f(four state values, which of them, its place in a head's state)
+    auto each_state = [&](auto&& f) {
+      const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+      for (int a = 0; a < KK; ++a)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int kd = 32 * a + 8 * g + 4 * u + r, n = col0 + wcol + l16;
+            if (kd < p.kd && n < p.vd) f(S[a][u], r, p.s_row * kd + p.s_col * n);
+          }
+    };
 
-  // whether any of the 32 channels are there (the first are; of a width that is no power of two the last may not be)
-  auto there = [&](int a) { return a <= KK / 2 || 32 * a < p.kd; };
-  // ---- the pairs: P_ij = e^{c_i - c_j} (q_i . k_j), as its transpose's tiles (lane: one i, four j)
-  auto pairs = [&](const LinDecays<C>& dec) {
-    constexpr int kUnits = C == 64 ? 6 : 2;       // 16 rows by 32 keys, those that see each other
+    auto start_of = [&](int ci) { return (chunk0 + (REV ? chunks - 1 - ci : ci)) * C; };
+    auto tokens_of = [&](int64_t t0) { return int(p.L - t0 < C ? p.L - t0 : C); };
+
+    LinTile<T, KD, C, kThreads> tq, tk;
+    LinTile<T, kWV, C, 64 * kWaves> tv;
+    T* const sv = sh.v + part * C * kWV;
+    T* const sp = STATE ? sh.p : sh.p + part * NPP * C * kWP;
+    if (!STATE) tq.init(p.q, b, h, start_of(0), 0, p.kd);
+    tk.init(p.k, b, h, start_of(0), 0, p.kd);
+    tv.init(p.v, b, h, start_of(0), col0, p.vd);
+    constexpr int64_t kOn = REV ? -C : C;           // tokens from a chunk to the next
+    // the log decays of a chunk, a chunk ahead of its operands
+    const float* gates = p.g + b * p.g_sb + h * p.g_sh + start_of(0) * p.g_sl;
+    const int gsl = int(p.g_sl);
+    float gate = 0.f;
+    auto load_gate = [&](int64_t t0) {
+      if (wave == kDecayWave) {
+        const int n = tokens_of(t0), lane = lin_lane();
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(gates), (short)0, ((n - 1) * gsl + 1) * 4, 0x00020000);
+        gate = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, lane < n ? lane * gsl * 4 : 0x7ffffff0, 0, 0));
+        gates += kOn * gsl;
+      }
+    };
+
+    double total = 0.0;                             // STATE: log2 of the segment's decay
+    bool anew = false;
+    // The state is held as a multiple `scale` (its logarithm, base 2) of the accumulators, which takes up the
+    // chunks' decays until it leaves 2^-16 .. 2^16: most chunks then leave the accumulators as they are.
+    double scale = 0.0;
+    // the factors of a chunk's tokens, of the gates that kDecayWave has loaded
+    auto decays = [&](LinDecays<C>& d) {
+      const int lane = lin_lane();
+      double c = double(gate) * 1.4426950408889634;
+      const bool start = c < -150.0;                // a decay below 2^-150 is none at all
+      if (start) c = 0.0;
+#pragma unroll
+      for (int s = 1; s < 64; s *= 2) {
+        const double o = __shfl_up(c, s);
+        if (lane >= s) c += o;
+      }
+      const uint64_t starts = __ballot(start);
+      const double all = __shfl(c, 63);
+      const uint64_t upto = (uint64_t(2) << lane) - 1;
+      const uint64_t before = starts & upto, after = starts & ~upto;
+      const double next = scale + all;
+      const bool fold = starts != 0 || !(next > -16.0 && next < 16.0);
+      const double held = fold ? 0.0 : next;
+      const float f = REV ? (after ? 0.f : lin_decay(float(all - c + scale))) : (before ? 0.f : lin_decay(float(c + scale)));
+      const float w = REV ? (before ? 0.f : lin_decay(float(c - held))) : (after ? 0.f : lin_decay(float(all - c - held)));
+      if (lane < C) {
+        d.hi[lane] = float(c);
+        d.lo[lane] = float(c - double(float(c)));
+        d.f[lane] = f * p.fscale;
+        d.w[lane] = w * p.wscale;
+        d.lim[lane] = REV ? (after ? __builtin_ctzll(after) - 1 : C) : (before ? 63 - __builtin_clzll(before) : 0);
+      }
+      if (lane == 0) {
+        d.mul = starts ? 0.f : fold ? lin_decay(float(next)) : 1.f;
+        d.before = __builtin_amdgcn_exp2f(float(scale));
+        d.after = __builtin_amdgcn_exp2f(float(held));
+      }
+      scale = held;
+      if (STATE) {
+        total += all;
+        anew |= starts != 0;
+      }
+    };
+
+    // whether any of the 32 channels are there (the first are; of a width that is no power of two the last may not be)
+    auto there = [&](int a) { return a <= KK / 2 || 32 * a < p.kd; };
+    // ---- the pairs: P_ij = e^{c_i - c_j} (q_i . k_j), as its transpose's tiles (lane: one i, four j)
+    auto pairs = [&](const LinDecays<C>& dec) {
+      constexpr int kUnits = C == 64 ? 6 : 2;       // 16 rows by 32 keys, those that see each other
 #pragma unroll 1
-    for (int unit = wave; unit < kUnits; unit += kWaves) {
-      // C = 64 forward: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1); backward: (3,1) (2,1) (1,1) (1,0) (0,1) (0,0)
-      int it = C == 32 ? unit : unit < 2 ? unit : unit / 2 + 1, ks = C == 32 || unit < 2 ? 0 : unit & 1;
-      if (REV) { it = IT - 1 - it; ks = KS - 1 - ks; }
-      f32x4 acc[2] = {};
-      frag fq[2], fk[2][2];                       // (those of the next product on their way during this one)
-      auto ask = [&](int a) {
-        fq[a & 1] = io::template row<KD>(sh.q, 16 * it + l16, 32 * a + 8 * g);
+      for (int unit = wave; unit < kUnits; unit += kWaves) {
+        // C = 64 forward: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1); backward: (3,1) (2,1) (1,1) (1,0) (0,1) (0,0)
+        int it = C == 32 ? unit : unit < 2 ? unit : unit / 2 + 1, ks = C == 32 || unit < 2 ? 0 : unit & 1;
+        if (REV) { it = IT - 1 - it; ks = KS - 1 - ks; }
+        f32x4 acc[2] = {};
+        frag fq[2], fk[2][2];                       // (those of the next product on their way during this one)
+        auto ask = [&](int a) {
+          fq[a & 1] = io::template row<KD>(sh.q, 16 * it + l16, 32 * a + 8 * g);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) fk[a & 1][u] = io::template row<KD>(sh.k, 32 * ks + 16 * u + l16, 32 * a + 8 * g);
+          for (int u = 0; u < 2; ++u) fk[a & 1][u] = io::template row<KD>(sh.k, 32 * ks + 16 * u + l16, 32 * a + 8 * g);
+        };
+        ask(0);
+#pragma unroll
+        for (int a = 0; a < KK; ++a) {
+          if (a + 1 < KK) ask(a + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          if (there(a)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) acc[u] = io::mma(fk[a & 1][u], fq[a & 1], acc[u]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const int i = 16 * it + l16;
+        const float chi = dec.hi[i], clo = dec.lo[i];
+        const int lim = dec.lim[i];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j0 = 32 * ks + 16 * u + 4 * g;
+          f32x4 val;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = j0 + r;
+            const float d = (chi - dec.hi[j]) + (clo - dec.lo[j]);
+            const bool seen = REV ? j >= i && j <= lim : j <= i && j >= lim;
+            val[r] = acc[u][r] * (__builtin_amdgcn_exp2f(seen ? (REV ? -d : d) : -1e30f) * p.pscale);
+          }
+#pragma unroll
+          for (int x = 0; x < NPP; ++x) {
+            io::store(sp + x * C * kWP + lin_at<T, kWP>(i, j0), val);
+            if (x + 1 < NPP)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) val[r] = lin_rest(val[r]);
+          }
+        }
+      }
+    };
+    // ---- out^T, columns of v down, tokens across: the part of the state
+    f32x4 acc[IT];
+    auto from_state = [&](const LinDecays<C>& dec) {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+      constexpr int kHalf = IT / 2;
+      frag fq[2][2], fs[NP];
+      auto ask = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) fq[i & 1][x] = io::template row<KD>(sh.q, 16 * (2 * (i % kHalf) + x) + l16, 32 * (i / kHalf) + 8 * g);
       };
       ask(0);
 #pragma unroll
-      for (int a = 0; a < KK; ++a) {
-        if (a + 1 < KK) ask(a + 1);
+      for (int i = 0; i < KK * kHalf; ++i) {
+        const int a = i / kHalf, it = 2 * (i % kHalf);
+        if (i + 1 < KK * kHalf) ask(i + 1);
         __builtin_amdgcn_sched_barrier(0);
         if (there(a)) {
+          if (it == 0) lin_split<T, NP>(__builtin_shufflevector(S[a][0], S[a][1], 0, 1, 2, 3, 4, 5, 6, 7), fs);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) acc[u] = io::mma(fk[a & 1][u], fq[a & 1], acc[u]);
+          for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) acc[it + x] = io::mma(fs[n], fq[i & 1][x], acc[it + x]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      const int i = 16 * it + l16;
-      const float chi = dec.hi[i], clo = dec.lo[i];
-      const int lim = dec.lim[i];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int j0 = 32 * ks + 16 * u + 4 * g;
-        f32x4 val;
+      for (int it = 0; it < IT; ++it) {
+        const float f = dec.f[16 * it + l16];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = j0 + r;
-          const float d = (chi - dec.hi[j]) + (clo - dec.lo[j]);
-          const bool seen = REV ? j >= i && j <= lim : j <= i && j >= lim;
-          val[r] = acc[u][r] * (__builtin_amdgcn_exp2f(seen ? (REV ? -d : d) : -1e30f) * p.pscale);
-        }
-#pragma unroll
-        for (int x = 0; x < NPP; ++x) {
-          io::store(sp + x * C * kWP + lin_at<T, kWP>(i, j0), val);
-          if (x + 1 < NPP)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) val[r] = lin_rest(val[r]);
-        }
+        for (int r = 0; r < 4; ++r) acc[it][r] *= f;
       }
-    }
-  };
-  // ---- out^T, columns of v down, tokens across: the part of the state
-  f32x4 acc[IT];
-  auto from_state = [&](const LinDecays<C>& dec) {
-#pragma unroll
-    for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-    constexpr int kHalf = IT / 2;
-    frag fq[2][2], fs[NP];
-    auto ask = [&](int i) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) fq[i & 1][x] = io::template row<KD>(sh.q, 16 * (2 * (i % kHalf) + x) + l16, 32 * (i / kHalf) + 8 * g);
     };
-    ask(0);
+    frag fv[KS];
+    auto values = [&] {
 #pragma unroll
-    for (int i = 0; i < KK * kHalf; ++i) {
-      const int a = i / kHalf, it = 2 * (i % kHalf);
-      if (i + 1 < KK * kHalf) ask(i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      if (there(a)) {
-        if (it == 0) lin_split<T, NP>(__builtin_shufflevector(S[a][0], S[a][1], 0, 1, 2, 3, 4, 5, 6, 7), fs);
+      for (int ks = 0; ks < KS; ++ks) fv[ks] = io::template column<kWV>(sv, 32 * ks + 8 * g, wcol, 4, l16);
+    };
+    // ... and that of the pairs; false if something of it is not finite
+    auto from_pairs = [&] {
+      float chk = 0.f;
+      auto seen = [](int it, int ks) { return REV ? 32 * ks + 31 >= 16 * it : 32 * ks <= 16 * it + 15; };
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
+      for (int x = 0; x < NPP; ++x) {
+        frag fp[IT][KS];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) acc[it + x] = io::mma(fs[n], fq[i & 1][x], acc[it + x]);
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            if (seen(it, ks)) fp[it][ks] = io::template row<kWP>(sp + x * C * kWP, 16 * it + l16, 32 * ks + 8 * g);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int it = 0; it < IT; ++it)
+            if (seen(it, ks)) acc[it] = io::mma(fv[ks], fp[it][ks], acc[it]);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const float f = dec.f[16 * it + l16];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[it][r] *= f;
-    }
-  };
-  frag fv[KS];
-  auto values = [&] {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) fv[ks] = io::template column<kWV>(sv, 32 * ks + 8 * g, wcol, 4, l16);
-  };
-  // ... and that of the pairs; false if something of it is not finite
-  auto from_pairs = [&] {
-    float chk = 0.f;
-    auto seen = [](int it, int ks) { return REV ? 32 * ks + 31 >= 16 * it : 32 * ks <= 16 * it + 15; };
-#pragma unroll
-    for (int x = 0; x < NPP; ++x) {
-      frag fp[IT][KS];
 #pragma unroll
       for (int it = 0; it < IT; ++it)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          if (seen(it, ks)) fp[it][ks] = io::template row<kWP>(sp + x * C * kWP, 16 * it + l16, 32 * ks + 8 * g);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int it = 0; it < IT; ++it)
-          if (seen(it, ks)) acc[it] = io::mma(fv[ks], fp[it][ks], acc[it]);
-    }
-#pragma unroll
-    for (int it = 0; it < IT; ++it)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) chk = fmaf(acc[it][r], 0.f, chk);
-    return __all(chk == 0.f);
-  };
-  // Four columns of a row of the chunk's tile of `out`; rows and columns that are not there are beyond it,
-  // and dropped.
-  const int ocols = p.vd - (col0 + wcol), osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
-  auto out_at = [&](int64_t t) { return static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + t * p.o_sl + col0 + wcol) * oes; };
-  auto x_at = [&](int64_t t) { return DOT ? LinTile<T, kWV, C, 64 * kWaves>::head(p.x, b, h, col0 + wcol) + t * p.x.sl : nullptr; };
-  char* out = out_at(start_of(0));
-  const T* xs = x_at(start_of(0));
-  // x's rows, asked for before they meet the result (16 bits a value: two a register)
-  constexpr int kXRegs = sizeof(T) == 2 ? 2 : 4;
-  uint32_t xv[DOT ? IT : 1][kXRegs];
-  auto load_x = [&](int n) {
-    constexpr int kOutside = 0x7ffffff0;
-    const int room = ocols - 4 * g, es = int(sizeof(T));
-    const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(xs), (short)0,
-                                                        ocols > 0 ? ((n - 1) * xsl + ocols) * es : 0, 0x00020000);
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int i = 16 * it + l16, at = i < n ? (i * xsl + 4 * g) * es : kOutside;
-      if (ocols >= 16) {
-        if constexpr (sizeof(T) == 2) {
-          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, 0);
-          xv[it][0] = v[0]; xv[it][1] = v[1];
-        } else {
-          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) xv[it][r] = v[r];
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < kXRegs; ++r) xv[it][r] = 0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int to = r < room ? at + r * es : kOutside;
-          if constexpr (sizeof(T) == 2)
-            xv[it][r / 2] |= uint32_t(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(from, to, 0, 0))) << (16 * (r % 2));
-          else
-            xv[it][r] = __builtin_amdgcn_raw_buffer_load_b32(from, to, 0, 0);
-        }
-      }
-    }
-  };
-  auto write = [&](int n) {
-    constexpr int kOutside = 0x7ffffff0;
-    const int room = ocols - 4 * g;               // columns that are there
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(out, (short)0,
-                                                        ocols > 0 ? ((n - 1) * osl + ocols) * oes : 0, 0x00020000);
-    const int at = (l16 * osl + 4 * g) * oes, step = 16 * osl * oes;
-    auto put = [&](f32x4 v, int to) {
-      if (sizeof(T) == 4 || p.out_f32) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, to, 0, 0);
-      } else {
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4)), rsrc, to, 0, 0);
-      }
+        for (int r = 0; r < 4; ++r) chk = fmaf(acc[it][r], 0.f, chk);
+      return __all(chk == 0.f);
     };
-    if (n == C && ocols >= 16) {
-#pragma unroll
-      for (int it = 0; it < IT; ++it) put(acc[it], at + it * step);
-    } else {
+    // Four columns of a row of the chunk's tile of `out`; rows and columns that are not there are beyond it,
+    // and dropped.
+    const int ocols = p.vd - (col0 + wcol), osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
+    auto out_at = [&](int64_t t) { return static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + t * p.o_sl + col0 + wcol) * oes; };
+    auto x_at = [&](int64_t t) { return DOT ? LinTile<T, kWV, C, 64 * kWaves>::head(p.x, b, h, col0 + wcol) + t * p.x.sl : nullptr; };
+    char* out = out_at(start_of(0));
+    const T* xs = x_at(start_of(0));
+    // x's rows, asked for before they meet the result (16 bits a value: two a register)
+    constexpr int kXRegs = sizeof(T) == 2 ? 2 : 4;
+    uint32_t xv[DOT ? IT : 1][kXRegs];
+    auto load_x = [&](int n) {
+      constexpr int kOutside = 0x7ffffff0;
+      const int room = ocols - 4 * g, es = int(sizeof(T));
+      const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(xs), (short)0,
+                                                          ocols > 0 ? ((n - 1) * xsl + ocols) * es : 0, 0x00020000);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        const int to = 16 * it + l16 < n ? at + it * step : kOutside;
-        put(acc[it], room >= 4 ? to : kOutside);
-        if (room > 0 && room < 4) {
+        const int i = 16 * it + l16, at = i < n ? (i * xsl + 4 * g) * es : kOutside;
+        if (ocols >= 16) {
+          if constexpr (sizeof(T) == 2) {
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(from, at, 0, 0);
+            xv[it][0] = v[0]; xv[it][1] = v[1];
+          } else {
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0);
 #pragma unroll
-          for (int r = 0; r < 3; ++r) {
-            const int one = r < room ? to + r * oes : kOutside;
-            if (sizeof(T) == 4 || p.out_f32)
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][r]), rsrc, one, 0, 0);
+            for (int r = 0; r < 4; ++r) xv[it][r] = v[r];
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < kXRegs; ++r) xv[it][r] = 0;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int to = r < room ? at + r * es : kOutside;
+            if constexpr (sizeof(T) == 2)
+              xv[it][r / 2] |= uint32_t(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(from, to, 0, 0))) << (16 * (r % 2));
             else
-              __builtin_amdgcn_raw_buffer_store_b16((short)bf16_rne(acc[it][r]), rsrc, one, 0, 0);
+              xv[it][r] = __builtin_amdgcn_raw_buffer_load_b32(from, to, 0, 0);
           }
         }
       }
-    }
-    if constexpr (DOT) {                          // out_i . x_i, for the decays' gradient
+    };
+    auto write = [&](int n) {
+      constexpr int kOutside = 0x7ffffff0;
+      const int room = ocols - 4 * g;               // columns that are there
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(out, (short)0,
+                                                          ocols > 0 ? ((n - 1) * osl + ocols) * oes : 0, 0x00020000);
+      const int at = (l16 * osl + 4 * g) * oes, step = 16 * osl * oes;
+      auto put = [&](f32x4 v, int to) {
+        if (sizeof(T) == 4 || p.out_f32) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, to, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4)), rsrc, to, 0, 0);
+        }
+      };
+      if (n == C && ocols >= 16) {
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
+        for (int it = 0; it < IT; ++it) put(acc[it], at + it * step);
+      } else {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          const int to = 16 * it + l16 < n ? at + it * step : kOutside;
+          put(acc[it], room >= 4 ? to : kOutside);
+          if (room > 0 && room < 4) {
+#pragma unroll
+            for (int r = 0; r < 3; ++r) {
+              const int one = r < room ? to + r * oes : kOutside;
+              if (sizeof(T) == 4 || p.out_f32)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][r]), rsrc, one, 0, 0);
+              else
+                __builtin_amdgcn_raw_buffer_store_b16((short)bf16_rne(acc[it][r]), rsrc, one, 0, 0);
+            }
+          }
+        }
+      }
+      if constexpr (DOT) {                          // out_i . x_i, for the decays' gradient
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          float sum = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = sizeof(T) == 4 ? __uint_as_float(xv[it][r % kXRegs])
+                                           : __uint_as_float(r % 2 ? xv[it][r / 2] & 0xffff0000u : xv[it][r / 2] << 16);
+            sum = fmaf(acc[it][r], x, sum);
+          }
+          sum += __shfl_xor(sum, 16);
+          sum += __shfl_xor(sum, 32);
+          if (g == 0) sh.dot[all_wave][16 * it + l16] = sum;
+        }
+      }
+    };
+    auto multiply = [&](float m) {
+      if (__builtin_amdgcn_readfirstlane(__float_as_int(m)) == __float_as_int(1.f)) return;
+#pragma unroll
+      for (int a = 0; a < KK; ++a)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[a][u][r] *= m;
+    };
+    // ---- the new state: w_j v_j in parts, so that nothing of what is added to fp32 is lost
+    auto update = [&](const LinDecays<C>& dec) {
+      multiply(dec.mul);
+      frag fk[2][2], fw[NX];
+      auto ask = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) fk[i & 1][u] = io::template column<KD>(sh.k, 32 * (i / KK) + 8 * g, 32 * (i % KK) + 4 * u, 8, l16);
+      };
+      ask(0);
+#pragma unroll
+      for (int i = 0; i < KS * KK; ++i) {
+        const int ks = i / KK, a = i % KK;
+        if (i + 1 < KS * KK) ask(i + 1);
+        if (a == 0) {
+          f32x8 x = io::wide(fv[ks]);
+          const f32x4* const w = reinterpret_cast<const f32x4*>(dec.w + 32 * ks + 8 * g);
+          x *= __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+          lin_split<T, NX>(x, fw);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (there(a)) {
+#pragma unroll
+          for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) S[a][u] = io::mma(fk[i & 1][u], fw[n], S[a][u]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
+    zero_state();
+    const int block = p.kd * p.vd;                  // of a head's state
+    if (!STATE) {
+      const float* const from = p.nseg > 1 ? p.seg + (bh * p.nseg + seg) * block : p.s0 ? p.s0 + bh * block : nullptr;
+      if (from) each_state([&](f32x4& s, int r, int at) { s[r] = from[at]; });
+    }
+
+    // Inside a chunk a token is kept from another by a zero factor, which an infinity or a NaN turns into a
+    // NaN.  If anything that comes out is not finite, what the wavefront has formed of the chunk is dropped,
+    // and the rest of the segment is walked token by token.
+    bool done = true;
+    int ci = 0;
+    int64_t t0 = start_of(0);
+    const T *now_q = tq.at, *now_k = tk.at, *now_v = tv.at;
+    load_gate(t0);
+    if (!STATE) tq.template load<REV>(tid, tokens_of(t0));
+    tk.template load<REV>(tid, tokens_of(t0));
+    tv.template load<REV>(64 * wave + lane, tokens_of(t0));
+    if (wave == kDecayWave) decays(sh.dec[part][0]);
+    if (chunks > 1) load_gate(t0 + kOn);
+    if (!STATE && tid == 0) sh.bad = 0;
+    for (;; ++ci, t0 += kOn) {
+      LinDecays<C>& dec = sh.dec[part][ci & 1];
+      const int n = tokens_of(t0);
+      lane = lin_lane();
+      tid = 64 * all_wave + lane;
+      const int vid = 64 * wave + lane;             // of the head's threads
+      l16 = lane & 15;
+      g = lane >> 4;
+      if (!STATE) tq.store(sh.q, tid, now_q, n);
+      tk.store(sh.k, tid, now_k, n);
+      tv.store(sv, vid, now_v, n);
+      __syncthreads();
+      const bool more = ci + 1 < chunks;
+      const int next = more ? tokens_of(t0 + kOn) : 0;
+      if (!STATE) now_q = tq.at;
+      now_k = tk.at;
+      now_v = tv.at;
+      if (wave == kDecayWave && more) decays(sh.dec[part][(ci + 1) & 1]);
+      if (!STATE) {
+        // (the next chunk's operands are asked for one by one, and not all of them at a time)
+        if (more) tq.template load<REV>(tid, next);
+        pairs(dec);
+        if (more) tk.template load<REV>(tid, next);
+        from_state(dec);
+        if (DOT) load_x(n);
+        __syncthreads();
+      }
+      if (STATE && more) tk.template load<REV>(tid, next);
+      if (more) tv.template load<REV>(vid, next);
+      if (ci + 2 < chunks) load_gate(t0 + 2 * kOn);
+      values();
+      if (!STATE) {
+        done = from_pairs();
+        if (done)
+          write(n);
+        else if (lane == 0)
+          sh.bad = 1;
+        out += kOn * osl * oes;
+        if (DOT) xs += kOn * xsl;
+      }
+      if (done) update(dec);
+      __syncthreads();
+      if (!STATE && sh.bad != 0) break;
+      if (DOT && vid < n) {
         float sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float x = sizeof(T) == 4 ? __uint_as_float(xv[it][r % kXRegs])
-                                         : __uint_as_float(r % 2 ? xv[it][r / 2] & 0xffff0000u : xv[it][r / 2] << 16);
-          sum = fmaf(acc[it][r], x, sum);
-        }
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
-        if (g == 0) sh.dot[all_wave][16 * it + l16] = sum;
+        for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][vid];
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p.dot + (nb * p.batch * p.H + bh) * p.L + t0, (short)0, n * 4, 0x00020000);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, vid * 4, 0, 0);
+      }
+      if (ci + 1 == chunks) break;
+    }
+    // the accumulators as the state itself
+    multiply(STATE || done ? sh.dec[part][ci & 1].after : sh.dec[part][ci & 1].before);
+    bool slow = !STATE && sh.bad != 0;
+    if (STATE) {
+      float chk = 0.f;
+#pragma unroll
+      for (int a = 0; a < KK; ++a)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) chk = fmaf(S[a][u][r], 0.f, chk);
+      slow = __syncthreads_or(chk != 0.f);
+      if (slow) {
+        zero_state();
+        ci = 0;
       }
     }
-  };
-  auto multiply = [&](float m) {
-    if (__builtin_amdgcn_readfirstlane(__float_as_int(m)) == __float_as_int(1.f)) return;
-#pragma unroll
-    for (int a = 0; a < KK; ++a)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) S[a][u][r] *= m;
-  };
-  // ---- the new state: w_j v_j in parts, so that nothing of what is added to fp32 is lost
-  auto update = [&](const LinDecays<C>& dec) {
-    multiply(dec.mul);
-    frag fk[2][2], fw[NX];
-    auto ask = [&](int i) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) fk[i & 1][u] = io::template column<KD>(sh.k, 32 * (i / KK) + 8 * g, 32 * (i % KK) + 4 * u, 8, l16);
-    };
-    ask(0);
-#pragma unroll
-    for (int i = 0; i < KS * KK; ++i) {
-      const int ks = i / KK, a = i % KK;
-      if (i + 1 < KS * KK) ask(i + 1);
-      if (a == 0) {
-        f32x8 x = io::wide(fv[ks]);
-        const f32x4* const w = reinterpret_cast<const f32x4*>(dec.w + 32 * ks + 8 * g);
-        x *= __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7);
-        lin_split<T, NX>(x, fw);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (there(a)) {
-#pragma unroll
-        for (int n = 0; n < NX; ++n)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) S[a][u] = io::mma(fk[i & 1][u], fw[n], S[a][u]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-
-  zero_state();
-  const int block = p.kd * p.vd;                  // of a head's state
-  if (!STATE) {
-    const float* const from = p.nseg > 1 ? p.seg + (bh * p.nseg + seg) * block : p.s0 ? p.s0 + bh * block : nullptr;
-    if (from) each_state([&](f32x4& s, int r, int at) { s[r] = from[at]; });
-  }
-
-  // Inside a chunk a token is kept from another by a zero factor, which an infinity or a NaN turns into a
-  // NaN.  If anything that comes out is not finite, what the wavefront has formed of the chunk is dropped,
-  // and the rest of the segment is walked token by token.
-  bool done = true;
-  int ci = 0;
-  int64_t t0 = start_of(0);
-  const T *now_q = tq.at, *now_k = tk.at, *now_v = tv.at;
-  load_gate(t0);
-  if (!STATE) tq.template load<REV>(tid, tokens_of(t0));
-  tk.template load<REV>(tid, tokens_of(t0));
-  tv.template load<REV>(64 * wave + lane, tokens_of(t0));
-  if (wave == kDecayWave) decays(sh.dec[part][0]);
-  if (chunks > 1) load_gate(t0 + kOn);
-  if (!STATE && tid == 0) sh.bad = 0;
-  for (;; ++ci, t0 += kOn) {
-    LinDecays<C>& dec = sh.dec[part][ci & 1];
-    const int n = tokens_of(t0);
-    lane = lin_lane();
-    tid = 64 * all_wave + lane;
-    const int vid = 64 * wave + lane;             // of the head's threads
-    l16 = lane & 15;
-    g = lane >> 4;
-    if (!STATE) tq.store(sh.q, tid, now_q, n);
-    tk.store(sh.k, tid, now_k, n);
-    tv.store(sv, vid, now_v, n);
-    __syncthreads();
-    const bool more = ci + 1 < chunks;
-    const int next = more ? tokens_of(t0 + kOn) : 0;
-    if (!STATE) now_q = tq.at;
-    now_k = tk.at;
-    now_v = tv.at;
-    if (wave == kDecayWave && more) decays(sh.dec[part][(ci + 1) & 1]);
-    if (!STATE) {
-      // (the next chunk's operands are asked for one by one, and not all of them at a time)
-      if (more) tq.template load<REV>(tid, next);
-      pairs(dec);
-      if (more) tk.template load<REV>(tid, next);
-      from_state(dec);
-      if (DOT) load_x(n);
-      __syncthreads();
-    }
-    if (STATE && more) tk.template load<REV>(tid, next);
-    if (more) tv.template load<REV>(vid, next);
-    if (ci + 2 < chunks) load_gate(t0 + 2 * kOn);
-    values();
-    if (!STATE) {
-      done = from_pairs();
-      if (done)
-        write(n);
-      else if (lane == 0)
-        sh.bad = 1;
-      out += kOn * osl * oes;
-      if (DOT) xs += kOn * xsl;
-    }
-    if (done) update(dec);
-    __syncthreads();
-    if (!STATE && sh.bad != 0) break;
-    if (DOT && vid < n) {
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][vid];
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(p.dot + (nb * p.batch * p.H + bh) * p.L + t0, (short)0, n * 4, 0x00020000);
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rsrc, vid * 4, 0, 0);
-    }
-    if (ci + 1 == chunks) break;
-  }
-  // the accumulators as the state itself
-  multiply(STATE || done ? sh.dec[part][ci & 1].after : sh.dec[part][ci & 1].before);
-  bool slow = !STATE && sh.bad != 0;
-  if (STATE) {
-    float chk = 0.f;
-#pragma unroll
-    for (int a = 0; a < KK; ++a)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) chk = fmaf(S[a][u][r], 0.f, chk);
-    slow = __syncthreads_or(chk != 0.f);
+    // ---- token by token, with choices in the place of zero factors; `done`: the first chunk stands
     if (slow) {
-      zero_state();
-      ci = 0;
-    }
-  }
-  // ---- token by token, with choices in the place of zero factors; `done`: the first chunk stands
-  if (slow) {
-    float* const row_q = reinterpret_cast<float*>(sh.k);           // [KD], and of k
-    float* const row_k = row_q + KD;
-    asm volatile("" : "+s"(ci));                  // (its addresses are not to be kept up to date by the loop above)
-    const T* const base_q = STATE ? nullptr : tq.head(p.q, b, h, 0);
-    const T *const base_k = tk.head(p.k, b, h, 0), *const base_v = tv.head(p.v, b, h, col0);
-    const float* const base_g = p.g + b * p.g_sb + h * p.g_sh;
+      float* const row_q = reinterpret_cast<float*>(sh.k);           // [KD], and of k
+      float* const row_k = row_q + KD;
+      asm volatile("" : "+s"(ci));                  // (its addresses are not to be kept up to date by the loop above)
+      const T* const base_q = STATE ? nullptr : tq.head(p.q, b, h, 0);
+      const T *const base_k = tk.head(p.k, b, h, 0), *const base_v = tv.head(p.v, b, h, col0);
+      const float* const base_g = p.g + b * p.g_sb + h * p.g_sh;
 #pragma unroll 1
-    for (; ci < chunks; ++ci) {
-      const int64_t t0 = start_of(ci);
-      const int n = tokens_of(t0);
-      const bool stands = !STATE && done;
+      for (; ci < chunks; ++ci) {
+        const int64_t t0 = start_of(ci);
+        const int n = tokens_of(t0);
+        const bool stands = !STATE && done;
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int64_t t = t0 + (REV ? n - 1 - i : i);
-        lane = lin_lane();
-        tid = 64 * all_wave + lane;
-        l16 = lane & 15;
-        g = lane >> 4;
-        __syncthreads();
-        for (int c = tid; c < KD; c += kThreads) {
-          row_q[c] = !STATE && c < p.kd ? io::widen(base_q[t * p.q.sl + c]) : 0.f;
-          row_k[c] = c < p.kd ? io::widen(base_k[t * p.k.sl + c]) : 0.f;
-        }
-        __syncthreads();
-        const int col = col0 + wcol + l16;
-        const float v = col < p.vd ? io::widen(base_v[t * p.v.sl + wcol + l16]) * p.wscale : 0.f;
-        const double c = double(base_g[t * p.g_sl]) * 1.4426950408889634;
-        const bool start = c < -150.0;
-        const float d = start ? 0.f : lin_decay(float(c));
-        float out = 0.f;
-        if (!stands) {
+        for (int i = 0; i < n; ++i) {
+          const int64_t t = t0 + (REV ? n - 1 - i : i);
+          lane = lin_lane();
+          tid = 64 * all_wave + lane;
+          l16 = lane & 15;
+          g = lane >> 4;
+          __syncthreads();
+          for (int c = tid; c < KD; c += kThreads) {
+            row_q[c] = !STATE && c < p.kd ? io::widen(base_q[t * p.q.sl + c]) : 0.f;
+            row_k[c] = c < p.kd ? io::widen(base_k[t * p.k.sl + c]) : 0.f;
+          }
+          __syncthreads();
+          const int col = col0 + wcol + l16;
+          const float v = col < p.vd ? io::widen(base_v[t * p.v.sl + wcol + l16]) * p.wscale : 0.f;
+          const double c = double(base_g[t * p.g_sl]) * 1.4426950408889634;
+          const bool start = c < -150.0;
+          const float d = start ? 0.f : lin_decay(float(c));
+          float out = 0.f;
+          if (!stands) {
 #pragma unroll
-          for (int a = 0; a < KK; ++a)
+            for (int a = 0; a < KK; ++a)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+              for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int kd = 32 * a + 8 * g + 4 * u + r;
-                float s = S[a][u][r];
-                if (!REV) s = start ? 0.f : s * d;
-                if (kd < p.kd) {
-                  s = fmaf(row_k[kd], v, s);
-                  out = fmaf(row_q[kd], s, out);
+                for (int r = 0; r < 4; ++r) {
+                  const int kd = 32 * a + 8 * g + 4 * u + r;
+                  float s = S[a][u][r];
+                  if (!REV) s = start ? 0.f : s * d;
+                  if (kd < p.kd) {
+                    s = fmaf(row_k[kd], v, s);
+                    out = fmaf(row_q[kd], s, out);
+                  }
+                  if (REV) s = start ? 0.f : s * d;
+                  S[a][u][r] = s;
                 }
-                if (REV) s = start ? 0.f : s * d;
-                S[a][u][r] = s;
+          }
+          if (!STATE) {
+            out += __shfl_xor(out, 16);
+            out += __shfl_xor(out, 32);
+            out *= p.fscale;
+            float dot = 0.f;
+            if (!stands && col < p.vd) {
+              if (g == 0) {
+                if (p.out_f32)
+                  reinterpret_cast<float*>(out_at(t))[l16] = out;
+                else
+                  io::narrow(reinterpret_cast<T*>(out_at(t)) + l16, out);
               }
-        }
-        if (!STATE) {
-          out += __shfl_xor(out, 16);
-          out += __shfl_xor(out, 32);
-          out *= p.fscale;
-          float dot = 0.f;
-          if (!stands && col < p.vd) {
-            if (g == 0) {
-              if (p.out_f32)
-                reinterpret_cast<float*>(out_at(t))[l16] = out;
-              else
-                io::narrow(reinterpret_cast<T*>(out_at(t)) + l16, out);
+              if (DOT) dot = out * io::widen(x_at(t)[l16]);
             }
-            if (DOT) dot = out * io::widen(x_at(t)[l16]);
-          }
-          if constexpr (DOT) {
-            // (what a wavefront whose first chunk stands has left there is that chunk's)
-            for (int x = 8; x > 0; x /= 2) dot += __shfl_xor(dot, x);
-            if (lane == 0 && !stands) sh.dot[all_wave][t - t0] = dot;
-            __syncthreads();
-            if (wave == 0 && lane == 0) {
-              float sum = 0.f;
-              for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][t - t0];
-              p.dot[(nb * p.batch * p.H + bh) * p.L + t] = sum;
+            if constexpr (DOT) {
+              // (what a wavefront whose first chunk stands has left there is that chunk's)
+              for (int x = 8; x > 0; x /= 2) dot += __shfl_xor(dot, x);
+              if (lane == 0 && !stands) sh.dot[all_wave][t - t0] = dot;
+              __syncthreads();
+              if (wave == 0 && lane == 0) {
+                float sum = 0.f;
+                for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][t - t0];
+                p.dot[(nb * p.batch * p.H + bh) * p.L + t] = sum;
+              }
             }
           }
         }
+        done = false;
       }
-      done = false;
     }
-  }
 
-  if (STATE) {
-    float* const to = p.seg + (bh * p.nseg + seg) * block;
-    each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
-    if (wave == kDecayWave && lane == 0 && nb == 0)
-      p.seg_decay[bh * p.nseg + seg] = anew ? -1.f : lin_decay(float(total));
-  } else if (p.s1 && seg == (REV ? 0 : p.nseg - 1)) {
-    float* const to = p.s1 + bh * block;
-    each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
-  }
-}
+    if (STATE) {
+      float* const to = p.seg + (bh * p.nseg + seg) * block;
+      each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
+      if (wave == kDecayWave && lane == 0 && nb == 0)
+        p.seg_decay[bh * p.nseg + seg] = anew ? -1.f : lin_decay(float(total));
+    } else if (p.s1 && seg == (REV ? 0 : p.nseg - 1)) {
+      float* const to = p.s1 + bh * block;
+      each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
+    }
+  };
 
-template <typename T, int KD, int NW, int HP, bool REV, bool STATE, bool DOT>
-hipError_t lin_launch(const LinParams& p, hipStream_t stream) {
-  const int64_t items = p.batch * (p.H / HP) * p.nblk * (STATE ? p.nseg - 1 : p.nseg);
-  if (items == 0) return hipSuccess;
-  lin_kernel<T, KD, NW, HP, REV, STATE, DOT><<<dim3(uint32_t(items)), dim3(64 * NW), 0, stream>>>(p);
-  return hipGetLastError();
+  // The heads of a token lie next to one another, so the rows of one head are a power of two apart as a
+  // rule, in one channel of the L2: an XCD takes the heads side by side.
+  const int item = xcd_contiguous_block(blockIdx.x, gridDim.x);
+  constexpr std::true_type backward;
+  constexpr std::false_type forward;
+  if constexpr (WALK == LinWalk::backward) {
+    segment(backward, walks.p[0], item);
+  } else if constexpr (WALK == LinWalk::forward || WALK == LinWalk::state) {
+    segment(forward, walks.p[0], item);
+  } else {
+    if (item & 1)
+      segment(backward, walks.p[1], item >> 1);
+    else
+      segment(forward, walks.p[0], item >> 1);
+  }
 }
 
 template <typename T, int KD, int NW, int HP>
-hipError_t lin_dispatch(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  if (state) return rev ? lin_launch<T, KD, NW, HP, true, true, false>(p, stream) : lin_launch<T, KD, NW, HP, false, true, false>(p, stream);
-  if constexpr (HP == 1)
-    if (p.dot) return rev ? lin_launch<T, KD, NW, HP, true, false, true>(p, stream) : lin_launch<T, KD, NW, HP, false, false, true>(p, stream);
-  return rev ? lin_launch<T, KD, NW, HP, true, false, false>(p, stream) : lin_launch<T, KD, NW, HP, false, false, false>(p, stream);
+hipError_t lin_launch(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  const bool state = walk == LinWalk::state || walk == LinWalk::states;
+  const int64_t items = p->batch * (p->H / HP) * p->nblk * (state ? p->nseg - 1 : p->nseg);
+  if (items == 0) return hipSuccess;
+  const dim3 one{uint32_t(items)}, both{uint32_t(2 * items)}, threads{64 * NW};
+  switch (walk) {
+    case LinWalk::forward: lin_kernel<T, KD, NW, HP, LinWalk::forward><<<one, threads, 0, stream>>>({{p[0]}}); break;
+    case LinWalk::backward: lin_kernel<T, KD, NW, HP, LinWalk::backward><<<one, threads, 0, stream>>>({{p[0]}}); break;
+    case LinWalk::state: lin_kernel<T, KD, NW, HP, LinWalk::state><<<one, threads, 0, stream>>>({{p[0]}}); break;
+    case LinWalk::states: lin_kernel<T, KD, NW, HP, LinWalk::states><<<both, threads, 0, stream>>>({{p[0], p[1]}}); break;
+    case LinWalk::grads:
+      // (do and v, the queries and keys of these walks, are each head's own)
+      if constexpr (HP == 1) lin_kernel<T, KD, NW, 1, LinWalk::grads><<<both, threads, 0, stream>>>({{p[0], p[1]}});
+      break;
+  }
+  return hipGetLastError();
 }
 
-template <typename T, int KD>
-hipError_t lin_choose(bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  if (p.vd > 64) return lin_dispatch<T, KD, 8, 1>(rev, state, p, stream);
-  return p.pairs ? lin_dispatch<T, KD, 8, 2>(rev, state, p, stream) : lin_dispatch<T, KD, 4, 1>(rev, state, p, stream);
+template <typename T, int KD> hipError_t lin_choose(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  if (p->vd > 64) return lin_launch<T, KD, 8, 1>(walk, p, stream);
+  return p->pairs ? lin_launch<T, KD, 8, 2>(walk, p, stream) : lin_launch<T, KD, 4, 1>(walk, p, stream);
 }
 
 }  // namespace

@@ -12,8 +12,9 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 // Segment states, from zero, into the states that enter the segments, in place: s := e^c s + own.  A thread has
 // one value of a head's state; eight segments' are asked for at once.
-template <bool REV>
-__global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams p, int blocks) {
+__global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams fwd, LinParams rev, int blocks) {
+  const bool REV = blockIdx.y != 0;
+  const LinParams& p = REV ? rev : fwd;
   const int block = p.kd * p.vd, at = int(blockIdx.x % blocks) * 256 + int(threadIdx.x);
   const int64_t bh = blockIdx.x / blocks;
   if (at >= block) return;
@@ -40,16 +41,10 @@ __global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams p, int blocks
   }
 }
 
-hipError_t lin_walk(bool bf16, bool rev, bool state, const LinParams& p, hipStream_t stream) {
-  switch (lin_kd(p.kd)) {
-    case 64: return bf16 ? launch_lin_bf16_64(rev, state, p, stream) : launch_lin_f32_64(rev, state, p, stream);
-    case 128: return bf16 ? launch_lin_bf16_128(rev, state, p, stream) : launch_lin_f32_128(rev, state, p, stream);
-    default: return bf16 ? launch_lin_bf16_256(rev, state, p, stream) : launch_lin_f32_256(rev, state, p, stream);
-  }
-}
-
 template <typename T>
-__global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* out, int64_t n, int share, int width) {
+__global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* out0, T* out1, int64_t n, int share, int width) {
+  T* const out = blockIdx.y ? out1 : out0;
+  part += blockIdx.y * n * share;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {   // [tokens * shared heads][width]
     const float* src = part + i / width * share * width + i % width;
     float s = 0.f;
@@ -206,32 +201,34 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
 
 }  // namespace
 
-hipError_t launch_lin_states(bool bf16, bool rev, const LinParams& p, hipStream_t stream) {
-  if (p.nseg == 1) return hipSuccess;
-  const hipError_t e = lin_walk(bf16, rev, true, p, stream);
+hipError_t launch_lin(bool bf16, LinWalk walk, const LinParams* p, hipStream_t stream) {
+  switch (lin_kd(p->kd)) {
+    case 64: return bf16 ? launch_lin_bf16_64(walk, p, stream) : launch_lin_f32_64(walk, p, stream);
+    case 128: return bf16 ? launch_lin_bf16_128(walk, p, stream) : launch_lin_f32_128(walk, p, stream);
+    default: return bf16 ? launch_lin_bf16_256(walk, p, stream) : launch_lin_f32_256(walk, p, stream);
+  }
+}
+
+hipError_t launch_lin_states(bool bf16, bool both, const LinParams* p, hipStream_t stream) {
+  if (p->nseg == 1) return hipSuccess;
+  const hipError_t e = launch_lin(bf16, both ? LinWalk::states : LinWalk::state, p, stream);
   if (e != hipSuccess) return e;
-  const int blocks = (p.kd * p.vd + 255) / 256;
-  const dim3 grid(uint32_t(p.batch * p.H * blocks));
-  if (rev)
-    lin_prefix_kernel<true><<<grid, dim3(256), 0, stream>>>(p, blocks);
-  else
-    lin_prefix_kernel<false><<<grid, dim3(256), 0, stream>>>(p, blocks);
+  const int blocks = (p->kd * p->vd + 255) / 256;
+  lin_prefix_kernel<<<dim3(uint32_t(p->batch * p->H * blocks), both ? 2 : 1), dim3(256), 0, stream>>>(p[0], p[both], blocks);
   return hipGetLastError();
 }
 
-hipError_t launch_lin(bool bf16, bool rev, const LinParams& p, hipStream_t stream) {
-  return lin_walk(bf16, rev, false, p, stream);
-}
-
-hipError_t launch_lin_heads(bool bf16, const float* part, void* out, int64_t tokens, int64_t H, int share, int width,
-                            hipStream_t stream) {
+hipError_t launch_lin_heads(bool bf16, const float* part, void* out0, void* out1, int64_t tokens, int64_t H, int share,
+                            int width, hipStream_t stream) {
   const int64_t n = tokens * (H / share) * width;
   const int64_t blocks = (n + 255) / 256;
-  const dim3 grid(uint32_t(blocks < (1 << 20) ? blocks : 1 << 20));
+  const dim3 grid(uint32_t(blocks < (1 << 20) ? blocks : 1 << 20), 2);
   if (bf16)
-    lin_heads_kernel<uint16_t><<<grid, dim3(256), 0, stream>>>(part, static_cast<uint16_t*>(out), n, share, width);
+    lin_heads_kernel<uint16_t><<<grid, dim3(256), 0, stream>>>(part, static_cast<uint16_t*>(out0),
+                                                               static_cast<uint16_t*>(out1), n, share, width);
   else
-    lin_heads_kernel<float><<<grid, dim3(256), 0, stream>>>(part, static_cast<float*>(out), n, share, width);
+    lin_heads_kernel<float><<<grid, dim3(256), 0, stream>>>(part, static_cast<float*>(out0), static_cast<float*>(out1), n,
+                                                            share, width);
   return hipGetLastError();
 }
 

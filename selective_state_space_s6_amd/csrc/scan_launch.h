@@ -319,22 +319,26 @@ struct LinParams {
 constexpr int lin_kd(int64_t kd) { return kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
 constexpr int lin_cols(int64_t vd) { return vd <= 64 ? 64 : 128; }
 constexpr int lin_chunk(bool bf16, int64_t kd) { return !bf16 && kd > 128 ? 32 : 64; }
+// What a launch walks: forward or backward; the segments' states only, forward, or in both directions (p[0] forward,
+// p[1] backward); a forward and a backward walk with their rows' products (both with `dot`, pairs == 0).
+enum class LinWalk { forward, backward, state, states, grads };
+// one launch, from s0 or (nseg > 1) from the states that enter the segments
+hipError_t launch_lin(bool bf16, LinWalk walk, const LinParams* p, hipStream_t stream);
 // nseg > 1: the states that enter the segments, from k, v and s0 (kd x vd, rows s_row apart, s_col == 1 or the
-// other way round)
-hipError_t launch_lin_states(bool bf16, bool rev, const LinParams& p, hipStream_t stream);
-// one walk, from s0 or (nseg > 1) from the states that enter the segments
-hipError_t launch_lin(bool bf16, bool rev, const LinParams& p, hipStream_t stream);
+// other way round); of both directions, or forward only
+hipError_t launch_lin_states(bool bf16, bool both, const LinParams* p, hipStream_t stream);
 // units of one element type and width of q and k
-hipError_t launch_lin_bf16_64(bool rev, bool state, const LinParams& p, hipStream_t stream);
-hipError_t launch_lin_bf16_128(bool rev, bool state, const LinParams& p, hipStream_t stream);
-hipError_t launch_lin_bf16_256(bool rev, bool state, const LinParams& p, hipStream_t stream);
-hipError_t launch_lin_f32_64(bool rev, bool state, const LinParams& p, hipStream_t stream);
-hipError_t launch_lin_f32_128(bool rev, bool state, const LinParams& p, hipStream_t stream);
-hipError_t launch_lin_f32_256(bool rev, bool state, const LinParams& p, hipStream_t stream);
+hipError_t launch_lin_bf16_64(LinWalk walk, const LinParams* p, hipStream_t stream);
+hipError_t launch_lin_bf16_128(LinWalk walk, const LinParams* p, hipStream_t stream);
+hipError_t launch_lin_bf16_256(LinWalk walk, const LinParams* p, hipStream_t stream);
+hipError_t launch_lin_f32_64(LinWalk walk, const LinParams* p, hipStream_t stream);
+hipError_t launch_lin_f32_128(LinWalk walk, const LinParams* p, hipStream_t stream);
+hipError_t launch_lin_f32_256(LinWalk walk, const LinParams* p, hipStream_t stream);
 
-// Sums over the heads that share one: part [tokens][H][width] fp32 -> out [tokens][H / share][width]
-hipError_t launch_lin_heads(bool bf16, const float* part, void* out, int64_t tokens, int64_t H, int share, int width,
-                            hipStream_t stream);
+// Sums over the heads that share one, for two gradients: part [2][tokens][H][width] fp32 ->
+// out0 and out1 [tokens][H / share][width]
+hipError_t launch_lin_heads(bool bf16, const float* part, void* out0, void* out1, int64_t tokens, int64_t H, int share,
+                            int width, hipStream_t stream);
 
 // The decays' gradient from the rows' products: dg_t = <last, dlast> + sum_{i >= t} (qdq_i - kdk_i)
 struct LinDecayParams {

@@ -1294,8 +1294,8 @@ static size_t ws_round(int64_t bytes) { return size_t(round_up(bytes, 256)); }
 struct LinPlan {
   int64_t seg_len = 0;          // tokens of a segment (the sequence's, or a multiple of 64)
   int32_t nseg = 1;
-  size_t seg_bytes = 0;         // states of one direction
   size_t fwd_bytes = 0, bwd_bytes = 0;
+  size_t off_rev = 0;           // the other direction's states and decays
   size_t off_decay = 0, off_qdq = 0, off_kdk = 0, off_last = 0, off_sums = 0, off_part = 0;
 };
 
@@ -1377,12 +1377,11 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       p.nseg = int32_t((chunks + len - 1) / len);
     }
     if (p.nseg > 1) {
-      p.seg_bytes = ws_round(f * bh * p.nseg * d.dk * d.dv);
-      p.fwd_bytes = p.seg_bytes + ws_round(f * bh * p.nseg);
+      p.off_decay = ws_round(f * bh * p.nseg * d.dk * d.dv);
+      p.fwd_bytes = p.off_decay + ws_round(f * bh * p.nseg);
     }
-    // the states of one direction, then of the other
-    p.off_decay = p.seg_bytes;
-    size_t off = p.fwd_bytes;
+    p.off_rev = p.fwd_bytes;
+    size_t off = 2 * p.fwd_bytes;
     if (want_dg) {
       p.off_qdq = off;
       off += ws_round(f * rows * lin_blocks(d.dk));
@@ -1394,7 +1393,7 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       off += ws_round(int64_t(sizeof(double)) * bh);
     }
     p.off_part = off;
-    if (d.nheads != d.qk_heads) off += ws_round(f * rows * d.dk);
+    if (d.nheads != d.qk_heads) off += ws_round(2 * f * rows * d.dk);
     p.bwd_bytes = off;
   }
   *out = p;
@@ -1508,8 +1507,8 @@ int linear_attention_fwd(const void* q, const void* k, const void* v, const floa
   p.s0 = initial_state; p.s1 = last_state;
   p.s_row = d.dv; p.s_col = 1;
   p.pscale = p.fscale = d.scale; p.wscale = 1.f;
-  e = selscan::launch_lin_states(bf16, false, p, s);
-  if (e == hipSuccess) e = selscan::launch_lin(bf16, false, p, s);
+  e = selscan::launch_lin_states(bf16, false, &p, s);
+  if (e == hipSuccess) e = selscan::launch_lin(bf16, selscan::LinWalk::forward, &p, s);
   st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   if (workspace == nullptr && pl.fwd_bytes > 0) {
     const hipError_t f = hipFreeAsync(ws, s);
@@ -1559,57 +1558,46 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
   float* part = reinterpret_cast<float*>(ws + pl.off_part);
   float* last = reinterpret_cast<float*>(ws + pl.off_last);
   const bool want_last = want_dg && dlast_state != nullptr;
-  // the states of the forward pass, as it forms them
-  selscan::LinParams p = lin_params(pl, tq, tk, tv, d.dk, d.dv, log_decay, d, ws);
-  p.s0 = initial_state;
-  p.s_row = d.dv; p.s_col = 1;
-  p.wscale = 1.f;
-  e = selscan::launch_lin_states(bf16, false, p, s);
-  // dq: do meets v, and the state S of the forward pass meets do (S read with its axes exchanged)
+  // the states S of the forward pass, and their gradient R from the last token on
+  char* const rev = ws + pl.off_rev;
+  selscan::LinParams walks[2] = {lin_params(pl, tq, tk, tv, d.dk, d.dv, log_decay, d, ws),
+                                  lin_params(pl, tk, tq, to, d.dk, d.dv, log_decay, d, rev)};
+  walks[0].s0 = initial_state; walks[1].s0 = dlast_state;
+  walks[0].s_row = walks[1].s_row = d.dv;
+  walks[0].s_col = walks[1].s_col = 1;
+  walks[0].wscale = 1.f; walks[1].wscale = d.scale;
+  e = selscan::launch_lin_states(bf16, true, walks, s);
+  // dq: do meets v, and S meets do; dk: v meets do, and R meets v (S and R read with their axes exchanged)
   if (e == hipSuccess) {
-    p = lin_params(pl, to, tv, tk, d.dv, d.dk, log_decay, d, ws);
-    lin_out(&p, shared ? part : dq, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
-    p.s0 = initial_state; p.s1 = want_last ? last : nullptr;
-    p.s_row = 1; p.s_col = d.dv;
-    p.pscale = p.fscale = d.scale; p.wscale = 1.f;
+    selscan::LinParams p[2] = {lin_params(pl, to, tv, tk, d.dv, d.dk, log_decay, d, ws),
+                               lin_params(pl, tv, to, tq, d.dv, d.dk, log_decay, d, rev)};
+    const int64_t rows = tokens * d.nheads * d.dk;
+    lin_out(&p[0], shared ? part : dq, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
+    lin_out(&p[1], shared ? part + rows : dk, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
+    p[0].s0 = initial_state; p[0].s1 = want_last ? last : nullptr;
+    p[1].s0 = dlast_state;
+    p[0].s_row = p[1].s_row = 1;
+    p[0].s_col = p[1].s_col = d.dv;
+    p[0].pscale = p[0].fscale = d.scale; p[0].wscale = 1.f;
+    p[1].pscale = p[1].wscale = d.scale; p[1].fscale = 1.f;
     if (want_dg) {
-      p.x = tq;
-      p.dot = reinterpret_cast<float*>(ws + pl.off_qdq);
+      p[0].x = tq; p[0].dot = reinterpret_cast<float*>(ws + pl.off_qdq);
+      p[1].x = tk; p[1].dot = reinterpret_cast<float*>(ws + pl.off_kdk);
+      e = selscan::launch_lin(bf16, selscan::LinWalk::grads, p, s);
+    } else {
+      e = selscan::launch_lin(bf16, selscan::LinWalk::forward, &p[0], s);
+      if (e == hipSuccess) e = selscan::launch_lin(bf16, selscan::LinWalk::backward, &p[1], s);
     }
-    e = selscan::launch_lin(bf16, false, p, s);
   }
   if (e == hipSuccess && shared)
-    e = selscan::launch_lin_heads(bf16, part, dq, tokens, d.nheads, int(d.nheads / d.qk_heads), int(d.dk), s);
-  // the gradient R of the states, from the last token on
-  if (e == hipSuccess) {
-    p = lin_params(pl, tk, tq, to, d.dk, d.dv, log_decay, d, ws);
-    p.s0 = dlast_state;
-    p.s_row = d.dv; p.s_col = 1;
-    p.wscale = d.scale;
-    e = selscan::launch_lin_states(bf16, true, p, s);
-  }
-  // dk: v meets do, and R meets v (R read with its axes exchanged)
-  if (e == hipSuccess) {
-    p = lin_params(pl, tv, to, tq, d.dv, d.dk, log_decay, d, ws);
-    lin_out(&p, shared ? part : dk, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
-    p.s0 = dlast_state;
-    p.s_row = 1; p.s_col = d.dv;
-    p.pscale = p.wscale = d.scale; p.fscale = 1.f;
-    if (want_dg) {
-      p.x = tk;
-      p.dot = reinterpret_cast<float*>(ws + pl.off_kdk);
-    }
-    e = selscan::launch_lin(bf16, true, p, s);
-  }
-  if (e == hipSuccess && shared)
-    e = selscan::launch_lin_heads(bf16, part, dk, tokens, d.nheads, int(d.nheads / d.qk_heads), int(d.dk), s);
+    e = selscan::launch_lin_heads(bf16, part, dq, dk, tokens, d.nheads, int(d.nheads / d.qk_heads), int(d.dk), s);
   if (e == hipSuccess && want_dg) {
     selscan::LinDecayParams c{};
     c.qdq = reinterpret_cast<float*>(ws + pl.off_qdq);
     c.kdk = reinterpret_cast<float*>(ws + pl.off_kdk);
     c.last = want_last ? last : nullptr;
     c.dlast = dlast_state;
-    c.g = log_decay; c.g_sb = p.g_sb; c.g_sl = p.g_sl; c.g_sh = p.g_sh;
+    c.g = log_decay; c.g_sb = walks[0].g_sb; c.g_sl = walks[0].g_sl; c.g_sh = walks[0].g_sh;
     c.dg = d.decay_tokens ? dlog_decay : nullptr;
     c.dg_heads = d.decay_tokens ? nullptr : dlog_decay;
     c.sums = reinterpret_cast<double*>(ws + pl.off_sums);
@@ -1620,12 +1608,11 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
   // dv: k meets q, and R meets k; R before the first token is the initial state's gradient (last: it
   // may take dlast_state's place)
   if (e == hipSuccess) {
-    p = lin_params(pl, tk, tq, to, d.dk, d.dv, log_decay, d, ws);
+    selscan::LinParams& p = walks[1];
     lin_out(&p, dv, false, d, d.seqlen * d.nheads * d.dv, d.nheads * d.dv, d.dv);
-    p.s0 = dlast_state; p.s1 = dinitial_state;
-    p.s_row = d.dv; p.s_col = 1;
-    p.pscale = p.wscale = d.scale; p.fscale = 1.f;
-    e = selscan::launch_lin(bf16, true, p, s);
+    p.s1 = dinitial_state;
+    p.pscale = d.scale; p.fscale = 1.f;
+    e = selscan::launch_lin(bf16, selscan::LinWalk::backward, &p, s);
   }
   st = e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   if (workspace == nullptr && pl.bwd_bytes > 0) {
