@@ -14,10 +14,16 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
-// VEC consecutive elements as they lie in memory: 16 bytes, or one element.
-template <typename T, int VEC> struct NormRaw {
+// VEC consecutive elements as they lie in memory: 16 bytes (EVEN: on a boundary of 16, else on any element's), or one
+// element.
+template <typename T, int VEC, bool EVEN> struct NormRaw {
   using type = u32x4;
-  static __device__ __forceinline__ type load(const T* p) { return *reinterpret_cast<const u32x4*>(p); }
+  static __device__ __forceinline__ type load(const T* p) {
+    if constexpr (EVEN) return *reinterpret_cast<const u32x4*>(p);
+    u32x4 r;
+    __builtin_memcpy(&r, p, 16);
+    return r;
+  }
   static __device__ __forceinline__ void widen(type r, float* v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -30,17 +36,17 @@ template <typename T, int VEC> struct NormRaw {
     }
   }
 };
-template <typename T> struct NormRaw<T, 1> {
+template <typename T, bool EVEN> struct NormRaw<T, 1, EVEN> {
   using type = T;
   static __device__ __forceinline__ type load(const T* p) { return *p; }
   static __device__ __forceinline__ void widen(type r, float* v) { v[0] = io_traits<T>::widen(r); }
 };
-template <int VEC> __device__ __forceinline__ void norm_load_f32(const float* p, float* v) {
+template <int VEC, bool EVEN> __device__ __forceinline__ void norm_load_f32(const float* p, float* v) {
   constexpr int N = VEC < 4 ? 1 : 4;
 #pragma unroll
-  for (int i = 0; i < VEC; i += N) NormRaw<float, N>::widen(NormRaw<float, N>::load(p + i), v + i);
+  for (int i = 0; i < VEC; i += N) NormRaw<float, N, EVEN>::widen(NormRaw<float, N, EVEN>::load(p + i), v + i);
 }
-template <typename T, int VEC> __device__ __forceinline__ void norm_store(T* p, const float* v) {
+template <typename T, int VEC, bool EVEN> __device__ __forceinline__ void norm_store(T* p, const float* v) {
   if constexpr (VEC == 1) {
     if constexpr (sizeof(T) == 2) *p = bf16_rne(v[0]); else *p = v[0];
   } else if constexpr (sizeof(T) == 2) {
@@ -49,26 +55,48 @@ template <typename T, int VEC> __device__ __forceinline__ void norm_store(T* p, 
     f x;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) x[i] = v[i];
-    *reinterpret_cast<b*>(p) = __builtin_convertvector(x, b);
+    const b r = __builtin_convertvector(x, b);
+    if constexpr (EVEN) *reinterpret_cast<b*>(p) = r; else __builtin_memcpy(p, &r, 16);
   } else {
     typedef __attribute__((ext_vector_type(4))) float f;
-    *reinterpret_cast<f*>(p) = f{v[0], v[1], v[2], v[3]};
+    const f r = {v[0], v[1], v[2], v[3]};
+    if constexpr (EVEN) *reinterpret_cast<f*>(p) = r; else __builtin_memcpy(p, &r, 16);
   }
 }
 
+// Where a thread's i-th piece of a group begins.  Of a width that is no multiple of VEC the last piece ends where the
+// group does: its first `had` values are the piece before's too, which counts them (both form and store the same bits).
+template <int VEC, bool EVEN> struct NormPlace {
+  int c, had;
+  bool in;
+  __device__ __forceinline__ NormPlace(int i, int lanes, int lane, int width) {
+    const int at = (i * lanes + lane) * VEC;
+    in = at < width;
+    c = EVEN || at + VEC <= width ? at : width - VEC;
+    had = at - c;
+  }
+  __device__ __forceinline__ bool counts(int e) const { return EVEN || e >= had; }
+};
+
 // What a thread has of a group of channels of one row, on its way: all that a row needs is asked for before
 // anything of it is waited for.
-template <typename T, int VEC, int EPT> struct NormPiece {
-  typename NormRaw<T, VEC>::type raw[EPT];
+template <typename T, int VEC, int EPT, bool EVEN> struct NormPiece {
+  using Raw = NormRaw<T, VEC, EVEN>;
+  typename Raw::type raw[EPT];
   __device__ __forceinline__ void load(const T* src, int lanes, int lane, int width) {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = (i * lanes + lane) * VEC;
-      raw[i] = typename NormRaw<T, VEC>::type{};
-      if (c < width) raw[i] = NormRaw<T, VEC>::load(src + c);
+      const NormPlace<VEC, EVEN> at(i, lanes, lane, width);
+      raw[i] = typename Raw::type{};
+      if (at.in) raw[i] = Raw::load(src + at.c);
     }
   }
-  __device__ __forceinline__ void widen(int i, float* v) const { NormRaw<T, VEC>::widen(raw[i], v); }
+  __device__ __forceinline__ void widen(int i, float* v) const { Raw::widen(raw[i], v); }
+  // everything has come
+  __device__ __forceinline__ void wait() {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) asm volatile("" : "+v"(raw[i]));
+  }
 };
 
 // The sum over the `lanes` threads of a group, in every one of them.
@@ -91,28 +119,29 @@ __device__ __forceinline__ float norm_act(float t, bool silu, float& slope) {
   return t * s;
 }
 
-template <typename T, int VEC, int EPT>
+template <typename T, int VEC, int EPT, bool EVEN>
 struct NormRow {
   float x[EPT * VEC];      // (x - mean) / sqrt(var + eps)
   float r;
-  __device__ __forceinline__ void form(const NormPiece<T, VEC, EPT>& raw, int lanes, int lane, int width, float eps, float* tmp) {
+  __device__ __forceinline__ void form(const NormPiece<T, VEC, EPT, EVEN>& raw, int lanes, int lane, int width, float eps, float* tmp) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
+      const NormPlace<VEC, EVEN> at(i, lanes, lane, width);
       raw.widen(i, x + i * VEC);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s += x[i * VEC + e];
+      for (int e = 0; e < VEC; ++e) s += at.counts(e) ? x[i * VEC + e] : 0.f;
     }
     const float inv = 1.f / float(width);
     const float mean = norm_sum(s, lanes, tmp) * inv;
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = (i * lanes + lane) * VEC;
+      const NormPlace<VEC, EVEN> at(i, lanes, lane, width);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        x[i * VEC + e] = c < width ? x[i * VEC + e] - mean : 0.f;
-        q = fmaf(x[i * VEC + e], x[i * VEC + e], q);
+        x[i * VEC + e] = at.in ? x[i * VEC + e] - mean : 0.f;
+        q = at.counts(e) ? fmaf(x[i * VEC + e], x[i * VEC + e], q) : q;
       }
     }
     r = 1.f / sqrtf(fmaf(norm_sum(q, lanes, tmp), inv, eps));
@@ -121,7 +150,7 @@ struct NormRow {
   }
 };
 
-template <typename T, int VEC, int EPT>
+template <typename T, int VEC, int EPT, bool EVEN>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
   __shared__ float tmp[4];
   const int lanes = p.lanes, lane = threadIdx.x % lanes;
@@ -130,19 +159,22 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
   const int64_t row = gi / p.groups, b = row / p.L, l = row % p.L;
   const int64_t c0 = gi % p.groups * p.width;
   const bool gate = p.z != nullptr;
-  NormPiece<T, VEC, EPT> x, z;
+  NormPiece<T, VEC, EPT, EVEN> x, z;
   x.load(static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0, lanes, lane, p.width);
   if (gate) z.load(static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0, lanes, lane, p.width);
   T* y = static_cast<T*>(p.y) + b * p.y_sb + l * p.y_sl + c0;
-  NormRow<T, VEC, EPT> n;
+  // (y may lie where z does, and another wavefront's piece may begin within this one's: z is there before the barriers)
+  if (!EVEN && gate && lanes > 64) z.wait();
+  NormRow<T, VEC, EPT, EVEN> n;
   n.form(x, lanes, lane, p.width, p.eps, tmp);
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
-    const int c = (i * lanes + lane) * VEC;
-    if (c >= p.width) break;
+    const NormPlace<VEC, EVEN> at(i, lanes, lane, p.width);
+    const int c = at.c;
+    if (!at.in) break;
     float w[VEC], o[VEC], t[VEC];
-    if (p.weight) norm_load_f32<VEC>(p.weight + c0 + c, w);
-    if (p.bias) norm_load_f32<VEC>(p.bias + c0 + c, o);
+    if (p.weight) norm_load_f32<VEC, EVEN>(p.weight + c0 + c, w);
+    if (p.bias) norm_load_f32<VEC, EVEN>(p.bias + c0 + c, o);
     if (gate) z.widen(i, t);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -150,14 +182,14 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
       float slope;
       o[e] = gate ? v * norm_act(t[e], p.silu, slope) : norm_act(v, p.silu, slope);
     }
-    norm_store<T, VEC>(y + c, o);
+    norm_store<T, VEC, EVEN>(y + c, o);
   }
 }
 
 // A workgroup keeps to `256 / lanes` groups of channels (of several rows at once where there are fewer groups)
 // and walks every `splits`-th row, so that the sums for weight and bias stay in registers.  The next row is
 // asked for before this one is looked at.
-template <typename T, int VEC, int EPT>
+template <typename T, int VEC, int EPT, bool EVEN>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   __shared__ float tmp[4];
   const int lanes = p.lanes, lane = threadIdx.x % lanes, slot = threadIdx.x / lanes;
@@ -171,16 +203,16 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   float w[EPT * VEC], o[EPT * VEC], dw[EPT * VEC], db[EPT * VEC];
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
-    const int c = (i * lanes + lane) * VEC;
+    const NormPlace<VEC, EVEN> at(i, lanes, lane, p.width);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) { w[i * VEC + e] = 1.f; o[i * VEC + e] = dw[i * VEC + e] = db[i * VEC + e] = 0.f; }
-    if (c < p.width) {
-      if (p.weight) norm_load_f32<VEC>(p.weight + c0 + c, w + i * VEC);
-      if (p.bias) norm_load_f32<VEC>(p.bias + c0 + c, o + i * VEC);
+    if (at.in) {
+      if (p.weight) norm_load_f32<VEC, EVEN>(p.weight + c0 + at.c, w + i * VEC);
+      if (p.bias) norm_load_f32<VEC, EVEN>(p.bias + c0 + at.c, o + i * VEC);
     }
   }
   const float inv = 1.f / float(p.width);
-  NormPiece<T, VEC, EPT> x, z, dy;
+  NormPiece<T, VEC, EPT, EVEN> x, z, dy;
   auto ask = [&](int64_t row) {
     const int64_t b = row / p.L, l = row % p.L;
     x.load(static_cast<const T*>(p.x) + b * p.x_sb + l * p.x_sl + c0, lanes, lane, p.width);
@@ -189,15 +221,15 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   };
   if (part < p.rows) ask(part);
   for (int64_t row = part; row < p.rows; row += step) {
-    const NormPiece<T, VEC, EPT> now_x = x, now_z = z, now_dy = dy;
+    const NormPiece<T, VEC, EPT, EVEN> now_x = x, now_z = z, now_dy = dy;
     if (EPT * VEC <= 16 && row + step < p.rows) ask(row + step);   // (wider groups leave no registers for it)
     const int64_t out = row * p.groups * p.width + c0;
-    NormRow<T, VEC, EPT> n;
+    NormRow<T, VEC, EPT, EVEN> n;
     n.form(now_x, lanes, lane, p.width, p.eps, tmp);
     float u[EPT * VEC], m1 = 0.f, m2 = 0.f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = (i * lanes + lane) * VEC;
+      const NormPlace<VEC, EVEN> at(i, lanes, lane, p.width);
       float d[VEC], t[VEC], dz[VEC];
       now_dy.widen(i, d);                         // (zero behind the group's end: nothing comes of it there)
       if (gate) now_z.widen(i, t);
@@ -213,13 +245,13 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
           norm_act(v, p.silu, slope);
           dn = d[e] * slope;
         }
+        u[k] = dn * w[k];
         dw[k] = fmaf(dn, n.x[k], dw[k]);
         db[k] += dn;
-        u[k] = dn * w[k];
-        m1 += u[k];
-        m2 = fmaf(u[k], n.x[k], m2);
+        m1 += at.counts(e) ? u[k] : 0.f;
+        m2 = at.counts(e) ? fmaf(u[k], n.x[k], m2) : m2;
       }
-      if (gate && c < p.width) norm_store<T, VEC>(static_cast<T*>(p.dz) + out + c, dz);
+      if (gate && at.in) norm_store<T, VEC, EVEN>(static_cast<T*>(p.dz) + out + at.c, dz);
     }
     m1 = norm_sum(m1, lanes, tmp) * inv;
     m2 = norm_sum(m2, lanes, tmp) * inv;
@@ -227,14 +259,14 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
     const float two = p.width == 2 ? n.r * n.r * p.eps : 0.f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = (i * lanes + lane) * VEC;
+      const NormPlace<VEC, EVEN> at(i, lanes, lane, p.width);
       float d[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float a = u[i * VEC + e] - m1;
         d[e] = n.r * (p.width == 2 ? a * two : fmaf(-n.x[i * VEC + e], m2, a));
       }
-      if (c < p.width) norm_store<T, VEC>(static_cast<T*>(p.dx) + out + c, d);
+      if (at.in) norm_store<T, VEC, EVEN>(static_cast<T*>(p.dx) + out + at.c, d);
     }
     if (EPT * VEC > 16 && row + step < p.rows) ask(row + step);
   }
@@ -249,15 +281,17 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   }
   const int span = lanes * p.gper < 64 ? 64 : lanes * p.gper;      // threads of one part
   if (int(threadIdx.x) % span >= lanes * p.gper) return;
-  const int64_t C = p.groups * p.width, at = split * (256 / span) + threadIdx.x / span;
+  const int64_t C = p.groups * p.width;
+  float* const own = p.part + 2 * C * (split * (256 / span) + threadIdx.x / span);
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
-    const int c = (i * lanes + lane) * VEC;
-    if (c >= p.width) break;
+    const NormPlace<VEC, EVEN> at(i, lanes, lane, p.width);
+    if (!at.in) break;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      p.part[2 * at * C + c0 + c + e] = dw[i * VEC + e];
-      p.part[(2 * at + 1) * C + c0 + c + e] = db[i * VEC + e];
+      if (!at.counts(e)) continue;
+      own[c0 + at.c + e] = dw[i * VEC + e];
+      own[C + c0 + at.c + e] = db[i * VEC + e];
     }
   }
 }
@@ -295,36 +329,39 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64
   }
 }
 
-template <typename T, int VEC, int EPT>
+template <typename T, int VEC, int EPT, bool EVEN>
 hipError_t norm_launch(bool bwd, const NormParams& p, hipStream_t stream) {
   if (bwd) {
-    norm_bwd_kernel<T, VEC, EPT><<<dim3(uint32_t(p.cblocks * p.splits)), dim3(256), 0, stream>>>(p);
+    norm_bwd_kernel<T, VEC, EPT, EVEN><<<dim3(uint32_t(p.cblocks * p.splits)), dim3(256), 0, stream>>>(p);
   } else {
     const int64_t per = 256 / p.lanes;
-    norm_fwd_kernel<T, VEC, EPT><<<dim3(uint32_t((p.rows * p.groups + per - 1) / per)), dim3(256), 0, stream>>>(p);
+    norm_fwd_kernel<T, VEC, EPT, EVEN><<<dim3(uint32_t((p.rows * p.groups + per - 1) / per)), dim3(256), 0, stream>>>(p);
   }
   return hipGetLastError();
 }
 
+template <typename T, bool EVEN>
+hipError_t norm_pieces(bool bwd, const NormParams& p, hipStream_t stream) {
+  constexpr int VEC = 16 / sizeof(T);
+  switch (p.ept) {
+    case 1: return norm_launch<T, VEC, 1, EVEN>(bwd, p, stream);
+    case 2: return norm_launch<T, VEC, 2, EVEN>(bwd, p, stream);
+  }
+  if (VEC == 8 || p.ept <= 4) return norm_launch<T, VEC, 4, EVEN>(bwd, p, stream);
+  return norm_launch<T, VEC, VEC == 8 ? 4 : 8, EVEN>(bwd, p, stream);
+}
+
 template <typename T>
 hipError_t norm_dispatch(bool bwd, const NormParams& p, hipStream_t stream) {
-  constexpr int VEC = 16 / sizeof(T);
-  if (!p.vec)
-    return p.ept <= 1 ? norm_launch<T, 1, 1>(bwd, p, stream) : p.ept <= 4 ? norm_launch<T, 1, 4>(bwd, p, stream)
-         : p.ept <= 8 ? norm_launch<T, 1, 8>(bwd, p, stream) : norm_launch<T, 1, 32>(bwd, p, stream);
-  switch (p.ept) {
-    case 1: return norm_launch<T, VEC, 1>(bwd, p, stream);
-    case 2: return norm_launch<T, VEC, 2>(bwd, p, stream);
-  }
-  if (VEC == 8 || p.ept <= 4) return norm_launch<T, VEC, 4>(bwd, p, stream);
-  return norm_launch<T, VEC, VEC == 8 ? 4 : 8>(bwd, p, stream);
+  if (p.width < 16 / int(sizeof(T))) return norm_launch<T, 1, 1, false>(bwd, p, stream);
+  return p.even ? norm_pieces<T, true>(bwd, p, stream) : norm_pieces<T, false>(bwd, p, stream);
 }
 
 }  // namespace
 
-NormPlan norm_plan(bool bf16, bool vec, int64_t rows, int64_t groups, int64_t width) {
+NormPlan norm_plan(bool bf16, int64_t rows, int64_t groups, int64_t width) {
   NormPlan pl{};
-  const int64_t per = vec ? (bf16 ? 8 : 4) : 1, pieces = (width + per - 1) / per;
+  const int64_t vec = bf16 ? 8 : 4, per = width < vec ? 1 : vec, pieces = (width + per - 1) / per;
   pl.lanes = 1;
   while (pl.lanes < 64 && pl.lanes < pieces) pl.lanes *= 2;
   if (width > 64 * kNormElems) pl.lanes = 256;

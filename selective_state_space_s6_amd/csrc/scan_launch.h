@@ -381,7 +381,7 @@ struct NormPlan {
   int64_t gper, cblocks, splits, parts;  // backward: groups side by side in a workgroup, blocks of them, workgroups
                         // that share the rows, partial sums of dweight and dbias
 };
-NormPlan norm_plan(bool bf16, bool vec, int64_t rows, int64_t groups, int64_t width);
+NormPlan norm_plan(bool bf16, int64_t rows, int64_t groups, int64_t width);
 struct NormParams {
   const void* x;
   const float* weight;  // [C], may be null
@@ -395,7 +395,8 @@ struct NormParams {
   float* dbias;
   float* part;          // workspace [parts][2][C], or null (neither is wanted)
   int64_t rows, L, groups;
-  int32_t width, silu, vec;
+  int32_t width, silu;
+  int32_t even;         // every group of channels begins and ends on 16 bytes
   int64_t x_sb, x_sl, z_sb, z_sl, y_sb, y_sl;
   float eps;
   int32_t lanes, ept;

@@ -1671,14 +1671,14 @@ static int norm_check(const selscan_norm_dims* dims) {
   const int64_t rows = d.batch * d.seqlen;
   if (rows > 0) {
     if (d.groups > kMost / rows) return SELSCAN_ERR_UNSUPPORTED;
-    const selscan::NormPlan pl = selscan::norm_plan(false, false, rows, d.groups, width);
-    if (rows * d.groups > ((int64_t(1) << 32) - 256) / pl.lanes) return SELSCAN_ERR_UNSUPPORTED;
+    const int64_t lanes = selscan::norm_plan(false, rows, d.groups, width).lanes;
+    if (rows * d.groups > ((int64_t(1) << 32) - 256) / lanes) return SELSCAN_ERR_UNSUPPORTED;
   }
   return SELSCAN_OK;
 }
 
-static size_t norm_bwd_bytes(const selscan_norm_dims& d, bool vec) {
-  const selscan::NormPlan pl = selscan::norm_plan(d.io_dtype == SELSCAN_BF16, vec, d.batch * d.seqlen, d.groups, d.dim / d.groups);
+static size_t norm_bwd_bytes(const selscan_norm_dims& d) {
+  const selscan::NormPlan pl = selscan::norm_plan(d.io_dtype == SELSCAN_BF16, d.batch * d.seqlen, d.groups, d.dim / d.groups);
   return ws_round(int64_t(sizeof(float)) * pl.parts * 2 * d.dim);
 }
 
@@ -1694,9 +1694,9 @@ static selscan::NormParams norm_params(const void* x, const float* weight, const
   auto sl = [&](int64_t s) { return d.seqlen > 1 ? s : 0; };
   p.x_sb = sb(d.x_sb); p.x_sl = sl(d.x_sl); p.z_sb = sb(d.z_sb); p.z_sl = sl(d.z_sl); p.y_sb = sb(d.y_sb); p.y_sl = sl(d.y_sl);
   p.eps = d.eps;
-  p.vec = p.width % v == 0 && all_aligned({x, weight, bias, z}, 16) && all_aligned(others, 16) && p.x_sb % v == 0 &&
+  p.even = p.width % v == 0 && all_aligned({x, weight, bias, z}, 16) && all_aligned(others, 16) && p.x_sb % v == 0 &&
           p.x_sl % v == 0 && p.y_sb % v == 0 && p.y_sl % v == 0 && (!z || (p.z_sb % v == 0 && p.z_sl % v == 0));
-  const selscan::NormPlan pl = selscan::norm_plan(bf16, p.vec, p.rows, p.groups, p.width);
+  const selscan::NormPlan pl = selscan::norm_plan(bf16, p.rows, p.groups, p.width);
   p.lanes = pl.lanes; p.ept = pl.ept;
   p.gper = pl.gper; p.cblocks = pl.cblocks; p.splits = pl.splits; p.parts = pl.parts;
   return p;
@@ -1733,8 +1733,7 @@ int group_norm_fwd(const void* x, const float* weight, const float* bias, const 
 
 size_t group_norm_bwd_workspace_size(const selscan_norm_dims* dims) {
   if (norm_check(dims) != SELSCAN_OK || dims->batch * dims->seqlen == 0) return 0;
-  const size_t a = norm_bwd_bytes(*dims, false), b = norm_bwd_bytes(*dims, true);   // the pointers decide which
-  return a > b ? a : b;
+  return norm_bwd_bytes(*dims);
 }
 
 int group_norm_bwd(const void* x, const float* weight, const float* bias, const void* z, const void* dy, void* dx,
