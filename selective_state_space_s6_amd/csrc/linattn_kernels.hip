@@ -41,18 +41,23 @@ __global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams fwd, LinParam
   }
 }
 
+// 2^log_lanes threads for a row of `width` columns.
 template <typename T>
-__global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* out0, T* out1, int64_t n, int share, int width) {
+__global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* out0, T* out1, int64_t rows, int share, int width,
+                                                        int log_lanes) {
   T* const out = blockIdx.y ? out1 : out0;
-  part += blockIdx.y * n * share;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {   // [tokens * shared heads][width]
-    const float* src = part + i / width * share * width + i % width;
+  part += blockIdx.y * rows * share * width;
+  const int c = threadIdx.x & ((1 << log_lanes) - 1), per = 256 >> log_lanes;
+  if (c >= width) return;
+  for (int64_t row = int64_t(blockIdx.x) * per + (threadIdx.x >> log_lanes); row < rows; row += int64_t(gridDim.x) * per) {
+    const float* const src = part + row * share * width + c;
     float s = 0.f;
+#pragma unroll 8
     for (int k = 0; k < share; ++k) s += src[int64_t(k) * width];
     if constexpr (sizeof(T) == 2)
-      out[i] = bf16_rne(s);
+      out[row * width + c] = bf16_rne(s);
     else
-      out[i] = s;
+      out[row * width + c] = s;
   }
 }
 
@@ -220,15 +225,16 @@ hipError_t launch_lin_states(bool bf16, bool both, const LinParams* p, hipStream
 
 hipError_t launch_lin_heads(bool bf16, const float* part, void* out0, void* out1, int64_t tokens, int64_t H, int share,
                             int width, hipStream_t stream) {
-  const int64_t n = tokens * (H / share) * width;
-  const int64_t blocks = (n + 255) / 256;
+  int log_lanes = 0;
+  while (1 << log_lanes < width) ++log_lanes;
+  const int64_t rows = tokens * (H / share), per = 256 >> log_lanes, blocks = (rows + per - 1) / per;
   const dim3 grid(uint32_t(blocks < (1 << 20) ? blocks : 1 << 20), 2);
   if (bf16)
     lin_heads_kernel<uint16_t><<<grid, dim3(256), 0, stream>>>(part, static_cast<uint16_t*>(out0),
-                                                               static_cast<uint16_t*>(out1), n, share, width);
+                                                               static_cast<uint16_t*>(out1), rows, share, width, log_lanes);
   else
-    lin_heads_kernel<float><<<grid, dim3(256), 0, stream>>>(part, static_cast<float*>(out0), static_cast<float*>(out1), n,
-                                                            share, width);
+    lin_heads_kernel<float><<<grid, dim3(256), 0, stream>>>(part, static_cast<float*>(out0), static_cast<float*>(out1), rows,
+                                                            share, width, log_lanes);
   return hipGetLastError();
 }
 

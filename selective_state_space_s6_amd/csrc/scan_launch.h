@@ -376,7 +376,7 @@ hipError_t launch_lin_step(bool bf16, const LinStepParams& p, hipStream_t stream
 // Group norm with an activation (norm_kernels.hip).
 constexpr int kNormElems = 32;          // of a group in one thread, at most
 struct NormPlan {
-  int32_t lanes;        // threads of a group: a power of two up to 64, or 256
+  int32_t log_lanes;    // threads of a group: a power of two up to 64, or 256
   int32_t ept;          // accesses of a thread
   int64_t gper, cblocks, splits, parts;  // backward: groups side by side in a workgroup, blocks of them, workgroups
                         // that share the rows, partial sums of dweight and dbias
@@ -399,7 +399,7 @@ struct NormParams {
   int32_t even;         // every group of channels begins and ends on 16 bytes
   int64_t x_sb, x_sl, z_sb, z_sl, y_sb, y_sl;
   float eps;
-  int32_t lanes, ept;
+  int32_t log_lanes, ept;
   int64_t gper, cblocks, splits, parts;
 };
 hipError_t launch_norm(bool bf16, bool bwd, const NormParams& p, hipStream_t stream);

@@ -1671,8 +1671,8 @@ static int norm_check(const selscan_norm_dims* dims) {
   const int64_t rows = d.batch * d.seqlen;
   if (rows > 0) {
     if (d.groups > kMost / rows) return SELSCAN_ERR_UNSUPPORTED;
-    const int64_t lanes = selscan::norm_plan(false, rows, d.groups, width).lanes;
-    if (rows * d.groups > ((int64_t(1) << 32) - 256) / lanes) return SELSCAN_ERR_UNSUPPORTED;
+    const int log_lanes = selscan::norm_plan(false, rows, d.groups, width).log_lanes;
+    if (rows * d.groups > ((int64_t(1) << 32) - 256) >> log_lanes) return SELSCAN_ERR_UNSUPPORTED;
   }
   return SELSCAN_OK;
 }
@@ -1697,7 +1697,7 @@ static selscan::NormParams norm_params(const void* x, const float* weight, const
   p.even = p.width % v == 0 && all_aligned({x, weight, bias, z}, 16) && all_aligned(others, 16) && p.x_sb % v == 0 &&
           p.x_sl % v == 0 && p.y_sb % v == 0 && p.y_sl % v == 0 && (!z || (p.z_sb % v == 0 && p.z_sl % v == 0));
   const selscan::NormPlan pl = selscan::norm_plan(bf16, p.rows, p.groups, p.width);
-  p.lanes = pl.lanes; p.ept = pl.ept;
+  p.log_lanes = pl.log_lanes; p.ept = pl.ept;
   p.gper = pl.gper; p.cblocks = pl.cblocks; p.splits = pl.splits; p.parts = pl.parts;
   return p;
 }
