@@ -61,9 +61,9 @@ __global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* ou
   }
 }
 
-// One workgroup per (batch row, head), 4096 tokens at a time from the last, four a thread.  The sums run in
+// One workgroup per (batch row, head), its threads' four tokens each at a time, from the last.  The sums run in
 // 64 bits: what a token's decay passes is the small difference of what follows it and what precedes it.
-constexpr int kDecayThreads = 1024;
+template <int kDecayThreads>
 __global__ __launch_bounds__(kDecayThreads) void lin_decay_kernel(LinDecayParams p) {
   __shared__ double tmp[kDecayThreads / 64];
   const int64_t bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
@@ -141,7 +141,9 @@ __global__ __launch_bounds__(256) void lin_decay_heads_kernel(const double* sums
 }
 
 // One workgroup per (batch row, head): S := a S + k v^T, o = scale q^T S, on a state of [K][V].  A row
-// of the state is taken by `lanes` lanes of 4 columns; the 256 / lanes rows of a pass are summed through LDS.
+// of the state is taken by `lanes` lanes of 4 columns, 16 bytes on any boundary of 4; the 256 / lanes rows of a pass are
+// summed through LDS.  Of a V that is no multiple of 4 the last lane's columns end where the row does: some are the lane
+// before's too, and both form and store the same bits (one instruction reads a row, a later one writes it).
 template <typename T>
 __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lanes) {
   __shared__ float sq[256], sk[256];
@@ -150,7 +152,9 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
   const int64_t src = p.read_slots ? int64_t(p.read_slots[b]) : b, dst = p.write_slots ? int64_t(p.write_slots[b]) : b;
   if (dst < 0 || dst >= p.slots) return;          // padding
   const bool from = src >= 0 && src < p.slots;
-  const int tid = threadIdx.x, col = (tid % lanes) * 4, row0 = tid / lanes, rows = 256 / lanes;
+  const int tid = threadIdx.x, first = (tid % lanes) * 4, row0 = tid / lanes, rows = 256 / lanes;
+  const bool wide = p.vd >= 4, in = first < p.vd;
+  const int col = wide && first + 4 > p.vd ? p.vd - 4 : first;
   const int64_t hk = h / p.share;
   auto at = [](const void* t, int64_t i) { return io_traits<T>::widen(static_cast<const T*>(t)[i]); };
   if (tid < p.kd) {
@@ -159,7 +163,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
   }
   f32x4 v = {0.f, 0.f, 0.f, 0.f}, o = v;
   for (int e = 0; e < 4; ++e)
-    if (col + e < p.vd) v[e] = at(p.v, b * p.v_sb + h * p.v_sh + col + e);
+    if (in && col + e < p.vd) v[e] = at(p.v, b * p.v_sb + h * p.v_sh + col + e);
   const float lg = p.g[b * p.g_sb + h * p.g_sh];
   const bool keep = from && !(double(lg) * 1.4426950408889634 < -150.0);
   const float a = expf(lg);
@@ -169,9 +173,9 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
   __syncthreads();
   for (int r = row0; r < p.kd; r += rows) {
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if (keep && col < p.vd) {
-      if (p.vec)
-        s = *reinterpret_cast<const f32x4*>(s_in + int64_t(r) * p.vd);
+    if (keep && in) {
+      if (wide)
+        __builtin_memcpy(&s, s_in + int64_t(r) * p.vd, 16);
       else
         for (int e = 0; e < 4; ++e)
           if (col + e < p.vd) s[e] = s_in[int64_t(r) * p.vd + e];
@@ -181,9 +185,9 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
       s[e] = keep ? fmaf(a, s[e], k * v[e]) : k * v[e];
       o[e] = fmaf(q, s[e], o[e]);
     }
-    if (col < p.vd) {
-      if (p.vec)
-        *reinterpret_cast<f32x4*>(s_out + int64_t(r) * p.vd) = s;
+    if (in) {
+      if (wide)
+        __builtin_memcpy(s_out + int64_t(r) * p.vd, &s, 16);
       else
         for (int e = 0; e < 4; ++e)
           if (col + e < p.vd) s_out[int64_t(r) * p.vd + e] = s[e];
@@ -191,7 +195,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
   }
   part[tid] = o;
   __syncthreads();
-  if (tid < lanes) {
+  if (tid < lanes && in) {
     for (int r = 1; r < rows; ++r) o += part[r * lanes + tid];
     T* dsto = static_cast<T*>(p.o) + b * p.o_sb + h * p.o_sh + col;
     for (int e = 0; e < 4; ++e)
@@ -239,7 +243,13 @@ hipError_t launch_lin_heads(bool bf16, const float* part, void* out0, void* out1
 }
 
 hipError_t launch_lin_decay(const LinDecayParams& p, hipStream_t stream) {
-  lin_decay_kernel<<<dim3(uint32_t(p.batch * p.H)), dim3(kDecayThreads), 0, stream>>>(p);
+  // As many threads as one step of the tokens takes (4096 heads of 64 tokens: 1024 threads 74 us, 256 17; 1024 heads
+  // of 1024 tokens 31 and 20; of more tokens, fewer threads have more steps, each of which waits for its sums).
+  const dim3 grid(uint32_t(p.batch * p.H));
+  if (p.L <= 1024)
+    lin_decay_kernel<256><<<grid, dim3(256), 0, stream>>>(p);
+  else
+    lin_decay_kernel<1024><<<grid, dim3(1024), 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.dg_heads) {
     lin_decay_heads_kernel<<<dim3(uint32_t((p.H + 255) / 256)), dim3(256), 0, stream>>>(p.sums, p.dg_heads, p.batch, p.H);

@@ -291,14 +291,13 @@ struct LinTensor {
   const void* p;
   int64_t sb, sl, sh;
   int32_t share;        // heads that share one row
-  int32_t vec;          // 1: 16-byte accesses (base and strides on 16 bytes)
 };
 // One walk over the chunks (the header of linattn_kernels.h): the operands in the roles that they have in it.
 struct LinParams {
   LinTensor q, k, v;
   void* out;            // [batch][tokens][H][vd] in the I/O type, or fp32 (out_f32)
   int64_t o_sb, o_sl, o_sh;
-  int32_t out_f32, out_vec;
+  int32_t out_f32;
   const float* g;       // logarithms of the decays
   int64_t g_sb, g_sl, g_sh;
   const float* s0;      // state that the walk begins with, (batch, head) blocks of kd * vd; may be null (zero)
@@ -367,7 +366,7 @@ struct LinStepParams {
   const int32_t* read_slots;  // may be null (0, 1, 2, ...)
   const int32_t* write_slots;
   int64_t slots, batch, H;
-  int32_t share, kd, vd, vec; // vec: the state's rows are on 16 bytes
+  int32_t share, kd, vd;
   int64_t q_sb, q_sh, k_sb, k_sh, v_sb, v_sh, o_sb, o_sh, g_sb, g_sh;
   float scale;
 };

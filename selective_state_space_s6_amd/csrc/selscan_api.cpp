@@ -1402,14 +1402,12 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
 
 static selscan::LinTensor lin_tensor(const void* ptr, const selscan_linattn_dims& d, int64_t heads, int64_t sb, int64_t sl,
                                      int64_t sh) {
-  const int64_t v = d.io_dtype == SELSCAN_BF16 ? 8 : 4;
   selscan::LinTensor t{};
   t.p = ptr;
   t.sb = d.batch > 1 ? sb : 0;
   t.sl = d.seqlen > 1 ? sl : 0;
   t.sh = heads > 1 ? sh : 0;
   t.share = int32_t(d.nheads / heads);
-  t.vec = aligned(ptr, 16) && t.sb % v == 0 && t.sl % v == 0 && t.sh % v == 0;
   return t;
 }
 
@@ -1436,11 +1434,9 @@ static selscan::LinParams lin_params(const LinPlan& pl, const selscan::LinTensor
 
 static void lin_out(selscan::LinParams* p, void* out, bool f32, const selscan_linattn_dims& d, int64_t sb, int64_t sl,
                     int64_t sh) {
-  const int64_t v = f32 || d.io_dtype == SELSCAN_F32 ? 4 : 8;
   p->out = out;
   p->out_f32 = f32;
   p->o_sb = d.batch > 1 ? sb : 0; p->o_sl = d.seqlen > 1 ? sl : 0; p->o_sh = d.nheads > 1 ? sh : 0;
-  p->out_vec = aligned(out, 16) && p->o_sb % v == 0 && p->o_sl % v == 0 && p->o_sh % v == 0;
 }
 
 void linear_attention_dims_init(selscan_linattn_dims* dims, int io_dtype, int64_t batch, int64_t seqlen, int64_t nheads,
@@ -1643,7 +1639,6 @@ int linear_attention_step(const void* q, const void* k, const void* v, const flo
   p.state = state; p.read_slots = read_slots; p.write_slots = write_slots; p.slots = slots;
   p.batch = d.batch; p.H = d.nheads; p.share = int32_t(d.nheads / d.qk_heads);
   p.kd = int32_t(d.dk); p.vd = int32_t(d.dv);
-  p.vec = aligned(state, 16) && d.dv % 4 == 0;
   p.q_sb = d.q_sb; p.q_sh = d.q_sh; p.k_sb = d.k_sb; p.k_sh = d.k_sh; p.v_sb = d.v_sb; p.v_sh = d.v_sh;
   p.o_sb = d.o_sb; p.o_sh = d.o_sh;
   p.g_sb = d.decay_tokens ? d.g_sb : 0; p.g_sh = d.g_sh;
