@@ -18,6 +18,19 @@ Options: ``discretization="euler"`` (Bbar = delta * B instead of the ZOH coeffic
 softplus(delta + delta_bias) (the bias alone is added without softplus).
 The innermost axis of every tensor must be unit-stride; other strides are passed through
 (zero strides, i.e. expanded views, are allowed).
+
+Linear attention with a decay for each head, and the output stage of such a layer:
+
+    o, last = linear_attention_fwd(q, k, v, log_decay, scale=K ** -0.5, return_last_state=True)
+    y = group_norm_fwd(o.flatten(2), weight, bias, z, groups=H)
+    d = group_norm_bwd(o.flatten(2), weight, bias, z, dy=dy, groups=H)
+    d = linear_attention_bwd(q, k, v, log_decay, do=d["dx"].view_as(o), scale=K ** -0.5)
+    o = linear_attention_step(q1, k1, v1, log_decay1, state=last)
+
+    q, k           [batch, L, Hk, K]    (H heads share Hk of them, in runs of H / Hk; K, V at most 256)
+    v, o           [batch, L, H, V]     the I/O type of q and k
+    log_decay      [H] or [batch, L, H] float32; -inf starts the state anew
+    state          [batch, H, K, V]     float32
 """
 from __future__ import annotations
 

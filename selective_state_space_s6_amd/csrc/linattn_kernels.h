@@ -9,6 +9,17 @@
 //     R'  = e^c R + sum_i e^{c_i} k_i v_i^T
 // The gradients are these two walks on other operands: dq = forward(do, v, k),
 // dk = backward(v, do, q), dv = backward(k, q, do).
+//
+// A chunk has 64 tokens: the pairs cost as many products as the state does at 64 channels, and the tiles of two
+// workgroups of eight wavefronts fit the LDS of a compute unit (256 fp32 channels: chunks of 32, one workgroup).  The
+// state never leaves the accumulators: their layout is, with the channels counted as 8 (l / 16) + 4 u + r, that
+// of the operand which meets the queries, so only its rounding into parts lies between.  Long sequences of few heads
+// are cut into segments; a pass over k and v forms each one's own state, a prefix what enters it.
+// What bounds it (1 x 32 heads x 16384, 128 x 128 bf16, 239 us; 105 us of bytes): the state pass takes 80 us, of which 52
+// are its bytes, the prefix 13, the walk 150.  In the walk the matrix units are busy 28 % of the time, the vector
+// units 53 %, and a wavefront waits 43 % of it: the products of one chunk hang on one another, three barriers part them, and
+// registers (128) and LDS hold four wavefronts a SIMD.  Four wavefronts of 32 columns, which read half as much from
+// the LDS, are slower (walk 169 us), as are two tiles of k and v in turns in the state pass (no gain).
 #pragma once
 
 #include <type_traits>
@@ -801,6 +812,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
   // The heads of a token lie next to one another, so the rows of one head are a power of two apart as a
   // rule, in one channel of the L2: an XCD takes the heads side by side.
   const int item = xcd_contiguous_block(blockIdx.x, gridDim.x);
+  // (Two walks at once fill the compute units where one does not: 2 x 6 heads x 333 fp32, forward and backward, 118 us
+  // one after the other, 86 so; where each fills them the time is the same.)
   constexpr std::true_type backward;
   constexpr std::false_type forward;
   if constexpr (WALK == LinWalk::backward) {
@@ -835,6 +848,9 @@ hipError_t lin_launch(LinWalk walk, const LinParams* p, hipStream_t stream) {
 }
 
 template <typename T, int KD> hipError_t lin_choose(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  // Eight wavefronts for 128 columns; of at most 64 columns a workgroup has four, or takes two heads that share their
+  // queries and keys, which it then stages once (4 x 80 heads on one q and k x 8192, 128 x 64 bf16: 660 us with
+  // a head each, 560 so).
   if (p->vd > 64) return lin_launch<T, KD, 8, 1>(walk, p, stream);
   return p->pairs ? lin_launch<T, KD, 8, 2>(walk, p, stream) : lin_launch<T, KD, 4, 1>(walk, p, stream);
 }
