@@ -573,7 +573,7 @@ typedef struct selscan_linattn_dims {
   int64_t k_sb, k_sl, k_sh;   /* axis is unit-stride.  Token strides at most 2^22, not used where */
   int64_t v_sb, v_sl, v_sh;   /* seqlen is 1 */
   int64_t o_sb, o_sl, o_sh;   /* o of the forward, do of the backward */
-  int64_t g_sb, g_sl, g_sh;   /* log_decay (decay_tokens 0: g_sh only) */
+  int64_t g_sb, g_sl, g_sh;   /* log_decay (decay_tokens 0: g_sh only), g_sl as the other token strides */
   int32_t decay_tokens;    /* 1: log_decay per token and head; 0: [nheads], the same for every token */
   float scale;             /* of o; finite */
 } selscan_linattn_dims;
@@ -619,8 +619,9 @@ size_t linear_attention_workspace_size(const selscan_linattn_dims* dims);
  *                    or NULL.  Zero where the state starts anew.
  *   dinitial_state : [batch][nheads][dk][dv] fp32, or NULL; it and dlast_state may be one buffer
  *   workspace      : linear_attention_bwd_workspace_size(dims, dlog_decay != NULL) bytes, as above
- * All outputs are written, never accumulated into; sums run in a fixed order.  nheads * dk and
- * nheads * dv must be at most 2^22 where seqlen is above 1.
+ * All outputs are written, never accumulated into; sums run in a fixed order.  Where dlog_decay is
+ * wanted, pairs and states keep 24 bits of mantissa in dq and dk, whose products with q and k it sums.
+ * nheads * dk and nheads * dv must be at most 2^22 where seqlen is above 1.
  */
 int linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay,
                          const float* initial_state, const void* d_o, const float* dlast_state, void* dq, void* dk,

@@ -62,10 +62,12 @@ __global__ __launch_bounds__(256) void lin_heads_kernel(const float* part, T* ou
 }
 
 // One workgroup per (batch row, head), its threads' four tokens each at a time, from the last.  The sums run in
-// 64 bits: what a token's decay passes is the small difference of what follows it and what precedes it.
+// 64 bits: what a token's decay passes is the small difference of what follows it and what precedes it.  A token that
+// starts anew ends the sums of those before it: what follows it adds up to zero, but for its rounding.
 template <int kDecayThreads>
 __global__ __launch_bounds__(kDecayThreads) void lin_decay_kernel(LinDecayParams p) {
   __shared__ double tmp[kDecayThreads / 64];
+  __shared__ int ends[kDecayThreads / 64];
   const int64_t bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   auto block_sum = [&](double v) {
@@ -103,23 +105,36 @@ __global__ __launch_bounds__(kDecayThreads) void lin_decay_kernel(LinDecayParams
       }
     }
 #pragma unroll
-    for (int e = 2; e >= 0; --e) v[e] += v[e + 1];
-    double all = v[0];
+    for (int e = 2; e >= 0; --e) v[e] += start[e + 1] ? 0.0 : v[e + 1];
+    // what this thread and those with later tokens add to an earlier token, and whether one of them starts anew
+    double all = start[0] ? 0.0 : v[0];
+    int end = start[0] || start[1] || start[2] || start[3];
     for (int d = 1; d < 64; d *= 2) {
       const double o = __shfl_up(all, d);
-      if (lane >= d) all += o;
+      const int oe = __shfl_up(end, d);
+      if (lane >= d) {
+        if (!end) all += o;
+        end |= oe;
+      }
     }
     __syncthreads();
-    if (lane == 63) tmp[wave] = all;
+    if (lane == 63) {
+      tmp[wave] = all;
+      ends[wave] = end;
+    }
     __syncthreads();
-    double later = carry + (all - v[0]);          // of the threads with later tokens
+    double later = carry;                         // of the wavefronts with later tokens
     for (int w = 0; w < kDecayThreads / 64; ++w) {
-      if (w < wave) later += tmp[w];
-      carry += tmp[w];
+      carry = ends[w] ? tmp[w] : carry + tmp[w];
+      if (w + 1 == wave) later = carry;
     }
+    const double o = __shfl_up(all, 1);
+    const int oe = __shfl_up(end, 1);
+    if (lane > 0) later = oe ? o : later + o;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 3; e >= 0; --e) {
       const double g = start[e] ? 0.0 : v[e] + later;
+      if (start[e]) later = 0.0;
       if (t + e < p.L) {
         if (p.dg) p.dg[(b * p.L + t + e) * p.H + h] = float(g);
         sum += g;
