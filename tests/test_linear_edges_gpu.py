@@ -47,6 +47,66 @@ def same(a, b):
         t.equal(a[k], b[k]) for k in a)
 
 
+# ---------------------------------------------------------------------- pairs of heads, segments, widths apart
+
+#          batch, L, H, Hk, K, V: two heads a workgroup and segments; K and V of different kernels; one token less than a
+#          chunk, one more than a segment
+WIDE_APART = [(1, 1100, 4, 1, 64, 64), (2, 705, 4, 2, 128, 32), (1, 640, 6, 3, 200, 64), (1, 900, 2, 2, 256, 16),
+              (1, 900, 2, 2, 16, 256), (1, 449, 2, 1, 1, 64), (1, 385, 2, 2, 64, 1), (3, 127, 8, 2, 7, 3), (1, 2049, 2, 2, 8, 8)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", WIDE_APART)
+def test_pairs_and_segments(size, io):
+    i = inputs(size, io, seed=21, decay="packed")
+    v = tensors(i, io)
+    o, last = fwd(v, i)
+    lin.check_forward(i, size, io, o, last)
+    lin.check_backward(i, size, io, bwd(v, i))
+    d = bwd(v, i, decay_grad=False)
+    assert "dlog_decay" not in d
+    full = bwd(v, i)
+    assert _torch().equal(d["dv"], full["dv"])
+    lin.check_backward(i, size, io, dict(d, dlog_decay=full["dlog_decay"]))
+
+
+@pytest.mark.parametrize("size", [(1, 90, 2, 1, 24, 40), (1, 330, 2, 2, 16, 16)])
+def test_gradients_against_differences(size):
+    """The loss <do, o> + <dlast, last> is linear in each of q, k, v and the initial state, so its difference over any step
+    is the gradient's product with it, up to rounding alone: n 2^-24 of the magnitudes on either side (test_linear_gpu.py).
+    In the decays a central difference is off by its own remainder too, which the 64-bit statement gives."""
+    B, L, H, Hk, K, V = size
+    i = inputs(size, "f32", seed=31, decay="token")
+    rng = np.random.default_rng(5)
+    d = bwd(tensors(i, "f32"), i)
+    n = (K + V + L / 16 + 100) * 2.0 ** -24 * 2
+    loss = lambda o, last: (host(o) * i["do"]).sum() + (host(last) * i["dlast"]).sum()       # noqa: E731
+    oracle_run = lambda j: orc.linear_fwd(*(j[a] for a in "qkvg"), j["scale"], j["S0"])      # noqa: E731
+    exact = lambda j: (lambda o, s: (o * i["do"]).sum() + (s * i["dlast"]).sum())(*oracle_run(j))    # noqa: E731
+    size_of = lambda j: (lambda o, s: (o * np.abs(i["do"])).sum() + (s * np.abs(i["dlast"])).sum())(*oracle_run(lin.absolute(j)))    # noqa: E731
+    base = loss(*fwd(tensors(i, "f32"), i))
+    for name, key in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("S0", "dinitial_state")):
+        step = host(d[key])
+        step /= np.sqrt((step ** 2).mean())                    # along the gradient, of size one
+        j = dict(i, **{name: (i[name] + step).astype(np.float32)})
+        step = j[name].astype(np.float64) - i[name]
+        diff, grad = loss(*fwd(tensors(j, "f32"), j)) - base, (host(d[key]) * step).sum()
+        bound = n * (size_of(i) + size_of(j) + size_of(dict(i, **{name: np.abs(step)})))
+        assert abs(diff - grad) <= bound, (name, diff, grad, bound)
+        assert abs(grad) > 10 * bound, name                    # the bound says something
+    step = 2e-2 * rng.uniform(-1, 1, i["g"].shape)
+    up, dn = (dict(i, g=(i["g"] + s * step).astype(np.float32)) for s in (1, -1))
+    step = (up["g"].astype(np.float64) - dn["g"]) / 2
+    diff = (loss(*fwd(tensors(up, "f32"), up)) - loss(*fwd(tensors(dn, "f32"), dn))) / 2
+    grad = (host(d["dlog_decay"]) * step).sum()
+    ref = (orc.linear_bwd(i["q"], i["k"], i["v"], i["g"], i["do"], i["scale"], i["S0"], i["dlast"])["dlog_decay"] * step).sum()
+    mid = dict(i, g=((up["g"].astype(np.float64) + dn["g"]) / 2).astype(np.float32))
+    rest = abs((exact(up) - exact(dn)) / 2 - ref) + n * size_of(mid)
+    # the decays' gradient is off by n 2^-24 of the magnitudes that pass each of L tokens
+    bound = rest + n * (size_of(up) + size_of(dn)) + n * np.abs(step).max() * L * size_of(i)
+    assert abs(diff - grad) <= bound, (diff, grad, bound)
+
+
 # ---------------------------------------------------------------------- values that are not finite
 
 def near_where_finite(got, ref, bound, what):
@@ -299,6 +359,54 @@ def test_a_state_that_is_continued_in_place():
         assert st == 0
         t.cuda.synchronize()
         assert t.equal(both, d["dinitial_state"]) and all(t.equal(out[k], d[k]) for k in out)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [2048, 2049, 4099, 8191, 8192])
+def test_wide_groups_in_place(width, io):
+    """Four wavefronts a group, whose last piece may begin within the one before's: y in the place of x, or of z."""
+    t, ss = _torch(), _ss()
+    size = (2, 3, 2, width)
+    i = nrm.inputs(size, io, True, "both", seed=6)
+    v = {k: dev(a, io if k in ("x", "z", "dy") else "f32") for k, a in i.items()}
+    args = (v["weight"], v["bias"])
+    want = ss.group_norm_fwd(v["x"], *args, v["z"], groups=2)
+    nrm.check(i, size, io, True, y=want)
+    nrm.check(i, size, io, True, d=ss.group_norm_bwd(v["x"], *args, v["z"], dy=v["dy"], groups=2))
+    for n in range(3):
+        x, z = v["x"].clone(), v["z"].clone()
+        assert t.equal(ss.group_norm_fwd(x, *args, v["z"], groups=2, y=x), want)
+        assert t.equal(ss.group_norm_fwd(v["x"], *args, z, groups=2, y=z), want) and t.equal(z, want)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_padded_rows(io):
+    """Keys of zero and a log decay of zero behind a sequence's end leave its state as it was."""
+    ends = [37, 64, 150, 1]
+    size = (4, 150, 2, 1, 32, 48)
+    i = inputs(size, io, seed=13, decay="token")
+    for b, n in enumerate(ends):
+        i["k"][b, n:] = 0.0
+        i["g"][b, n:] = 0.0
+    _, last = fwd(tensors(i, io), i)
+    for b, n in enumerate(ends):
+        j = {k: a[b:b + 1, :n] if k in ("q", "k", "v", "do", "g") else a[b:b + 1] if k in ("S0", "dlast") else a for k, a in i.items()}
+        _, rl = orc.linear_fwd(*(j[a] for a in "qkvg"), i["scale"], j["S0"])
+        _, ml = orc.linear_fwd(*(lin.absolute(j)[a] for a in "qkvg"), i["scale"], np.abs(j["S0"]))
+        lin.near(last[b:b + 1], rl, lin.units(size, io)[0] * ml, "row %d" % b)
+
+
+def test_slots_read_twice():
+    t, ss = _torch(), _ss()
+    H, K, V = 2, 24, 37
+    state = t.randn(6, H, K, V, device="cuda")
+    before = state.clone()
+    q, k, v = (t.randn(4, H, w, device="cuda") for w in (K, K, V))
+    ids = lambda *a: t.tensor(a, dtype=t.int32, device="cuda")                          # noqa: E731
+    o = t.full((4, H, V), 7.0, device="cuda")
+    ss.linear_attention_step(q, k, v, -t.rand(H, device="cuda"), state=state, o=o, read_slots=ids(1, 1, 1, 1), write_slots=ids(0, 3, 5, -1))
+    assert t.equal(state[[1, 2, 4]], before[[1, 2, 4]]) and (o[3] == 7.0).all() and not (o[:3] == 7.0).any()
+    assert not t.equal(state[0], state[5])
 
 
 # ---------------------------------------------------------------------- offsets beyond 32 bits
