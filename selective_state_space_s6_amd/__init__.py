@@ -984,16 +984,23 @@ def _linattn_dims(on, q, k, v, log_decay, o, scale, step=False):
     if Hk == 0 or H % Hk:
         raise ValueError("the heads of v (%d) must be a multiple of those of q and k (%d)" % (H, Hk))
     batch, L = (lead[0], 1) if step else lead
-    strides = []
-    for name, t, shape in (("q", q, lead + (Hk, K)), ("k", k, lead + (Hk, K)), ("v", v, lead + (H, V)), ("o", o, lead + (H, V))):
-        on.check(name, t, io, shape, contiguous=False)
-        s = t.stride()
-        if s[-1] != 1 and shape[-1] > 1:
-            raise ValueError("%s: the last axis must be unit-stride" % name)
-        strides += (s[0], 0, s[1]) if step else (s[0], s[1] if L > 1 else 0, s[2])      # (one token: any stride)
-    tokens = log_decay.dim() > 1
+    qk, vo, at = q.shape, lead + (H, V), on.index
+    sq, sk, sv, so, g = q.stride(), k.stride(), v.stride(), o.stride(), log_decay.stride()
+    if not (k.dtype is io and v.dtype is io and o.dtype is io and k.shape == qk and v.shape == vo and o.shape == vo
+            and k.get_device() == at and v.get_device() == at and o.get_device() == at):
+        for name, t, shape in (("k", k, qk), ("v", v, vo), ("o", o, vo)):
+            on.check(name, t, io, shape, contiguous=False)
+    if (K > 1 and not sq[-1] == sk[-1] == 1) or (V > 1 and not sv[-1] == so[-1] == 1):
+        raise ValueError("q, k, v and o: the last axis must be unit-stride")
+    tokens = len(g) > 1
     on.check("log_decay", log_decay, torch.float32, lead + (H,) if tokens else (H,), contiguous=False)
-    g = log_decay.stride()
+    # (one token: any stride between tokens)
+    if step:
+        strides = (sq[0], 0, sq[1], sk[0], 0, sk[1], sv[0], 0, sv[1], so[0], 0, so[1])
+    elif L > 1:
+        strides = sq[:3] + sk[:3] + sv[:3] + so[:3]
+    else:
+        strides = (sq[0], 0, sq[2], sk[0], 0, sk[2], sv[0], 0, sv[2], so[0], 0, so[2])
     g = (0, 0, g[0]) if not tokens else (g[0], 0, g[1]) if step else g
     return LinattnDims(SELSCAN_ABI_VERSION, _io_code(io), batch, L, H, Hk, K, V, *strides, *g, 1 if tokens else 0, scale)
 
@@ -1013,11 +1020,11 @@ def linear_attention_fwd(q, k, v, log_decay, *, scale: float = 1.0, o=None, init
         raise ValueError("q and v must be [batch, L, heads, width]")
     with _On(q, stream) as on:
         if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+            o = q.new_empty(v.shape)
         dims = _linattn_dims(on, q, k, v, log_decay, o, scale)
         states = (dims.batch, dims.nheads, dims.dk, dims.dv)
         if last_state is None and return_last_state:
-            last_state = torch.empty(states, dtype=torch.float32, device=q.device)
+            last_state = q.new_empty(states, dtype=torch.float32)
         on.check("initial_state", initial_state, torch.float32, states)
         on.check("last_state", last_state, torch.float32, states)
         ref = ctypes.byref(dims)
@@ -1043,7 +1050,7 @@ def linear_attention_bwd(q, k, v, log_decay, *, do, scale: float = 1.0, initial_
         states = (dims.batch, dims.nheads, dims.dk, dims.dv)
         on.check("initial_state", initial_state, torch.float32, states)
         on.check("dlast_state", dlast_state, torch.float32, states)
-        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=q.device)      # noqa: E731
+        new = lambda shape, dtype: q.new_empty(shape, dtype=dtype)      # noqa: E731
         out = {"dq": new(q.shape, q.dtype), "dk": new(q.shape, q.dtype), "dv": new(v.shape, q.dtype)}
         if decay_grad:
             out["dlog_decay"] = new(log_decay.shape, torch.float32)
@@ -1072,7 +1079,7 @@ def linear_attention_step(q, k, v, log_decay, *, state, scale: float = 1.0, o=No
         raise ValueError("q and v must be [batch, heads, width] (one token per batch row)")
     with _On(q, stream) as on:
         if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+            o = q.new_empty(v.shape)
         dims = _linattn_dims(on, q, k, v, log_decay, o, scale, step=True)
         slots = state.shape[0]
         on.check("state", state, torch.float32, (slots, dims.nheads, dims.dk, dims.dv))
@@ -1091,17 +1098,16 @@ def _norm_dims(on, x, weight, bias, z, y, groups, eps, activation):
     import torch
     if x.dim() not in (2, 3):
         raise ValueError("x must be [batch, L, C] or [rows, C]")
-    io, shape, strides = x.dtype, x.shape, []
-    for name, t in (("x", x), ("z", z), ("y", y)):
-        if t is None:
-            strides += (0, 0)
-            continue
-        on.check(name, t, io, shape, contiguous=False)
-        s = t.stride()
-        if s[-1] != 1 and shape[-1] > 1:
-            raise ValueError("%s: the channel axis must be unit-stride" % name)
-        strides += (0, s[0]) if len(s) == 2 else s[:2]
+    io, shape = x.dtype, x.shape
     C = shape[-1]
+    sx, sz, sy = x.stride(), (0, 0, 1), y.stride()
+    if z is not None:
+        on.check("z", z, io, shape, contiguous=False)
+        sz = z.stride()
+    on.check("y", y, io, shape, contiguous=False)
+    if C > 1 and not sx[-1] == sz[-1] == sy[-1] == 1:
+        raise ValueError("x, z and y: the channel axis must be unit-stride")
+    strides = sx[:2] + sz[:2] + sy[:2] if len(shape) == 3 else (0, sx[0], 0, sz[0], 0, sy[0])
     on.check("weight", weight, torch.float32, (C,))
     on.check("bias", bias, torch.float32, (C,))
     batch, L = (1, shape[0]) if len(shape) == 2 else shape[:2]
@@ -1134,12 +1140,12 @@ def group_norm_bwd(x, weight=None, bias=None, z=None, *, dy, groups: int, eps: f
     with _On(x, stream) as on:
         dims = _norm_dims(on, x, weight, bias, z, dy, groups, eps, activation)
         C = (x.shape[-1],)
-        out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device)}
+        out = {"dx": x.new_empty(x.shape)}
         if z is not None:
-            out["dz"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out["dz"] = x.new_empty(x.shape)
         for name, t in (("dweight", weight), ("dbias", bias)):
             if t is not None:
-                out[name] = torch.empty(C, dtype=torch.float32, device=x.device)
+                out[name] = x.new_empty(C, dtype=torch.float32)
         ref = ctypes.byref(dims)
         need = lib().group_norm_bwd_workspace_size(ref) if weight is not None or bias is not None else 0
         keep, ws, nbytes = on.workspace(workspace, need)
