@@ -676,8 +676,8 @@ void group_norm_dims_init(selscan_norm_dims* dims, int io_dtype, int64_t batch, 
 /*
  * group_norm_fwd -- x, z (or NULL: no gate), y in dims->io_dtype; weight, bias: [dim] fp32, or NULL
  * (ones, zeros).  y may be x or z themselves (same strides); its rows must not overlap otherwise
- * (else SELSCAN_ERR_UNSUPPORTED).  batch * seqlen * groups must be below 2^31 and the call's
- * threads below 2^32.  Never allocates.  Status codes as selective_scan_fwd.
+ * (else SELSCAN_ERR_UNSUPPORTED).  batch * seqlen * groups must be below 2^31, and below 2^24
+ * where a group has more than 2048 channels.  Never allocates.  Status codes as selective_scan_fwd.
  */
 int group_norm_fwd(const void* x, const float* weight, const float* bias, const void* z, void* y,
                    const selscan_norm_dims* dims, void* stream);

@@ -5,11 +5,11 @@
 // Backward, dn = dy act'(n) (gate: dy act(z), dz = dy n act'(z)), u = dn w, r = 1 / sqrt(var + eps):
 //     dx = r (u - mean(u) - xh mean(u xh)),  dw = sum dn xh,  db = sum dn
 //
-// A group lies in the registers of up to 64 lanes (four wavefronts above 2048 channels), 16 bytes of each operand a lane and
+// A group lies in the registers of up to 64 lanes, or of four wavefronts, 16 bytes of each operand a lane and
 // piece, so that a row is read once: the mean, then the squares of what is off it (not E x^2 - mean^2, which cancels),
 // both in fp32.  Results are rounded once.  Memory bounds the forward (16384 x 32 x 128 bf16, gate: 80 us, 5.0
 // TB/s; a large copy 5.2); the backward (16384 x 40 x 64: 115 us for 420 MB, 3.7 TB/s) also waits for its
-// two sums in a row, one after the other, with four wavefronts a SIMD: more registers for rows on their way leave fewer.
+// two sums in a row, one after the other, with three to seven wavefronts a SIMD.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -184,7 +184,8 @@ template <typename T, int VEC, int EPT, bool EVEN>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
   __shared__ float tmp[4];
   const int lanes = 1 << p.log_lanes, lane = threadIdx.x & (lanes - 1);
-  const uint32_t gi = blockIdx.x * (256u >> p.log_lanes) + (threadIdx.x >> p.log_lanes), groups = uint32_t(p.groups);
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x, groups = uint32_t(p.groups);
+  const uint32_t gi = block * (256u >> p.log_lanes) + (threadIdx.x >> p.log_lanes);
   if (gi >= uint32_t(p.rows) * groups) return;
   // (32 bits hold rows and groups; divisions of 64 take as many instructions as the row's arithmetic: 91 us in the place
   // of 82, 16384 rows of 32 x 128 with a gate)
@@ -221,8 +222,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
 }
 
 // A workgroup keeps to `256 / lanes` groups of channels (of several rows at once where there are fewer groups)
-// and walks every `splits`-th row, so that the sums for weight and bias stay in registers.  The next row is
-// asked for before this one is looked at (16384 x 40 x 64: 195 us without, 181 with, forward and backward).
+// and walks every `splits`-th row, so that the sums for weight and bias stay in registers.  (The next row
+// asked for ahead takes registers that more wavefronts make better use of: 16384 x 32 x 128 fp32 271 us, 262 without.)
 template <typename T, int VEC, int EPT, bool EVEN>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   __shared__ float tmp[4];
@@ -254,20 +255,18 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
     if (gate) z.load(static_cast<const T*>(p.z) + b * p.z_sb + l * p.z_sl + c0, lanes, lane, p.width);
     dy.load(static_cast<const T*>(p.dy) + b * p.y_sb + l * p.y_sl + c0, lanes, lane, p.width);
   };
-  if (part < p.rows) ask(part);
   for (int64_t row = part; row < p.rows; row += step) {
-    const NormPiece<T, VEC, EPT, EVEN> now_x = x, now_z = z, now_dy = dy;
-    if (EPT * VEC <= 16 && row + step < p.rows) ask(row + step);   // (wider groups leave no registers for it)
+    ask(row);
     const int64_t out = row * p.groups * p.width + c0;
     NormRow<T, VEC, EPT, EVEN> n;
-    n.form(now_x, lanes, lane, p.width, p.eps, tmp);
+    n.form(x, lanes, lane, p.width, p.eps, tmp);
     float u[EPT * VEC], m1 = 0.f, m2 = 0.f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
       const NormPlace<VEC, EVEN> at(i, lanes, lane, p.width);
       float d[VEC], t[VEC], dz[VEC];
-      now_dy.widen(i, d);                         // (zero behind the group's end: nothing comes of it there)
-      if (gate) now_z.widen(i, t);
+      dy.widen(i, d);                         // (zero behind the group's end: nothing comes of it there)
+      if (gate) z.widen(i, t);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const int k = i * VEC + e;
@@ -303,7 +302,6 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
       }
       if (at.in) norm_store<T, VEC, EVEN>(static_cast<T*>(p.dx) + out + at.c, d);
     }
-    if (EPT * VEC > 16 && row + step < p.rows) ask(row + step);
   }
   if (!p.part) return;
   // the rows that a wavefront takes at once, into its first threads
@@ -370,7 +368,9 @@ hipError_t norm_launch(bool bwd, const NormParams& p, hipStream_t stream) {
     norm_bwd_kernel<T, VEC, EPT, EVEN><<<dim3(uint32_t(p.cblocks * p.splits)), dim3(256), 0, stream>>>(p);
   } else {
     const int64_t per = 256 >> p.log_lanes;
-    norm_fwd_kernel<T, VEC, EPT, EVEN><<<dim3(uint32_t((p.rows * p.groups + per - 1) / per)), dim3(256), 0, stream>>>(p);
+    const int64_t blocks = (p.rows * p.groups + per - 1) / per, kSide = 1 << 20;     // (2^32 threads a side at most)
+    const dim3 grid(uint32_t(blocks < kSide ? blocks : kSide), uint32_t((blocks + kSide - 1) / kSide));
+    norm_fwd_kernel<T, VEC, EPT, EVEN><<<grid, dim3(256), 0, stream>>>(p);
   }
   return hipGetLastError();
 }
@@ -389,16 +389,21 @@ hipError_t norm_pieces(bool bwd, const NormParams& p, hipStream_t stream) {
 template <typename T>
 hipError_t norm_dispatch(bool bwd, const NormParams& p, hipStream_t stream) {
   if (p.width < 16 / int(sizeof(T))) return norm_launch<T, 1, 1, false>(bwd, p, stream);
+  // (The masks of a last piece cost 16384 x 32 x 128 bf16 92 -> 97 us forward, x 40 x 64 117 -> 129 backward.)
   return p.even ? norm_pieces<T, true>(bwd, p, stream) : norm_pieces<T, false>(bwd, p, stream);
 }
 
 }  // namespace
 
-NormPlan norm_plan(bool bf16, int64_t rows, int64_t groups, int64_t width) {
+NormPlan norm_plan(bool bf16, bool bwd, int64_t rows, int64_t groups, int64_t width) {
   NormPlan pl{};
   const int64_t vec = bf16 ? 8 : 4, per = width < vec ? 1 : vec, pieces = (width + per - 1) / per;
   while (pl.log_lanes < 6 && 1 << pl.log_lanes < pieces) ++pl.log_lanes;
-  if (width > 64 * kNormElems) pl.log_lanes = 8;
+  // Four wavefronts for a group that would be more than four pieces a lane of one; in the backward, which holds six
+  // values for each of the forward's two, more than two (16384 x 2 x 2048 bf16, a gate: forward 81 us with one
+  // wavefront a group, 85 with four, backward 223 and 157; 8192 x 2 x 2048 fp32 81 and 73, 201 and 148; 16384 x 4 x 1024
+  // bf16 77 and 112, 167 and 225).
+  if (pieces > (bwd ? 128 : 256)) pl.log_lanes = 8;
   const int64_t lanes = 1 << pl.log_lanes, slots = 256 / lanes;
   pl.ept = int32_t((pieces + lanes - 1) / lanes);
   pl.gper = 1;

@@ -373,14 +373,13 @@ struct LinStepParams {
 hipError_t launch_lin_step(bool bf16, const LinStepParams& p, hipStream_t stream);
 
 // Group norm with an activation (norm_kernels.hip).
-constexpr int kNormElems = 32;          // of a group in one thread, at most
 struct NormPlan {
   int32_t log_lanes;    // threads of a group: a power of two up to 64, or 256
   int32_t ept;          // accesses of a thread
   int64_t gper, cblocks, splits, parts;  // backward: groups side by side in a workgroup, blocks of them, workgroups
                         // that share the rows, partial sums of dweight and dbias
 };
-NormPlan norm_plan(bool bf16, int64_t rows, int64_t groups, int64_t width);
+NormPlan norm_plan(bool bf16, bool bwd, int64_t rows, int64_t groups, int64_t width);
 struct NormParams {
   const void* x;
   const float* weight;  // [C], may be null

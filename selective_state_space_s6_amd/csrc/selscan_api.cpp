@@ -1662,23 +1662,21 @@ static int norm_check(const selscan_norm_dims* dims) {
   if (d.dim > (int64_t(1) << 20) || width > 8192) return SELSCAN_ERR_UNSUPPORTED;
   const int64_t kMost = (int64_t(1) << 31) - 1;
   if (d.batch > kMost || d.seqlen > kMost || (d.batch > 0 && d.seqlen > kMost / d.batch)) return SELSCAN_ERR_UNSUPPORTED;
-  // a launch has fewer than 2^32 threads
   const int64_t rows = d.batch * d.seqlen;
   if (rows > 0) {
     if (d.groups > kMost / rows) return SELSCAN_ERR_UNSUPPORTED;
-    const int log_lanes = selscan::norm_plan(false, rows, d.groups, width).log_lanes;
-    if (rows * d.groups > ((int64_t(1) << 32) - 256) >> log_lanes) return SELSCAN_ERR_UNSUPPORTED;
+    if (width > 2048 && rows * d.groups >= int64_t(1) << 24) return SELSCAN_ERR_UNSUPPORTED;
   }
   return SELSCAN_OK;
 }
 
 static size_t norm_bwd_bytes(const selscan_norm_dims& d) {
-  const selscan::NormPlan pl = selscan::norm_plan(d.io_dtype == SELSCAN_BF16, d.batch * d.seqlen, d.groups, d.dim / d.groups);
+  const selscan::NormPlan pl = selscan::norm_plan(d.io_dtype == SELSCAN_BF16, true, d.batch * d.seqlen, d.groups, d.dim / d.groups);
   return ws_round(int64_t(sizeof(float)) * pl.parts * 2 * d.dim);
 }
 
 static selscan::NormParams norm_params(const void* x, const float* weight, const float* bias, const void* z,
-                                       std::initializer_list<const void*> others, const selscan_norm_dims& d) {
+                                       std::initializer_list<const void*> others, bool bwd, const selscan_norm_dims& d) {
   selscan::NormParams p{};
   const bool bf16 = d.io_dtype == SELSCAN_BF16;
   const int64_t v = bf16 ? 8 : 4;
@@ -1691,7 +1689,7 @@ static selscan::NormParams norm_params(const void* x, const float* weight, const
   p.eps = d.eps;
   p.even = p.width % v == 0 && all_aligned({x, weight, bias, z}, 16) && all_aligned(others, 16) && p.x_sb % v == 0 &&
           p.x_sl % v == 0 && p.y_sb % v == 0 && p.y_sl % v == 0 && (!z || (p.z_sb % v == 0 && p.z_sl % v == 0));
-  const selscan::NormPlan pl = selscan::norm_plan(bf16, p.rows, p.groups, p.width);
+  const selscan::NormPlan pl = selscan::norm_plan(bf16, bwd, p.rows, p.groups, p.width);
   p.log_lanes = pl.log_lanes; p.ept = pl.ept;
   p.gper = pl.gper; p.cblocks = pl.cblocks; p.splits = pl.splits; p.parts = pl.parts;
   return p;
@@ -1720,7 +1718,7 @@ int group_norm_fwd(const void* x, const float* weight, const float* bias, const 
   if (!empty && (!x || !y)) return SELSCAN_ERR_NULL;
   if (!all_aligned({x, z, y}, bf16 ? 2 : 4) || !all_aligned({weight, bias}, 4)) return SELSCAN_ERR_ALIGN;
   if (empty) return SELSCAN_OK;
-  selscan::NormParams p = norm_params(x, weight, bias, z, {y}, d);
+  selscan::NormParams p = norm_params(x, weight, bias, z, {y}, false, d);
   p.y = y;
   const hipError_t e = selscan::launch_norm(bf16, false, p, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
@@ -1748,7 +1746,7 @@ int group_norm_bwd(const void* x, const float* weight, const float* bias, const 
     if (e == hipSuccess && dbias) e = selscan::launch_fill_zero(dbias, d.dim, s);
     return e == hipSuccess ? SELSCAN_OK : hip_fail(e);
   }
-  selscan::NormParams p = norm_params(x, weight, bias, z, {dy, dx, dz}, d);
+  selscan::NormParams p = norm_params(x, weight, bias, z, {dy, dx, dz}, true, d);
   p.dy = dy; p.dx = dx; p.dz = dz; p.dweight = dweight; p.dbias = dbias;
   const size_t need = dweight || dbias ? group_norm_bwd_workspace_size(dims) : 0;
   void* ws = workspace;
