@@ -637,6 +637,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     // Inside a chunk a token is kept from another by a zero factor, which an infinity or a NaN turns into a
     // NaN.  If anything that comes out is not finite, what the wavefront has formed of the chunk is dropped,
     // and the rest of the segment is walked token by token.
+    // whether anything takes the state behind the last chunk
+    const bool wanted = STATE || (p.s1 && seg == (REV ? 0 : p.nseg - 1));
     bool done = true;
     int ci = 0;
     int64_t t0 = start_of(0);
@@ -688,7 +690,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
         out += kOn * osl * oes;
         if (DOT) xs += kOn * xsl;
       }
-      if (done) update(dec);
+      if (done && (more || wanted)) update(dec);
       __syncthreads();
       if (!STATE && sh.bad != 0) break;
       if (DOT && vid < n) {
@@ -803,7 +805,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
       if (wave == kDecayWave && lane == 0 && nb == 0)
         p.seg_decay[bh * p.nseg + seg] = anew ? -1.f : lin_decay(float(total));
-    } else if (p.s1 && seg == (REV ? 0 : p.nseg - 1)) {
+    } else if (wanted) {
       float* const to = p.s1 + bh * block;
       each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
     }
