@@ -156,7 +156,8 @@ __device__ __forceinline__ float lin_decay(float log2d) {
 }
 
 // Tokens of a chunk: the LDS of a compute unit holds the tiles of a chunk of 64, but not those of 256
-// fp32 channels.
+// fp32 channels.  (Chunks of 32 for all of fp32, two workgroups a compute unit: 2 x 16 heads x 4096, 64 x 64, 79 us in
+// the place of 80; 128 x 128, whose registers then spill, 231 in the place of 198.)
 template <typename T, int KD> constexpr int lin_chunk_of() { return sizeof(T) == 4 && KD == 256 ? 32 : 64; }
 
 // Wavefronts that a SIMD is to hold, NW of them a workgroup: as many as the LDS of a compute unit holds tiles for.
