@@ -345,12 +345,16 @@ struct LinDecayParams {
   const float* kdk;     // [nk][batch][H][L]
   const float* last;    // [batch][H][state], with dlast; both may be null (zero)
   const float* dlast;
+  const float* states;  // nseg > 1: [batch][H][nseg][state], what enters each segment ...
+  const float* grads;   // ... and its gradient, which enters from behind
   const float* g;
   int64_t g_sb, g_sl, g_sh;
   float* dg;            // [batch][L][H], or null: the heads' sums only
-  double* sums;         // workspace [batch][H]
+  double* sums;         // workspace [batch][H][nseg]
   float* dg_heads;      // [H], or null
   int64_t batch, L, H, state;
+  int64_t seg_len;      // tokens of a segment
+  int32_t nseg;
   int32_t nq, nk;
 };
 hipError_t launch_lin_decay(const LinDecayParams& p, hipStream_t stream);

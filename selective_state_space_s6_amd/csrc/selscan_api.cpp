@@ -1390,7 +1390,7 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       p.off_last = off;
       off += ws_round(f * bh * d.dk * d.dv);
       p.off_sums = off;
-      off += ws_round(int64_t(sizeof(double)) * bh);
+      off += ws_round(int64_t(sizeof(double)) * bh * p.nseg);
     }
     p.off_part = off;
     if (d.nheads != d.qk_heads) off += ws_round(2 * f * rows * d.dk);
@@ -1591,6 +1591,8 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
     selscan::LinDecayParams c{};
     c.qdq = reinterpret_cast<float*>(ws + pl.off_qdq);
     c.kdk = reinterpret_cast<float*>(ws + pl.off_kdk);
+    c.states = walks[0].seg; c.grads = walks[1].seg;
+    c.seg_len = pl.seg_len; c.nseg = pl.nseg;
     c.last = want_last ? last : nullptr;
     c.dlast = dlast_state;
     c.g = log_decay; c.g_sb = walks[0].g_sb; c.g_sl = walks[0].g_sl; c.g_sh = walks[0].g_sh;
