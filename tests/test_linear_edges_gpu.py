@@ -178,6 +178,24 @@ def test_gradients_of_a_document_next_to_one_that_is_not_finite(size, io):
         assert np.isfinite(host(d["dinitial_state"])).all()
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("name,value", [("v", np.inf), ("do", np.nan), ("k", -np.inf), ("q", np.inf)])
+def test_decay_gradient_of_documents_next_to_one_that_is_not_finite(name, value, io):
+    """Documents that lie across segments, one of them not finite: the others' gradients are the same."""
+    size = (1, 900, 2, 1, 64, 64)
+    i = inputs(size, io, seed=9, decay="token")
+    for c in (400, 640, 800):
+        i["g"][:, c] = -np.inf
+    clean = bwd(tensors(i, io), i)
+    lin.check_backward(i, size, io, clean)
+    j = dict(i, **{name: i[name].copy()})
+    j[name][0, 700] = value
+    got = bwd(tensors(j, io), j)["dlog_decay"]
+    assert not np.isfinite(host(got)[0, 640:800]).all()
+    got[:, 640:800] = clean["dlog_decay"][:, 640:800]
+    lin.check_backward(i, size, io, dict(clean, dlog_decay=got))
+
+
 def test_sums_that_leave_the_range():
     """Products beyond fp32's largest value are infinite, whatever lies beside them."""
     i = inputs((1, 130, 1, 1, 16, 16), "f32", seed=2, decay="fixed")
