@@ -596,8 +596,8 @@ void linear_attention_dims_init(selscan_linattn_dims* dims, int io_dtype, int64_
  *                    stream-ordered on `stream`.  Not to be used by other work until the enqueued
  *                    call has finished (two captured graphs that may run at once need one each).
  * Products are formed of the inputs as they are and summed in fp32.  With bf16 I/O the pairs of a
- * chunk are rounded to bf16 before they meet v, the state keeps 16 bits of mantissa where it
- * meets q and 24 where it is carried.
+ * chunk keep 16 bits of mantissa where they meet v, the state 16 where it meets q and 24 where it
+ * is carried; the result is rounded once.
  * batch * nheads * ceil(dv / 64) must be below 2^22.  Pointers and status codes otherwise as
  * selective_scan_fwd; seqlen == 0 hands the initial state (zeros if NULL) to last_state.
  */

@@ -52,6 +52,14 @@ template <typename T, int W> __device__ __forceinline__ int lin_at(int row, int 
   return row * W + ((col / V) ^ f) * V + col % V;
 }
 
+// Place of the pairs of row i and keys j .. in their tile: of the 16 x 16 blocks only those that see each other are
+// kept, by rows of blocks (the backward's mirrored, `it` and `jt` counted from the end).  A row of fp32 has four 16-byte pieces, exchanged by bits
+// of the row; one of bf16 has two, and a block's sixteen rows lie on all banks as they are.
+template <typename T> __device__ __forceinline__ int lin_pair_at(int it, int jt, int row, int col) {
+  constexpr int V = 16 / int(sizeof(T)), f = sizeof(T) == 4 ? 3 : 0;
+  return ((it * (it + 1) / 2 + jt) * 16 + row) * 16 + ((col / V) ^ ((row >> 2) & f)) * V + col % V;
+}
+
 // What the walk needs of an element type: eight consecutive values of a contraction in one
 // fragment (lane l: row or column l % 16, values 8 (l / 16) ..), and the product of two.
 template <typename T> struct lin_io;
@@ -75,6 +83,7 @@ template <> struct lin_io<uint16_t> {
   template <int W> static __device__ __forceinline__ frag row(const uint16_t* tile, int r, int c) {
     return *reinterpret_cast<const frag*>(tile + lin_at<uint16_t, W>(r, c));
   }
+  static __device__ __forceinline__ frag pair(const uint16_t* tile, int at) { return *reinterpret_cast<const frag*>(tile + at); }
   static __device__ __forceinline__ f32x8 wide(frag a) { return __builtin_convertvector(a, f32x8); }
   static __device__ __forceinline__ frag round(f32x8 a) { return __builtin_convertvector(a, frag); }
   static __device__ __forceinline__ void narrow(uint16_t* p, float v) { *p = bf16_rne(v); }
@@ -101,6 +110,11 @@ template <> struct lin_io<float> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = tile[lin_at<float, W>(r0 + e, col)];
     return v;
+  }
+  static __device__ __forceinline__ frag pair(const float* tile, int at) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(tile + at);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(tile + (at ^ 4));       // (the piece beside it)
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   static __device__ __forceinline__ f32x8 wide(frag a) { return a; }
   static __device__ __forceinline__ frag round(f32x8 a) { return a; }
@@ -176,12 +190,12 @@ template <int C> struct alignas(16) LinDecays {
 
 template <typename T, int KD, int NW, int HP, bool STATE, bool DOT>
 struct alignas(16) LinShared {
-  static constexpr int NPP = sizeof(T) == 2 && DOT ? 3 : 1;       // parts of the pairs on the matrix cores
-  static constexpr int C = lin_chunk_of<T, KD>(), kWP = C * int(sizeof(T)) < 128 ? 128 / int(sizeof(T)) : C;
+  static constexpr int NPP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2;   // parts of the pairs on the matrix cores
+  static constexpr int C = lin_chunk_of<T, KD>(), IT = C / 16, kPairs = IT * (IT + 1) / 2 * 256;
   T q[STATE ? 8 : C * KD];
   T k[C * KD];
   T v[C * 16 * NW];
-  T p[STATE ? 8 : HP * NPP * C * kWP];
+  T p[STATE ? 8 : HP * NPP * kPairs + 8];                          // (8 zeros behind them)
   LinDecays<C> dec[HP][2];  // this chunk's, and the next one's
   float dot[DOT ? NW : 1][DOT ? C : 1];
   int bad;
@@ -269,8 +283,8 @@ template <LinWalk WALK> struct LinWalks { LinParams p[WALK == LinWalk::states ||
 // its accumulators, which are at once the operand of its product with the queries.
 // STATE: only the state at the segment's end, from zero.
 // DOT: the rows' products with x too.  The decays' gradient is what remains of their sum over all later tokens in
-// one walk less that in the other, so pairs and state then go to the matrix cores with 24 bits.  Else the pairs
-// are rounded to 8, as the result is, and the state to 16.
+// one walk less that in the other, so pairs and state then go to the matrix cores with 24 bits.  Else both go
+// there with 16, twice the result's own (pairs of 8 bits would add as much again to its rounding).
 template <typename T, int KD, int NW, int HP, LinWalk WALK>
 __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::grads>())) void lin_kernel(LinWalks<WALK> walks) {
   constexpr bool STATE = WALK == LinWalk::state || WALK == LinWalk::states, DOT = WALK == LinWalk::grads;
@@ -285,7 +299,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
   auto segment = [&](auto reversed, const LinParams& p, const int item) __attribute__((always_inline)) {
     constexpr bool REV = decltype(reversed)::value;
     constexpr int kWaves = NW / HP;                 // of a head
-    constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kWP = Sh::kWP, kThreads = 64 * NW;
+    constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kPairs = Sh::kPairs, kThreads = 64 * NW;
     constexpr int kDecayWave = kWaves - 1;          // has the least to do with the pairs
 
     const int all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), part = all_wave / kWaves, wave = all_wave % kWaves;
@@ -323,7 +337,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     LinTile<T, KD, C, kThreads> tq, tk;
     LinTile<T, kWV, C, 64 * kWaves> tv;
     T* const sv = sh.v + part * C * kWV;
-    T* const sp = STATE ? sh.p : sh.p + part * NPP * C * kWP;
+    T* const sp = STATE ? sh.p : sh.p + part * NPP * kPairs;
+    const int nothing = (HP - part) * NPP * kPairs;
     if (!STATE) tq.init(p.q, b, h, start_of(0), 0, p.kd);
     tk.init(p.k, b, h, start_of(0), 0, p.kd);
     tv.init(p.v, b, h, start_of(0), col0, p.vd);
@@ -419,6 +434,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int j0 = 32 * ks + 16 * u + 4 * g;
+          const int pi = REV ? IT - 1 - it : it, pj = REV ? IT - 1 - 2 * ks - u : 2 * ks + u;
+          if (pj > pi) continue;                    // (the block beyond the diagonal's)
           f32x4 val;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -429,7 +446,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
           }
 #pragma unroll
           for (int x = 0; x < NPP; ++x) {
-            io::store(sp + x * C * kWP + lin_at<T, kWP>(i, j0), val);
+            io::store(sp + x * kPairs + lin_pair_at<T>(pi, pj, l16, 4 * g), val);
             if (x + 1 < NPP)
 #pragma unroll
               for (int r = 0; r < 4; ++r) val[r] = lin_rest(val[r]);
@@ -481,12 +498,19 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       auto seen = [](int it, int ks) { return REV ? 32 * ks + 31 >= 16 * it : 32 * ks <= 16 * it + 15; };
 #pragma unroll
       for (int x = 0; x < NPP; ++x) {
+        if (x > 0) __builtin_amdgcn_sched_barrier(0);
         frag fp[IT][KS];
 #pragma unroll
         for (int it = 0; it < IT; ++it)
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks)
-            if (seen(it, ks)) fp[it][ks] = io::template row<kWP>(sp + x * C * kWP, 16 * it + l16, 32 * ks + 8 * g);
+            if (seen(it, ks)) {
+              // (lane groups 0 and 1 have the first block's values, 2 and 3 the second's: of the diagonal's, one is not kept)
+              const int pi = REV ? IT - 1 - it : it, pj = REV ? IT - 1 - 2 * ks : 2 * ks, more = REV ? -(g >> 1) : g >> 1;
+              const int at = lin_pair_at<T>(pi, pj, 16 * more + l16, 8 * (g & 1));
+              const bool whole = REV ? pj <= pi : pj < pi;
+              fp[it][ks] = io::pair(sp, whole || pj + more <= pi ? x * kPairs + at : nothing);
+            }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -651,6 +675,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     if (wave == kDecayWave) decays(sh.dec[part][0]);
     if (chunks > 1) load_gate(t0 + kOn);
     if (!STATE && tid == 0) sh.bad = 0;
+    if (!STATE && tid < 8) sh.p[HP * NPP * kPairs + tid] = T(0);
     for (;; ++ci, t0 += kOn) {
       LinDecays<C>& dec = sh.dec[part][ci & 1];
       const int n = tokens_of(t0);

@@ -1,0 +1,34 @@
+"""What linear attention keeps of its sums, against its 64-bit statement: the bits of what meets the matrix
+cores, and the range of the states.
+
+Tolerances as in test_linear_gpu.py, where a pair or a state in two bf16 parts is off by at most 2^-17 of
+itself: the first part leaves at most 2^-8 of its power of two, whose own rounding is 2^-9 of that."""
+import numpy as np
+import pytest
+
+from oracle import linear as orc
+from tests import test_linear_gpu as lin
+
+pytestmark = pytest.mark.gpu
+
+dev, host, inputs = lin.dev, lin.host, lin.inputs
+TWO_PARTS = 2.0 ** -17
+
+
+@pytest.mark.parametrize("decay", ["fixed", "token", "packed", "grow"])
+@pytest.mark.parametrize("size", lin.SIZES + [(1, 1100, 4, 1, 64, 64), (2, 705, 4, 2, 128, 32), (1, 900, 2, 2, 16, 256)])
+def test_bf16_results_are_rounded_once(size, decay):
+    """2^-8 of the result, its own rounding, and 16 bits of what adds up to it: not 8 bits of each pair."""
+    i = inputs(size, "bf16", seed=sum(size) + 2, decay=decay)
+    n, _, out = lin.units(size, "bf16")
+    args = lambda j: tuple(j[a] for a in "qkvg")                                          # noqa: E731
+    a = lin.absolute(i)
+    (ro, _), (mo, _) = (orc.linear_fwd(*args(j), i["scale"], j["S0"]) for j in (i, a))
+    o, _ = lin.forward(i, "bf16")
+    lin.near(o, ro, out * np.abs(ro) + (n + 2 * TWO_PARTS) * mo, "o")
+    ref, mag = (orc.linear_bwd(*args(j), j["do"], i["scale"], j["S0"], j["dlast"]) for j in (i, a))
+    for decay_grad in (True, False):
+        d = lin.backward(i, "bf16", decay_grad=decay_grad)
+        for k in ("dq", "dk", "dv"):
+            more = size[2] // size[3] * 2.0 ** -24
+            lin.near(d[k], ref[k], out * np.abs(ref[k]) + (n + more + 2 * TWO_PARTS) * mag[k], "%s, decay_grad %s" % (k, decay_grad))
