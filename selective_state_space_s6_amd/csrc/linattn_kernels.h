@@ -41,6 +41,7 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
 constexpr float kTiny = 1.401298464e-45f;      // 2^-149
+constexpr int kNowhere = 0x3ffffff0;            // a place in bytes beyond any state, another state's added to it too
 
 // Place of (row, column) in an LDS tile of W columns.  A row's 16-byte pieces are exchanged with one another by
 // bits of the row, so that both ways of reading spread over the banks: sixteen rows of one column of
@@ -278,6 +279,41 @@ struct LinTile {
 
 template <LinWalk WALK> struct LinWalks { LinParams p[WALK == LinWalk::states || WALK == LinWalk::grads ? 2 : 1]; };
 
+// One of a kernel's LinWalks, its first argument, read anew: what comes of it is not kept from before.
+__device__ __forceinline__ const LinParams& lin_again(int i) {
+  auto at = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return ((const LinParams*)at)[i];
+}
+
+// A workgroup's part of a walk: head `part` of its heads, a block of columns, a segment.
+template <int C, int HP, int COLS, bool STATE, bool REV> struct LinPlace {
+  int nb, seg, chunks, col0;
+  int64_t h, b, bh, chunk0, L;
+  __device__ __forceinline__ LinPlace(const LinParams& p, int item, int part) {
+    const int segs = STATE ? p.nseg - 1 : p.nseg;   // (nothing is behind the last segment)
+    const int H = int(p.H), heads = H / HP, sidx = item / heads / p.nblk % segs;
+    nb = item / heads % p.nblk;
+    h = item % heads * HP + part;
+    b = item / heads / p.nblk / segs;
+    bh = b * H + h;
+    seg = STATE && REV ? sidx + 1 : sidx;
+    chunk0 = int64_t(seg) * p.seg_chunks;
+    chunks = int(p.nchunks - chunk0 < p.seg_chunks ? p.nchunks - chunk0 : p.seg_chunks);
+    col0 = nb * COLS;
+    L = p.L;
+  }
+  __device__ __forceinline__ int64_t start_of(int ci) const { return (chunk0 + (REV ? chunks - 1 - ci : ci)) * C; }
+  __device__ __forceinline__ int tokens_of(int64_t t0) const { return int(L - t0 < C ? L - t0 : C); }
+  // column `col` of a row of `out`, and of x
+  __device__ __forceinline__ char* out_at(const LinParams& p, int64_t t, int col, int size) const {
+    return static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + t * p.o_sl + col) * size;
+  }
+  template <typename T> __device__ __forceinline__ const T* x_at(const LinParams& p, int64_t t, int col) const {
+    return static_cast<const T*>(p.x.p) + b * p.x.sb + (h / p.x.share) * p.x.sh + t * p.x.sl + col;
+  }
+};
+
 // One workgroup of NW wavefronts walks the chunks of one segment of HP heads of one batch row that share their
 // queries and keys, for 16 NW / HP columns of v each: a wavefront owns 16 of them, and the state's [KD][16] in
 // its accumulators, which are at once the operand of its product with the queries.
@@ -291,6 +327,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
   using io = lin_io<T>;
   using frag = typename io::frag;
   constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2;   // parts of the state on the matrix cores
+  constexpr bool kBoth = WALK == LinWalk::states || WALK == LinWalk::grads;
   constexpr int NX = sizeof(T) == 2 ? 3 : 1;      // the state is held in fp32: what is added to it keeps 24 bits
   using Sh = LinShared<T, KD, NW, HP, STATE, DOT>;
   constexpr int NPP = Sh::NPP;
@@ -304,35 +341,41 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
 
     const int all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), part = all_wave / kWaves, wave = all_wave % kWaves;
     int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
-    const int segs = STATE ? p.nseg - 1 : p.nseg;   // (nothing is behind the last segment)
-    const int H = int(p.H), heads = H / HP, nb = item / heads % p.nblk, sidx = item / heads / p.nblk % segs;
-    const int64_t h = item % heads * HP + part, b = item / heads / p.nblk / segs, bh = b * H + h;
-    const int seg = STATE && REV ? sidx + 1 : sidx;
-    const int64_t chunk0 = int64_t(seg) * p.seg_chunks;
-    const int chunks = int(p.nchunks - chunk0 < p.seg_chunks ? p.nchunks - chunk0 : p.seg_chunks);
-    const int col0 = nb * kWV, wcol = wave * 16;
+    using Place = LinPlace<C, HP, kWV, STATE, REV>;
+    const Place place(p, item, part);
+    const int nb = place.nb, chunks = place.chunks, col0 = place.col0, wcol = wave * 16;
+    const int64_t h = place.h, b = place.b, bh = place.bh;
 
     f32x4 S[KK][2];
-    auto zero_state = [&] {
-#pragma unroll
-      for (int a = 0; a < KK; ++a) S[a][0] = S[a][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    };
-    // f(four state values, which of them, its place in a head's state)
-    auto each_state = [&](auto&& f) {
-      const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4;
+    // f(four state values, which of them, its place in a head's state in bytes): beyond the state for what is not there, where loads give
+    // zero and stores are dropped
+    auto each_state = [&](const LinParams& p, int col0, auto&& f) __attribute__((always_inline)) {
+      const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4, n = col0 + wcol + l16;
+      const int row = 4 * int(p.s_row), col = n < p.vd ? 4 * int(p.s_col) * n : kNowhere, left = p.kd - 8 * g;
 #pragma unroll
       for (int a = 0; a < KK; ++a)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int kd = 32 * a + 8 * g + 4 * u + r, n = col0 + wcol + l16;
-            if (kd < p.kd && n < p.vd) f(S[a][u], r, p.s_row * kd + p.s_col * n);
+            const int kd = 32 * a + 4 * u + r;
+            f(S[a][u], r, kd < left ? row * (8 * g + kd) + col : kNowhere);
           }
     };
+    auto state_at = [](const float* at, const LinParams& p) {
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(at), (short)0, at ? p.kd * p.vd * 4 : 0, 0x00020000);
+    };
+    auto load_state = [&](const LinParams& p, int col0, const float* at) __attribute__((always_inline)) {
+      const auto from = state_at(at, p);
+      each_state(p, col0, [&](f32x4& s, int r, int at) { s[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, at, 0, 0)); });
+    };
+    auto store_state = [&](const LinParams& p, int col0, float* at) __attribute__((always_inline)) {
+      const auto to = state_at(at, p);
+      each_state(p, col0, [&](f32x4& s, int r, int at) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s[r]), to, at, 0, 0); });
+    };
 
-    auto start_of = [&](int ci) { return (chunk0 + (REV ? chunks - 1 - ci : ci)) * C; };
-    auto tokens_of = [&](int64_t t0) { return int(p.L - t0 < C ? p.L - t0 : C); };
+    auto start_of = [&](int ci) { return place.start_of(ci); };
+    auto tokens_of = [&](int64_t t0) { return place.tokens_of(t0); };
 
     LinTile<T, KD, C, kThreads> tq, tk;
     LinTile<T, kWV, C, 64 * kWaves> tv;
@@ -526,10 +569,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     // Four columns of a row of the chunk's tile of `out`; rows and columns that are not there are beyond it,
     // and dropped.
     const int ocols = p.vd - (col0 + wcol), osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
-    auto out_at = [&](int64_t t) { return static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + t * p.o_sl + col0 + wcol) * oes; };
-    auto x_at = [&](int64_t t) { return DOT ? LinTile<T, kWV, C, 64 * kWaves>::head(p.x, b, h, col0 + wcol) + t * p.x.sl : nullptr; };
-    char* out = out_at(start_of(0));
-    const T* xs = x_at(start_of(0));
+    char* out = place.out_at(p, start_of(0), col0 + wcol, oes);
+    const T* xs = DOT ? place.template x_at<T>(p, start_of(0), col0 + wcol) : nullptr;
     // x's rows, asked for before they meet the result (16 bits a value: two a register)
     constexpr int kXRegs = sizeof(T) == 2 ? 2 : 4;
     uint32_t xv[DOT ? IT : 1][kXRegs];
@@ -652,18 +693,18 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       }
     };
 
-    zero_state();
-    const int block = p.kd * p.vd;                  // of a head's state
-    if (!STATE) {
-      const float* const from = p.nseg > 1 ? p.seg + (bh * p.nseg + seg) * block : p.s0 ? p.s0 + bh * block : nullptr;
-      if (from) each_state([&](f32x4& s, int r, int at) { s[r] = from[at]; });
-    }
+    auto first_state = [&](const LinParams& p, const Place& place) __attribute__((always_inline)) {
+      const int block = p.kd * p.vd;                // of a head's state
+      load_state(p, place.col0, STATE ? nullptr : p.nseg > 1 ? p.seg + (place.bh * p.nseg + place.seg) * block : p.s0 ? p.s0 + place.bh * block : nullptr);
+    };
+    first_state(p, place);
 
     // Inside a chunk a token is kept from another by a zero factor, which an infinity or a NaN turns into a
     // NaN.  If anything that comes out is not finite, what the wavefront has formed of the chunk is dropped,
-    // and the rest of the segment is walked token by token.
+    // and the rest of the segment is walked token by token.  Where the state before the chunk is not finite, it may be
+    // by the multiple that it is held as (up to 2^16 of it): it is formed again then, token by token from the first.
     // whether anything takes the state behind the last chunk
-    const bool wanted = STATE || (p.s1 && seg == (REV ? 0 : p.nseg - 1));
+    const bool wanted = STATE || (p.s1 && place.seg == (REV ? 0 : p.nseg - 1));
     bool done = true;
     int ci = 0;
     int64_t t0 = start_of(0);
@@ -730,110 +771,113 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     }
     // the accumulators as the state itself
     multiply(STATE || done ? sh.dec[part][ci & 1].after : sh.dec[part][ci & 1].before);
-    bool slow = !STATE && sh.bad != 0;
-    if (STATE) {
-      float chk = 0.f;
+    {
+      // (What follows forms its places anew: kept through the walk, they would not leave its registers room.)
+      const LinParams& p = lin_again(kBoth && REV ? 1 : 0);
+      int it = item;
+      asm volatile("" : "+s"(it), "+s"(ci));
+      const Place place(p, it, part);
+      const int col0 = place.col0, chunks = place.chunks;
+      const int64_t h = place.h, b = place.b, bh = place.bh;
+      const bool bad = !STATE && sh.bad != 0, ends = STATE || (p.s1 && place.seg == (REV ? 0 : p.nseg - 1));
+      bool again = false;
+      if (STATE || bad || ends) {
+        float chk = 0.f;
 #pragma unroll
-      for (int a = 0; a < KK; ++a)
+        for (int a = 0; a < KK; ++a)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) chk = fmaf(S[a][u][r], 0.f, chk);
-      slow = __syncthreads_or(chk != 0.f);
-      if (slow) {
-        zero_state();
-        ci = 0;
+            for (int r = 0; r < 4; ++r) chk = fmaf(S[a][u][r], 0.f, chk);
+        again = __syncthreads_or(chk != 0.f);
       }
-    }
-    // ---- token by token, with choices in the place of zero factors; `done`: the first chunk stands
-    if (slow) {
-      float* const row_q = reinterpret_cast<float*>(sh.k);           // [KD], and of k
-      float* const row_k = row_q + KD;
-      asm volatile("" : "+s"(ci));                  // (its addresses are not to be kept up to date by the loop above)
-      const T* const base_q = STATE ? nullptr : tq.head(p.q, b, h, 0);
-      const T *const base_k = tk.head(p.k, b, h, 0), *const base_v = tv.head(p.v, b, h, col0);
-      const float* const base_g = p.g + b * p.g_sb + h * p.g_sh;
+      // ---- token by token, with choices in the place of zero factors; the chunks before `from` stand, `done`: that one too
+      if (bad || again) {
+        const int from = STATE ? 0 : bad ? ci : chunks, oes = p.out_f32 ? 4 : int(sizeof(T));
+        if (again) first_state(p, place);
+        float* const row_q = reinterpret_cast<float*>(sh.k);         // [KD], and of k
+        float* const row_k = row_q + KD;
+        const T* const base_q = STATE ? nullptr : tq.head(p.q, b, h, 0);
+        const T *const base_k = tk.head(p.k, b, h, 0), *const base_v = tv.head(p.v, b, h, col0);
+        const float* const base_g = p.g + b * p.g_sb + h * p.g_sh;
 #pragma unroll 1
-      for (; ci < chunks; ++ci) {
-        const int64_t t0 = start_of(ci);
-        const int n = tokens_of(t0);
-        const bool stands = !STATE && done;
+        for (int ci = again ? 0 : from; ci < chunks; ++ci) {
+          const int64_t t0 = place.start_of(ci);
+          const int n = place.tokens_of(t0);
+          const bool stands = !STATE && (ci < from || (ci == from && done));
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          const int64_t t = t0 + (REV ? n - 1 - i : i);
-          lane = lin_lane();
-          tid = 64 * all_wave + lane;
-          l16 = lane & 15;
-          g = lane >> 4;
-          __syncthreads();
-          for (int c = tid; c < KD; c += kThreads) {
-            row_q[c] = !STATE && c < p.kd ? io::widen(base_q[t * p.q.sl + c]) : 0.f;
-            row_k[c] = c < p.kd ? io::widen(base_k[t * p.k.sl + c]) : 0.f;
-          }
-          __syncthreads();
-          const int col = col0 + wcol + l16;
-          const float v = col < p.vd ? io::widen(base_v[t * p.v.sl + wcol + l16]) * p.wscale : 0.f;
-          const double c = double(base_g[t * p.g_sl]) * 1.4426950408889634;
-          const bool start = c < -150.0;
-          const float d = start ? 0.f : lin_decay(float(c));
-          float out = 0.f;
-          if (!stands) {
-#pragma unroll
-            for (int a = 0; a < KK; ++a)
-#pragma unroll
-              for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const int kd = 32 * a + 8 * g + 4 * u + r;
-                  float s = S[a][u][r];
-                  if (!REV) s = start ? 0.f : s * d;
-                  if (kd < p.kd) {
-                    s = fmaf(row_k[kd], v, s);
-                    out = fmaf(row_q[kd], s, out);
-                  }
-                  if (REV) s = start ? 0.f : s * d;
-                  S[a][u][r] = s;
-                }
-          }
-          if (!STATE) {
-            out += __shfl_xor(out, 16);
-            out += __shfl_xor(out, 32);
-            out *= p.fscale;
-            float dot = 0.f;
-            if (!stands && col < p.vd) {
-              if (g == 0) {
-                if (p.out_f32)
-                  reinterpret_cast<float*>(out_at(t))[l16] = out;
-                else
-                  io::narrow(reinterpret_cast<T*>(out_at(t)) + l16, out);
-              }
-              if (DOT) dot = out * io::widen(x_at(t)[l16]);
+          for (int i = 0; i < n; ++i) {
+            const int64_t t = t0 + (REV ? n - 1 - i : i);
+            const int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
+            __syncthreads();
+            for (int c = tid; c < KD; c += kThreads) {
+              row_q[c] = !STATE && c < p.kd ? io::widen(base_q[t * p.q.sl + c]) : 0.f;
+              row_k[c] = c < p.kd ? io::widen(base_k[t * p.k.sl + c]) : 0.f;
             }
-            if constexpr (DOT) {
-              // (what a wavefront whose first chunk stands has left there is that chunk's)
-              for (int x = 8; x > 0; x /= 2) dot += __shfl_xor(dot, x);
-              if (lane == 0 && !stands) sh.dot[all_wave][t - t0] = dot;
-              __syncthreads();
-              if (wave == 0 && lane == 0) {
-                float sum = 0.f;
-                for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][t - t0];
-                p.dot[(nb * p.batch * p.H + bh) * p.L + t] = sum;
+            __syncthreads();
+            const int col = col0 + wcol + l16;
+            const float v = col < p.vd ? io::widen(base_v[t * p.v.sl + wcol + l16]) * p.wscale : 0.f;
+            const double c = double(base_g[t * p.g_sl]) * 1.4426950408889634;
+            const bool start = c < -150.0;
+            const float d = start ? 0.f : lin_decay(float(c));
+            float out = 0.f;
+            if (!stands || again) {
+#pragma unroll
+              for (int a = 0; a < KK; ++a)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) {
+                    const int kd = 32 * a + 8 * g + 4 * u + r;
+                    float s = S[a][u][r];
+                    if (!REV) s = start ? 0.f : s * d;
+                    if (kd < p.kd) {
+                      s = fmaf(row_k[kd], v, s);
+                      out = fmaf(row_q[kd], s, out);
+                    }
+                    if (REV) s = start ? 0.f : s * d;
+                    S[a][u][r] = s;
+                  }
+            }
+            if (!STATE) {
+              out += __shfl_xor(out, 16);
+              out += __shfl_xor(out, 32);
+              out *= p.fscale;
+              float dot = 0.f;
+              if (!stands && col < p.vd) {
+                if (g == 0) {
+                  char* const to = place.out_at(p, t, col, oes);
+                  if (p.out_f32)
+                    *reinterpret_cast<float*>(to) = out;
+                  else
+                    io::narrow(reinterpret_cast<T*>(to), out);
+                }
+                if (DOT) dot = out * io::widen(*place.template x_at<T>(p, t, col));
+              }
+              if constexpr (DOT) {
+                // (what a wavefront whose first chunk stands has left there is that chunk's)
+                for (int x = 8; x > 0; x /= 2) dot += __shfl_xor(dot, x);
+                if (lane == 0 && !stands) sh.dot[all_wave][t - t0] = dot;
+                __syncthreads();
+                if (ci >= from && wave == 0 && lane == 0) {
+                  float sum = 0.f;
+                  for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][t - t0];
+                  p.dot[(place.nb * p.batch * p.H + bh) * p.L + t] = sum;
+                }
               }
             }
           }
         }
-        done = false;
       }
-    }
 
-    if (STATE) {
-      float* const to = p.seg + (bh * p.nseg + seg) * block;
-      each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
-      if (wave == kDecayWave && lane == 0 && nb == 0)
-        p.seg_decay[bh * p.nseg + seg] = anew ? -1.f : lin_decay(float(total));
-    } else if (wanted) {
-      float* const to = p.s1 + bh * block;
-      each_state([&](f32x4& s, int r, int at) { to[at] = s[r]; });
+      const int block = p.kd * p.vd;
+      if (STATE) {
+        store_state(p, col0, p.seg + (bh * p.nseg + place.seg) * block);
+        if (wave == kDecayWave && lin_lane() == 0 && place.nb == 0)
+          p.seg_decay[bh * p.nseg + place.seg] = anew ? -1.f : lin_decay(float(total));
+      } else if (ends) {
+        store_state(p, col0, p.s1 + bh * block);
+      }
     }
   };
 

@@ -32,3 +32,28 @@ def test_bf16_results_are_rounded_once(size, decay):
         for k in ("dq", "dk", "dv"):
             more = size[2] // size[3] * 2.0 ** -24
             lin.near(d[k], ref[k], out * np.abs(ref[k]) + (n + more + 2 * TWO_PARTS) * mag[k], "%s, decay_grad %s" % (k, decay_grad))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("at", ["the chunk's last token", "the sequence's last token", "both directions"])
+@pytest.mark.parametrize("size", [(1, 64, 2, 2, 16, 16), (2, 200, 2, 1, 64, 64), (1, 200, 2, 2, 128, 128), (1, 1500, 2, 1, 64, 130),
+                                  (1, 200, 1, 1, 256, 256)])
+def test_states_up_to_the_largest_value(size, at, io):
+    """States of 3e34 and more behind tokens whose decays add up to 2^-14 and less: within fp32, and kept."""
+    B, L, H, Hk, K, V = size
+    i = inputs(size, io, seed=41)
+    i["g"] = np.full((B, L, H), -0.15, np.float32)
+    token = L - 1 if at == "the sequence's last token" else 63
+    i["k"][:, token, :, 3] = lin.bf(1.0e17, io)
+    i["v"][:, token, :, 5] = lin.bf(3.0e17, io)
+    if at == "both directions":
+        i["q"][:, min(64, L - 1), :, 2] = lin.bf(1.0e17, io)
+        i["do"][:, min(64, L - 1), :, 7] = lin.bf(3.0e17, io)
+        if L == 64:
+            i["k"][:, 63] = i["v"][:, 63] = 0.0                # (the two would meet beyond the largest value)
+        i["S0"][:, :, 2, 7] = i["S0"][:, :, 3, 5] = 0.0
+        i["k"][:, :, :, 2] = i["v"][:, :, :, 7] = 0.0
+    o, last = lin.forward(i, io)
+    lin.check_forward(i, size, io, o, last)
+    if at == "both directions":
+        lin.check_backward(i, size, io, lin.backward(i, io))
