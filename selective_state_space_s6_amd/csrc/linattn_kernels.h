@@ -22,6 +22,7 @@
 // the LDS, are slower (walk 169 us), as are two tiles of k and v in turns in the state pass (no gain).
 #pragma once
 
+#include <cmath>
 #include <type_traits>
 
 #include "device_common.h"
@@ -163,10 +164,14 @@ __device__ __forceinline__ int lin_lane() {
   return int(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, uint32_t(zero))));
 }
 
-// A product of decays that fp32 cannot hold is held at its smallest value: only a token that starts
-// anew ends an infinity.
+// 2^x, its subnormal values too (the instruction gives zero in their place).
+__device__ __forceinline__ float lin_exp2(float x) {
+  return x < -100.f ? __builtin_amdgcn_exp2f(x + 64.f) * 5.421010862e-20f : __builtin_amdgcn_exp2f(x);
+}
+// A token's decay, 2^-150 and more: only a token that starts anew ends an infinity.  (Of finite values, what a product
+// of decays leaves below fp32's smallest value is nothing; one that is not finite is walked token by token.)
 __device__ __forceinline__ float lin_decay(float log2d) {
-  const float d = __builtin_amdgcn_exp2f(log2d);
+  const float d = lin_exp2(log2d);
   return d < kTiny ? kTiny : d;
 }
 
@@ -422,8 +427,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       const double next = scale + all;
       const bool fold = starts != 0 || !(next > -16.0 && next < 16.0);
       const double held = fold ? 0.0 : next;
-      const float f = REV ? (after ? 0.f : lin_decay(float(all - c + scale))) : (before ? 0.f : lin_decay(float(c + scale)));
-      const float w = REV ? (before ? 0.f : lin_decay(float(c - held))) : (after ? 0.f : lin_decay(float(all - c - held)));
+      const float f = REV ? (after ? 0.f : lin_exp2(float(all - c + scale))) : (before ? 0.f : lin_exp2(float(c + scale)));
+      const float w = REV ? (before ? 0.f : lin_exp2(float(c - held))) : (after ? 0.f : lin_exp2(float(all - c - held)));
       if (lane < C) {
         d.hi[lane] = float(c);
         d.lo[lane] = float(c - double(float(c)));
@@ -432,7 +437,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
         d.lim[lane] = REV ? (after ? __builtin_ctzll(after) - 1 : C) : (before ? 63 - __builtin_clzll(before) : 0);
       }
       if (lane == 0) {
-        d.mul = starts ? 0.f : fold ? lin_decay(float(next)) : 1.f;
+        d.mul = starts ? 0.f : fold ? lin_exp2(float(next)) : 1.f;
         d.before = __builtin_amdgcn_exp2f(float(scale));
         d.after = __builtin_amdgcn_exp2f(float(held));
       }
@@ -874,7 +879,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       if (STATE) {
         store_state(p, col0, p.seg + (bh * p.nseg + place.seg) * block);
         if (wave == kDecayWave && lin_lane() == 0 && place.nb == 0)
-          p.seg_decay[bh * p.nseg + place.seg] = anew ? -1.f : lin_decay(float(total));
+          p.seg_decay[bh * p.nseg + place.seg] = anew ? -HUGE_VAL : total;
       } else if (ends) {
         store_state(p, col0, p.s1 + bh * block);
       }

@@ -2,6 +2,8 @@
 // states that enter the segments, sums over shared heads, the decays' gradient) and the decode step.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "device_common.h"
 #include "scan_launch.h"
 
@@ -11,7 +13,8 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 // Memory bounds all of these.  Segment states, from zero, into the states that enter the segments, in place: s := e^c s + own.  A thread has
-// one value of a head's state; eight segments' are asked for at once.
+// one value of a head's state; eight segments' are asked for at once.  The product with a segment's decay is formed in
+// 64 bits, where neither overflows nor vanishes what meets a state that is small, zero or large.
 __global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams fwd, LinParams rev, int blocks) {
   const bool REV = blockIdx.y != 0;
   const LinParams& p = REV ? rev : fwd;
@@ -20,10 +23,11 @@ __global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams fwd, LinParam
   if (at >= block) return;
   float s = p.s0 ? p.s0[bh * block + at] : 0.f;
   float* const ws = p.seg + bh * p.nseg * block + at;
-  const float* const decay = p.seg_decay + bh * p.nseg;
+  const double* const decay = p.seg_decay + bh * p.nseg;
   for (int first = 0; first < p.nseg; first += 8) {
     const int n = p.nseg - first < 8 ? p.nseg - first : 8;
-    float own[8], d[8];
+    float own[8];
+    double d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int k = first + i + 1 < p.nseg ? first + i : 0;        // (nothing was left behind the last segment)
@@ -36,7 +40,10 @@ __global__ __launch_bounds__(256) void lin_prefix_kernel(LinParams fwd, LinParam
       if (i < n) {
         const int seg = REV ? p.nseg - 1 - first - i : first + i;
         ws[int64_t(seg) * block] = s;
-        s = d[i] < 0.f ? own[i] : fmaf(d[i], s, own[i]);
+        // (beyond 2^+-1000 whatever is not zero is infinite, and what is finite vanishes)
+        const double whole = fmin(fmax(rint(d[i]), -1000.0), 1000.0);
+        const double by = ldexp(double(__builtin_amdgcn_exp2f(float(fmax(d[i] - whole, -1.0)))), int(whole));
+        s = d[i] == -HUGE_VAL ? own[i] : float(fma(by, double(s), double(own[i])));
       }
   }
 }

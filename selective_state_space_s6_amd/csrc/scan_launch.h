@@ -304,7 +304,7 @@ struct LinParams {
   float* s1;            // state that it ends with, or null
   int64_t s_row, s_col; // strides of s0 and s1 within a block
   float* seg;           // workspace: [batch][H][nseg] blocks of kd * vd, laid out as s0's
-  float* seg_decay;     // workspace: [batch][H][nseg], negative where the state starts anew
+  double* seg_decay;    // workspace: [batch][H][nseg], log2 of the segment's decay, -infinity where the state starts anew
   LinTensor x;          // dot: out . x per token, [nblk][batch][H][L]; null: not wanted
   float* dot;
   int64_t batch, L, H;

@@ -1378,7 +1378,7 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
     }
     if (p.nseg > 1) {
       p.off_decay = ws_round(f * bh * p.nseg * d.dk * d.dv);
-      p.fwd_bytes = p.off_decay + ws_round(f * bh * p.nseg);
+      p.fwd_bytes = p.off_decay + ws_round(int64_t(sizeof(double)) * bh * p.nseg);
     }
     p.off_rev = p.fwd_bytes;
     size_t off = 2 * p.fwd_bytes;
@@ -1428,7 +1428,7 @@ static selscan::LinParams lin_params(const LinPlan& pl, const selscan::LinTensor
   p.nblk = int32_t(lin_blocks(vd));
   p.pairs = vd <= 64 && q.share % 2 == 0 && k.share % 2 == 0;
   p.seg = static_cast<float*>(ws);
-  p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off_decay);
+  p.seg_decay = reinterpret_cast<double*>(static_cast<char*>(ws) + pl.off_decay);
   return p;
 }
 

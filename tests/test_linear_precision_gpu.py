@@ -57,3 +57,43 @@ def test_states_up_to_the_largest_value(size, at, io):
     lin.check_forward(i, size, io, o, last)
     if at == "both directions":
         lin.check_backward(i, size, io, lin.backward(i, io))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 1500, 2, 1, 64, 64), (1, 1100, 1, 1, 128, 130)])
+def test_segments_that_grow_beyond_the_range(size, io):
+    """Decays of e per token over a segment and more: a state of zeros stays one, and what is finite behind it."""
+    B, L, H, Hk, K, V = size
+    i = inputs(size, io, seed=43)
+    i["g"][:, :400] = 1.0
+    i["k"][:, :400] = 0.0
+    o, last = lin.forward(i, io, S0=False)
+    lin.check_forward(i, size, io, o, last, S0=False)
+    i = inputs(size, io, seed=44)
+    i["g"][:, -400:] = 1.0
+    i["do"][:, -400:] = 0.0
+    d = lin.backward(i, io, dlast=False)
+    n, mixed, out = lin.units(size, io)
+    ref, mag = (orc.linear_bwd(*(j[a] for a in ("q", "k", "v", "g", "do")), i["scale"], j["S0"]) for j in (i, lin.absolute(i)))
+    for k in ("dk", "dv", "dinitial_state"):
+        lin.near(d[k], ref[k], out * np.abs(ref[k]) + (mixed + H / Hk * 2.0 ** -24) * mag[k], k)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 150, 2, 1, 64, 64), (1, 1500, 2, 1, 64, 64), (2, 200, 1, 1, 256, 200)])
+def test_large_states_that_decay(size, io):
+    """A state of 1e36 whose decays leave fp32 is nothing, in a chunk and over segments.  Without keys o is q S0 by a
+    factor.  Where it is subnormal its roundings are half of 2^-149 each, however small it is: that of the decay since the
+    chunk's start, which the scale multiplies, that of the two's product, and as much again for the chunks before: together
+    2^-149 (1 + scale) of what q S0 sums up."""
+    B, L, H, Hk, K, V = size
+    i = inputs(size, io, seed=45)
+    i["k"][:] = 0.0
+    i["g"][:] = -2.0
+    i["S0"] = (1e36 * np.sign(i["S0"])).astype(np.float32)
+    o, last = lin.forward(i, io)
+    (ro, rl), (mo, ml) = (orc.linear_fwd(*(j[a] for a in "qkvg"), i["scale"], j["S0"]) for j in (i, lin.absolute(i)))
+    n, _, out = lin.units(size, io)
+    whole = np.repeat(np.abs(i["q"]).sum(-1), H // Hk, 2)[..., None] * 1e36
+    lin.near(o, ro, out * np.abs(ro) + (n + 2.0 ** -17) * mo + 2.0 ** -149 * (1 + i["scale"]) * whole, "o")
+    lin.near(last, rl, n * ml + 2.0 ** -149 * 1e36, "last_state")
