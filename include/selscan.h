@@ -564,7 +564,7 @@ typedef struct selscan_linattn_dims {
   int32_t abi_version;     /* SELSCAN_ABI_VERSION */
   int32_t io_dtype;        /* enum selscan_dtype: q, k, v, o (and do, dq, dk, dv) */
   int64_t batch;           /* >= 0 */
-  int64_t seqlen;          /* >= 0 */
+  int64_t seqlen;          /* >= 0, below 2^31 */
   int64_t nheads;          /* H >= 1: heads of v and o */
   int64_t qk_heads;        /* heads of q and k, a divisor of nheads */
   int64_t dk;              /* K: 1 .. 256 */
@@ -621,7 +621,8 @@ size_t linear_attention_workspace_size(const selscan_linattn_dims* dims);
  *   workspace      : linear_attention_bwd_workspace_size(dims, dlog_decay != NULL) bytes, as above
  * All outputs are written, never accumulated into; sums run in a fixed order.  Where dlog_decay is
  * wanted, pairs and states keep 24 bits of mantissa in dq and dk, whose products with q and k it sums.
- * nheads * dk and nheads * dv must be at most 2^22 where seqlen is above 1.
+ * batch * nheads * ceil(max(dk, dv) / 64) must be below 2^22, and nheads * dk and nheads * dv at most 2^22
+ * where seqlen is above 1.
  */
 int linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay,
                          const float* initial_state, const void* d_o, const float* dlast_state, void* dq, void* dk,
@@ -637,7 +638,8 @@ size_t linear_attention_bwd_workspace_size(const selscan_linattn_dims* dims, int
  * the states are updated in place.  An id that is negative, or not below `slots`, names no slot; a
  * row whose write id names none is padding: it is skipped, its o is left as it was.  Ids of rows
  * that are written must differ from one another, and a slot that one row writes must not be read by
- * another row of the same call.  o is formed from the new state.  Never allocates.
+ * another row of the same call.  o is formed from the new state.  Never allocates.  batch * nheads * ceil(dv / 64)
+ * must be below 2^22.
  */
 int linear_attention_step(const void* q, const void* k, const void* v, const float* log_decay, void* o, float* state,
                           int64_t slots, const int32_t* read_slots, const int32_t* write_slots,

@@ -1347,7 +1347,8 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
     for (int64_t s : {d.q_sl, d.k_sl, d.v_sl, d.o_sl, d.decay_tokens ? d.g_sl : int64_t(0)})
       if (s > kMaxRow) return SELSCAN_ERR_UNSUPPORTED;
   // workgroups of 256 threads, fewer than 2^32 threads a launch
-  const int64_t kMaxItems = int64_t(1) << 22, wide = d.dk > d.dv ? d.dk : d.dv;
+  // (the columns are those of v, in the backward of q and k too)
+  const int64_t kMaxItems = int64_t(1) << 22, wide = bwd && d.dk > d.dv ? d.dk : d.dv;
   if (d.batch >= kMaxItems || d.nheads >= kMaxItems || d.batch * d.nheads >= kMaxItems ||
       d.batch * d.nheads * ((wide + 63) / 64) >= kMaxItems)
     return SELSCAN_ERR_UNSUPPORTED;

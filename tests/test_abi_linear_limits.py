@@ -1,0 +1,27 @@
+"""The sizes that linear attention takes, as include/selscan.h gives them (no GPU: each call ends at the pointers'
+alignment, which is looked at behind the sizes)."""
+import pytest
+
+import selective_state_space_s6_amd as ss
+from tests.test_abi_linear import ODD, bwd, fwd, lin, step
+
+UNSUPPORTED, ALIGN = -3, -4
+
+
+@pytest.mark.parametrize("batch,H,K,V,takes", [
+    (1 << 20, 1, 256, 64, True), (1 << 20, 1, 256, 256, False), (1 << 20, 1, 64, 256, False), (1 << 20, 3, 200, 1, True),
+    (1 << 21, 1, 256, 65, False), ((1 << 22) - 1, 1, 256, 64, True), (1 << 22, 1, 1, 1, False), (1 << 11, 1 << 10, 256, 64, True)])
+def test_workgroups_of_the_forward_and_the_step(batch, H, K, V, takes):
+    """batch * nheads * ceil(dv / 64) below 2^22, whatever dk is."""
+    want = ALIGN if takes else UNSUPPORTED
+    for io in (ss.SELSCAN_F32, ss.SELSCAN_BF16):
+        assert fwd(lin(io, batch, 5, H, H, K, V), q=ODD) == want
+        assert step(lin(io, batch, 1, H, H, K, V), q=ODD, slots=batch) == want
+
+
+@pytest.mark.parametrize("batch,H,K,V,takes", [
+    (1 << 20, 1, 256, 64, False), (1 << 20, 1, 64, 256, False), (1 << 20, 1, 128, 192, True), (1 << 20, 1, 192, 64, True),
+    ((1 << 22) - 1, 1, 64, 64, True), (1 << 22, 1, 1, 1, False)])
+def test_workgroups_of_the_backward(batch, H, K, V, takes):
+    """batch * nheads * ceil(max(dk, dv) / 64) below 2^22."""
+    assert bwd(lin(ss.SELSCAN_F32, batch, 5, H, H, K, V), q=ODD) == (ALIGN if takes else UNSUPPORTED)
