@@ -918,6 +918,7 @@ hipError_t lin_launch(LinWalk walk, const LinParams* p, hipStream_t stream) {
     case LinWalk::states: lin_kernel<T, KD, NW, HP, LinWalk::states><<<both, threads, 0, stream>>>({{p[0], p[1]}}); break;
     case LinWalk::grads:
       // (do and v, the queries and keys of these walks, are each head's own)
+      if constexpr (HP > 1) return hipErrorInvalidValue;
       if constexpr (HP == 1) lin_kernel<T, KD, NW, 1, LinWalk::grads><<<both, threads, 0, stream>>>({{p[0], p[1]}});
       break;
   }
