@@ -619,8 +619,16 @@ size_t linear_attention_workspace_size(const selscan_linattn_dims* dims);
  *                    or NULL.  Zero where the state starts anew.
  *   dinitial_state : [batch][nheads][dk][dv] fp32, or NULL; it and dlast_state may be one buffer
  *   workspace      : linear_attention_bwd_workspace_size(dims, dlog_decay != NULL) bytes, as above
- * All outputs are written, never accumulated into; sums run in a fixed order.  Where dlog_decay is
- * wanted, pairs and states keep 24 bits of mantissa in dq and dk, whose products with q and k it sums.
+ * All outputs are written, never accumulated into; sums run in a fixed order.  No other gradient goes by
+ * whether dlog_decay is wanted; pairs keep 16 bits of mantissa with bf16 I/O, states 24 in dq and dk and 16 in dv.
+ * dlog_decay_t sums what passes token t, products of a key and a row of v before it, a query and a row of do from it
+ * on, and the decays between, in fp32 and over chunks in 64 bits.  It is off by some 2^-24 of the magnitudes of these
+ * addends, and of those of the tokens up to 512 behind t (fp32 wider than 128: 256) if the decays of these are above 1/64.
+ * It is finite wherever all that passes t is.
+ * The workspace holds 2 batch seqlen nheads dk fp32 values where nheads is not qk_heads (each head's own dq and dk),
+ * and for dlog_decay 9/8 of a dk x dv state for every 64 (32) tokens of a head, of which what lies between every eighth is
+ * used by strong decays only: 2.7 and 1.5 GB for 4 x 8192 tokens of 80 heads on one, 128 x 64.
+ * With dlog_decay, ceil(seqlen / 512) (256) batch nheads ceil(max(dk, dv) / 64) must be below 2^23.
  * batch * nheads * ceil(max(dk, dv) / 64) must be below 2^22, and nheads * dk and nheads * dv at most 2^22
  * where seqlen is above 1.
  */

@@ -62,6 +62,61 @@ def linear_bwd(q, k, v, g, do, scale=1.0, S0=None, dlast=None):
     return dict(dq=share(dq), dk=share(dk), dv=dv, dlog_decay=dg, dinitial_state=R)
 
 
+def linear_decay_parts(q, k, v, g, do, scale=1.0, S0=None, dlast=None, chunk=64):
+    """dlog_decay [B, L, H] by chunks, what passes a token's decay: "pairs" of its chunk that lie on both sides of it;
+    sums over "x" [B, L, H] from it on, of the state S before the chunk with the chunk's tokens; sums over "y" before it,
+    of the chunk's tokens with the gradient R behind the chunk; "through" [B, chunks, H], S with R.  Also
+    "starts", whether any token of a chunk starts anew, "log2" of its decay and "least" of its tokens'; "beside", <S, R> behind
+    each chunk."""
+    B, L, H, V = v.shape
+    qh, kh, v, do = _heads(q, H), _heads(k, H), np.asarray(v, np.float64), np.asarray(do, np.float64)
+    a, start = _decays(g, B, L, H)
+    K, n = qh.shape[-1], -(-L // chunk)
+    S = np.zeros((B, H, K, V)) if S0 is None else np.asarray(S0, np.float64)
+    R = np.zeros((B, H, K, V)) if dlast is None else np.asarray(dlast, np.float64)
+    at_start, at_end = [], [None] * n
+    for t in range(L):
+        if t % chunk == 0:
+            at_start.append(S)
+        S = _kept(a[:, t], start[:, t], S) + kh[:, t, :, :, None] * v[:, t, :, None, :]
+    at_start.append(S)
+    for t in range(L - 1, -1, -1):
+        if t == L - 1 or (t + 1) % chunk == 0:
+            at_end[t // chunk] = R
+        R = _kept(a[:, t], start[:, t], R + scale * qh[:, t, :, :, None] * do[:, t, :, None, :])
+    out = {k: np.zeros((B, L, H)) for k in ("pairs", "x", "y")}
+    out.update({k: np.zeros((B, n, H)) for k in ("through", "log2", "least", "beside")}, starts=np.zeros((B, n, H), bool))
+    for c in range(n):
+        r = slice(c * chunk, min(L, (c + 1) * chunk))
+        m = r.stop - r.start
+        begins = start[:, r].cumsum(1)                        # how often it has begun, per token
+        with np.errstate(divide="ignore"):
+            log = np.where(start[:, r], 0.0, np.log(np.where(start[:, r], 1.0, a[:, r]))).cumsum(1)
+        P = np.exp(np.minimum(log[:, :, None] - log[:, None], 700.0)) * (begins[:, :, None] == begins[:, None])
+        P *= np.tril(np.ones((m, m)))[None, :, :, None]
+        f = np.exp(log) * (begins == 0)
+        w = np.exp(log[:, -1:] - log) * (begins == begins[:, -1:])
+        M = scale * P * np.einsum("bihk,bjhk->bijh", qh[:, r], kh[:, r]) * np.einsum("bihv,bjhv->bijh", do[:, r], v[:, r])
+        for t in range(m):
+            out["pairs"][:, r.start + t] = M[:, t:, :t].sum((1, 2))
+        out["x"][:, r] = scale * f * np.einsum("bihk,bhkv,bihv->bih", qh[:, r], at_start[c], do[:, r])
+        out["y"][:, r] = w * np.einsum("bjhk,bhkv,bjhv->bjh", kh[:, r], at_end[c], v[:, r])
+        out["starts"][:, c] = start[:, r].any(1)
+        out["log2"][:, c] = log[:, -1] * np.log2(np.e)
+        with np.errstate(divide="ignore"):
+            out["least"][:, c] = np.log2(np.where(start[:, r], 1.0, a[:, r])).min(1)
+        out["through"][:, c] = np.where(out["starts"][:, c], 0.0, np.exp(log[:, -1]) * (at_start[c] * at_end[c]).sum((-1, -2)))
+        out["beside"][:, c] = (at_start[c + 1] * at_end[c]).sum((-1, -2))
+    total = np.array(out["pairs"])
+    for c in range(n):
+        r = slice(c * chunk, min(L, (c + 1) * chunk))
+        x, y = out["x"][:, r], out["y"][:, r]
+        total[:, r] += x[:, ::-1].cumsum(1)[:, ::-1] + out["through"][:, c:c + 1]
+        total[:, r.start + 1:r.stop] += y[:, :-1].cumsum(1)
+    out["dlog_decay"] = np.where(start, 0.0, total)
+    return out
+
+
 def linear_step(q, k, v, g, S, scale=1.0):
     """One token from states S [B, H, K, V]: (o [B, H, V], new states)."""
     o, S = linear_fwd(q[:, None], k[:, None], v[:, None], np.broadcast_to(g, v.shape[:2])[:, None], scale, S)

@@ -1040,8 +1040,8 @@ def linear_attention_bwd(q, k, v, log_decay, *, do, scale: float = 1.0, initial_
                          decay_grad: bool = True, workspace=None, stream=None) -> dict:
     """Gradients of linear_attention_fwd (same inputs and options) given do ([batch, L, H, V]) and
     optionally dlast_state.  Returns a dict of contiguous tensors: dq, dk, dv in q's dtype; dlog_decay
-    (unless decay_grad is False) in log_decay's shape and, with an initial_state, dinitial_state in
-    float32."""
+    (unless decay_grad is False, which leaves the others as they are) in log_decay's shape and, with an
+    initial_state, dinitial_state in float32."""
     import torch
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must be [batch, L, heads, width]")

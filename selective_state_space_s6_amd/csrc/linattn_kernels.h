@@ -26,104 +26,11 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "linattn_device.h"
 #include "scan_launch.h"
 
 namespace selscan {
 namespace {
-
-typedef __attribute__((ext_vector_type(2))) float f32x2;
-typedef __attribute__((ext_vector_type(4))) float f32x4;
-typedef __attribute__((ext_vector_type(8))) float f32x8;
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-
-constexpr float kTiny = 1.401298464e-45f;      // 2^-149
-constexpr int kNowhere = 0x3ffffff0;            // a place in bytes beyond any state, another state's added to it too
-
-// Place of (row, column) in an LDS tile of W columns.  A row's 16-byte pieces are exchanged with one another by
-// bits of the row, so that both ways of reading spread over the banks: sixteen rows of one column of
-// pieces, and four neighbouring rows of four neighbouring pieces.  (Rows of 128 bytes share 256 in pairs.)
-template <typename T, int W> __device__ __forceinline__ int lin_at(int row, int col) {
-  constexpr int V = 16 / int(sizeof(T)), kPieces = W / V;
-  static_assert(kPieces >= 8, "");
-  const int f = kPieces >= 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-  return row * W + ((col / V) ^ f) * V + col % V;
-}
-
-// Place of the pairs of row i and keys j .. in their tile: of the 16 x 16 blocks only those that see each other are
-// kept, by rows of blocks (the backward's mirrored, `it` and `jt` counted from the end).  A row of fp32 has four 16-byte pieces, exchanged by bits
-// of the row; one of bf16 has two, and a block's sixteen rows lie on all banks as they are.
-template <typename T> __device__ __forceinline__ int lin_pair_at(int it, int jt, int row, int col) {
-  constexpr int V = 16 / int(sizeof(T)), f = sizeof(T) == 4 ? 3 : 0;
-  return ((it * (it + 1) / 2 + jt) * 16 + row) * 16 + ((col / V) ^ ((row >> 2) & f)) * V + col % V;
-}
-
-// What the walk needs of an element type: eight consecutive values of a contraction in one
-// fragment (lane l: row or column l % 16, values 8 (l / 16) ..), and the product of two.
-template <typename T> struct lin_io;
-template <> struct lin_io<uint16_t> {
-  using frag = bf16x8;
-  static constexpr int kVec = 8;               // elements of 16 bytes
-  static __device__ __forceinline__ f32x4 mma(frag a, frag b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-  // a column: values at rows r0 .. r0 + 7 of a tile; the 16 lanes of a group ask for 4 rows of four 4-element
-  // pieces (lane i: row i / 4, piece i % 4), and the transposing read hands each lane its column
-  template <int W>
-  static __device__ __forceinline__ frag column(const uint16_t* tile, int r0, int first, int spread, int l16) {
-    const int col = first + spread * (l16 & 3), r = r0 + (l16 >> 2);
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(tile + lin_at<uint16_t, W>(r, col)));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(tile + lin_at<uint16_t, W>(r + 4, col)));
-    struct { s16x4 a, b; } v = {a, b};
-    return __builtin_bit_cast(frag, v);
-  }
-  template <int W> static __device__ __forceinline__ frag row(const uint16_t* tile, int r, int c) {
-    return *reinterpret_cast<const frag*>(tile + lin_at<uint16_t, W>(r, c));
-  }
-  static __device__ __forceinline__ frag pair(const uint16_t* tile, int at) { return *reinterpret_cast<const frag*>(tile + at); }
-  static __device__ __forceinline__ f32x8 wide(frag a) { return __builtin_convertvector(a, f32x8); }
-  static __device__ __forceinline__ frag round(f32x8 a) { return __builtin_convertvector(a, frag); }
-  static __device__ __forceinline__ void narrow(uint16_t* p, float v) { *p = bf16_rne(v); }
-  static __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
-  static __device__ __forceinline__ void store(uint16_t* p, f32x4 v) { *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4); }
-};
-template <> struct lin_io<float> {
-  using frag = f32x8;
-  static constexpr int kVec = 4;
-  static __device__ __forceinline__ f32x4 mma(frag a, frag b, f32x4 c) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-    return c;
-  }
-  template <int W> static __device__ __forceinline__ frag row(const float* tile, int r, int c) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(tile + lin_at<float, W>(r, c));
-    const f32x4 b = *reinterpret_cast<const f32x4*>(tile + lin_at<float, W>(r, c + 4));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-  template <int W>
-  static __device__ __forceinline__ frag column(const float* tile, int r0, int first, int spread, int l16) {
-    const int col = first + spread * (l16 >> 2) + (l16 & 3);
-    frag v;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = tile[lin_at<float, W>(r0 + e, col)];
-    return v;
-  }
-  static __device__ __forceinline__ frag pair(const float* tile, int at) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(tile + at);
-    const f32x4 b = *reinterpret_cast<const f32x4*>(tile + (at ^ 4));       // (the piece beside it)
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-  static __device__ __forceinline__ f32x8 wide(frag a) { return a; }
-  static __device__ __forceinline__ frag round(f32x8 a) { return a; }
-  static __device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
-  static __device__ __forceinline__ float widen(float b) { return b; }
-  static __device__ __forceinline__ void store(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
-};
 
 // x as a sum of N values of the matrix cores' type (the first rounds x, the next what that left).  Where x is
 // not finite, neither is the sum.
@@ -156,29 +63,12 @@ __device__ __forceinline__ void lin_split(f32x8 x, typename lin_io<T>::frag* out
 // What rounding to bfloat16 leaves of a value.
 __device__ __forceinline__ float lin_rest(float v) { return v - float(__bf16(v)); }
 
-// The lane's number, formed anew wherever it is asked for: kept, what is formed of it (places in tiles and
-// tensors) would not leave the walk's registers room.
-__device__ __forceinline__ int lin_lane() {
-  int zero = 0;
-  asm volatile("" : "+s"(zero));
-  return int(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, uint32_t(zero))));
-}
-
-// 2^x, its subnormal values too (the instruction gives zero in their place).
-__device__ __forceinline__ float lin_exp2(float x) {
-  return x < -100.f ? __builtin_amdgcn_exp2f(x + 64.f) * 5.421010862e-20f : __builtin_amdgcn_exp2f(x);
-}
 // A token's decay, 2^-150 and more: only a token that starts anew ends an infinity.  (Of finite values, what a product
 // of decays leaves below fp32's smallest value is nothing; one that is not finite is walked token by token.)
 __device__ __forceinline__ float lin_decay(float log2d) {
   const float d = lin_exp2(log2d);
   return d < kTiny ? kTiny : d;
 }
-
-// Tokens of a chunk: the LDS of a compute unit holds the tiles of a chunk of 64, but not those of 256
-// fp32 channels.  (Chunks of 32 for all of fp32, two workgroups a compute unit: 2 x 16 heads x 4096, 64 x 64, 79 us in
-// the place of 80; 128 x 128, whose registers then spill, 231 in the place of 198.)
-template <typename T, int KD> constexpr int lin_chunk_of() { return sizeof(T) == 4 && KD == 256 ? 32 : 64; }
 
 // Wavefronts that a SIMD is to hold, NW of them a workgroup: as many as the LDS of a compute unit holds tiles for.
 template <typename T, int KD, int NW, bool DOT> constexpr int lin_waves() {
@@ -194,92 +84,18 @@ template <int C> struct alignas(16) LinDecays {
   float before, after;      // the held state's scale before the chunk, and behind it
 };
 
-template <typename T, int KD, int NW, int HP, bool STATE, bool DOT>
+template <typename T, int KD, int NW, int HP, int C, bool STATE, bool DOT>
 struct alignas(16) LinShared {
-  static constexpr int NPP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2;   // parts of the pairs on the matrix cores
-  static constexpr int C = lin_chunk_of<T, KD>(), IT = C / 16, kPairs = IT * (IT + 1) / 2 * 256;
+  static constexpr int NPP = sizeof(T) == 4 ? 1 : 2;      // parts of the pairs on the matrix cores
+  static constexpr int IT = C / 16, kPairs = IT * (IT + 1) / 2 * 256;
   T q[STATE ? 8 : C * KD];
   T k[C * KD];
   T v[C * 16 * NW];
   T p[STATE ? 8 : HP * NPP * kPairs + 8];                          // (8 zeros behind them)
   LinDecays<C> dec[HP][2];  // this chunk's, and the next one's
   float dot[DOT ? NW : 1][DOT ? C : 1];
+  float cross[NW];
   int bad;
-};
-
-// An operand's tile of C rows and W columns on its way: the n tokens of a chunk, zeros elsewhere.  A
-// thread has 16-byte pieces of a row (on any element's boundary).  Where the width is not a multiple of a
-// piece, the last one is read so that it ends where the row does, and its values are moved when they are
-// stored; rows shorter than a piece are read element by element then.
-// (What a call forms of `tid`, it forms again at each chunk: kept, it would not leave the registers room.)
-template <typename T, int W, int C, int THREADS>
-struct LinTile {
-  static constexpr int V = lin_io<T>::kVec, kPieces = W / V, kRows = THREADS / kPieces, N = C / kRows;
-  static_assert(N >= 1 && N * kRows == C, "");
-  static constexpr int kOutside = 0x7ffffff0;    // beyond any tile: reads as zero
-  u32x4 piece[N];
-  const T* at;            // the next chunk's first token
-  int sl, cols;
-  bool even;
-
-  static __device__ __forceinline__ const T* head(const LinTensor& x, int64_t b, int64_t h, int col0) {
-    return static_cast<const T*>(x.p) + b * x.sb + (h / x.share) * x.sh + col0;
-  }
-  __device__ __forceinline__ void init(const LinTensor& x, int64_t b, int64_t h, int64_t t0, int col0, int width) {
-    at = head(x, b, h, col0) + t0 * x.sl;
-    sl = int(x.sl);
-    cols = width - col0 < W ? width - col0 : W;
-    even = cols % V == 0;
-  }
-  // asks for the pieces of a chunk and goes on to the next
-  template <bool REV> __device__ __forceinline__ void load(int tid, int n) {
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), (short)0,
-                                                        ((n - 1) * sl + cols) * int(sizeof(T)), 0x00020000);
-    const int row0 = tid / kPieces, step = kRows * sl * int(sizeof(T));
-    int c = (tid % kPieces) * V;
-    const bool in = c < cols;
-    if (c + V > cols) c = cols - V;
-    const int to = in && c >= 0 ? (row0 * sl + c) * int(sizeof(T)) : kOutside;
-    if (n == C) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, to + i * step, 0, 0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        piece[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, row0 + i * kRows < n ? to + i * step : kOutside, 0, 0);
-    }
-    at += (REV ? -int64_t(C) : int64_t(C)) * sl;
-  }
-  // ... and their place in the tile; `now`: the chunk's first token
-  __device__ __forceinline__ void store(T* tile, int tid, const T* now, int n) {
-    const int row0 = tid / kPieces, c = (tid % kPieces) * V;
-    if (!even) {
-      int cols = this->cols;
-      asm volatile("" : "+s"(cols));
-      const int by = (V - cols % V) * int(sizeof(T));
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        u32x4 x = piece[i];
-        if (by & 2) x = u32x4{(x[0] >> 16) | (x[1] << 16), (x[1] >> 16) | (x[2] << 16), (x[2] >> 16) | (x[3] << 16), x[3] >> 16};
-        if (by & 4) x = u32x4{x[1], x[2], x[3], 0};
-        if (by & 8) x = u32x4{x[2], x[3], 0, 0};
-        if (c + V > cols) piece[i] = x;           // the end of a row: down by V - cols % V values
-      }
-      if (cols < V) {
-        if (c == 0)
-#pragma unroll 1
-          for (int i = 0; i < N; ++i)
-#pragma unroll 1
-            for (int e = 0; e < V; ++e) {
-              const int row = row0 + i * kRows;
-              tile[lin_at<T, W>(row, e)] = e < cols && row < n ? now[int64_t(row) * sl + e] : T(0);
-            }
-        if (c == 0) return;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + lin_at<T, W>(row0 + i * kRows, c)) = piece[i];
-  }
 };
 
 template <LinWalk WALK> struct LinWalks { LinParams p[WALK == LinWalk::states || WALK == LinWalk::grads ? 2 : 1]; };
@@ -323,30 +139,45 @@ template <int C, int HP, int COLS, bool STATE, bool REV> struct LinPlace {
 // queries and keys, for 16 NW / HP columns of v each: a wavefront owns 16 of them, and the state's [KD][16] in
 // its accumulators, which are at once the operand of its product with the queries.
 // STATE: only the state at the segment's end, from zero.
-// DOT: the rows' products with x too.  The decays' gradient is what remains of their sum over all later tokens in
-// one walk less that in the other, so pairs and state then go to the matrix cores with 24 bits.  Else both go
-// there with 16, twice the result's own (pairs of 8 bits would add as much again to its rounding).
-template <typename T, int KD, int NW, int HP, LinWalk WALK>
+// DOT: the products of x with the rows' parts of the state too, the state between every lin_span() chunks, and a mark for
+// chunks that need it themselves (lin_between_kernel).  For the spans that have one, with a span in a segment's place:
+// KEEP: only the state before each chunk.  CROSS: only its products with the backward walk's behind the chunk.
+// bf16: pairs and state go to the matrix cores with 16 bits, twice the result's own (pairs of 8 bits would add as
+// much again to its rounding), the state with 24 where its products give the decays' gradient, an fp32 result.
+template <typename T, int KD, int NW, int HP, int C, LinWalk WALK>
 __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::grads>())) void lin_kernel(LinWalks<WALK> walks) {
-  constexpr bool STATE = WALK == LinWalk::state || WALK == LinWalk::states, DOT = WALK == LinWalk::grads;
+  constexpr bool CROSS = WALK == LinWalk::cross, KEEP = WALK == LinWalk::keep;
+  constexpr bool STATE = WALK == LinWalk::state || WALK == LinWalk::states || CROSS || KEEP, OWN = STATE && !CROSS && !KEEP;
+  constexpr bool DOT = WALK == LinWalk::grads;
   using io = lin_io<T>;
   using frag = typename io::frag;
   constexpr int NP = sizeof(T) == 4 ? 1 : DOT ? 3 : 2;   // parts of the state on the matrix cores
   constexpr bool kBoth = WALK == LinWalk::states || WALK == LinWalk::grads;
   constexpr int NX = sizeof(T) == 2 ? 3 : 1;      // the state is held in fp32: what is added to it keeps 24 bits
-  using Sh = LinShared<T, KD, NW, HP, STATE, DOT>;
+  using Sh = LinShared<T, KD, NW, HP, C, STATE, DOT>;
   constexpr int NPP = Sh::NPP;
   __shared__ Sh sh;
 
+  if constexpr (KEEP || CROSS) {
+    // nothing to do where no chunk has a mark
+    const LinParams& p = walks.p[0];
+    const int item = xcd_contiguous_block(blockIdx.x, gridDim.x), heads = int(p.H) / HP, seg = item / heads / p.nblk % p.nseg;
+    const int64_t bh = int64_t(item / heads / p.nblk / p.nseg) * p.H + item % heads * HP, chunk0 = int64_t(seg) * p.seg_chunks;
+    const int each = int(p.nchunks - chunk0 < p.seg_chunks ? p.nchunks - chunk0 : p.seg_chunks) * p.marks_each;
+    int any = 0;
+    for (int i = threadIdx.x; i < 2 * HP * each; i += 64 * NW)
+      any |= p.marks[(((i / each & 1) * p.batch * p.H + bh + i / each / 2) * p.nchunks + chunk0) * p.marks_each + i % each];
+    if (!__syncthreads_or(any)) return;
+  }
   auto segment = [&](auto reversed, const LinParams& p, const int item) __attribute__((always_inline)) {
     constexpr bool REV = decltype(reversed)::value;
     constexpr int kWaves = NW / HP;                 // of a head
-    constexpr int C = Sh::C, KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kPairs = Sh::kPairs, kThreads = 64 * NW;
+    constexpr int KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kPairs = Sh::kPairs, kThreads = 64 * NW;
     constexpr int kDecayWave = kWaves - 1;          // has the least to do with the pairs
 
     const int all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), part = all_wave / kWaves, wave = all_wave % kWaves;
     int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
-    using Place = LinPlace<C, HP, kWV, STATE, REV>;
+    using Place = LinPlace<C, HP, kWV, OWN, REV>;
     const Place place(p, item, part);
     const int nb = place.nb, chunks = place.chunks, col0 = place.col0, wcol = wave * 16;
     const int64_t h = place.h, b = place.b, bh = place.bh;
@@ -354,9 +185,10 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     f32x4 S[KK][2];
     // f(four state values, which of them, its place in a head's state in bytes): beyond the state for what is not there, where loads give
     // zero and stores are dropped
-    auto each_state = [&](const LinParams& p, int col0, auto&& f) __attribute__((always_inline)) {
-      const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4, n = col0 + wcol + l16;
-      const int row = 4 * int(p.s_row), col = n < p.vd ? 4 * int(p.s_col) * n : kNowhere, left = p.kd - 8 * g;
+    auto each_state = [&](const LinParams& p, int col0, int row, int col, auto&& f) __attribute__((always_inline)) {
+      const int lane = lin_lane(), l16 = lane & 15, g = lane >> 4, n = col0 + wcol + l16, left = p.kd - 8 * g;
+      row *= 4;
+      col = n < p.vd ? 4 * col * n : kNowhere;
 #pragma unroll
       for (int a = 0; a < KK; ++a)
 #pragma unroll
@@ -367,16 +199,14 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
             f(S[a][u], r, kd < left ? row * (8 * g + kd) + col : kNowhere);
           }
     };
-    auto state_at = [](const float* at, const LinParams& p) {
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(at), (short)0, at ? p.kd * p.vd * 4 : 0, 0x00020000);
-    };
-    auto load_state = [&](const LinParams& p, int col0, const float* at) __attribute__((always_inline)) {
-      const auto from = state_at(at, p);
-      each_state(p, col0, [&](f32x4& s, int r, int at) { s[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, at, 0, 0)); });
+    auto load_state = [&](const LinParams& p, int col0, const float* at, int row, int col, int size) __attribute__((always_inline)) {
+      const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(at), (short)0, size * 4, 0x00020000);
+      each_state(p, col0, row, col, [&](f32x4& s, int r, int at) { s[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, at, 0, 0)); });
     };
     auto store_state = [&](const LinParams& p, int col0, float* at) __attribute__((always_inline)) {
-      const auto to = state_at(at, p);
-      each_state(p, col0, [&](f32x4& s, int r, int at) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s[r]), to, at, 0, 0); });
+      const auto to = __builtin_amdgcn_make_buffer_rsrc(at, (short)0, p.kd * p.vd * 4, 0x00020000);
+      each_state(p, col0, int(p.s_row), int(p.s_col),
+                 [&](f32x4& s, int r, int at) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s[r]), to, at, 0, 0); });
     };
 
     auto start_of = [&](int ci) { return place.start_of(ci); };
@@ -410,10 +240,14 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     // chunks' decays until it leaves 2^-16 .. 2^16: most chunks then leave the accumulators as they are.
     double scale = 0.0;
     // the factors of a chunk's tokens, of the gates that kDecayWave has loaded
-    auto decays = [&](LinDecays<C>& d) {
+    auto mark = [&](const LinParams& p, const Place& place, int64_t chunk, bool marked) {
+      p.marks[(((REV ? p.batch * p.H : 0) + place.bh) * p.nchunks + chunk) * p.nblk + place.nb] = marked;
+    };
+    auto decays = [&](LinDecays<C>& d, int64_t chunk) {
       const int lane = lin_lane();
       double c = double(gate) * 1.4426950408889634;
       const bool start = c < -150.0;                // a decay below 2^-150 is none at all
+      const bool any_strong = DOT && !REV && __ballot(c < kStrong) != 0;
       if (start) c = 0.0;
 #pragma unroll
       for (int s = 1; s < 64; s *= 2) {
@@ -442,6 +276,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
         d.after = __builtin_amdgcn_exp2f(float(held));
       }
       scale = held;
+      if (DOT && p.marks && lane == 0)
+        mark(p, place, chunk, !REV && starts == 0 && all > kGone && any_strong && (chunk > 0 || p.ends & 1) && (chunk + 1 < p.nchunks || p.ends & 2));
       if (STATE) {
         total += all;
         anew |= starts != 0;
@@ -507,17 +343,17 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     auto from_state = [&](const LinDecays<C>& dec) {
 #pragma unroll
       for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
-      constexpr int kHalf = IT / 2;
+      constexpr int kTwo = IT / 2;
       frag fq[2][2], fs[NP];
       auto ask = [&](int i) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) fq[i & 1][x] = io::template row<KD>(sh.q, 16 * (2 * (i % kHalf) + x) + l16, 32 * (i / kHalf) + 8 * g);
+        for (int x = 0; x < 2; ++x) fq[i & 1][x] = io::template row<KD>(sh.q, 16 * (2 * (i % kTwo) + x) + l16, 32 * (i / kTwo) + 8 * g);
       };
       ask(0);
 #pragma unroll
-      for (int i = 0; i < KK * kHalf; ++i) {
-        const int a = i / kHalf, it = 2 * (i % kHalf);
-        if (i + 1 < KK * kHalf) ask(i + 1);
+      for (int i = 0; i < KK * kTwo; ++i) {
+        const int a = i / kTwo, it = 2 * (i % kTwo);
+        if (i + 1 < KK * kTwo) ask(i + 1);
         __builtin_amdgcn_sched_barrier(0);
         if (there(a)) {
           if (it == 0) lin_split<T, NP>(__builtin_shufflevector(S[a][0], S[a][1], 0, 1, 2, 3, 4, 5, 6, 7), fs);
@@ -610,6 +446,84 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
         }
       }
     };
+    // the products of x with what a row has of the state
+    auto dots = [&] {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        float sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x = sizeof(T) == 4 ? __uint_as_float(xv[it][r % kXRegs])
+                                         : __uint_as_float(r % 2 ? xv[it][r / 2] & 0xffff0000u : xv[it][r / 2] << 16);
+          sum = fmaf(acc[it][r], x, sum);
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (g == 0) sh.dot[all_wave][16 * it + l16] = sum;
+      }
+    };
+    // A state kept at `to`, a block of [the walk of dq's rows][c_row]: a lane of the backward walk, whose rows and columns are
+    // exchanged, then has four values in one access.
+    auto kept_at = [&](const LinParams& p, float* at) {
+      return __builtin_amdgcn_make_buffer_rsrc(at, (short)0, int(CROSS ? p.vd : p.kd) * int(p.c_row) * 4, 0x00020000);
+    };
+    auto keep = [&](const LinParams& p, const Place& place, float* at, float scale) __attribute__((always_inline)) {
+      const auto to = kept_at(p, at);
+      const int lane = lin_lane(), n = place.col0 + wcol + (lane & 15), kd0 = 8 * (lane >> 4), row = 4 * int(p.c_row);
+      const int off = n < int(p.c_row) ? row * kd0 + 4 * n : kNowhere;
+#pragma unroll
+      for (int a = 0; a < KK; ++a)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(n < p.vd ? __float_as_uint(S[a][u][r] * scale) : 0u, to, off + row * (32 * a + 4 * u + r), 0, 0);
+    };
+    auto kept_block = [&](const LinParams& p, const Place& place, int64_t chunk) {
+      return p.kept + (place.bh * p.nchunks + chunk) * (int64_t(CROSS ? p.vd : p.kd) * p.c_row);
+    };
+    // what a walk keeps before chunk `chunk` of its direction: the states between every lin_span() chunks, or (KEEP) the others
+    auto keep_some = [&](const LinParams& p, const Place& place, int64_t chunk, float scale) __attribute__((always_inline)) {
+      if (KEEP || (DOT && !REV)) {
+        if ((chunk % lin_span() == 0) != KEEP) keep(p, place, kept_block(p, place, chunk), scale);
+      } else if (DOT && (chunk + 1) % lin_span() == 0 && chunk + 1 < p.nchunks) {
+        keep(p, place, p.back + (place.bh * ((p.nchunks + lin_span() - 1) / lin_span()) + (chunk + 1) / lin_span()) * (int64_t(p.kd) * p.c_row), scale);
+      }
+    };
+    // ... and the sum of its products with the walk's
+    f32x4 kept[CROSS ? KK : 1][2];
+    auto load_kept = [&](const LinParams& p, const Place& place, int64_t chunk, int half) __attribute__((always_inline)) {
+      const auto from = kept_at(p, kept_block(p, place, chunk));
+      const int lane = lin_lane(), n = place.col0 + wcol + (lane & 15), kd0 = 8 * (lane >> 4);
+      const int at = n < p.vd ? 4 * (n * int(p.c_row) + kd0) : kNowhere;
+#pragma unroll
+      for (int a = KK / 2 * half; a < KK / 2 * (half + 1); ++a)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          kept[a][u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at + 4 * (32 * a + 4 * u), 0, 0));
+    };
+    auto cross = [&](const LinParams& p, float scale) __attribute__((always_inline)) {
+      const int left = p.kd - 8 * (lin_lane() >> 4);
+      float sum = 0.f;
+#pragma unroll
+      for (int a = 0; a < KK; ++a)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = kept[a][u][r];
+            sum = fmaf(32 * a + 4 * u + r < left ? x : 0.f, S[a][u][r] * scale, sum);      // (behind a row's end lies the next one)
+          }
+#pragma unroll
+      for (int x = 32; x > 0; x /= 2) sum += __shfl_xor(sum, x);
+      if (lin_lane() == 0) sh.cross[all_wave] = sum;
+    };
+    auto store_cross = [&](const LinParams& p, const Place& place, int64_t chunk) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) sum += sh.cross[part * kWaves + w];
+      if (lin_lane() == 0) p.cross[(place.nb * p.batch * p.H + place.bh) * p.nchunks + chunk] = sum;
+    };
     auto write = [&](int n) {
       constexpr int kOutside = 0x7ffffff0;
       const int room = ocols - 4 * g;               // columns that are there
@@ -641,21 +555,6 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
                 __builtin_amdgcn_raw_buffer_store_b16((short)bf16_rne(acc[it][r]), rsrc, one, 0, 0);
             }
           }
-        }
-      }
-      if constexpr (DOT) {                          // out_i . x_i, for the decays' gradient
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-          float sum = 0.f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float x = sizeof(T) == 4 ? __uint_as_float(xv[it][r % kXRegs])
-                                           : __uint_as_float(r % 2 ? xv[it][r / 2] & 0xffff0000u : xv[it][r / 2] << 16);
-            sum = fmaf(acc[it][r], x, sum);
-          }
-          sum += __shfl_xor(sum, 16);
-          sum += __shfl_xor(sum, 32);
-          if (g == 0) sh.dot[all_wave][16 * it + l16] = sum;
         }
       }
     };
@@ -700,7 +599,26 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
 
     auto first_state = [&](const LinParams& p, const Place& place) __attribute__((always_inline)) {
       const int block = p.kd * p.vd;                // of a head's state
-      load_state(p, place.col0, STATE ? nullptr : p.nseg > 1 ? p.seg + (place.bh * p.nseg + place.seg) * block : p.s0 ? p.s0 + place.bh * block : nullptr);
+      const float* from = p.s0 ? p.s0 + place.bh * block : nullptr;
+      int row = int(p.s_row), col = int(p.s_col), size = block;
+      if (OWN) {
+        from = nullptr;
+      } else if (KEEP || CROSS) {
+        if (place.seg != (CROSS ? p.nseg - 1 : 0)) {
+          row = CROSS ? 1 : int(p.c_row);
+          col = CROSS ? int(p.c_row) : 1;
+          size = (CROSS ? p.vd : p.kd) * int(p.c_row);
+          from = CROSS ? p.back + (place.bh * p.nseg + place.seg + 1) * size : p.kept + (place.bh * p.nchunks + place.chunk0) * size;
+        }
+      } else if (p.nseg > 1) {
+        from = p.seg + (place.bh * p.nseg + place.seg) * block;
+      }
+      if (from) {
+        load_state(p, place.col0, from, row, col, size);
+      } else {
+#pragma unroll
+        for (int a = 0; a < KK; ++a) S[a][0] = S[a][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
     };
     first_state(p, place);
 
@@ -709,16 +627,18 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     // and the rest of the segment is walked token by token.  Where the state before the chunk is not finite, it may be
     // by the multiple that it is held as (up to 2^16 of it): it is formed again then, token by token from the first.
     // whether anything takes the state behind the last chunk
-    const bool wanted = STATE || (p.s1 && place.seg == (REV ? 0 : p.nseg - 1));
+    const bool wanted = OWN || (p.s1 && place.seg == (REV ? 0 : p.nseg - 1));
+    const bool with = DOT && p.dot != nullptr;     // the decays' gradient is
     bool done = true;
     int ci = 0;
     int64_t t0 = start_of(0);
     const T *now_q = tq.at, *now_k = tk.at, *now_v = tv.at;
+    if (CROSS) load_kept(p, place, t0 / C, 0);
     load_gate(t0);
     if (!STATE) tq.template load<REV>(tid, tokens_of(t0));
     tk.template load<REV>(tid, tokens_of(t0));
     tv.template load<REV>(64 * wave + lane, tokens_of(t0));
-    if (wave == kDecayWave) decays(sh.dec[part][0]);
+    if (wave == kDecayWave) decays(sh.dec[part][0], t0 / C);
     if (chunks > 1) load_gate(t0 + kOn);
     if (!STATE && tid == 0) sh.bad = 0;
     if (!STATE && tid < 8) sh.p[HP * NPP * kPairs + tid] = T(0);
@@ -730,6 +650,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       const int vid = 64 * wave + lane;             // of the head's threads
       l16 = lane & 15;
       g = lane >> 4;
+      // (half of what is kept is on its way through the update, half from here on)
+      if (CROSS) load_kept(p, place, t0 / C, 1);
       if (!STATE) tq.store(sh.q, tid, now_q, n);
       tk.store(sh.k, tid, now_k, n);
       tv.store(sv, vid, now_v, n);
@@ -739,20 +661,29 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       if (!STATE) now_q = tq.at;
       now_k = tk.at;
       now_v = tv.at;
-      if (wave == kDecayWave && more) decays(sh.dec[part][(ci + 1) & 1]);
+      if (wave == kDecayWave && more) decays(sh.dec[part][(ci + 1) & 1], t0 / C + (REV ? -1 : 1));
       if (!STATE) {
         // (the next chunk's operands are asked for one by one, and not all of them at a time)
         if (more) tq.template load<REV>(tid, next);
+        if (DOT && with) keep_some(p, place, t0 / C, dec.before);
         pairs(dec);
         if (more) tk.template load<REV>(tid, next);
         from_state(dec);
-        if (DOT) load_x(n);
         __syncthreads();
+      }
+      if (KEEP) keep_some(p, place, t0 / C, dec.before);
+      if (CROSS) {
+        cross(p, dec.before);
+        if (more) load_kept(p, place, t0 / C - 1, 0);
       }
       if (STATE && more) tk.template load<REV>(tid, next);
       if (more) tv.template load<REV>(vid, next);
       if (ci + 2 < chunks) load_gate(t0 + 2 * kOn);
       values();
+      if (DOT && with) {
+        load_x(n);
+        dots();
+      }
       if (!STATE) {
         done = from_pairs();
         if (done)
@@ -765,7 +696,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       if (done && (more || wanted)) update(dec);
       __syncthreads();
       if (!STATE && sh.bad != 0) break;
-      if (DOT && vid < n) {
+      if (CROSS && wave == 0) store_cross(p, place, t0 / C);
+      if (DOT && with && vid < n) {
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][vid];
@@ -810,6 +742,23 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
           const int64_t t0 = place.start_of(ci);
           const int n = place.tokens_of(t0);
           const bool stands = !STATE && (ci < from || (ci == from && done));
+          const bool with = ci >= from && DOT && p.dot != nullptr;
+          if ((DOT && with) || KEEP) keep_some(p, place, t0 / C, 1.f);
+          if (DOT && with && wave == kDecayWave && lin_lane() == 0) mark(p, place, t0 / C, true);
+          if (CROSS) {
+            load_kept(p, place, t0 / C, 0);
+            load_kept(p, place, t0 / C, 1);
+            cross(p, 1.f);
+            __syncthreads();
+            if (wave == 0) store_cross(p, place, t0 / C);
+          }
+          // the state before the chunk, what the tokens since have left of it, and whether that is none
+          f32x4 S0[DOT ? KK : 1][2];
+          if constexpr (DOT)
+#pragma unroll
+            for (int a = 0; a < KK; ++a) S0[a][0] = S[a][0], S0[a][1] = S[a][1];
+          float left = p.fscale;
+          bool gone = false;
 #pragma unroll 1
           for (int i = 0; i < n; ++i) {
             const int64_t t = t0 + (REV ? n - 1 - i : i);
@@ -825,7 +774,11 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
             const double c = double(base_g[t * p.g_sl]) * 1.4426950408889634;
             const bool start = c < -150.0;
             const float d = start ? 0.f : lin_decay(float(c));
-            float out = 0.f;
+            float out = 0.f, of_state = 0.f;
+            if (DOT && !REV) {
+              gone |= start;
+              left *= d;
+            }
             if (!stands || again) {
 #pragma unroll
               for (int a = 0; a < KK; ++a)
@@ -839,6 +792,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
                     if (kd < p.kd) {
                       s = fmaf(row_k[kd], v, s);
                       out = fmaf(row_q[kd], s, out);
+                      if (DOT) of_state = fmaf(row_q[kd], S0[a][u][r], of_state);
                     }
                     if (REV) s = start ? 0.f : s * d;
                     S[a][u][r] = s;
@@ -848,7 +802,6 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
               out += __shfl_xor(out, 16);
               out += __shfl_xor(out, 32);
               out *= p.fscale;
-              float dot = 0.f;
               if (!stands && col < p.vd) {
                 if (g == 0) {
                   char* const to = place.out_at(p, t, col, oes);
@@ -857,30 +810,35 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
                   else
                     io::narrow(reinterpret_cast<T*>(to), out);
                 }
-                if (DOT) dot = out * io::widen(*place.template x_at<T>(p, t, col));
               }
-              if constexpr (DOT) {
+              if (DOT && with) {
+                float dot = 0.f;
+                if (!gone && col < p.vd) dot = of_state * left * io::widen(*place.template x_at<T>(p, t, col));
                 // (what a wavefront whose first chunk stands has left there is that chunk's)
-                for (int x = 8; x > 0; x /= 2) dot += __shfl_xor(dot, x);
+                for (int x = 32; x > 0; x /= 2) dot += __shfl_xor(dot, x);
                 if (lane == 0 && !stands) sh.dot[all_wave][t - t0] = dot;
                 __syncthreads();
-                if (ci >= from && wave == 0 && lane == 0) {
+                if (wave == 0 && lane == 0) {
                   float sum = 0.f;
                   for (int w = 0; w < kWaves; ++w) sum += sh.dot[part * kWaves + w][t - t0];
                   p.dot[(place.nb * p.batch * p.H + bh) * p.L + t] = sum;
                 }
               }
             }
+            if (DOT && REV) {
+              gone |= start;
+              left *= d;
+            }
           }
         }
       }
 
       const int block = p.kd * p.vd;
-      if (STATE) {
+      if (OWN) {
         store_state(p, col0, p.seg + (bh * p.nseg + place.seg) * block);
         if (wave == kDecayWave && lin_lane() == 0 && place.nb == 0)
           p.seg_decay[bh * p.nseg + place.seg] = anew ? -HUGE_VAL : total;
-      } else if (ends) {
+      } else if (!STATE && ends) {
         store_state(p, col0, p.s1 + bh * block);
       }
     }
@@ -893,9 +851,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
   // one after the other, 86 so; where each fills them the time is the same.)
   constexpr std::true_type backward;
   constexpr std::false_type forward;
-  if constexpr (WALK == LinWalk::backward) {
+  if constexpr (WALK == LinWalk::backward || WALK == LinWalk::cross) {
     segment(backward, walks.p[0], item);
-  } else if constexpr (WALK == LinWalk::forward || WALK == LinWalk::state) {
+  } else if constexpr (!kBoth) {
     segment(forward, walks.p[0], item);
   } else {
     if (item & 1)
@@ -905,27 +863,45 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
   }
 }
 
-template <typename T, int KD, int NW, int HP>
-hipError_t lin_launch(LinWalk walk, const LinParams* p, hipStream_t stream) {
-  const bool state = walk == LinWalk::state || walk == LinWalk::states;
-  const int64_t items = p->batch * (p->H / HP) * p->nblk * (state ? p->nseg - 1 : p->nseg);
+template <typename T, int KD, int NW, int HP, int C, LinWalk WALK>
+hipError_t lin_start(const LinParams* p, int64_t segs, hipStream_t stream) {
+  constexpr int kWalks = sizeof(LinWalks<WALK>) / sizeof(LinParams);
+  const int64_t items = kWalks * p->batch * (p->H / HP) * p->nblk * segs;
   if (items == 0) return hipSuccess;
-  const dim3 one{uint32_t(items)}, both{uint32_t(2 * items)}, threads{64 * NW};
-  switch (walk) {
-    case LinWalk::forward: lin_kernel<T, KD, NW, HP, LinWalk::forward><<<one, threads, 0, stream>>>({{p[0]}}); break;
-    case LinWalk::backward: lin_kernel<T, KD, NW, HP, LinWalk::backward><<<one, threads, 0, stream>>>({{p[0]}}); break;
-    case LinWalk::state: lin_kernel<T, KD, NW, HP, LinWalk::state><<<one, threads, 0, stream>>>({{p[0]}}); break;
-    case LinWalk::states: lin_kernel<T, KD, NW, HP, LinWalk::states><<<both, threads, 0, stream>>>({{p[0], p[1]}}); break;
-    case LinWalk::grads:
-      // (do and v, the queries and keys of these walks, are each head's own)
-      if constexpr (HP > 1) return hipErrorInvalidValue;
-      if constexpr (HP == 1) lin_kernel<T, KD, NW, 1, LinWalk::grads><<<both, threads, 0, stream>>>({{p[0], p[1]}});
-      break;
-  }
+  LinWalks<WALK> walks;
+  for (int i = 0; i < kWalks; ++i) walks.p[i] = p[i];
+  lin_kernel<T, KD, NW, HP, C, WALK><<<dim3(uint32_t(items)), dim3(64 * NW), 0, stream>>>(walks);
   return hipGetLastError();
 }
 
+template <typename T, int KD, int NW, int HP>
+hipError_t lin_launch(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  constexpr int C = lin_chunk(sizeof(T) == 2, KD);
+  switch (walk) {
+    case LinWalk::forward: return lin_start<T, KD, NW, HP, C, LinWalk::forward>(p, p->nseg, stream);
+    case LinWalk::backward: return lin_start<T, KD, NW, HP, C, LinWalk::backward>(p, p->nseg, stream);
+    case LinWalk::state: return lin_start<T, KD, NW, HP, C, LinWalk::state>(p, p->nseg - 1, stream);
+    case LinWalk::states: return lin_start<T, KD, NW, HP, C, LinWalk::states>(p, p->nseg - 1, stream);
+    case LinWalk::cross: return lin_start<T, KD, NW, HP, C, LinWalk::cross>(p, p->nseg, stream);
+    // (the keys of these walks, and the queries, are do and v, each head's own)
+    case LinWalk::keep:
+      if constexpr (HP == 1) return lin_start<T, KD, NW, 1, C, LinWalk::keep>(p, p->nseg, stream);
+      break;
+    case LinWalk::grads:
+      if constexpr (HP == 1) return lin_start<T, KD, NW, 1, C, LinWalk::grads>(p, p->nseg, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
 template <typename T, int KD> hipError_t lin_choose(LinWalk walk, const LinParams* p, hipStream_t stream) {
+  // (Gradients whose other width is above 128 have its chunks, and v's columns are more than 128 then.)
+  if constexpr (sizeof(T) == 4 && KD < 256)
+    if (p->chunk == 32) {
+      if (walk == LinWalk::grads) return lin_start<T, KD, 8, 1, 32, LinWalk::grads>(p, p->nseg, stream);
+      if (walk == LinWalk::keep) return lin_start<T, KD, 8, 1, 32, LinWalk::keep>(p, p->nseg, stream);
+      if (walk == LinWalk::cross) return lin_start<T, KD, 8, 1, 32, LinWalk::cross>(p, p->nseg, stream);
+      return hipErrorInvalidValue;
+    }
   // Eight wavefronts for 128 columns; of at most 64 columns a workgroup has four, or takes two heads that share their
   // queries and keys, which it then stages once (4 x 80 heads on one q and k x 8192, 128 x 64 bf16: 660 us with
   // a head each, 560 so).

@@ -305,22 +305,37 @@ struct LinParams {
   int64_t s_row, s_col; // strides of s0 and s1 within a block
   float* seg;           // workspace: [batch][H][nseg] blocks of kd * vd, laid out as s0's
   double* seg_decay;    // workspace: [batch][H][nseg], log2 of the segment's decay, -infinity where the state starts anew
-  LinTensor x;          // dot: out . x per token, [nblk][batch][H][L]; null: not wanted
+  LinTensor x;          // grads: the products of x with the rows' parts of the state, [nblk][batch][H][L] (null: not wanted)
   float* dot;
+  float* kept;          // the states before chunks, [batch][H][nchunks] blocks of [dv][c_row]: written by grads (forward,
+  int64_t c_row;        // every lin_span()-th) and keep (the others), read by cross; c_row: dk to a multiple of 4
+  float* back;          // grads, backward: the gradients between every lin_span() chunks, [batch][H][ceil(nchunks / lin_span())] blocks
+  int32_t* marks;       // [2][batch][H][nchunks][marks_each]: written by grads, read by keep and cross, which leave spans without one
+  int32_t marks_each;   // blocks of columns of grads
+  int32_t ends;         // grads: 1: there is an initial state, 2: a gradient of the last one
+  float* cross;         // cross: its product with the gradient behind the chunk, [nblk][batch][H][nchunks]
   int64_t batch, L, H;
   int32_t kd, vd;       // width of q and k, of v and out (1 .. 256)
   float pscale, fscale, wscale;   // of the pairs, of a row's product with the state, of its share in the state
-  int64_t nchunks;      // ceil(L / lin_chunk())
+  int32_t chunk;        // tokens of a chunk
+  int64_t nchunks;      // ceil(L / chunk)
   int64_t seg_chunks;   // chunks of a segment
   int32_t nseg, nblk;   // segments; blocks of lin_cols() columns
   int32_t pairs;        // 1: heads 2 i and 2 i + 1 share their q and k and vd is at most 64: a workgroup takes both
 };
 constexpr int lin_kd(int64_t kd) { return kd <= 64 ? 64 : kd <= 128 ? 128 : 256; }
 constexpr int lin_cols(int64_t vd) { return vd <= 64 ? 64 : 128; }
+// Chunks between states that the decays' gradient starts from.
+constexpr int lin_span() { return 8; }
+// Tokens of a chunk: the LDS of a compute unit holds the tiles of a chunk of 64, but not those of 256
+// fp32 channels.  (Chunks of 32 for all of fp32, two workgroups a compute unit: 2 x 16 heads x 4096, 64 x 64, 79 us in
+// the place of 80; 128 x 128, whose registers then spill, 231 in the place of 198.)
 constexpr int lin_chunk(bool bf16, int64_t kd) { return !bf16 && kd > 128 ? 32 : 64; }
 // What a launch walks: forward or backward; the segments' states only, forward, or in both directions (p[0] forward,
-// p[1] backward); a forward and a backward walk with their rows' products (both with `dot`, pairs == 0).
-enum class LinWalk { forward, backward, state, states, grads };
+// p[1] backward); a forward and a backward walk of what shares no queries and keys (pairs == 0), with their rows' products if wanted;
+// of spans with a mark (segments of lin_span() chunks) the states before all chunks (forward), and their products with the
+// gradients behind them (backward).
+enum class LinWalk { forward, backward, state, states, grads, keep, cross };
 // one launch, from s0 or (nseg > 1) from the states that enter the segments
 hipError_t launch_lin(bool bf16, LinWalk walk, const LinParams* p, hipStream_t stream);
 // nseg > 1: the states that enter the segments, from k, v and s0 (kd x vd, rows s_row apart, s_col == 1 or the
@@ -339,25 +354,42 @@ hipError_t launch_lin_f32_256(LinWalk walk, const LinParams* p, hipStream_t stre
 hipError_t launch_lin_heads(bool bf16, const float* part, void* out0, void* out1, int64_t tokens, int64_t H, int share,
                             int width, hipStream_t stream);
 
-// The decays' gradient from the rows' products: dg_t = <last, dlast> + sum_{i >= t} (qdq_i - kdk_i)
+// The decays' gradient, from the pairs of each chunk and what the walks have left of the states before and behind it.
 struct LinDecayParams {
-  const float* qdq;     // [nq][batch][H][L]
-  const float* kdk;     // [nk][batch][H][L]
-  const float* last;    // [batch][H][state], with dlast; both may be null (zero)
-  const float* dlast;
-  const float* states;  // nseg > 1: [batch][H][nseg][state], what enters each segment ...
-  const float* grads;   // ... and its gradient, which enters from behind
+  LinTensor rows[2], cols[2];     // q and do; k and v
+  int32_t dk, dv;
+  const float* qdq;     // [nq][batch][H][L]: q . (the state's part of dq)
+  const float* kdk;     // [nq][batch][H][L]: k . (the state's part of dk)
+  const double* between;  // [batch][H][nchunks]: e^c <S, R>, or null (zero)
   const float* g;
   int64_t g_sb, g_sl, g_sh;
+  float scale;
   float* dg;            // [batch][L][H], or null: the heads' sums only
-  double* sums;         // workspace [batch][H][nseg]
+  double* sums;         // workspace [H][batch][nchunks]
   float* dg_heads;      // [H], or null
-  int64_t batch, L, H, state;
-  int64_t seg_len;      // tokens of a segment
-  int32_t nseg;
-  int32_t nq, nk;
+  int64_t batch, L, H, nchunks;
+  int32_t chunk, nq;
 };
-hipError_t launch_lin_decay(const LinDecayParams& p, hipStream_t stream);
+// e^c <S, R> of each chunk, S the state before it and R the gradient behind it
+struct LinBetweenParams {
+  const float* qdq;     // as LinDecayParams
+  const float* kdk;
+  const float* cross;   // [nz][batch][H][nchunks]: <S, R> of spans with a mark
+  const float* kept;    // as LinParams
+  const float* back;
+  const int32_t* marks;
+  const float* last;    // [batch][H][state]: the last state and its gradient, or null (zero)
+  const float* dlast;
+  const float* g;
+  int64_t g_sb, g_sl, g_sh;
+  double* between;
+  int64_t batch, L, H, nchunks;
+  int64_t state, kept_state;      // values of a state, and of a kept one
+  int32_t chunk, nq, nz, marks_each;
+  int32_t initial;      // there is an initial state
+};
+hipError_t launch_lin_between(const LinBetweenParams& p, hipStream_t stream);
+hipError_t launch_lin_decay(bool bf16, const LinDecayParams& p, hipStream_t stream);
 
 // One token per batch row, states in slots.
 struct LinStepParams {

@@ -1296,10 +1296,14 @@ struct LinPlan {
   int32_t nseg = 1;
   size_t fwd_bytes = 0, bwd_bytes = 0;
   size_t off_rev = 0;           // the other direction's states and decays
-  size_t off_decay = 0, off_qdq = 0, off_kdk = 0, off_last = 0, off_sums = 0, off_part = 0;
+  int64_t chunk = 64, nchunks = 0;                      // of the gradients
+  size_t off_decay = 0, off_qdq = 0, off_kdk = 0, off_kept = 0, off_back = 0, off_cross = 0, off_marks = 0;
+  size_t off_between = 0, off_last = 0, off_sums = 0, off_part = 0;
 };
 
 static int64_t lin_blocks(int64_t vd) { return (vd + selscan::lin_cols(vd) - 1) / selscan::lin_cols(vd); }
+
+static int64_t lin_spans(int64_t nchunks) { return (nchunks + selscan::lin_span() - 1) / selscan::lin_span(); }
 
 // Rows of `width` elements on axes of these sizes and strides: whether none overlaps another.
 static bool rows_apart(std::initializer_list<std::pair<int64_t, int64_t>> axes, int64_t width) {
@@ -1381,6 +1385,10 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       p.off_decay = ws_round(f * bh * p.nseg * d.dk * d.dv);
       p.fwd_bytes = p.off_decay + ws_round(int64_t(sizeof(double)) * bh * p.nseg);
     }
+    p.chunk = selscan::lin_chunk(bf16, wide);
+    p.nchunks = (d.seqlen + p.chunk - 1) / p.chunk;
+    // (a workgroup of 512 threads for each span of the decays' gradient)
+    if (bwd && want_dg && lin_spans(p.nchunks) * bh * ((wide + 63) / 64) >= 2 * kMaxItems) return SELSCAN_ERR_UNSUPPORTED;
     p.off_rev = p.fwd_bytes;
     size_t off = 2 * p.fwd_bytes;
     if (want_dg) {
@@ -1388,10 +1396,20 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       off += ws_round(f * rows * lin_blocks(d.dk));
       p.off_kdk = off;
       off += ws_round(f * rows * lin_blocks(d.dk));
+      p.off_kept = off;
+      off += ws_round(f * bh * p.nchunks * d.dv * round_up(d.dk, 4));
+      p.off_back = off;
+      off += ws_round(f * bh * lin_spans(p.nchunks) * d.dv * round_up(d.dk, 4));
+      p.off_cross = off;
+      off += ws_round(f * bh * p.nchunks * lin_blocks(d.dv));
+      p.off_marks = off;
+      off += ws_round(2 * int64_t(sizeof(int32_t)) * bh * p.nchunks * lin_blocks(d.dk));
+      p.off_between = off;
+      off += ws_round(int64_t(sizeof(double)) * bh * p.nchunks);
       p.off_last = off;
       off += ws_round(f * bh * d.dk * d.dv);
       p.off_sums = off;
-      off += ws_round(int64_t(sizeof(double)) * bh * p.nseg);
+      off += ws_round(int64_t(sizeof(double)) * bh * p.nchunks);
     }
     p.off_part = off;
     if (d.nheads != d.qk_heads) off += ws_round(2 * f * rows * d.dk);
@@ -1415,14 +1433,15 @@ static selscan::LinTensor lin_tensor(const void* ptr, const selscan_linattn_dims
 // One walk: queries and keys of width kd, values of width vd.
 static selscan::LinParams lin_params(const LinPlan& pl, const selscan::LinTensor& q, const selscan::LinTensor& k,
                                      const selscan::LinTensor& v, int64_t kd, int64_t vd, const float* g,
-                                     const selscan_linattn_dims& d, void* ws) {
+                                     const selscan_linattn_dims& d, void* ws, int64_t chunk = 0) {
   selscan::LinParams p{};
   p.q = q; p.k = k; p.v = v;
   p.g = g;
   p.g_sb = d.decay_tokens ? d.g_sb : 0; p.g_sl = d.decay_tokens ? d.g_sl : 0; p.g_sh = d.g_sh;
   p.batch = d.batch; p.L = d.seqlen; p.H = d.nheads;
   p.kd = int32_t(kd); p.vd = int32_t(vd);
-  const int64_t chunk = selscan::lin_chunk(d.io_dtype == SELSCAN_BF16, kd);
+  if (chunk == 0) chunk = selscan::lin_chunk(d.io_dtype == SELSCAN_BF16, kd);
+  p.chunk = int32_t(chunk);
   p.nchunks = (d.seqlen + chunk - 1) / chunk;
   p.seg_chunks = (pl.seg_len + chunk - 1) / chunk;
   p.nseg = pl.nseg;
@@ -1552,9 +1571,7 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
                            tv = lin_tensor(v, d, d.nheads, d.v_sb, d.v_sl, d.v_sh),
                            to = lin_tensor(d_o, d, d.nheads, d.o_sb, d.o_sl, d.o_sh);
   const int64_t tokens = d.batch * d.seqlen;
-  float* part = reinterpret_cast<float*>(ws + pl.off_part);
-  float* last = reinterpret_cast<float*>(ws + pl.off_last);
-  const bool want_last = want_dg && dlast_state != nullptr;
+  float* const part = reinterpret_cast<float*>(ws + pl.off_part);
   // the states S of the forward pass, and their gradient R from the last token on
   char* const rev = ws + pl.off_rev;
   selscan::LinParams walks[2] = {lin_params(pl, tq, tk, tv, d.dk, d.dv, log_decay, d, ws),
@@ -1564,14 +1581,29 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
   walks[0].s_col = walks[1].s_col = 1;
   walks[0].wscale = 1.f; walks[1].wscale = d.scale;
   e = selscan::launch_lin_states(bf16, true, walks, s);
-  // dq: do meets v, and S meets do; dk: v meets do, and R meets v (S and R read with their axes exchanged)
+  // dq: do meets v, and S meets do; dk: v meets do, and R meets v (S and R read with their axes exchanged).
+  // (Not a bit of them goes by whether the decays' gradient is wanted too.)
+  selscan::LinBetweenParams z{};
+  // (one chunk without a state before it, or without a gradient behind it: nothing passes all of it)
+  const bool between = want_dg && (pl.nchunks > 1 || (initial_state && dlast_state));
+  float* const kept = reinterpret_cast<float*>(ws + pl.off_kept);
+  float* const back = reinterpret_cast<float*>(ws + pl.off_back);
+  float* const last = reinterpret_cast<float*>(ws + pl.off_last);
+  int32_t* const marks = reinterpret_cast<int32_t*>(ws + pl.off_marks);
+  const int32_t marks_each = int32_t(lin_blocks(d.dk));
+  auto in_spans = [&](selscan::LinParams* p) {
+    p->kept = kept; p->back = back; p->c_row = round_up(d.dk, 4);
+    p->marks = marks; p->marks_each = marks_each;
+    p->seg_chunks = selscan::lin_span();
+    p->nseg = int32_t(lin_spans(pl.nchunks));
+  };
   if (e == hipSuccess) {
-    selscan::LinParams p[2] = {lin_params(pl, to, tv, tk, d.dv, d.dk, log_decay, d, ws),
-                               lin_params(pl, tv, to, tq, d.dv, d.dk, log_decay, d, rev)};
+    selscan::LinParams p[2] = {lin_params(pl, to, tv, tk, d.dv, d.dk, log_decay, d, ws, pl.chunk),
+                               lin_params(pl, tv, to, tq, d.dv, d.dk, log_decay, d, rev, pl.chunk)};
     const int64_t rows = tokens * d.nheads * d.dk;
     lin_out(&p[0], shared ? part : dq, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
     lin_out(&p[1], shared ? part + rows : dk, shared, d, d.seqlen * d.nheads * d.dk, d.nheads * d.dk, d.dk);
-    p[0].s0 = initial_state; p[0].s1 = want_last ? last : nullptr;
+    p[0].s0 = initial_state;
     p[1].s0 = dlast_state;
     p[0].s_row = p[1].s_row = 1;
     p[0].s_col = p[1].s_col = d.dv;
@@ -1580,32 +1612,70 @@ int linear_attention_bwd(const void* q, const void* k, const void* v, const floa
     if (want_dg) {
       p[0].x = tq; p[0].dot = reinterpret_cast<float*>(ws + pl.off_qdq);
       p[1].x = tk; p[1].dot = reinterpret_cast<float*>(ws + pl.off_kdk);
-      e = selscan::launch_lin(bf16, selscan::LinWalk::grads, p, s);
-    } else {
-      e = selscan::launch_lin(bf16, selscan::LinWalk::forward, &p[0], s);
-      if (e == hipSuccess) e = selscan::launch_lin(bf16, selscan::LinWalk::backward, &p[1], s);
+      p[0].kept = kept; p[1].back = back;
+      p[0].c_row = p[1].c_row = round_up(d.dk, 4);
+      p[0].marks = p[1].marks = marks;
+      p[0].ends = (initial_state ? 1 : 0) | (dlast_state ? 2 : 0);
+      if (between && dlast_state) p[0].s1 = last;
     }
+    e = selscan::launch_lin(bf16, selscan::LinWalk::grads, p, s);
   }
   if (e == hipSuccess && shared)
     e = selscan::launch_lin_heads(bf16, part, dq, dk, tokens, d.nheads, int(d.nheads / d.qk_heads), int(d.dk), s);
+  // the decays' gradient: S before the chunks and R behind them, in spans with a mark each for itself
+  float* const cross = reinterpret_cast<float*>(ws + pl.off_cross);
+  if (e == hipSuccess && between) {
+    selscan::LinParams p = lin_params(pl, tv, tv, tk, d.dv, d.dk, log_decay, d, ws, pl.chunk);
+    p.pairs = 0;
+    p.s0 = initial_state;
+    p.s_row = 1; p.s_col = d.dv;
+    p.wscale = 1.f;
+    in_spans(&p);
+    e = selscan::launch_lin(bf16, selscan::LinWalk::keep, &p, s);
+  }
+  if (e == hipSuccess && between) {
+    selscan::LinParams p = lin_params(pl, tk, tq, to, d.dk, d.dv, log_decay, d, rev, pl.chunk);
+    p.s0 = dlast_state;
+    p.s_row = d.dv; p.s_col = 1;
+    p.wscale = d.scale;
+    p.cross = cross;
+    in_spans(&p);
+    e = selscan::launch_lin(bf16, selscan::LinWalk::cross, &p, s);
+  }
+  if (e == hipSuccess && between) {
+    z.qdq = reinterpret_cast<float*>(ws + pl.off_qdq);
+    z.kdk = reinterpret_cast<float*>(ws + pl.off_kdk);
+    z.cross = cross;
+    z.kept = kept; z.back = back;
+    z.marks = marks; z.marks_each = marks_each;
+    z.last = last; z.dlast = dlast_state;
+    z.g = log_decay; z.g_sb = walks[0].g_sb; z.g_sl = walks[0].g_sl; z.g_sh = walks[0].g_sh;
+    z.between = reinterpret_cast<double*>(ws + pl.off_between);
+    z.batch = d.batch; z.L = d.seqlen; z.H = d.nheads; z.nchunks = pl.nchunks;
+    z.state = d.dk * d.dv; z.kept_state = d.dv * round_up(d.dk, 4);
+    z.chunk = int32_t(pl.chunk); z.nq = int32_t(lin_blocks(d.dk)); z.nz = int32_t(lin_blocks(d.dv));
+    z.initial = initial_state != nullptr;
+    e = selscan::launch_lin_between(z, s);
+  }
   if (e == hipSuccess && want_dg) {
     selscan::LinDecayParams c{};
+    c.rows[0] = tq; c.rows[1] = to; c.cols[0] = tk; c.cols[1] = tv;
+    c.dk = int32_t(d.dk); c.dv = int32_t(d.dv);
     c.qdq = reinterpret_cast<float*>(ws + pl.off_qdq);
     c.kdk = reinterpret_cast<float*>(ws + pl.off_kdk);
-    c.states = walks[0].seg; c.grads = walks[1].seg;
-    c.seg_len = pl.seg_len; c.nseg = pl.nseg;
-    c.last = want_last ? last : nullptr;
-    c.dlast = dlast_state;
+    c.between = between ? z.between : nullptr;
     c.g = log_decay; c.g_sb = walks[0].g_sb; c.g_sl = walks[0].g_sl; c.g_sh = walks[0].g_sh;
+    c.scale = d.scale;
     c.dg = d.decay_tokens ? dlog_decay : nullptr;
     c.dg_heads = d.decay_tokens ? nullptr : dlog_decay;
     c.sums = reinterpret_cast<double*>(ws + pl.off_sums);
-    c.batch = d.batch; c.L = d.seqlen; c.H = d.nheads; c.state = d.dk * d.dv;
-    c.nq = c.nk = int32_t(lin_blocks(d.dk));
-    e = selscan::launch_lin_decay(c, s);
+    c.batch = d.batch; c.L = d.seqlen; c.H = d.nheads; c.nchunks = pl.nchunks;
+    c.chunk = int32_t(pl.chunk);
+    c.nq = int32_t(lin_blocks(d.dk));
+    e = selscan::launch_lin_decay(bf16, c, s);
   }
-  // dv: k meets q, and R meets k; R before the first token is the initial state's gradient (last: it
-  // may take dlast_state's place)
+  // dv: k meets q, and R meets k; R before the first token is the initial state's gradient (last: it may take
+  // dlast_state's place)
   if (e == hipSuccess) {
     selscan::LinParams& p = walks[1];
     lin_out(&p, dv, false, d, d.seqlen * d.nheads * d.dv, d.nheads * d.dv, d.dv);

@@ -25,3 +25,15 @@ def test_workgroups_of_the_forward_and_the_step(batch, H, K, V, takes):
 def test_workgroups_of_the_backward(batch, H, K, V, takes):
     """batch * nheads * ceil(max(dk, dv) / 64) below 2^22."""
     assert bwd(lin(ss.SELSCAN_F32, batch, 5, H, H, K, V), q=ODD) == (ALIGN if takes else UNSUPPORTED)
+
+
+@pytest.mark.parametrize("io,batch,L,H,K,V,takes", [
+    (ss.SELSCAN_BF16, 1 << 10, 1 << 21, 1, 64, 64, True), (ss.SELSCAN_BF16, 1 << 11, 1 << 21, 1, 64, 64, False),
+    (ss.SELSCAN_BF16, 1 << 11, (1 << 21) - 512, 1, 64, 64, True), (ss.SELSCAN_BF16, 1 << 10, 1 << 21, 1, 65, 1, False), (ss.SELSCAN_BF16, 1365, 1 << 19, 1, 200, 1, True), (ss.SELSCAN_BF16, 1366, 1 << 19, 2, 200, 1, False),
+    (ss.SELSCAN_BF16, 1 << 10, 1 << 21, 1, 200, 1, False), (ss.SELSCAN_F32, 1 << 8, 1 << 20, 1, 20, 129, True),
+    (ss.SELSCAN_F32, 1 << 8, (1 << 21) + 1, 2, 20, 200, False)])
+def test_spans_of_the_decays_gradient(io, batch, L, H, K, V, takes):
+    """ceil(seqlen / 512) (fp32 wider than 128: 256) batch nheads ceil(max(dk, dv) / 64) below 2^23."""
+    d = lin(io, batch, L, H, H, K, V)
+    assert bwd(d, q=ODD) == ALIGN                             # without it
+    assert bwd(d, q=ODD, dg=0x100000) == (ALIGN if takes else UNSUPPORTED)

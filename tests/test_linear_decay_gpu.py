@@ -1,0 +1,93 @@
+"""The gradient of linear attention's decays on the GPU: its error at weak, strong and mixed decays, and what is not
+finite in it.  Bounds in linear_bounds.py."""
+import numpy as np
+import pytest
+
+from oracle import linear as orc
+from tests import linear_bounds as bounds
+from tests import test_linear_gpu as lin
+from tests.test_oracle_linear_decay import with_decay
+
+pytestmark = pytest.mark.gpu
+
+dev, host = lin.dev, lin.host
+
+#        one chunk; two; heads that share; segments and spans (a last one of one chunk, of one token); widths apart; sequences
+#        that are not split
+SIZES = [(2, 40, 2, 1, 24, 40), (1, 130, 2, 2, 16, 24), (2, 513, 4, 2, 64, 64), (1, 1500, 2, 1, 64, 130), (1, 577, 1, 1, 256, 256),
+         (1, 330, 2, 1, 200, 20), (1, 330, 1, 1, 20, 200), (1, 700, 2, 2, 37, 83), (1, 500, 344, 344, 4, 4), (1, 520, 344, 172, 4, 5)]
+
+
+def cast(i, io):
+    return {k: lin.bf(v, io) if k in ("q", "k", "v", "do") else v for k, v in i.items()}
+
+
+def check(got, i, size, io, S0, dlast, what):
+    ref, bound = bounds.decay_bound(i, size, io, S0, dlast)
+    got = host(got)
+    if i["g"].ndim == 1:
+        ref, bound = ref.sum((0, 1)), bound.sum((0, 1))
+        lin.near(got, ref, bound + 2.0 ** -24 * np.abs(ref), what)
+        return
+    lin.near(got, ref, bound, what)
+    norm = bounds.norms(got - ref, ref)[np.abs(ref).max(1) > 1e-20]
+    assert norm.size == 0 or norm.max() <= bounds.NORM, (what, norm.max())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", ["fixed", "token", "packed", "fast", -0.02, -2.0, -5.0, -10.0, -20.0, "mixed"])
+@pytest.mark.parametrize("size", SIZES)
+def test_weak_and_strong_decays(size, decay, io):
+    i = cast(with_decay(size, decay, seed=sum(size)), io)
+    for ends in (True, False):
+        d = lin.backward(i, io, S0=ends, dlast=ends)
+        check(d["dlog_decay"], i, size, io, ends, ends, "%s %s ends %s" % (size, decay, ends))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("S0,dlast", [(True, False), (False, True)])
+@pytest.mark.parametrize("size", [(2, 40, 2, 1, 24, 40), (1, 600, 3, 1, 32, 16)])
+def test_one_end(size, S0, dlast, io):
+    for decay in ("token", "mixed"):
+        i = cast(with_decay(size, decay, seed=5), io)
+        check(lin.backward(i, io, S0=S0, dlast=dlast)["dlog_decay"], i, size, io, S0, dlast, decay)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", ["token", "mixed", "packed"])
+@pytest.mark.parametrize("size", [(1, 700, 4, 2, 64, 64), (1, 330, 2, 2, 128, 128), (3, 64, 2, 1, 40, 16), (1, 330, 2, 1, 20, 200)])
+def test_other_gradients_are_the_same_without_it(size, decay, io):
+    t = lin._torch()
+    i = cast(with_decay(size, decay, seed=6), io)
+    a, b = lin.backward(i, io), lin.backward(i, io, decay_grad=False)
+    assert all(t.equal(a[k], b[k]) for k in ("dq", "dk", "dv", "dinitial_state"))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["v", "k", "q", "do", "q, then v", "do, then k", "v of a chunk's first", "do of a chunk's last"])
+@pytest.mark.parametrize("size", [(1, 900, 2, 1, 64, 64), (2, 150, 2, 2, 32, 48), (1, 450, 344, 344, 4, 4), (1, 300, 1, 1, 20, 200)])
+def test_what_is_not_finite(size, where, io):
+    """dlog_decay_t has the keys and rows of v before t and the queries and rows of do from t on: with one that is not finite it
+    is finite where its definition is, and what it is without the others."""
+    B, L, H, Hk, K, V = size
+    i = cast(with_decay(size, "token", seed=7), io)
+    i["g"][:, 20] = i["g"][:, L - 10] = -np.inf
+    at = {"v of a chunk's first": 128, "do of a chunk's last": 127}.get(where, 70)
+    bad = {n: at for n in (("v",) if where[0] == "v" else ("do",) if where[:2] == "do" else (where[0],))}
+    if "then" in where:
+        bad[where[-1]] = at + 25
+    clean = dict(i, **{n: i[n].copy() for n in bad})
+    i = dict(i, **{n: i[n].copy() for n in bad})
+    value = {"v": np.inf, "k": -np.inf, "q": np.nan, "do": np.inf}
+    for n, t in bad.items():
+        i[n][0, t] = value[n]
+        clean[n][0, t] = 0.0
+    got = host(lin.backward(i, io)["dlog_decay"])
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = orc.linear_bwd(i["q"], i["k"], i["v"], i["g"], i["do"], i["scale"], i["S0"], i["dlast"])["dlog_decay"]
+    fine = np.isfinite(want) | np.isinf(i["g"])               # (zero where the state starts anew)
+    assert not fine.all()
+    assert np.array_equal(np.isfinite(got), fine), np.argwhere(np.isfinite(got) != fine)[:5]
+    ref, bound = bounds.decay_bound(clean, size, io)
+    # (spans with it have products of their own: what is finite has the bound of what passes it)
+    lin.near(np.where(fine, got, 0.0), np.where(fine, ref, 0.0), bound, where)
