@@ -169,20 +169,26 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
       any |= p.marks[(((i / each & 1) * p.batch * p.H + bh + i / each / 2) * p.nchunks + chunk0) * p.marks_each + i % each];
     if (!__syncthreads_or(any)) return;
   }
-  auto segment = [&](auto reversed, const LinParams& p, const int item) __attribute__((always_inline)) {
+  auto segment = [&](auto reversed, const int item) __attribute__((always_inline)) {
     constexpr bool REV = decltype(reversed)::value;
     constexpr int kWaves = NW / HP;                 // of a head
     constexpr int KK = KD / 32, KS = C / 32, IT = C / 16, kWV = 16 * kWaves, kPairs = Sh::kPairs, kThreads = 64 * NW;
     constexpr int kDecayWave = kWaves - 1;          // has the least to do with the pairs
 
     const int all_wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), part = all_wave / kWaves, wave = all_wave % kWaves;
-    int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
     using Place = LinPlace<C, HP, kWV, OWN, REV>;
-    const Place place(p, item, part);
+    f32x4 S[KK][2];
+    int begin = 0;                                  // the chunk that the walk begins with (again, behind one that was walked token by token)
+    do {
+    // (Parameters and places are formed anew here, and behind the walk: kept, they would not leave its registers room.)
+    const LinParams& p = lin_again(kBoth && REV ? 1 : 0);
+    int it = item;
+    asm volatile("" : "+s"(it), "+s"(begin));
+    int lane = lin_lane(), tid = 64 * all_wave + lane, l16 = lane & 15, g = lane >> 4;
+    const Place place(p, it, part);
     const int nb = place.nb, chunks = place.chunks, col0 = place.col0, wcol = wave * 16;
     const int64_t h = place.h, b = place.b, bh = place.bh;
 
-    f32x4 S[KK][2];
     // f(four state values, which of them, its place in a head's state in bytes): beyond the state for what is not there, where loads give
     // zero and stores are dropped
     auto each_state = [&](const LinParams& p, int col0, int row, int col, auto&& f) __attribute__((always_inline)) {
@@ -217,12 +223,9 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     T* const sv = sh.v + part * C * kWV;
     T* const sp = STATE ? sh.p : sh.p + part * NPP * kPairs;
     const int nothing = (HP - part) * NPP * kPairs;
-    if (!STATE) tq.init(p.q, b, h, start_of(0), 0, p.kd);
-    tk.init(p.k, b, h, start_of(0), 0, p.kd);
-    tv.init(p.v, b, h, start_of(0), col0, p.vd);
     constexpr int64_t kOn = REV ? -C : C;           // tokens from a chunk to the next
     // the log decays of a chunk, a chunk ahead of its operands
-    const float* gates = p.g + b * p.g_sb + h * p.g_sh + start_of(0) * p.g_sl;
+    const float* gates = nullptr;
     const int gsl = int(p.g_sl);
     float gate = 0.f;
     auto load_gate = [&](int64_t t0) {
@@ -410,8 +413,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     // Four columns of a row of the chunk's tile of `out`; rows and columns that are not there are beyond it,
     // and dropped.
     const int ocols = p.vd - (col0 + wcol), osl = int(p.o_sl), xsl = int(p.x.sl), oes = p.out_f32 ? 4 : int(sizeof(T));
-    char* out = place.out_at(p, start_of(0), col0 + wcol, oes);
-    const T* xs = DOT ? place.template x_at<T>(p, start_of(0), col0 + wcol) : nullptr;
+    char* out = nullptr;
+    const T* xs = nullptr;
     // x's rows, asked for before they meet the result (16 bits a value: two a register)
     constexpr int kXRegs = sizeof(T) == 2 ? 2 : 4;
     uint32_t xv[DOT ? IT : 1][kXRegs];
@@ -620,26 +623,33 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
         for (int a = 0; a < KK; ++a) S[a][0] = S[a][1] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
     };
-    first_state(p, place);
+    if (begin == 0) first_state(p, place);
 
     // Inside a chunk a token is kept from another by a zero factor, which an infinity or a NaN turns into a
-    // NaN.  If anything that comes out is not finite, what the wavefront has formed of the chunk is dropped,
-    // and the rest of the segment is walked token by token.  Where the state before the chunk is not finite, it may be
-    // by the multiple that it is held as (up to 2^16 of it): it is formed again then, token by token from the first.
+    // NaN.  If anything that comes out is not finite, what the wavefront has formed of the chunk is dropped, and it and
+    // those behind it are walked token by token until the state is finite.  Where the state before the chunk is not, it may be
+    // by the multiple that it is held as (up to 2^16 of it): all of the segment is walked so then, from its first token.
     // whether anything takes the state behind the last chunk
     const bool wanted = OWN || (p.s1 && place.seg == (REV ? 0 : p.nseg - 1));
     const bool with = DOT && p.dot != nullptr;     // the decays' gradient is
     bool done = true;
-    int ci = 0;
-    int64_t t0 = start_of(0);
+    int ci = begin;
+    int64_t t0 = start_of(ci);
+    if (!STATE) tq.init(p.q, b, h, t0, 0, p.kd);
+    tk.init(p.k, b, h, t0, 0, p.kd);
+    tv.init(p.v, b, h, t0, col0, p.vd);
+    gates = p.g + b * p.g_sb + h * p.g_sh + t0 * p.g_sl;
+    if (!STATE) out = place.out_at(p, t0, col0 + wcol, oes);
+    if (DOT) xs = place.template x_at<T>(p, t0, col0 + wcol);
+    begin = 0;
     const T *now_q = tq.at, *now_k = tk.at, *now_v = tv.at;
     if (CROSS) load_kept(p, place, t0 / C, 0);
     load_gate(t0);
     if (!STATE) tq.template load<REV>(tid, tokens_of(t0));
     tk.template load<REV>(tid, tokens_of(t0));
     tv.template load<REV>(64 * wave + lane, tokens_of(t0));
-    if (wave == kDecayWave) decays(sh.dec[part][0], t0 / C);
-    if (chunks > 1) load_gate(t0 + kOn);
+    if (wave == kDecayWave) decays(sh.dec[part][ci & 1], t0 / C);
+    if (ci + 1 < chunks) load_gate(t0 + kOn);
     if (!STATE && tid == 0) sh.bad = 0;
     if (!STATE && tid < 8) sh.p[HP * NPP * kPairs + tid] = T(0);
     for (;; ++ci, t0 += kOn) {
@@ -709,7 +719,6 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
     // the accumulators as the state itself
     multiply(STATE || done ? sh.dec[part][ci & 1].after : sh.dec[part][ci & 1].before);
     {
-      // (What follows forms its places anew: kept through the walk, they would not leave its registers room.)
       const LinParams& p = lin_again(kBoth && REV ? 1 : 0);
       int it = item;
       asm volatile("" : "+s"(it), "+s"(ci));
@@ -830,7 +839,22 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
               left *= d;
             }
           }
+          if (!STATE && !(again && from > 0) && ci >= from && ci + 1 < chunks) {
+            // back to chunks
+            float chk = 0.f;
+#pragma unroll
+            for (int a = 0; a < KK; ++a)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) chk = fmaf(S[a][u][r], 0.f, chk);
+            if (!__syncthreads_or(chk != 0.f)) {
+              begin = ci + 1;
+              break;
+            }
+          }
         }
+        if (begin > 0) continue;
       }
 
       const int block = p.kd * p.vd;
@@ -842,6 +866,7 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
         store_state(p, col0, p.s1 + bh * block);
       }
     }
+    } while (begin > 0);
   };
 
   // The heads of a token lie next to one another, so the rows of one head are a power of two apart as a
@@ -852,14 +877,14 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
   constexpr std::true_type backward;
   constexpr std::false_type forward;
   if constexpr (WALK == LinWalk::backward || WALK == LinWalk::cross) {
-    segment(backward, walks.p[0], item);
+    segment(backward, item);
   } else if constexpr (!kBoth) {
-    segment(forward, walks.p[0], item);
+    segment(forward, item);
   } else {
     if (item & 1)
-      segment(backward, walks.p[1], item >> 1);
+      segment(backward, item >> 1);
     else
-      segment(forward, walks.p[0], item >> 1);
+      segment(forward, item >> 1);
   }
 }
 

@@ -97,3 +97,25 @@ def test_large_states_that_decay(size, io):
     whole = np.repeat(np.abs(i["q"]).sum(-1), H // Hk, 2)[..., None] * 1e36
     lin.near(o, ro, out * np.abs(ro) + (n + 2.0 ** -17) * mo + 2.0 ** -149 * (1 + i["scale"]) * whole, "o")
     lin.near(last, rl, n * ml + 2.0 ** -149 * 1e36, "last_state")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 450, 4, 2, 32, 48), (1, 1500, 2, 1, 64, 130), (1, 320, 300, 100, 20, 64)])
+def test_chunks_behind_what_is_not_finite(size, io):
+    """A value that is not finite ends with its document in the same chunk: from the next chunk on, which starts anew, the same
+    bits as without it, walked by chunks and not token by token."""
+    t = lin._torch()
+    B, L, H, Hk, K, V = size
+    i = inputs(size, io, seed=47)
+    i["g"][:, 64] = i["g"][:, 70] = i["g"][:, 110] = i["g"][:, 128] = -np.inf
+    (o, last), grads = lin.forward(i, io), lin.backward(i, io)
+    for name in ("q", "k", "v", "do"):
+        j = dict(i, **{name: i[name].copy()})
+        j[name][0, 90] = np.inf
+        (o2, last2), g2 = lin.forward(j, io), lin.backward(j, io)
+        if name != "do":
+            assert not t.isfinite(o2[0, 70:110]).all() and t.isfinite(o2[0, :70]).all() and t.isfinite(o2[0, 110:]).all()
+        assert t.equal(o2[:, 128:], o[:, 128:]) and t.equal(last2, last) and t.equal(o2[:, :64], o[:, :64]), name
+        for k in ("dq", "dk", "dv"):
+            assert t.equal(g2[k][:, 128:], grads[k][:, 128:]) and t.equal(g2[k][:, :64], grads[k][:, :64]), (name, k)
+        assert t.equal(g2["dinitial_state"], grads["dinitial_state"]), name
