@@ -131,11 +131,22 @@ __device__ __forceinline__ float norm_sum(float v, int lanes, float* tmp) {
   return v;
 }
 
-// act(t) and act'(t)
-__device__ __forceinline__ float norm_act(float t, bool silu, float& slope) {
+// act(t) and act'(t).  The exponent -t log2 e is off by 2^-24 of itself when it is rounded, and the sigmoid by |t| times as
+// much; the reciprocal instruction by 2^-23.  Results in bf16 keep nothing of that; in fp32 the exponent's rest (and
+// that of log2 e) and a step of Newton's put it right.
+template <typename T> __device__ __forceinline__ float norm_act(float t, bool silu, float& slope) {
   if (!silu) { slope = 1.f; return t; }
-  const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-t * kLog2e));
-  slope = fmaf(t * s, 1.f - s, s);
+  if constexpr (sizeof(T) == 2) {
+    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-t * kLog2e));
+    slope = fmaf(t * s, 1.f - s, s);
+    return t * s;
+  }
+  constexpr float kLow = 1.92596302e-8f;          // log2 e less its fp32 value
+  const float x = fminf(-t * kLog2e, 127.9f);     // (beyond it the sigmoid is zero, and 1 + e^-t a number)
+  const float rest = x < 127.9f && x > -200.f ? fmaf(-t, kLog2e, -x) - t * kLow : 0.f;
+  const float e0 = __builtin_amdgcn_exp2f(x), e = fmaf(e0, rest * 0.693147181f, e0), d = 1.f + e;
+  const float r = __builtin_amdgcn_rcpf(d), s = x < 127.9f ? fmaf(fmaf(-d, r, 1.f), r, r) : 0.f;
+  slope = fmaf(t * s, e * s, s);                  // (1 - s is e s)
   return t * s;
 }
 
@@ -215,7 +226,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormParams p) {
     for (int e = 0; e < VEC; ++e) {
       const float v = fmaf(n.x[i * VEC + e], p.weight ? w[e] : 1.f, p.bias ? o[e] : 0.f);
       float slope;
-      o[e] = gate ? v * norm_act(t[e], p.silu, slope) : norm_act(v, p.silu, slope);
+      o[e] = gate ? v * norm_act<T>(t[e], p.silu, slope) : norm_act<T>(v, p.silu, slope);
     }
     norm_store<T, VEC, EVEN>(y + c, o);
   }
@@ -273,10 +284,10 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
         const float v = fmaf(n.x[k], w[k], o[k]);
         float slope, dn;
         if (gate) {
-          dn = d[e] * norm_act(t[e], p.silu, slope);
+          dn = d[e] * norm_act<T>(t[e], p.silu, slope);
           dz[e] = d[e] * v * slope;
         } else {
-          norm_act(v, p.silu, slope);
+          norm_act<T>(v, p.silu, slope);
           dn = d[e] * slope;
         }
         u[k] = dn * w[k];
@@ -329,12 +340,13 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormParams p) {
   }
 }
 
-// dweight and dbias: 8 columns a workgroup, every 32nd part a row of threads; eight parts asked for at once
+// dweight and dbias: 8 columns a workgroup, every 32nd part a row of threads; eight parts asked for at once.  The parts, sums of
+// some tens of rows in fp32 (in the registers that a row leaves), are added up in 64 bits.
 __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64_t parts, int64_t C, float* dw, float* db) {
-  __shared__ float s[2][32][9];
+  __shared__ double s[2][32][9];
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
   const int64_t c = int64_t(blockIdx.x) * 8 + x;
-  float a = 0.f, b = 0.f;
+  double a = 0.0, b = 0.0;
   if (c < C) {
     for (int64_t i = y; i < parts; i += 256) {
       float u[8], v[8];
@@ -346,8 +358,8 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        a += i + 32 * k < parts ? u[k] : 0.f;
-        b += i + 32 * k < parts ? v[k] : 0.f;
+        a += i + 32 * k < parts ? double(u[k]) : 0.0;
+        b += i + 32 * k < parts ? double(v[k]) : 0.0;
       }
     }
   }
@@ -355,10 +367,10 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const float* part, int64
   s[1][y][x] = b;
   __syncthreads();
   if (y < 2 && c < C) {
-    float t = 0.f;
+    double t = 0.0;
     for (int i = 0; i < 32; ++i) t += s[y][i][x];
     float* const out = y == 0 ? dw : db;
-    if (out) out[c] = t;
+    if (out) out[c] = float(t);
   }
 }
 
