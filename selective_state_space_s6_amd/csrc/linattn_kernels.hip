@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStepParams p, int lane
     if (in && col + e < p.vd) v[e] = at(p.v, b * p.v_sb + h * p.v_sh + col + e);
   const float lg = p.g[b * p.g_sb + h * p.g_sh];
   const bool keep = from && !(double(lg) * 1.4426950408889634 < -150.0);
-  const float a = expf(lg);
+  const float a = fmaxf(expf(lg), kTiny);         // (2^-150 and more, as in lin_decay(): only a token that starts anew ends an infinity)
   const int64_t block = int64_t(p.kd) * p.vd;
   const float* s_in = p.state + (src * p.H + h) * block + col;
   float* s_out = p.state + (dst * p.H + h) * block + col;

@@ -119,3 +119,23 @@ def test_chunks_behind_what_is_not_finite(size, io):
         for k in ("dq", "dk", "dv"):
             assert t.equal(g2[k][:, 128:], grads[k][:, 128:]) and t.equal(g2[k][:, :64], grads[k][:, :64]), (name, k)
         assert t.equal(g2["dinitial_state"], grads["dinitial_state"]), name
+
+
+@pytest.mark.parametrize("log_decay", [-88.0, -103.2, -103.5, -103.9, -103.97, -103.98, -np.inf])
+def test_a_step_keeps_an_infinite_state_as_the_walk_does(log_decay):
+    """Decays down to 2^-150 keep an infinity, and hold what is finite to half of 2^-149 of it; below it the state starts anew."""
+    import selective_state_space_s6_amd as ss
+    t = lin._torch()
+    ones = lambda *s: t.ones(*s, device="cuda")                                           # noqa: E731
+    q, v, g = ones(1, 1, 4), ones(1, 1, 8), t.tensor([log_decay], device="cuda")
+    for value in (np.inf, 1e38):
+        state = t.full((1, 1, 4, 8), value, device="cuda")
+        o2, last = ss.linear_attention_fwd(q[:, None], q[:, None], v[:, None], g, initial_state=state, return_last_state=True)
+        o = ss.linear_attention_step(q, q, v, g, state=state)
+        anew = log_decay * np.log2(np.e) < -150.0
+        for got, each in ((o, 4.0), (o2, 4.0), (state, 1.0), (last, 1.0)):
+            want = each * (1.0 + (0.0 if anew else np.exp(log_decay) * value))
+            if np.isinf(want):
+                assert t.isposinf(got).all()
+            else:                                             # (2^-22 of the decay, and the sum's and o's roundings)
+                assert np.all(np.abs(host(got) - want) <= want * 2.0 ** -20 + each * 2.0 ** -149 * value)
