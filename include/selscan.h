@@ -630,7 +630,7 @@ size_t linear_attention_workspace_size(const selscan_linattn_dims* dims);
  * and for dlog_decay 9/8 of a dk x dv state for every 64 (32) tokens of a head, of which what lies between every eighth is
  * used by strong decays only: 2.7 and 1.5 GB for 4 x 8192 tokens of 80 heads on one, 128 x 64.
  * With dlog_decay, ceil(seqlen / 512) (256) batch nheads ceil(max(dk, dv) / 64) must be below 2^23.
- * batch * nheads * ceil(max(dk, dv) / 64) must be below 2^22, and nheads * dk and nheads * dv at most 2^22
+ * batch * nheads * ceil(max(dk, dv) / 64) must be below 2^22, batch * nheads * seqlen at most 2^48, and nheads * dk and nheads * dv at most 2^22
  * where seqlen is above 1.
  */
 int linear_attention_bwd(const void* q, const void* k, const void* v, const float* log_decay,

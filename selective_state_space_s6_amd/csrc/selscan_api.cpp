@@ -1357,6 +1357,8 @@ static int lin_plan(const selscan_linattn_dims* dims, bool bwd, bool want_dg, Li
       d.batch * d.nheads * ((wide + 63) / 64) >= kMaxItems)
     return SELSCAN_ERR_UNSUPPORTED;
   if (d.seqlen > (int64_t(1) << 31) - 1) return SELSCAN_ERR_UNSUPPORTED;
+  // (the sizes of the backward's workspace in 64 bits)
+  if (bwd && d.batch * d.nheads * d.seqlen > int64_t(1) << 48) return SELSCAN_ERR_UNSUPPORTED;
   // the gradients are contiguous: their tokens are this far apart
   if (bwd && d.seqlen > 1 && d.nheads * wide > kMaxRow) return SELSCAN_ERR_UNSUPPORTED;
   LinPlan p;

@@ -37,3 +37,14 @@ def test_spans_of_the_decays_gradient(io, batch, L, H, K, V, takes):
     d = lin(io, batch, L, H, H, K, V)
     assert bwd(d, q=ODD) == ALIGN                             # without it
     assert bwd(d, q=ODD, dg=0x100000) == (ALIGN if takes else UNSUPPORTED)
+
+
+@pytest.mark.parametrize("batch,L,takes", [(1 << 18, 1 << 30, True), (1 << 18, (1 << 30) + 1, False), ((1 << 22) - 1, (1 << 31) - 1, False)])
+def test_workspaces_whose_size_has_64_bits(batch, L, takes):
+    """batch * nheads * seqlen at most 2^48: 2 fp32 values of dk for each where heads share queries and keys."""
+    import ctypes
+    d = lin(ss.SELSCAN_BF16, batch, L, 1, 1, 256, 64)
+    assert bwd(d, q=ODD) == (ALIGN if takes else UNSUPPORTED)
+    e = lin(ss.SELSCAN_BF16, batch // 2, L, 2, 1, 256, 64)
+    need = ss.lib().linear_attention_bwd_workspace_size(ctypes.byref(e), 0)
+    assert need >= 2 * 4 * 256 * L * (batch // 2) * 2 if takes else need == 0
