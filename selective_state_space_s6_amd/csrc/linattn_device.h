@@ -28,8 +28,8 @@ constexpr double kStrong = -6.0, kGone = -100.0;
 constexpr int kNowhere = 0x3ffffff0;            // a place in bytes beyond any state, another state's added to it too
 
 // Place of (row, column) in an LDS tile of W columns.  A row's 16-byte pieces are exchanged with one another by
-// bits of the row, so that both ways of reading spread over the banks: sixteen rows of one column of
-// pieces, and four neighbouring rows of four neighbouring pieces.  (Rows of 128 bytes share 256 in pairs.)
+// bits of the row, so that both ways of reading, sixteen rows of one column of pieces and four neighbouring rows of four
+// neighbouring pieces, spread over the banks more than plain rows would.  (Rows of 128 bytes share 256 in pairs.)
 template <typename T, int W> __device__ __forceinline__ int lin_at(int row, int col) {
   constexpr int V = 16 / int(sizeof(T)), kPieces = W / V;
   static_assert(kPieces >= 8, "");

@@ -15,10 +15,10 @@
 // state never leaves the accumulators: their layout is, with the channels counted as 8 (l / 16) + 4 u + r, that
 // of the operand which meets the queries, so only its rounding into parts lies between.  Long sequences of few heads
 // are cut into segments; a pass over k and v forms each one's own state, a prefix what enters it.
-// What bounds it (1 x 32 heads x 16384, 128 x 128 bf16, 239 us; 105 us of bytes): the state pass takes 80 us, of which 52
-// are its bytes, the prefix 13, the walk 150.  In the walk the matrix units are busy 28 % of the time, the vector
-// units 53 %, and a wavefront waits 43 % of it: the products of one chunk hang on one another, three barriers part them, and
-// registers (128) and LDS hold four wavefronts a SIMD.  Four wavefronts of 32 columns, which read half as much from
+// What bounds it (1 x 32 heads x 16384, 128 x 128 bf16, 243 us; 105 us of bytes): the state pass takes 81 us, of which 52
+// are its bytes, the prefix 13, the walk 149.  In the walk the matrix units are busy 29 % of the time, the vector
+// units 52 %, and a wavefront waits 42 % of it: the products of one chunk hang on one another, three barriers part them, and
+// registers (128) and LDS hold four wavefronts a SIMD; 37 % of the LDS's cycles are bank conflicts.  Four wavefronts of 32 columns, which read half as much from
 // the LDS, are slower (walk 169 us), as are two tiles of k and v in turns in the state pass (no gain).
 #pragma once
 

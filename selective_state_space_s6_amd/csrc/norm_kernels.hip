@@ -8,7 +8,7 @@
 // A group lies in the registers of up to 64 lanes, or of four wavefronts, 16 bytes of each operand a lane and
 // piece, so that a row is read once: the mean, then the squares of what is off it (not E x^2 - mean^2, which cancels),
 // both in fp32.  Results are rounded once.  Memory bounds the forward (16384 x 32 x 128 bf16, gate: 80 us, 5.0
-// TB/s; a large copy 5.2); the backward (16384 x 40 x 64: 115 us for 420 MB, 3.7 TB/s) also waits for its
+// TB/s; a large copy 5.2); the backward (16384 x 40 x 64: 110 us for 420 MB, 3.8 TB/s) also waits for its
 // two sums in a row, one after the other, with three to seven wavefronts a SIMD.
 #include <hip/hip_runtime.h>
 
