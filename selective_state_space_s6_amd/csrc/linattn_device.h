@@ -24,7 +24,7 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 constexpr float kTiny = 1.401298464e-45f;      // 2^-149
 // Where the decays' gradient takes the product of a state and its gradient from the chunks beside it, and where not
 // (lin_between_kernel): log2 of a token's decay, and of a chunk's.
-constexpr double kStrong = -6.0, kGone = -100.0;
+constexpr double kStrong = -6.0, kGone = -149.0;
 constexpr int kNowhere = 0x3ffffff0;            // a place in bytes beyond any state, another state's added to it too
 
 // Place of (row, column) in an LDS tile of W columns.  A row's 16-byte pieces are exchanged with one another by

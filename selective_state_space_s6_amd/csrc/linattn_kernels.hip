@@ -100,7 +100,7 @@ template <typename V> __device__ __forceinline__ V lin_before(V v) { return lin_
 // Z = e^c <S, R>.  Beside a chunk, <S', R'> = Z + sum Y behind it (S' the state there) and Z + sum X before it, so that from one such
 // product Z follows from chunk to chunk.  What that loses is 2^-24 of the X and Y on the way, of which a token's gradient is
 // a share of the size of its decay: 1/64 of it still leaves more than four digits.  So the walks keep S and R between every lin_span() chunks only; a chunk in which a token starts anew,
-// or whose decay is below 2^-100, has Z = 0.  A chunk with a stronger decay that is neither is
+// or whose decay is below fp32's smallest, 2^-149, has Z = 0.  A chunk with a stronger decay that is neither is
 // marked, and so is one with a value that is not finite: in such spans S is formed before each chunk (the walk `keep`)
 // and met by R behind it (`cross`).
 // One workgroup for lin_span() chunks of a head (4 x 4096 tokens of 16 heads, 128 x 128: 20 us).

@@ -7,7 +7,7 @@ rounding.  With m(g) the sum of the addends' magnitudes, the sum of |x| times th
 for every h > 0, e^-(1-h)x - e^-x being at least h x e^-x.
 
 What passes a whole chunk, Z, follows from the chunk behind it within spans of 8 chunks, so it has the 2^-24 of what
-that is formed of: the x and y on the way to the span's end, or to a chunk in which a token starts anew or whose decay is below 2^-100,
+that is formed of: the x and y on the way to the span's end, or to a chunk in which a token starts anew or whose decay is below 2^-149,
 and <S, R> there.  Not in spans with a chunk that has a token below 2^-6 and is neither: there Z has only its own.
 
 These are worst cases.  Roundings are as often up as down: an addend's are off by 2^-25 n^1/2 in the mean square, and the 2 * 8 *
@@ -36,7 +36,7 @@ def parts(i, size, io, S0=True, dlast=True, chunk=None):
 
 def marked(p, n, S0, dlast):
     """[B, chunks, H]: whether a chunk's span has one that is to have its own product."""
-    own = (p["least"] < -6.0) & ~p["starts"] & (p["log2"] > -100.0)
+    own = (p["least"] < -6.0) & ~p["starts"] & (p["log2"] > -149.0)
     if not S0:
         own[:, 0] = False
     if not dlast:
@@ -59,7 +59,7 @@ def decay_bound(i, size, io, S0=True, dlast=True):
         slower = parts(dict(a, g=np.asarray(a["g"], np.float64) * (1 - h)), size, io, S0, dlast)
     bound = n * u * mag["dlog_decay"] + 2 * u * np.abs(slower["dlog_decay"] - mag["dlog_decay"]) / h
     chunks = ref["through"].shape[1]
-    cut = ref["starts"] | (ref["log2"] < -100.0)
+    cut = ref["starts"] | (ref["log2"] < -149.0)
     if not S0:
         cut[:, 0] = True
     if not dlast:

@@ -22,8 +22,9 @@ def cast(i, io):
     return {k: lin.bf(v, io) if k in ("q", "k", "v", "do") else v for k, v in i.items()}
 
 
-def check(got, i, size, io, S0, dlast, what):
+def check(got, i, size, io, S0, dlast, what, more=0.0):
     ref, bound = bounds.decay_bound(i, size, io, S0, dlast)
+    bound = bound + more
     got = host(got)
     if i["g"].ndim == 1:
         ref, bound = ref.sum((0, 1)), bound.sum((0, 1))
@@ -91,3 +92,29 @@ def test_what_is_not_finite(size, where, io):
     ref, bound = bounds.decay_bound(clean, size, io)
     # (spans with it have products of their own: what is finite has the bound of what passes it)
     lin.near(np.where(fine, got, 0.0), np.where(fine, ref, 0.0), bound, where)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("total", [-60.0, -95.0, -101.0])
+def test_what_passes_a_whole_chunk_alone(total, io):
+    """A chunk without keys and queries: what passes its tokens is the state before it, large, and the gradient behind it, by decays
+    that add up to e^total.  A product of decays that fp32 holds as a subnormal number is off by half of 2^-149 at most,
+    however small it is, and so is a second one that it meets (the chunk's and a token's): an addend by 2^-149 of what it is without
+    decays."""
+    size = (1, 192, 2, 2, 16, 24)
+    i = cast(with_decay(size, "fixed", seed=9), io)
+    for decay in ("even", "one"):
+        g = np.full((1, 192, 2), -0.01, np.float32)
+        g[:, 64:128] = total / 64 if decay == "even" else -0.01
+        if decay == "one":
+            g[:, 100] = total + 0.63
+        j = dict(i, g=g, S0=(1e15 * i["S0"]).astype(np.float32), dlast=(1e15 * i["dlast"]).astype(np.float32))
+        for n in ("q", "k"):
+            j[n] = i[n].copy()
+            j[n][:, 64:128] = 0.0
+        without = bounds.parts(dict(bounds.absolute(j), g=np.zeros_like(g)), size, io)["dlog_decay"]
+        check(lin.backward(j, io)["dlog_decay"], j, size, io, True, True, "%s %s" % (total, decay), 2.0 ** -149 * without)
+        if decay == "one":
+            # (the span has products of its own; in the other, what is 512 tokens behind has its share in the error: the bound's)
+            got, ref = host(lin.backward(j, io)["dlog_decay"])[:, 70:120], bounds.parts(j, size, io)["dlog_decay"][:, 70:120]
+            assert np.all(np.abs(got / ref - 1) < 1e-4), (got[0, 0], ref[0, 0])
