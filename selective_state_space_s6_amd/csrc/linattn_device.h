@@ -136,7 +136,7 @@ struct LinTile {
   bool even;
 
   static __device__ __forceinline__ const T* head(const LinTensor& x, int64_t b, int64_t h, int col0) {
-    return static_cast<const T*>(x.p) + b * x.sb + (h / x.share) * x.sh + col0;
+    return static_cast<const T*>(x.p) + b * x.sb + int64_t(uint32_t(h) / uint32_t(x.share)) * x.sh + col0;
   }
   __device__ __forceinline__ void init(const LinTensor& x, int64_t b, int64_t h, int64_t t0, int col0, int width) {
     at = head(x, b, h, col0) + t0 * x.sl;

@@ -112,11 +112,14 @@ template <int C, int HP, int COLS, bool STATE, bool REV> struct LinPlace {
   int nb, seg, chunks, col0;
   int64_t h, b, bh, chunk0, L;
   __device__ __forceinline__ LinPlace(const LinParams& p, int item, int part) {
-    const int segs = STATE ? p.nseg - 1 : p.nseg;   // (nothing is behind the last segment)
-    const int H = int(p.H), heads = H / HP, sidx = item / heads / p.nblk % segs;
-    nb = item / heads % p.nblk;
-    h = item % heads * HP + part;
-    b = item / heads / p.nblk / segs;
+    // (32 bits, unsigned: a division of 64 takes a hundred instructions and more)
+    const uint32_t segs = uint32_t(STATE ? p.nseg - 1 : p.nseg);    // (nothing is behind the last segment)
+    const uint32_t H = uint32_t(p.H), heads = H / HP, rest = uint32_t(item) / heads, blk = uint32_t(p.nblk);
+    const uint32_t segments = rest / blk, row = segments / segs;
+    const int sidx = int(segments - row * segs);
+    nb = int(rest - segments * blk);
+    h = (uint32_t(item) - rest * heads) * HP + part;
+    b = row;
     bh = b * H + h;
     seg = STATE && REV ? sidx + 1 : sidx;
     chunk0 = int64_t(seg) * p.seg_chunks;
@@ -131,7 +134,7 @@ template <int C, int HP, int COLS, bool STATE, bool REV> struct LinPlace {
     return static_cast<char*>(p.out) + (b * p.o_sb + h * p.o_sh + t * p.o_sl + col) * size;
   }
   template <typename T> __device__ __forceinline__ const T* x_at(const LinParams& p, int64_t t, int col) const {
-    return static_cast<const T*>(p.x.p) + b * p.x.sb + (h / p.x.share) * p.x.sh + t * p.x.sl + col;
+    return static_cast<const T*>(p.x.p) + b * p.x.sb + int64_t(uint32_t(h) / uint32_t(p.x.share)) * p.x.sh + t * p.x.sl + col;
   }
 };
 
