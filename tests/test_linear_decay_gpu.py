@@ -118,3 +118,26 @@ def test_what_passes_a_whole_chunk_alone(total, io):
             # (the span has products of its own; in the other, what is 512 tokens behind has its share in the error: the bound's)
             got, ref = host(lin.backward(j, io)["dlog_decay"])[:, 70:120], bounds.parts(j, size, io)["dlog_decay"][:, 70:120]
             assert np.all(np.abs(got / ref - 1) < 1e-4), (got[0, 0], ref[0, 0])
+
+
+def test_states_kept_far_apart():
+    """64 rows of the same sequence, whose kept states take more than 2^31 values: every row's gradients are the first's."""
+    import selective_state_space_s6_amd as ss
+    t = lin._torch()
+    B, L, H, K, V = 64, 4160, 32, 128, 128
+    gen = t.Generator(device="cuda").manual_seed(1)
+    new = lambda *s: t.randn(*s, device="cuda", generator=gen)                            # noqa: E731
+    q, k, v, do = (new(1, L, H, 128).bfloat16().expand(B, L, H, 128) for _ in range(4))
+    g = -0.1 * t.rand(1, L, H, device="cuda", generator=gen)
+    g[:, 1000::1500] = -6.0                                   # (some spans have products of their own)
+    g[:, 2000] = -float("inf")
+    dlast = new(1, H, K, V).expand(B, H, K, V).contiguous()
+    d = ss.linear_attention_bwd(q, k, v, g.expand(B, L, H), do=do, scale=K ** -0.5, dlast_state=dlast)
+    for name in ("dlog_decay", "dq", "dk", "dv"):
+        for row in (1, 31, 62, 63):
+            assert t.equal(d[name][row], d[name][0]), (name, row)
+    assert t.isfinite(d["dlog_decay"]).all() and (d["dlog_decay"][:, 2000] == 0).all()
+    # and the first row's, alone in segments, up to rounding: 2^-8 of dq and dk, NORM of the decays'
+    one = ss.linear_attention_bwd(q[:1], k[:1], v[:1], g, do=do[:1], scale=K ** -0.5, dlast_state=dlast[:1])
+    a, b = host(d["dlog_decay"][:1]), host(one["dlog_decay"])
+    assert bounds.norms(a - b, b).max() <= 2 * bounds.NORM
