@@ -755,7 +755,8 @@ __global__ __launch_bounds__(64 * NW, (lin_waves<T, KD, NW, WALK == LinWalk::gra
           const int n = place.tokens_of(t0);
           const bool stands = !STATE && (ci < from || (ci == from && done));
           const bool with = ci >= from && DOT && p.dot != nullptr;
-          if ((DOT && with) || KEEP) keep_some(p, place, t0 / C, 1.f);
+          // (a wavefront whose first chunk stands holds the state behind it by now, and has kept the one before it)
+          if (((DOT && with) || KEEP) && (!stands || again)) keep_some(p, place, t0 / C, 1.f);
           if (DOT && with && wave == kDecayWave && lin_lane() == 0) mark(p, place, t0 / C, true);
           if (CROSS) {
             load_kept(p, place, t0 / C, 0);

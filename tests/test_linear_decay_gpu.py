@@ -141,3 +141,22 @@ def test_states_kept_far_apart():
     one = ss.linear_attention_bwd(q[:1], k[:1], v[:1], g, do=do[:1], scale=K ** -0.5, dlast_state=dlast[:1])
     a, b = host(d["dlog_decay"][:1]), host(one["dlog_decay"])
     assert bounds.norms(a - b, b).max() <= 2 * bounds.NORM
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("name,at", [("k", 520), ("q", 500), ("k", 512), ("q", 511), ("v", 520), ("do", 500)])
+@pytest.mark.parametrize("size", [(1, 800, 2, 2, 64, 48), (1, 700, 344, 344, 20, 4), (2, 1100, 2, 1, 128, 130)])
+def test_one_channel_that_is_not_finite_beside_a_span_s_end(size, name, at, io):
+    """Where the walks keep a state, a chunk of which one channel's wavefront alone is not finite: what the others keep is the
+    state before the chunk."""
+    B, L, H, Hk, K, V = size
+    i = cast(with_decay(size, "token", seed=11), io)
+    clean = dict(i, **{name: i[name].copy()})
+    i = dict(i, **{name: i[name].copy()})
+    i[name][0, at, 0, 3], clean[name][0, at, 0, 3] = np.inf, 0.0
+    got = host(lin.backward(i, io)["dlog_decay"])
+    with np.errstate(invalid="ignore", over="ignore"):
+        fine = np.isfinite(orc.linear_bwd(i["q"], i["k"], i["v"], i["g"], i["do"], i["scale"], i["S0"], i["dlast"])["dlog_decay"])
+    assert not fine.all() and np.array_equal(np.isfinite(got), fine), np.argwhere(np.isfinite(got) != fine)[:5]
+    ref, bound = bounds.decay_bound(clean, size, io)
+    lin.near(np.where(fine, got, 0.0), np.where(fine, ref, 0.0), bound, name)
